@@ -419,6 +419,176 @@ SSM_API int ssm_ssd_fwd(const void* u, const void* delta, const float* A, const 
                         const float* D, const void* z, const float* dt_bias, const float* h0, void* y,
                         float* h_last, const ssm_ssd_dims* dims, void* stream);
 
+/* ------------------------------------------------------------------------------
+ * Linear attention with a decay for each head.
+ *
+ * The masked linear attention that a scan with a scalar decay is dual to
+ * (yo3nglau.github.io "Mamba 与状态空间模型：面试问题与推荐回答" Q10), with query and key
+ * rows of their own for each head or for each group of heads, tokens in rows, and requests
+ * of different lengths packed one behind the other.  Per head h, with a state S of dk x dv
+ * float32 values:
+ *
+ *   S_t = e^{g_t} S_{t-1} + k_t v_t^T        o_t = scale * S_t^T q_t
+ *
+ * Layouts (last index contiguous; a token's heads contiguous; `*_stride` elements from one
+ * token to the next, so that q, k and v may be columns of one projection):
+ *   q, k : (tokens, kheads, dk) in io_dtype; head h reads head h / (nheads / kheads)
+ *   v, o : (tokens, nheads, dv) in io_dtype
+ *   g    : float32 (tokens, nheads), the log of the decay, <= 0; with head_decay = 1
+ *          float32 (nheads,), one decay for all tokens of a head.  A value below -128
+ *          (-inf among them) counts as -128, whose factor is zero in float32.
+ *   cu_seqlens : int32 (nseq + 1), on the device, ascending: sequence s is tokens
+ *          cu_seqlens[s] .. cu_seqlens[s+1] - 1 (none at all is allowed).  NULL: nseq
+ *          sequences of tokens / nseq each.  Values are held to 0 .. tokens.  Rows that
+ *          belong to no sequence are neither read nor written.
+ *   states : float32 (nslots, nheads, dk, dv); slots (int32 (nseq,), on the device) names
+ *          the state of each sequence; NULL: nslots >= nseq states in order.  A sequence
+ *          whose slot is negative, not below nslots or already named by an earlier
+ *          sequence of the call is skipped: its rows of o and every state stay as they
+ *          were (padding of a fixed-size batch).
+ *
+ * Sums and states are float32.  The products run on the matrix cores on bf16 operands;
+ * operands that are not bf16 inputs (the state, the decayed products, and everything when
+ * io_dtype is SSM_F32) are split into two bf16 parts, which leaves out under 2^-17 of each.
+ * A NaN or infinity in a token reaches outputs of earlier tokens of its sequence at most
+ * within its block of 64 tokens, and never another sequence.
+ * Ownership, asynchrony and the error rules are those of ssm_selective_scan_fwd. */
+
+/* Largest dk and dv. */
+#define SSM_LINATTN_MAX_DIM 256
+
+typedef struct ssm_linattn_dims {
+    int64_t tokens;    /* >= 1: rows of q, k, v, o and g */
+    int64_t nseq;      /* 1 .. 65535 sequences (single-token step: equal to tokens) */
+    int64_t nheads;    /* 1 .. 65535: heads of v, o, g and the states */
+    int64_t kheads;    /* >= 1 heads of q and k; nheads % kheads == 0 */
+    int64_t dk, dv;    /* 1 .. SSM_LINATTN_MAX_DIM */
+    int64_t q_stride, k_stride, v_stride, o_stride; /* elements between tokens; 0: packed */
+    int64_t nslots;    /* states in the arrays of states (ignored without states) */
+    int64_t piece_len; /* 0: library choice; else tokens of a piece of a sequence, a
+                          multiple of 64 (same result up to rounding) */
+    int32_t io_dtype;  /* ssm_dtype of q, k, v, o */
+    int32_t head_decay;/* 1: g is (nheads,); 0: (tokens, nheads) */
+    float scale;
+    int32_t reserved;  /* must be 0 */
+    void* workspace;   /* device memory, 256-byte aligned; may be NULL when the size is 0 */
+    size_t workspace_bytes;
+} ssm_linattn_dims;
+
+/* Bytes of workspace of ssm_linattn_fwd (0 when it needs none, or for dims it refuses). */
+SSM_API size_t ssm_linattn_fwd_workspace_bytes(const ssm_linattn_dims* dims);
+
+/* Enqueue the forward over whole sequences.  s0 (nullable: zeros): the states before the
+ * first tokens; s_last (nullable): the states after the last ones; s_last may be s0 itself
+ * (the states are then updated in place) but must not overlap any other array.  slots needs
+ * s0 or s_last.  Returns an ssm_status value. */
+SSM_API int ssm_linattn_fwd(const void* q, const void* k, const void* v, const float* g, const int32_t* cu_seqlens,
+                            const int32_t* slots, const float* s0, void* o, float* s_last,
+                            const ssm_linattn_dims* dims, void* stream);
+
+/* One token of each sequence (tokens == nseq, no cu_seqlens): states read and updated in
+ * place (required), o written.  Needs no workspace. */
+SSM_API int ssm_linattn_step(const void* q, const void* k, const void* v, const float* g, const int32_t* slots,
+                             float* states, void* o, const ssm_linattn_dims* dims, void* stream);
+
+/* Where ssm_linattn_bwd writes the gradients (device pointers, packed):
+ *   dq, dk : (tokens, kheads, dk) in io_dtype, summed over the heads that share them
+ *   dv     : (tokens, nheads, dv) in io_dtype
+ *   dg     : float32, the shape of g; nullable (not computed)
+ *   ds0    : float32 (nseq, nheads, dk, dv); required with s0, nullable without */
+typedef struct ssm_linattn_grads {
+    void* dq;
+    void* dk;
+    void* dv;
+    float* dg;
+    float* ds0;
+} ssm_linattn_grads;
+
+/* Bytes of workspace of ssm_linattn_bwd (never 0 for valid dims; 0 for dims it refuses):
+ * the states and state gradients at the pieces' ends, three or more floats per token and
+ * head for dg, and float32 dq and dk per head when heads share them. */
+SSM_API size_t ssm_linattn_bwd_workspace_bytes(const ssm_linattn_dims* dims);
+
+/* Enqueue the gradients of
+ *     sum dout * o  +  sum ds_last * s_last
+ * for the forward with the same q, k, v, g, cu_seqlens and s0 (no slots: s0, ds_last and
+ * ds0 are (nseq, nheads, dk, dv), nslots is ignored).  dout: as o, with o_stride; ds_last
+ * nullable.  States are recomputed from the inputs.  Rows of no sequence get zero gradients.
+ * Every sum runs in a fixed order.  No output overlaps an input, another output or the
+ * workspace (SSM_ERR_ALIAS). */
+SSM_API int ssm_linattn_bwd(const void* q, const void* k, const void* v, const float* g, const int32_t* cu_seqlens,
+                            const float* s0, const void* dout, const float* ds_last, const ssm_linattn_grads* grads,
+                            const ssm_linattn_dims* dims, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * The norms around a block.  RMS norm of n values x with a weight w:
+ *     norm(x; w)_i = w_i x_i / sqrt(mean_j x_j^2 + eps)
+ * Rows are last-index contiguous; sums and statistics are float32. */
+
+/* Largest group (ssm_gated_norm_*) and row (ssm_add_norm_*). */
+#define SSM_NORM_MAX_DIM 16384
+
+/* The norm behind a mixer with its SiLU gate (gongshangzheng.github.io "Mamba" §3.1 has the
+ * gate branch), over groups of a row's channels (a head's, or all of them):
+ *   gate_first = 1: y = norm(x SiLU(z); w)      gate_first = 0: y = norm(x; w) SiLU(z)
+ *   x, z, y : (rows, ngroups * group) in io_dtype; z nullable (no gate)
+ *   w       : float32 (ngroups * group,), or (group,) for every group when shared_weight
+ * y may be x or z itself (same stride), else it overlaps no input. */
+typedef struct ssm_gated_norm_dims {
+    int64_t rows;      /* >= 1 */
+    int64_t ngroups;   /* >= 1 */
+    int64_t group;     /* 1 .. SSM_NORM_MAX_DIM */
+    int64_t x_stride, z_stride, y_stride; /* elements between rows; 0: packed */
+    int32_t io_dtype;
+    int32_t gate_first;
+    int32_t shared_weight;
+    float eps;         /* > 0 */
+    void* workspace;   /* backward: 256-byte aligned device memory */
+    size_t workspace_bytes;
+} ssm_gated_norm_dims;
+
+SSM_API int ssm_gated_norm_fwd(const void* x, const void* z, const float* w, void* y, const ssm_gated_norm_dims* dims,
+                               void* stream);
+SSM_API size_t ssm_gated_norm_bwd_workspace_bytes(const ssm_gated_norm_dims* dims);
+/* Gradients of sum(dy * y).  dy, dx, dz: packed (rows, ngroups * group) in io_dtype (y_stride
+ * is ignored); dz required with z and refused without (SSM_ERR_NULL); dw: float32, w's shape,
+ * summed in a fixed order.  Outputs overlap no input, one another or the workspace. */
+SSM_API int ssm_gated_norm_bwd(const void* x, const void* z, const float* w, const void* dy, void* dx, void* dz,
+                               float* dw, const ssm_gated_norm_dims* dims, void* stream);
+
+/* The residual stream between two blocks: the norm after a block (post, nullable: none),
+ * the residual scale (per channel, nullable: ones), the addition, and the norm before the
+ * next block:
+ *   a = norm(x; post) or x      r = res + scale * a      y = norm(r; w)
+ *   x, y   : (rows, dim) in io_dtype;   res, r : (rows, dim) in res_dtype; res nullable
+ *   scale, post, w : float32 (dim,)
+ * y is the norm of r as it is stored (rounded to res_dtype), so that the gradients, which
+ * start from r, are those of what ran.  r may be res itself; no other overlap. */
+typedef struct ssm_add_norm_dims {
+    int64_t rows;      /* >= 1 */
+    int64_t dim;       /* 1 .. SSM_NORM_MAX_DIM */
+    int64_t x_stride, res_stride, r_stride, y_stride; /* elements between rows; 0: packed */
+    int32_t io_dtype;
+    int32_t res_dtype;
+    float eps;         /* > 0 */
+    int32_t reserved;  /* must be 0 */
+    void* workspace;   /* backward: 256-byte aligned device memory */
+    size_t workspace_bytes;
+} ssm_add_norm_dims;
+
+SSM_API int ssm_add_norm_fwd(const void* x, const void* res, const float* scale, const float* post, const float* w,
+                             void* r, void* y, const ssm_add_norm_dims* dims, void* stream);
+SSM_API size_t ssm_add_norm_bwd_workspace_bytes(const ssm_add_norm_dims* dims);
+/* Gradients of sum(dy * y) + sum(dr * r) (dr nullable: none arrives at r from elsewhere).
+ * x, r as the forward had and gave them (x may be NULL without scale and post).
+ *   dx : (rows, dim) in io_dtype;  dres : (rows, dim) in res_dtype, the gradient at res,
+ *   nullable; may be dr itself;  dw : float32 (dim,);  dscale, dpost : float32 (dim,),
+ *   required with scale and post.
+ * dy, dr, dx, dres are packed.  Sums over rows run in a fixed order. */
+SSM_API int ssm_add_norm_bwd(const void* x, const void* r, const float* scale, const float* post, const float* w,
+                             const void* dy, const void* dr, void* dx, void* dres, float* dw, float* dscale,
+                             float* dpost, const ssm_add_norm_dims* dims, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

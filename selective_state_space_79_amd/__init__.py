@@ -1,10 +1,10 @@
 """Python binding of libssm.so, the MI355X selective scan (forward, decode step,
 backward, fused convolution front end, and the chunked scalar-decay pass with
-per-head step sizes).
+per-head step sizes), and of the operators of a block around it (``blocks.py``: linear
+attention with a decay for each head, norms with gate and residual scale).
 
-Argument marshalling only: every step of the scan runs in the HIP kernels of
-``csrc/scan_fwd.hip``, ``csrc/scan_bwd.hip`` and ``csrc/ssd_fwd.hip`` behind the C ABI
-of ``include/ssm.h``.  There is no CPU or PyTorch fallback: if the library is missing,
+Argument marshalling only: every step runs in the HIP kernels of ``csrc/`` behind the C
+ABI of ``include/ssm.h``.  There is no CPU or PyTorch fallback: if the library is missing,
 every call raises.
 
 The ``ssm_*`` functions carry the C names (see ``EXPORTED``) and take raw device
@@ -16,6 +16,9 @@ from __future__ import annotations
 
 import ctypes
 import os
+
+from . import blocks
+from .blocks import *  # noqa: F401,F403  (the operators of a block around the mixer)
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "libssm.so")
@@ -42,7 +45,7 @@ EXPORTED = ("ssm_selective_scan_fwd", "ssm_selective_scan_fwd_state", "ssm_selec
             "ssm_selective_scan_fwd_conv", "ssm_selective_scan_step_conv", "ssm_ssd_fwd",
             "ssm_ssd_fwd_workspace_bytes", "ssm_ssd_fwd_plan", "ssm_selective_scan_ckpt_bytes",
             "ssm_selective_scan_fwd_ckpt", "ssm_selective_scan_bwd_ckpt", "ssm_selective_scan_fwd_noalloc",
-            "ssm_selective_scan_noalloc_scratch_bytes")
+            "ssm_selective_scan_noalloc_scratch_bytes", *blocks.EXPORTED)
 SSM_MAX_DSTATE_BWD = 128
 
 
@@ -188,6 +191,7 @@ def load_library():
         lib.ssm_selective_scan_noalloc_scratch_bytes.restype = ctypes.c_size_t
         lib.ssm_status_string.argtypes = [ctypes.c_int]
         lib.ssm_status_string.restype = ctypes.c_char_p
+        blocks.declare(lib)
         _lib = lib
     return _lib
 
