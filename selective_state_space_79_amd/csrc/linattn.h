@@ -45,7 +45,8 @@ struct LinattnPass {
     int32_t nseq, nslots, npieces, pieced;
     int32_t st_t;             // states lie (vd, kd) instead of (kd, vd)
     int32_t reverse, out_f32;
-    int32_t vec;              // bit n: rows of x1.. x4 (bits 0..3) and out (bit 4) allow 16-byte access
+    int32_t wide;             // rows of x1 .. x4 allow 16-byte loads at 32-bit offsets
+    int32_t pairs;            // out allows stores of two bf16
     float wscale, oscale;
 };
 
@@ -83,11 +84,16 @@ __device__ inline uint32_t pack2(float a, float b) {
 __device__ inline float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ inline float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// x = hi + lo in two bf16 parts (hi = bf16(x), lo = bf16(x - hi)): what is left out is
-// under 2^-17 of x, so products of split operands keep float32 sums to about 2^-17.
-__device__ inline void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-    hi = pack2(a, b);
-    lo = pack2(a - bf_lo(hi), b - bf_hi(hi));
+// Two values in N bf16 parts each (part 0 is bf16(x), the next the rounded rest, ...), packed
+// in pairs.  One rounding leaves at most 2^-9 of the power of two above x, so two parts leave
+// under 2^-17 of x and three parts, which hold 24 bits, all of a float32.
+template <int N> __device__ inline void split(float a, float b, uint32_t (&w)[N]) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        w[n] = pack2(a, b);
+        a -= bf_lo(w[n]);
+        b -= bf_hi(w[n]);
+    }
 }
 
 __device__ inline f32x4 mma(const u32x4& a, const u32x4& b, const f32x4& c) {
@@ -153,14 +159,10 @@ __device__ inline int find_slot(const int32_t* slots, int nslots, int s) {
 // Element offset of piece p of 8 bf16 in row r of a tile with W columns.  The pieces of a
 // row are permuted by the row so that both reads of a tile touch distinct banks: 8 rows at
 // one piece (operands along a row), and 4 rows at 4 neighbouring pieces (transposed).
-template <int W> __device__ inline int at_piece(int r, int p) {
-    if constexpr (W >= 128)
-        return r * W + 8 * (p ^ (4 * (r & 3) + ((r >> 2) & 3)));
-    else if constexpr (W == 64)
-        return r * W + 8 * (p ^ (4 * ((r >> 1) & 1) + ((r >> 2) & 3)));
-    else
-        return r * W + 8 * (p ^ ((r >> 2) & 3));
+template <int W> __device__ constexpr int twist(int r) {
+    return W >= 128 ? 4 * (r & 3) + ((r >> 2) & 3) : W == 64 ? 4 * ((r >> 1) & 1) + ((r >> 2) & 3) : (r >> 2) & 3;
 }
+template <int W> __device__ constexpr int at_piece(int r, int p) { return r * W + 8 * (p ^ twist<W>(r)); }
 
 // Operand along the rows of a tile: lane 16g + i gets columns 32 kb + 8g .. + 7 of row r0 + i.
 template <int W> __device__ inline u32x4 row_op(const uint16_t* t, int r0, int kb, int lane) {
@@ -181,64 +183,141 @@ template <int W, int SPREAD> __device__ inline u32x4 col_op(const uint16_t* t, i
     return u32x4{u.x, u.y, v.x, v.y};
 }
 
-// ---------------------------------------------------------------- rows into tiles
-// A tile of C rows of W columns on its way from memory to LDS in this thread's registers.
-template <int PARTS, int C, int W> struct Stage {
+// Rows r0 + 4g .. + 3 of column c0 + i for lane 16g + i: a tile in the layout of a product.
+template <int W> __device__ inline uint2 tile_op(const uint16_t* t, int r0, int c0, int lane) {
+    const int r = r0 + 4 * (lane >> 4) + ((lane >> 2) & 3), c = c0 + 4 * (lane & 3);
+    return __builtin_bit_cast(
+        uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(t + at_piece<W>(r, c >> 3) + (c & 7))));
+}
+
+// Products of operands in NA and NB parts: those whose part numbers add up to at most `most`
+// (the rest is below what the parts themselves leave out).
+template <int NA, int NB>
+__device__ inline f32x4 mma_parts(const u32x4 (&a)[NA], const u32x4 (&b)[NB], f32x4 c) {
+    constexpr int most = (NA > NB ? NA : NB) - 1;
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+            if (i + j <= most) c = mma(a[i], b[j], c);
+    return c;
+}
+
+// Sum over the 16 lanes of a row (every lane gets it): rotations within the row.
+__device__ inline float sum16(float v) {
+    const auto ror = [](float x, auto c) {
+        return __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(x), decltype(c)::value, 0xf, 0xf, true));
+    };
+    v += ror(v, std::integral_constant<int, 0x128>{});
+    v += ror(v, std::integral_constant<int, 0x124>{});
+    v += ror(v, std::integral_constant<int, 0x122>{});
+    v += ror(v, std::integral_constant<int, 0x121>{});
+    return v;
+}
+// The value of the lane's neighbour (lanes 2n and 2n + 1 swap).
+__device__ inline float swap1(float v) {
+    return __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(v), 0xB1, 0xf, 0xf, true));
+}
+
+// Barrier for LDS traffic only: outstanding loads of the next chunk are not waited for.
+__device__ inline void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// ---------------------------------------------------------------- memory
+// Rows of a chunk through a buffer descriptor on its first token: rows at or behind `hi`
+// and columns past the row's end read as zero and are not written.
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+constexpr uint32_t kPast = 0x80000000u;   // an offset past every window (windows are < 2^31)
+
+__device__ inline Rsrc rows_rsrc(const char* row0, int64_t pitch, int64_t rows, int c) {
+    const int64_t n = rows < c ? rows : c;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(row0), 0, int(n * pitch), 0x00020000);
+}
+
+// 16 bytes per lane from a buffer straight into LDS: lane l's bytes land at lds + 16 l (lds
+// wave-uniform).  (A plain device function: the builtin inside a kernel template leaves the
+// template without a host stub.)
+__device__ inline void load_lds16(Rsrc r, void* lds, uint32_t voff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, voff, 0, 0, 0);
+}
+
+// A tile of C rows of W columns from memory to LDS.  bf16 rows (PARTS 1) go straight there,
+// each lane fetching the piece that its slot of the permuted row holds; float32 rows
+// (PARTS 3) pass through registers, where they are split.  No copy of the next chunk is held
+// back: the other workgroup of the CU computes while this one's loads are in flight.
+template <int PARTS, int C, int W> struct Tile {
     static constexpr int N = C * W / 8 / kThreads;   // pieces of 8 values per thread
     static_assert(C * W / 8 % kThreads == 0, "whole pieces per thread");
-    u32x4 r[N][PARTS];   // 8 bf16, or 8 float32
+    static constexpr int E = PARTS == 1 ? 2 : 4;
+    static constexpr int RS = kThreads / (W / 8);    // rows between a thread's pieces
+    static constexpr int Q = PARTS == 1 ? 1 : 2;     // 16-byte loads per piece
 
-    // rows of tokens first .. (or downwards), those in [lo, hi) only; `row` points at the
-    // head's first column, w columns are real
-    __device__ inline void load(const char* row, int64_t stride, int64_t c0, bool rev, int64_t lo, int64_t hi, int w,
-                                bool vec) {
-        constexpr int E = PARTS == 1 ? 2 : 4;
+    __device__ static inline uint32_t offset(int tid, int n, int pitch, bool rev, int w) {
+        const int rr = tid / (W / 8) + RS * n, slot = tid % (W / 8);
+        const int col = 8 * (PARTS == 1 ? slot ^ twist<W>(rr) : slot);
+        return col < w ? uint32_t((rev ? C - 1 - rr : rr) * pitch + col * E) : kPast;
+    }
+    u32x4 r[PARTS == 1 ? 1 : N][Q];
+
+    __device__ inline void load(uint16_t* tile, int tid, const char* row0, int64_t pitch, int64_t rows, bool rev, int w) {
+        const Rsrc b = rows_rsrc(row0, pitch, rows, C);
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            const int idx = int(threadIdx.x) + kThreads * n;
-            const int rr = idx / (W / 8), col = 8 * (idx % (W / 8));
-            const int64_t t = c0 + (rev ? C - 1 - rr : rr);
-            const bool ok = t >= lo && t < hi && col < w;
-            const char* q = row + (t * stride + col) * E;
+            const uint32_t o = offset(tid, n, int(pitch), rev, w);
+            if constexpr (PARTS == 1) {
+                load_lds16(b, tile + 8 * (kThreads * n + (__builtin_amdgcn_readfirstlane(tid) & ~63)), o);
+            } else {
 #pragma unroll
-            for (int h = 0; h < PARTS; ++h) r[n][h] = u32x4{0, 0, 0, 0};
-            if (ok) {
-                if (vec) {
-#pragma unroll
-                    for (int h = 0; h < PARTS; ++h) r[n][h] = *reinterpret_cast<const u32x4*>(q + 16 * h);
-                } else if constexpr (PARTS == 1) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (col + e < w)
-                            r[n][0][e / 2] |= uint32_t(reinterpret_cast<const uint16_t*>(q)[e]) << (16 * (e & 1));
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (col + e < w) r[n][e / 4][e % 4] = reinterpret_cast<const uint32_t*>(q)[e];
-                }
+                for (int h = 0; h < Q; ++h)
+                    r[n][h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, o == kPast ? o : o + 16 * h, 0, 0));
             }
         }
     }
-    __device__ inline void store(uint16_t* tile) const {
+    // float32 rows: what load() brought, in parts
+    __device__ inline void store(uint16_t* tile, int tid) const {
+        if constexpr (PARTS > 1) {
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const int idx = int(threadIdx.x) + kThreads * n;
-            const int o = at_piece<W>(idx / (W / 8), idx % (W / 8));
-            if constexpr (PARTS == 1) {
-                *reinterpret_cast<u32x4*>(tile + o) = r[n][0];
-            } else {
-                u32x4 hi, lo;
+            for (int n = 0; n < N; ++n) put(tile, tid + kThreads * n, r[n]);
+        }
+    }
+    __device__ static inline void put(uint16_t* tile, int idx, const u32x4 (&x)[Q]) {
+        const int o = at_piece<W>(idx / (W / 8), idx % (W / 8));
+        if constexpr (PARTS == 1) {
+            *reinterpret_cast<u32x4*>(tile + o) = x[0];
+        } else {
+            u32x4 v[PARTS];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    uint32_t a, b;
-                    const u32x4& v = r[n][e / 2];
-                    split2(__uint_as_float(v[2 * (e & 1)]), __uint_as_float(v[2 * (e & 1) + 1]), a, b);
-                    hi[e] = a;
-                    lo[e] = b;
-                }
-                *reinterpret_cast<u32x4*>(tile + o) = hi;
-                *reinterpret_cast<u32x4*>(tile + C * W + o) = lo;
+            for (int e = 0; e < 4; ++e) {
+                uint32_t w[PARTS];
+                split<PARTS>(__uint_as_float(x[e / 2][2 * (e & 1)]), __uint_as_float(x[e / 2][2 * (e & 1) + 1]), w);
+#pragma unroll
+                for (int k = 0; k < PARTS; ++k) v[k][e] = w[k];
             }
+#pragma unroll
+            for (int k = 0; k < PARTS; ++k) *reinterpret_cast<u32x4*>(tile + k * C * W + o) = v[k];
+        }
+    }
+    // any alignment, any row length w: value by value
+    __device__ static inline void copy_any(uint16_t* tile, int tid, const char* row0, int64_t pitch, int64_t rows, bool rev,
+                                           int w) {
+#pragma unroll 1
+        for (int n = 0; n < N; ++n) {
+            const int idx = tid + kThreads * n;
+            const int col = 8 * (idx % (W / 8)), rr = rev ? C - 1 - idx / (W / 8) : idx / (W / 8);
+            const char* q = row0 + rr * pitch + col * E;
+            u32x4 x[Q];
+#pragma unroll
+            for (int h = 0; h < Q; ++h) x[h] = u32x4{0, 0, 0, 0};
+            if (rr < rows) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (col + e >= w) continue;
+                    if constexpr (PARTS == 1)
+                        x[0][e / 2] |= uint32_t(reinterpret_cast<const uint16_t*>(q)[e]) << (16 * (e & 1));
+                    else
+                        x[e / 4][e % 4] = reinterpret_cast<const uint32_t*>(q)[e];
+                }
+            }
+            put(tile, idx, x);
         }
     }
 };
@@ -256,46 +335,64 @@ __device__ inline double shfl_up_f64(double v, int d) {
     return __hiloint2double(__shfl_up(__double2hiint(v), d), __shfl_up(__double2loint(v), d));
 }
 
-// One wave: lane r brings row r's log decay.  Returns the chunk's total in log2 units.
-template <int C> __device__ inline double scan_decays(Decays<C>& d, float g, float wscale, int lane) {
-    g = g < kMinDecay ? kMinDecay : g;
-    double s = lane < C ? double(g) * 1.4426950408889634 : 0.0;
+// One wave: lane r brings row r's log decay and keeps its values until the chunk's turn.
+template <int C> struct DecayLane {
+    float hi, lo, in, out;
+    __device__ inline double scan(float g, float wscale, int lane) {
+        g = g < kMinDecay ? kMinDecay : g;
+        double s = lane < C ? double(g) * 1.4426950408889634 : 0.0;
 #pragma unroll
-    for (int k = 1; k < C; k <<= 1) {
-        const double o = shfl_up_f64(s, k);
-        if (lane >= k) s += o;
+        for (int k = 1; k < C; k <<= 1) {
+            const double o = shfl_up_f64(s, k);
+            if (lane >= k) s += o;
+        }
+        const double end = __hiloint2double(__shfl(__double2hiint(s), C - 1), __shfl(__double2loint(s), C - 1));
+        hi = float(s);
+        lo = float(s - double(hi));
+        in = __builtin_amdgcn_exp2f(hi);
+        out = wscale * __builtin_amdgcn_exp2f(float(end - s));
+        return end;
     }
-    const double end = __hiloint2double(__shfl(__double2hiint(s), C - 1), __shfl(__double2loint(s), C - 1));
-    if (lane < C) {
-        const float hi = float(s);
-        d.hi[lane] = hi;
-        d.lo[lane] = float(s - double(hi));
-        d.in[lane] = __builtin_amdgcn_exp2f(hi);
-        d.out[lane] = wscale * __builtin_amdgcn_exp2f(float(end - s));
-        if (lane == C - 1) d.all = __builtin_amdgcn_exp2f(hi);
+    __device__ inline void put(Decays<C>& d, int lane) const {
+        if (lane < C) {
+            d.hi[lane] = hi;
+            d.lo[lane] = lo;
+            d.in[lane] = in;
+            d.out[lane] = out;
+            if (lane == C - 1) d.all = in;
+        }
     }
-    return end;
-}
+};
+
+// Blocks of 16 x 32 of P that hold a tile on or below the diagonal: rows 16 it, columns 32 jb.
+__device__ constexpr int p_block(int it, int jb) { return it < 2 ? it : 2 * it - 2 + jb; }
 
 // ---------------------------------------------------------------- the pass
 // One workgroup of four waves walks one piece of one head's sequence for 64 * NT columns
 // of the output.  Each wave keeps the state's 16 * NT columns of its own in registers, in
 // the layout in which the matrix unit leaves a product; the rows of a tile of 16 are
 // numbered (8a + 4t + b for row 4a + b of tile t of a pair) so that a pair of tiles is the
-// right operand of the read-out as it stands, with no exchange between lanes.
+// right operand of the read-out as it stands, with no exchange between lanes.  The decays
+// of keys go to the value rows, so that the state's left operand is the key rows as read.
+//
+// Parts: products that end in a float32 output (the state, the row dots) take three parts
+// of what is not a bf16 input; those that end in a bf16 output take two.
 template <int PARTS, int KD, int NT, int C, int MODE>
 __global__ void __launch_bounds__(kThreads, 2) linattn_pass_kernel(ssm_detail::LinattnPass p) {
     using namespace ssm_detail;
     constexpr bool FULL = MODE >= kLinFull, DOTS = MODE >= kLinDots, CROSS = MODE == kLinCross;
     constexpr int BV = 64 * NT, IT = C / 16, JB = C / 32, KB = KD / 32;
+    constexpr int SP = DOTS || PARTS == 3 ? 3 : 2;    // parts of the state in the read-out
+    constexpr int PP = PARTS == 3 ? 3 : 2;            // parts of P
+    constexpr int NBLK = C == 64 ? 6 : 2, PB = NBLK * 512;
+    static_assert(C == 64 || C == 32, "chunk");
     __shared__ __align__(16) uint16_t X2[PARTS * C * KD];
     __shared__ __align__(16) uint16_t X3[PARTS * C * BV];
     __shared__ __align__(16) uint16_t X1[FULL ? PARTS * C * KD : 8];
-    __shared__ __align__(16) uint16_t PT[FULL ? 2 * C * C : 8];   // decayed x1 . x2, two parts
+    __shared__ __align__(16) uint16_t PT[FULL ? PP * PB : 8];   // decayed x1 . x2
     __shared__ __align__(16) uint16_t X4[DOTS ? PARTS * C * BV : 8];
     __shared__ float part[DOTS ? kWaves * C : 1];
-    __shared__ float rowsum[CROSS ? kWaves * C : 1];
-    __shared__ float colsum[CROSS ? kWaves * C : 1];
+    __shared__ float cross[CROSS ? 2 * 10 * 16 : 1];   // row and column sums of the tiles
     __shared__ Decays<C> dec;
 
     const int tid = threadIdx.x, lane = tid & 63, g4 = lane >> 4, l16 = lane & 15;
@@ -318,6 +415,7 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_pass_kernel(ssm_detail::L
     const int64_t hi = sq.end - lo > p.piece ? lo + p.piece : sq.end;
     const bool last = p.reverse ? local == 0 : hi == sq.end;
     if (!FULL && last) return;                                         // no piece starts from its state
+    const bool rev = p.reverse;
 
     constexpr int E = PARTS == 1 ? 2 : 4;
     const int c_wave = slice * BV + wave * 16 * NT;                    // this wave's first column
@@ -326,9 +424,10 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_pass_kernel(ssm_detail::L
     const char* b3 = static_cast<const char*>(p.x3) + (int64_t(h / p.r3) * p.vd + slice * BV) * E;
     const char* b4 = DOTS ? static_cast<const char*>(p.x4) + (int64_t(h / p.r4) * p.vd + slice * BV) * E : nullptr;
     const int w3 = p.vd - slice * BV;
+    const int64_t pitch1 = p.s1 * E, pitch2 = p.s2 * E, pitch3 = p.s3 * E, pitch4 = p.s4 * E;
 
-    f32x4 S[2 * KB][NT];
     // ------------------------------------------------ starting state
+    f32x4 S[2 * KB][NT];
     const int64_t rs = p.st_t ? 1 : p.vd, cs = p.st_t ? p.kd : 1;
     const int64_t ssz = int64_t(p.kd) * p.vd;
     const float* src = nullptr;
@@ -347,43 +446,65 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_pass_kernel(ssm_detail::L
                 const int row = 32 * (m >> 1) + 8 * g4 + 4 * (m & 1) + r, col = c_wave + 16 * nt + l16;
                 S[m][nt][r] = src && row < p.kd && col < p.vd ? src[row * rs + col * cs] : 0.0f;
             }
-
-    // tiles above the diagonal that share a block of 32 with one on it stay zero
+    // tiles above the diagonal that share a block with one on it stay zero
     if constexpr (FULL) {
-        for (int i = tid; i < 2 * C * C / 2; i += kThreads) reinterpret_cast<uint32_t*>(PT)[i] = 0;
+        for (int i = tid; i < PP * PB / 2; i += kThreads) reinterpret_cast<uint32_t*>(PT)[i] = 0;
     }
 
-    Stage<PARTS, C, KD> t1, t2;
-    Stage<PARTS, C, BV> t3, t4;
-    float gnext = 0.0f;
-    double total = 0.0;
     const int64_t nch = (hi - lo + C - 1) / C;
-    auto fetch = [&](int64_t n) {
-        const int64_t c0 = lo + (p.reverse ? nch - 1 - n : n) * C;
-        if constexpr (FULL) t1.load(b1, p.s1, c0, p.reverse, lo, hi, p.kd, p.vec & 1);
-        t2.load(b2, p.s2, c0, p.reverse, lo, hi, p.kd, p.vec & 2);
-        t3.load(b3, p.s3, c0, p.reverse, lo, hi, w3, p.vec & 4);
-        if constexpr (DOTS) t4.load(b4, p.s4, c0, p.reverse, lo, hi, w3, p.vec & 8);
-        if (wave == 0) {
-            // against time the decay of a step belongs to the later of its two tokens
-            const int64_t t = c0 + (p.reverse ? C - 1 - lane : lane);
-            const int64_t tg = p.reverse ? t + 1 : t;
-            const bool ok = lane < C && t >= lo && t < hi && tg < sq.end;
-            gnext = ok ? p.g[tg * p.sg + h] : 0.0f;
-        }
+    auto first_of = [&](int64_t n) { return lo + (rev ? nch - 1 - n : n) * C; };
+    // the last wave brings the decays, a chunk ahead; against time the decay of a step
+    // belongs to the later of its two tokens
+    constexpr int kDecWave = kWaves - 1;
+    DecayLane<C> dl;
+    double total = 0.0;
+    float gn = 0.0f;
+    auto decay = [&](int64_t n) {
+        const int64_t t = first_of(n) + (rev ? C - 1 - lane : lane), tg = rev ? t + 1 : t;
+        return n < nch && lane < C && t < hi && tg < sq.end ? p.g[tg * p.sg + h] : 0.0f;
     };
-    if (nch > 0) fetch(0);
+    if (wave == kDecWave && nch > 0) {
+        total += dl.scan(decay(0), p.wscale, lane);
+        gn = decay(1);
+    }
 
     for (int64_t n = 0; n < nch; ++n) {
-        const int64_t c0 = lo + (p.reverse ? nch - 1 - n : n) * C;
-        __syncthreads();                        // the last chunk's readers are done
-        if constexpr (FULL) t1.store(X1);
-        t2.store(X2);
-        t3.store(X3);
-        if constexpr (DOTS) t4.store(X4);
-        if (wave == 0) total += scan_decays<C>(dec, gnext, p.wscale, lane);
-        if (n + 1 < nch) fetch(n + 1);
-        __syncthreads();
+        const int64_t c0 = first_of(n);
+        // the lane as the loop's own value: operand addresses are cheap to form anew, and held
+        // across the loop they would take the registers that the state needs
+        int lane = tid & 63;
+        asm volatile("" : "+v"(lane));
+        const int tid = 64 * wave + lane, g4 = lane >> 4, l16 = lane & 15;
+        lds_barrier();                          // the last chunk's readers are done
+        {
+            const int64_t rows = hi - c0;
+            Tile<PARTS, C, KD> t1, t2;
+            Tile<PARTS, C, BV> t3, t4;
+            if (p.wide) {
+                t2.load(X2, tid, b2 + c0 * pitch2, pitch2, rows, rev, p.kd);
+                if constexpr (FULL) t1.load(X1, tid, b1 + c0 * pitch1, pitch1, rows, rev, p.kd);
+                t3.load(X3, tid, b3 + c0 * pitch3, pitch3, rows, rev, w3);
+                if constexpr (DOTS) t4.load(X4, tid, b4 + c0 * pitch4, pitch4, rows, rev, w3);
+                t2.store(X2, tid);
+                if constexpr (FULL) t1.store(X1, tid);
+                t3.store(X3, tid);
+                if constexpr (DOTS) t4.store(X4, tid);
+            } else {
+                t2.copy_any(X2, tid, b2 + c0 * pitch2, pitch2, rows, rev, p.kd);
+                if constexpr (FULL) t1.copy_any(X1, tid, b1 + c0 * pitch1, pitch1, rows, rev, p.kd);
+                t3.copy_any(X3, tid, b3 + c0 * pitch3, pitch3, rows, rev, w3);
+                if constexpr (DOTS) t4.copy_any(X4, tid, b4 + c0 * pitch4, pitch4, rows, rev, w3);
+            }
+        }
+        if (wave == kDecWave) {
+            dl.put(dec, lane);
+            if (n + 1 < nch) {                  // the next chunk's, while this one's rows arrive
+                total += dl.scan(gn, p.wscale, lane);
+                gn = decay(n + 2);
+            }
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        lds_barrier();
 
         f32x4 acc[IT][NT];
         if constexpr (FULL) {
@@ -394,61 +515,53 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_pass_kernel(ssm_detail::L
                 f32x4 a = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb) {
-                    const u32x4 k0 = row_op<KD>(X2, 16 * jt, kb, lane), q0 = row_op<KD>(X1, 16 * it, kb, lane);
-                    a = mma(k0, q0, a);
-                    if constexpr (PARTS == 2) {
-                        const u32x4 k1 = row_op<KD>(X2 + C * KD, 16 * jt, kb, lane);
-                        const u32x4 q1 = row_op<KD>(X1 + C * KD, 16 * it, kb, lane);
-                        a = mma(k1, q0, a);
-                        a = mma(k0, q1, a);
+                    u32x4 k[PARTS], q[PARTS];
+#pragma unroll
+                    for (int i = 0; i < PARTS; ++i) {
+                        k[i] = row_op<KD>(X2 + i * C * KD, 16 * jt, kb, lane);
+                        q[i] = row_op<KD>(X1 + i * C * KD, 16 * it, kb, lane);
                     }
+                    a = mma_parts<PARTS, PARTS>(k, q, a);
                 }
                 const int i = 16 * it + l16, j0 = 16 * jt + 4 * g4;
                 const float gi = dec.hi[i], ei = dec.lo[i];
+                const f32x4 gj = *reinterpret_cast<const f32x4*>(&dec.hi[j0]), ej = *reinterpret_cast<const f32x4*>(&dec.lo[j0]);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const float w = __builtin_amdgcn_exp2f((gi - dec.hi[j0 + r]) + (ei - dec.lo[j0 + r]));
+                    const float w = __builtin_amdgcn_exp2f((gi - gj[r]) + (ei - ej[r]));
                     a[r] = j0 + r <= i ? a[r] * (w * p.wscale) : 0.0f;
                 }
-                uint2 hiw, low;
-                split2(a[0], a[1], hiw.x, low.x);
-                split2(a[2], a[3], hiw.y, low.y);
-                const int o = at_piece<C>(i, j0 >> 3) + (j0 & 7);
-                *reinterpret_cast<uint2*>(PT + o) = hiw;
-                *reinterpret_cast<uint2*>(PT + C * C + o) = low;
+                uint32_t u[PP], v[PP];
+                split<PP>(a[0], a[1], u);
+                split<PP>(a[2], a[3], v);
+                const int o = p_block(it, jt >> 1) * 512 + at_piece<32>(l16, 2 * (jt & 1) + (g4 >> 1)) + 4 * (g4 & 1);
+#pragma unroll
+                for (int k = 0; k < PP; ++k) *reinterpret_cast<uint2*>(PT + k * PB + o) = uint2{u[k], v[k]};
                 if constexpr (CROSS) {
-                    // the other product of the same rows: x3 . x4, over this slice's columns
+                    // the other product of the same rows, x3 . x4 over this slice's columns;
+                    // sums below the diagonal by rows and by columns of the same values
                     f32x4 b = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                     for (int kb = 0; kb < BV / 32; ++kb) {
-                        const u32x4 k0 = row_op<BV>(X3, 16 * jt, kb, lane), q0 = row_op<BV>(X4, 16 * it, kb, lane);
-                        b = mma(k0, q0, b);
-                        if constexpr (PARTS == 2) {
-                            const u32x4 k1 = row_op<BV>(X3 + C * BV, 16 * jt, kb, lane);
-                            const u32x4 q1 = row_op<BV>(X4 + C * BV, 16 * it, kb, lane);
-                            b = mma(k1, q0, b);
-                            b = mma(k0, q1, b);
+                        u32x4 k[PARTS], q[PARTS];
+#pragma unroll
+                        for (int i2 = 0; i2 < PARTS; ++i2) {
+                            k[i2] = row_op<BV>(X3 + i2 * C * BV, 16 * jt, kb, lane);
+                            q[i2] = row_op<BV>(X4 + i2 * C * BV, 16 * it, kb, lane);
                         }
+                        b = mma_parts<PARTS, PARTS>(k, q, b);
                     }
-                    // sums below the diagonal, by rows and by columns of the same products
-                    float row = 0.0f, csum[4];
+                    float row = 0.0f;
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const float x = j0 + r < i ? a[r] * b[r] : 0.0f;
                         row += x;
-                        float col = x;
-#pragma unroll
-                        for (int d = 1; d < 16; d <<= 1) col += __shfl_xor(col, d);
-                        csum[r] = col;
+                        const float col = sum16(x);
+                        if (l16 == 0) cross[160 + 16 * m + 4 * g4 + r] = col;
                     }
                     row += __shfl_xor(row, 16);
                     row += __shfl_xor(row, 32);
-                    // each (tile row, tile column) is one slot: fixed order, no atomics
-                    if (g4 == 0) rowsum[jt * C + i] = row;
-                    if (l16 == 0) {
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) colsum[it * C + j0 + r] = csum[r];
-                    }
+                    if (g4 == 0) cross[16 * m + l16] = row;
                 }
             }
             // ---- the incoming state's share, e^{G_i} R^T x1_i
@@ -458,30 +571,24 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_pass_kernel(ssm_detail::L
                 for (int nt = 0; nt < NT; ++nt) acc[it][nt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
-                u32x4 sh[NT], sl[NT];
+                u32x4 sp[NT][SP];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const f32x4& s = S[2 * kb + (e >> 1)][nt];
-                        uint32_t a, b;
-                        split2(s[2 * (e & 1)], s[2 * (e & 1) + 1], a, b);
-                        sh[nt][e] = a;
-                        sl[nt][e] = b;
+                        uint32_t w[SP];
+                        split<SP>(s[2 * (e & 1)], s[2 * (e & 1) + 1], w);
+#pragma unroll
+                        for (int k = 0; k < SP; ++k) sp[nt][k][e] = w[k];
                     }
 #pragma unroll
                 for (int it = 0; it < IT; ++it) {
-                    const u32x4 q0 = row_op<KD>(X1, 16 * it, kb, lane);
+                    u32x4 q[PARTS];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        acc[it][nt] = mma(q0, sh[nt], acc[it][nt]);
-                        acc[it][nt] = mma(q0, sl[nt], acc[it][nt]);
-                    }
-                    if constexpr (PARTS == 2) {
-                        const u32x4 q1 = row_op<KD>(X1 + C * KD, 16 * it, kb, lane);
+                    for (int i = 0; i < PARTS; ++i) q[i] = row_op<KD>(X1 + i * C * KD, 16 * it, kb, lane);
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) acc[it][nt] = mma(q1, sh[nt], acc[it][nt]);
-                    }
+                    for (int nt = 0; nt < NT; ++nt) acc[it][nt] = mma_parts<PARTS, SP>(q, sp[nt], acc[it][nt]);
                 }
             }
 #pragma unroll
@@ -496,27 +603,23 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_pass_kernel(ssm_detail::L
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const int col = wave * 16 * NT + 16 * nt + l16;
-                            const int o = at_piece<BV>(16 * it + 4 * g4 + r, col >> 3) + (col & 7);
-                            float x = __uint_as_float(uint32_t(X4[o]) << 16);
-                            if constexpr (PARTS == 2) x += __uint_as_float(uint32_t(X4[C * BV + o]) << 16);
-                            d[r] = fmaf(x, acc[it][nt][r], d[r]);
+                        for (int i = 0; i < PARTS; ++i) {
+                            const uint2 x = tile_op<BV>(X4 + i * C * BV, 16 * it, wave * 16 * NT + 16 * nt, lane);
+                            d[0] = fmaf(bf_lo(x.x), acc[it][nt][0], d[0]);
+                            d[1] = fmaf(bf_hi(x.x), acc[it][nt][1], d[1]);
+                            d[2] = fmaf(bf_lo(x.y), acc[it][nt][2], d[2]);
+                            d[3] = fmaf(bf_hi(x.y), acc[it][nt][3], d[3]);
                         }
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        float v = d[r];
-#pragma unroll
-                        for (int k = 1; k < 16; k <<= 1) v += __shfl_xor(v, k);
-                        if (l16 == 0) part[wave * C + 16 * it + 4 * g4 + r] = v;
-                    }
+                    for (int r = 0; r < 4; ++r) d[r] = sum16(d[r]);
+                    if (l16 == 0) *reinterpret_cast<f32x4*>(&part[wave * C + 16 * it + 4 * g4]) = d;
                 }
             }
-            __syncthreads();                    // P (and the dots) are there
+            lds_barrier();                      // P (and the dots) are there
             if constexpr (DOTS) {
                 if (tid < C) {
-                    const int64_t t = c0 + (p.reverse ? C - 1 - tid : tid);
-                    if (t >= lo && t < hi) {
+                    const int64_t t = c0 + (rev ? C - 1 - tid : tid);
+                    if (t < hi) {
                         float v = 0.0f;
 #pragma unroll
                         for (int w = 0; w < kWaves; ++w) v += part[w * C + tid];
@@ -525,8 +628,8 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_pass_kernel(ssm_detail::L
                         if constexpr (CROSS) {
                             const int it = tid >> 4;
                             float rsv = 0.0f, csv = 0.0f;
-                            for (int m = 0; m <= it; ++m) rsv += rowsum[m * C + tid];
-                            for (int m = it; m < IT; ++m) csv += colsum[m * C + tid];
+                            for (int m = 0; m <= it; ++m) rsv += cross[16 * (it * (it + 1) / 2 + m) + l16];
+                            for (int m = it; m < IT; ++m) csv += cross[160 + 16 * (m * (m + 1) / 2 + it) + l16];
                             p.cross[o] = (rsv - csv) * p.oscale;
                         }
                     }
@@ -535,29 +638,6 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_pass_kernel(ssm_detail::L
         }
 
         // ---- the chunk's own share, P x3, and the outgoing state
-        u32x4 v0[JB][NT], v1[PARTS == 2 ? JB : 1][NT];
-#pragma unroll
-        for (int jb = 0; jb < JB; ++jb)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                v0[jb][nt] = col_op<BV, 0>(X3, 32 * jb, wave * 16 * NT + 16 * nt, lane);
-                if constexpr (PARTS == 2)
-                    v1[jb][nt] = col_op<BV, 0>(X3 + C * BV, 32 * jb, wave * 16 * NT + 16 * nt, lane);
-            }
-        if constexpr (FULL) {
-#pragma unroll
-            for (int it = 0; it < IT; ++it)
-#pragma unroll
-                for (int jb = 0; jb <= it / 2; ++jb) {
-                    const u32x4 p0 = row_op<C>(PT, 16 * it, jb, lane), p1 = row_op<C>(PT + C * C, 16 * it, jb, lane);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        acc[it][nt] = mma(p0, v0[jb][nt], acc[it][nt]);
-                        acc[it][nt] = mma(p1, v0[jb][nt], acc[it][nt]);
-                        if constexpr (PARTS == 2) acc[it][nt] = mma(p0, v1[jb][nt], acc[it][nt]);
-                    }
-                }
-        }
         const float all = dec.all;
 #pragma unroll
         for (int m = 0; m < 2 * KB; ++m)
@@ -567,60 +647,104 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_pass_kernel(ssm_detail::L
                 for (int r = 0; r < 4; ++r) S[m][nt][r] *= all;
 #pragma unroll
         for (int jb = 0; jb < JB; ++jb) {
-            u32x4 vh[NT], vl[NT];
+            u32x4 v[NT][PARTS];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < PARTS; ++i)
+                    v[nt][i] = col_op<BV, 0>(X3 + i * C * BV, 32 * jb, wave * 16 * NT + 16 * nt, lane);
+            if constexpr (FULL) {
+#pragma unroll
+                for (int it = 2 * jb; it < IT; ++it) {
+                    u32x4 q[PP];
+#pragma unroll
+                    for (int k = 0; k < PP; ++k) q[k] = row_op<32>(PT + k * PB + p_block(it, jb) * 512, 0, 0, lane);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) acc[it][nt] = mma_parts<PP, PARTS>(q, v[nt], acc[it][nt]);
+                }
+            }
+            u32x4 vp[NT][3];
             const f32x4 f0 = *reinterpret_cast<const f32x4*>(&dec.out[32 * jb + 8 * g4]);
             const f32x4 f1 = *reinterpret_cast<const f32x4*>(&dec.out[32 * jb + 8 * g4 + 4]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    float x = bf_lo(v0[jb][nt][e]), y = bf_hi(v0[jb][nt][e]);
-                    if constexpr (PARTS == 2) {
-                        x += bf_lo(v1[jb][nt][e]);
-                        y += bf_hi(v1[jb][nt][e]);
+                    float x = 0.0f, y = 0.0f;
+#pragma unroll
+                    for (int i = PARTS - 1; i >= 0; --i) {
+                        x += bf_lo(v[nt][i][e]);
+                        y += bf_hi(v[nt][i][e]);
                     }
                     const f32x4& f = e < 2 ? f0 : f1;
-                    uint32_t a, b;
-                    split2(x * f[2 * (e & 1)], y * f[2 * (e & 1) + 1], a, b);
-                    vh[nt][e] = a;
-                    vl[nt][e] = b;
+                    uint32_t w[3];
+                    split<3>(x * f[2 * (e & 1)], y * f[2 * (e & 1) + 1], w);
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) vp[nt][k][e] = w[k];
                 }
 #pragma unroll
             for (int m = 0; m < 2 * KB; ++m) {
-                const u32x4 k0 = col_op<KD, 1>(X2, 32 * jb, 32 * (m >> 1) + 4 * (m & 1), lane);
+                u32x4 k[PARTS];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    S[m][nt] = mma(k0, vh[nt], S[m][nt]);
-                    S[m][nt] = mma(k0, vl[nt], S[m][nt]);
-                }
-                if constexpr (PARTS == 2) {
-                    const u32x4 k1 = col_op<KD, 1>(X2 + C * KD, 32 * jb, 32 * (m >> 1) + 4 * (m & 1), lane);
+                for (int i = 0; i < PARTS; ++i)
+                    k[i] = col_op<KD, 1>(X2 + i * C * KD, 32 * jb, 32 * (m >> 1) + 4 * (m & 1), lane);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) S[m][nt] = mma(k1, vh[nt], S[m][nt]);
-                }
+                for (int nt = 0; nt < NT; ++nt) S[m][nt] = mma_parts<PARTS, 3>(k, vp[nt], S[m][nt]);
             }
         }
 
         if constexpr (FULL) {
+            // rows behind the piece's end fall outside the window
+            const int oe = PARTS == 3 || p.out_f32 ? 4 : 2;
+            const int64_t pitch = p.so * oe;
+            const Rsrc ro = rows_rsrc(static_cast<char*>(p.out) + c0 * pitch + int64_t(h) * p.vd * oe, pitch, hi - c0, C);
+            if (oe == 4) {
 #pragma unroll
-            for (int it = 0; it < IT; ++it)
+                for (int it = 0; it < IT; ++it)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = 16 * it + 4 * g4 + r;
-                    const int64_t t = c0 + (p.reverse ? C - 1 - row : row);
-                    if (t < lo || t >= hi) continue;
+                    for (int r = 0; r < 4; ++r) {
+                        const int row = 16 * it + 4 * g4 + r;
+                        const uint32_t ob = uint32_t((rev ? C - 1 - row : row) * pitch);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const int col = c_wave + 16 * nt + l16;
-                        if (col >= p.vd) continue;
-                        const int64_t o = t * p.so + int64_t(h) * p.vd + col;
-                        const float x = acc[it][nt][r] * p.oscale;
-                        if (PARTS == 2 || p.out_f32)
-                            static_cast<float*>(p.out)[o] = x;
-                        else
-                            static_cast<uint16_t*>(p.out)[o] = IOT<uint16_t>::from_f32(x);
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const int col = c_wave + 16 * nt + l16;
+                            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[it][nt][r] * p.oscale), ro,
+                                                                  col < p.vd ? ob + 4 * col : kPast, 0, 0);
+                        }
                     }
-                }
+            } else if (p.pairs) {
+                // neighbouring lanes swap one row for another: two columns of one row each
+                const bool odd = lane & 1;
+#pragma unroll
+                for (int it = 0; it < IT; ++it)
+#pragma unroll
+                    for (int r = 0; r < 4; r += 2) {
+                        const int row = 16 * it + 4 * g4 + r + odd;
+                        const uint32_t ob = uint32_t((rev ? C - 1 - row : row) * pitch);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const float x = acc[it][nt][r] * p.oscale, y = acc[it][nt][r + 1] * p.oscale;
+                            const float got = swap1(odd ? x : y);
+                            const int col = c_wave + 16 * nt + (l16 & ~1);
+                            __builtin_amdgcn_raw_buffer_store_b32(odd ? pack2(got, y) : pack2(x, got), ro,
+                                                                  col < p.vd ? ob + 2 * col : kPast, 0, 0);
+                        }
+                    }
+            } else {
+#pragma unroll
+                for (int it = 0; it < IT; ++it)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int row = 16 * it + 4 * g4 + r;
+                        const uint32_t ob = uint32_t((rev ? C - 1 - row : row) * pitch);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const int col = c_wave + 16 * nt + l16;
+                            __builtin_amdgcn_raw_buffer_store_b16(IOT<uint16_t>::from_f32(acc[it][nt][r] * p.oscale), ro,
+                                                                  col < p.vd ? ob + 2 * col : kPast, 0, 0);
+                        }
+                    }
+            }
         }
     }
 
@@ -631,14 +755,14 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_pass_kernel(ssm_detail::L
         if (last && p.s_out) {
             dst = p.s_out + (int64_t(slot) * p.H + h) * ssz;
             // against time the state before the first token has that token's decay too
-            if (p.reverse && sq.end > sq.start) {
+            if (rev && sq.end > sq.start) {
                 const float g = p.g[sq.start * p.sg + h];
                 mul = __builtin_amdgcn_exp2f((g < kMinDecay ? kMinDecay : g) * kLog2e);
             }
         }
     } else {
         dst = p.carry + (pi * p.H + h) * ssz;
-        if (wave == 0 && lane == 0 && slice == 0) p.tot[pi * p.H + h] = __builtin_amdgcn_exp2f(float(total));
+        if (wave == kDecWave && lane == 0 && slice == 0) p.tot[pi * p.H + h] = __builtin_amdgcn_exp2f(float(total));
     }
     if (dst) {
 #pragma unroll
@@ -658,19 +782,20 @@ template <int MODE> inline bool launch_pass(const ssm_detail::LinattnPass& p, bo
     const int64_t blocks = int64_t(p.npieces) * p.H * p.nslices;
     const dim3 grid(static_cast<uint32_t>(blocks)), block(kThreads);
     const bool two = ssm_detail::linattn_slice(p.kd, p.vd) == 128;
-#define SSM_LIN_CASE(K, NTV, CF)                                                                    \
+    // float32 rows take three times the LDS: chunks of 32 keep two workgroups on a CU
+#define SSM_LIN_CASE(K, NTV)                                                                        \
     do {                                                                                            \
         if (f32)                                                                                    \
-            launch_kernel(linattn_pass_kernel<2, K, NTV, CF, MODE>, grid, block, 0, s, p);           \
+            launch_kernel(linattn_pass_kernel<3, K, NTV, 32, MODE>, grid, block, 0, s, p);           \
         else                                                                                        \
             launch_kernel(linattn_pass_kernel<1, K, NTV, 64, MODE>, grid, block, 0, s, p);           \
     } while (0)
     if (p.kd <= 64) {
-        if (two) SSM_LIN_CASE(64, 2, 64); else SSM_LIN_CASE(64, 1, 64);
+        if (two) SSM_LIN_CASE(64, 2); else SSM_LIN_CASE(64, 1);
     } else if (p.kd <= 128) {
-        if (two) SSM_LIN_CASE(128, 2, 32); else SSM_LIN_CASE(128, 1, 32);
+        if (two) SSM_LIN_CASE(128, 2); else SSM_LIN_CASE(128, 1);
     } else if (p.kd <= 256) {
-        SSM_LIN_CASE(256, 1, 32);
+        SSM_LIN_CASE(256, 1);
     } else {
         return false;
     }
@@ -698,6 +823,8 @@ inline int check_dims(const ssm_linattn_dims* d, Sizes* z) {
     z->v = d->v_stride ? d->v_stride : d->nheads * d->dv;
     z->o = d->o_stride ? d->o_stride : d->nheads * d->dv;
     const int64_t lim = int64_t(1) << 40;
+    // output windows of a chunk stay below 2^31 bytes
+    if (z->o * (d->io_dtype == SSM_BF16 ? 2 : 4) >= (int64_t(1) << 24)) return SSM_ERR_DIMS;
     if (z->q < d->kheads * d->dk || z->k < d->kheads * d->dk || z->v < d->nheads * d->dv || z->o < d->nheads * d->dv)
         return SSM_ERR_DIMS;
     for (const int64_t s : {z->q, z->k, z->v, z->o})
@@ -708,10 +835,13 @@ inline int check_dims(const ssm_linattn_dims* d, Sizes* z) {
 
 inline size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-inline bool rows16(const void* q, int64_t stride, int64_t width, int64_t e) {
-    return !misaligned(q, 16) && stride * e % 16 == 0 && width * e % 16 == 0 && width % 8 == 0;
+// Rows that the 16-byte loads at 32-bit offsets of a chunk can take.
+inline bool wide_rows(const void* q, int64_t stride, int64_t width, int64_t e) {
+    return !misaligned(q, 16) && stride * e % 16 == 0 && width % 8 == 0 && stride * e < (int64_t(1) << 24);
 }
-
+inline bool pair_rows(const void* q, int64_t stride, int64_t width) {
+    return !misaligned(q, 4) && stride % 2 == 0 && width % 2 == 0;
+}
 
 }  // namespace la
 }  // namespace

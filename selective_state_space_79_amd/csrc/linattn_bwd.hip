@@ -279,8 +279,6 @@ int ssm_linattn_bwd(const void* q, const void* k, const void* v, const float* g,
     const int32_t rep = static_cast<int32_t>(d.nheads / d.kheads);
     const bool f32 = d.io_dtype == SSM_F32, shared = rep > 1;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const int bq = rows16(q, z.q, d.dk, z.e), bk = rows16(k, z.k, d.dk, z.e), bv = rows16(v, z.v, d.dv, z.e),
-              bo = rows16(dout, z.o, d.dv, z.e);
 
     LinattnPass base = {};
     base.g = g; base.cu = cu_seqlens; base.sg = d.head_decay ? 0 : d.nheads;
@@ -290,29 +288,31 @@ int ssm_linattn_bwd(const void* q, const void* k, const void* v, const float* g,
     base.nseq = static_cast<int32_t>(d.nseq); base.nslots = base.nseq;
     base.r1 = base.r2 = base.r3 = base.r4 = 1;
     base.wscale = base.oscale = 1.0f;
+    base.wide = wide_rows(q, z.q, d.dk, z.e) && wide_rows(k, z.k, d.dk, z.e) && wide_rows(v, z.v, d.dv, z.e) &&
+                wide_rows(dout, z.o, d.dv, z.e);
 
     // S in order of time: (k, v); dS against it: (q, do)
     LinattnPass sf = base;
     sf.x2 = k; sf.s2 = z.k; sf.r2 = rep; sf.x3 = v; sf.s3 = z.v;
     sf.kd = static_cast<int32_t>(d.dk); sf.vd = static_cast<int32_t>(d.dv); sf.nslices = static_cast<int32_t>(pl.slices_s);
-    sf.s_in = s0; sf.carry = fwd; sf.tot = totf; sf.vec = bk << 1 | bv << 2;
+    sf.s_in = s0; sf.carry = fwd; sf.tot = totf;
     LinattnPass sr = sf;
     sr.x2 = q; sr.s2 = z.q; sr.x3 = dout; sr.s3 = z.o; sr.s_in = ds_last; sr.carry = rev; sr.tot = totr;
-    sr.reverse = 1; sr.wscale = d.scale; sr.vec = bq << 1 | bo << 2;
+    sr.reverse = 1; sr.wscale = d.scale;
 
     LinattnPass pq = base;   // dq = (do, v, k) from S
     pq.x1 = dout; pq.s1 = z.o; pq.x2 = v; pq.s2 = z.v; pq.x3 = k; pq.s3 = z.k; pq.r3 = rep; pq.x4 = q; pq.s4 = z.q; pq.r4 = rep;
     pq.kd = static_cast<int32_t>(d.dv); pq.vd = static_cast<int32_t>(d.dk); pq.nslices = static_cast<int32_t>(pl.slices_q);
     pq.s_in = s0; pq.st_t = 1; pq.carry = fwd; pq.oscale = d.scale;
     pq.out = shared ? static_cast<void*>(wq) : gr.dq; pq.out_f32 = shared; pq.so = d.nheads * d.dk;
-    pq.dots = da; pq.cross = de; pq.vec = bo | bv << 1 | bk << 2 | bq << 3;
+    pq.dots = da; pq.cross = de; pq.pairs = pair_rows(gr.dq, pq.so, d.dk);
     LinattnPass pk = pq;     // dk = (v, do, q) from dS
     pk.x1 = v; pk.s1 = z.v; pk.x2 = dout; pk.s2 = z.o; pk.x3 = q; pk.s3 = z.q; pk.x4 = k; pk.s4 = z.k;
     pk.s_in = ds_last; pk.carry = rev; pk.oscale = 1.0f; pk.wscale = d.scale; pk.reverse = 1;
     pk.out = shared ? static_cast<void*>(wkk) : gr.dk; pk.dots = db; pk.cross = nullptr;
-    pk.vec = bv | bo << 1 | bq << 2 | bk << 3;
+    pk.pairs = pair_rows(gr.dk, pk.so, d.dk);
     LinattnPass pv = sr;     // dv = (k, q, do) from dS
-    pv.x1 = k; pv.s1 = z.k; pv.r1 = rep; pv.out = gr.dv; pv.so = wv; pv.s_out = gr.ds0; pv.vec = sr.vec | bk;
+    pv.x1 = k; pv.s1 = z.k; pv.r1 = rep; pv.out = gr.dv; pv.so = wv; pv.s_out = gr.ds0; pv.pairs = pair_rows(gr.dv, wv, d.dv);
 
     launch_error = hipSuccess;
     if (pl.pieced) {

@@ -240,7 +240,8 @@ int ssm_linattn_fwd(const void* q, const void* k, const void* v, const float* g,
     p.nslices = static_cast<int32_t>(cdiv(d.dv, ssm_detail::linattn_slice(d.dk, d.dv)));
     p.nseq = static_cast<int32_t>(d.nseq); p.nslots = static_cast<int32_t>(states ? d.nslots : d.nseq);
     p.npieces = static_cast<int32_t>(pl.npieces); p.pieced = pl.pieced;
-    p.vec = (rows16(q, z.q, d.dk, z.e) ? 1 : 0) | (rows16(k, z.k, d.dk, z.e) ? 2 : 0) | (rows16(v, z.v, d.dv, z.e) ? 4 : 0);
+    p.wide = wide_rows(q, z.q, d.dk, z.e) && wide_rows(k, z.k, d.dk, z.e) && wide_rows(v, z.v, d.dv, z.e);
+    p.pairs = pair_rows(o, z.o, d.dv);
     p.wscale = 1.0f; p.oscale = d.scale;
     const bool f32 = d.io_dtype == SSM_F32;
     hipStream_t s = static_cast<hipStream_t>(stream);
