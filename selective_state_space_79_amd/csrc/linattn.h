@@ -56,7 +56,7 @@ bool launch_linattn_pass(const LinattnPass& p, bool f32, LinattnMode mode, hipSt
 bool launch_linattn_grad_pass(const LinattnPass& p, bool f32, LinattnMode mode, hipStream_t s);  // modes 2, 3
 void launch_linattn_carry(const LinattnPass& p, hipStream_t s);
 // columns of the output that one workgroup computes
-int linattn_slice(int64_t kd, int64_t vd);
+int linattn_slice(int64_t vd);
 
 }  // namespace ssm_detail
 
@@ -219,6 +219,13 @@ __device__ inline float swap1(float v) {
     return __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(v), 0xB1, 0xf, 0xf, true));
 }
 
+// Waits until at most N vector-memory operations are under way (the instruction's own
+// encoding, so that the compiler counts from it too).
+template <int N> __device__ inline void wait_memory() {
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+    asm volatile("" ::: "memory");
+}
+
 // Barrier for LDS traffic only: outstanding loads of the next chunk are not waited for.
 __device__ inline void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
@@ -242,19 +249,19 @@ __device__ inline void load_lds16(Rsrc r, void* lds, uint32_t voff) {
 
 // A tile of C rows of W columns from memory to LDS.  bf16 rows (PARTS 1) go straight there,
 // each lane fetching the piece that its slot of the permuted row holds; float32 rows
-// (PARTS 3) pass through registers, where they are split.  No copy of the next chunk is held
-// back: the other workgroup of the CU computes while this one's loads are in flight.
-template <int PARTS, int C, int W> struct Tile {
-    static constexpr int N = C * W / 8 / kThreads;   // pieces of 8 values per thread
-    static_assert(C * W / 8 % kThreads == 0, "whole pieces per thread");
+// (PARTS 3) pass through registers, where they are split.
+template <int PARTS, int C, int W, int T> struct Tile {   // T threads
+    static constexpr bool HALF = C * W / 8 < T;                 // fewer pieces of 8 values than threads
+    static constexpr int N = HALF ? 1 : C * W / 8 / T;          // pieces per thread
+    static_assert(HALF ? PARTS > 1 : C * W / 8 % T == 0, "whole pieces per thread");
     static constexpr int E = PARTS == 1 ? 2 : 4;
-    static constexpr int RS = kThreads / (W / 8);    // rows between a thread's pieces
+    static constexpr int RS = T / (W / 8);    // rows between a thread's pieces
     static constexpr int Q = PARTS == 1 ? 1 : 2;     // 16-byte loads per piece
 
     __device__ static inline uint32_t offset(int tid, int n, int pitch, bool rev, int w) {
         const int rr = tid / (W / 8) + RS * n, slot = tid % (W / 8);
         const int col = 8 * (PARTS == 1 ? slot ^ twist<W>(rr) : slot);
-        return col < w ? uint32_t((rev ? C - 1 - rr : rr) * pitch + col * E) : kPast;
+        return col < w && (!HALF || rr < C) ? uint32_t((rev ? C - 1 - rr : rr) * pitch + col * E) : kPast;
     }
     u32x4 r[PARTS == 1 ? 1 : N][Q];
 
@@ -264,7 +271,7 @@ template <int PARTS, int C, int W> struct Tile {
         for (int n = 0; n < N; ++n) {
             const uint32_t o = offset(tid, n, int(pitch), rev, w);
             if constexpr (PARTS == 1) {
-                load_lds16(b, tile + 8 * (kThreads * n + (__builtin_amdgcn_readfirstlane(tid) & ~63)), o);
+                load_lds16(b, tile + 8 * (T * n + (__builtin_amdgcn_readfirstlane(tid) & ~63)), o);
             } else {
 #pragma unroll
                 for (int h = 0; h < Q; ++h)
@@ -276,7 +283,8 @@ template <int PARTS, int C, int W> struct Tile {
     __device__ inline void store(uint16_t* tile, int tid) const {
         if constexpr (PARTS > 1) {
 #pragma unroll
-            for (int n = 0; n < N; ++n) put(tile, tid + kThreads * n, r[n]);
+            for (int n = 0; n < N; ++n)
+                if (!HALF || tid < C * W / 8) put(tile, tid + T * n, r[n]);
         }
     }
     __device__ static inline void put(uint16_t* tile, int idx, const u32x4 (&x)[Q]) {
@@ -301,7 +309,8 @@ template <int PARTS, int C, int W> struct Tile {
                                            int w) {
 #pragma unroll 1
         for (int n = 0; n < N; ++n) {
-            const int idx = tid + kThreads * n;
+            const int idx = tid + T * n;
+            if (HALF && idx >= C * W / 8) break;
             const int col = 8 * (idx % (W / 8)), rr = rev ? C - 1 - idx / (W / 8) : idx / (W / 8);
             const char* q = row0 + rr * pitch + col * E;
             u32x4 x[Q];
@@ -368,32 +377,43 @@ template <int C> struct DecayLane {
 __device__ constexpr int p_block(int it, int jb) { return it < 2 ? it : 2 * it - 2 + jb; }
 
 // ---------------------------------------------------------------- the pass
-// One workgroup of four waves walks one piece of one head's sequence for 64 * NT columns
-// of the output.  Each wave keeps the state's 16 * NT columns of its own in registers, in
-// the layout in which the matrix unit leaves a product; the rows of a tile of 16 are
-// numbered (8a + 4t + b for row 4a + b of tile t of a pair) so that a pair of tiles is the
-// right operand of the read-out as it stands, with no exchange between lanes.  The decays
-// of keys go to the value rows, so that the state's left operand is the key rows as read.
+// One workgroup walks one piece of one head's sequence for 16 columns of the output per
+// wave.  Each wave keeps the state's columns of its own in registers, in the layout in which
+// the matrix unit leaves a product; the rows of a tile of 16 are numbered (8a + 4t + b for
+// row 4a + b of tile t of a pair) so that a pair of tiles is the right operand of the
+// read-out as it stands, with no exchange between lanes.  The decays of keys go to the value
+// rows, so that the state's left operand is the key rows as read.
+//
+// Eight waves (128 columns) share the tiles and the products x1 . x2, and two such
+// workgroups fit a CU up to 128 state rows; narrow heads take four waves.
 //
 // Parts: products that end in a float32 output (the state, the row dots) take three parts
 // of what is not a bf16 input; those that end in a bf16 output take two.
-template <int PARTS, int KD, int NT, int C, int MODE>
-__global__ void __launch_bounds__(kThreads, 2) linattn_pass_kernel(ssm_detail::LinattnPass p) {
+constexpr int pass_waves(int KD, int NW) { return KD == 256 ? NW / 4 : NW / 2; }   // per SIMD
+
+template <int PARTS, int KD, int NW, int C, int MODE>
+__global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW)) linattn_pass_kernel(ssm_detail::LinattnPass p) {
     using namespace ssm_detail;
     constexpr bool FULL = MODE >= kLinFull, DOTS = MODE >= kLinDots, CROSS = MODE == kLinCross;
-    constexpr int BV = 64 * NT, IT = C / 16, JB = C / 32, KB = KD / 32;
+    constexpr int T = 64 * NW, BV = 16 * NW, IT = C / 16, JB = C / 32, KB = KD / 32;
+    constexpr int NTILE = IT * (IT + 1) / 2, MT = (NTILE + NW - 1) / NW;   // tiles of P, and the most of one wave
     constexpr int SP = DOTS || PARTS == 3 ? 3 : 2;    // parts of the state in the read-out
     constexpr int PP = PARTS == 3 ? 3 : 2;            // parts of P
     constexpr int NBLK = C == 64 ? 6 : 2, PB = NBLK * 512;
     static_assert(C == 64 || C == 32, "chunk");
-    __shared__ __align__(16) uint16_t X2[PARTS * C * KD];
-    __shared__ __align__(16) uint16_t X3[PARTS * C * BV];
+    // bf16 rows come straight into LDS, each tile as soon as the last chunk's readers are
+    // done with it: x2 (read to the end) and without a read-out x3 have a second tile
+    constexpr bool DMA = PARTS == 1, TWO2 = DMA && !DOTS, TWO3 = DMA && !FULL;
+    __shared__ __align__(16) uint16_t X2a[PARTS * C * KD], X2b[TWO2 ? C * KD : 8];
+    __shared__ __align__(16) uint16_t X3a[PARTS * C * BV], X3b[TWO3 ? C * BV : 8];
     __shared__ __align__(16) uint16_t X1[FULL ? PARTS * C * KD : 8];
     __shared__ __align__(16) uint16_t PT[FULL ? PP * PB : 8];   // decayed x1 . x2
     __shared__ __align__(16) uint16_t X4[DOTS ? PARTS * C * BV : 8];
-    __shared__ float part[DOTS ? kWaves * C : 1];
-    __shared__ float cross[CROSS ? 2 * 10 * 16 : 1];   // row and column sums of the tiles
-    __shared__ Decays<C> dec;
+    __shared__ Decays<C> decs[2];
+    // row dots, and the tiles' row and column sums: over x1, once its readers are done
+    float* part = reinterpret_cast<float*>(X1);
+    float* cross = part + NW * C;
+    static_assert(!DOTS || PARTS * C * KD * 2 >= (NW * C + 32 * NTILE) * 4, "the sums fit x1's tile");
 
     const int tid = threadIdx.x, lane = tid & 63, g4 = lane >> 4, l16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -418,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_pass_kernel(ssm_detail::L
     const bool rev = p.reverse;
 
     constexpr int E = PARTS == 1 ? 2 : 4;
-    const int c_wave = slice * BV + wave * 16 * NT;                    // this wave's first column
+    const int c_wave = slice * BV + wave * 16;                         // this wave's first column
     const char* b1 = FULL ? static_cast<const char*>(p.x1) + int64_t(h / p.r1) * p.kd * E : nullptr;
     const char* b2 = static_cast<const char*>(p.x2) + int64_t(h / p.r2) * p.kd * E;
     const char* b3 = static_cast<const char*>(p.x3) + (int64_t(h / p.r3) * p.vd + slice * BV) * E;
@@ -427,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_pass_kernel(ssm_detail::L
     const int64_t pitch1 = p.s1 * E, pitch2 = p.s2 * E, pitch3 = p.s3 * E, pitch4 = p.s4 * E;
 
     // ------------------------------------------------ starting state
-    f32x4 S[2 * KB][NT];
+    f32x4 S[2 * KB];
     const int64_t rs = p.st_t ? 1 : p.vd, cs = p.st_t ? p.kd : 1;
     const int64_t ssz = int64_t(p.kd) * p.vd;
     const float* src = nullptr;
@@ -440,22 +460,20 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_pass_kernel(ssm_detail::L
 #pragma unroll
     for (int m = 0; m < 2 * KB; ++m)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = 32 * (m >> 1) + 8 * g4 + 4 * (m & 1) + r, col = c_wave + 16 * nt + l16;
-                S[m][nt][r] = src && row < p.kd && col < p.vd ? src[row * rs + col * cs] : 0.0f;
-            }
+        for (int r = 0; r < 4; ++r) {
+            const int row = 32 * (m >> 1) + 8 * g4 + 4 * (m & 1) + r, col = c_wave + l16;
+            S[m][r] = src && row < p.kd && col < p.vd ? src[row * rs + col * cs] : 0.0f;
+        }
     // tiles above the diagonal that share a block with one on it stay zero
     if constexpr (FULL) {
-        for (int i = tid; i < PP * PB / 2; i += kThreads) reinterpret_cast<uint32_t*>(PT)[i] = 0;
+        for (int i = tid; i < PP * PB / 2; i += T) reinterpret_cast<uint32_t*>(PT)[i] = 0;
     }
 
     const int64_t nch = (hi - lo + C - 1) / C;
     auto first_of = [&](int64_t n) { return lo + (rev ? nch - 1 - n : n) * C; };
     // the last wave brings the decays, a chunk ahead; against time the decay of a step
     // belongs to the later of its two tokens
-    constexpr int kDecWave = kWaves - 1;
+    constexpr int kDecWave = NW - 1;
     DecayLane<C> dl;
     double total = 0.0;
     float gn = 0.0f;
@@ -465,26 +483,67 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_pass_kernel(ssm_detail::L
     };
     if (wave == kDecWave && nch > 0) {
         total += dl.scan(decay(0), p.wscale, lane);
+        dl.put(decs[0], lane);
         gn = decay(1);
     }
+    Tile<PARTS, C, KD, T> t1, t2;
+    Tile<PARTS, C, BV, T> t3, t4;
+    // the tile of chunk n, at once (bf16) or into registers; `any` rows are copied at the
+    // chunk's own turn
+    auto load1 = [&](int64_t n, int tid) {
+        const int64_t c0 = first_of(n);
+        t1.load(X1, tid, b1 + c0 * pitch1, pitch1, hi - c0, rev, p.kd);
+    };
+    auto load2 = [&](int64_t n, int tid, uint16_t* to) {
+        const int64_t c0 = first_of(n);
+        t2.load(to, tid, b2 + c0 * pitch2, pitch2, hi - c0, rev, p.kd);
+    };
+    auto load3 = [&](int64_t n, int tid, uint16_t* to) {
+        const int64_t c0 = first_of(n);
+        t3.load(to, tid, b3 + c0 * pitch3, pitch3, hi - c0, rev, w3);
+    };
+    auto load4 = [&](int64_t n, int tid) {
+        const int64_t c0 = first_of(n);
+        t4.load(X4, tid, b4 + c0 * pitch4, pitch4, hi - c0, rev, w3);
+    };
+    const bool ahead = DMA && p.wide;          // tiles are loaded ahead of their chunk
+    if (ahead && nch > 0) {
+        load2(0, tid, X2a);
+        load3(0, tid, X3a);
+        if constexpr (FULL) load1(0, tid);
+        if constexpr (DOTS) load4(0, tid);
+    }
+    wait_memory<0>();
 
-    for (int64_t n = 0; n < nch; ++n) {
+    // one chunk; ODD picks the tiles of odd chunks where there are two
+    auto chunk = [&](const int64_t n, auto odd_c) {
+        constexpr bool ODD = decltype(odd_c)::value;
+        uint16_t* const X2 = TWO2 && ODD ? X2b : X2a;
+        uint16_t* const X3 = TWO3 && ODD ? X3b : X3a;
+        Decays<C>& dec = decs[ODD];
         const int64_t c0 = first_of(n);
         // the lane as the loop's own value: operand addresses are cheap to form anew, and held
         // across the loop they would take the registers that the state needs
-        int lane = tid & 63;
+        int lane = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
         asm volatile("" : "+v"(lane));
         const int tid = 64 * wave + lane, g4 = lane >> 4, l16 = lane & 15;
-        lds_barrier();                          // the last chunk's readers are done
-        {
+        if (ahead) {
+            // this chunk's rows; what was stored since they were asked for may still be under way
+            if constexpr (!FULL || DOTS)
+                wait_memory<0>();
+            else if (p.pairs)
+                wait_memory<2 * IT>();
+            else
+                wait_memory<4 * IT>();
+            lds_barrier();
+        } else {
+            lds_barrier();                      // the last chunk's readers are done
             const int64_t rows = hi - c0;
-            Tile<PARTS, C, KD> t1, t2;
-            Tile<PARTS, C, BV> t3, t4;
             if (p.wide) {
-                t2.load(X2, tid, b2 + c0 * pitch2, pitch2, rows, rev, p.kd);
-                if constexpr (FULL) t1.load(X1, tid, b1 + c0 * pitch1, pitch1, rows, rev, p.kd);
-                t3.load(X3, tid, b3 + c0 * pitch3, pitch3, rows, rev, w3);
-                if constexpr (DOTS) t4.load(X4, tid, b4 + c0 * pitch4, pitch4, rows, rev, w3);
+                load2(n, tid, X2);
+                if constexpr (FULL) load1(n, tid);
+                load3(n, tid, X3);
+                if constexpr (DOTS) load4(n, tid);
                 t2.store(X2, tid);
                 if constexpr (FULL) t1.store(X1, tid);
                 t3.store(X3, tid);
@@ -495,21 +554,38 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_pass_kernel(ssm_detail::L
                 t3.copy_any(X3, tid, b3 + c0 * pitch3, pitch3, rows, rev, w3);
                 if constexpr (DOTS) t4.copy_any(X4, tid, b4 + c0 * pitch4, pitch4, rows, rev, w3);
             }
+            lds_barrier();
         }
-        if (wave == kDecWave) {
-            dl.put(dec, lane);
-            if (n + 1 < nch) {                  // the next chunk's, while this one's rows arrive
+        // the next chunk's decays, and what can be loaded of its rows; behind the last write to
+        // LDS of this phase, which otherwise waits for loads into LDS that are under way
+        auto next = [&] {
+            if (wave == kDecWave && n + 1 < nch) {
                 total += dl.scan(gn, p.wscale, lane);
+                dl.put(decs[!ODD], lane);
                 gn = decay(n + 2);
             }
-        }
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        lds_barrier();
+            if (ahead && n + 1 < nch) {
+                if constexpr (TWO2) load2(n + 1, tid, ODD ? X2a : X2b);
+                if constexpr (TWO3) load3(n + 1, tid, ODD ? X3a : X3b);
+            }
+        };
+        // the value rows of this wave's columns
+        u32x4 v[JB][PARTS];
+        auto values = [&] {
+#pragma unroll
+            for (int jb = 0; jb < JB; ++jb)
+#pragma unroll
+                for (int i = 0; i < PARTS; ++i) v[jb][i] = col_op<BV, 0>(X3 + i * C * BV, 32 * jb, wave * 16, lane);
+        };
 
-        f32x4 acc[IT][NT];
+        f32x4 acc[IT];
         if constexpr (FULL) {
             // ---- P = x1 . x2 under the decays, tiles of 16 x 16 on and below the diagonal
-            for (int m = wave; m < IT * (IT + 1) / 2; m += kWaves) {
+            float rsum[MT], csum[MT][4];
+#pragma unroll
+            for (int mm = 0; mm < MT; ++mm) {
+                const int m = wave + NW * mm;
+                if (m >= NTILE) break;
                 const int it = m < 1 ? 0 : m < 3 ? 1 : m < 6 ? 2 : 3;
                 const int jt = m - it * (it + 1) / 2;
                 f32x4 a = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -556,85 +632,103 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_pass_kernel(ssm_detail::L
                     for (int r = 0; r < 4; ++r) {
                         const float x = j0 + r < i ? a[r] * b[r] : 0.0f;
                         row += x;
-                        const float col = sum16(x);
-                        if (l16 == 0) cross[160 + 16 * m + 4 * g4 + r] = col;
+                        csum[mm][r] = sum16(x);
                     }
                     row += __shfl_xor(row, 16);
-                    row += __shfl_xor(row, 32);
-                    if (g4 == 0) cross[16 * m + l16] = row;
+                    rsum[mm] = row + __shfl_xor(row, 32);
                 }
             }
+            next();
             // ---- the incoming state's share, e^{G_i} R^T x1_i
 #pragma unroll
-            for (int it = 0; it < IT; ++it)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) acc[it][nt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int it = 0; it < IT; ++it) acc[it] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
-                u32x4 sp[NT][SP];
+                u32x4 sp[SP];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int e = 0; e < 4; ++e) {
+                    const f32x4& s = S[2 * kb + (e >> 1)];
+                    uint32_t w[SP];
+                    split<SP>(s[2 * (e & 1)], s[2 * (e & 1) + 1], w);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const f32x4& s = S[2 * kb + (e >> 1)][nt];
-                        uint32_t w[SP];
-                        split<SP>(s[2 * (e & 1)], s[2 * (e & 1) + 1], w);
-#pragma unroll
-                        for (int k = 0; k < SP; ++k) sp[nt][k][e] = w[k];
-                    }
+                    for (int k = 0; k < SP; ++k) sp[k][e] = w[k];
+                }
 #pragma unroll
                 for (int it = 0; it < IT; ++it) {
                     u32x4 q[PARTS];
 #pragma unroll
                     for (int i = 0; i < PARTS; ++i) q[i] = row_op<KD>(X1 + i * C * KD, 16 * it, kb, lane);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) acc[it][nt] = mma_parts<PARTS, SP>(q, sp[nt], acc[it][nt]);
+                    acc[it] = mma_parts<PARTS, SP>(q, sp, acc[it]);
                 }
             }
+            f32x4 d[DOTS ? IT : 1];
 #pragma unroll
             for (int it = 0; it < IT; ++it) {
                 const f32x4 e = *reinterpret_cast<const f32x4*>(&dec.in[16 * it + 4 * g4]);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[it][nt][r] *= e[r];
+                for (int r = 0; r < 4; ++r) acc[it][r] *= e[r];
                 if constexpr (DOTS) {
-                    f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
+                    d[it] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int i = 0; i < PARTS; ++i) {
+                        const uint2 x = tile_op<BV>(X4 + i * C * BV, 16 * it, wave * 16, lane);
+                        d[it][0] = fmaf(bf_lo(x.x), acc[it][0], d[it][0]);
+                        d[it][1] = fmaf(bf_hi(x.x), acc[it][1], d[it][1]);
+                        d[it][2] = fmaf(bf_lo(x.y), acc[it][2], d[it][2]);
+                        d[it][3] = fmaf(bf_hi(x.y), acc[it][3], d[it][3]);
+                    }
 #pragma unroll
-                        for (int i = 0; i < PARTS; ++i) {
-                            const uint2 x = tile_op<BV>(X4 + i * C * BV, 16 * it, wave * 16 * NT + 16 * nt, lane);
-                            d[0] = fmaf(bf_lo(x.x), acc[it][nt][0], d[0]);
-                            d[1] = fmaf(bf_hi(x.x), acc[it][nt][1], d[1]);
-                            d[2] = fmaf(bf_lo(x.y), acc[it][nt][2], d[2]);
-                            d[3] = fmaf(bf_hi(x.y), acc[it][nt][3], d[3]);
-                        }
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) d[r] = sum16(d[r]);
-                    if (l16 == 0) *reinterpret_cast<f32x4*>(&part[wave * C + 16 * it + 4 * g4]) = d;
+                    for (int r = 0; r < 4; ++r) d[it][r] = sum16(d[it][r]);
                 }
             }
-            lds_barrier();                      // P (and the dots) are there
+            values();
+            lds_barrier();                      // P is there; x1, x3 and x4 have been read
             if constexpr (DOTS) {
+                if (l16 == 0) {
+#pragma unroll
+                    for (int it = 0; it < IT; ++it) *reinterpret_cast<f32x4*>(&part[wave * C + 16 * it + 4 * g4]) = d[it];
+                }
+                if constexpr (CROSS) {
+#pragma unroll
+                    for (int mm = 0; mm < MT; ++mm) {
+                        const int m = wave + NW * mm;
+                        if (m >= NTILE) break;
+                        if (g4 == 0) cross[16 * m + l16] = rsum[mm];
+                        if (l16 == 0) {
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) cross[16 * (NTILE + m) + 4 * g4 + r] = csum[mm][r];
+                        }
+                    }
+                }
+                lds_barrier();
                 if (tid < C) {
                     const int64_t t = c0 + (rev ? C - 1 - tid : tid);
                     if (t < hi) {
                         float v = 0.0f;
 #pragma unroll
-                        for (int w = 0; w < kWaves; ++w) v += part[w * C + tid];
+                        for (int w = 0; w < NW; ++w) v += part[w * C + tid];
                         const int64_t o = (int64_t(slice) * p.T + t) * p.H + h;
                         p.dots[o] = v * p.oscale;
                         if constexpr (CROSS) {
                             const int it = tid >> 4;
                             float rsv = 0.0f, csv = 0.0f;
                             for (int m = 0; m <= it; ++m) rsv += cross[16 * (it * (it + 1) / 2 + m) + l16];
-                            for (int m = it; m < IT; ++m) csv += cross[160 + 16 * (m * (m + 1) / 2 + it) + l16];
+                            for (int m = it; m < IT; ++m) csv += cross[16 * (NTILE + m * (m + 1) / 2 + it) + l16];
                             p.cross[o] = (rsv - csv) * p.oscale;
                         }
                     }
                 }
             }
+            if (ahead && n + 1 < nch) {
+                load3(n + 1, tid, X3);
+                if constexpr (DOTS)
+                    load4(n + 1, tid);
+                else
+                    load1(n + 1, tid);
+            }
+        } else {
+            next();
+            values();
         }
 
         // ---- the chunk's own share, P x3, and the outgoing state
@@ -642,110 +736,95 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_pass_kernel(ssm_detail::L
 #pragma unroll
         for (int m = 0; m < 2 * KB; ++m)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) S[m][nt][r] *= all;
+            for (int r = 0; r < 4; ++r) S[m][r] *= all;
 #pragma unroll
         for (int jb = 0; jb < JB; ++jb) {
-            u32x4 v[NT][PARTS];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < PARTS; ++i)
-                    v[nt][i] = col_op<BV, 0>(X3 + i * C * BV, 32 * jb, wave * 16 * NT + 16 * nt, lane);
             if constexpr (FULL) {
 #pragma unroll
                 for (int it = 2 * jb; it < IT; ++it) {
                     u32x4 q[PP];
 #pragma unroll
                     for (int k = 0; k < PP; ++k) q[k] = row_op<32>(PT + k * PB + p_block(it, jb) * 512, 0, 0, lane);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) acc[it][nt] = mma_parts<PP, PARTS>(q, v[nt], acc[it][nt]);
+                    acc[it] = mma_parts<PP, PARTS>(q, v[jb], acc[it]);
                 }
             }
-            u32x4 vp[NT][3];
+            u32x4 vp[3];
             const f32x4 f0 = *reinterpret_cast<const f32x4*>(&dec.out[32 * jb + 8 * g4]);
             const f32x4 f1 = *reinterpret_cast<const f32x4*>(&dec.out[32 * jb + 8 * g4 + 4]);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int e = 0; e < 4; ++e) {
+                float x = 0.0f, y = 0.0f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float x = 0.0f, y = 0.0f;
-#pragma unroll
-                    for (int i = PARTS - 1; i >= 0; --i) {
-                        x += bf_lo(v[nt][i][e]);
-                        y += bf_hi(v[nt][i][e]);
-                    }
-                    const f32x4& f = e < 2 ? f0 : f1;
-                    uint32_t w[3];
-                    split<3>(x * f[2 * (e & 1)], y * f[2 * (e & 1) + 1], w);
-#pragma unroll
-                    for (int k = 0; k < 3; ++k) vp[nt][k][e] = w[k];
+                for (int i = PARTS - 1; i >= 0; --i) {
+                    x += bf_lo(v[jb][i][e]);
+                    y += bf_hi(v[jb][i][e]);
                 }
+                const f32x4& f = e < 2 ? f0 : f1;
+                uint32_t w[3];
+                split<3>(x * f[2 * (e & 1)], y * f[2 * (e & 1) + 1], w);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) vp[k][e] = w[k];
+            }
 #pragma unroll
             for (int m = 0; m < 2 * KB; ++m) {
                 u32x4 k[PARTS];
 #pragma unroll
                 for (int i = 0; i < PARTS; ++i)
                     k[i] = col_op<KD, 1>(X2 + i * C * KD, 32 * jb, 32 * (m >> 1) + 4 * (m & 1), lane);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) S[m][nt] = mma_parts<PARTS, 3>(k, vp[nt], S[m][nt]);
+                S[m] = mma_parts<PARTS, 3>(k, vp, S[m]);
             }
         }
 
         if constexpr (FULL) {
             // rows behind the piece's end fall outside the window
             const int oe = PARTS == 3 || p.out_f32 ? 4 : 2;
-            const int64_t pitch = p.so * oe;
-            const Rsrc ro = rows_rsrc(static_cast<char*>(p.out) + c0 * pitch + int64_t(h) * p.vd * oe, pitch, hi - c0, C);
+            const int64_t pitch64 = p.so * oe;
+            const Rsrc ro = rows_rsrc(static_cast<char*>(p.out) + c0 * pitch64 + int64_t(h) * p.vd * oe, pitch64, hi - c0, C);
+            const int pitch = rev ? -int(pitch64) : int(pitch64);
+            const int lane0 = int(pitch64) * (rev ? C - 1 : 0) + 4 * g4 * pitch;
             if (oe == 4) {
+                const int col = c_wave + l16;
+                const uint32_t o0 = lane0 + 4 * col;
 #pragma unroll
                 for (int it = 0; it < IT; ++it)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int row = 16 * it + 4 * g4 + r;
-                        const uint32_t ob = uint32_t((rev ? C - 1 - row : row) * pitch);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            const int col = c_wave + 16 * nt + l16;
-                            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[it][nt][r] * p.oscale), ro,
-                                                                  col < p.vd ? ob + 4 * col : kPast, 0, 0);
-                        }
-                    }
+                    for (int r = 0; r < 4; ++r)
+                        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[it][r] * p.oscale), ro,
+                                                              col < p.vd ? o0 + uint32_t((16 * it + r) * pitch) : kPast, 0, 0);
             } else if (p.pairs) {
                 // neighbouring lanes swap one row for another: two columns of one row each
                 const bool odd = lane & 1;
+                const int col = c_wave + (l16 & ~1);
+                const uint32_t o0 = lane0 + (odd ? pitch : 0) + 2 * col;
 #pragma unroll
                 for (int it = 0; it < IT; ++it)
 #pragma unroll
                     for (int r = 0; r < 4; r += 2) {
-                        const int row = 16 * it + 4 * g4 + r + odd;
-                        const uint32_t ob = uint32_t((rev ? C - 1 - row : row) * pitch);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            const float x = acc[it][nt][r] * p.oscale, y = acc[it][nt][r + 1] * p.oscale;
-                            const float got = swap1(odd ? x : y);
-                            const int col = c_wave + 16 * nt + (l16 & ~1);
-                            __builtin_amdgcn_raw_buffer_store_b32(odd ? pack2(got, y) : pack2(x, got), ro,
-                                                                  col < p.vd ? ob + 2 * col : kPast, 0, 0);
-                        }
+                        const float x = acc[it][r] * p.oscale, y = acc[it][r + 1] * p.oscale;
+                        const float got = swap1(odd ? x : y);
+                        __builtin_amdgcn_raw_buffer_store_b32(odd ? pack2(got, y) : pack2(x, got), ro,
+                                                              col < p.vd ? o0 + uint32_t((16 * it + r) * pitch) : kPast, 0, 0);
                     }
             } else {
+                const int col = c_wave + l16;
+                const uint32_t o0 = lane0 + 2 * col;
 #pragma unroll
                 for (int it = 0; it < IT; ++it)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int row = 16 * it + 4 * g4 + r;
-                        const uint32_t ob = uint32_t((rev ? C - 1 - row : row) * pitch);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            const int col = c_wave + 16 * nt + l16;
-                            __builtin_amdgcn_raw_buffer_store_b16(IOT<uint16_t>::from_f32(acc[it][nt][r] * p.oscale), ro,
-                                                                  col < p.vd ? ob + 2 * col : kPast, 0, 0);
-                        }
-                    }
+                    for (int r = 0; r < 4; ++r)
+                        __builtin_amdgcn_raw_buffer_store_b16(IOT<uint16_t>::from_f32(acc[it][r] * p.oscale), ro,
+                                                              col < p.vd ? o0 + uint32_t((16 * it + r) * pitch) : kPast, 0, 0);
             }
         }
+        if (ahead && n + 1 < nch && !TWO2) {
+            lds_barrier();                      // x2 (and with row dots x1) has been read
+            load2(n + 1, tid, X2);
+            if constexpr (DOTS) load1(n + 1, tid);
+        }
+    };
+    for (int64_t n = 0; n < nch; n += 2) {
+        chunk(n, std::false_type{});
+        if (n + 1 < nch) chunk(n + 1, std::true_type{});
     }
 
     // ------------------------------------------------ the state that leaves
@@ -768,37 +847,39 @@ __global__ void __launch_bounds__(kThreads, 2) linattn_pass_kernel(ssm_detail::L
 #pragma unroll
         for (int m = 0; m < 2 * KB; ++m)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = 32 * (m >> 1) + 8 * g4 + 4 * (m & 1) + r, col = c_wave + 16 * nt + l16;
-                    if (row < p.kd && col < p.vd) dst[row * rs + col * cs] = mul * S[m][nt][r];
-                }
+            for (int r = 0; r < 4; ++r) {
+                const int row = 32 * (m >> 1) + 8 * g4 + 4 * (m & 1) + r, col = c_wave + l16;
+                if (row < p.kd && col < p.vd) dst[row * rs + col * cs] = mul * S[m][r];
+            }
     }
 }
 
 // Chooses the kernel of a pass's sizes and starts it.
 template <int MODE> inline bool launch_pass(const ssm_detail::LinattnPass& p, bool f32, hipStream_t s) {
     const int64_t blocks = int64_t(p.npieces) * p.H * p.nslices;
-    const dim3 grid(static_cast<uint32_t>(blocks)), block(kThreads);
-    const bool two = ssm_detail::linattn_slice(p.kd, p.vd) == 128;
+    const bool wide = ssm_detail::linattn_slice(p.vd) == 128;
+    const dim3 grid(static_cast<uint32_t>(blocks)), block(wide ? 512 : 256);
     // float32 rows take three times the LDS: chunks of 32 keep two workgroups on a CU
-#define SSM_LIN_CASE(K, NTV)                                                                        \
+#define SSM_LIN_CASE(K, NW)                                                                         \
     do {                                                                                            \
         if (f32)                                                                                    \
-            launch_kernel(linattn_pass_kernel<3, K, NTV, 32, MODE>, grid, block, 0, s, p);           \
+            launch_kernel(linattn_pass_kernel<3, K, NW, 32, MODE>, grid, block, 0, s, p);            \
         else                                                                                        \
-            launch_kernel(linattn_pass_kernel<1, K, NTV, 64, MODE>, grid, block, 0, s, p);           \
+            launch_kernel(linattn_pass_kernel<1, K, NW, 64, MODE>, grid, block, 0, s, p);            \
     } while (0)
-    if (p.kd <= 64) {
-        if (two) SSM_LIN_CASE(64, 2); else SSM_LIN_CASE(64, 1);
-    } else if (p.kd <= 128) {
-        if (two) SSM_LIN_CASE(128, 2); else SSM_LIN_CASE(128, 1);
-    } else if (p.kd <= 256) {
-        SSM_LIN_CASE(256, 1);
-    } else {
+#define SSM_LIN_WAVES(K)                                                                            \
+    do {                                                                                            \
+        if (wide) SSM_LIN_CASE(K, 8); else SSM_LIN_CASE(K, 4);                                      \
+    } while (0)
+    if (p.kd <= 64)
+        SSM_LIN_WAVES(64);
+    else if (p.kd <= 128)
+        SSM_LIN_WAVES(128);
+    else if (p.kd <= 256)
+        SSM_LIN_WAVES(256);
+    else
         return false;
-    }
+#undef SSM_LIN_WAVES
 #undef SSM_LIN_CASE
     return true;
 }

@@ -180,8 +180,8 @@ struct GradPlan {
 // Pieces of at most 1024 tokens: the error of dg's running sum grows with the piece, and the
 // states of pieces this long are a sixteenth of the rows' bytes at dk = dv = 128.
 inline int make_grad_plan(const ssm_linattn_dims* d, bool packed, GradPlan* pl) {
-    pl->slices_q = cdiv(d->dk, ssm_detail::linattn_slice(d->dv, d->dk));
-    pl->slices_s = cdiv(d->dv, ssm_detail::linattn_slice(d->dk, d->dv));
+    pl->slices_q = cdiv(d->dk, ssm_detail::linattn_slice(d->dk));
+    pl->slices_s = cdiv(d->dv, ssm_detail::linattn_slice(d->dv));
     const int64_t units = d->nheads * pl->slices_q;
     const int64_t each = packed ? d->tokens : d->tokens / d->nseq;
     int64_t piece = d->piece_len;

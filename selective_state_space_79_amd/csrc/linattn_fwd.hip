@@ -138,7 +138,7 @@ struct Plan {
 // Pieces along the tokens.  A workgroup walks its piece chunk by chunk, so the longest
 // sequence alone bounds the time when there are fewer workgroups than the card holds.
 inline int make_plan(const ssm_linattn_dims* d, bool packed, Plan* pl) {
-    const int64_t slices = cdiv(d->dv, ssm_detail::linattn_slice(d->dk, d->dv));
+    const int64_t slices = cdiv(d->dv, ssm_detail::linattn_slice(d->dv));
     const int64_t units = d->nheads * slices;
     const int64_t each = packed ? d->tokens : d->tokens / d->nseq;
     int64_t piece = d->piece_len;
@@ -165,7 +165,7 @@ inline int make_plan(const ssm_linattn_dims* d, bool packed, Plan* pl) {
 }  // namespace la
 }  // namespace
 
-int ssm_detail::linattn_slice(int64_t kd, int64_t vd) { return kd <= 128 && vd > 64 ? 128 : 64; }
+int ssm_detail::linattn_slice(int64_t vd) { return vd > 64 ? 128 : 64; }
 
 bool ssm_detail::launch_linattn_pass(const LinattnPass& p, bool f32, LinattnMode mode, hipStream_t s) {
     return mode == kLinStates ? la::launch_pass<kLinStates>(p, f32, s) : la::launch_pass<kLinFull>(p, f32, s);
@@ -237,7 +237,7 @@ int ssm_linattn_fwd(const void* q, const void* k, const void* v, const float* g,
     p.r1 = p.r2 = static_cast<int32_t>(d.nheads / d.kheads);
     p.r3 = p.r4 = 1;
     p.H = static_cast<int32_t>(d.nheads); p.kd = static_cast<int32_t>(d.dk); p.vd = static_cast<int32_t>(d.dv);
-    p.nslices = static_cast<int32_t>(cdiv(d.dv, ssm_detail::linattn_slice(d.dk, d.dv)));
+    p.nslices = static_cast<int32_t>(cdiv(d.dv, ssm_detail::linattn_slice(d.dv)));
     p.nseq = static_cast<int32_t>(d.nseq); p.nslots = static_cast<int32_t>(states ? d.nslots : d.nseq);
     p.npieces = static_cast<int32_t>(pl.npieces); p.pieced = pl.pieced;
     p.wide = wide_rows(q, z.q, d.dk, z.e) && wide_rows(k, z.k, d.dk, z.e) && wide_rows(v, z.v, d.dv, z.e);
