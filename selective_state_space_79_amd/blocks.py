@@ -21,6 +21,7 @@ __all__ = ["SSM_LINATTN_MAX_DIM", "SSM_NORM_MAX_DIM", "SsmLinattnDims", "SsmLina
            "ssm_add_norm_bwd_workspace_bytes"]
 
 _vp = ctypes.c_void_p
+_ref = ctypes.byref
 _i64, _i32, _f32 = ctypes.c_int64, ctypes.c_int32, ctypes.c_float
 
 SSM_LINATTN_MAX_DIM = 256
@@ -85,88 +86,99 @@ def declare(lib):
         f.restype = ctypes.c_size_t
 
 
+_bound = {}     # C name -> function of the loaded library
+
+
 def _package():
     import selective_state_space_79_amd as ssm
 
     return ssm
 
 
-def _lib():
-    return _package().load_library()
+def _fn(name):
+    f = _bound.get(name)
+    if f is None:
+        f = _bound[name] = getattr(_package().load_library(), name)
+    return f
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _raw_stream(device, stream):
+def _call(name, args, device, stream):
+    """Calls a C entry point; args: pointers and struct references, before the stream."""
     import torch
 
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
-
-
-def _call(name, tensors, structs, device, stream):
-    import torch
-
-    f = getattr(_lib(), name)
-    args = [None if t is None else t.data_ptr() for t in tensors]
+    f = _fn(name)
+    index = device if device >= 0 else torch.cuda.current_device()
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
     # a launch goes to the current device, so that has to be the tensors'
-    if device.index is None or device.index == torch.cuda.current_device():
-        return f(*args, *map(ctypes.byref, structs), _raw_stream(device, stream))
-    with torch.cuda.device(device):
-        return f(*args, *map(ctypes.byref, structs), _raw_stream(device, stream))
+    if index == torch._C._cuda_getDevice():
+        return f(*args, raw)
+    with torch.cuda.device(index):
+        return f(*args, raw)
 
 
 def ssm_linattn_fwd(q, k, v, g, cu_seqlens, slots, s0, o, s_last, dims, stream=None) -> int:
     """C entry point of the forward; returns the status."""
-    return _call("ssm_linattn_fwd", (q, k, v, g, cu_seqlens, slots, s0, o, s_last), (dims,), q.device, stream)
+    return _call("ssm_linattn_fwd", (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _ptr(cu_seqlens),
+                                     _ptr(slots), _ptr(s0), o.data_ptr(), _ptr(s_last), _ref(dims)),
+                 q.get_device(), stream)
 
 
 def ssm_linattn_step(q, k, v, g, slots, states, o, dims, stream=None) -> int:
     """C entry point of the single-token step; returns the status."""
-    return _call("ssm_linattn_step", (q, k, v, g, slots, states, o), (dims,), q.device, stream)
+    return _call("ssm_linattn_step", (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _ptr(slots),
+                                      states.data_ptr(), o.data_ptr(), _ref(dims)), q.get_device(), stream)
 
 
 def ssm_linattn_bwd(q, k, v, g, cu_seqlens, s0, do, ds_last, grads, dims, stream=None) -> int:
     """C entry point of the gradients; returns the status."""
-    return _call("ssm_linattn_bwd", (q, k, v, g, cu_seqlens, s0, do, ds_last), (grads, dims), q.device, stream)
+    return _call("ssm_linattn_bwd", (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _ptr(cu_seqlens),
+                                     _ptr(s0), do.data_ptr(), _ptr(ds_last), _ref(grads), _ref(dims)),
+                 q.get_device(), stream)
 
 
 def ssm_gated_norm_fwd(x, z, w, y, dims, stream=None) -> int:
     """C entry point of the gated norm; returns the status."""
-    return _call("ssm_gated_norm_fwd", (x, z, w, y), (dims,), x.device, stream)
+    return _call("ssm_gated_norm_fwd", (x.data_ptr(), _ptr(z), w.data_ptr(), y.data_ptr(), _ref(dims)),
+                 x.get_device(), stream)
 
 
 def ssm_gated_norm_bwd(x, z, w, dy, dx, dz, dw, dims, stream=None) -> int:
     """C entry point of the gated norm's gradients; returns the status."""
-    return _call("ssm_gated_norm_bwd", (x, z, w, dy, dx, dz, dw), (dims,), x.device, stream)
+    return _call("ssm_gated_norm_bwd", (x.data_ptr(), _ptr(z), w.data_ptr(), dy.data_ptr(), dx.data_ptr(), _ptr(dz),
+                                        dw.data_ptr(), _ref(dims)), x.get_device(), stream)
 
 
 def ssm_add_norm_fwd(x, res, scale, post, w, r, y, dims, stream=None) -> int:
     """C entry point of the residual addition with its norms; returns the status."""
-    return _call("ssm_add_norm_fwd", (x, res, scale, post, w, r, y), (dims,), x.device, stream)
+    return _call("ssm_add_norm_fwd", (x.data_ptr(), _ptr(res), _ptr(scale), _ptr(post), w.data_ptr(), r.data_ptr(),
+                                      y.data_ptr(), _ref(dims)), x.get_device(), stream)
 
 
 def ssm_add_norm_bwd(x, r, scale, post, w, dy, dr, dx, dres, dw, dscale, dpost, dims, stream=None) -> int:
     """C entry point of the residual addition's gradients; returns the status."""
-    return _call("ssm_add_norm_bwd", (x, r, scale, post, w, dy, dr, dx, dres, dw, dscale, dpost), (dims,), r.device,
-                 stream)
+    return _call("ssm_add_norm_bwd", (_ptr(x), r.data_ptr(), _ptr(scale), _ptr(post), w.data_ptr(), dy.data_ptr(),
+                                      _ptr(dr), dx.data_ptr(), _ptr(dres), dw.data_ptr(), _ptr(dscale), _ptr(dpost),
+                                      _ref(dims)), r.get_device(), stream)
 
 
 def ssm_linattn_fwd_workspace_bytes(dims) -> int:
-    return int(_lib().ssm_linattn_fwd_workspace_bytes(ctypes.byref(dims)))
+    return int(_fn("ssm_linattn_fwd_workspace_bytes")(_ref(dims)))
 
 
 def ssm_linattn_bwd_workspace_bytes(dims) -> int:
-    return int(_lib().ssm_linattn_bwd_workspace_bytes(ctypes.byref(dims)))
+    return int(_fn("ssm_linattn_bwd_workspace_bytes")(_ref(dims)))
 
 
 def ssm_gated_norm_bwd_workspace_bytes(dims) -> int:
-    return int(_lib().ssm_gated_norm_bwd_workspace_bytes(ctypes.byref(dims)))
+    return int(_fn("ssm_gated_norm_bwd_workspace_bytes")(_ref(dims)))
 
 
 def ssm_add_norm_bwd_workspace_bytes(dims) -> int:
-    return int(_lib().ssm_add_norm_bwd_workspace_bytes(ctypes.byref(dims)))
+    return int(_fn("ssm_add_norm_bwd_workspace_bytes")(_ref(dims)))
 
 
 # ------------------------------------------------------------------ checks
@@ -185,48 +197,51 @@ def _need(cond, text):
         raise ValueError(text)
 
 
-def _device(ref, **tensors):
-    if not ref.is_cuda:
+def _device(ref, *tensors):
+    """All on ref's device, which is a GPU.  The checks of this module run before every call
+    of a few microseconds: they touch each tensor once."""
+    d = ref.get_device()
+    if d < 0:
         raise ValueError("device tensors are needed")
-    for name, t in tensors.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} must be on {ref.device}")
+    for t in tensors:
+        if t is not None and t.get_device() != d:
+            raise ValueError(f"all tensors must be on {ref.device}")
 
 
 def _dense(name, t, dtype, *shapes):
-    """A contiguous tensor of one of these shapes (or None)."""
-    if t is None:
-        return
+    """A contiguous tensor of one of these shapes."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
-    if tuple(t.shape) not in shapes:
+    if t.shape not in shapes:
         raise ValueError(f"{name} must be {' or '.join(map(str, shapes))}, not {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
-def _tokens(name, t):
-    """(tokens, heads, width, elements between tokens) of a (T, heads, width) or
-    (batch, L, heads, width) tensor whose heads are contiguous within a token."""
-    sh, st = t.shape, t.stride()
+def _step(name, t, sh):
+    """Elements between the tokens of a (T, heads, width) or (batch, L, heads, width) tensor
+    whose heads are contiguous within a token (0: packed)."""
+    if t.is_contiguous():
+        return 0
+    st = t.stride()
     heads, width = sh[-2], sh[-1]
     if not ((width == 1 or st[-1] == 1) and (heads == 1 or st[-2] == width)):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     if len(sh) == 3:
-        n, step = sh[0], st[0]
-    else:
-        n = sh[0] * sh[1]
-        step = st[1] if sh[1] > 1 else st[0]
-        if sh[0] > 1 and sh[1] > 1 and st[0] != sh[1] * st[1]:
-            raise ValueError(f"{name}: batch rows must follow one another")
-    return n, heads, width, (0 if n == 1 else step)
+        return st[0] if sh[0] > 1 else 0
+    if sh[0] > 1 and sh[1] > 1 and st[0] != sh[1] * st[1]:
+        raise ValueError(f"{name}: batch rows must follow one another")
+    return st[1] if sh[1] > 1 else st[0] if sh[0] > 1 else 0
+
+
+_HERE = contextlib.nullcontext()
 
 
 def _on(stream):
     """Allocations for a call on another stream belong to that stream."""
     import torch
 
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _HERE if stream is None else torch.cuda.stream(stream)
 
 
 def _workspace(need, given, device):
@@ -255,34 +270,33 @@ def make_linattn_dims(tokens, nseq, nheads, kheads, dk, dv, *, io_dtype=1, scale
 def _linattn_dims(q, k, v, g, scale, nseq):
     import torch
 
-    if not q.dim() == k.dim() == v.dim() or q.dim() not in (3, 4):
+    sq, sk, sv = q.shape, k.shape, v.shape
+    if len(sq) not in (3, 4):
         raise ValueError("q, k and v must all be (tokens, heads, d) or all (batch, L, heads, d)")
-    io = _io("q", q)
-    if k.dtype is not q.dtype or v.dtype is not q.dtype:
+    if sq != sk or sq[:-2] != sv[:-2] or len(sv) != len(sq):
+        raise ValueError("q and k must have one shape, and v their tokens")
+    dt = q.dtype
+    if k.dtype is not dt or v.dtype is not dt:
         raise TypeError("q, k and v must have one dtype")
-    n, kheads, dk, sq = _tokens("q", q)
-    if k.shape != q.shape:
-        raise ValueError("q and k must have one shape")
-    nv, heads, dv, sv = _tokens("v", v)
-    if v.shape[:-2] != q.shape[:-2]:
-        raise ValueError("q, k and v must have the same tokens")
+    heads = sv[-2]
     per_head = g.dim() == 1
-    _dense("g", g, torch.float32, (heads,) if per_head else tuple(v.shape[:-1]))
-    if nseq is None:
-        nseq = q.shape[0] if q.dim() == 4 else 1
-    return SsmLinattnDims(n, nseq, heads, kheads, dk, dv, sq, _tokens("k", k)[3], sv, 0, 0, 0, io, int(per_head), scale,
-                          0, None, 0)
+    _dense("g", g, torch.float32, (heads,) if per_head else sv[:-1])
+    n = sq[0]
+    if len(sq) == 4:
+        nseq, n = n, n * sq[1]
+    return SsmLinattnDims(n, 1 if nseq is None else nseq, heads, sq[-2], sq[-1], sv[-1], _step("q", q, sq),
+                          _step("k", k, sk), _step("v", v, sv), 0, 0, 0, _io("q", q), per_head, scale, 0, None, 0)
 
 
-def _rows_out(name, out, like, dims):
+def _rows_out(out, like, dims):
     """The given output, or a new packed one, with its stride in dims."""
     import torch
 
     if out is None:
         return torch.empty(like.shape, dtype=like.dtype, device=like.device)
     if out.dtype is not like.dtype or out.shape != like.shape:
-        raise ValueError(f"{name} must have the shape and dtype of v")
-    dims.o_stride = _tokens(name, out)[3]
+        raise ValueError("out must have the shape and dtype of v")
+    dims.o_stride = _step("out", out, out.shape)
     return out
 
 
@@ -302,36 +316,54 @@ def linattn_fwd(q, k, v, g, *, scale=1.0, cu_seqlens=None, s0=None, s_last=None,
     """
     import torch
 
-    nseq = None
-    if cu_seqlens is not None:
-        _need(q.dim() == 3, "cu_seqlens needs packed (tokens, heads, d) tensors")
-        nseq = cu_seqlens.numel() - 1
-        _dense("cu_seqlens", cu_seqlens, torch.int32, (nseq + 1,))
-    _device(q, k=k, v=v, g=g, cu_seqlens=cu_seqlens, s0=s0, s_last=s_last, slots=slots, out=out, workspace=workspace)
+    _device(q, k, v, g, cu_seqlens, s0, s_last, slots, out, workspace)
+    nseq = _packed(q, cu_seqlens)
     dims = _linattn_dims(q, k, v, g, scale, nseq)
     dims.piece_len = piece_len
-    lib = _lib()
-    state = (dims.nheads, dims.dk, dims.dv)
     with _on(stream):
-        if return_state and s_last is None:
-            n = dims.nseq if slots is None else (s0.shape[0] if s0 is not None else None)
-            _need(n is not None, "slots without states: give s0 or s_last")
-            s_last = torch.empty((n,) + state, dtype=torch.float32, device=q.device)
-            if slots is not None:
-                s_last.copy_(s0)
-        for name, t in (("s0", s0), ("s_last", s_last)):
-            if t is not None:
-                dims.nslots = t.shape[0]
-                _dense(name, t, torch.float32, (t.shape[0],) + state)
-        if s0 is not None and s_last is not None:
-            _need(s0.shape == s_last.shape, "s0 and s_last must have one shape")
-        _dense("slots", slots, torch.int32, (dims.nseq,))
-        o = _rows_out("out", out, v, dims)
-        need = lib.ssm_linattn_fwd_workspace_bytes(ctypes.byref(dims))
-        workspace, dims.workspace_bytes = _workspace(need, workspace, q.device)
-        dims.workspace = _ptr(workspace)
-        _ok(ssm_linattn_fwd(q, k, v, g, cu_seqlens, slots, s0, o, s_last, dims, stream), "ssm_linattn_fwd")
+        if return_state or s0 is not None or s_last is not None:
+            s_last = _states(dims, q, s0, s_last, slots, return_state)
+        if slots is not None:
+            _dense("slots", slots, torch.int32, (dims.nseq,))
+        o = _rows_out(out, v, dims)
+        need = _fn("ssm_linattn_fwd_workspace_bytes")(_ref(dims))
+        if need:
+            workspace, dims.workspace_bytes = _workspace(need, workspace, q.device)
+            dims.workspace = workspace.data_ptr()
+        st = ssm_linattn_fwd(q, k, v, g, cu_seqlens, slots, s0, o, s_last, dims, stream)
+    if st:
+        raise _package().SsmError(st, "ssm_linattn_fwd")
     return (o, s_last) if return_state else o
+
+
+def _packed(q, cu_seqlens):
+    import torch
+
+    if cu_seqlens is None:
+        return None
+    _need(q.dim() == 3, "cu_seqlens needs packed (tokens, heads, d) tensors")
+    n = cu_seqlens.numel()
+    _dense("cu_seqlens", cu_seqlens, torch.int32, (n,))
+    return n - 1
+
+
+def _states(dims, q, s0, s_last, slots, make):
+    """Checks the states of a forward call, and makes the final ones when asked for."""
+    import torch
+
+    state = (dims.nheads, dims.dk, dims.dv)
+    if make and s_last is None:
+        n = dims.nseq if slots is None else (s0.shape[0] if s0 is not None else None)
+        _need(n is not None, "slots without states: give s0 or s_last")
+        # states that no sequence names keep what they were
+        s_last = torch.empty((n,) + state, dtype=torch.float32, device=q.device) if slots is None else s0.clone()
+    for name, t in (("s0", s0), ("s_last", s_last)):
+        if t is not None:
+            dims.nslots = t.shape[0]
+            _dense(name, t, torch.float32, (dims.nslots,) + state)
+    if s0 is not None and s_last is not None:
+        _need(s0.shape == s_last.shape, "s0 and s_last must have one shape")
+    return s_last
 
 
 def linattn_step(q, k, v, g, states, *, slots=None, scale=1.0, out=None, stream=None):
@@ -341,15 +373,21 @@ def linattn_step(q, k, v, g, states, *, slots=None, scale=1.0, out=None, stream=
     out of range or named before are skipped.  Returns o."""
     import torch
 
-    _need(q.dim() == 3, "q must be (batch, heads, dk)")
-    _device(q, k=k, v=v, g=g, states=states, slots=slots, out=out)
-    dims = _linattn_dims(q, k, v, g, scale, q.shape[0])
-    dims.nslots = states.shape[0]
-    _dense("states", states, torch.float32, (states.shape[0], dims.nheads, dims.dk, dims.dv))
-    _dense("slots", slots, torch.int32, (dims.nseq,))
+    _device(q, k, v, g, states, slots, out)
+    sq = q.shape
+    if len(sq) != 3:
+        raise ValueError("q must be (batch, heads, dk)")
+    dims = _linattn_dims(q, k, v, g, scale, sq[0])
+    ss = states.shape
+    dims.nslots = ss[0]
+    _dense("states", states, torch.float32, (ss[0], v.shape[1], sq[2], v.shape[2]))
+    if slots is not None:
+        _dense("slots", slots, torch.int32, (sq[0],))
     with _on(stream):
-        o = _rows_out("out", out, v, dims)
-        _ok(ssm_linattn_step(q, k, v, g, slots, states, o, dims, stream), "ssm_linattn_step")
+        o = _rows_out(out, v, dims)
+        st = ssm_linattn_step(q, k, v, g, slots, states, o, dims, stream)
+    if st:
+        raise _package().SsmError(st, "ssm_linattn_step")
     return o
 
 
@@ -360,42 +398,42 @@ def linattn_bwd(q, k, v, g, *, do, scale=1.0, cu_seqlens=None, s0=None, ds_last=
     (float32, g's shape) and, with s0, ds0 (float32).  Rows of no sequence are zero."""
     import torch
 
-    nseq = None
-    if cu_seqlens is not None:
-        _need(q.dim() == 3, "cu_seqlens needs packed (tokens, heads, d) tensors")
-        nseq = cu_seqlens.numel() - 1
-        _dense("cu_seqlens", cu_seqlens, torch.int32, (nseq + 1,))
-    _device(q, k=k, v=v, g=g, do=do, cu_seqlens=cu_seqlens, s0=s0, ds_last=ds_last, workspace=workspace)
+    _device(q, k, v, g, do, cu_seqlens, s0, ds_last, workspace)
+    nseq = _packed(q, cu_seqlens)
     dims = _linattn_dims(q, k, v, g, scale, nseq)
     dims.piece_len = piece_len
     if do.dtype is not v.dtype or do.shape != v.shape:
         raise ValueError("do must have the shape and dtype of v")
-    dims.o_stride = _tokens("do", do)[3]
+    dims.o_stride = _step("do", do, do.shape)
     state = (dims.nseq, dims.nheads, dims.dk, dims.dv)
-    _dense("s0", s0, torch.float32, state)
-    _dense("ds_last", ds_last, torch.float32, state)
+    for name, t in (("s0", s0), ("ds_last", ds_last)):
+        if t is not None:
+            _dense(name, t, torch.float32, state)
     dims.nslots = dims.nseq
+    dev = q.device
     with _on(stream):
-        res = {"dq": torch.empty(q.shape, dtype=q.dtype, device=q.device),
-               "dk": torch.empty(k.shape, dtype=q.dtype, device=q.device),
-               "dv": torch.empty(v.shape, dtype=q.dtype, device=q.device),
-               "dg": torch.empty(g.shape, dtype=g.dtype, device=q.device)}
+        res = {"dq": torch.empty(q.shape, dtype=q.dtype, device=dev), "dk": torch.empty(k.shape, dtype=q.dtype, device=dev),
+               "dv": torch.empty(v.shape, dtype=q.dtype, device=dev), "dg": torch.empty(g.shape, dtype=g.dtype, device=dev)}
         if s0 is not None:
-            res["ds0"] = torch.empty_like(s0)
-        need = _lib().ssm_linattn_bwd_workspace_bytes(ctypes.byref(dims))
-        workspace, dims.workspace_bytes = _workspace(need, workspace, q.device)
-        dims.workspace = _ptr(workspace)
+            res["ds0"] = torch.empty(state, dtype=s0.dtype, device=dev)
+        need = _fn("ssm_linattn_bwd_workspace_bytes")(_ref(dims))
+        if need:
+            workspace, dims.workspace_bytes = _workspace(need, workspace, dev)
+            dims.workspace = workspace.data_ptr()
         grads = SsmLinattnGrads(*[_ptr(res.get(n)) for n, _ in SsmLinattnGrads._fields_])
-        _ok(ssm_linattn_bwd(q, k, v, g, cu_seqlens, s0, do, ds_last, grads, dims, stream), "ssm_linattn_bwd")
+        st = ssm_linattn_bwd(q, k, v, g, cu_seqlens, s0, do, ds_last, grads, dims, stream)
+    _ok(st, "ssm_linattn_bwd")
     return res
 
 
 # ------------------------------------------------------------------ norms
-def _matrix(name, t):
-    """(rows, columns, elements between rows) of a tensor whose leading dimensions collapse."""
-    sh, st = t.shape, t.stride()
+def _matrix(name, t, sh):
+    """Elements between the rows of a tensor whose leading dimensions collapse (0: packed)."""
     if len(sh) < 2:
         raise ValueError(f"{name} must have rows")
+    if t.is_contiguous():
+        return 0
+    st = t.stride()
     if sh[-1] > 1 and st[-1] != 1:
         raise ValueError(f"{name}: a row must be contiguous")
     rows, step = 1, 0
@@ -407,23 +445,28 @@ def _matrix(name, t):
         if not step:
             step = s
         rows *= n
-    return rows, sh[-1], step
+    return step
+
+
+def _rows(t, sh):
+    return sh[0] if len(sh) == 2 else t.numel() // max(1, sh[-1])
 
 
 def _gated_dims(x, z, weight, group_size, gate_first, eps):
     import torch
 
-    rows, dim, sx = _matrix("x", x)
+    sh = x.shape
+    sx, dim = _matrix("x", x, sh), sh[-1]
     group = dim if group_size is None else int(group_size)
     _need(group >= 1 and dim % group == 0, "group_size must divide x's last dimension")
     sz = 0
     if z is not None:
-        if z.dtype is not x.dtype or z.shape != x.shape:
+        if z.dtype is not x.dtype or z.shape != sh:
             raise ValueError("z must have the shape and dtype of x")
-        sz = _matrix("z", z)[2]
+        sz = _matrix("z", z, sh)
     _dense("weight", weight, torch.float32, (dim,), (group,))
     shared = weight.numel() == group and group != dim
-    return SsmGatedNormDims(rows, dim // group, group, sx, sz, 0, _io("x", x), int(bool(gate_first)), int(shared), eps,
+    return SsmGatedNormDims(_rows(x, sh), dim // group, group, sx, sz, 0, _io("x", x), bool(gate_first), shared, eps,
                             None, 0)
 
 
@@ -433,7 +476,7 @@ def gated_norm_fwd(x, z, weight, *, group_size=None, gate_first=True, eps=1e-5, 
     (group_size,) for every group.  out may be x or z.  Returns y, x's shape and dtype."""
     import torch
 
-    _device(x, z=z, weight=weight, out=out)
+    _device(x, z, weight, out)
     dims = _gated_dims(x, z, weight, group_size, gate_first, eps)
     with _on(stream):
         if out is None:
@@ -441,7 +484,7 @@ def gated_norm_fwd(x, z, weight, *, group_size=None, gate_first=True, eps=1e-5, 
         else:
             if out.dtype is not x.dtype or out.shape != x.shape:
                 raise ValueError("out must have the shape and dtype of x")
-            dims.y_stride = _matrix("out", out)[2]
+            dims.y_stride = _matrix("out", out, out.shape)
         _ok(ssm_gated_norm_fwd(x, z, weight, out, dims, stream), "ssm_gated_norm_fwd")
     return out
 
@@ -452,15 +495,15 @@ def gated_norm_bwd(x, z, weight, *, dy, group_size=None, gate_first=True, eps=1e
     dweight (float32)."""
     import torch
 
-    _device(x, z=z, weight=weight, dy=dy, workspace=workspace)
+    _device(x, z, weight, dy, workspace)
     dims = _gated_dims(x, z, weight, group_size, gate_first, eps)
-    _dense("dy", dy, x.dtype, tuple(x.shape))
+    _dense("dy", dy, x.dtype, x.shape)
     with _on(stream):
         res = {"dx": torch.empty(x.shape, dtype=x.dtype, device=x.device)}
         if z is not None:
             res["dz"] = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         res["dweight"] = torch.empty_like(weight)
-        need = _lib().ssm_gated_norm_bwd_workspace_bytes(ctypes.byref(dims))
+        need = ssm_gated_norm_bwd_workspace_bytes(dims)
         workspace, dims.workspace_bytes = _workspace(need, workspace, x.device)
         dims.workspace = _ptr(workspace)
         _ok(ssm_gated_norm_bwd(x, z, weight, dy, res["dx"], res.get("dz"), res["dweight"], dims, stream),
@@ -471,16 +514,21 @@ def gated_norm_bwd(x, z, weight, *, dy, group_size=None, gate_first=True, eps=1e
 def _add_dims(x, res, weight, scale, post_weight, eps):
     import torch
 
-    rows, dim, sx = _matrix("x", x)
-    for name, t in (("weight", weight), ("scale", scale), ("post_weight", post_weight)):
-        _dense(name, t, torch.float32, (dim,))
-    sres, rt = 0, _io("x", x)
+    sh = x.shape
+    sx, dim = _matrix("x", x, sh), sh[-1]
+    _dense("weight", weight, torch.float32, (dim,))
+    if scale is not None:
+        _dense("scale", scale, torch.float32, (dim,))
+    if post_weight is not None:
+        _dense("post_weight", post_weight, torch.float32, (dim,))
+    io = _io("x", x)
+    sres, rt = 0, io
     if res is not None:
-        if res.shape != x.shape:
+        if res.shape != sh:
             raise ValueError("the residual must have x's shape")
         rt = _io("residual", res)
-        sres = _matrix("residual", res)[2]
-    return SsmAddNormDims(rows, dim, sx, sres, 0, 0, _io("x", x), rt, eps, 0, None, 0)
+        sres = _matrix("residual", res, sh)
+    return SsmAddNormDims(_rows(x, sh), dim, sx, sres, 0, 0, io, rt, eps, 0, None, 0)
 
 
 def add_norm_fwd(x, residual, weight, *, scale=None, post_weight=None, eps=1e-5, residual_out=None, out=None,
@@ -491,8 +539,7 @@ def add_norm_fwd(x, residual, weight, *, scale=None, post_weight=None, eps=1e-5,
     residual.  Returns (y, r)."""
     import torch
 
-    _device(x, residual=residual, weight=weight, scale=scale, post_weight=post_weight, residual_out=residual_out,
-            out=out)
+    _device(x, residual, weight, scale, post_weight, residual_out, out)
     dims = _add_dims(x, residual, weight, scale, post_weight, eps)
     with _on(stream):
         if residual_out is None:
@@ -501,13 +548,13 @@ def add_norm_fwd(x, residual, weight, *, scale=None, post_weight=None, eps=1e-5,
             if residual_out.shape != x.shape or (residual is not None and residual_out.dtype is not residual.dtype):
                 raise ValueError("residual_out must have x's shape and the residual's dtype")
             dims.res_dtype = _io("residual_out", residual_out)
-            dims.r_stride = _matrix("residual_out", residual_out)[2]
+            dims.r_stride = _matrix("residual_out", residual_out, residual_out.shape)
         if out is None:
             out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         else:
             if out.dtype is not x.dtype or out.shape != x.shape:
                 raise ValueError("out must have the shape and dtype of x")
-            dims.y_stride = _matrix("out", out)[2]
+            dims.y_stride = _matrix("out", out, out.shape)
         _ok(ssm_add_norm_fwd(x, residual, scale, post_weight, weight, residual_out, out, dims, stream),
             "ssm_add_norm_fwd")
     return out, residual_out
@@ -520,11 +567,12 @@ def add_norm_bwd(x, r, weight, *, dy, dr=None, scale=None, post_weight=None, eps
     and dpost_weight (float32)."""
     import torch
 
-    _device(x, r=r, weight=weight, dy=dy, dr=dr, scale=scale, post_weight=post_weight, workspace=workspace)
+    _device(x, r, weight, dy, dr, scale, post_weight, workspace)
     dims = _add_dims(x, r, weight, scale, post_weight, eps)
     dims.r_stride, dims.res_stride = dims.res_stride, 0
-    _dense("dy", dy, x.dtype, tuple(x.shape))
-    _dense("dr", dr, r.dtype, tuple(r.shape))
+    _dense("dy", dy, x.dtype, x.shape)
+    if dr is not None:
+        _dense("dr", dr, r.dtype, r.shape)
     with _on(stream):
         res = {"dx": torch.empty(x.shape, dtype=x.dtype, device=x.device),
                "dresidual": torch.empty(x.shape, dtype=r.dtype, device=x.device), "dweight": torch.empty_like(weight)}
@@ -532,7 +580,7 @@ def add_norm_bwd(x, r, weight, *, dy, dr=None, scale=None, post_weight=None, eps
             res["dscale"] = torch.empty_like(scale)
         if post_weight is not None:
             res["dpost_weight"] = torch.empty_like(post_weight)
-        need = _lib().ssm_add_norm_bwd_workspace_bytes(ctypes.byref(dims))
+        need = ssm_add_norm_bwd_workspace_bytes(dims)
         workspace, dims.workspace_bytes = _workspace(need, workspace, x.device)
         dims.workspace = _ptr(workspace)
         _ok(ssm_add_norm_bwd(x, r, scale, post_weight, weight, dy, dr, res["dx"], res["dresidual"], res["dweight"],
