@@ -55,8 +55,11 @@ enum LinattnMode { kLinStates = 0, kLinFull = 1, kLinDots = 2, kLinCross = 3 };
 bool launch_linattn_pass(const LinattnPass& p, bool f32, LinattnMode mode, hipStream_t s);       // modes 0, 1
 bool launch_linattn_grad_pass(const LinattnPass& p, bool f32, LinattnMode mode, hipStream_t s);  // modes 2, 3
 void launch_linattn_carry(const LinattnPass& p, hipStream_t s);
-// columns of the output that one workgroup computes
-int linattn_slice(int64_t vd);
+// How a pass over vd columns is cut: 128 columns of a head to a workgroup, 64, or two heads
+// of up to 64 that share x1 and x2
+enum LinattnShape { kWide, kNarrow, kTwoHeads };
+inline LinattnShape linattn_shape(int64_t vd, bool pairs) { return vd > 64 ? kWide : pairs ? kTwoHeads : kNarrow; }
+inline int linattn_slice(int64_t vd) { return vd > 64 ? 128 : 64; }
 
 }  // namespace ssm_detail
 
@@ -250,7 +253,7 @@ __device__ inline void load_lds16(Rsrc r, void* lds, uint32_t voff) {
 // A tile of C rows of W columns from memory to LDS.  bf16 rows (PARTS 1) go straight there,
 // each lane fetching the piece that its slot of the permuted row holds; float32 rows
 // (PARTS 3) pass through registers, where they are split.
-template <int PARTS, int C, int W, int T> struct Tile {   // T threads
+template <int PARTS, int C, int W, int T, int HW = W> struct Tile {   // T threads
     static constexpr bool HALF = C * W / 8 < T;                 // fewer pieces of 8 values than threads
     static constexpr int N = HALF ? 1 : C * W / 8 / T;          // pieces per thread
     static_assert(HALF ? PARTS > 1 : C * W / 8 % T == 0, "whole pieces per thread");
@@ -258,10 +261,13 @@ template <int PARTS, int C, int W, int T> struct Tile {   // T threads
     static constexpr int RS = T / (W / 8);    // rows between a thread's pieces
     static constexpr int Q = PARTS == 1 ? 1 : 2;     // 16-byte loads per piece
 
+    // HW columns of the tile belong to one head, w of them real: column c of the tile is
+    // column c % HW of the (c / HW)-th head, w behind the one before
+    __device__ static inline int column(int c, int w) { return HW == W ? c : (c / HW) * w + c % HW; }
     __device__ static inline uint32_t offset(int tid, int n, int pitch, bool rev, int w) {
         const int rr = tid / (W / 8) + RS * n, slot = tid % (W / 8);
         const int col = 8 * (PARTS == 1 ? slot ^ twist<W>(rr) : slot);
-        return col < w && (!HALF || rr < C) ? uint32_t((rev ? C - 1 - rr : rr) * pitch + col * E) : kPast;
+        return col % HW < w && (!HALF || rr < C) ? uint32_t((rev ? C - 1 - rr : rr) * pitch + column(col, w) * E) : kPast;
     }
     u32x4 r[PARTS == 1 ? 1 : N][Q];
 
@@ -312,14 +318,14 @@ template <int PARTS, int C, int W, int T> struct Tile {   // T threads
             const int idx = tid + T * n;
             if (HALF && idx >= C * W / 8) break;
             const int col = 8 * (idx % (W / 8)), rr = rev ? C - 1 - idx / (W / 8) : idx / (W / 8);
-            const char* q = row0 + rr * pitch + col * E;
+            const char* q = row0 + rr * pitch + column(col, w) * E;
             u32x4 x[Q];
 #pragma unroll
             for (int h = 0; h < Q; ++h) x[h] = u32x4{0, 0, 0, 0};
             if (rr < rows) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    if (col + e >= w) continue;
+                    if (col % HW + e >= w) continue;
                     if constexpr (PARTS == 1)
                         x[0][e / 2] |= uint32_t(reinterpret_cast<const uint16_t*>(q)[e]) << (16 * (e & 1));
                     else
@@ -385,13 +391,15 @@ __device__ constexpr int p_block(int it, int jb) { return it < 2 ? it : 2 * it -
 // rows, so that the state's left operand is the key rows as read.
 //
 // Eight waves (128 columns) share the tiles and the products x1 . x2, and two such
-// workgroups fit a CU up to 128 state rows; narrow heads take four waves.
+// workgroups fit a CU up to 128 state rows.  Heads of up to 64 columns that share x1 and x2
+// go two to a workgroup (NH), each with its own decays on the same products; other narrow
+// heads take four waves.
 //
 // Parts: products that end in a float32 output (the state, the row dots) take three parts
 // of what is not a bf16 input; those that end in a bf16 output take two.
 constexpr int pass_waves(int KD, int NW) { return KD == 256 ? NW / 4 : NW / 2; }   // per SIMD
 
-template <int PARTS, int KD, int NW, int C, int MODE>
+template <int PARTS, int KD, int NW, int C, int MODE, int NH>
 __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW)) linattn_pass_kernel(ssm_detail::LinattnPass p) {
     using namespace ssm_detail;
     constexpr bool FULL = MODE >= kLinFull, DOTS = MODE >= kLinDots, CROSS = MODE == kLinCross;
@@ -400,16 +408,19 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW)) linattn_pass_kern
     constexpr int SP = DOTS || PARTS == 3 ? 3 : 2;    // parts of the state in the read-out
     constexpr int PP = PARTS == 3 ? 3 : 2;            // parts of P
     constexpr int NBLK = C == 64 ? 6 : 2, PB = NBLK * 512;
+    constexpr int HW = BV / NH, WH = NW / NH;         // columns and waves of one head
     static_assert(C == 64 || C == 32, "chunk");
+    static_assert(NH == 1 || (NH == 2 && !DOTS), "heads");
     // bf16 rows come straight into LDS, each tile as soon as the last chunk's readers are
-    // done with it: x2 (read to the end) and without a read-out x3 have a second tile
-    constexpr bool DMA = PARTS == 1, TWO2 = DMA && !DOTS, TWO3 = DMA && !FULL;
+    // done with it: x2 (read to the end) and without a read-out x3 have a second tile, where
+    // that still leaves room for two workgroups on a CU
+    constexpr bool DMA = PARTS == 1, TWO2 = DMA && !DOTS && !(FULL && KD == 128 && NH == 2), TWO3 = DMA && !FULL;
     __shared__ __align__(16) uint16_t X2a[PARTS * C * KD], X2b[TWO2 ? C * KD : 8];
     __shared__ __align__(16) uint16_t X3a[PARTS * C * BV], X3b[TWO3 ? C * BV : 8];
     __shared__ __align__(16) uint16_t X1[FULL ? PARTS * C * KD : 8];
-    __shared__ __align__(16) uint16_t PT[FULL ? PP * PB : 8];   // decayed x1 . x2
+    __shared__ __align__(16) uint16_t PTs[FULL ? NH * PP * PB : 8];   // decayed x1 . x2, per head
     __shared__ __align__(16) uint16_t X4[DOTS ? PARTS * C * BV : 8];
-    __shared__ Decays<C> decs[2];
+    __shared__ Decays<C> decs[2][NH];
     // row dots, and the tiles' row and column sums: over x1, once its readers are done
     float* part = reinterpret_cast<float*>(X1);
     float* cross = part + NW * C;
@@ -419,11 +430,11 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW)) linattn_pass_kern
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // neighbouring workgroups run on different XCDs: give each XCD neighbouring heads, so
     // that slices of one head and heads that share rows meet in one L2
-    const int per = p.H * p.nslices;
+    const int per = p.H / NH * p.nslices;
     int at = int(blockIdx.x % per);
     if (per % 8 == 0) at = (at % 8) * (per / 8) + at / 8;
     const int64_t pi = blockIdx.x / per;
-    const int h = at / p.nslices, slice = at % p.nslices;
+    const int slice = at % p.nslices, h0 = at / p.nslices * NH, hw = wave / WH, h = h0 + hw;   // h: this wave's head
     const int seq = find_seq(p, pi);
     if (seq < 0) return;
     const Seq sq = seq_range(p, seq);
@@ -438,11 +449,11 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW)) linattn_pass_kern
     const bool rev = p.reverse;
 
     constexpr int E = PARTS == 1 ? 2 : 4;
-    const int c_wave = slice * BV + wave * 16;                         // this wave's first column
-    const char* b1 = FULL ? static_cast<const char*>(p.x1) + int64_t(h / p.r1) * p.kd * E : nullptr;
-    const char* b2 = static_cast<const char*>(p.x2) + int64_t(h / p.r2) * p.kd * E;
-    const char* b3 = static_cast<const char*>(p.x3) + (int64_t(h / p.r3) * p.vd + slice * BV) * E;
-    const char* b4 = DOTS ? static_cast<const char*>(p.x4) + (int64_t(h / p.r4) * p.vd + slice * BV) * E : nullptr;
+    const int c_wave = slice * BV + (wave % WH) * 16;                  // this wave's first column of its head
+    const char* b1 = FULL ? static_cast<const char*>(p.x1) + int64_t(h0 / p.r1) * p.kd * E : nullptr;
+    const char* b2 = static_cast<const char*>(p.x2) + int64_t(h0 / p.r2) * p.kd * E;
+    const char* b3 = static_cast<const char*>(p.x3) + (int64_t(h0 / p.r3) * p.vd + slice * BV) * E;
+    const char* b4 = DOTS ? static_cast<const char*>(p.x4) + (int64_t(h0 / p.r4) * p.vd + slice * BV) * E : nullptr;
     const int w3 = p.vd - slice * BV;
     const int64_t pitch1 = p.s1 * E, pitch2 = p.s2 * E, pitch3 = p.s3 * E, pitch4 = p.s4 * E;
 
@@ -452,7 +463,7 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW)) linattn_pass_kern
     const int64_t ssz = int64_t(p.kd) * p.vd;
     const float* src = nullptr;
     if (FULL) {
-        if (p.pieced)
+        if (p.pieced && len > p.piece)
             src = p.carry + (pi * p.H + h) * ssz;
         else if (p.s_in)
             src = p.s_in + (int64_t(slot) * p.H + h) * ssz;
@@ -466,14 +477,14 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW)) linattn_pass_kern
         }
     // tiles above the diagonal that share a block with one on it stay zero
     if constexpr (FULL) {
-        for (int i = tid; i < PP * PB / 2; i += T) reinterpret_cast<uint32_t*>(PT)[i] = 0;
+        for (int i = tid; i < NH * PP * PB / 2; i += T) reinterpret_cast<uint32_t*>(PTs)[i] = 0;
     }
 
     const int64_t nch = (hi - lo + C - 1) / C;
     auto first_of = [&](int64_t n) { return lo + (rev ? nch - 1 - n : n) * C; };
-    // the last wave brings the decays, a chunk ahead; against time the decay of a step
-    // belongs to the later of its two tokens
-    constexpr int kDecWave = NW - 1;
+    // the last wave of a head brings its decays, a chunk ahead; against time the decay of a
+    // step belongs to the later of its two tokens
+    const bool dec_wave = wave % WH == WH - 1;
     DecayLane<C> dl;
     double total = 0.0;
     float gn = 0.0f;
@@ -481,13 +492,14 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW)) linattn_pass_kern
         const int64_t t = first_of(n) + (rev ? C - 1 - lane : lane), tg = rev ? t + 1 : t;
         return n < nch && lane < C && t < hi && tg < sq.end ? p.g[tg * p.sg + h] : 0.0f;
     };
-    if (wave == kDecWave && nch > 0) {
+    if (dec_wave && nch > 0) {
         total += dl.scan(decay(0), p.wscale, lane);
-        dl.put(decs[0], lane);
+        dl.put(decs[0][hw], lane);
         gn = decay(1);
     }
     Tile<PARTS, C, KD, T> t1, t2;
-    Tile<PARTS, C, BV, T> t3, t4;
+    Tile<PARTS, C, BV, T, HW> t3;
+    Tile<PARTS, C, BV, T> t4;
     // the tile of chunk n, at once (bf16) or into registers; `any` rows are copied at the
     // chunk's own turn
     auto load1 = [&](int64_t n, int tid) {
@@ -520,7 +532,8 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW)) linattn_pass_kern
         constexpr bool ODD = decltype(odd_c)::value;
         uint16_t* const X2 = TWO2 && ODD ? X2b : X2a;
         uint16_t* const X3 = TWO3 && ODD ? X3b : X3a;
-        Decays<C>& dec = decs[ODD];
+        Decays<C>& dec = decs[ODD][hw];
+        uint16_t* const PT = PTs + hw * PP * PB;
         const int64_t c0 = first_of(n);
         // the lane as the loop's own value: operand addresses are cheap to form anew, and held
         // across the loop they would take the registers that the state needs
@@ -529,7 +542,7 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW)) linattn_pass_kern
         const int tid = 64 * wave + lane, g4 = lane >> 4, l16 = lane & 15;
         if (ahead) {
             // this chunk's rows; what was stored since they were asked for may still be under way
-            if constexpr (!FULL || DOTS)
+            if constexpr (!FULL || !TWO2)
                 wait_memory<0>();
             else if (p.pairs)
                 wait_memory<2 * IT>();
@@ -559,9 +572,9 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW)) linattn_pass_kern
         // the next chunk's decays, and what can be loaded of its rows; behind the last write to
         // LDS of this phase, which otherwise waits for loads into LDS that are under way
         auto next = [&] {
-            if (wave == kDecWave && n + 1 < nch) {
+            if (dec_wave && n + 1 < nch) {
                 total += dl.scan(gn, p.wscale, lane);
-                dl.put(decs[!ODD], lane);
+                dl.put(decs[!ODD][hw], lane);
                 gn = decay(n + 2);
             }
             if (ahead && n + 1 < nch) {
@@ -600,19 +613,24 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW)) linattn_pass_kern
                     a = mma_parts<PARTS, PARTS>(k, q, a);
                 }
                 const int i = 16 * it + l16, j0 = 16 * jt + 4 * g4;
-                const float gi = dec.hi[i], ei = dec.lo[i];
-                const f32x4 gj = *reinterpret_cast<const f32x4*>(&dec.hi[j0]), ej = *reinterpret_cast<const f32x4*>(&dec.lo[j0]);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float w = __builtin_amdgcn_exp2f((gi - gj[r]) + (ei - ej[r]));
-                    a[r] = j0 + r <= i ? a[r] * (w * p.wscale) : 0.0f;
-                }
-                uint32_t u[PP], v[PP];
-                split<PP>(a[0], a[1], u);
-                split<PP>(a[2], a[3], v);
                 const int o = p_block(it, jt >> 1) * 512 + at_piece<32>(l16, 2 * (jt & 1) + (g4 >> 1)) + 4 * (g4 & 1);
+                f32x4 raw = a;
 #pragma unroll
-                for (int k = 0; k < PP; ++k) *reinterpret_cast<uint2*>(PT + k * PB + o) = uint2{u[k], v[k]};
+                for (int hh = 0; hh < NH; ++hh) {
+                    const Decays<C>& dd = decs[ODD][hh];
+                    const float gi = dd.hi[i], ei = dd.lo[i];
+                    const f32x4 gj = *reinterpret_cast<const f32x4*>(&dd.hi[j0]), ej = *reinterpret_cast<const f32x4*>(&dd.lo[j0]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float w = __builtin_amdgcn_exp2f((gi - gj[r]) + (ei - ej[r]));
+                        a[r] = j0 + r <= i ? raw[r] * (w * p.wscale) : 0.0f;
+                    }
+                    uint32_t u[PP], v[PP];
+                    split<PP>(a[0], a[1], u);
+                    split<PP>(a[2], a[3], v);
+#pragma unroll
+                    for (int k = 0; k < PP; ++k) *reinterpret_cast<uint2*>(PTs + (hh * PP + k) * PB + o) = uint2{u[k], v[k]};
+                }
                 if constexpr (CROSS) {
                     // the other product of the same rows, x3 . x4 over this slice's columns;
                     // sums below the diagonal by rows and by columns of the same values
@@ -841,7 +859,7 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW)) linattn_pass_kern
         }
     } else {
         dst = p.carry + (pi * p.H + h) * ssz;
-        if (wave == kDecWave && lane == 0 && slice == 0) p.tot[pi * p.H + h] = __builtin_amdgcn_exp2f(float(total));
+        if (dec_wave && lane == 0 && slice == 0) p.tot[pi * p.H + h] = __builtin_amdgcn_exp2f(float(total));
     }
     if (dst) {
 #pragma unroll
@@ -856,20 +874,23 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW)) linattn_pass_kern
 
 // Chooses the kernel of a pass's sizes and starts it.
 template <int MODE> inline bool launch_pass(const ssm_detail::LinattnPass& p, bool f32, hipStream_t s) {
-    const int64_t blocks = int64_t(p.npieces) * p.H * p.nslices;
-    const bool wide = ssm_detail::linattn_slice(p.vd) == 128;
-    const dim3 grid(static_cast<uint32_t>(blocks)), block(wide ? 512 : 256);
+    const int shape = MODE >= ssm_detail::kLinDots ? ssm_detail::linattn_shape(p.vd, false)
+                                                   : ssm_detail::linattn_shape(p.vd, p.r1 % 2 == 0 && p.r2 % 2 == 0);
+    const int64_t blocks = int64_t(p.npieces) * (shape == ssm_detail::kTwoHeads ? p.H / 2 : p.H) * p.nslices;
+    const dim3 grid(static_cast<uint32_t>(blocks)), block(shape == ssm_detail::kNarrow ? 256 : 512);
     // float32 rows take three times the LDS: chunks of 32 keep two workgroups on a CU
-#define SSM_LIN_CASE(K, NW)                                                                         \
+#define SSM_LIN_CASE(K, NW, NH)                                                                     \
     do {                                                                                            \
         if (f32)                                                                                    \
-            launch_kernel(linattn_pass_kernel<3, K, NW, 32, MODE>, grid, block, 0, s, p);            \
+            launch_kernel(linattn_pass_kernel<3, K, NW, 32, MODE, NH>, grid, block, 0, s, p);        \
         else                                                                                        \
-            launch_kernel(linattn_pass_kernel<1, K, NW, 64, MODE>, grid, block, 0, s, p);            \
+            launch_kernel(linattn_pass_kernel<1, K, NW, 64, MODE, NH>, grid, block, 0, s, p);        \
     } while (0)
 #define SSM_LIN_WAVES(K)                                                                            \
     do {                                                                                            \
-        if (wide) SSM_LIN_CASE(K, 8); else SSM_LIN_CASE(K, 4);                                      \
+        if (shape == ssm_detail::kWide) SSM_LIN_CASE(K, 8, 1);                                      \
+        else if (shape == ssm_detail::kNarrow) SSM_LIN_CASE(K, 4, 1);                               \
+        else if constexpr (MODE < ssm_detail::kLinDots) SSM_LIN_CASE(K, 8, 2);                      \
     } while (0)
     if (p.kd <= 64)
         SSM_LIN_WAVES(64);

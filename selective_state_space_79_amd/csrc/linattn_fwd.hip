@@ -19,7 +19,7 @@ template <int VW> __global__ void __launch_bounds__(kThreads) linattn_carry_kern
     const Seq sq = seq_range(p, seq);
     const int64_t base = piece_base(p, seq);
     int64_t n = (sq.end - sq.start + p.piece - 1) / p.piece;
-    n = n < 1 ? 1 : n;
+    if (n < 2) return;   // a single piece starts from the user's state
     if (base + n > p.npieces) n = p.npieces - base;
     vf s = {};
     if (p.s_in) s = *reinterpret_cast<const vf*>(p.s_in + (int64_t(slot) * p.H + h) * ssz + e);
@@ -135,24 +135,41 @@ struct Plan {
     size_t carry, tot;   // bytes
 };
 
-// Pieces along the tokens.  A workgroup walks its piece chunk by chunk, so the longest
-// sequence alone bounds the time when there are fewer workgroups than the card holds.
+// Pieces along the tokens.  A workgroup walks its piece chunk by chunk, so with few heads
+// and sequences the walk's length bounds the time; pieces cost a second pass over keys and
+// values and their states' bytes.  The estimate, in microseconds (measured on heads of
+// 128 x 128): 4.5 for a chunk of a full pass and 2 for one of the states' pass while the
+// workgroups fit the card, in rounds of 512, and the bytes at 4 TB/s.  How long the sequences
+// of a packed call are is not known here: one long one is assumed.
+inline int64_t choose_piece(const ssm_linattn_dims* d, int64_t units, int64_t each, bool packed) {
+    const double state = 4.0 * static_cast<double>(d->nheads * d->dk * d->dv) / 4e6;      // us per copy of one piece's states
+    const double rows = 2.0 * static_cast<double>(d->tokens) *
+                        static_cast<double>(d->nheads * d->dv + d->kheads * d->dk) / 4e6;    // us of keys and values
+    const int64_t nseq = packed ? 1 : d->nseq;
+    const auto rounds = [&](int64_t groups) { return static_cast<double>(cdiv(groups, 512)); };
+    const double whole_walk = rounds(units * nseq) * 4.5 * static_cast<double>(cdiv(each, 64));
+    double best = whole_walk > 2 * rows ? whole_walk : 2 * rows;
+    int64_t piece = 0;
+    for (int64_t n = 1; 64 * n < each; n = n < 4 ? n + 1 : n * 3 / 2) {
+        const int64_t pieces = nseq * cdiv(each, 64 * n);
+        const double full = rounds(units * pieces) * 4.5 * static_cast<double>(n), pre = full * (2.0 / 4.5);
+        const double t = (full > 2 * rows ? full : 2 * rows) + (pre > rows ? pre : rows) +
+                         4 * state * static_cast<double>(pieces) + 8;
+        if (t < best) {
+            best = t;
+            piece = 64 * n;
+        }
+    }
+    return piece;
+}
+
 inline int make_plan(const ssm_linattn_dims* d, bool packed, Plan* pl) {
     const int64_t slices = cdiv(d->dv, ssm_detail::linattn_slice(d->dv));
+    const bool pairs = ssm_detail::linattn_shape(d->dv, d->nheads / d->kheads % 2 == 0) == ssm_detail::kTwoHeads;
     const int64_t units = d->nheads * slices;
     const int64_t each = packed ? d->tokens : d->tokens / d->nseq;
     int64_t piece = d->piece_len;
-    if (piece == 0) {
-        const int64_t slots = 512;   // two workgroups on each of 256 CUs
-        if (units * d->nseq >= slots && !packed) {
-            piece = 0;
-        } else {
-            const int64_t want = cdiv(2 * slots, units);
-            piece = cdiv(cdiv(d->tokens, want), 64) * 64;
-            if (piece < 256) piece = 256;
-        }
-        if (piece >= each) piece = 0;
-    }
+    if (piece == 0) piece = choose_piece(d, pairs ? units / 2 : units, each, packed);
     pl->pieced = piece > 0 && piece < each;
     pl->piece = pl->pieced ? piece : (int64_t(1) << 31);
     pl->npieces = !pl->pieced ? d->nseq : packed ? d->tokens / piece + d->nseq : d->nseq * cdiv(each, piece);
@@ -164,8 +181,6 @@ inline int make_plan(const ssm_linattn_dims* d, bool packed, Plan* pl) {
 
 }  // namespace la
 }  // namespace
-
-int ssm_detail::linattn_slice(int64_t vd) { return vd > 64 ? 128 : 64; }
 
 bool ssm_detail::launch_linattn_pass(const LinattnPass& p, bool f32, LinattnMode mode, hipStream_t s) {
     return mode == kLinStates ? la::launch_pass<kLinStates>(p, f32, s) : la::launch_pass<kLinFull>(p, f32, s);
