@@ -47,14 +47,20 @@ struct LinattnPass {
     int32_t reverse, out_f32;
     int32_t wide;             // rows of x1 .. x4 allow 16-byte loads at 32-bit offsets
     int32_t pairs;            // out allows stores of two bf16
+    int32_t exact;            // a float32 output depends on the state
     float wscale, oscale;
+};
+
+// Passes of one launch, over the grid's y: they differ in rows, direction and states only.
+struct LinattnPasses {
+    LinattnPass p[2];
 };
 
 // The launches return false for sizes that no kernel covers (nothing launched).
 enum LinattnMode { kLinStates = 0, kLinFull = 1, kLinDots = 2, kLinCross = 3 };
-bool launch_linattn_pass(const LinattnPass& p, bool f32, LinattnMode mode, hipStream_t s);       // modes 0, 1
-bool launch_linattn_grad_pass(const LinattnPass& p, bool f32, LinattnMode mode, hipStream_t s);  // modes 2, 3
-void launch_linattn_carry(const LinattnPass& p, hipStream_t s);
+bool launch_linattn_pass(const LinattnPasses& p, int count, bool f32, LinattnMode mode, hipStream_t s);       // modes 0, 1
+bool launch_linattn_grad_pass(const LinattnPasses& p, int count, bool f32, LinattnMode mode, hipStream_t s);  // modes 2, 3
+void launch_linattn_carry(const LinattnPasses& p, int count, hipStream_t s);
 // How a pass over vd columns is cut: 128 columns of a head to a workgroup, 64, or two heads
 // of up to 64 that share x1 and x2
 enum LinattnShape { kWide, kNarrow, kTwoHeads };
@@ -218,9 +224,7 @@ __device__ inline float sum16(float v) {
     return v;
 }
 // The value of the lane's neighbour (lanes 2n and 2n + 1 swap).
-__device__ inline float swap1(float v) {
-    return __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(v), 0xB1, 0xf, 0xf, true));
-}
+__device__ inline uint32_t swap1(uint32_t v) { return __builtin_amdgcn_update_dpp(0u, v, 0xB1, 0xf, 0xf, true); }
 
 // Waits until at most N vector-memory operations are under way (the instruction's own
 // encoding, so that the compiler counts from it too).
@@ -243,11 +247,27 @@ __device__ inline Rsrc rows_rsrc(const char* row0, int64_t pitch, int64_t rows, 
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(row0), 0, int(n * pitch), 0x00020000);
 }
 
-// 16 bytes per lane from a buffer straight into LDS: lane l's bytes land at lds + 16 l (lds
-// wave-uniform).  (A plain device function: the builtin inside a kernel template leaves the
-// template without a host stub.)
-__device__ inline void load_lds16(Rsrc r, void* lds, uint32_t voff) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, voff, 0, 0, 0);
+// 16 bytes per lane from a window straight into LDS: lane l's bytes land at lds + 16 l (lds
+// wave-uniform); one more vector-memory operation under way, which the caller waits for
+// (wait_memory) before a barrier.  Written out, because the compiler waits for all such loads
+// before every LDS access it cannot tell apart from theirs, which would undo loading ahead.
+// There is no register output.  The wait states cover m0 and descriptors that vector
+// instructions left behind.
+__device__ inline void load_lds16(const u32x4& window, uint32_t lds, uint32_t voff) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds), "v"(voff), "s"(window)
+                 : "memory", "m0");
+}
+__device__ inline uint32_t lds_address(const void* q) {
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void*)q));
+}
+__device__ inline u32x4 rows_window(const char* row0, int64_t pitch, int64_t rows, int c) {
+    const int64_t n = (rows < c ? rows : c) * pitch;
+    const uint64_t a = reinterpret_cast<uint64_t>(row0);
+    return u32x4{uint32_t(__builtin_amdgcn_readfirstlane(int(a))),
+                 uint32_t(__builtin_amdgcn_readfirstlane(int(a >> 32))) & 0xffffu,
+                 uint32_t(__builtin_amdgcn_readfirstlane(int(n))), 0x00020000u};
 }
 
 // A tile of C rows of W columns from memory to LDS.  bf16 rows (PARTS 1) go straight there,
@@ -264,24 +284,35 @@ template <int PARTS, int C, int W, int T, int HW = W> struct Tile {   // T threa
     // HW columns of the tile belong to one head, w of them real: column c of the tile is
     // column c % HW of the (c / HW)-th head, w behind the one before
     __device__ static inline int column(int c, int w) { return HW == W ? c : (c / HW) * w + c % HW; }
-    __device__ static inline uint32_t offset(int tid, int n, int pitch, bool rev, int w) {
-        const int rr = tid / (W / 8) + RS * n, slot = tid % (W / 8);
-        const int col = 8 * (PARTS == 1 ? slot ^ twist<W>(rr) : slot);
-        return col % HW < w && (!HALF || rr < C) ? uint32_t((rev ? C - 1 - rr : rr) * pitch + column(col, w) * E) : kPast;
+    // Byte offsets of a thread's pieces from the chunk's first token: the first of even and of
+    // odd pieces (rows RS apart are twisted alike, or every second of them), past the window
+    // where there is no such column; further ones step by rows and stay past it.
+    static constexpr int ODD = PARTS == 1 && twist<W>(RS) != 0 ? 2 : 1;
+    uint32_t off[ODD];
+    int step;
+    __device__ inline void prepare(int tid, int64_t pitch, bool rev, int w) {
+        step = int(rev ? -ODD * RS * pitch : ODD * RS * pitch);
+#pragma unroll
+        for (int n = 0; n < ODD; ++n) {
+            const int rr = tid / (W / 8) + RS * n, slot = tid % (W / 8);
+            const int col = 8 * (PARTS == 1 ? slot ^ twist<W>(rr) : slot);
+            off[n] = col % HW < w && (!HALF || rr < C) ? uint32_t((rev ? C - 1 - rr : rr) * int(pitch) + column(col, w) * E)
+                                                       : kPast;
+        }
     }
     u32x4 r[PARTS == 1 ? 1 : N][Q];
 
-    __device__ inline void load(uint16_t* tile, int tid, const char* row0, int64_t pitch, int64_t rows, bool rev, int w) {
-        const Rsrc b = rows_rsrc(row0, pitch, rows, C);
+    __device__ inline void load(uint16_t* tile, int wave, const char* row0, int64_t pitch, int64_t rows) {
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            const uint32_t o = offset(tid, n, int(pitch), rev, w);
+            const uint32_t o = off[n % ODD] + uint32_t(n / ODD * step);
             if constexpr (PARTS == 1) {
-                load_lds16(b, tile + 8 * (T * n + (__builtin_amdgcn_readfirstlane(tid) & ~63)), o);
+                load_lds16(rows_window(row0, pitch, rows, C), lds_address(tile) + 16 * (T * n + 64 * wave), o);
             } else {
+                const Rsrc b = rows_rsrc(row0, pitch, rows, C);
 #pragma unroll
                 for (int h = 0; h < Q; ++h)
-                    r[n][h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, o == kPast ? o : o + 16 * h, 0, 0));
+                    r[n][h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, o + 16 * h, 0, 0));
             }
         }
     }
@@ -339,43 +370,55 @@ template <int PARTS, int C, int W, int T, int HW = W> struct Tile {   // T threa
 
 // Decays of one chunk.  The sums run in float64 and are kept in two floats, so that a
 // difference of two of them is right to float32 of the difference, however far they fell.
-template <int C> struct Decays {
+// The state in registers is R / s with a scale s that takes the chunks' decays in its place
+// (no product per value and chunk); it is folded in before it falls below 2^-60.
+template <int C> struct __align__(16) Decays {
     float hi[C], lo[C];   // G in log2 units
-    float in[C];          // e^{G_i}: the incoming state's share at row i
-    float out[C];         // w e^{G_C - G_j}: row j's share in the outgoing state
-    float all;            // e^{G_C}
+    float in[C];          // o s e^{G_i}: the incoming state's share at row i
+    float out[C];         // w e^{G_C - G_j} / s': row j's share in the outgoing state
+    float fold;           // what the state is multiplied with: 1, or s e^{G_C} where s' is 1 again
 };
 
-__device__ inline double shfl_up_f64(double v, int d) {
-    return __hiloint2double(__shfl_up(__double2hiint(v), d), __shfl_up(__double2loint(v), d));
+// v of the lane that a DPP control names, 0 where there is none (or the row is masked out).
+template <int CTRL, int ROWS> __device__ inline double dpp_f64(double v) {
+    const int lo = __builtin_amdgcn_update_dpp(0, __double2loint(v), CTRL, ROWS, 0xf, false);
+    const int hi = __builtin_amdgcn_update_dpp(0, __double2hiint(v), CTRL, ROWS, 0xf, false);
+    return __hiloint2double(hi, lo);
+}
+// Inclusive sum over the lanes of a wave: within rows of 16, then over the rows.
+__device__ inline double scan_f64(double v) {
+    v += dpp_f64<0x111, 0xf>(v);   // from 1, 2, 4, 8 lanes below
+    v += dpp_f64<0x112, 0xf>(v);
+    v += dpp_f64<0x114, 0xf>(v);
+    v += dpp_f64<0x118, 0xf>(v);
+    v += dpp_f64<0x142, 0xa>(v);   // lane 15 of rows 0 and 2 to rows 1 and 3
+    v += dpp_f64<0x143, 0xc>(v);   // lane 31 to rows 2 and 3
+    return v;
+}
+__device__ inline double lane_f64(double v, int lane) {
+    return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), lane),
+                            __builtin_amdgcn_readlane(__double2loint(v), lane));
 }
 
-// One wave: lane r brings row r's log decay and keeps its values until the chunk's turn.
+// One wave: lane r brings row r's log decay and works out the chunk's values.
 template <int C> struct DecayLane {
-    float hi, lo, in, out;
-    __device__ inline double scan(float g, float wscale, int lane) {
+    double scale = 0.0;   // log2 of s, the same in every lane
+    // Returns the chunk's total in log2 units.
+    __device__ inline double next(Decays<C>& d, float g, float wscale, float oscale, int lane) {
         g = g < kMinDecay ? kMinDecay : g;
-        double s = lane < C ? double(g) * 1.4426950408889634 : 0.0;
-#pragma unroll
-        for (int k = 1; k < C; k <<= 1) {
-            const double o = shfl_up_f64(s, k);
-            if (lane >= k) s += o;
-        }
-        const double end = __hiloint2double(__shfl(__double2hiint(s), C - 1), __shfl(__double2loint(s), C - 1));
-        hi = float(s);
-        lo = float(s - double(hi));
-        in = __builtin_amdgcn_exp2f(hi);
-        out = wscale * __builtin_amdgcn_exp2f(float(end - s));
-        return end;
-    }
-    __device__ inline void put(Decays<C>& d, int lane) const {
+        const double s = scan_f64(lane < C ? double(g) * 1.4426950408889634 : 0.0);
+        const double end = lane_f64(s, C - 1);
+        const bool fold = !(scale + end > -60.0);
         if (lane < C) {
+            const float hi = float(s);
             d.hi[lane] = hi;
-            d.lo[lane] = lo;
-            d.in[lane] = in;
-            d.out[lane] = out;
-            if (lane == C - 1) d.all = in;
+            d.lo[lane] = float(s - double(hi));
+            d.in[lane] = oscale * __builtin_amdgcn_exp2f(float(scale + s));
+            d.out[lane] = wscale * __builtin_amdgcn_exp2f(float(fold ? end - s : -scale - s));
+            if (lane == 0) d.fold = fold ? __builtin_amdgcn_exp2f(float(scale + end)) : 1.0f;
         }
+        scale = fold ? 0.0 : scale + end;
+        return end;
     }
 };
 
@@ -395,16 +438,19 @@ __device__ constexpr int p_block(int it, int jb) { return it < 2 ? it : 2 * it -
 // go two to a workgroup (NH), each with its own decays on the same products; other narrow
 // heads take four waves.
 //
-// Parts: products that end in a float32 output (the state, the row dots) take three parts
-// of what is not a bf16 input; those that end in a bf16 output take two.
-constexpr int pass_waves(int KD, int NW) { return KD == 256 ? NW / 4 : NW / 2; }   // per SIMD
+// Parts: products that end in a float32 output (row dots, and the state where the caller
+// gets it: VP) take three parts of what is not a bf16 input; those that end in a bf16
+// output take two.
+constexpr int pass_waves(int KD, int NW, int NT) { return KD == 256 ? NW / 4 : NW / 2; }   // per SIMD
 
-template <int PARTS, int KD, int NW, int C, int MODE, int NH>
-__global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW)) linattn_pass_kernel(ssm_detail::LinattnPass p) {
+template <int PARTS, int KD, int NW, int NT, int C, int MODE, int NH, int VP>
+__global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_kernel(ssm_detail::LinattnPasses passes) {
     using namespace ssm_detail;
+    const LinattnPass& p = passes.p[blockIdx.y];
     constexpr bool FULL = MODE >= kLinFull, DOTS = MODE >= kLinDots, CROSS = MODE == kLinCross;
-    constexpr int T = 64 * NW, BV = 16 * NW, IT = C / 16, JB = C / 32, KB = KD / 32;
-    constexpr int NTILE = IT * (IT + 1) / 2, MT = (NTILE + NW - 1) / NW;   // tiles of P, and the most of one wave
+    constexpr int T = 64 * NW, BV = 16 * NT * NW, IT = C / 16, JB = C / 32, KB = KD / 32;
+    constexpr int TW = NH == 1 ? NW - 1 : NW;         // waves with tiles of P: the one with the decays has none
+    constexpr int NTILE = IT * (IT + 1) / 2, MT = (NTILE + TW - 1) / TW;   // tiles of P, and the most of one wave
     constexpr int SP = DOTS || PARTS == 3 ? 3 : 2;    // parts of the state in the read-out
     constexpr int PP = PARTS == 3 ? 3 : 2;            // parts of P
     constexpr int NBLK = C == 64 ? 6 : 2, PB = NBLK * 512;
@@ -449,7 +495,7 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW)) linattn_pass_kern
     const bool rev = p.reverse;
 
     constexpr int E = PARTS == 1 ? 2 : 4;
-    const int c_wave = slice * BV + (wave % WH) * 16;                  // this wave's first column of its head
+    const int c_wave = slice * BV + (wave % WH) * 16 * NT;             // this wave's first column of its head
     const char* b1 = FULL ? static_cast<const char*>(p.x1) + int64_t(h0 / p.r1) * p.kd * E : nullptr;
     const char* b2 = static_cast<const char*>(p.x2) + int64_t(h0 / p.r2) * p.kd * E;
     const char* b3 = static_cast<const char*>(p.x3) + (int64_t(h0 / p.r3) * p.vd + slice * BV) * E;
@@ -458,7 +504,7 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW)) linattn_pass_kern
     const int64_t pitch1 = p.s1 * E, pitch2 = p.s2 * E, pitch3 = p.s3 * E, pitch4 = p.s4 * E;
 
     // ------------------------------------------------ starting state
-    f32x4 S[2 * KB];
+    f32x4 S[2 * KB][NT];
     const int64_t rs = p.st_t ? 1 : p.vd, cs = p.st_t ? p.kd : 1;
     const int64_t ssz = int64_t(p.kd) * p.vd;
     const float* src = nullptr;
@@ -471,9 +517,9 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW)) linattn_pass_kern
 #pragma unroll
     for (int m = 0; m < 2 * KB; ++m)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = 32 * (m >> 1) + 8 * g4 + 4 * (m & 1) + r, col = c_wave + l16;
-            S[m][r] = src && row < p.kd && col < p.vd ? src[row * rs + col * cs] : 0.0f;
+        for (int x = 0; x < 4 * NT; ++x) {
+            const int nt = x >> 2, r = x & 3, row = 32 * (m >> 1) + 8 * g4 + 4 * (m & 1) + r, col = c_wave + 16 * nt + l16;
+            S[m][nt][r] = src && row < p.kd && col < p.vd ? src[row * rs + col * cs] : 0.0f;
         }
     // tiles above the diagonal that share a block with one on it stay zero
     if constexpr (FULL) {
@@ -487,43 +533,47 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW)) linattn_pass_kern
     const bool dec_wave = wave % WH == WH - 1;
     DecayLane<C> dl;
     double total = 0.0;
+    const float p_scale = p.wscale * p.oscale;
     float gn = 0.0f;
     auto decay = [&](int64_t n) {
         const int64_t t = first_of(n) + (rev ? C - 1 - lane : lane), tg = rev ? t + 1 : t;
         return n < nch && lane < C && t < hi && tg < sq.end ? p.g[tg * p.sg + h] : 0.0f;
     };
     if (dec_wave && nch > 0) {
-        total += dl.scan(decay(0), p.wscale, lane);
-        dl.put(decs[0][hw], lane);
+        total += dl.next(decs[0][hw], decay(0), p.wscale, p.oscale, lane);
         gn = decay(1);
     }
     Tile<PARTS, C, KD, T> t1, t2;
     Tile<PARTS, C, BV, T, HW> t3;
     Tile<PARTS, C, BV, T> t4;
+    t2.prepare(tid, pitch2, rev, p.kd);
+    t3.prepare(tid, pitch3, rev, w3);
+    if constexpr (FULL) t1.prepare(tid, pitch1, rev, p.kd);
+    if constexpr (DOTS) t4.prepare(tid, pitch4, rev, w3);
     // the tile of chunk n, at once (bf16) or into registers; `any` rows are copied at the
     // chunk's own turn
-    auto load1 = [&](int64_t n, int tid) {
+    auto load1 = [&](int64_t n) {
         const int64_t c0 = first_of(n);
-        t1.load(X1, tid, b1 + c0 * pitch1, pitch1, hi - c0, rev, p.kd);
+        t1.load(X1, wave, b1 + c0 * pitch1, pitch1, hi - c0);
     };
-    auto load2 = [&](int64_t n, int tid, uint16_t* to) {
+    auto load2 = [&](int64_t n, uint16_t* to) {
         const int64_t c0 = first_of(n);
-        t2.load(to, tid, b2 + c0 * pitch2, pitch2, hi - c0, rev, p.kd);
+        t2.load(to, wave, b2 + c0 * pitch2, pitch2, hi - c0);
     };
-    auto load3 = [&](int64_t n, int tid, uint16_t* to) {
+    auto load3 = [&](int64_t n, uint16_t* to) {
         const int64_t c0 = first_of(n);
-        t3.load(to, tid, b3 + c0 * pitch3, pitch3, hi - c0, rev, w3);
+        t3.load(to, wave, b3 + c0 * pitch3, pitch3, hi - c0);
     };
-    auto load4 = [&](int64_t n, int tid) {
+    auto load4 = [&](int64_t n) {
         const int64_t c0 = first_of(n);
-        t4.load(X4, tid, b4 + c0 * pitch4, pitch4, hi - c0, rev, w3);
+        t4.load(X4, wave, b4 + c0 * pitch4, pitch4, hi - c0);
     };
     const bool ahead = DMA && p.wide;          // tiles are loaded ahead of their chunk
     if (ahead && nch > 0) {
-        load2(0, tid, X2a);
-        load3(0, tid, X3a);
-        if constexpr (FULL) load1(0, tid);
-        if constexpr (DOTS) load4(0, tid);
+        load2(0, X2a);
+        load3(0, X3a);
+        if constexpr (FULL) load1(0);
+        if constexpr (DOTS) load4(0);
     }
     wait_memory<0>();
 
@@ -545,18 +595,18 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW)) linattn_pass_kern
             if constexpr (!FULL || !TWO2)
                 wait_memory<0>();
             else if (p.pairs)
-                wait_memory<2 * IT>();
+                wait_memory<2 * IT * NT>();
             else
-                wait_memory<4 * IT>();
+                wait_memory<4 * IT * NT>();
             lds_barrier();
         } else {
             lds_barrier();                      // the last chunk's readers are done
             const int64_t rows = hi - c0;
             if (p.wide) {
-                load2(n, tid, X2);
-                if constexpr (FULL) load1(n, tid);
-                load3(n, tid, X3);
-                if constexpr (DOTS) load4(n, tid);
+                load2(n, X2);
+                if constexpr (FULL) load1(n);
+                load3(n, X3);
+                if constexpr (DOTS) load4(n);
                 t2.store(X2, tid);
                 if constexpr (FULL) t1.store(X1, tid);
                 t3.store(X3, tid);
@@ -569,48 +619,52 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW)) linattn_pass_kern
             }
             lds_barrier();
         }
-        // the next chunk's decays, and what can be loaded of its rows; behind the last write to
-        // LDS of this phase, which otherwise waits for loads into LDS that are under way
-        auto next = [&] {
+        if (ahead && n + 1 < nch) {
+            if constexpr (TWO2) load2(n + 1, ODD ? X2a : X2b);
+            if constexpr (TWO3) load3(n + 1, ODD ? X3a : X3b);
+        }
+        auto next = [&] {                        // the next chunk's decays
             if (dec_wave && n + 1 < nch) {
-                total += dl.scan(gn, p.wscale, lane);
-                dl.put(decs[!ODD][hw], lane);
+                total += dl.next(decs[!ODD][hw], gn, p.wscale, p.oscale, lane);
                 gn = decay(n + 2);
-            }
-            if (ahead && n + 1 < nch) {
-                if constexpr (TWO2) load2(n + 1, tid, ODD ? X2a : X2b);
-                if constexpr (TWO3) load3(n + 1, tid, ODD ? X3a : X3b);
             }
         };
         // the value rows of this wave's columns
-        u32x4 v[JB][PARTS];
+        const int w0 = wave * 16 * NT;           // this wave's first column of the tile
+        u32x4 v[JB][NT][PARTS];
         auto values = [&] {
 #pragma unroll
             for (int jb = 0; jb < JB; ++jb)
 #pragma unroll
-                for (int i = 0; i < PARTS; ++i) v[jb][i] = col_op<BV, 0>(X3 + i * C * BV, 32 * jb, wave * 16, lane);
+                for (int x = 0; x < NT * PARTS; ++x)
+                    v[jb][x / PARTS][x % PARTS] =
+                        col_op<BV, 0>(X3 + (x % PARTS) * C * BV, 32 * jb, w0 + 16 * (x / PARTS), lane);
         };
 
-        f32x4 acc[IT];
+        f32x4 acc[IT][NT];
         if constexpr (FULL) {
             // ---- P = x1 . x2 under the decays, tiles of 16 x 16 on and below the diagonal
             float rsum[MT], csum[MT][4];
 #pragma unroll
             for (int mm = 0; mm < MT; ++mm) {
-                const int m = wave + NW * mm;
-                if (m >= NTILE) break;
+                const int m = wave + TW * mm;
+                if (m >= NTILE || wave >= TW) break;
                 const int it = m < 1 ? 0 : m < 3 ? 1 : m < 6 ? 2 : 3;
                 const int jt = m - it * (it + 1) / 2;
                 f32x4 a = {0.0f, 0.0f, 0.0f, 0.0f};
+                constexpr int AHEAD = PARTS == 1 ? (KB < 4 ? KB : 4) : 1;   // operands in flight
 #pragma unroll
-                for (int kb = 0; kb < KB; ++kb) {
-                    u32x4 k[PARTS], q[PARTS];
+                for (int k0 = 0; k0 < KB; k0 += AHEAD) {
+                    u32x4 k[AHEAD][PARTS], q[AHEAD][PARTS];
 #pragma unroll
-                    for (int i = 0; i < PARTS; ++i) {
-                        k[i] = row_op<KD>(X2 + i * C * KD, 16 * jt, kb, lane);
-                        q[i] = row_op<KD>(X1 + i * C * KD, 16 * it, kb, lane);
+                    for (int x = 0; x < AHEAD * PARTS; ++x) {
+                        const int kb = x / PARTS, i = x % PARTS;
+                        k[kb][i] = row_op<KD>(X2 + i * C * KD, 16 * jt, k0 + kb, lane);
+                        q[kb][i] = row_op<KD>(X1 + i * C * KD, 16 * it, k0 + kb, lane);
                     }
-                    a = mma_parts<PARTS, PARTS>(k, q, a);
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int kb = 0; kb < AHEAD; ++kb) a = mma_parts<PARTS, PARTS>(k[kb], q[kb], a);
                 }
                 const int i = 16 * it + l16, j0 = 16 * jt + 4 * g4;
                 const int o = p_block(it, jt >> 1) * 512 + at_piece<32>(l16, 2 * (jt & 1) + (g4 >> 1)) + 4 * (g4 & 1);
@@ -623,7 +677,7 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW)) linattn_pass_kern
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const float w = __builtin_amdgcn_exp2f((gi - gj[r]) + (ei - ej[r]));
-                        a[r] = j0 + r <= i ? raw[r] * (w * p.wscale) : 0.0f;
+                        a[r] = j0 + r <= i ? raw[r] * (w * p_scale) : 0.0f;
                     }
                     uint32_t u[PP], v[PP];
                     split<PP>(a[0], a[1], u);
@@ -659,41 +713,44 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW)) linattn_pass_kern
             next();
             // ---- the incoming state's share, e^{G_i} R^T x1_i
 #pragma unroll
-            for (int it = 0; it < IT; ++it) acc[it] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int x = 0; x < IT * NT; ++x) acc[x / NT][x % NT] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
-                u32x4 sp[SP];
+                u32x4 q[IT][PARTS];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const f32x4& s = S[2 * kb + (e >> 1)];
+                for (int x = 0; x < IT * PARTS; ++x)
+                    q[x / PARTS][x % PARTS] = row_op<KD>(X1 + (x % PARTS) * C * KD, 16 * (x / PARTS), kb, lane);
+                if (PARTS == 1) __builtin_amdgcn_sched_barrier(0);
+                u32x4 sp[NT][SP];
+#pragma unroll
+                for (int x = 0; x < 4 * NT; ++x) {
+                    const int nt = x >> 2, e = x & 3;
+                    const f32x4& s = S[2 * kb + (e >> 1)][nt];
                     uint32_t w[SP];
                     split<SP>(s[2 * (e & 1)], s[2 * (e & 1) + 1], w);
 #pragma unroll
-                    for (int k = 0; k < SP; ++k) sp[k][e] = w[k];
+                    for (int k = 0; k < SP; ++k) sp[nt][k][e] = w[k];
                 }
 #pragma unroll
-                for (int it = 0; it < IT; ++it) {
-                    u32x4 q[PARTS];
-#pragma unroll
-                    for (int i = 0; i < PARTS; ++i) q[i] = row_op<KD>(X1 + i * C * KD, 16 * it, kb, lane);
-                    acc[it] = mma_parts<PARTS, SP>(q, sp, acc[it]);
-                }
+                for (int x = 0; x < IT * NT; ++x)
+                    acc[x / NT][x % NT] = mma_parts<PARTS, SP>(q[x / NT], sp[x % NT], acc[x / NT][x % NT]);
             }
             f32x4 d[DOTS ? IT : 1];
 #pragma unroll
             for (int it = 0; it < IT; ++it) {
                 const f32x4 e = *reinterpret_cast<const f32x4*>(&dec.in[16 * it + 4 * g4]);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) acc[it][r] *= e[r];
+                for (int x = 0; x < 4 * NT; ++x) acc[it][x >> 2][x & 3] *= e[x & 3];
                 if constexpr (DOTS) {
                     d[it] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int i = 0; i < PARTS; ++i) {
-                        const uint2 x = tile_op<BV>(X4 + i * C * BV, 16 * it, wave * 16, lane);
-                        d[it][0] = fmaf(bf_lo(x.x), acc[it][0], d[it][0]);
-                        d[it][1] = fmaf(bf_hi(x.x), acc[it][1], d[it][1]);
-                        d[it][2] = fmaf(bf_lo(x.y), acc[it][2], d[it][2]);
-                        d[it][3] = fmaf(bf_hi(x.y), acc[it][3], d[it][3]);
+                    for (int y = 0; y < NT * PARTS; ++y) {
+                        const int nt = y / PARTS;
+                        const uint2 x = tile_op<BV>(X4 + (y % PARTS) * C * BV, 16 * it, w0 + 16 * nt, lane);
+                        d[it][0] = fmaf(bf_lo(x.x), acc[it][nt][0], d[it][0]);
+                        d[it][1] = fmaf(bf_hi(x.x), acc[it][nt][1], d[it][1]);
+                        d[it][2] = fmaf(bf_lo(x.y), acc[it][nt][2], d[it][2]);
+                        d[it][3] = fmaf(bf_hi(x.y), acc[it][nt][3], d[it][3]);
                     }
 #pragma unroll
                     for (int r = 0; r < 4; ++r) d[it][r] = sum16(d[it][r]);
@@ -709,8 +766,8 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW)) linattn_pass_kern
                 if constexpr (CROSS) {
 #pragma unroll
                     for (int mm = 0; mm < MT; ++mm) {
-                        const int m = wave + NW * mm;
-                        if (m >= NTILE) break;
+                        const int m = wave + TW * mm;
+                        if (m >= NTILE || wave >= TW) break;
                         if (g4 == 0) cross[16 * m + l16] = rsum[mm];
                         if (l16 == 0) {
 #pragma unroll
@@ -726,23 +783,23 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW)) linattn_pass_kern
 #pragma unroll
                         for (int w = 0; w < NW; ++w) v += part[w * C + tid];
                         const int64_t o = (int64_t(slice) * p.T + t) * p.H + h;
-                        p.dots[o] = v * p.oscale;
+                        p.dots[o] = v;
                         if constexpr (CROSS) {
                             const int it = tid >> 4;
                             float rsv = 0.0f, csv = 0.0f;
                             for (int m = 0; m <= it; ++m) rsv += cross[16 * (it * (it + 1) / 2 + m) + l16];
                             for (int m = it; m < IT; ++m) csv += cross[16 * (NTILE + m * (m + 1) / 2 + it) + l16];
-                            p.cross[o] = (rsv - csv) * p.oscale;
+                            p.cross[o] = rsv - csv;
                         }
                     }
                 }
             }
             if (ahead && n + 1 < nch) {
-                load3(n + 1, tid, X3);
+                load3(n + 1, X3);
                 if constexpr (DOTS)
-                    load4(n + 1, tid);
+                    load4(n + 1);
                 else
-                    load1(n + 1, tid);
+                    load1(n + 1);
             }
         } else {
             next();
@@ -750,11 +807,13 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW)) linattn_pass_kern
         }
 
         // ---- the chunk's own share, P x3, and the outgoing state
-        const float all = dec.all;
+        const float fold = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, dec.fold)));
+        if (fold != 1.0f) {
 #pragma unroll
-        for (int m = 0; m < 2 * KB; ++m)
+            for (int m = 0; m < 2 * KB; ++m)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) S[m][r] *= all;
+                for (int x = 0; x < 4 * NT; ++x) S[m][x >> 2][x & 3] *= fold;
+        }
 #pragma unroll
         for (int jb = 0; jb < JB; ++jb) {
             if constexpr (FULL) {
@@ -763,81 +822,94 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW)) linattn_pass_kern
                     u32x4 q[PP];
 #pragma unroll
                     for (int k = 0; k < PP; ++k) q[k] = row_op<32>(PT + k * PB + p_block(it, jb) * 512, 0, 0, lane);
-                    acc[it] = mma_parts<PP, PARTS>(q, v[jb], acc[it]);
+                    #pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) acc[it][nt] = mma_parts<PP, PARTS>(q, v[jb][nt], acc[it][nt]);
                 }
             }
-            u32x4 vp[3];
+            u32x4 vp[NT][VP];
             const f32x4 f0 = *reinterpret_cast<const f32x4*>(&dec.out[32 * jb + 8 * g4]);
             const f32x4 f1 = *reinterpret_cast<const f32x4*>(&dec.out[32 * jb + 8 * g4 + 4]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int z = 0; z < 4 * NT; ++z) {
+                const int nt = z >> 2, e = z & 3;
                 float x = 0.0f, y = 0.0f;
 #pragma unroll
                 for (int i = PARTS - 1; i >= 0; --i) {
-                    x += bf_lo(v[jb][i][e]);
-                    y += bf_hi(v[jb][i][e]);
+                    x += bf_lo(v[jb][nt][i][e]);
+                    y += bf_hi(v[jb][nt][i][e]);
                 }
                 const f32x4& f = e < 2 ? f0 : f1;
-                uint32_t w[3];
-                split<3>(x * f[2 * (e & 1)], y * f[2 * (e & 1) + 1], w);
+                uint32_t w[VP];
+                split<VP>(x * f[2 * (e & 1)], y * f[2 * (e & 1) + 1], w);
 #pragma unroll
-                for (int k = 0; k < 3; ++k) vp[k][e] = w[k];
+                for (int k = 0; k < VP; ++k) vp[nt][k][e] = w[k];
             }
+            constexpr int AHEAD = PARTS == 1 ? 4 : 1;   // operands in flight
 #pragma unroll
-            for (int m = 0; m < 2 * KB; ++m) {
-                u32x4 k[PARTS];
+            for (int m0 = 0; m0 < 2 * KB; m0 += AHEAD) {
+                u32x4 k[AHEAD][PARTS];
 #pragma unroll
-                for (int i = 0; i < PARTS; ++i)
-                    k[i] = col_op<KD, 1>(X2 + i * C * KD, 32 * jb, 32 * (m >> 1) + 4 * (m & 1), lane);
-                S[m] = mma_parts<PARTS, 3>(k, vp, S[m]);
+                for (int x = 0; x < AHEAD * PARTS; ++x) {
+                    const int m = m0 + x / PARTS, i = x % PARTS;
+                    k[x / PARTS][i] = col_op<KD, 1>(X2 + i * C * KD, 32 * jb, 32 * (m >> 1) + 4 * (m & 1), lane);
+                }
+                if (AHEAD > 1) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int x = 0; x < AHEAD * NT; ++x)
+                    S[m0 + x / NT][x % NT] = mma_parts<PARTS, VP>(k[x / NT], vp[x % NT], S[m0 + x / NT][x % NT]);
             }
         }
 
         if constexpr (FULL) {
-            // rows behind the piece's end fall outside the window
+            // rows behind the piece's end fall outside the window, as do columns past the head's
             const int oe = PARTS == 3 || p.out_f32 ? 4 : 2;
             const int64_t pitch64 = p.so * oe;
             const Rsrc ro = rows_rsrc(static_cast<char*>(p.out) + c0 * pitch64 + int64_t(h) * p.vd * oe, pitch64, hi - c0, C);
             const int pitch = rev ? -int(pitch64) : int(pitch64);
             const int lane0 = int(pitch64) * (rev ? C - 1 : 0) + 4 * g4 * pitch;
             if (oe == 4) {
-                const int col = c_wave + l16;
-                const uint32_t o0 = lane0 + 4 * col;
 #pragma unroll
-                for (int it = 0; it < IT; ++it)
+                for (int nt = 0; nt < NT; ++nt) {
+                    const int col = c_wave + 16 * nt + l16;
+                    const uint32_t o0 = col < p.vd ? lane0 + 4 * col : kPast;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[it][r] * p.oscale), ro,
-                                                              col < p.vd ? o0 + uint32_t((16 * it + r) * pitch) : kPast, 0, 0);
+                    for (int x = 0; x < 4 * IT; ++x)
+                        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[x >> 2][nt][x & 3]), ro,
+                                                              o0 + uint32_t((16 * (x >> 2) + (x & 3)) * pitch), 0, 0);
+                }
             } else if (p.pairs) {
                 // neighbouring lanes swap one row for another: two columns of one row each
                 const bool odd = lane & 1;
-                const int col = c_wave + (l16 & ~1);
-                const uint32_t o0 = lane0 + (odd ? pitch : 0) + 2 * col;
+                const uint32_t pick = odd ? 0x03020706u : 0x05040100u;   // own and the neighbour's halves
 #pragma unroll
-                for (int it = 0; it < IT; ++it)
+                for (int nt = 0; nt < NT; ++nt) {
+                    const int col = c_wave + 16 * nt + (l16 & ~1);
+                    const uint32_t o0 = col < p.vd ? lane0 + (odd ? pitch : 0) + 2 * col : kPast;
 #pragma unroll
-                    for (int r = 0; r < 4; r += 2) {
-                        const float x = acc[it][r] * p.oscale, y = acc[it][r + 1] * p.oscale;
-                        const float got = swap1(odd ? x : y);
-                        __builtin_amdgcn_raw_buffer_store_b32(odd ? pack2(got, y) : pack2(x, got), ro,
-                                                              col < p.vd ? o0 + uint32_t((16 * it + r) * pitch) : kPast, 0, 0);
-                    }
+                    for (int it = 0; it < IT; ++it)
+#pragma unroll
+                        for (int r = 0; r < 4; r += 2) {
+                            const uint32_t own = pack2(acc[it][nt][r], acc[it][nt][r + 1]);
+                            __builtin_amdgcn_raw_buffer_store_b32(__builtin_amdgcn_perm(swap1(own), own, pick), ro,
+                                                                  o0 + uint32_t((16 * it + r) * pitch), 0, 0);
+                        }
+                }
             } else {
-                const int col = c_wave + l16;
-                const uint32_t o0 = lane0 + 2 * col;
 #pragma unroll
-                for (int it = 0; it < IT; ++it)
+                for (int nt = 0; nt < NT; ++nt) {
+                    const int col = c_wave + 16 * nt + l16;
+                    const uint32_t o0 = col < p.vd ? lane0 + 2 * col : kPast;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        __builtin_amdgcn_raw_buffer_store_b16(IOT<uint16_t>::from_f32(acc[it][r] * p.oscale), ro,
-                                                              col < p.vd ? o0 + uint32_t((16 * it + r) * pitch) : kPast, 0, 0);
+                    for (int x = 0; x < 4 * IT; ++x)
+                        __builtin_amdgcn_raw_buffer_store_b16(IOT<uint16_t>::from_f32(acc[x >> 2][nt][x & 3]), ro,
+                                                              o0 + uint32_t((16 * (x >> 2) + (x & 3)) * pitch), 0, 0);
+                }
             }
         }
         if (ahead && n + 1 < nch && !TWO2) {
             lds_barrier();                      // x2 (and with row dots x1) has been read
-            load2(n + 1, tid, X2);
-            if constexpr (DOTS) load1(n + 1, tid);
+            load2(n + 1, X2);
+            if constexpr (DOTS) load1(n + 1);
         }
     };
     for (int64_t n = 0; n < nch; n += 2) {
@@ -847,14 +919,18 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW)) linattn_pass_kern
 
     // ------------------------------------------------ the state that leaves
     float* dst = nullptr;
-    float mul = 1.0f;
+    // the scale that the registers' state still has, from its head's wave
+    __syncthreads();
+    if (dec_wave && lane == 0) decs[0][hw].fold = __builtin_amdgcn_exp2f(float(dl.scale));
+    __syncthreads();
+    float mul = decs[0][hw].fold;
     if (FULL) {
         if (last && p.s_out) {
             dst = p.s_out + (int64_t(slot) * p.H + h) * ssz;
             // against time the state before the first token has that token's decay too
             if (rev && sq.end > sq.start) {
                 const float g = p.g[sq.start * p.sg + h];
-                mul = __builtin_amdgcn_exp2f((g < kMinDecay ? kMinDecay : g) * kLog2e);
+                mul *= __builtin_amdgcn_exp2f((g < kMinDecay ? kMinDecay : g) * kLog2e);
             }
         }
     } else {
@@ -865,32 +941,34 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW)) linattn_pass_kern
 #pragma unroll
         for (int m = 0; m < 2 * KB; ++m)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = 32 * (m >> 1) + 8 * g4 + 4 * (m & 1) + r, col = c_wave + l16;
-                if (row < p.kd && col < p.vd) dst[row * rs + col * cs] = mul * S[m][r];
+            for (int x = 0; x < 4 * NT; ++x) {
+                const int nt = x >> 2, r = x & 3, row = 32 * (m >> 1) + 8 * g4 + 4 * (m & 1) + r, col = c_wave + 16 * nt + l16;
+                if (row < p.kd && col < p.vd) dst[row * rs + col * cs] = mul * S[m][nt][r];
             }
     }
 }
 
 // Chooses the kernel of a pass's sizes and starts it.
-template <int MODE> inline bool launch_pass(const ssm_detail::LinattnPass& p, bool f32, hipStream_t s) {
+template <int MODE> inline bool launch_pass(const ssm_detail::LinattnPasses& q, int count, bool f32, hipStream_t s) {
+    const LinattnPass& p = q.p[0];
     const int shape = MODE >= ssm_detail::kLinDots ? ssm_detail::linattn_shape(p.vd, false)
                                                    : ssm_detail::linattn_shape(p.vd, p.r1 % 2 == 0 && p.r2 % 2 == 0);
     const int64_t blocks = int64_t(p.npieces) * (shape == ssm_detail::kTwoHeads ? p.H / 2 : p.H) * p.nslices;
-    const dim3 grid(static_cast<uint32_t>(blocks)), block(shape == ssm_detail::kNarrow ? 256 : 512);
+    const dim3 grid(static_cast<uint32_t>(blocks), count), block(shape == ssm_detail::kNarrow ? 256 : 512);
     // float32 rows take three times the LDS: chunks of 32 keep two workgroups on a CU
+    constexpr bool GRAD = MODE >= ssm_detail::kLinDots;
+    const auto start = [&](auto* kernel) { launch_kernel(kernel, grid, block, 0, s, q); };
 #define SSM_LIN_CASE(K, NW, NH)                                                                     \
     do {                                                                                            \
-        if (f32)                                                                                    \
-            launch_kernel(linattn_pass_kernel<3, K, NW, 32, MODE, NH>, grid, block, 0, s, p);        \
-        else                                                                                        \
-            launch_kernel(linattn_pass_kernel<1, K, NW, 64, MODE, NH>, grid, block, 0, s, p);        \
+        if (f32) start(linattn_pass_kernel<3, K, NW, 1, 32, MODE, NH, 3>);                          \
+        else if (GRAD || p.exact) start(linattn_pass_kernel<1, K, NW, 1, 64, MODE, NH, 3>);         \
+        else start(linattn_pass_kernel<1, K, NW, 1, 64, MODE, NH, GRAD ? 3 : 2>);                   \
     } while (0)
 #define SSM_LIN_WAVES(K)                                                                            \
     do {                                                                                            \
         if (shape == ssm_detail::kWide) SSM_LIN_CASE(K, 8, 1);                                      \
         else if (shape == ssm_detail::kNarrow) SSM_LIN_CASE(K, 4, 1);                               \
-        else if constexpr (MODE < ssm_detail::kLinDots) SSM_LIN_CASE(K, 8, 2);                      \
+        else if constexpr (!GRAD) SSM_LIN_CASE(K, 8, 2);                                            \
     } while (0)
     if (p.kd <= 64)
         SSM_LIN_WAVES(64);

@@ -34,6 +34,7 @@ struct GradTail {
     float* part;            // [pieces][H] sums of dg (decay per head)
     float* dg;
     int32_t slices, head_decay;
+    int32_t open_end;       // a gradient arrives at the final states
 };
 
 // <S, dS> at the start of each piece, one workgroup per piece and head.
@@ -51,8 +52,18 @@ __global__ void __launch_bounds__(kThreads) linattn_cross_kernel(GradTail t) {
     const float* u = local ? t.fwd + (pi * p.H + h) * n : t.s0 ? t.s0 + (int64_t(seq) * p.H + h) * n : nullptr;
     const float* v = local ? t.rev + ((pi - 1) * p.H + h) * n : t.s0 ? t.ds0 + (int64_t(seq) * p.H + h) * n : nullptr;
     float s = 0.0f;
-    if (u)
-        for (int64_t i = threadIdx.x; i < n; i += kThreads) s = fmaf(u[i], v[i], s);
+    const int64_t n4 = n % 4 == 0 && !((reinterpret_cast<uintptr_t>(u) | reinterpret_cast<uintptr_t>(v)) & 15) ? n : 0;
+    if (u) {
+        f32x4 a = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+        for (int64_t i = 4 * threadIdx.x; i < n4; i += 4 * kThreads) {
+            const f32x4 x = *reinterpret_cast<const f32x4*>(u + i), y = *reinterpret_cast<const f32x4*>(v + i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a[e] = fmaf(x[e], y[e], a[e]);
+        }
+        s = (a[0] + a[1]) + (a[2] + a[3]);
+        for (int64_t i = n4 + threadIdx.x; i < n; i += kThreads) s = fmaf(u[i], v[i], s);
+    }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
@@ -67,27 +78,26 @@ __global__ void __launch_bounds__(kThreads) linattn_cross_kernel(GradTail t) {
     }
 }
 
-// dg of one piece for 16 heads: 16 threads of a head take a part of the tokens each, add it
-// up, then walk it again from the sum of the parts before.  Sums in float64.
-__global__ void __launch_bounds__(kThreads) linattn_dg_kernel(GradTail t) {
-    __shared__ double sums[16][17];
+// dg of one piece for 16 heads.  64 threads of a head take 16 tokens each at a time: their
+// sum, the sums of the threads before, then the running values.  Sums in float64.  Where the
+// next piece's start is known too, what the running sum misses there is spread over the piece
+// in proportion (the errors of the terms walk at random; this halves them and more).
+constexpr int kDgThreads = 1024, kDgParts = kDgThreads / 16, kDgTokens = 16;
+
+__global__ void __launch_bounds__(kDgThreads) linattn_dg_kernel(GradTail t) {
+    __shared__ double sums[kDgParts][17];
     const LinattnPass& p = t.p;
     const int64_t pi = blockIdx.x;
     const int hh = threadIdx.x & 15, part = threadIdx.x >> 4, h = blockIdx.y * 16 + hh;
     const int seq = find_seq(p, pi);
-    if (seq < 0) {
-        if (t.head_decay && part == 0 && h < p.H) t.part[pi * p.H + h] = 0.0f;
-        return;
-    }
-    const Seq sq = seq_range(p, seq);
-    const int64_t local = pi - piece_base(p, seq), len = sq.end - sq.start;
+    const Seq sq = seq < 0 ? Seq{0, 0} : seq_range(p, seq);
+    const int64_t local = seq < 0 ? -1 : pi - piece_base(p, seq), len = sq.end - sq.start;
+    const bool on = h < p.H;
     if (local < 0 || local * p.piece >= len) {
-        if (t.head_decay && part == 0 && h < p.H) t.part[pi * p.H + h] = 0.0f;
+        if (t.head_decay && part == 0 && on) t.part[pi * p.H + h] = 0.0f;
         return;
     }
     const int64_t lo = sq.start + local * p.piece, hi = sq.end - lo > p.piece ? lo + p.piece : sq.end;
-    const int64_t step = (hi - lo + 15) / 16;
-    const int64_t t0 = lo + part * step < hi ? lo + part * step : hi, t1 = t0 + step < hi ? t0 + step : hi;
     const int64_t plane = p.T * p.H;
     auto f = [&](int64_t tok) {
         double s = 0.0;
@@ -97,26 +107,52 @@ __global__ void __launch_bounds__(kThreads) linattn_dg_kernel(GradTail t) {
         }
         return s;
     };
-    double s = 0.0;
-    if (h < p.H)
-        for (int64_t tok = t0; tok < t1; ++tok) s += f(tok);
-    sums[hh][part] = s;
-    __syncthreads();
-    double run = h < p.H ? double(t.x[pi * p.H + h]) : 0.0;
-    for (int k = 0; k < part; ++k) run += sums[hh][k];
-    __syncthreads();
-    double all = 0.0;
-    if (h < p.H)
-        for (int64_t tok = t0; tok < t1; ++tok) {
-            all += run;
-            if (!t.head_decay) t.dg[tok * p.H + h] = float(run);
-            run += f(tok);
-        }
-    if (t.head_decay) {
-        sums[hh][part] = all;
+    // the closing error: in one walk of the sums, before the walk that writes
+    double miss = 0.0;
+    const double start = on ? double(t.x[pi * p.H + h]) : 0.0;
+    if (hi < sq.end || !t.open_end) {
+        double s = 0.0;
+        if (on)
+            for (int64_t tok = lo + part; tok < hi; tok += kDgParts) s += f(tok);
+        sums[part][hh] = s;
         __syncthreads();
-        if (part == 0 && h < p.H) {
-            for (int k = 1; k < 16; ++k) all += sums[hh][k];
+        s = start;
+        for (int k = 0; k < kDgParts; ++k) s += sums[k][hh];
+        __syncthreads();
+        miss = ((hi < sq.end && on ? double(t.x[(pi + 1) * p.H + h]) : 0.0) - s) / double(hi - lo);
+    }
+    double run = start, all = 0.0;
+    for (int64_t base = lo; base < hi; base += kDgParts * kDgTokens) {
+        const int64_t t0 = base + part * kDgTokens;
+        double v[kDgTokens], s = 0.0;
+#pragma unroll
+        for (int k = 0; k < kDgTokens; ++k) {
+            v[k] = on && t0 + k < hi ? f(t0 + k) : 0.0;
+            s += v[k];
+        }
+        sums[part][hh] = s;
+        __syncthreads();
+        double r = run;
+        for (int k = 0; k < kDgParts; ++k) {
+            const double o = sums[k][hh];
+            if (k < part) r += o;
+            run += o;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kDgTokens; ++k)
+            if (on && t0 + k < hi) {
+                const double d = r + miss * double(t0 + k - lo);
+                all += d;
+                if (!t.head_decay) t.dg[(t0 + k) * p.H + h] = float(d);
+                r += v[k];
+            }
+    }
+    if (t.head_decay) {
+        sums[part][hh] = all;
+        __syncthreads();
+        if (part == 0 && on) {
+            for (int k = 1; k < kDgParts; ++k) all += sums[k][hh];
             t.part[pi * p.H + h] = float(all);
         }
     }
@@ -137,19 +173,36 @@ __global__ void __launch_bounds__(kThreads) linattn_dg_sum_kernel(GradTail t) {
     if (threadIdx.x == 0) t.dg[h] = float(sums[0]);
 }
 
-// Sums the heads that share a row: out[t][kh] = sum_r part[t][kh * rep + r].
-template <typename IO>
-__global__ void __launch_bounds__(kThreads) linattn_group_kernel(LinattnPass p, const float* part, IO* out, int rep,
-                                                                 int width) {
-    const int64_t kheads = p.H / rep, n = p.T * kheads * width;
+// Sums the heads that share a row, out[t][kh] = sum_r part[t][kh * rep + r], for dq and dk
+// (the grid's y); one workgroup takes whole tokens, VW columns a thread.  Bound by the bytes
+// of the parts.
+struct GroupArgs {
+    const float* part[2];
+    void* out[2];
+    int32_t rep, width, kheads;
+};
+template <typename IO, int VW>
+__global__ void __launch_bounds__(kThreads) linattn_group_kernel(LinattnPass p, GroupArgs a) {
+    typedef float vf __attribute__((ext_vector_type(VW)));
+    const int per = a.width / VW, n = a.kheads * per;   // threads' work of one token
     const int64_t lo = p.cu ? seq_range(p, 0).start : 0, hi = p.cu ? seq_range(p, p.nseq - 1).end : p.T;
-    for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < n; i += int64_t(gridDim.x) * kThreads) {
-        const int64_t d = i % width, th = i / width, tok = th / kheads;
-        const float* q = part + th * rep * width + d;
-        float s = 0.0f;
-        if (tok >= lo && tok < hi)
-            for (int r = 0; r < rep; ++r) s += q[int64_t(r) * width];
-        out[i] = IOT<IO>::from_f32(s);
+    const float* part = a.part[blockIdx.y];
+    IO* out = static_cast<IO*>(a.out[blockIdx.y]);
+    for (int64_t tok = blockIdx.x; tok < p.T; tok += gridDim.x) {
+        const bool on = tok >= lo && tok < hi;
+        for (int i = threadIdx.x; i < n; i += kThreads) {
+            const int kh = i / per, d = (i - kh * per) * VW;
+            const float* q = part + (tok * p.H + int64_t(kh) * a.rep) * a.width + d;
+            vf s = {};
+            if (on) {
+#pragma unroll 4
+                for (int r = 0; r < a.rep; ++r) s += *reinterpret_cast<const vf*>(q + int64_t(r) * a.width);
+            }
+            IO raw[VW];
+#pragma unroll
+            for (int e = 0; e < VW; ++e) raw[e] = IOT<IO>::from_f32(s[e]);
+            __builtin_memcpy(out + (tok * a.kheads + kh) * a.width + d, raw, sizeof(raw));
+        }
     }
 }
 
@@ -188,7 +241,7 @@ inline int make_grad_plan(const ssm_linattn_dims* d, bool packed, GradPlan* pl) 
     if (piece == 0) {
         piece = 1024;
         const int64_t slots = 512;
-        while (piece > 256 && cdiv(d->tokens, piece) * units < slots) piece /= 2;
+        while (piece > 64 && cdiv(d->tokens, piece) * units < slots) piece /= 2;
     }
     pl->pieced = piece < each;
     pl->piece = pl->pieced ? piece : (int64_t(1) << 31);
@@ -208,8 +261,8 @@ inline int make_grad_plan(const ssm_linattn_dims* d, bool packed, GradPlan* pl) 
 }  // namespace la
 }  // namespace
 
-bool ssm_detail::launch_linattn_grad_pass(const LinattnPass& p, bool f32, LinattnMode mode, hipStream_t s) {
-    return mode == kLinDots ? la::launch_pass<kLinDots>(p, f32, s) : la::launch_pass<kLinCross>(p, f32, s);
+bool ssm_detail::launch_linattn_grad_pass(const LinattnPasses& p, int count, bool f32, LinattnMode mode, hipStream_t s) {
+    return mode == kLinDots ? la::launch_pass<kLinDots>(p, count, f32, s) : la::launch_pass<kLinCross>(p, count, f32, s);
 }
 
 extern "C" {
@@ -288,6 +341,7 @@ int ssm_linattn_bwd(const void* q, const void* k, const void* v, const float* g,
     base.nseq = static_cast<int32_t>(d.nseq); base.nslots = base.nseq;
     base.r1 = base.r2 = base.r3 = base.r4 = 1;
     base.wscale = base.oscale = 1.0f;
+    base.exact = gr.dg || gr.ds0;
     base.wide = wide_rows(q, z.q, d.dk, z.e) && wide_rows(k, z.k, d.dk, z.e) && wide_rows(v, z.v, d.dv, z.e) &&
                 wide_rows(dout, z.o, d.dv, z.e);
 
@@ -306,48 +360,46 @@ int ssm_linattn_bwd(const void* q, const void* k, const void* v, const float* g,
     pq.s_in = s0; pq.st_t = 1; pq.carry = fwd; pq.oscale = d.scale;
     pq.out = shared ? static_cast<void*>(wq) : gr.dq; pq.out_f32 = shared; pq.so = d.nheads * d.dk;
     pq.dots = da; pq.cross = de; pq.pairs = pair_rows(gr.dq, pq.so, d.dk);
+    pq.exact = 0;
     LinattnPass pk = pq;     // dk = (v, do, q) from dS
     pk.x1 = v; pk.s1 = z.v; pk.x2 = dout; pk.s2 = z.o; pk.x3 = q; pk.s3 = z.q; pk.x4 = k; pk.s4 = z.k;
     pk.s_in = ds_last; pk.carry = rev; pk.oscale = 1.0f; pk.wscale = d.scale; pk.reverse = 1;
     pk.out = shared ? static_cast<void*>(wkk) : gr.dk; pk.dots = db; pk.cross = nullptr;
     pk.pairs = pair_rows(gr.dk, pk.so, d.dk);
     LinattnPass pv = sr;     // dv = (k, q, do) from dS
-    pv.x1 = k; pv.s1 = z.k; pv.r1 = rep; pv.out = gr.dv; pv.so = wv; pv.s_out = gr.ds0; pv.pairs = pair_rows(gr.dv, wv, d.dv);
+    pv.x1 = k; pv.s1 = z.k; pv.r1 = rep; pv.out = gr.dv; pv.so = wv; pv.s_out = gr.ds0; pv.exact = gr.ds0 != nullptr; pv.pairs = pair_rows(gr.dv, wv, d.dv);
 
     launch_error = hipSuccess;
     if (pl.pieced) {
-        launch_linattn_pass(sf, f32, kLinStates, s);
-        launch_linattn_carry(sf, s);
-        launch_linattn_pass(sr, f32, kLinStates, s);
-        launch_linattn_carry(sr, s);
+        launch_linattn_pass({{sf, sr}}, 2, f32, kLinStates, s);
+        launch_linattn_carry({{sf, sr}}, 2, s);
     }
     if (gr.dg) {
-        launch_linattn_grad_pass(pq, f32, kLinCross, s);
-        launch_linattn_grad_pass(pk, f32, kLinDots, s);
+        launch_linattn_grad_pass({{pq, pq}}, 1, f32, kLinCross, s);
+        launch_linattn_grad_pass({{pk, pk}}, 1, f32, kLinDots, s);
     } else {
-        launch_linattn_pass(pq, f32, kLinFull, s);
-        launch_linattn_pass(pk, f32, kLinFull, s);
+        launch_linattn_pass({{pq, pk}}, 2, f32, kLinFull, s);
     }
-    launch_linattn_pass(pv, f32, kLinFull, s);
+    launch_linattn_pass({{pv, pv}}, 1, f32, kLinFull, s);
     if (shared) {
-        const int64_t n = d.tokens * wk;
-        const dim3 grid(static_cast<uint32_t>(cdiv(n, kThreads) < 65536 ? cdiv(n, kThreads) : 65536)), block(kThreads);
-        const int w = static_cast<int>(d.dk), r = rep;
+        GroupArgs ga = {{wq, wkk}, {gr.dq, gr.dk}, rep, static_cast<int32_t>(d.dk), static_cast<int32_t>(d.kheads)};
+        const dim3 grid(static_cast<uint32_t>(d.tokens < 65536 ? d.tokens : 65536), 2), block(kThreads);
+        const bool v4 = d.dk % 4 == 0 && !misaligned(gr.dq, 4 * z.e) && !misaligned(gr.dk, 4 * z.e);
         if (f32) {
-            launch_kernel(linattn_group_kernel<float>, grid, block, 0, s, base, wq, static_cast<float*>(gr.dq), r, w);
-            launch_kernel(linattn_group_kernel<float>, grid, block, 0, s, base, wkk, static_cast<float*>(gr.dk), r, w);
+            if (v4) launch_kernel(linattn_group_kernel<float, 4>, grid, block, 0, s, base, ga);
+            else launch_kernel(linattn_group_kernel<float, 1>, grid, block, 0, s, base, ga);
         } else {
-            launch_kernel(linattn_group_kernel<uint16_t>, grid, block, 0, s, base, wq, static_cast<uint16_t*>(gr.dq), r, w);
-            launch_kernel(linattn_group_kernel<uint16_t>, grid, block, 0, s, base, wkk, static_cast<uint16_t*>(gr.dk), r, w);
+            if (v4) launch_kernel(linattn_group_kernel<uint16_t, 4>, grid, block, 0, s, base, ga);
+            else launch_kernel(linattn_group_kernel<uint16_t, 1>, grid, block, 0, s, base, ga);
         }
     }
     if (gr.dg) {
         GradTail t = {};
         t.p = sf; t.fwd = fwd; t.rev = rev; t.s0 = s0; t.ds0 = gr.ds0; t.a = da; t.b = db; t.e = de; t.x = x;
-        t.part = part; t.dg = gr.dg; t.slices = static_cast<int32_t>(pl.slices_q); t.head_decay = d.head_decay;
+        t.part = part; t.dg = gr.dg; t.slices = static_cast<int32_t>(pl.slices_q); t.head_decay = d.head_decay; t.open_end = ds_last != nullptr;
         const uint32_t np = static_cast<uint32_t>(pl.npieces), hh = static_cast<uint32_t>(d.nheads);
         launch_kernel(linattn_cross_kernel, dim3(np, hh), dim3(kThreads), 0, s, t);
-        launch_kernel(linattn_dg_kernel, dim3(np, (hh + 15) / 16), dim3(kThreads), 0, s, t);
+        launch_kernel(linattn_dg_kernel, dim3(np, (hh + 15) / 16), dim3(kDgThreads), 0, s, t);
         if (d.head_decay) launch_kernel(linattn_dg_sum_kernel, dim3(hh), dim3(kThreads), 0, s, t);
     }
     if (cu_seqlens)

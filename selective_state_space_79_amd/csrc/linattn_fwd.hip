@@ -9,11 +9,12 @@ namespace la {
 // ---------------------------------------------------------------- pieces' starting states
 // Walks the pieces of one sequence and head: each piece's own end state (from a zero start)
 // is replaced by the state it starts from.  Bound by the states' bytes; 4 values per thread.
-template <int VW> __global__ void __launch_bounds__(kThreads) linattn_carry_kernel(ssm_detail::LinattnPass p) {
+template <int VW> __global__ void __launch_bounds__(kThreads) linattn_carry_kernel(ssm_detail::LinattnPasses q) {
+    const LinattnPass& p = q.p[blockIdx.y / q.p[0].H];
     typedef float vf __attribute__((ext_vector_type(VW)));
     const int64_t ssz = int64_t(p.kd) * p.vd;
     const int64_t e = (int64_t(blockIdx.x) * kThreads + threadIdx.x) * VW;
-    const int h = blockIdx.y, seq = blockIdx.z;
+    const int h = blockIdx.y % p.H, seq = blockIdx.z;
     const int slot = find_slot(p.slots, p.nslots, seq);
     if (slot < 0 || e >= ssz) return;
     const Seq sq = seq_range(p, seq);
@@ -23,16 +24,28 @@ template <int VW> __global__ void __launch_bounds__(kThreads) linattn_carry_kern
     if (base + n > p.npieces) n = p.npieces - base;
     vf s = {};
     if (p.s_in) s = *reinterpret_cast<const vf*>(p.s_in + (int64_t(slot) * p.H + h) * ssz + e);
-    for (int64_t m = 0; m < n; ++m) {
-        const int64_t pi = base + (p.reverse ? n - 1 - m : m);
-        float* c = p.carry + (pi * p.H + h) * ssz + e;
-        if (m + 1 < n) {
-            const vf own = *reinterpret_cast<const vf*>(c);
-            const float t = p.tot[pi * p.H + h];
-            *reinterpret_cast<vf*>(c) = s;
-            s = t * s + own;
-        } else {
-            *reinterpret_cast<vf*>(c) = s;
+    // the pieces' own states are asked for four ahead
+    constexpr int A = 4;
+    const auto at = [&](int64_t m) { return ((base + (p.reverse ? n - 1 - m : m)) * p.H + h); };
+    vf own[A];
+    float t[A];
+#pragma unroll
+    for (int k = 0; k < A; ++k)
+        if (k + 1 < n) {
+            own[k] = *reinterpret_cast<const vf*>(p.carry + at(k) * ssz + e);
+            t[k] = p.tot[at(k)];
+        }
+    for (int64_t m0 = 0; m0 < n; m0 += A) {
+#pragma unroll
+        for (int k = 0; k < A; ++k) {
+            const int64_t m = m0 + k;
+            if (m >= n) break;
+            *reinterpret_cast<vf*>(p.carry + at(m) * ssz + e) = s;
+            if (m + 1 < n) s = t[k] * s + own[k];
+            if (m + A + 1 < n) {
+                own[k] = *reinterpret_cast<const vf*>(p.carry + at(m + A) * ssz + e);
+                t[k] = p.tot[at(m + A)];
+            }
         }
     }
 }
@@ -135,32 +148,18 @@ struct Plan {
     size_t carry, tot;   // bytes
 };
 
-// Pieces along the tokens.  A workgroup walks its piece chunk by chunk, so with few heads
-// and sequences the walk's length bounds the time; pieces cost a second pass over keys and
-// values and their states' bytes.  The estimate, in microseconds (measured on heads of
-// 128 x 128): 4.5 for a chunk of a full pass and 2 for one of the states' pass while the
-// workgroups fit the card, in rounds of 512, and the bytes at 4 TB/s.  How long the sequences
-// of a packed call are is not known here: one long one is assumed.
-inline int64_t choose_piece(const ssm_linattn_dims* d, int64_t units, int64_t each, bool packed) {
-    const double state = 4.0 * static_cast<double>(d->nheads * d->dk * d->dv) / 4e6;      // us per copy of one piece's states
-    const double rows = 2.0 * static_cast<double>(d->tokens) *
-                        static_cast<double>(d->nheads * d->dv + d->kheads * d->dk) / 4e6;    // us of keys and values
-    const int64_t nseq = packed ? 1 : d->nseq;
-    const auto rounds = [&](int64_t groups) { return static_cast<double>(cdiv(groups, 512)); };
-    const double whole_walk = rounds(units * nseq) * 4.5 * static_cast<double>(cdiv(each, 64));
-    double best = whole_walk > 2 * rows ? whole_walk : 2 * rows;
-    int64_t piece = 0;
-    for (int64_t n = 1; 64 * n < each; n = n < 4 ? n + 1 : n * 3 / 2) {
-        const int64_t pieces = nseq * cdiv(each, 64 * n);
-        const double full = rounds(units * pieces) * 4.5 * static_cast<double>(n), pre = full * (2.0 / 4.5);
-        const double t = (full > 2 * rows ? full : 2 * rows) + (pre > rows ? pre : rows) +
-                         4 * state * static_cast<double>(pieces) + 8;
-        if (t < best) {
-            best = t;
-            piece = 64 * n;
-        }
-    }
-    return piece;
+// Pieces along the tokens.  A workgroup walks its piece chunk by chunk, 3.6 us for 64 tokens
+// of a 128 x 128 head alone on its CU and 8.8 us for two side by side, so work is cut into the
+// 512 workgroups that the card holds at once; more, smaller pieces only add states to carry.
+// Measured, us: 131072 tokens of 16 heads 754 in 512 workgroups (pieces of 4096), 794 in 1024,
+// 884 in 2048; 8 ragged prompts of 8192 tokens in all, 32 heads, 136 in pieces of 512, 168 of
+// 256, 254 of 2048.  Cutting costs two launches and a second pass over keys and values:
+// sequences of up to 256 tokens stay whole.
+inline int64_t choose_piece(const ssm_linattn_dims* d, int64_t units, int64_t each) {
+    const int64_t want = 512 / units;   // pieces of the whole call
+    if (want < 2 || each <= 256) return 0;
+    const int64_t piece = cdiv(cdiv(d->tokens, want), 64) * 64;
+    return piece < each ? piece : 0;
 }
 
 inline int make_plan(const ssm_linattn_dims* d, bool packed, Plan* pl) {
@@ -169,7 +168,7 @@ inline int make_plan(const ssm_linattn_dims* d, bool packed, Plan* pl) {
     const int64_t units = d->nheads * slices;
     const int64_t each = packed ? d->tokens : d->tokens / d->nseq;
     int64_t piece = d->piece_len;
-    if (piece == 0) piece = choose_piece(d, pairs ? units / 2 : units, each, packed);
+    if (piece == 0) piece = choose_piece(d, pairs ? units / 2 : units, each);
     pl->pieced = piece > 0 && piece < each;
     pl->piece = pl->pieced ? piece : (int64_t(1) << 31);
     pl->npieces = !pl->pieced ? d->nseq : packed ? d->tokens / piece + d->nseq : d->nseq * cdiv(each, piece);
@@ -182,18 +181,19 @@ inline int make_plan(const ssm_linattn_dims* d, bool packed, Plan* pl) {
 }  // namespace la
 }  // namespace
 
-bool ssm_detail::launch_linattn_pass(const LinattnPass& p, bool f32, LinattnMode mode, hipStream_t s) {
-    return mode == kLinStates ? la::launch_pass<kLinStates>(p, f32, s) : la::launch_pass<kLinFull>(p, f32, s);
+bool ssm_detail::launch_linattn_pass(const LinattnPasses& p, int count, bool f32, LinattnMode mode, hipStream_t s) {
+    return mode == kLinStates ? la::launch_pass<kLinStates>(p, count, f32, s) : la::launch_pass<kLinFull>(p, count, f32, s);
 }
 
-void ssm_detail::launch_linattn_carry(const LinattnPass& p, hipStream_t s) {
+void ssm_detail::launch_linattn_carry(const LinattnPasses& q, int count, hipStream_t s) {
+    const LinattnPass& p = q.p[0];
     const int64_t ssz = int64_t(p.kd) * p.vd;
-    const bool v4 = ssz % 4 == 0 && !misaligned(p.s_in, 16);
-    const dim3 grid(static_cast<uint32_t>(cdiv(ssz, la::kThreads * (v4 ? 4 : 1))), p.H, p.nseq);
+    const bool v4 = ssz % 4 == 0 && !misaligned(p.s_in, 16) && !misaligned(q.p[1].s_in, 16);
+    const dim3 grid(static_cast<uint32_t>(cdiv(ssz, la::kThreads * (v4 ? 4 : 1))), p.H * count, p.nseq);
     if (v4)
-        launch_kernel(la::linattn_carry_kernel<4>, grid, dim3(la::kThreads), 0, s, p);
+        launch_kernel(la::linattn_carry_kernel<4>, grid, dim3(la::kThreads), 0, s, q);
     else
-        launch_kernel(la::linattn_carry_kernel<1>, grid, dim3(la::kThreads), 0, s, p);
+        launch_kernel(la::linattn_carry_kernel<1>, grid, dim3(la::kThreads), 0, s, q);
 }
 
 extern "C" {
@@ -257,6 +257,7 @@ int ssm_linattn_fwd(const void* q, const void* k, const void* v, const float* g,
     p.npieces = static_cast<int32_t>(pl.npieces); p.pieced = pl.pieced;
     p.wide = wide_rows(q, z.q, d.dk, z.e) && wide_rows(k, z.k, d.dk, z.e) && wide_rows(v, z.v, d.dv, z.e);
     p.pairs = pair_rows(o, z.o, d.dv);
+    p.exact = s_last != nullptr;
     p.wscale = 1.0f; p.oscale = d.scale;
     const bool f32 = d.io_dtype == SSM_F32;
     hipStream_t s = static_cast<hipStream_t>(stream);
@@ -264,10 +265,10 @@ int ssm_linattn_fwd(const void* q, const void* k, const void* v, const float* g,
     if (pl.pieced) {
         p.carry = static_cast<float*>(d.workspace);
         p.tot = reinterpret_cast<float*>(static_cast<char*>(d.workspace) + pl.carry);
-        ssm_detail::launch_linattn_pass(p, f32, ssm_detail::kLinStates, s);
-        ssm_detail::launch_linattn_carry(p, s);
+        ssm_detail::launch_linattn_pass({{p, p}}, 1, f32, ssm_detail::kLinStates, s);
+        ssm_detail::launch_linattn_carry({{p, p}}, 1, s);
     }
-    ssm_detail::launch_linattn_pass(p, f32, ssm_detail::kLinFull, s);
+    ssm_detail::launch_linattn_pass({{p, p}}, 1, f32, ssm_detail::kLinFull, s);
     return ssm_detail::launch_error == hipSuccess ? SSM_OK : SSM_ERR_HIP;
 }
 
