@@ -505,8 +505,8 @@ typedef struct ssm_linattn_grads {
 } ssm_linattn_grads;
 
 /* Bytes of workspace of ssm_linattn_bwd (never 0 for valid dims; 0 for dims it refuses):
- * the states and state gradients at the pieces' ends, three or more floats per token and
- * head for dg, and float32 dq and dk per head when heads share them. */
+ * the states and state gradients at the pieces' ends, and float32 dq and dk per head (heads
+ * that share them are added up, and dg is formed, from these). */
 SSM_API size_t ssm_linattn_bwd_workspace_bytes(const ssm_linattn_dims* dims);
 
 /* Enqueue the gradients of

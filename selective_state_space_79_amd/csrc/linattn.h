@@ -26,7 +26,6 @@ struct LinattnPass {
     const void* x1;
     const void* x2;
     const void* x3;
-    const void* x4;           // rows dotted with the state's share of the output (row dots)
     void* out;                // I/O type, or float32 when out_f32
     const float* g;           // log decays
     const int32_t* cu;        // starts of the packed sequences; null: equal lengths
@@ -35,19 +34,17 @@ struct LinattnPass {
     float* s_out;             // user's final states, nullable
     float* carry;             // [pieces][H][kd][vd] (or transposed): the pieces' states
     float* tot;               // [pieces][H]: the pieces' decays
-    float* dots;              // row dots: [slices][T][H] of x4 . (state's share)
-    float* cross;             // row dots with CROSS: [slices][T][H], see linattn_bwd.hip
-    int64_t s1, s2, s3, s4, so, sg;   // elements between tokens
+    int64_t s1, s2, s3, so, sg;   // elements between tokens
     int64_t T, L;             // tokens; tokens of each sequence when cu is null
     int64_t piece;            // tokens of a piece (a multiple of the chunk)
-    int32_t r1, r2, r3, r4;   // heads that share one head of x1, x2, x3, x4
+    int32_t r1, r2, r3;       // heads that share one head of x1, x2, x3
     int32_t H, kd, vd, nslices;
     int32_t nseq, nslots, npieces, pieced;
     int32_t st_t;             // states lie (vd, kd) instead of (kd, vd)
     int32_t reverse, out_f32;
-    int32_t wide;             // rows of x1 .. x4 allow 16-byte loads at 32-bit offsets
+    int32_t wide;             // rows of x1 .. x3 allow 16-byte loads at 32-bit offsets
     int32_t pairs;            // out allows stores of two bf16
-    int32_t exact;            // a float32 output depends on the state
+    int32_t exact;            // a float32 output depends on the state's values
     float wscale, oscale;
 };
 
@@ -57,9 +54,11 @@ struct LinattnPasses {
 };
 
 // The launches return false for sizes that no kernel covers (nothing launched).
-enum LinattnMode { kLinStates = 0, kLinFull = 1, kLinDots = 2, kLinCross = 3 };
+// kLinStates: the pieces' own end states; kLinFull: the outputs; kLinExact: the outputs in
+// float32, with every product of float32's precision (bf16 rows: out_f32 set).
+enum LinattnMode { kLinStates = 0, kLinFull = 1, kLinExact = 2 };
 bool launch_linattn_pass(const LinattnPasses& p, int count, bool f32, LinattnMode mode, hipStream_t s);       // modes 0, 1
-bool launch_linattn_grad_pass(const LinattnPasses& p, int count, bool f32, LinattnMode mode, hipStream_t s);  // modes 2, 3
+bool launch_linattn_exact(const LinattnPasses& p, int count, bool f32, hipStream_t s);   // (float32 rows: mode 1)
 void launch_linattn_carry(const LinattnPasses& p, int count, hipStream_t s);
 // How a pass over vd columns is cut: 128 columns of a head to a workgroup, 64, or two heads
 // of up to 64 that share x1 and x2
@@ -192,13 +191,6 @@ template <int W, int SPREAD> __device__ inline u32x4 col_op(const uint16_t* t, i
     return u32x4{u.x, u.y, v.x, v.y};
 }
 
-// Rows r0 + 4g .. + 3 of column c0 + i for lane 16g + i: a tile in the layout of a product.
-template <int W> __device__ inline uint2 tile_op(const uint16_t* t, int r0, int c0, int lane) {
-    const int r = r0 + 4 * (lane >> 4) + ((lane >> 2) & 3), c = c0 + 4 * (lane & 3);
-    return __builtin_bit_cast(
-        uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(t + at_piece<W>(r, c >> 3) + (c & 7))));
-}
-
 // Products of operands in NA and NB parts: those whose part numbers add up to at most `most`
 // (the rest is below what the parts themselves leave out).
 template <int NA, int NB>
@@ -212,17 +204,6 @@ __device__ inline f32x4 mma_parts(const u32x4 (&a)[NA], const u32x4 (&b)[NB], f3
     return c;
 }
 
-// Sum over the 16 lanes of a row (every lane gets it): rotations within the row.
-__device__ inline float sum16(float v) {
-    const auto ror = [](float x, auto c) {
-        return __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(x), decltype(c)::value, 0xf, 0xf, true));
-    };
-    v += ror(v, std::integral_constant<int, 0x128>{});
-    v += ror(v, std::integral_constant<int, 0x124>{});
-    v += ror(v, std::integral_constant<int, 0x122>{});
-    v += ror(v, std::integral_constant<int, 0x121>{});
-    return v;
-}
 // The value of the lane's neighbour (lanes 2n and 2n + 1 swap).
 __device__ inline uint32_t swap1(uint32_t v) { return __builtin_amdgcn_update_dpp(0u, v, 0xB1, 0xf, 0xf, true); }
 
@@ -438,8 +419,8 @@ __device__ constexpr int p_block(int it, int jb) { return it < 2 ? it : 2 * it -
 // go two to a workgroup (NH), each with its own decays on the same products; other narrow
 // heads take four waves.
 //
-// Parts: products that end in a float32 output (row dots, and the state where the caller
-// gets it: VP) take three parts of what is not a bf16 input; those that end in a bf16
+// Parts: products that end in a float32 output (the exact mode's, and the state where the
+// caller gets it: VP) take three parts of what is not a bf16 input; those that end in a bf16
 // output take two.
 constexpr int pass_waves(int KD, int NW, int NT) { return KD == 256 ? NW / 4 : NW / 2; }   // per SIMD
 
@@ -447,31 +428,25 @@ template <int PARTS, int KD, int NW, int NT, int C, int MODE, int NH, int VP>
 __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_kernel(ssm_detail::LinattnPasses passes) {
     using namespace ssm_detail;
     const LinattnPass& p = passes.p[blockIdx.y];
-    constexpr bool FULL = MODE >= kLinFull, DOTS = MODE >= kLinDots, CROSS = MODE == kLinCross;
+    constexpr bool FULL = MODE >= kLinFull, EXACT = MODE == kLinExact;
     constexpr int T = 64 * NW, BV = 16 * NT * NW, IT = C / 16, JB = C / 32, KB = KD / 32;
     constexpr int TW = NH == 1 ? NW - 1 : NW;         // waves with tiles of P: the one with the decays has none
     constexpr int NTILE = IT * (IT + 1) / 2, MT = (NTILE + TW - 1) / TW;   // tiles of P, and the most of one wave
-    constexpr int SP = DOTS || PARTS == 3 ? 3 : 2;    // parts of the state in the read-out
-    constexpr int PP = PARTS == 3 ? 3 : 2;            // parts of P
+    constexpr int SP = EXACT || PARTS == 3 ? 3 : 2, PP = SP;   // parts of the state and of P in the output
     constexpr int NBLK = C == 64 ? 6 : 2, PB = NBLK * 512;
     constexpr int HW = BV / NH, WH = NW / NH;         // columns and waves of one head
     static_assert(C == 64 || C == 32, "chunk");
-    static_assert(NH == 1 || (NH == 2 && !DOTS), "heads");
+    static_assert(NH == 1 || (NH == 2 && !EXACT), "heads");
     // bf16 rows come straight into LDS, each tile as soon as the last chunk's readers are
     // done with it: x2 (read to the end) and without a read-out x3 have a second tile, where
-    // that still leaves room for two workgroups on a CU
-    constexpr bool DMA = PARTS == 1, TWO2 = DMA && !DOTS && !(FULL && KD == 128 && NH == 2), TWO3 = DMA && !FULL;
+    // that still leaves room for two workgroups on a CU.  The exact output's third part of P
+    // takes that room: there the state goes on first, and then all three tiles are free.
+    constexpr bool DMA = PARTS == 1, TWO2 = DMA && !EXACT && !(FULL && KD == 128 && NH == 2), TWO3 = DMA && !FULL;
     __shared__ __align__(16) uint16_t X2a[PARTS * C * KD], X2b[TWO2 ? C * KD : 8];
     __shared__ __align__(16) uint16_t X3a[PARTS * C * BV], X3b[TWO3 ? C * BV : 8];
     __shared__ __align__(16) uint16_t X1[FULL ? PARTS * C * KD : 8];
     __shared__ __align__(16) uint16_t PTs[FULL ? NH * PP * PB : 8];   // decayed x1 . x2, per head
-    __shared__ __align__(16) uint16_t X4[DOTS ? PARTS * C * BV : 8];
     __shared__ Decays<C> decs[2][NH];
-    // row dots, and the tiles' row and column sums: over x1, once its readers are done
-    float* part = reinterpret_cast<float*>(X1);
-    float* cross = part + NW * C;
-    static_assert(!DOTS || PARTS * C * KD * 2 >= (NW * C + 32 * NTILE) * 4, "the sums fit x1's tile");
-
     const int tid = threadIdx.x, lane = tid & 63, g4 = lane >> 4, l16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // neighbouring workgroups run on different XCDs: give each XCD neighbouring heads, so
@@ -499,9 +474,8 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
     const char* b1 = FULL ? static_cast<const char*>(p.x1) + int64_t(h0 / p.r1) * p.kd * E : nullptr;
     const char* b2 = static_cast<const char*>(p.x2) + int64_t(h0 / p.r2) * p.kd * E;
     const char* b3 = static_cast<const char*>(p.x3) + (int64_t(h0 / p.r3) * p.vd + slice * BV) * E;
-    const char* b4 = DOTS ? static_cast<const char*>(p.x4) + (int64_t(h0 / p.r4) * p.vd + slice * BV) * E : nullptr;
     const int w3 = p.vd - slice * BV;
-    const int64_t pitch1 = p.s1 * E, pitch2 = p.s2 * E, pitch3 = p.s3 * E, pitch4 = p.s4 * E;
+    const int64_t pitch1 = p.s1 * E, pitch2 = p.s2 * E, pitch3 = p.s3 * E;
 
     // ------------------------------------------------ starting state
     f32x4 S[2 * KB][NT];
@@ -545,11 +519,9 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
     }
     Tile<PARTS, C, KD, T> t1, t2;
     Tile<PARTS, C, BV, T, HW> t3;
-    Tile<PARTS, C, BV, T> t4;
     t2.prepare(tid, pitch2, rev, p.kd);
     t3.prepare(tid, pitch3, rev, w3);
     if constexpr (FULL) t1.prepare(tid, pitch1, rev, p.kd);
-    if constexpr (DOTS) t4.prepare(tid, pitch4, rev, w3);
     // the tile of chunk n, at once (bf16) or into registers; `any` rows are copied at the
     // chunk's own turn
     auto load1 = [&](int64_t n) {
@@ -564,16 +536,11 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
         const int64_t c0 = first_of(n);
         t3.load(to, wave, b3 + c0 * pitch3, pitch3, hi - c0);
     };
-    auto load4 = [&](int64_t n) {
-        const int64_t c0 = first_of(n);
-        t4.load(X4, wave, b4 + c0 * pitch4, pitch4, hi - c0);
-    };
     const bool ahead = DMA && p.wide;          // tiles are loaded ahead of their chunk
     if (ahead && nch > 0) {
         load2(0, X2a);
         load3(0, X3a);
         if constexpr (FULL) load1(0);
-        if constexpr (DOTS) load4(0);
     }
     wait_memory<0>();
 
@@ -592,7 +559,7 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
         const int tid = 64 * wave + lane, g4 = lane >> 4, l16 = lane & 15;
         if (ahead) {
             // this chunk's rows; what was stored since they were asked for may still be under way
-            if constexpr (!FULL || !TWO2)
+            if constexpr (!FULL)
                 wait_memory<0>();
             else if (p.pairs)
                 wait_memory<2 * IT * NT>();
@@ -606,16 +573,13 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
                 load2(n, X2);
                 if constexpr (FULL) load1(n);
                 load3(n, X3);
-                if constexpr (DOTS) load4(n);
                 t2.store(X2, tid);
                 if constexpr (FULL) t1.store(X1, tid);
                 t3.store(X3, tid);
-                if constexpr (DOTS) t4.store(X4, tid);
             } else {
                 t2.copy_any(X2, tid, b2 + c0 * pitch2, pitch2, rows, rev, p.kd);
                 if constexpr (FULL) t1.copy_any(X1, tid, b1 + c0 * pitch1, pitch1, rows, rev, p.kd);
                 t3.copy_any(X3, tid, b3 + c0 * pitch3, pitch3, rows, rev, w3);
-                if constexpr (DOTS) t4.copy_any(X4, tid, b4 + c0 * pitch4, pitch4, rows, rev, w3);
             }
             lds_barrier();
         }
@@ -644,7 +608,6 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
         f32x4 acc[IT][NT];
         if constexpr (FULL) {
             // ---- P = x1 . x2 under the decays, tiles of 16 x 16 on and below the diagonal
-            float rsum[MT], csum[MT][4];
 #pragma unroll
             for (int mm = 0; mm < MT; ++mm) {
                 const int m = wave + TW * mm;
@@ -685,30 +648,6 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
 #pragma unroll
                     for (int k = 0; k < PP; ++k) *reinterpret_cast<uint2*>(PTs + (hh * PP + k) * PB + o) = uint2{u[k], v[k]};
                 }
-                if constexpr (CROSS) {
-                    // the other product of the same rows, x3 . x4 over this slice's columns;
-                    // sums below the diagonal by rows and by columns of the same values
-                    f32x4 b = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int kb = 0; kb < BV / 32; ++kb) {
-                        u32x4 k[PARTS], q[PARTS];
-#pragma unroll
-                        for (int i2 = 0; i2 < PARTS; ++i2) {
-                            k[i2] = row_op<BV>(X3 + i2 * C * BV, 16 * jt, kb, lane);
-                            q[i2] = row_op<BV>(X4 + i2 * C * BV, 16 * it, kb, lane);
-                        }
-                        b = mma_parts<PARTS, PARTS>(k, q, b);
-                    }
-                    float row = 0.0f;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float x = j0 + r < i ? a[r] * b[r] : 0.0f;
-                        row += x;
-                        csum[mm][r] = sum16(x);
-                    }
-                    row += __shfl_xor(row, 16);
-                    rsum[mm] = row + __shfl_xor(row, 32);
-                }
             }
             next();
             // ---- the incoming state's share, e^{G_i} R^T x1_i
@@ -735,129 +674,84 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
                 for (int x = 0; x < IT * NT; ++x)
                     acc[x / NT][x % NT] = mma_parts<PARTS, SP>(q[x / NT], sp[x % NT], acc[x / NT][x % NT]);
             }
-            f32x4 d[DOTS ? IT : 1];
 #pragma unroll
             for (int it = 0; it < IT; ++it) {
                 const f32x4 e = *reinterpret_cast<const f32x4*>(&dec.in[16 * it + 4 * g4]);
 #pragma unroll
                 for (int x = 0; x < 4 * NT; ++x) acc[it][x >> 2][x & 3] *= e[x & 3];
-                if constexpr (DOTS) {
-                    d[it] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int y = 0; y < NT * PARTS; ++y) {
-                        const int nt = y / PARTS;
-                        const uint2 x = tile_op<BV>(X4 + (y % PARTS) * C * BV, 16 * it, w0 + 16 * nt, lane);
-                        d[it][0] = fmaf(bf_lo(x.x), acc[it][nt][0], d[it][0]);
-                        d[it][1] = fmaf(bf_hi(x.x), acc[it][nt][1], d[it][1]);
-                        d[it][2] = fmaf(bf_lo(x.y), acc[it][nt][2], d[it][2]);
-                        d[it][3] = fmaf(bf_hi(x.y), acc[it][nt][3], d[it][3]);
-                    }
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) d[it][r] = sum16(d[it][r]);
-                }
-            }
-            values();
-            lds_barrier();                      // P is there; x1, x3 and x4 have been read
-            if constexpr (DOTS) {
-                if (l16 == 0) {
-#pragma unroll
-                    for (int it = 0; it < IT; ++it) *reinterpret_cast<f32x4*>(&part[wave * C + 16 * it + 4 * g4]) = d[it];
-                }
-                if constexpr (CROSS) {
-#pragma unroll
-                    for (int mm = 0; mm < MT; ++mm) {
-                        const int m = wave + TW * mm;
-                        if (m >= NTILE || wave >= TW) break;
-                        if (g4 == 0) cross[16 * m + l16] = rsum[mm];
-                        if (l16 == 0) {
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) cross[16 * (NTILE + m) + 4 * g4 + r] = csum[mm][r];
-                        }
-                    }
-                }
-                lds_barrier();
-                if (tid < C) {
-                    const int64_t t = c0 + (rev ? C - 1 - tid : tid);
-                    if (t < hi) {
-                        float v = 0.0f;
-#pragma unroll
-                        for (int w = 0; w < NW; ++w) v += part[w * C + tid];
-                        const int64_t o = (int64_t(slice) * p.T + t) * p.H + h;
-                        p.dots[o] = v;
-                        if constexpr (CROSS) {
-                            const int it = tid >> 4;
-                            float rsv = 0.0f, csv = 0.0f;
-                            for (int m = 0; m <= it; ++m) rsv += cross[16 * (it * (it + 1) / 2 + m) + l16];
-                            for (int m = it; m < IT; ++m) csv += cross[16 * (NTILE + m * (m + 1) / 2 + it) + l16];
-                            p.cross[o] = rsv - csv;
-                        }
-                    }
-                }
-            }
-            if (ahead && n + 1 < nch) {
-                load3(n + 1, X3);
-                if constexpr (DOTS)
-                    load4(n + 1);
-                else
-                    load1(n + 1);
             }
         } else {
             next();
-            values();
         }
+        values();
 
-        // ---- the chunk's own share, P x3, and the outgoing state
-        const float fold = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, dec.fold)));
-        if (fold != 1.0f) {
+        // ---- the outgoing state
+        auto onward = [&] {
+            const float fold = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, dec.fold)));
+            if (fold != 1.0f) {
 #pragma unroll
-            for (int m = 0; m < 2 * KB; ++m)
+                for (int m = 0; m < 2 * KB; ++m)
 #pragma unroll
-                for (int x = 0; x < 4 * NT; ++x) S[m][x >> 2][x & 3] *= fold;
-        }
+                    for (int x = 0; x < 4 * NT; ++x) S[m][x >> 2][x & 3] *= fold;
+            }
 #pragma unroll
-        for (int jb = 0; jb < JB; ++jb) {
-            if constexpr (FULL) {
+            for (int jb = 0; jb < JB; ++jb) {
+                u32x4 vp[NT][VP];
+                const f32x4 f0 = *reinterpret_cast<const f32x4*>(&dec.out[32 * jb + 8 * g4]);
+                const f32x4 f1 = *reinterpret_cast<const f32x4*>(&dec.out[32 * jb + 8 * g4 + 4]);
+#pragma unroll
+                for (int z = 0; z < 4 * NT; ++z) {
+                    const int nt = z >> 2, e = z & 3;
+                    float x = 0.0f, y = 0.0f;
+#pragma unroll
+                    for (int i = PARTS - 1; i >= 0; --i) {
+                        x += bf_lo(v[jb][nt][i][e]);
+                        y += bf_hi(v[jb][nt][i][e]);
+                    }
+                    const f32x4& f = e < 2 ? f0 : f1;
+                    uint32_t w[VP];
+                    split<VP>(x * f[2 * (e & 1)], y * f[2 * (e & 1) + 1], w);
+#pragma unroll
+                    for (int k = 0; k < VP; ++k) vp[nt][k][e] = w[k];
+                }
+                constexpr int AHEAD = PARTS == 1 ? (TWO2 ? 4 : 2) : 1;   // operands in flight
+#pragma unroll
+                for (int m0 = 0; m0 < 2 * KB; m0 += AHEAD) {
+                    u32x4 k[AHEAD][PARTS];
+#pragma unroll
+                    for (int x = 0; x < AHEAD * PARTS; ++x) {
+                        const int m = m0 + x / PARTS, i = x % PARTS;
+                        k[x / PARTS][i] = col_op<KD, 1>(X2 + i * C * KD, 32 * jb, 32 * (m >> 1) + 4 * (m & 1), lane);
+                    }
+                    if (AHEAD > 1) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int x = 0; x < AHEAD * NT; ++x)
+                        S[m0 + x / NT][x % NT] = mma_parts<PARTS, VP>(k[x / NT], vp[x % NT], S[m0 + x / NT][x % NT]);
+                }
+            }
+        };
+        if constexpr (FULL) {
+            if constexpr (!TWO2) onward();
+            lds_barrier();                      // P is there; x1 and x3 have been read (and x2, if the state is on)
+            if (ahead && n + 1 < nch) {
+                if constexpr (!TWO2) load2(n + 1, X2);
+                load3(n + 1, X3);
+                load1(n + 1);
+            }
+            // ---- the chunk's own share, P x3
+#pragma unroll
+            for (int jb = 0; jb < JB; ++jb)
 #pragma unroll
                 for (int it = 2 * jb; it < IT; ++it) {
                     u32x4 q[PP];
 #pragma unroll
                     for (int k = 0; k < PP; ++k) q[k] = row_op<32>(PT + k * PB + p_block(it, jb) * 512, 0, 0, lane);
-                    #pragma unroll
+#pragma unroll
                     for (int nt = 0; nt < NT; ++nt) acc[it][nt] = mma_parts<PP, PARTS>(q, v[jb][nt], acc[it][nt]);
                 }
-            }
-            u32x4 vp[NT][VP];
-            const f32x4 f0 = *reinterpret_cast<const f32x4*>(&dec.out[32 * jb + 8 * g4]);
-            const f32x4 f1 = *reinterpret_cast<const f32x4*>(&dec.out[32 * jb + 8 * g4 + 4]);
-#pragma unroll
-            for (int z = 0; z < 4 * NT; ++z) {
-                const int nt = z >> 2, e = z & 3;
-                float x = 0.0f, y = 0.0f;
-#pragma unroll
-                for (int i = PARTS - 1; i >= 0; --i) {
-                    x += bf_lo(v[jb][nt][i][e]);
-                    y += bf_hi(v[jb][nt][i][e]);
-                }
-                const f32x4& f = e < 2 ? f0 : f1;
-                uint32_t w[VP];
-                split<VP>(x * f[2 * (e & 1)], y * f[2 * (e & 1) + 1], w);
-#pragma unroll
-                for (int k = 0; k < VP; ++k) vp[nt][k][e] = w[k];
-            }
-            constexpr int AHEAD = PARTS == 1 ? 4 : 1;   // operands in flight
-#pragma unroll
-            for (int m0 = 0; m0 < 2 * KB; m0 += AHEAD) {
-                u32x4 k[AHEAD][PARTS];
-#pragma unroll
-                for (int x = 0; x < AHEAD * PARTS; ++x) {
-                    const int m = m0 + x / PARTS, i = x % PARTS;
-                    k[x / PARTS][i] = col_op<KD, 1>(X2 + i * C * KD, 32 * jb, 32 * (m >> 1) + 4 * (m & 1), lane);
-                }
-                if (AHEAD > 1) __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int x = 0; x < AHEAD * NT; ++x)
-                    S[m0 + x / NT][x % NT] = mma_parts<PARTS, VP>(k[x / NT], vp[x % NT], S[m0 + x / NT][x % NT]);
-            }
+            if constexpr (TWO2) onward();
+        } else {
+            onward();
         }
 
         if constexpr (FULL) {
@@ -906,11 +800,6 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
                 }
             }
         }
-        if (ahead && n + 1 < nch && !TWO2) {
-            lds_barrier();                      // x2 (and with row dots x1) has been read
-            load2(n + 1, X2);
-            if constexpr (DOTS) load1(n + 1);
-        }
     };
     for (int64_t n = 0; n < nch; n += 2) {
         chunk(n, std::false_type{});
@@ -951,24 +840,28 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
 // Chooses the kernel of a pass's sizes and starts it.
 template <int MODE> inline bool launch_pass(const ssm_detail::LinattnPasses& q, int count, bool f32, hipStream_t s) {
     const LinattnPass& p = q.p[0];
-    const int shape = MODE >= ssm_detail::kLinDots ? ssm_detail::linattn_shape(p.vd, false)
+    const int shape = MODE == ssm_detail::kLinExact ? ssm_detail::linattn_shape(p.vd, false)
                                                    : ssm_detail::linattn_shape(p.vd, p.r1 % 2 == 0 && p.r2 % 2 == 0);
     const int64_t blocks = int64_t(p.npieces) * (shape == ssm_detail::kTwoHeads ? p.H / 2 : p.H) * p.nslices;
     const dim3 grid(static_cast<uint32_t>(blocks), count), block(shape == ssm_detail::kNarrow ? 256 : 512);
     // float32 rows take three times the LDS: chunks of 32 keep two workgroups on a CU
-    constexpr bool GRAD = MODE >= ssm_detail::kLinDots;
+    constexpr bool EXACT = MODE == ssm_detail::kLinExact;
     const auto start = [&](auto* kernel) { launch_kernel(kernel, grid, block, 0, s, q); };
 #define SSM_LIN_CASE(K, NW, NH)                                                                     \
     do {                                                                                            \
-        if (f32) start(linattn_pass_kernel<3, K, NW, 1, 32, MODE, NH, 3>);                          \
-        else if (GRAD || p.exact) start(linattn_pass_kernel<1, K, NW, 1, 64, MODE, NH, 3>);         \
-        else start(linattn_pass_kernel<1, K, NW, 1, 64, MODE, NH, GRAD ? 3 : 2>);                   \
+        if constexpr (EXACT) {                                                                      \
+            start(linattn_pass_kernel<1, K, NW, 1, 64, MODE, NH, 3>);                               \
+        } else {                                                                                    \
+            if (f32) start(linattn_pass_kernel<3, K, NW, 1, 32, MODE, NH, 3>);                      \
+            else if (p.exact) start(linattn_pass_kernel<1, K, NW, 1, 64, MODE, NH, 3>);             \
+            else start(linattn_pass_kernel<1, K, NW, 1, 64, MODE, NH, 2>);                          \
+        }                                                                                           \
     } while (0)
 #define SSM_LIN_WAVES(K)                                                                            \
     do {                                                                                            \
         if (shape == ssm_detail::kWide) SSM_LIN_CASE(K, 8, 1);                                      \
         else if (shape == ssm_detail::kNarrow) SSM_LIN_CASE(K, 4, 1);                               \
-        else if constexpr (!GRAD) SSM_LIN_CASE(K, 8, 2);                                            \
+        else if constexpr (!EXACT) SSM_LIN_CASE(K, 8, 2);                                           \
     } while (0)
     if (p.kd <= 64)
         SSM_LIN_WAVES(64);

@@ -4,18 +4,15 @@
 // time from the forward's states S, dk and dv against it from the gradient dS of the state).
 // States are kept at the ends of pieces of the sequences only and walked again inside.
 //
-// The decays' gradient.  dg_t = e^{g_t} <S_{t-1}, dS_t>.  In a chunk that state S_in enters
-// and that the gradient dS_out enters from behind, with D the decays between two tokens,
-//   a_i = scale e^{G_i} q_i S_in do_i           (what token i reads from before the chunk)
-//   b_j = e^{G_C - G_j} k_j dS_out v_j          (what later chunks read of token j)
-//   M_ij = scale D_ij (q_i . k_j)(do_i . v_j)   (what token i reads of token j < i)
-// dg_t sums every read that crosses t: with X_in = <S_in, dS_in> at the chunk's start, all
-// reads that cross it,
-//   dg_t = X_in + sum_{j<t} (b_j - a_j) + sum_{i>=t>j} M_ij
-//        = X_in + sum_{j<t} (b_j - a_j - e_j),   e_j = sum_i M_ji - sum_i M_ij.
-// The e_j come from the row and column sums of one M, so what they leave in sums outside
-// the rectangle i >= t > j cancels to float32 rounding.  X_in is taken afresh at each piece
-// as a product of the two states there, so the error of a running sum spans one piece.
+// The decays' gradient.  dg_t = e^{g_t} <S_{t-1}, dS_t> is the sum of all reads that cross t.
+// What token i reads in all is q_i . dq_i, what is read of token j is k_j . dk_j, so from one
+// token to the next dg changes by
+//   dg_{t+1} = dg_t + k_t . dk_t - q_t . dq_t
+// A running sum of these carries the error of every read that came and went.  So dq and dk
+// are formed to float32 here (kLinExact), and the sum starts afresh at each piece from
+// <S, dS>, with what it misses at the next piece's start spread over the piece.  dq and dk
+// per head go through float32 arrays, where the heads that share a row are added up, the row
+// products taken and the outputs rounded in one more pass.
 #include "linattn.h"
 
 namespace {
@@ -27,13 +24,11 @@ struct GradTail {
     const float* rev;       // [pieces][H][dk dv] state gradients that the pieces start from, behind
     const float* s0;
     const float* ds0;
-    const float* a;         // [slices][T][H]
-    const float* b;
-    const float* e;
+    const float* f;         // [T][H] k . dk - q . dq
     float* x;               // [pieces][H] <S, dS> at the pieces' starts
     float* part;            // [pieces][H] sums of dg (decay per head)
     float* dg;
-    int32_t slices, head_decay;
+    int32_t head_decay;
     int32_t open_end;       // a gradient arrives at the final states
 };
 
@@ -78,61 +73,57 @@ __global__ void __launch_bounds__(kThreads) linattn_cross_kernel(GradTail t) {
     }
 }
 
-// dg of one piece for 16 heads.  64 threads of a head take 16 tokens each at a time: their
-// sum, the sums of the threads before, then the running values.  Sums in float64.  Where the
-// next piece's start is known too, what the running sum misses there is spread over the piece
-// in proportion (the errors of the terms walk at random; this halves them and more).
+// dg of one piece for 16 heads: 64 threads of a head take 16 tokens each at a time, their
+// sum, the sums of the threads before, then the running values.  Sums in float64.
 constexpr int kDgThreads = 1024, kDgParts = kDgThreads / 16, kDgTokens = 16;
 
 __global__ void __launch_bounds__(kDgThreads) linattn_dg_kernel(GradTail t) {
-    __shared__ double sums[kDgParts][17];
+    __shared__ double sums[kDgParts][16];
     const LinattnPass& p = t.p;
     const int64_t pi = blockIdx.x;
     const int hh = threadIdx.x & 15, part = threadIdx.x >> 4, h = blockIdx.y * 16 + hh;
     const int seq = find_seq(p, pi);
     const Seq sq = seq < 0 ? Seq{0, 0} : seq_range(p, seq);
-    const int64_t local = seq < 0 ? -1 : pi - piece_base(p, seq), len = sq.end - sq.start;
+    const int64_t local = seq < 0 ? -1 : pi - piece_base(p, seq);
     const bool on = h < p.H;
-    if (local < 0 || local * p.piece >= len) {
+    if (local < 0 || local * p.piece >= sq.end - sq.start) {
         if (t.head_decay && part == 0 && on) t.part[pi * p.H + h] = 0.0f;
         return;
     }
     const int64_t lo = sq.start + local * p.piece, hi = sq.end - lo > p.piece ? lo + p.piece : sq.end;
-    const int64_t plane = p.T * p.H;
-    auto f = [&](int64_t tok) {
-        double s = 0.0;
-        for (int k = 0; k < t.slices; ++k) {
-            const int64_t o = k * plane + tok * p.H + h;
-            s += (double(t.b[o]) - double(t.a[o])) - double(t.e[o]);
-        }
-        return s;
-    };
-    // the closing error: in one walk of the sums, before the walk that writes
-    double miss = 0.0;
     const double start = on ? double(t.x[pi * p.H + h]) : 0.0;
+    const float* f = t.f + h;
+    // what the running sum misses at the next piece's start, or at an end that no gradient
+    // reaches (there dg is zero)
+    double miss = 0.0;
     if (hi < sq.end || !t.open_end) {
         double s = 0.0;
         if (on)
-            for (int64_t tok = lo + part; tok < hi; tok += kDgParts) s += f(tok);
+            for (int64_t tok = lo + part; tok < hi; tok += kDgParts) s += double(f[tok * p.H]);
         sums[part][hh] = s;
         __syncthreads();
         s = start;
+#pragma unroll 4
         for (int k = 0; k < kDgParts; ++k) s += sums[k][hh];
         __syncthreads();
-        miss = ((hi < sq.end && on ? double(t.x[(pi + 1) * p.H + h]) : 0.0) - s) / double(hi - lo);
+        if (on && hi < sq.end) {   // that piece's <S, dS> has the decay of its first token, as dg there
+            s -= double(t.x[(pi + 1) * p.H + h]);
+        }
+        miss = -s / double(hi - lo);
     }
     double run = start, all = 0.0;
     for (int64_t base = lo; base < hi; base += kDgParts * kDgTokens) {
         const int64_t t0 = base + part * kDgTokens;
-        double v[kDgTokens], s = 0.0;
+        float v[kDgTokens];
+        double s = 0.0;
 #pragma unroll
-        for (int k = 0; k < kDgTokens; ++k) {
-            v[k] = on && t0 + k < hi ? f(t0 + k) : 0.0;
-            s += v[k];
-        }
+        for (int k = 0; k < kDgTokens; ++k) v[k] = on && t0 + k < hi ? f[(t0 + k) * p.H] : 0.0f;
+#pragma unroll
+        for (int k = 0; k < kDgTokens; ++k) s += double(v[k]);
         sums[part][hh] = s;
         __syncthreads();
         double r = run;
+#pragma unroll 4
         for (int k = 0; k < kDgParts; ++k) {
             const double o = sums[k][hh];
             if (k < part) r += o;
@@ -145,13 +136,14 @@ __global__ void __launch_bounds__(kDgThreads) linattn_dg_kernel(GradTail t) {
                 const double d = r + miss * double(t0 + k - lo);
                 all += d;
                 if (!t.head_decay) t.dg[(t0 + k) * p.H + h] = float(d);
-                r += v[k];
+                r += double(v[k]);
             }
     }
     if (t.head_decay) {
         sums[part][hh] = all;
         __syncthreads();
         if (part == 0 && on) {
+#pragma unroll 4
             for (int k = 1; k < kDgParts; ++k) all += sums[k][hh];
             t.part[pi * p.H + h] = float(all);
         }
@@ -173,37 +165,94 @@ __global__ void __launch_bounds__(kThreads) linattn_dg_sum_kernel(GradTail t) {
     if (threadIdx.x == 0) t.dg[h] = float(sums[0]);
 }
 
-// Sums the heads that share a row, out[t][kh] = sum_r part[t][kh * rep + r], for dq and dk
-// (the grid's y); one workgroup takes whole tokens, VW columns a thread.  Bound by the bytes
-// of the parts.
+// From dq and dk per head in float32: the sums over the heads that share a row, rounded, and
+// f = k . dk - q . dq of each token and head.  LPR lanes take a row, 4 columns each (VW of
+// them in one access); bound by the bytes of the parts.
 struct GroupArgs {
-    const float* part[2];
-    void* out[2];
+    const float* dq;
+    const float* dk;
+    const void* q;
+    const void* k;
+    void* out_q;
+    void* out_k;
+    float* f;               // null: not wanted
+    int64_t sq, sk;
     int32_t rep, width, kheads;
 };
-template <typename IO, int VW>
+template <typename IO, int VW, int LPR>
 __global__ void __launch_bounds__(kThreads) linattn_group_kernel(LinattnPass p, GroupArgs a) {
     typedef float vf __attribute__((ext_vector_type(VW)));
-    const int per = a.width / VW, n = a.kheads * per;   // threads' work of one token
+    constexpr int M = 4 / VW;   // accesses per thread
+    const int lane = threadIdx.x % LPR;
     const int64_t lo = p.cu ? seq_range(p, 0).start : 0, hi = p.cu ? seq_range(p, p.nseq - 1).end : p.T;
-    const float* part = a.part[blockIdx.y];
-    IO* out = static_cast<IO*>(a.out[blockIdx.y]);
-    for (int64_t tok = blockIdx.x; tok < p.T; tok += gridDim.x) {
+    const int64_t rows = p.T * a.kheads, step = int64_t(gridDim.x) * (kThreads / LPR);
+    for (int64_t row = int64_t(blockIdx.x) * (kThreads / LPR) + threadIdx.x / LPR; row < rows; row += step) {
+        const int64_t tok = row / a.kheads;
+        const int kh = int(row - tok * a.kheads);
         const bool on = tok >= lo && tok < hi;
-        for (int i = threadIdx.x; i < n; i += kThreads) {
-            const int kh = i / per, d = (i - kh * per) * VW;
-            const float* q = part + (tok * p.H + int64_t(kh) * a.rep) * a.width + d;
-            vf s = {};
-            if (on) {
-#pragma unroll 4
-                for (int r = 0; r < a.rep; ++r) s += *reinterpret_cast<const vf*>(q + int64_t(r) * a.width);
-            }
-            IO raw[VW];
+        float q[4], k[4], sq[4], sk[4];
 #pragma unroll
-            for (int e = 0; e < VW; ++e) raw[e] = IOT<IO>::from_f32(s[e]);
-            __builtin_memcpy(out + (tok * a.kheads + kh) * a.width + d, raw, sizeof(raw));
+        for (int e = 0; e < 4; ++e) q[e] = k[e] = sq[e] = sk[e] = 0.0f;
+        if (on && a.f) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int c = VW == 4 ? 4 * lane + e : lane + LPR * e;
+                if (c < a.width) {
+                    q[e] = IOT<IO>::to_f32(static_cast<const IO*>(a.q)[tok * a.sq + int64_t(kh) * a.width + c]);
+                    k[e] = IOT<IO>::to_f32(static_cast<const IO*>(a.k)[tok * a.sk + int64_t(kh) * a.width + c]);
+                }
+            }
+        }
+        const int64_t base = (tok * p.H + int64_t(kh) * a.rep) * a.width;
+        if (on)
+#pragma unroll 2
+            for (int r = 0; r < a.rep; ++r) {
+                float d = 0.0f;
+#pragma unroll
+                for (int m = 0; m < M; ++m) {
+                    const int c = VW == 4 ? 4 * lane : lane + LPR * m;
+                    vf x = {}, y = {};
+                    if (c < a.width) {
+                        x = *reinterpret_cast<const vf*>(a.dq + base + int64_t(r) * a.width + c);
+                        y = *reinterpret_cast<const vf*>(a.dk + base + int64_t(r) * a.width + c);
+                    }
+#pragma unroll
+                    for (int e = 0; e < VW; ++e) {
+                        sq[m * VW + e] += x[e];
+                        sk[m * VW + e] += y[e];
+                        d = fmaf(k[m * VW + e], y[e], d);
+                        d = fmaf(-q[m * VW + e], x[e], d);
+                    }
+                }
+                if (a.f) {
+#pragma unroll
+                    for (int z = 1; z < LPR; z <<= 1) d += __shfl_xor(d, z);
+                    if (lane == 0) a.f[tok * p.H + int64_t(kh) * a.rep + r] = d;
+                }
+            }
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            const int c = VW == 4 ? 4 * lane : lane + LPR * m;
+            if (c >= a.width) continue;
+            IO x[VW], y[VW];
+#pragma unroll
+            for (int e = 0; e < VW; ++e) {
+                x[e] = IOT<IO>::from_f32(sq[m * VW + e]);
+                y[e] = IOT<IO>::from_f32(sk[m * VW + e]);
+            }
+            __builtin_memcpy(static_cast<IO*>(a.out_q) + row * a.width + c, x, sizeof(x));
+            __builtin_memcpy(static_cast<IO*>(a.out_k) + row * a.width + c, y, sizeof(y));
         }
     }
+}
+
+template <typename IO, int VW> void run_group(const LinattnPass& p, const GroupArgs& a, hipStream_t s) {
+    const int lpr = a.width <= 64 ? 16 : a.width <= 128 ? 32 : 64;
+    const int64_t blocks = cdiv(p.T * a.kheads, kThreads / lpr);
+    const dim3 grid(static_cast<uint32_t>(blocks < 16384 ? blocks : 16384)), block(kThreads);
+    if (lpr == 16) launch_kernel(linattn_group_kernel<IO, VW, 16>, grid, block, 0, s, p, a);
+    else if (lpr == 32) launch_kernel(linattn_group_kernel<IO, VW, 32>, grid, block, 0, s, p, a);
+    else launch_kernel(linattn_group_kernel<IO, VW, 64>, grid, block, 0, s, p, a);
 }
 
 // Rows of no sequence (before the first and behind the last): zero gradients.
@@ -226,7 +275,7 @@ struct GradPlan {
     int64_t piece, npieces;
     bool pieced;
     int64_t slices_q, slices_s;   // of passes with kd = dv, vd = dk, and with kd = dk, vd = dv
-    size_t carry, tot, dots, wide, x;   // bytes of one buffer each
+    size_t carry, tot, f, wide;   // bytes of one buffer each
     size_t bytes;
 };
 
@@ -251,18 +300,17 @@ inline int make_grad_plan(const ssm_linattn_dims* d, bool packed, GradPlan* pl) 
         return SSM_ERR_DIMS;
     pl->carry = pl->pieced ? up256(static_cast<size_t>(pl->npieces * d->nheads * d->dk * d->dv) * 4) : 0;
     pl->tot = up256(static_cast<size_t>(pl->npieces * d->nheads) * 4);
-    pl->x = pl->tot;
-    pl->dots = up256(static_cast<size_t>(pl->slices_q * d->tokens * d->nheads) * 4);
-    pl->wide = d->nheads == d->kheads ? 0 : up256(static_cast<size_t>(d->tokens * d->nheads * d->dk) * 4);
-    pl->bytes = 2 * pl->carry + 4 * pl->tot + 3 * pl->dots + 2 * pl->wide;
+    pl->f = up256(static_cast<size_t>(d->tokens * d->nheads) * 4);
+    pl->wide = up256(static_cast<size_t>(d->tokens * d->nheads * d->dk) * 4);
+    pl->bytes = 2 * pl->carry + 4 * pl->tot + pl->f + 2 * pl->wide;
     return SSM_OK;
 }
 
 }  // namespace la
 }  // namespace
 
-bool ssm_detail::launch_linattn_grad_pass(const LinattnPasses& p, int count, bool f32, LinattnMode mode, hipStream_t s) {
-    return mode == kLinDots ? la::launch_pass<kLinDots>(p, count, f32, s) : la::launch_pass<kLinCross>(p, count, f32, s);
+bool ssm_detail::launch_linattn_exact(const LinattnPasses& p, int count, bool f32, hipStream_t s) {
+    return f32 ? launch_linattn_pass(p, count, true, kLinFull, s) : la::launch_pass<kLinExact>(p, count, false, s);
 }
 
 extern "C" {
@@ -321,11 +369,9 @@ int ssm_linattn_bwd(const void* q, const void* k, const void* v, const float* g,
     float* rev = take(pl.carry);
     float* totf = take(pl.tot);
     float* totr = take(pl.tot);
-    float* x = take(pl.x);
+    float* x = take(pl.tot);
     float* part = take(pl.tot);
-    float* da = take(pl.dots);
-    float* db = take(pl.dots);
-    float* de = take(pl.dots);
+    float* f = take(pl.f);
     float* wq = take(pl.wide);
     float* wkk = take(pl.wide);
 
@@ -339,7 +385,7 @@ int ssm_linattn_bwd(const void* q, const void* k, const void* v, const float* g,
     base.piece = pl.piece; base.npieces = static_cast<int32_t>(pl.npieces); base.pieced = pl.pieced;
     base.H = static_cast<int32_t>(d.nheads);
     base.nseq = static_cast<int32_t>(d.nseq); base.nslots = base.nseq;
-    base.r1 = base.r2 = base.r3 = base.r4 = 1;
+    base.r1 = base.r2 = base.r3 = 1;
     base.wscale = base.oscale = 1.0f;
     base.exact = gr.dg || gr.ds0;
     base.wide = wide_rows(q, z.q, d.dk, z.e) && wide_rows(k, z.k, d.dk, z.e) && wide_rows(v, z.v, d.dv, z.e) &&
@@ -354,18 +400,18 @@ int ssm_linattn_bwd(const void* q, const void* k, const void* v, const float* g,
     sr.x2 = q; sr.s2 = z.q; sr.x3 = dout; sr.s3 = z.o; sr.s_in = ds_last; sr.carry = rev; sr.tot = totr;
     sr.reverse = 1; sr.wscale = d.scale;
 
+    // per head in float32 where dg is formed from them or heads share a row, else at once
+    const bool apart = shared || gr.dg;
     LinattnPass pq = base;   // dq = (do, v, k) from S
-    pq.x1 = dout; pq.s1 = z.o; pq.x2 = v; pq.s2 = z.v; pq.x3 = k; pq.s3 = z.k; pq.r3 = rep; pq.x4 = q; pq.s4 = z.q; pq.r4 = rep;
+    pq.x1 = dout; pq.s1 = z.o; pq.x2 = v; pq.s2 = z.v; pq.x3 = k; pq.s3 = z.k; pq.r3 = rep;
     pq.kd = static_cast<int32_t>(d.dv); pq.vd = static_cast<int32_t>(d.dk); pq.nslices = static_cast<int32_t>(pl.slices_q);
-    pq.s_in = s0; pq.st_t = 1; pq.carry = fwd; pq.oscale = d.scale;
-    pq.out = shared ? static_cast<void*>(wq) : gr.dq; pq.out_f32 = shared; pq.so = d.nheads * d.dk;
-    pq.dots = da; pq.cross = de; pq.pairs = pair_rows(gr.dq, pq.so, d.dk);
-    pq.exact = 0;
+    pq.s_in = s0; pq.st_t = 1; pq.carry = fwd; pq.oscale = d.scale; pq.exact = 0;
+    pq.out = apart ? static_cast<void*>(wq) : gr.dq; pq.out_f32 = apart; pq.so = d.nheads * d.dk;
+    pq.pairs = pair_rows(gr.dq, pq.so, d.dk);
     LinattnPass pk = pq;     // dk = (v, do, q) from dS
-    pk.x1 = v; pk.s1 = z.v; pk.x2 = dout; pk.s2 = z.o; pk.x3 = q; pk.s3 = z.q; pk.x4 = k; pk.s4 = z.k;
+    pk.x1 = v; pk.s1 = z.v; pk.x2 = dout; pk.s2 = z.o; pk.x3 = q; pk.s3 = z.q;
     pk.s_in = ds_last; pk.carry = rev; pk.oscale = 1.0f; pk.wscale = d.scale; pk.reverse = 1;
-    pk.out = shared ? static_cast<void*>(wkk) : gr.dk; pk.dots = db; pk.cross = nullptr;
-    pk.pairs = pair_rows(gr.dk, pk.so, d.dk);
+    pk.out = apart ? static_cast<void*>(wkk) : gr.dk; pk.pairs = pair_rows(gr.dk, pk.so, d.dk);
     LinattnPass pv = sr;     // dv = (k, q, do) from dS
     pv.x1 = k; pv.s1 = z.k; pv.r1 = rep; pv.out = gr.dv; pv.so = wv; pv.s_out = gr.ds0; pv.exact = gr.ds0 != nullptr; pv.pairs = pair_rows(gr.dv, wv, d.dv);
 
@@ -374,29 +420,27 @@ int ssm_linattn_bwd(const void* q, const void* k, const void* v, const float* g,
         launch_linattn_pass({{sf, sr}}, 2, f32, kLinStates, s);
         launch_linattn_carry({{sf, sr}}, 2, s);
     }
-    if (gr.dg) {
-        launch_linattn_grad_pass({{pq, pq}}, 1, f32, kLinCross, s);
-        launch_linattn_grad_pass({{pk, pk}}, 1, f32, kLinDots, s);
-    } else {
+    if (gr.dg)
+        launch_linattn_exact({{pq, pk}}, 2, f32, s);
+    else
         launch_linattn_pass({{pq, pk}}, 2, f32, kLinFull, s);
-    }
     launch_linattn_pass({{pv, pv}}, 1, f32, kLinFull, s);
-    if (shared) {
-        GroupArgs ga = {{wq, wkk}, {gr.dq, gr.dk}, rep, static_cast<int32_t>(d.dk), static_cast<int32_t>(d.kheads)};
-        const dim3 grid(static_cast<uint32_t>(d.tokens < 65536 ? d.tokens : 65536), 2), block(kThreads);
+    if (apart) {
+        const GroupArgs ga = {wq, wkk, q, k, gr.dq, gr.dk, gr.dg ? f : nullptr, z.q, z.k, rep, static_cast<int32_t>(d.dk),
+                              static_cast<int32_t>(d.kheads)};
         const bool v4 = d.dk % 4 == 0 && !misaligned(gr.dq, 4 * z.e) && !misaligned(gr.dk, 4 * z.e);
         if (f32) {
-            if (v4) launch_kernel(linattn_group_kernel<float, 4>, grid, block, 0, s, base, ga);
-            else launch_kernel(linattn_group_kernel<float, 1>, grid, block, 0, s, base, ga);
+            if (v4) run_group<float, 4>(base, ga, s);
+            else run_group<float, 1>(base, ga, s);
         } else {
-            if (v4) launch_kernel(linattn_group_kernel<uint16_t, 4>, grid, block, 0, s, base, ga);
-            else launch_kernel(linattn_group_kernel<uint16_t, 1>, grid, block, 0, s, base, ga);
+            if (v4) run_group<uint16_t, 4>(base, ga, s);
+            else run_group<uint16_t, 1>(base, ga, s);
         }
     }
     if (gr.dg) {
         GradTail t = {};
-        t.p = sf; t.fwd = fwd; t.rev = rev; t.s0 = s0; t.ds0 = gr.ds0; t.a = da; t.b = db; t.e = de; t.x = x;
-        t.part = part; t.dg = gr.dg; t.slices = static_cast<int32_t>(pl.slices_q); t.head_decay = d.head_decay; t.open_end = ds_last != nullptr;
+        t.p = sf; t.fwd = fwd; t.rev = rev; t.s0 = s0; t.ds0 = gr.ds0; t.f = f; t.x = x;
+        t.part = part; t.dg = gr.dg; t.head_decay = d.head_decay; t.open_end = ds_last != nullptr;
         const uint32_t np = static_cast<uint32_t>(pl.npieces), hh = static_cast<uint32_t>(d.nheads);
         launch_kernel(linattn_cross_kernel, dim3(np, hh), dim3(kThreads), 0, s, t);
         launch_kernel(linattn_dg_kernel, dim3(np, (hh + 15) / 16), dim3(kDgThreads), 0, s, t);
@@ -404,7 +448,7 @@ int ssm_linattn_bwd(const void* q, const void* k, const void* v, const float* g,
     }
     if (cu_seqlens)
         launch_kernel(linattn_zero_kernel, dim3(256), dim3(kThreads), 0, s, base,
-                      shared ? nullptr : static_cast<char*>(gr.dq), wk * z.e, shared ? nullptr : static_cast<char*>(gr.dk),
+                      apart ? nullptr : static_cast<char*>(gr.dq), wk * z.e, apart ? nullptr : static_cast<char*>(gr.dk),
                       wk * z.e, static_cast<char*>(gr.dv), wv * z.e,
                       gr.dg && !d.head_decay ? reinterpret_cast<char*>(gr.dg) : nullptr, d.nheads * 4);
     return launch_error == hipSuccess ? SSM_OK : SSM_ERR_HIP;

@@ -250,7 +250,7 @@ int ssm_linattn_fwd(const void* q, const void* k, const void* v, const float* g,
     p.T = d.tokens; p.L = cu_seqlens ? 0 : d.tokens / d.nseq;
     p.piece = pl.piece;
     p.r1 = p.r2 = static_cast<int32_t>(d.nheads / d.kheads);
-    p.r3 = p.r4 = 1;
+    p.r3 = 1;
     p.H = static_cast<int32_t>(d.nheads); p.kd = static_cast<int32_t>(d.dk); p.vd = static_cast<int32_t>(d.dv);
     p.nslices = static_cast<int32_t>(cdiv(d.dv, ssm_detail::linattn_slice(d.dv)));
     p.nseq = static_cast<int32_t>(d.nseq); p.nslots = static_cast<int32_t>(states ? d.nslots : d.nseq);
