@@ -334,14 +334,22 @@ template <int PARTS, int C, int W, int T, int HW = W> struct Tile {   // T threa
             u32x4 x[Q];
 #pragma unroll
             for (int h = 0; h < Q; ++h) x[h] = u32x4{0, 0, 0, 0};
-            if (rr < rows) {
+            // values past the row's end are read from its last column and dropped, so that the
+            // eight loads go out together
+            const int left = rr < rows ? w - col % HW : 0;
+            if (left > 0) {
+                uint32_t y[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    if (col % HW + e >= w) continue;
-                    if constexpr (PARTS == 1)
-                        x[0][e / 2] |= uint32_t(reinterpret_cast<const uint16_t*>(q)[e]) << (16 * (e & 1));
-                    else
-                        x[e / 4][e % 4] = reinterpret_cast<const uint32_t*>(q)[e];
+                    const int c = e < left ? e : left - 1;
+                    if constexpr (PARTS == 1) y[e] = reinterpret_cast<const uint16_t*>(q)[c];
+                    else y[e] = reinterpret_cast<const uint32_t*>(q)[c];
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t z = e < left ? y[e] : 0u;
+                    if constexpr (PARTS == 1) x[0][e / 2] |= z << (16 * (e & 1));
+                    else x[e / 4][e % 4] = z;
                 }
             }
             put(tile, idx, x);
@@ -440,8 +448,12 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
     // bf16 rows come straight into LDS, each tile as soon as the last chunk's readers are
     // done with it: x2 (read to the end) and without a read-out x3 have a second tile, where
     // that still leaves room for two workgroups on a CU.  The exact output's third part of P
-    // takes that room: there the state goes on first, and then all three tiles are free.
-    constexpr bool DMA = PARTS == 1, TWO2 = DMA && !EXACT && !(FULL && KD == 128 && NH == 2), TWO3 = DMA && !FULL;
+    // takes that room: there the state goes on first (EARLY), and then all three tiles are
+    // free.  Two heads' P takes it too: x2 is asked for behind everything else (203 us for
+    // 2 x 8192 tokens of 64 heads of 64 with 128 states, 239 us with the state first).
+    // float32 rows are held in registers from one chunk to the next.
+    constexpr bool DMA = PARTS == 1, EARLY = EXACT, TWO2 = DMA && !EXACT && !(FULL && KD == 128 && NH == 2),
+                   TWO3 = DMA && !FULL;
     __shared__ __align__(16) uint16_t X2a[PARTS * C * KD], X2b[TWO2 ? C * KD : 8];
     __shared__ __align__(16) uint16_t X3a[PARTS * C * BV], X3b[TWO3 ? C * BV : 8];
     __shared__ __align__(16) uint16_t X1[FULL ? PARTS * C * KD : 8];
@@ -537,12 +549,12 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
         t3.load(to, wave, b3 + c0 * pitch3, pitch3, hi - c0);
     };
     const bool ahead = DMA && p.wide;          // tiles are loaded ahead of their chunk
-    if (ahead && nch > 0) {
+    if (p.wide && nch > 0) {
         load2(0, X2a);
         load3(0, X3a);
         if constexpr (FULL) load1(0);
     }
-    wait_memory<0>();
+    if constexpr (DMA) wait_memory<0>();
 
     // one chunk; ODD picks the tiles of odd chunks where there are two
     auto chunk = [&](const int64_t n, auto odd_c) {
@@ -559,7 +571,7 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
         const int tid = 64 * wave + lane, g4 = lane >> 4, l16 = lane & 15;
         if (ahead) {
             // this chunk's rows; what was stored since they were asked for may still be under way
-            if constexpr (!FULL)
+            if constexpr (!FULL || (!EARLY && !TWO2))
                 wait_memory<0>();
             else if (p.pairs)
                 wait_memory<2 * IT * NT>();
@@ -569,13 +581,15 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
         } else {
             lds_barrier();                      // the last chunk's readers are done
             const int64_t rows = hi - c0;
-            if (p.wide) {
-                load2(n, X2);
-                if constexpr (FULL) load1(n);
-                load3(n, X3);
+            if (!DMA && p.wide) {
                 t2.store(X2, tid);
                 if constexpr (FULL) t1.store(X1, tid);
                 t3.store(X3, tid);
+                if (n + 1 < nch) {
+                    load2(n + 1, X2);
+                    load3(n + 1, X3);
+                    if constexpr (FULL) load1(n + 1);
+                }
             } else {
                 t2.copy_any(X2, tid, b2 + c0 * pitch2, pitch2, rows, rev, p.kd);
                 if constexpr (FULL) t1.copy_any(X1, tid, b1 + c0 * pitch1, pitch1, rows, rev, p.kd);
@@ -714,7 +728,7 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
 #pragma unroll
                     for (int k = 0; k < VP; ++k) vp[nt][k][e] = w[k];
                 }
-                constexpr int AHEAD = PARTS == 1 ? (TWO2 ? 4 : 2) : 1;   // operands in flight
+                constexpr int AHEAD = PARTS == 1 ? (EARLY ? 2 : 4) : 1;   // operands in flight
 #pragma unroll
                 for (int m0 = 0; m0 < 2 * KB; m0 += AHEAD) {
                     u32x4 k[AHEAD][PARTS];
@@ -731,10 +745,10 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
             }
         };
         if constexpr (FULL) {
-            if constexpr (!TWO2) onward();
+            if constexpr (EARLY) onward();
             lds_barrier();                      // P is there; x1 and x3 have been read (and x2, if the state is on)
             if (ahead && n + 1 < nch) {
-                if constexpr (!TWO2) load2(n + 1, X2);
+                if constexpr (EARLY) load2(n + 1, X2);
                 load3(n + 1, X3);
                 load1(n + 1);
             }
@@ -749,7 +763,7 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) acc[it][nt] = mma_parts<PP, PARTS>(q, v[jb][nt], acc[it][nt]);
                 }
-            if constexpr (TWO2) onward();
+            if constexpr (!EARLY) onward();
         } else {
             onward();
         }
@@ -798,6 +812,12 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
                         __builtin_amdgcn_raw_buffer_store_b16(IOT<uint16_t>::from_f32(acc[x >> 2][nt][x & 3]), ro,
                                                               o0 + uint32_t((16 * (x >> 2) + (x & 3)) * pitch), 0, 0);
                 }
+            }
+        }
+        if constexpr (DMA && FULL && !EARLY && !TWO2) {
+            if (ahead && n + 1 < nch) {
+                lds_barrier();                  // x2 has been read
+                load2(n + 1, X2);
             }
         }
     };

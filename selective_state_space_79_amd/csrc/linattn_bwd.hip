@@ -32,10 +32,34 @@ struct GradTail {
     int32_t open_end;       // a gradient arrives at the final states
 };
 
-// <S, dS> at the start of each piece, one workgroup per piece and head.
-__global__ void __launch_bounds__(kThreads) linattn_cross_kernel(GradTail t) {
+// Rows of no sequence (before the first and behind the last): zero gradients.  Workgroup
+// `first` of `count`; the widths are in bytes, multiples of 2.
+struct ZeroRows {
+    char* rows[4];
+    int64_t width[4];
+};
+__device__ inline void zero_rows(const LinattnPass& p, const ZeroRows& z, int64_t first, int64_t count) {
+    if (!p.cu) return;
+    const int64_t lo = seq_range(p, 0).start, hi = seq_range(p, p.nseq - 1).end;
+    const int64_t free = p.T - (hi > lo ? hi - lo : 0);
+    for (int64_t i = first; i < free; i += count) {
+        const int64_t t = i < lo ? i : p.T - free + i;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            for (int64_t e = threadIdx.x; z.rows[k] && e < z.width[k] / 2; e += kThreads)
+                reinterpret_cast<uint16_t*>(z.rows[k] + t * z.width[k])[e] = 0;
+    }
+}
+__global__ void __launch_bounds__(kThreads) linattn_zero_kernel(LinattnPass p, ZeroRows z) {
+    zero_rows(p, z, blockIdx.x, gridDim.x);
+}
+
+// <S, dS> at the start of each piece, one workgroup per piece and head; and the rows of no
+// sequence.
+__global__ void __launch_bounds__(kThreads) linattn_cross_kernel(GradTail t, ZeroRows z) {
     __shared__ float red[kWaves];
     const LinattnPass& p = t.p;
+    if (blockIdx.y == 0) zero_rows(p, z, blockIdx.x, gridDim.x);
     const int64_t pi = blockIdx.x;
     const int h = blockIdx.y;
     const int seq = find_seq(p, pi);
@@ -255,21 +279,6 @@ template <typename IO, int VW> void run_group(const LinattnPass& p, const GroupA
     else launch_kernel(linattn_group_kernel<IO, VW, 64>, grid, block, 0, s, p, a);
 }
 
-// Rows of no sequence (before the first and behind the last): zero gradients.
-__global__ void __launch_bounds__(kThreads) linattn_zero_kernel(LinattnPass p, char* a, int64_t na, char* b, int64_t nb,
-                                                                char* c, int64_t nc, char* d, int64_t nd) {
-    const int64_t lo = seq_range(p, 0).start, hi = seq_range(p, p.nseq - 1).end;
-    const int64_t free = p.T - (hi > lo ? hi - lo : 0);
-    for (int64_t i = blockIdx.x; i < free; i += gridDim.x) {
-        const int64_t t = i < lo ? i : p.T - free + i;
-        char* rows[4] = {a, b, c, d};
-        const int64_t n[4] = {na, nb, nc, nd};
-        for (int k = 0; k < 4; ++k)   // bytes of a row: a multiple of 2
-            for (int64_t e = threadIdx.x; rows[k] && e < n[k] / 2; e += kThreads)
-                reinterpret_cast<uint16_t*>(rows[k] + t * n[k])[e] = 0;
-    }
-}
-
 // ---------------------------------------------------------------- host
 struct GradPlan {
     int64_t piece, npieces;
@@ -437,20 +446,20 @@ int ssm_linattn_bwd(const void* q, const void* k, const void* v, const float* g,
             else run_group<uint16_t, 1>(base, ga, s);
         }
     }
+    const ZeroRows zero = {{apart ? nullptr : static_cast<char*>(gr.dq), apart ? nullptr : static_cast<char*>(gr.dk),
+                            static_cast<char*>(gr.dv),
+                            gr.dg && !d.head_decay ? reinterpret_cast<char*>(gr.dg) : nullptr},
+                           {wk * z.e, wk * z.e, wv * z.e, d.nheads * 4}};
     if (gr.dg) {
         GradTail t = {};
         t.p = sf; t.fwd = fwd; t.rev = rev; t.s0 = s0; t.ds0 = gr.ds0; t.f = f; t.x = x;
         t.part = part; t.dg = gr.dg; t.head_decay = d.head_decay; t.open_end = ds_last != nullptr;
         const uint32_t np = static_cast<uint32_t>(pl.npieces), hh = static_cast<uint32_t>(d.nheads);
-        launch_kernel(linattn_cross_kernel, dim3(np, hh), dim3(kThreads), 0, s, t);
+        launch_kernel(linattn_cross_kernel, dim3(np, hh), dim3(kThreads), 0, s, t, zero);
         launch_kernel(linattn_dg_kernel, dim3(np, (hh + 15) / 16), dim3(kDgThreads), 0, s, t);
         if (d.head_decay) launch_kernel(linattn_dg_sum_kernel, dim3(hh), dim3(kThreads), 0, s, t);
     }
-    if (cu_seqlens)
-        launch_kernel(linattn_zero_kernel, dim3(256), dim3(kThreads), 0, s, base,
-                      apart ? nullptr : static_cast<char*>(gr.dq), wk * z.e, apart ? nullptr : static_cast<char*>(gr.dk),
-                      wk * z.e, static_cast<char*>(gr.dv), wv * z.e,
-                      gr.dg && !d.head_decay ? reinterpret_cast<char*>(gr.dg) : nullptr, d.nheads * 4);
+    if (!gr.dg && cu_seqlens) launch_kernel(linattn_zero_kernel, dim3(256), dim3(kThreads), 0, s, base, zero);
     return launch_error == hipSuccess ? SSM_OK : SSM_ERR_HIP;
 }
 
