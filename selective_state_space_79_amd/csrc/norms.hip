@@ -17,28 +17,37 @@ struct V8 {
     float e[8];
 };
 
-// 8 values at column col of a row with w columns; out of range reads as 0.
-template <typename IO> __device__ inline V8 load8(const IO* row, int col, int w, bool on, bool vec) {
-    V8 v;
-    if (!on || col >= w) {
+// 8 values at column col of a row with w columns, as they lie in memory (so that a row can be
+// asked for while another is worked on); out of range reads as 0.
+template <typename IO> struct Raw8 {
+    uint4 u[sizeof(IO) / 2];
+    __device__ inline void load(const IO* row, int col, int w, bool on, bool vec) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v.e[i] = 0.0f;
-        return v;
-    }
-    if (vec) {
-        IO raw[8];
+        for (int k = 0; k < int(sizeof(IO) / 2); ++k) u[k] = make_uint4(0, 0, 0, 0);
+        if (!on || col >= w) return;
+        if (vec) {
 #pragma unroll
-        for (int k = 0; k < int(sizeof(raw) / 16); ++k) {
-            const uint4 u = reinterpret_cast<const uint4*>(row + col)[k];
-            __builtin_memcpy(reinterpret_cast<char*>(raw) + 16 * k, &u, 16);
+            for (int k = 0; k < int(sizeof(IO) / 2); ++k) u[k] = reinterpret_cast<const uint4*>(row + col)[k];
+        } else {
+            IO raw[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) raw[i] = col + i < w ? row[col + i] : IO(0);
+            __builtin_memcpy(u, raw, sizeof(raw));
         }
+    }
+    __device__ inline V8 values() const {
+        IO raw[8];
+        __builtin_memcpy(raw, u, sizeof(raw));
+        V8 v;
 #pragma unroll
         for (int i = 0; i < 8; ++i) v.e[i] = IOT<IO>::to_f32(raw[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v.e[i] = col + i < w ? IOT<IO>::to_f32(row[col + i]) : 0.0f;
+        return v;
     }
-    return v;
+};
+template <typename IO> __device__ inline V8 load8(const IO* row, int col, int w, bool on, bool vec) {
+    Raw8<IO> r;
+    r.load(row, col, w, on, vec);
+    return r.values();
 }
 
 template <typename IO> __device__ inline void store8(IO* row, int col, int w, bool on, bool vec, const V8& v) {
@@ -60,32 +69,69 @@ template <typename IO> __device__ inline void store8(IO* row, int col, int w, bo
     }
 }
 
+// A row of float32 weights in LDS, each thread's 8 values in two planes of 4, so that a
+// wave's 16-byte reads lie side by side.  In the backward kernels the weights would take as
+// many registers as a row.
+template <int T> struct LdsWeights {
+    float* at;   // [2][T][4]
+    __device__ inline void put(const V8& v, int t) const {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) at[(e >> 2) * 4 * T + 4 * t + (e & 3)] = v.e[e];
+    }
+    __device__ inline V8 get(int t) const {
+        V8 v;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float4 u = *reinterpret_cast<const float4*>(at + h * 4 * T + 4 * t);
+            v.e[4 * h] = u.x;
+            v.e[4 * h + 1] = u.y;
+            v.e[4 * h + 2] = u.z;
+            v.e[4 * h + 3] = u.w;
+        }
+        return v;
+    }
+};
+
 __device__ inline V8 loadw(const float* w, int col, int n) { return load8<float>(w, col, n, w != nullptr, false); }
 
 template <int TPG> constexpr int block_threads() { return TPG < 256 ? 256 : TPG; }
 
-// Sums over the TPG threads of a group.  With more than one wave, a slot of LDS per wave;
-// two sets are used in turn, so one barrier per sum is enough.
+// Sums over the TPG threads of a group, one or several at once.  With more than one wave, a
+// slot of LDS per wave; two sets are used in turn, so one barrier is enough.  The barrier
+// waits for LDS only: rows asked for ahead stay under way.
 template <int TPG> struct Summer {
-    static constexpr int kWaves = block_threads<TPG>() / 64;
-    float* red;   // [2][kWaves]
+    static constexpr int kWaves = block_threads<TPG>() / 64, kMost = 3;
+    static constexpr int kFloats = 2 * kWaves * kMost;
+    float* red;   // [2][kWaves][kMost]
     int turn = 0;
-    __device__ inline float operator()(float v) {
+    template <int N> __device__ inline void all(float (&v)[N]) {
 #pragma unroll
-        for (int d = 1; d < (TPG < 64 ? TPG : 64); d <<= 1) v += __shfl_xor(v, d);
+        for (int d = 1; d < (TPG < 64 ? TPG : 64); d <<= 1)
+#pragma unroll
+            for (int n = 0; n < N; ++n) v[n] += __shfl_xor(v[n], d);
         if constexpr (TPG > 64) {
             constexpr int per = TPG / 64;
             const int wave = threadIdx.x >> 6;
-            float* r = red + turn * kWaves;
+            float* r = red + turn * kWaves * kMost;
             turn ^= 1;
-            if ((threadIdx.x & 63) == 0) r[wave] = v;
-            __syncthreads();
-            v = 0.0f;
+            if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+                for (int n = 0; n < N; ++n) r[wave * kMost + n] = v[n];
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
             const int w0 = wave / per * per;
 #pragma unroll
-            for (int i = 0; i < per; ++i) v += r[w0 + i];
+            for (int n = 0; n < N; ++n) {
+                v[n] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < per; ++i) v[n] += r[(w0 + i) * kMost + n];
+            }
         }
-        return v;
+    }
+    __device__ inline float operator()(float v) {
+        float x[1] = {v};
+        all(x);
+        return x[0];
     }
 };
 
@@ -124,7 +170,7 @@ struct GatedArgs {
 
 template <typename IO, int TPG, int V, bool FIRST>
 __global__ void __launch_bounds__(block_threads<TPG>()) gated_norm_fwd_kernel(GatedArgs p) {
-    __shared__ float red[2 * Summer<TPG>::kWaves];
+    __shared__ float red[Summer<TPG>::kFloats];
     Summer<TPG> sum{red};
     const int lane = threadIdx.x % TPG;
     const Place at = place<TPG>(p.rows, p.ngroups);
@@ -200,74 +246,87 @@ __device__ inline void store_part(float* part, const V8 (&s)[V], const Place& at
 }
 
 template <typename IO, int TPG, int V, bool FIRST>
-__global__ void __launch_bounds__(block_threads<TPG>()) gated_norm_bwd_kernel(GatedArgs p) {
-    __shared__ float red[2 * Summer<TPG>::kWaves];
-    __shared__ float lds[TPG < 256 ? 2048 : 1];
+__global__ void __launch_bounds__(block_threads<TPG>(), 4) gated_norm_bwd_kernel(GatedArgs p) {
+    constexpr int T = block_threads<TPG>();
+    __shared__ float red[Summer<TPG>::kFloats];
+    __shared__ __align__(16) float wl[V * 8 * T];   // weights; at the end the slots' sums
     Summer<TPG> sum{red};
-    const int lane = threadIdx.x % TPG;
+    const int tid = threadIdx.x, lane = tid % TPG;
     const Place at = place<TPG>(p.rows, p.ngroups);
     const int64_t off = int64_t(at.group) * p.n, dim = int64_t(p.ngroups) * p.n;
-    V8 w[V], dw[V];
+    V8 dw[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        w[i] = loadw(p.w + (p.shared ? 0 : off), 8 * (lane + TPG * i), p.n);
+        LdsWeights<T>{wl + i * 8 * T}.put(loadw(p.w + (p.shared ? 0 : off), 8 * (lane + TPG * i), p.n), tid);
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[i].e[e] = 0.0f;
     }
     const int64_t loops = (p.rows + at.step - 1) / at.step;
-    for (int64_t l = 0; l < loops; ++l) {
-        const int64_t row = at.row + l * at.step;
+    Raw8<IO> nx[V], nz[V], ng[V];   // the next row's
+    auto fetch = [&](int64_t row) {
         const bool on = at.on && row < p.rows;
-        const IO* xr = static_cast<const IO*>(p.x) + row * p.sx + off;
-        const IO* zr = static_cast<const IO*>(p.z) + row * p.sz + off;
-        const IO* dr = static_cast<const IO*>(p.dy) + row * dim + off;
-        V8 x[V], z[V], g[V];
-        float q = 0.0f, t = 0.0f;
-        // p = x SiLU(z) or x; g = the gradient at the normalised values: dy w, with the gate
-        // behind the norm dy w SiLU(z)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int col = 8 * (lane + TPG * i);
-            x[i] = load8<IO>(xr, col, p.n, on, p.vec);
-            g[i] = load8<IO>(dr, col, p.n, on, p.vec);
-            if (p.z) z[i] = load8<IO>(zr, col, p.n, on, p.vec);
+            nx[i].load(static_cast<const IO*>(p.x) + row * p.sx + off, col, p.n, on, p.vec);
+            ng[i].load(static_cast<const IO*>(p.dy) + row * dim + off, col, p.n, on, p.vec);
+            nz[i].load(static_cast<const IO*>(p.z) + row * p.sz + off, col, p.n, on && p.z, p.vec);
+        }
+    };
+    fetch(at.row);
+    for (int64_t l = 0; l < loops; ++l) {
+        const int64_t row = at.row + l * at.step;
+        const bool on = at.on && row < p.rows;
+        Raw8<IO> rx[V], rz[V], rg[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            rx[i] = nx[i];
+            rz[i] = nz[i];
+            rg[i] = ng[i];
+        }
+        if (l + 1 < loops) fetch(row + at.step);
+        // p = x SiLU(z) or x; g = the gradient at the normalised values: dy w, with the gate
+        // behind the norm dy w SiLU(z)
+        float qt[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const V8 x = rx[i].values(), z = rz[i].values(), g = rg[i].values(), w = LdsWeights<T>{wl + i * 8 * T}.get(tid);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float a = p.z ? silu_f32(z[i].e[e]) : 1.0f;
-                const float v = FIRST ? x[i].e[e] * a : x[i].e[e];
-                const float u = (FIRST ? g[i].e[e] : g[i].e[e] * a) * w[i].e[e];
-                q = fmaf(v, v, q);
-                t = fmaf(u, v, t);
+                const float a = p.z ? silu_f32(z.e[e]) : 1.0f;
+                const float v = FIRST ? x.e[e] * a : x.e[e];
+                const float u = (FIRST ? g.e[e] : g.e[e] * a) * w.e[e];
+                qt[0] = fmaf(v, v, qt[0]);
+                qt[1] = fmaf(u, v, qt[1]);
             }
         }
-        q = sum(q);
-        t = sum(t);
-        const float rs = __builtin_amdgcn_rsqf(fmaf(q, p.inv_n, p.eps));
-        const float k = t * p.inv_n * rs * rs * rs;   // mean(g n) of n = p rs, times rs^2
+        sum.all(qt);
+        const float rs = __builtin_amdgcn_rsqf(fmaf(qt[0], p.inv_n, p.eps));
+        const float k = qt[1] * p.inv_n * rs * rs * rs;   // mean(g n) of n = p rs, times rs^2
         IO* dxr = static_cast<IO*>(p.y) + row * dim + off;
         IO* dzr = static_cast<IO*>(p.dz) + row * dim + off;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
+            const V8 x = rx[i].values(), z = rz[i].values(), g = rg[i].values(), w = LdsWeights<T>{wl + i * 8 * T}.get(tid);
             V8 dx, dz;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float zz = p.z ? z[i].e[e] : 0.0f;
-                const float sg = p.z ? sigmoid_f32(zz) : 1.0f;
+                const float zz = z.e[e], sg = p.z ? sigmoid_f32(zz) : 1.0f;
                 const float a = p.z ? zz * sg : 1.0f, slope = sg * fmaf(zz, 1.0f - sg, 1.0f);
-                const float xx = x[i].e[e], dy = g[i].e[e];
+                const float xx = x.e[e], dy = g.e[e];
                 const float v = FIRST ? xx * a : xx;
                 const float up = FIRST ? dy : dy * a;
                 dw[i].e[e] = fmaf(up, v * rs, dw[i].e[e]);
-                const float dp = fmaf(up * w[i].e[e], rs, -v * k);
+                const float dp = fmaf(up * w.e[e], rs, -v * k);
                 dx.e[e] = FIRST ? dp * a : dp;
-                dz.e[e] = (FIRST ? dp * xx : dy * xx * rs * w[i].e[e]) * slope;
+                dz.e[e] = (FIRST ? dp * xx : dy * xx * rs * w.e[e]) * slope;
             }
             const int col = 8 * (lane + TPG * i);
             store8<IO>(dxr, col, p.n, on, p.vec, dx);
             if (p.z) store8<IO>(dzr, col, p.n, on, p.vec, dz);
         }
     }
-    store_part<TPG, V>(p.part, dw, at, p.ngroups, p.n, p.shared, lds);
+    store_part<TPG, V>(p.part, dw, at, p.ngroups, p.n, p.shared, wl);
 }
 
 struct AddArgs {
@@ -288,7 +347,7 @@ struct AddArgs {
 
 template <typename IO, typename RT, int TPG, int V>
 __global__ void __launch_bounds__(block_threads<TPG>()) add_norm_fwd_kernel(AddArgs p) {
-    __shared__ float red[2 * Summer<TPG>::kWaves];
+    __shared__ float red[Summer<TPG>::kFloats];
     Summer<TPG> sum{red};
     const int lane = threadIdx.x % TPG;
     const Place at = place<TPG>(p.rows, 1);
@@ -343,67 +402,109 @@ __global__ void __launch_bounds__(block_threads<TPG>()) add_norm_fwd_kernel(AddA
 }
 
 template <typename IO, typename RT, int TPG, int V>
-__global__ void __launch_bounds__(block_threads<TPG>()) add_norm_bwd_kernel(AddArgs p) {
-    __shared__ float red[2 * Summer<TPG>::kWaves];
-    __shared__ float lds[TPG < 256 ? 2048 : 1];
+__global__ void __launch_bounds__(block_threads<TPG>(), 4) add_norm_bwd_kernel(AddArgs p) {
+    constexpr int T = block_threads<TPG>(), PL = V * 8 * T;
+    constexpr bool HELD = V == 1;   // weights in LDS (past 8192 columns they are read again)
+    __shared__ float red[Summer<TPG>::kFloats];
+    __shared__ __align__(16) float wl[HELD ? 3 * PL : 4];   // w, scale, post; at the end the slots' sums
     Summer<TPG> sum{red};
-    const int lane = threadIdx.x % TPG;
+    const int tid = threadIdx.x, lane = tid % TPG;
     const Place at = place<TPG>(p.rows, 1);
-    V8 w[V], sc[V], po[V], dw[V], dsc[V], dpo[V];
+    V8 dw[V], dsc[V], dpo[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int col = 8 * (lane + TPG * i);
-        w[i] = loadw(p.w, col, p.n);
-        sc[i] = loadw(p.scale, col, p.n);
-        po[i] = loadw(p.post, col, p.n);
+        if constexpr (HELD) {
+            LdsWeights<T>{wl}.put(loadw(p.w, col, p.n), tid);
+            LdsWeights<T>{wl + PL}.put(loadw(p.scale, col, p.n), tid);
+            LdsWeights<T>{wl + 2 * PL}.put(loadw(p.post, col, p.n), tid);
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[i].e[e] = dsc[i].e[e] = dpo[i].e[e] = 0.0f;
     }
+    auto weight = [&](int which, const float* q, int i) {
+        if constexpr (HELD) return LdsWeights<T>{wl + which * PL}.get(tid);
+        else return loadw(q, 8 * (lane + TPG * i), p.n);
+    };
     const int64_t loops = (p.rows + at.step - 1) / at.step;
-    for (int64_t l = 0; l < loops; ++l) {
-        const int64_t row = at.row + l * at.step;
+    Raw8<IO> nx[V], ny[V];          // the next row's
+    Raw8<RT> nr[V], nd[V];
+    auto fetch = [&](int64_t row) {
         const bool on = at.on && row < p.rows;
-        V8 x[V], r[V], dy[V], d[V];
-        float q = 0.0f, t = 0.0f, qx = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int col = 8 * (lane + TPG * i);
-            r[i] = load8<RT>(static_cast<const RT*>(p.res) + row * p.sr, col, p.n, on, p.vec);
-            dy[i] = load8<IO>(static_cast<const IO*>(p.dy) + row * p.n, col, p.n, on, p.vec);
-            d[i] = load8<RT>(static_cast<const RT*>(p.dr) + row * p.n, col, p.n, on && p.dr, p.vec);
-            x[i] = load8<IO>(static_cast<const IO*>(p.x) + row * p.sx, col, p.n, on && (p.scale || p.post), p.vec);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                q = fmaf(r[i].e[e], r[i].e[e], q);
-                t = fmaf(dy[i].e[e] * w[i].e[e], r[i].e[e], t);
-                qx = fmaf(x[i].e[e], x[i].e[e], qx);
-            }
+            nr[i].load(static_cast<const RT*>(p.res) + row * p.sr, col, p.n, on, p.vec);
+            ny[i].load(static_cast<const IO*>(p.dy) + row * p.n, col, p.n, on, p.vec);
+            nd[i].load(static_cast<const RT*>(p.dr) + row * p.n, col, p.n, on && p.dr, p.vec);
+            nx[i].load(static_cast<const IO*>(p.x) + row * p.sx, col, p.n, on && (p.scale || p.post), p.vec);
         }
-        q = sum(q);
-        t = sum(t);
-        const float rr = __builtin_amdgcn_rsqf(fmaf(q, p.inv_n, p.eps));
-        const float k = t * p.inv_n * rr * rr * rr;
-        float rx = 1.0f, tx = 0.0f;
-        if (p.post) rx = __builtin_amdgcn_rsqf(fmaf(sum(qx), p.inv_n, p.eps));
+    };
+    fetch(at.row);
+    for (int64_t l = 0; l < loops; ++l) {
+        const int64_t row = at.row + l * at.step;
+        const bool on = at.on && row < p.rows;
+        Raw8<IO> rx[V], ry[V];
+        Raw8<RT> rr8[V], rd[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
+            rx[i] = nx[i];
+            ry[i] = ny[i];
+            rr8[i] = nr[i];
+            rd[i] = nd[i];
+        }
+        if (l + 1 < loops) fetch(row + at.step);
+        float sums[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const V8 x = rx[i].values(), y = ry[i].values(), r = rr8[i].values(), w = weight(0, p.w, i);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                dw[i].e[e] = fmaf(dy[i].e[e], r[i].e[e] * rr, dw[i].e[e]);
-                // the gradient at r, then at a, then at the normalised x
-                d[i].e[e] += fmaf(dy[i].e[e] * w[i].e[e], rr, -r[i].e[e] * k);
+                sums[0] = fmaf(r.e[e], r.e[e], sums[0]);
+                sums[1] = fmaf(y.e[e] * w.e[e], r.e[e], sums[1]);
+                sums[2] = fmaf(x.e[e], x.e[e], sums[2]);
+            }
+        }
+        sum.all(sums);
+        const float rr = __builtin_amdgcn_rsqf(fmaf(sums[0], p.inv_n, p.eps));
+        const float k = sums[1] * p.inv_n * rr * rr * rr;
+        const float rx1 = p.post ? __builtin_amdgcn_rsqf(fmaf(sums[2], p.inv_n, p.eps)) : 1.0f;
+        float tx = 0.0f;
+        V8 d[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            {
+                const V8 y = ry[i].values(), r = rr8[i].values(), w = weight(0, p.w, i);
+                d[i] = rd[i].values();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    dw[i].e[e] = fmaf(y.e[e], r.e[e] * rr, dw[i].e[e]);
+                    // the gradient at r, then at a, then at the normalised x
+                    d[i].e[e] += fmaf(y.e[e] * w.e[e], rr, -r.e[e] * k);
+                }
             }
             if (p.r) store8<RT>(static_cast<RT*>(p.r) + row * p.n, 8 * (lane + TPG * i), p.n, on, p.vec, d[i]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float n = x[i].e[e] * rx;
-                if (p.scale) {
-                    dsc[i].e[e] = fmaf(d[i].e[e], p.post ? n * po[i].e[e] : n, dsc[i].e[e]);
-                    d[i].e[e] *= sc[i].e[e];
-                }
+            const V8 x = rx[i].values();
+            if (p.scale) {
+                const V8 sc = weight(1, p.scale, i);
                 if (p.post) {
+                    const V8 po = weight(2, p.post, i);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) dsc[i].e[e] = fmaf(d[i].e[e], x.e[e] * rx1 * po.e[e], dsc[i].e[e]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) dsc[i].e[e] = fmaf(d[i].e[e], x.e[e], dsc[i].e[e]);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) d[i].e[e] *= sc.e[e];
+            }
+            if (p.post) {
+                const V8 po = weight(2, p.post, i);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float n = x.e[e] * rx1;
                     dpo[i].e[e] = fmaf(d[i].e[e], n, dpo[i].e[e]);
-                    d[i].e[e] *= po[i].e[e];
+                    d[i].e[e] *= po.e[e];
                     tx = fmaf(d[i].e[e], n, tx);
                 }
             }
@@ -411,39 +512,52 @@ __global__ void __launch_bounds__(block_threads<TPG>()) add_norm_bwd_kernel(AddA
         if (p.post) {
             const float m = sum(tx) * p.inv_n;
 #pragma unroll
-            for (int i = 0; i < V; ++i)
+            for (int i = 0; i < V; ++i) {
+                const V8 x = rx[i].values();
 #pragma unroll
-                for (int e = 0; e < 8; ++e) d[i].e[e] = rx * fmaf(-m * rx, x[i].e[e], d[i].e[e]);
+                for (int e = 0; e < 8; ++e) d[i].e[e] = rx1 * fmaf(-m * rx1, x.e[e], d[i].e[e]);
+            }
         }
 #pragma unroll
         for (int i = 0; i < V; ++i)
             store8<IO>(static_cast<IO*>(p.y) + row * p.n, 8 * (lane + TPG * i), p.n, on, p.vec, d[i]);
     }
     const int64_t plane = int64_t(gridDim.x) * p.n;
-    store_part<TPG, V>(p.part, dw, at, 1, p.n, true, lds);
-    if (p.scale) store_part<TPG, V>(p.part + plane, dsc, at, 1, p.n, true, lds);
-    if (p.post) store_part<TPG, V>(p.part + 2 * plane, dpo, at, 1, p.n, true, lds);
+    store_part<TPG, V>(p.part, dw, at, 1, p.n, true, wl);
+    if (p.scale) store_part<TPG, V>(p.part + plane, dsc, at, 1, p.n, true, wl);
+    if (p.post) store_part<TPG, V>(p.part + 2 * plane, dpo, at, 1, p.n, true, wl);
 }
 
-// Sums `count` partial rows of n values, in a fixed order: 16 columns x 16 rows a workgroup.
-// Plane b of the grid's y goes to out0, out1, out2.
-__global__ void __launch_bounds__(256) sum_rows_kernel(const float* part, int64_t count, int64_t n, float* out0,
-                                                       float* out1, float* out2) {
-    __shared__ float s[256];
+// Sums `count` partial rows of n values, in a fixed order: 16 columns x 64 rows a workgroup,
+// eight rows of a thread under way at once.  Plane b of the grid's y goes to out0, out1, out2.
+constexpr int kSumLanes = 64;
+__global__ void __launch_bounds__(16 * kSumLanes) sum_rows_kernel(const float* part, int64_t count, int64_t n,
+                                                                  float* out0, float* out1, float* out2) {
+    __shared__ float s[kSumLanes][16];
     float* out = blockIdx.y == 0 ? out0 : blockIdx.y == 1 ? out1 : out2;
     if (!out) return;
     const int c = threadIdx.x & 15, r = threadIdx.x >> 4;
     const int64_t col = int64_t(blockIdx.x) * 16 + c;
     const float* q = part + blockIdx.y * count * n + col;
     float v = 0.0f;
-    if (col < n)
-        for (int64_t i = r; i < count; i += 16) v += q[i * n];
-    s[threadIdx.x] = v;
-    __syncthreads();
-    if (r == 0 && col < n) {
-        for (int i = 1; i < 16; ++i) v += s[16 * i + c];
-        out[col] = v;
+    if (col < n) {
+        int64_t i = r;
+        for (; i + 7 * kSumLanes < count; i += 8 * kSumLanes) {
+            float x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = q[(i + k * kSumLanes) * n];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v += x[k];
+        }
+        for (; i < count; i += kSumLanes) v += q[i * n];
     }
+    s[r][c] = v;
+    __syncthreads();
+    for (int d = kSumLanes / 2; d > 0; d >>= 1) {
+        if (r < d) s[r][c] += s[r + d][c];
+        __syncthreads();
+    }
+    if (r == 0 && col < n) out[col] = s[0][c];
 }
 
 // ---------------------------------------------------------------- host
@@ -632,7 +746,7 @@ int ssm_gated_norm_bwd(const void* x, const void* z, const float* w, const void*
     ssm_detail::launch_error = hipSuccess;
     gated(a, d, tpg, blocks, true, s);
     const int64_t n = d.shared_weight ? d.group : dim;
-    launch_kernel(sum_rows_kernel, dim3(static_cast<uint32_t>(cdiv(n, 16))), dim3(256), 0, s, a.part,
+    launch_kernel(sum_rows_kernel, dim3(static_cast<uint32_t>(cdiv(n, 16))), dim3(16 * kSumLanes), 0, s, a.part,
                   d.shared_weight ? blocks : lanes, n, dw, static_cast<float*>(nullptr), static_cast<float*>(nullptr));
     return ssm_detail::launch_error == hipSuccess ? SSM_OK : SSM_ERR_HIP;
 }
@@ -713,7 +827,7 @@ int ssm_add_norm_bwd(const void* x, const void* r, const float* scale, const flo
     hipStream_t s = static_cast<hipStream_t>(stream);
     ssm_detail::launch_error = hipSuccess;
     add(a, d, tpg, blocks, true, s);
-    launch_kernel(sum_rows_kernel, dim3(static_cast<uint32_t>(cdiv(d.dim, 16)), 3), dim3(256), 0, s, a.part, blocks,
+    launch_kernel(sum_rows_kernel, dim3(static_cast<uint32_t>(cdiv(d.dim, 16)), 3), dim3(16 * kSumLanes), 0, s, a.part, blocks,
                   d.dim, dw, scale ? dscale : nullptr, post ? dpost : nullptr);
     return ssm_detail::launch_error == hipSuccess ? SSM_OK : SSM_ERR_HIP;
 }
