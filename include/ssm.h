@@ -460,10 +460,11 @@ SSM_API int ssm_ssd_fwd(const void* u, const void* delta, const float* A, const 
 typedef struct ssm_linattn_dims {
     int64_t tokens;    /* >= 1: rows of q, k, v, o and g */
     int64_t nseq;      /* 1 .. 65535 sequences (single-token step: equal to tokens) */
-    int64_t nheads;    /* 1 .. 65535: heads of v, o, g and the states */
+    int64_t nheads;    /* 1 .. 32767: heads of v, o, g and the states */
     int64_t kheads;    /* >= 1 heads of q and k; nheads % kheads == 0 */
     int64_t dk, dv;    /* 1 .. SSM_LINATTN_MAX_DIM */
-    int64_t q_stride, k_stride, v_stride, o_stride; /* elements between tokens; 0: packed */
+    int64_t q_stride, k_stride, v_stride, o_stride; /* elements between tokens; 0: packed;
+                          a token of o at most 16 MiB from the next */
     int64_t nslots;    /* states in the arrays of states (ignored without states) */
     int64_t piece_len; /* 0: library choice; else tokens of a piece of a sequence, a
                           multiple of 64 (same result up to rounding) */

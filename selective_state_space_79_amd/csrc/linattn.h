@@ -360,7 +360,7 @@ template <int PARTS, int C, int W, int T, int HW = W> struct Tile {   // T threa
 // Decays of one chunk.  The sums run in float64 and are kept in two floats, so that a
 // difference of two of them is right to float32 of the difference, however far they fell.
 // The state in registers is R / s with a scale s that takes the chunks' decays in its place
-// (no product per value and chunk); it is folded in before it falls below 2^-60.
+// (no product per value and chunk); it is folded in before it leaves 2^-60 .. 2^60.
 template <int C> struct __align__(16) Decays {
     float hi[C], lo[C];   // G in log2 units
     float in[C];          // o s e^{G_i}: the incoming state's share at row i
@@ -397,7 +397,7 @@ template <int C> struct DecayLane {
         g = g < kMinDecay ? kMinDecay : g;
         const double s = scan_f64(lane < C ? double(g) * 1.4426950408889634 : 0.0);
         const double end = lane_f64(s, C - 1);
-        const bool fold = !(scale + end > -60.0);
+        const bool fold = !(fabs(scale + end) < 60.0);
         if (lane < C) {
             const float hi = float(s);
             d.hi[lane] = hi;
@@ -907,7 +907,7 @@ inline int check_dims(const ssm_linattn_dims* d, Sizes* z) {
     if (d->tokens < 1 || d->nseq < 1 || d->nheads < 1 || d->kheads < 1 || d->dk < 1 || d->dv < 1) return SSM_ERR_EMPTY;
     if (d->io_dtype != SSM_F32 && d->io_dtype != SSM_BF16) return SSM_ERR_DTYPE;
     if (d->nheads % d->kheads != 0 || d->dk > SSM_LINATTN_MAX_DIM || d->dv > SSM_LINATTN_MAX_DIM) return SSM_ERR_DIMS;
-    if (d->nseq > 65535 || d->nheads > 65535 || d->tokens > (int64_t(1) << 31) - 1) return SSM_ERR_DIMS;
+    if (d->nseq > 65535 || d->nheads > 32767 || d->tokens > (int64_t(1) << 31) - 1) return SSM_ERR_DIMS;
     if (d->head_decay != 0 && d->head_decay != 1) return SSM_ERR_DIMS;
     if (d->reserved != 0) return SSM_ERR_DIMS;
     if (d->piece_len < 0 || d->piece_len % 64 != 0 || d->piece_len > (int64_t(1) << 31)) return SSM_ERR_DIMS;
@@ -925,6 +925,9 @@ inline int check_dims(const ssm_linattn_dims* d, Sizes* z) {
     z->e = d->io_dtype == SSM_BF16 ? 2 : 4;
     return SSM_OK;
 }
+
+// Workgroups of one launch: a grid has fewer than 2^32 threads.
+constexpr int64_t kMostGroups = int64_t(1) << 22;
 
 inline size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 

@@ -304,8 +304,7 @@ inline int make_grad_plan(const ssm_linattn_dims* d, bool packed, GradPlan* pl) 
     pl->pieced = piece < each;
     pl->piece = pl->pieced ? piece : (int64_t(1) << 31);
     pl->npieces = !pl->pieced ? d->nseq : packed ? d->tokens / piece + d->nseq : d->nseq * cdiv(each, piece);
-    const int64_t most = (int64_t(1) << 31) - 1;
-    if (pl->npieces > most / (d->nheads * (pl->slices_q > pl->slices_s ? pl->slices_q : pl->slices_s)))
+    if (pl->npieces > kMostGroups / (d->nheads * (pl->slices_q > pl->slices_s ? pl->slices_q : pl->slices_s)))
         return SSM_ERR_DIMS;
     pl->carry = pl->pieced ? up256(static_cast<size_t>(pl->npieces * d->nheads * d->dk * d->dv) * 4) : 0;
     pl->tot = up256(static_cast<size_t>(pl->npieces * d->nheads) * 4);
@@ -326,11 +325,11 @@ extern "C" {
 
 size_t ssm_linattn_bwd_workspace_bytes(const ssm_linattn_dims* dims) {
     la::Sizes z;
-    la::GradPlan pl, dense;
-    if (la::check_dims(dims, &z) != SSM_OK || la::make_grad_plan(dims, true, &pl) != SSM_OK) return 0;
-    size_t n = pl.bytes;
-    if (dims->tokens % dims->nseq == 0 && la::make_grad_plan(dims, false, &dense) == SSM_OK && dense.bytes > n)
-        n = dense.bytes;
+    la::GradPlan pl;
+    if (la::check_dims(dims, &z) != SSM_OK) return 0;
+    size_t n = 0;
+    if (la::make_grad_plan(dims, true, &pl) == SSM_OK) n = pl.bytes;
+    if (dims->tokens % dims->nseq == 0 && la::make_grad_plan(dims, false, &pl) == SSM_OK && pl.bytes > n) n = pl.bytes;
     return n;
 }
 

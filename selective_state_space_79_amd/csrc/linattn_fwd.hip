@@ -172,7 +172,7 @@ inline int make_plan(const ssm_linattn_dims* d, bool packed, Plan* pl) {
     pl->pieced = piece > 0 && piece < each;
     pl->piece = pl->pieced ? piece : (int64_t(1) << 31);
     pl->npieces = !pl->pieced ? d->nseq : packed ? d->tokens / piece + d->nseq : d->nseq * cdiv(each, piece);
-    if (pl->npieces > ((int64_t(1) << 31) - 1) / units) return SSM_ERR_DIMS;
+    if (pl->npieces > kMostGroups / units) return SSM_ERR_DIMS;
     pl->carry = pl->pieced ? up256(static_cast<size_t>(pl->npieces * d->nheads * d->dk * d->dv) * 4) : 0;
     pl->tot = pl->pieced ? up256(static_cast<size_t>(pl->npieces * d->nheads) * 4) : 0;
     return SSM_OK;
@@ -200,13 +200,13 @@ extern "C" {
 
 size_t ssm_linattn_fwd_workspace_bytes(const ssm_linattn_dims* dims) {
     la::Sizes z;
-    la::Plan pl, dense;
+    la::Plan pl;
     if (la::check_dims(dims, &z) != SSM_OK) return 0;
     // with and without cu_seqlens: the larger of the two
-    if (la::make_plan(dims, true, &pl) != SSM_OK) return 0;
-    size_t n = pl.carry + pl.tot;
-    if (dims->tokens % dims->nseq == 0 && la::make_plan(dims, false, &dense) == SSM_OK && dense.carry + dense.tot > n)
-        n = dense.carry + dense.tot;
+    size_t n = 0;
+    if (la::make_plan(dims, true, &pl) == SSM_OK) n = pl.carry + pl.tot;
+    if (dims->tokens % dims->nseq == 0 && la::make_plan(dims, false, &pl) == SSM_OK && pl.carry + pl.tot > n)
+        n = pl.carry + pl.tot;
     return n;
 }
 
@@ -311,7 +311,7 @@ int ssm_linattn_step(const void* q, const void* k, const void* v, const float* g
     a.tpr_log2 = lg;
     a.nslices = static_cast<int32_t>(cdiv(d.dv, vw << lg));
     const int64_t blocks = d.nseq * d.nheads * a.nslices;
-    if (blocks > (int64_t(1) << 31) - 1) return SSM_ERR_DIMS;
+    if (blocks > 2 * kMostGroups) return SSM_ERR_DIMS;
     const dim3 grid(static_cast<uint32_t>(blocks)), block(kThreads);
     hipStream_t s = static_cast<hipStream_t>(stream);
     ssm_detail::launch_error = hipSuccess;

@@ -1,0 +1,219 @@
+"""Host-side checks of the block operators (linear attention, norms) that need no GPU: every
+refusal is returned before anything reaches the HIP runtime, so the calls are made with fake
+(never dereferenced) device addresses; the binding's own checks raise on the CPU."""
+import ctypes
+
+import pytest
+
+import selective_state_space_79_amd as ssm
+
+GAP = 1 << 32                      # between the fake arrays
+
+
+def at(n, off=0):
+    return (1 + n) * GAP + off
+
+
+def lin(**kw):
+    base = dict(tokens=100, nseq=2, nheads=4, kheads=2, dk=64, dv=32)
+    base.update({k: kw.pop(k) for k in list(kw) if k in base})
+    return ssm.make_linattn_dims(**base, **kw)
+
+
+def call(name, dims, pointers, structs=(), **change):
+    """A C entry point on fake addresses in the order of `pointers`; change: name -> address."""
+    lib = ssm.load_library()
+    args = [change.get(p, at(i) if not p.startswith("-") else None) for i, p in enumerate(pointers)]
+    return getattr(lib, name)(*args, *map(ctypes.byref, structs), ctypes.byref(dims) if dims is not None else None, None)
+
+
+FWD = ["q", "k", "v", "g", "-cu", "-slots", "-s0", "o", "-s_last"]
+STEP = ["q", "k", "v", "g", "-slots", "states", "o"]
+BWD = ["q", "k", "v", "g", "-cu", "-s0", "do", "-ds_last"]
+GATED = ["x", "-z", "w", "y"]
+GATED_B = ["x", "-z", "w", "dy", "dx", "-dz", "dw"]
+ADD = ["x", "-res", "-scale", "-post", "w", "r", "y"]
+ADD_B = ["-x", "r", "-scale", "-post", "w", "dy", "-dr", "dx", "-dres", "dw", "-dscale", "-dpost"]
+
+
+def fwd(dims, **change):
+    return call("ssm_linattn_fwd", dims, FWD, **change)
+
+
+def grads(**change):
+    g = ssm.SsmLinattnGrads(at(20), at(21), at(22), at(23), None)
+    for k, v in change.items():
+        setattr(g, k, v)
+    return g
+
+
+def bwd(dims, g=None, **change):
+    return call("ssm_linattn_bwd", dims, BWD, (g or grads(),), **change)
+
+
+def with_workspace(dims, need):
+    dims.workspace, dims.workspace_bytes = at(40), need
+    return dims
+
+
+def test_linattn_null_and_empty():
+    assert fwd(None) == ssm.SSM_ERR_NULL
+    for p in ("q", "k", "v", "g", "o"):
+        assert fwd(lin(), **{p: None}) == ssm.SSM_ERR_NULL
+    assert fwd(lin(), **{"-slots": at(30)}) == ssm.SSM_ERR_NULL           # slots without states
+    assert call("ssm_linattn_step", lin(tokens=2, nslots=2), STEP, states=None) == ssm.SSM_ERR_NULL
+    assert bwd(lin(), grads(dq=None)) == ssm.SSM_ERR_NULL
+    assert bwd(lin(), **{"-s0": at(30)}) == ssm.SSM_ERR_NULL              # s0 without ds0
+    for field in ("tokens", "nseq", "nheads", "kheads", "dk", "dv"):
+        for v in (0, -3):
+            assert fwd(lin(**{field: v})) == ssm.SSM_ERR_EMPTY
+            assert bwd(lin(**{field: v})) == ssm.SSM_ERR_EMPTY
+
+
+@pytest.mark.parametrize("bad", [dict(kheads=3), dict(dk=257), dict(dv=257), dict(nseq=65536), dict(nheads=32768, kheads=1),
+                                 dict(tokens=1 << 31), dict(head_decay=2), dict(reserved=1), dict(piece_len=-64),
+                                 dict(piece_len=100), dict(q_stride=127), dict(k_stride=1), dict(v_stride=127),
+                                 dict(o_stride=100), dict(q_stride=1 << 40), dict(o_stride=1 << 23), dict(nseq=3)])
+def test_linattn_sizes(bad):
+    assert fwd(lin(**bad)) == ssm.SSM_ERR_DIMS
+    if "nseq" not in bad or bad["nseq"] != 3:
+        assert ssm.ssm_linattn_fwd_workspace_bytes(lin(**bad)) == 0
+        assert ssm.ssm_linattn_bwd_workspace_bytes(lin(**bad)) == 0
+
+
+def test_linattn_states_and_types():
+    assert fwd(lin(io_dtype=7)) == ssm.SSM_ERR_DTYPE
+    for n in (0, 1, -1):
+        assert fwd(lin(nslots=n), **{"-s0": at(30)}) == ssm.SSM_ERR_DIMS   # fewer states than sequences
+    assert call("ssm_linattn_step", lin(), STEP) == ssm.SSM_ERR_DIMS       # tokens != nseq
+    assert call("ssm_linattn_step", lin(tokens=2, nslots=1), STEP) == ssm.SSM_ERR_DIMS
+    for p in ("q", "k", "v", "o", "g"):
+        i = FWD.index(p)
+        assert fwd(lin(), **{p: at(i, 1)}) == ssm.SSM_ERR_ALIGN
+        assert fwd(lin(io_dtype=0), **{p: at(i, 2)}) == ssm.SSM_ERR_ALIGN
+    for p in ("-cu", "-slots", "-s0", "-s_last"):
+        assert fwd(lin(nslots=2), **{"-s0": at(30), p: at(31, 2)}) == ssm.SSM_ERR_ALIGN
+
+
+def test_linattn_workspace_and_overlaps():
+    big = dict(tokens=4096, nseq=1, nheads=2, kheads=2, dk=64, dv=64)
+    need = ssm.ssm_linattn_fwd_workspace_bytes(lin(**big))
+    assert need > 0
+    assert fwd(lin(**big)) == ssm.SSM_ERR_WORKSPACE
+    assert fwd(with_workspace(lin(**big), need // 2)) == ssm.SSM_ERR_WORKSPACE
+    d = with_workspace(lin(**big), need)
+    d.workspace = at(40, 128)
+    assert fwd(d) == ssm.SSM_ERR_WORKSPACE
+    d.workspace = at(0)
+    assert fwd(d) == ssm.SSM_ERR_ALIAS
+    # o over an input; columns of one buffer are no overlap, one column on is
+    assert fwd(lin(), o=at(0)) == ssm.SSM_ERR_ALIAS
+    row = 2 * 64 + 4 * 32
+    cols = dict(q_stride=row, o_stride=row)
+    assert fwd(lin(**cols), o=at(0, 2 * 2 * 64 - 2)) == ssm.SSM_ERR_ALIAS
+    assert fwd(lin(nslots=2), **{"-s0": at(30), "-s_last": at(30, 4)}) == ssm.SSM_ERR_ALIAS
+    assert fwd(lin(nslots=2), **{"-s0": at(30), "-s_last": at(7)}) == ssm.SSM_ERR_ALIAS
+    assert call("ssm_linattn_step", lin(tokens=2, nslots=2), STEP, states=at(0)) == ssm.SSM_ERR_ALIAS
+    need = ssm.ssm_linattn_bwd_workspace_bytes(lin())
+    assert need > 0 and bwd(lin()) == ssm.SSM_ERR_WORKSPACE
+    d = with_workspace(lin(), need)
+    assert bwd(d, grads(dk=at(20))) == ssm.SSM_ERR_ALIAS
+    assert bwd(d, grads(dv=at(2))) == ssm.SSM_ERR_ALIAS
+    d.workspace = at(23)
+    assert bwd(d) == ssm.SSM_ERR_ALIAS
+
+
+def gated(rows=10, ngroups=2, group=64, x_stride=0, z_stride=0, y_stride=0, io=1, first=1, shared=0, eps=1e-5, ws=None,
+          bytes_=0):
+    return ssm.SsmGatedNormDims(rows, ngroups, group, x_stride, z_stride, y_stride, io, first, shared, eps, ws, bytes_)
+
+
+def added(rows=10, dim=64, x_stride=0, res_stride=0, r_stride=0, y_stride=0, io=1, res=0, eps=1e-5, reserved=0, ws=None,
+          bytes_=0):
+    return ssm.SsmAddNormDims(rows, dim, x_stride, res_stride, r_stride, y_stride, io, res, eps, reserved, ws, bytes_)
+
+
+def test_norm_refusals():
+    for p in ("x", "w", "y"):
+        assert call("ssm_gated_norm_fwd", gated(), GATED, **{p: None}) == ssm.SSM_ERR_NULL
+    assert call("ssm_gated_norm_fwd", None, GATED) == ssm.SSM_ERR_NULL
+    assert call("ssm_gated_norm_bwd", gated(), GATED_B, **{"-z": at(30)}) == ssm.SSM_ERR_NULL      # z without dz
+    assert call("ssm_add_norm_bwd", added(), ADD_B, **{"-scale": at(30)}) == ssm.SSM_ERR_NULL      # no dscale
+    assert call("ssm_add_norm_bwd", added(), ADD_B, **{"-post": at(30), "-dpost": at(31)}) == ssm.SSM_ERR_NULL  # no x
+    for bad in (dict(rows=0), dict(ngroups=0), dict(group=-1)):
+        assert call("ssm_gated_norm_fwd", gated(**bad), GATED) == ssm.SSM_ERR_EMPTY
+    for bad in (dict(group=16385), dict(x_stride=127), dict(y_stride=-5), dict(first=2), dict(shared=3), dict(eps=0.0),
+                dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf")), dict(rows=1 << 41), dict(ngroups=1 << 21)):
+        assert call("ssm_gated_norm_fwd", gated(**bad), GATED) == ssm.SSM_ERR_DIMS
+        assert ssm.ssm_gated_norm_bwd_workspace_bytes(gated(**bad)) == 0
+    for bad in (dict(dim=16385), dict(x_stride=63), dict(res_stride=1), dict(r_stride=2), dict(eps=0.0), dict(reserved=1)):
+        assert call("ssm_add_norm_fwd", added(**bad), ADD) == ssm.SSM_ERR_DIMS
+        assert ssm.ssm_add_norm_bwd_workspace_bytes(added(**bad)) == 0
+    assert call("ssm_gated_norm_fwd", gated(io=2), GATED) == ssm.SSM_ERR_DTYPE
+    assert call("ssm_add_norm_fwd", added(res=5), ADD) == ssm.SSM_ERR_DTYPE
+    assert call("ssm_gated_norm_fwd", gated(), GATED, x=at(0, 1)) == ssm.SSM_ERR_ALIGN
+    assert call("ssm_add_norm_fwd", added(), ADD, r=at(5, 2)) == ssm.SSM_ERR_ALIGN
+    assert call("ssm_gated_norm_bwd", gated(), GATED_B) == ssm.SSM_ERR_WORKSPACE
+    assert call("ssm_add_norm_bwd", added(), ADD_B) == ssm.SSM_ERR_WORKSPACE
+    # y over w, over a part of x; x itself and a column beside x are allowed (and would launch)
+    assert call("ssm_gated_norm_fwd", gated(), GATED, y=at(2)) == ssm.SSM_ERR_ALIAS
+    assert call("ssm_gated_norm_fwd", gated(), GATED, y=at(0, 16)) == ssm.SSM_ERR_ALIAS
+    assert call("ssm_gated_norm_fwd", gated(y_stride=200), GATED, y=at(0)) == ssm.SSM_ERR_ALIAS
+    assert call("ssm_add_norm_fwd", added(), ADD, y=at(5)) == ssm.SSM_ERR_ALIAS
+    assert call("ssm_add_norm_fwd", added(), ADD, **{"-res": at(5, 64)}) == ssm.SSM_ERR_ALIAS
+    need = ssm.ssm_gated_norm_bwd_workspace_bytes(gated())
+    assert need > 0
+    assert call("ssm_gated_norm_bwd", gated(ws=at(40), bytes_=need), GATED_B, dx=at(0)) == ssm.SSM_ERR_ALIAS
+    assert call("ssm_gated_norm_bwd", gated(ws=at(6), bytes_=need), GATED_B) == ssm.SSM_ERR_ALIAS
+
+
+def test_binding_checks_its_arguments():
+    import torch
+
+    q = torch.zeros(8, 2, 16)
+    with pytest.raises(ValueError, match="device"):
+        ssm.linattn_fwd(q, q, q, torch.zeros(8, 2))
+    with pytest.raises(ValueError, match="device"):
+        ssm.linattn_step(q, q, q, torch.zeros(8, 2), torch.zeros(8, 2, 16, 16))
+    with pytest.raises(ValueError, match="device"):
+        ssm.gated_norm_fwd(q, None, torch.zeros(16))
+    with pytest.raises(ValueError, match="device"):
+        ssm.add_norm_fwd(q, None, torch.zeros(16))
+    # the checks behind the device's, on the CPU
+    dims = ssm.blocks._linattn_dims(q, q, torch.zeros(8, 4, 24), torch.zeros(8, 4), 0.5, None)
+    assert (dims.tokens, dims.nseq, dims.nheads, dims.kheads, dims.dk, dims.dv, dims.head_decay) == (8, 1, 4, 2, 16, 24, 0)
+    d4 = ssm.blocks._linattn_dims(q.view(2, 4, 2, 16), q.view(2, 4, 2, 16), q.view(2, 4, 2, 16), torch.zeros(2), 1.0, None)
+    assert (d4.tokens, d4.nseq, d4.head_decay) == (8, 2, 1)
+    wide = torch.zeros(8, 100)
+    part = wide[:, 3:35].view(8, 2, 16)
+    assert ssm.blocks._step("q", part, part.shape) == 100
+    with pytest.raises(ValueError, match="contiguous"):
+        ssm.blocks._step("q", torch.zeros(8, 16, 2).transpose(1, 2), torch.Size((8, 2, 16)))
+    with pytest.raises(ValueError, match="follow"):
+        ssm.blocks._step("q", torch.zeros(2, 6, 2, 16)[:, :4], torch.Size((2, 4, 2, 16)))
+    with pytest.raises(ValueError, match="one shape"):
+        ssm.blocks._linattn_dims(q, q[:, :1], q, torch.zeros(8, 2), 1.0, None)
+    with pytest.raises(TypeError, match="dtype"):
+        ssm.blocks._linattn_dims(q, q.bfloat16(), q, torch.zeros(8, 2), 1.0, None)
+    with pytest.raises(ValueError, match="g must be"):
+        ssm.blocks._linattn_dims(q, q, q, torch.zeros(8, 3), 1.0, None)
+    with pytest.raises(TypeError, match="bfloat16 or float32"):
+        ssm.blocks._io("x", torch.zeros(1, dtype=torch.float16))
+    assert ssm.blocks._matrix("x", torch.zeros(4, 3, 20)[:, :, :16], torch.Size((4, 3, 16))) == 20
+    with pytest.raises(ValueError, match="evenly"):
+        ssm.blocks._matrix("x", torch.zeros(4, 3, 16)[:, :2], torch.Size((4, 2, 16)))
+
+
+def test_workspace_sizes_cover_both_plans():
+    """The forward's workspace does not depend on whether sequences are packed: the larger of
+    the two plans is asked for, whatever the piece length."""
+    for tokens, nseq in ((4096, 1), (4096, 4), (8192, 8), (100, 2), (64, 64), (131072, 1)):
+        for piece in (0, 64, 1024):
+            d = lin(tokens=tokens, nseq=nseq, nheads=8, kheads=2, dk=128, dv=128, piece_len=piece)
+            need = ssm.ssm_linattn_fwd_workspace_bytes(d)
+            with_workspace(d, need)
+            if need:
+                short = lin(tokens=tokens, nseq=nseq, nheads=8, kheads=2, dk=128, dv=128, piece_len=piece)
+                packed = fwd(short, **{"-cu": at(30)}) == ssm.SSM_ERR_WORKSPACE
+                dense = fwd(short) == ssm.SSM_ERR_WORKSPACE
+                assert packed or dense
