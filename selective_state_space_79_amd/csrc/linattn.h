@@ -76,6 +76,7 @@ using ssm_detail::LinattnPass;
 constexpr int kThreads = 256;
 constexpr int kWaves = 4;
 constexpr float kMinDecay = -128.0f;   // e^-128 is zero in float32; keeps sums of -inf apart
+constexpr float kLn2 = 0.69314718f;
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -389,6 +390,13 @@ __device__ inline double lane_f64(double v, int lane) {
                             __builtin_amdgcn_readlane(__double2loint(v), lane));
 }
 
+// 2^x with the part of x that float32 drops brought back: a decay of 2^-50 would else be off
+// by 2^-19 of itself, and the decays' gradient sums such errors over a piece.
+__device__ inline float exp2_of(double x) {
+    const float hi = float(x), e = __builtin_amdgcn_exp2f(hi);
+    return fmaf(e * kLn2, float(x - double(hi)), e);
+}
+
 // One wave: lane r brings row r's log decay and works out the chunk's values.
 template <int C> struct DecayLane {
     double scale = 0.0;   // log2 of s, the same in every lane
@@ -402,9 +410,9 @@ template <int C> struct DecayLane {
             const float hi = float(s);
             d.hi[lane] = hi;
             d.lo[lane] = float(s - double(hi));
-            d.in[lane] = oscale * __builtin_amdgcn_exp2f(float(scale + s));
-            d.out[lane] = wscale * __builtin_amdgcn_exp2f(float(fold ? end - s : -scale - s));
-            if (lane == 0) d.fold = fold ? __builtin_amdgcn_exp2f(float(scale + end)) : 1.0f;
+            d.in[lane] = oscale * exp2_of(scale + s);
+            d.out[lane] = wscale * exp2_of(fold ? end - s : -scale - s);
+            if (lane == 0) d.fold = fold ? exp2_of(scale + end) : 1.0f;
         }
         scale = fold ? 0.0 : scale + end;
         return end;
@@ -830,7 +838,7 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
     float* dst = nullptr;
     // the scale that the registers' state still has, from its head's wave
     __syncthreads();
-    if (dec_wave && lane == 0) decs[0][hw].fold = __builtin_amdgcn_exp2f(float(dl.scale));
+    if (dec_wave && lane == 0) decs[0][hw].fold = exp2_of(dl.scale);
     __syncthreads();
     float mul = decs[0][hw].fold;
     if (FULL) {
@@ -844,7 +852,7 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
         }
     } else {
         dst = p.carry + (pi * p.H + h) * ssz;
-        if (dec_wave && lane == 0 && slice == 0) p.tot[pi * p.H + h] = __builtin_amdgcn_exp2f(float(total));
+        if (dec_wave && lane == 0 && slice == 0) p.tot[pi * p.H + h] = exp2_of(total);
     }
     if (dst) {
 #pragma unroll

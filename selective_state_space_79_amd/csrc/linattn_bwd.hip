@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kThreads) linattn_zero_kernel(LinattnPass p, Z
 // <S, dS> at the start of each piece, one workgroup per piece and head; and the rows of no
 // sequence.
 __global__ void __launch_bounds__(kThreads) linattn_cross_kernel(GradTail t, ZeroRows z) {
-    __shared__ float red[kWaves];
+    __shared__ double red[kWaves];
     const LinattnPass& p = t.p;
     if (blockIdx.y == 0) zero_rows(p, z, blockIdx.x, gridDim.x);
     const int64_t pi = blockIdx.x;
@@ -70,18 +70,16 @@ __global__ void __launch_bounds__(kThreads) linattn_cross_kernel(GradTail t, Zer
     const int64_t n = int64_t(p.kd) * p.vd;
     const float* u = local ? t.fwd + (pi * p.H + h) * n : t.s0 ? t.s0 + (int64_t(seq) * p.H + h) * n : nullptr;
     const float* v = local ? t.rev + ((pi - 1) * p.H + h) * n : t.s0 ? t.ds0 + (int64_t(seq) * p.H + h) * n : nullptr;
-    float s = 0.0f;
+    double s = 0.0;
     const int64_t n4 = n % 4 == 0 && !((reinterpret_cast<uintptr_t>(u) | reinterpret_cast<uintptr_t>(v)) & 15) ? n : 0;
     if (u) {
-        f32x4 a = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
         for (int64_t i = 4 * threadIdx.x; i < n4; i += 4 * kThreads) {
             const f32x4 x = *reinterpret_cast<const f32x4*>(u + i), y = *reinterpret_cast<const f32x4*>(v + i);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) a[e] = fmaf(x[e], y[e], a[e]);
+            for (int e = 0; e < 4; ++e) s = fma(double(x[e]), double(y[e]), s);
         }
-        s = (a[0] + a[1]) + (a[2] + a[3]);
-        for (int64_t i = n4 + threadIdx.x; i < n; i += kThreads) s = fmaf(u[i], v[i], s);
+        for (int64_t i = n4 + threadIdx.x; i < n; i += kThreads) s = fma(double(u[i]), double(v[i]), s);
     }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
@@ -91,9 +89,9 @@ __global__ void __launch_bounds__(kThreads) linattn_cross_kernel(GradTail t, Zer
         s = (red[0] + red[1]) + (red[2] + red[3]);
         if (local) {   // the gradient there is that of the piece's first state: one decay on
             const float g = p.g[(sq.start + local * p.piece) * p.sg + h];
-            s *= __builtin_amdgcn_exp2f((g < kMinDecay ? kMinDecay : g) * kLog2e);
+            s *= double(__builtin_amdgcn_exp2f((g < kMinDecay ? kMinDecay : g) * kLog2e));
         }
-        t.x[pi * p.H + h] = s;
+        t.x[pi * p.H + h] = float(s);
     }
 }
 
@@ -231,7 +229,7 @@ __global__ void __launch_bounds__(kThreads) linattn_group_kernel(LinattnPass p, 
         if (on)
 #pragma unroll 2
             for (int r = 0; r < a.rep; ++r) {
-                float d = 0.0f;
+                double d = 0.0;
 #pragma unroll
                 for (int m = 0; m < M; ++m) {
                     const int c = VW == 4 ? 4 * lane : lane + LPR * m;
@@ -244,14 +242,14 @@ __global__ void __launch_bounds__(kThreads) linattn_group_kernel(LinattnPass p, 
                     for (int e = 0; e < VW; ++e) {
                         sq[m * VW + e] += x[e];
                         sk[m * VW + e] += y[e];
-                        d = fmaf(k[m * VW + e], y[e], d);
-                        d = fmaf(-q[m * VW + e], x[e], d);
+                        d = fma(double(k[m * VW + e]), double(y[e]), d);
+                        d = fma(double(-q[m * VW + e]), double(x[e]), d);
                     }
                 }
                 if (a.f) {
 #pragma unroll
                     for (int z = 1; z < LPR; z <<= 1) d += __shfl_xor(d, z);
-                    if (lane == 0) a.f[tok * p.H + int64_t(kh) * a.rep + r] = d;
+                    if (lane == 0) a.f[tok * p.H + int64_t(kh) * a.rep + r] = float(d);
                 }
             }
 #pragma unroll
