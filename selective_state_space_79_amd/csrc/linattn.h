@@ -115,9 +115,16 @@ struct Seq {
     int64_t start, end;   // tokens
 };
 
+// A value that all lanes have, for the scalar unit: what was read through a pointer that
+// stores may reach stays in vector registers else, and all that is worked out from it.
+__device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ inline int64_t uniform(int64_t v) {
+    return int64_t(uint64_t(uint32_t(uniform(int(v)))) | (uint64_t(uint32_t(uniform(int(v >> 32)))) << 32));
+}
+
 __device__ inline Seq seq_range(const LinattnPass& p, int s) {
     if (!p.cu) return {int64_t(s) * p.L, int64_t(s + 1) * p.L};
-    int64_t a = p.cu[s], b = p.cu[s + 1];
+    int64_t a = uniform(p.cu[s]), b = uniform(p.cu[s + 1]);
     a = a < 0 ? 0 : (a > p.T ? p.T : a);
     b = b < a ? a : (b > p.T ? p.T : b);
     return {a, b};
@@ -173,21 +180,30 @@ template <int W> __device__ constexpr int twist(int r) {
 }
 template <int W> __device__ constexpr int at_piece(int r, int p) { return r * W + 8 * (p ^ twist<W>(r)); }
 
-// Operand along the rows of a tile: lane 16g + i gets columns 32 kb + 8g .. + 7 of row r0 + i.
-template <int W> __device__ inline u32x4 row_op(const uint16_t* t, int r0, int kb, int lane) {
-    return *reinterpret_cast<const u32x4*>(t + at_piece<W>(r0 + (lane & 15), 4 * kb + (lane >> 4)));
+// Byte offset of a lane's operand along the rows of a tile: lane 16g + i takes columns 8g ..
+// + 7 of row i.  Rows 16 n further on are twisted alike, and columns 32 kb further on differ
+// in bits of their own: (offset ^ 64 kb) + 2 W r0.  Offsets are formed by such steps from one
+// value a chunk, since each would else cost a handful of vector instructions, which is what
+// the passes spend most of their time on (left to the compiler: 529 a wave and chunk beside
+// 97 matrix products).
+template <int W> __device__ inline uint32_t row_base(int lane) { return 2 * at_piece<W>(lane & 15, lane >> 4); }
+template <int W> __device__ inline u32x4 row_op(const uint16_t* t, int r0, int kb, uint32_t base) {
+    return *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(t) + (base ^ (64 * kb)) + 2 * W * r0);
 }
 
 // Transposed operand (ds_read_b64_tr_b16: of the four bf16 that lanes 4j + a of a group of
 // 16 address, lane 4a + e gets element e of lane 4j + a as its element j).  Contraction
 // slots 0..7 of lane 16g + i are rows r0 + 8g .. + 7; its column is
-//   spread = 0: c0 + i;   spread = 1: c0 + 8 (i / 4) + i % 4.
-template <int W, int SPREAD> __device__ inline u32x4 col_op(const uint16_t* t, int r0, int c0, int lane) {
-    const int j = (lane >> 2) & 3, a = lane & 3;
-    const int r = r0 + 8 * (lane >> 4) + j;
-    const int c = c0 + (SPREAD ? 8 : 4) * a;
-    const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(t + at_piece<W>(r, c >> 3) + (c & 7)));
-    const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(t + at_piece<W>(r + 4, c >> 3) + (c & 7)));
+//   SPREAD = 0: c0 + i;   SPREAD = 1: 32 kb + 4 half + 8 (i / 4) + i % 4.
+// Rows 4 further on differ in the twist's lowest bit.
+template <int W, int SPREAD> __device__ inline uint32_t col_base(int c0, int lane) {
+    const int r = 8 * (lane >> 4) + ((lane >> 2) & 3), c = c0 + (SPREAD ? 8 : 4) * (lane & 3);
+    return 2 * (at_piece<W>(r, c >> 3) + (c & 7));
+}
+template <int W> __device__ inline u32x4 col_op(const uint16_t* t, int r0, int kb, int half, uint32_t base) {
+    const char* const at = reinterpret_cast<const char*>(t) + 2 * W * r0 + 8 * half;
+    const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + (base ^ (64 * kb))));
+    const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 8 * W + (base ^ (64 * kb + 16))));
     const uint2 u = __builtin_bit_cast(uint2, x), v = __builtin_bit_cast(uint2, y);
     return u32x4{u.x, u.y, v.x, v.y};
 }
@@ -617,6 +633,8 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
         };
         // the value rows of this wave's columns
         const int w0 = wave * 16 * NT;           // this wave's first column of the tile
+        static_assert(NT == 1, "one tile of columns a wave");
+        const uint32_t base3 = col_base<BV, 0>(w0, lane), base2 = col_base<KD, 1>(0, lane), base = row_base<KD>(lane);
         u32x4 v[JB][NT][PARTS];
         auto values = [&] {
 #pragma unroll
@@ -624,7 +642,7 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
 #pragma unroll
                 for (int x = 0; x < NT * PARTS; ++x)
                     v[jb][x / PARTS][x % PARTS] =
-                        col_op<BV, 0>(X3 + (x % PARTS) * C * BV, 32 * jb, w0 + 16 * (x / PARTS), lane);
+                        col_op<BV>(X3 + (x % PARTS) * C * BV, 32 * jb, 0, 0, base3);
         };
 
         f32x4 acc[IT][NT];
@@ -644,8 +662,8 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
 #pragma unroll
                     for (int x = 0; x < AHEAD * PARTS; ++x) {
                         const int kb = x / PARTS, i = x % PARTS;
-                        k[kb][i] = row_op<KD>(X2 + i * C * KD, 16 * jt, k0 + kb, lane);
-                        q[kb][i] = row_op<KD>(X1 + i * C * KD, 16 * it, k0 + kb, lane);
+                        k[kb][i] = row_op<KD>(X2 + i * C * KD, 16 * jt, k0 + kb, base);
+                        q[kb][i] = row_op<KD>(X1 + i * C * KD, 16 * it, k0 + kb, base);
                     }
                     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -680,7 +698,7 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
                 u32x4 q[IT][PARTS];
 #pragma unroll
                 for (int x = 0; x < IT * PARTS; ++x)
-                    q[x / PARTS][x % PARTS] = row_op<KD>(X1 + (x % PARTS) * C * KD, 16 * (x / PARTS), kb, lane);
+                    q[x / PARTS][x % PARTS] = row_op<KD>(X1 + (x % PARTS) * C * KD, 16 * (x / PARTS), kb, base);
                 if (PARTS == 1) __builtin_amdgcn_sched_barrier(0);
                 u32x4 sp[NT][SP];
 #pragma unroll
@@ -724,9 +742,9 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
 #pragma unroll
                 for (int z = 0; z < 4 * NT; ++z) {
                     const int nt = z >> 2, e = z & 3;
-                    float x = 0.0f, y = 0.0f;
+                    float x = bf_lo(v[jb][nt][PARTS - 1][e]), y = bf_hi(v[jb][nt][PARTS - 1][e]);
 #pragma unroll
-                    for (int i = PARTS - 1; i >= 0; --i) {
+                    for (int i = PARTS - 2; i >= 0; --i) {
                         x += bf_lo(v[jb][nt][i][e]);
                         y += bf_hi(v[jb][nt][i][e]);
                     }
@@ -743,7 +761,7 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
 #pragma unroll
                     for (int x = 0; x < AHEAD * PARTS; ++x) {
                         const int m = m0 + x / PARTS, i = x % PARTS;
-                        k[x / PARTS][i] = col_op<KD, 1>(X2 + i * C * KD, 32 * jb, 32 * (m >> 1) + 4 * (m & 1), lane);
+                        k[x / PARTS][i] = col_op<KD>(X2 + i * C * KD, 32 * jb, m >> 1, m & 1, base2);
                     }
                     if (AHEAD > 1) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -761,13 +779,14 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
                 load1(n + 1);
             }
             // ---- the chunk's own share, P x3
+            const uint32_t base_p = row_base<32>(lane);
 #pragma unroll
             for (int jb = 0; jb < JB; ++jb)
 #pragma unroll
                 for (int it = 2 * jb; it < IT; ++it) {
                     u32x4 q[PP];
 #pragma unroll
-                    for (int k = 0; k < PP; ++k) q[k] = row_op<32>(PT + k * PB + p_block(it, jb) * 512, 0, 0, lane);
+                    for (int k = 0; k < PP; ++k) q[k] = row_op<32>(PT + k * PB + p_block(it, jb) * 512, 0, 0, base_p);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) acc[it][nt] = mma_parts<PP, PARTS>(q, v[jb][nt], acc[it][nt]);
                 }
