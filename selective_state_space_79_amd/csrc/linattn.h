@@ -690,6 +690,7 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
                 }
             }
             next();
+            __builtin_amdgcn_s_setprio(1);   // a workgroup in its products goes before one that stores or waits (1.5%)
             // ---- the incoming state's share, e^{G_i} R^T x1_i
 #pragma unroll
             for (int x = 0; x < IT * NT; ++x) acc[x / NT][x % NT] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -771,12 +772,22 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
             }
         };
         if constexpr (FULL) {
-            if constexpr (EARLY) onward();
-            lds_barrier();                      // P is there; x1 and x3 have been read (and x2, if the state is on)
+            lds_barrier();                      // P is there; x1 and x3 have been read
+            // the exact output has no registers left to hold the loads' offsets: kept in scratch
+            // memory they would be waited for behind every load and store under way
             if (ahead && n + 1 < nch) {
-                if constexpr (EARLY) load2(n + 1, X2);
+                if constexpr (EARLY) t3.prepare(tid, pitch3, rev, w3);
                 load3(n + 1, X3);
+                if constexpr (EARLY) t1.prepare(tid, pitch1, rev, p.kd);
                 load1(n + 1);
+            }
+            if constexpr (EARLY) {
+                onward();
+                if (ahead && n + 1 < nch) {
+                    lds_barrier();              // x2 has been read
+                    t2.prepare(tid, pitch2, rev, p.kd);
+                    load2(n + 1, X2);
+                }
             }
             // ---- the chunk's own share, P x3
             const uint32_t base_p = row_base<32>(lane);
@@ -795,6 +806,7 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
             onward();
         }
 
+        __builtin_amdgcn_s_setprio(0);
         if constexpr (FULL) {
             // rows behind the piece's end fall outside the window, as do columns past the head's
             const int oe = PARTS == 3 || p.out_f32 ? 4 : 2;
