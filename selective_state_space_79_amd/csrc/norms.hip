@@ -28,6 +28,8 @@ template <typename IO> struct Raw8 {
         if (vec) {
 #pragma unroll
             for (int k = 0; k < int(sizeof(IO) / 2); ++k) u[k] = reinterpret_cast<const uint4*>(row + col)[k];
+        } else if (col + 8 <= w) {
+            __builtin_memcpy(u, row + col, sizeof(u));   // 16 bytes at any address, as far as the row goes
         } else {
             IO raw[8];
 #pragma unroll
@@ -62,6 +64,8 @@ template <typename IO> __device__ inline void store8(IO* row, int col, int w, bo
             __builtin_memcpy(&u, reinterpret_cast<const char*>(raw) + 16 * k, 16);
             reinterpret_cast<uint4*>(row + col)[k] = u;
         }
+    } else if (col + 8 <= w) {
+        __builtin_memcpy(row + col, raw, sizeof(raw));
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
