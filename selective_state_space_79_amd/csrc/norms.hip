@@ -100,6 +100,22 @@ __device__ inline V8 loadw(const float* w, int col, int n) { return load8<float>
 
 template <int TPG> constexpr int block_threads() { return TPG < 256 ? 256 : TPG; }
 
+// v plus its value in the lane that a DPP control names.
+template <int CTRL> __device__ inline float plus_dpp(float v) {
+    return v + __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(v), CTRL, 0xf, 0xf, true));
+}
+// The sum over each N neighbouring lanes (N a power of two up to 64), the same in all of
+// them: each step's partner holds the other half's sum in every lane.
+template <int N> __device__ inline float lanes_sum(float v) {
+    if (N > 1) v = plus_dpp<0xB1>(v);    // lane ^ 1
+    if (N > 2) v = plus_dpp<0x4E>(v);    // lane ^ 2
+    if (N > 4) v = plus_dpp<0x141>(v);   // mirrored in 8
+    if (N > 8) v = plus_dpp<0x140>(v);   // mirrored in 16
+    if (N > 16) v += __shfl_xor(v, 16);
+    if (N > 32) v += __shfl_xor(v, 32);
+    return v;
+}
+
 // Sums over the TPG threads of a group, one or several at once.  With more than one wave, a
 // slot of LDS per wave; two sets are used in turn, so one barrier is enough.  The barrier
 // waits for LDS only: rows asked for ahead stay under way.
@@ -110,9 +126,7 @@ template <int TPG> struct Summer {
     int turn = 0;
     template <int N> __device__ inline void all(float (&v)[N]) {
 #pragma unroll
-        for (int d = 1; d < (TPG < 64 ? TPG : 64); d <<= 1)
-#pragma unroll
-            for (int n = 0; n < N; ++n) v[n] += __shfl_xor(v[n], d);
+        for (int n = 0; n < N; ++n) v[n] = lanes_sum<(TPG < 64 ? TPG : 64)>(v[n]);
         if constexpr (TPG > 64) {
             constexpr int per = TPG / 64;
             const int wave = threadIdx.x >> 6;
@@ -123,13 +137,10 @@ template <int TPG> struct Summer {
                 for (int n = 0; n < N; ++n) r[wave * kMost + n] = v[n];
             }
             asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            const int w0 = wave / per * per;
+            // a wave's number in each lane: read one by one they would take 48 registers
+            const int from = wave / per * per + (threadIdx.x & (per - 1));
 #pragma unroll
-            for (int n = 0; n < N; ++n) {
-                v[n] = 0.0f;
-#pragma unroll
-                for (int i = 0; i < per; ++i) v[n] += r[(w0 + i) * kMost + n];
-            }
+            for (int n = 0; n < N; ++n) v[n] = lanes_sum<per>(r[from * kMost + n]);
         }
     }
     __device__ inline float operator()(float v) {
