@@ -160,7 +160,9 @@ struct Place {
 };
 template <int TPG> __device__ inline Place place(int64_t rows, int ngroups) {
     constexpr int spb = block_threads<TPG>() / TPG;
-    const int64_t slot = int64_t(blockIdx.x) * spb + threadIdx.x / TPG, slots = int64_t(gridDim.x) * spb;
+    int own = threadIdx.x / TPG;
+    if (TPG >= 64) own = __builtin_amdgcn_readfirstlane(own);   // rows' addresses on the scalar unit
+    const int64_t slot = int64_t(blockIdx.x) * spb + own, slots = int64_t(gridDim.x) * spb;
     Place p;
     p.step = slots / ngroups;
     p.row = slot / ngroups;
