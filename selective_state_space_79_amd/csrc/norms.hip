@@ -290,10 +290,11 @@ __global__ void __launch_bounds__(block_threads<TPG>(), 4) gated_norm_bwd_kernel
             nz[i].load(static_cast<const IO*>(p.z) + row * p.sz + off, col, p.n, on && p.z, p.vec);
         }
     };
-    fetch(at.row);
+    if (V == 1) fetch(at.row);
     for (int64_t l = 0; l < loops; ++l) {
         const int64_t row = at.row + l * at.step;
         const bool on = at.on && row < p.rows;
+        if (V > 1) fetch(row);
         Raw8<IO> rx[V], rz[V], rg[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(block_threads<TPG>(), 4) gated_norm_bwd_kernel
             rz[i] = nz[i];
             rg[i] = ng[i];
         }
-        if (l + 1 < loops) fetch(row + at.step);
+        if (V == 1 && l + 1 < loops) fetch(row + at.step);
         // p = x SiLU(z) or x; g = the gradient at the normalised values: dy w, with the gate
         // behind the norm dy w SiLU(z)
         float qt[2] = {0.0f, 0.0f};
@@ -457,10 +458,11 @@ __global__ void __launch_bounds__(block_threads<TPG>(), 4) add_norm_bwd_kernel(A
             nx[i].load(static_cast<const IO*>(p.x) + row * p.sx, col, p.n, on && (p.scale || p.post), p.vec);
         }
     };
-    fetch(at.row);
+    if (V == 1) fetch(at.row);
     for (int64_t l = 0; l < loops; ++l) {
         const int64_t row = at.row + l * at.step;
         const bool on = at.on && row < p.rows;
+        if (V > 1) fetch(row);
         Raw8<IO> rx[V], ry[V];
         Raw8<RT> rr8[V], rd[V];
 #pragma unroll
@@ -470,7 +472,7 @@ __global__ void __launch_bounds__(block_threads<TPG>(), 4) add_norm_bwd_kernel(A
             rr8[i] = nr[i];
             rd[i] = nd[i];
         }
-        if (l + 1 < loops) fetch(row + at.step);
+        if (V == 1 && l + 1 < loops) fetch(row + at.step);
         float sums[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -500,7 +502,9 @@ __global__ void __launch_bounds__(block_threads<TPG>(), 4) add_norm_bwd_kernel(A
                     d[i].e[e] += fmaf(y.e[e] * w.e[e], rr, -r.e[e] * k);
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);   // else the weights of every step below are read here and spill
             if (p.r) store8<RT>(static_cast<RT*>(p.r) + row * p.n, 8 * (lane + TPG * i), p.n, on, p.vec, d[i]);
+            __builtin_amdgcn_sched_barrier(0);
             const V8 x = rx[i].values();
             if (p.scale) {
                 const V8 sc = weight(1, p.scale, i);
@@ -515,6 +519,7 @@ __global__ void __launch_bounds__(block_threads<TPG>(), 4) add_norm_bwd_kernel(A
 #pragma unroll
                 for (int e = 0; e < 8; ++e) d[i].e[e] *= sc.e[e];
             }
+            __builtin_amdgcn_sched_barrier(0);
             if (p.post) {
                 const V8 po = weight(2, p.post, i);
 #pragma unroll
