@@ -75,6 +75,7 @@ using ssm_detail::LinattnPass;
 
 constexpr int kThreads = 256;
 constexpr int kWaves = 4;
+constexpr int64_t kCus = 256;
 constexpr float kMinDecay = -128.0f;   // e^-128 is zero in float32; keeps sums of -inf apart
 constexpr float kLn2 = 0.69314718f;
 
@@ -899,8 +900,11 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
 // Chooses the kernel of a pass's sizes and starts it.
 template <int MODE> inline bool launch_pass(const ssm_detail::LinattnPasses& q, int count, bool f32, hipStream_t s) {
     const LinattnPass& p = q.p[0];
-    const int shape = MODE == ssm_detail::kLinExact ? ssm_detail::linattn_shape(p.vd, false)
-                                                   : ssm_detail::linattn_shape(p.vd, p.r1 % 2 == 0 && p.r2 % 2 == 0);
+    // two heads in a workgroup share loads and products, but while each head finds a CU of its
+    // own four waves of one SIMD each are sooner done than eight (three float32 prompts of up to
+    // 130 tokens and 6 heads 26.5 us against 30.7; 2 x 8192 tokens of 64 heads 243 against 208)
+    const bool two = MODE != ssm_detail::kLinExact && p.r1 % 2 == 0 && p.r2 % 2 == 0 && int64_t(p.npieces) * p.H > kCus;
+    const int shape = ssm_detail::linattn_shape(p.vd, two);
     const int64_t blocks = int64_t(p.npieces) * (shape == ssm_detail::kTwoHeads ? p.H / 2 : p.H) * p.nslices;
     const dim3 grid(static_cast<uint32_t>(blocks), count), block(shape == ssm_detail::kNarrow ? 256 : 512);
     // float32 rows take three times the LDS: chunks of 32 keep two workgroups on a CU

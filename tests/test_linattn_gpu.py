@@ -600,3 +600,23 @@ def test_a_block_with_its_norms():
     assert far(a["dscale"] + e["dscale"], L["sc"].grad) < 2 ** -5 and far(a["dweight"], L["w2"].grad) < 2 ** -5
     assert far(a["dpost_weight"] + e["dweight"], L["w1"].grad) < 2 ** -5 and far(b["dweight"], L["wn"].grad) < 2 ** -5
     assert far(c["dg"], L["g"].grad) < 2 ** -5
+
+
+@pytest.mark.parametrize("dk,dv,io,kheads,piece", [(64, 64, "bf16", 1, 64), (128, 48, "bf16", 3, 0), (200, 64, "bf16", 3, 64),
+                                                   (72, 40, "f32", 3, 0), (256, 33, "f32", 1, 64), (20, 64, "f32", 3, 64)])
+def test_many_sequences_of_narrow_heads(dk, dv, io, kheads, piece):
+    """More heads and sequences than CUs: heads that share queries and keys go two to a workgroup."""
+    import torch
+    import selective_state_space_79_amd as ssm
+
+    announce(f"many sequences {dk} {dv} {io} {kheads} {piece}")
+    c = Case([1, 0, 33, 64, 70] * 9, 6, kheads, dk, dv, io, seed=dk + dv)
+    o, s = ssm.linattn_fwd(c.q, c.k, c.v, c.g, scale=c.scale, cu_seqlens=c.cu, s0=c.s0, return_state=True,
+                           piece_len=piece)
+    plain = ssm.linattn_fwd(c.q, c.k, c.v, c.g, scale=c.scale, cu_seqlens=c.cu, s0=c.s0, piece_len=piece)
+    r = ssm.linattn_bwd(c.q, c.k, c.v, c.g, do=c.do, scale=c.scale, cu_seqlens=c.cu, s0=c.s0, ds_last=c.ds_last,
+                        piece_len=piece)
+    torch.cuda.synchronize()
+    check_fwd(c, o, s)
+    check_fwd(c, plain)
+    check_grads(c, r)
