@@ -55,7 +55,8 @@ __global__ void __launch_bounds__(kThreads) linattn_zero_kernel(LinattnPass p, Z
 }
 
 // <S, dS> at the start of each piece, one workgroup per piece and head; and the rows of no
-// sequence.
+// sequence.  Bound by the states' bytes and one round of loads: 17 us for 16 pieces of 32 heads
+// of 128 x 128 (134 MB).
 __global__ void __launch_bounds__(kThreads) linattn_cross_kernel(GradTail t, ZeroRows z) {
     __shared__ double red[kWaves];
     const LinattnPass& p = t.p;
@@ -96,7 +97,8 @@ __global__ void __launch_bounds__(kThreads) linattn_cross_kernel(GradTail t, Zer
 }
 
 // dg of one piece for 16 heads: 64 threads of a head take 16 tokens each at a time, their
-// sum, the sums of the threads before, then the running values.  Sums in float64.
+// sum, the sums of the threads before, then the running values.  Sums in float64.  Bound by
+// the latency of its rounds: 21 us for 4 x 4096 tokens of 32 heads, whose values are 4 MB.
 constexpr int kDgThreads = 1024, kDgParts = kDgThreads / 16, kDgTokens = 16;
 
 __global__ void __launch_bounds__(kDgThreads) linattn_dg_kernel(GradTail t) {
@@ -189,7 +191,8 @@ __global__ void __launch_bounds__(kThreads) linattn_dg_sum_kernel(GradTail t) {
 
 // From dq and dk per head in float32: the sums over the heads that share a row, rounded, and
 // f = k . dk - q . dq of each token and head.  LPR lanes take a row, 4 columns each (VW of
-// them in one access); bound by the bytes of the parts.
+// them in one access).  Bound by the bytes of the parts: 138 us for 16384 tokens of 32 heads of
+// 128 in groups of 4 (671 MB, 4.9 TB/s).
 struct GroupArgs {
     const float* dq;
     const float* dk;

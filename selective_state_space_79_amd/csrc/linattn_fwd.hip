@@ -8,7 +8,8 @@ namespace la {
 
 // ---------------------------------------------------------------- pieces' starting states
 // Walks the pieces of one sequence and head: each piece's own end state (from a zero start)
-// is replaced by the state it starts from.  Bound by the states' bytes; 4 values per thread.
+// is replaced by the state it starts from.  Bound by the states' bytes, read and written once:
+// 17 us for 21 pieces of 32 heads of 128 x 128, 5.1 TB/s; 4 values per thread.
 template <int VW> __global__ void __launch_bounds__(kThreads) linattn_carry_kernel(ssm_detail::LinattnPasses q) {
     const LinattnPass& p = q.p[blockIdx.y / q.p[0].H];
     typedef float vf __attribute__((ext_vector_type(VW)));
@@ -67,7 +68,9 @@ struct StepArgs {
 // One workgroup per sequence, head and slice of the state's columns; a row of the slice is
 // read by 2^tpr_log2 threads of VW columns each, the rows of the state go round over the
 // threads.  Everything is one pass over the state, its loads in flight before q and k are
-// looked at; the read-out is summed over the row groups in LDS in a fixed order.
+// looked at; the read-out is summed over the row groups in LDS in a fixed order.  Bound by
+// the states' bytes: 256 sequences of 64 heads of 128 x 64 in 213 us, 5.04 TB/s (a plain copy
+// 5.15); one sequence of 32 heads of 128 x 128 takes 5.6 us on the card and 9.6 with its launch.
 template <typename IO, int VW>
 __global__ void __launch_bounds__(kThreads) linattn_step_kernel(StepArgs p) {
     typedef float vf __attribute__((ext_vector_type(VW)));
@@ -151,9 +154,10 @@ struct Plan {
 // Pieces along the tokens.  A workgroup walks its piece chunk by chunk, 3.6 us for 64 tokens
 // of a 128 x 128 head alone on its CU and 8.8 us for two side by side, so work is cut into the
 // 512 workgroups that the card holds at once; more, smaller pieces only add states to carry.
-// Measured, us: 131072 tokens of 16 heads 754 in 512 workgroups (pieces of 4096), 794 in 1024,
-// 884 in 2048; 8 ragged prompts of 8192 tokens in all, 32 heads, 136 in pieces of 512, 168 of
-// 256, 254 of 2048.  Cutting costs two launches and a second pass over keys and values:
+// Measured, us: 131072 tokens of 16 heads 723 in pieces of 4096, 787 of 2048, 810 of 8192; 8
+// ragged prompts of 8192 tokens in all, 32 heads, 161 in pieces of 512, 180 of 320, 154 of 704,
+// 270 of 2048; 2 x 8192 tokens of 64 shared heads of 64 189 in pieces of 1024, 222 of 512, 273
+// of 2048.  Cutting costs two launches and a second pass over keys and values:
 // sequences of up to 256 tokens stay whole.
 inline int64_t choose_piece(const ssm_linattn_dims* d, int64_t units, int64_t each) {
     const int64_t want = 512 / units;   // pieces of the whole call

@@ -6,6 +6,17 @@
 // wave with several groups side by side, or 2 .. 16 waves that exchange one number per
 // reduction through LDS.  One vector per thread (two for rows over 8192) keeps registers
 // few and leaves the loads in flight to the number of waves.
+//
+// The gradients hold the next row's values while one is worked on, up to 8192 columns (above,
+// the registers for it would lie in scratch memory: 358 us against 186 for the gate norm of
+// 4096 bf16 rows of 16384), and the sums for the weights' gradients in registers over a
+// workgroup's rows; 1024 workgroups' partial sums are then added in a fixed order.
+//
+// Measured: gated forward 16384 rows of 64 groups of 64 in 75 us (5.4 TB/s; a plain copy 5.15),
+// 1535 wide 38 us (4.0 TB/s); its gradient 16383 rows of 1536 in 69 us (3.7 TB/s, 56 us of it
+// the rows, 5 the partial sums); residual norm 4096 wide 150 us (5.4 TB/s), its gradient at
+// 2048 columns with both weights in 129 us (4.7 TB/s), 4096 without 147 us (5.5 TB/s), 8192
+// 224 us (3.6 TB/s), 16384 581 us (1.4 TB/s, bound by registers).
 #include "rows.h"
 
 namespace {
