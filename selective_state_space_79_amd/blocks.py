@@ -227,11 +227,17 @@ def _step(name, t, sh):
     heads, width = sh[-2], sh[-1]
     if not ((width == 1 or st[-1] == 1) and (heads == 1 or st[-2] == width)):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    if len(sh) == 3:
-        return st[0] if sh[0] > 1 else 0
-    if sh[0] > 1 and sh[1] > 1 and st[0] != sh[1] * st[1]:
+    if len(sh) == 4 and sh[0] > 1 and sh[1] > 1 and st[0] != sh[1] * st[1]:
         raise ValueError(f"{name}: batch rows must follow one another")
-    return st[1] if sh[1] > 1 else st[0] if sh[0] > 1 else 0
+    tokens = next(((n, s) for n, s in zip(sh[-3::-1], st[-3::-1]) if n > 1), None)
+    return 0 if tokens is None else _apart(name, tokens[1], heads * width)
+
+
+def _apart(name, step, width):
+    """A step between rows that is one (0 would be taken for packed rows)."""
+    if step < width:
+        raise ValueError(f"{name}: rows must not overlap (an expanded tensor has to be copied first)")
+    return step
 
 
 _HERE = contextlib.nullcontext()
@@ -436,16 +442,16 @@ def _matrix(name, t, sh):
     st = t.stride()
     if sh[-1] > 1 and st[-1] != 1:
         raise ValueError(f"{name}: a row must be contiguous")
-    rows, step = 1, 0
+    rows, step = 1, None
     for n, s in zip(reversed(sh[:-1]), reversed(st[:-1])):
         if n == 1:
             continue
-        if step and s != step * rows:
+        if step is not None and s != step * rows:
             raise ValueError(f"{name}: rows must be evenly spaced")
-        if not step:
+        if step is None:
             step = s
         rows *= n
-    return step
+    return 0 if step is None else _apart(name, step, sh[-1])
 
 
 def _rows(t, sh):

@@ -217,3 +217,30 @@ def test_workspace_sizes_cover_both_plans():
                 packed = fwd(short, **{"-cu": at(30)}) == ssm.SSM_ERR_WORKSPACE
                 dense = fwd(short) == ssm.SSM_ERR_WORKSPACE
                 assert packed or dense
+
+
+def test_expanded_rows_are_refused():
+    """A step of 0 from row to row reads as packed rows: it must not reach a launch."""
+    import torch
+    from selective_state_space_79_amd import blocks
+
+    row = torch.zeros(1, 2, 8)
+    for t in (row.expand(5, 2, 8), row.unsqueeze(0).expand(3, 5, 2, 8), row.unsqueeze(0).expand(3, 1, 2, 8),
+              torch.zeros(40).as_strided((4, 2, 8), (8, 8, 1))):
+        with pytest.raises(ValueError, match="overlap"):
+            blocks._step("q", t, t.shape)
+    for t in (torch.zeros(8).expand(5, 8), torch.zeros(1, 1, 8).expand(3, 5, 8), torch.zeros(40).as_strided((4, 8), (4, 1))):
+        with pytest.raises(ValueError, match="overlap"):
+            blocks._matrix("x", t, t.shape)
+    with pytest.raises(ValueError, match="evenly"):
+        t = torch.zeros(3, 1, 8).expand(3, 5, 8)
+        blocks._matrix("x", t, t.shape)
+    wide = torch.zeros(3, 5, 2, 24)
+    assert blocks._step("q", wide[0], (5, 2, 24)) == 0
+    with pytest.raises(ValueError, match="heads"):
+        blocks._step("q", wide[..., :8], (3, 5, 2, 8))
+    cols = torch.zeros(3, 5, 48)
+    assert blocks._step("q", cols[..., :16].unflatten(-1, (2, 8)), (3, 5, 2, 8)) == 48
+    assert blocks._step("q", cols[:1, :1, :16].unflatten(-1, (2, 8)), (1, 1, 2, 8)) == 0
+    assert blocks._matrix("x", cols[..., :16], (3, 5, 16)) == 48
+    assert blocks._matrix("x", cols[:, :1, :16], (3, 1, 16)) == 240

@@ -620,3 +620,26 @@ def test_many_sequences_of_narrow_heads(dk, dv, io, kheads, piece):
     check_fwd(c, o, s)
     check_fwd(c, plain)
     check_grads(c, r)
+
+
+def test_expanded_inputs_are_refused():
+    """Broadcast views whose rows share memory have no step between rows: an error, no launch."""
+    import torch
+    import selective_state_space_79_amd as ssm
+
+    announce("expanded inputs")
+    q = torch.zeros(5, 2, 8, device="cuda")
+    one = torch.ones(1, 2, 8, device="cuda").expand(5, 2, 8)
+    g = torch.zeros(5, 2, device="cuda")
+    for name in ("q", "k", "v"):
+        with pytest.raises(ValueError, match="overlap"):
+            ssm.linattn_fwd(**{**dict(q=q, k=q, v=q), name: one}, g=g)
+    with pytest.raises(ValueError):
+        ssm.linattn_bwd(q, q, q, g, do=torch.ones(1, device="cuda").expand(5, 2, 8))
+    with pytest.raises(ValueError, match="overlap"):
+        ssm.linattn_step(q, q, one, g, torch.zeros(5, 2, 8, 8, device="cuda"))
+    x, w = torch.zeros(5, 8, device="cuda"), torch.ones(8, device="cuda")
+    with pytest.raises(ValueError, match="overlap"):
+        ssm.gated_norm_fwd(x, w.expand(5, 8), w)
+    with pytest.raises(ValueError, match="overlap"):
+        ssm.add_norm_fwd(x, w.expand(5, 8), w)
