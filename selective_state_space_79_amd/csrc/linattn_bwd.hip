@@ -416,11 +416,11 @@ int ssm_linattn_bwd(const void* q, const void* k, const void* v, const float* g,
     pq.kd = static_cast<int32_t>(d.dv); pq.vd = static_cast<int32_t>(d.dk); pq.nslices = static_cast<int32_t>(pl.slices_q);
     pq.s_in = s0; pq.st_t = 1; pq.carry = fwd; pq.oscale = d.scale; pq.exact = 0;
     pq.out = apart ? static_cast<void*>(wq) : gr.dq; pq.out_f32 = apart; pq.so = d.nheads * d.dk;
-    pq.pairs = pair_rows(gr.dq, pq.so, d.dk);
+    pq.pairs = !apart && pair_rows(gr.dq, pq.so, d.dk);
     LinattnPass pk = pq;     // dk = (v, do, q) from dS
     pk.x1 = v; pk.s1 = z.v; pk.x2 = dout; pk.s2 = z.o; pk.x3 = q; pk.s3 = z.q;
     pk.s_in = ds_last; pk.carry = rev; pk.oscale = 1.0f; pk.wscale = d.scale; pk.reverse = 1;
-    pk.out = apart ? static_cast<void*>(wkk) : gr.dk; pk.pairs = pair_rows(gr.dk, pk.so, d.dk);
+    pk.out = apart ? static_cast<void*>(wkk) : gr.dk; pk.pairs = !apart && pair_rows(gr.dk, pk.so, d.dk);
     LinattnPass pv = sr;     // dv = (k, q, do) from dS
     pv.x1 = k; pv.s1 = z.k; pv.r1 = rep; pv.out = gr.dv; pv.so = wv; pv.s_out = gr.ds0; pv.exact = gr.ds0 != nullptr; pv.pairs = pair_rows(gr.dv, wv, d.dv);
 
