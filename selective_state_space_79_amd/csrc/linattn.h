@@ -556,8 +556,8 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
     const int64_t nch = (hi - lo + C - 1) / C;
     // The pieces' own states are summed from each piece's last chunk to its first: what is read
     // last is what the pass with the read-out asks for first, and is still in the memory-side
-    // cache as far as that goes (131072 tokens of 16
-    // heads 812 -> 798 us, 2 x 8192 of 64 shared heads 197 -> 190).
+    // cache as far as that goes (131072 tokens of 16 heads 812 -> 798 us, 2 x 8192 tokens of 64
+    // shared heads 197 -> 190).
     const bool back = rev == FULL;
     auto first_of = [&](int64_t n) { return lo + (back ? nch - 1 - n : n) * C; };
     // the last wave of a head brings its decays, a chunk ahead; against time the decay of a

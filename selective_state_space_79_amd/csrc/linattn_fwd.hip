@@ -66,14 +66,18 @@ struct StepArgs {
 };
 
 // One workgroup per sequence, head and slice of the state's columns; a row of the slice is
-// read by 2^tpr_log2 threads of VW columns each, the rows of the state go round over the
+// read by 2^tpr_log2 threads of 4 columns each, the rows of the state go round over the
 // threads.  Everything is one pass over the state, its loads in flight before q and k are
 // looked at; the read-out is summed over the row groups in LDS in a fixed order.  Bound by
 // the states' bytes: 256 sequences of 64 heads of 128 x 64 in 213 us, 5.04 TB/s (a plain copy
 // 5.15); one sequence of 32 heads of 128 x 128 takes 5.6 us on the card and 9.6 with its launch.
-template <typename IO, int VW>
+//
+// 16 bytes are read and written at any alignment as far as the row goes (29 sequences of 32
+// heads of 125 x 135 50 us by single values, 36 so).
+template <typename IO>
 __global__ void __launch_bounds__(kThreads) linattn_step_kernel(StepArgs p) {
-    typedef float vf __attribute__((ext_vector_type(VW)));
+    constexpr int VW = 4;
+    typedef f32x4 vf;
     constexpr int R = 8;   // rows in flight per thread
     __shared__ float sq[SSM_LINATTN_MAX_DIM], sk[SSM_LINATTN_MAX_DIM];
     __shared__ float red[kThreads * VW];
@@ -90,13 +94,33 @@ __global__ void __launch_bounds__(kThreads) linattn_step_kernel(StepArgs p) {
     }
     const int tpr = 1 << p.tpr_log2, rows = kThreads >> p.tpr_log2;
     const int r0 = tid >> p.tpr_log2, col = (slice * tpr + (tid & (tpr - 1))) * VW;
-    const bool on = col < p.dv;
+    const bool on = col < p.dv, whole = col + VW <= p.dv;
+    const auto read = [&](const float* q) {
+        vf x = {};
+        if (whole) {
+            __builtin_memcpy(&x, q, sizeof(x));
+        } else {
+#pragma unroll
+            for (int e = 0; e < VW; ++e)
+                if (col + e < p.dv) x[e] = q[e];
+        }
+        return x;
+    };
+    const auto write = [&](float* q, const vf& x) {
+        if (whole) {
+            __builtin_memcpy(q, &x, sizeof(x));
+        } else {
+#pragma unroll
+            for (int e = 0; e < VW; ++e)
+                if (col + e < p.dv) q[e] = x[e];
+        }
+    };
     float* S = p.states + (int64_t(slot) * p.H + h) * p.dk * p.dv + col;
     vf s[R];
 #pragma unroll
     for (int n = 0; n < R; ++n) {
         const int r = r0 + n * rows;
-        if (on && r < p.dk) s[n] = *reinterpret_cast<const vf*>(S + int64_t(r) * p.dv);
+        if (on && r < p.dk) s[n] = read(S + int64_t(r) * p.dv);
     }
     const IO* q = static_cast<const IO*>(p.q) + b * p.sq + int64_t(h / p.rep) * p.dk;
     const IO* k = static_cast<const IO*>(p.k) + b * p.sk + int64_t(h / p.rep) * p.dk;
@@ -112,7 +136,7 @@ __global__ void __launch_bounds__(kThreads) linattn_step_kernel(StepArgs p) {
     if (on) {
         const IO* vr = static_cast<const IO*>(p.v) + b * p.sv + int64_t(h) * p.dv + col;
 #pragma unroll
-        for (int e = 0; e < VW; ++e) v[e] = IOT<IO>::to_f32(vr[e]);
+        for (int e = 0; e < VW; ++e) v[e] = whole || col + e < p.dv ? IOT<IO>::to_f32(vr[e]) : 0.0f;
     }
     float g = p.g[b * p.sg + h];
     g = g < kMinDecay ? kMinDecay : g;
@@ -125,10 +149,10 @@ __global__ void __launch_bounds__(kThreads) linattn_step_kernel(StepArgs p) {
         for (int n = 0; n < R; ++n) {
             const int r = base + r0 + n * rows;
             if (!(on && r < p.dk)) continue;
-            if (base > 0) s[n] = *reinterpret_cast<const vf*>(S + int64_t(r) * p.dv);
+            if (base > 0) s[n] = read(S + int64_t(r) * p.dv);
             s[n] = a * s[n] + sk[r] * v;
             o += sq[r] * s[n];
-            *reinterpret_cast<vf*>(S + int64_t(r) * p.dv) = s[n];
+            write(S + int64_t(r) * p.dv, s[n]);
         }
     }
     *reinterpret_cast<vf*>(&red[tid * VW]) = o;
@@ -306,7 +330,7 @@ int ssm_linattn_step(const void* q, const void* k, const void* v, const float* g
     a.H = static_cast<int32_t>(d.nheads); a.rep = static_cast<int32_t>(d.nheads / d.kheads);
     a.dk = static_cast<int32_t>(d.dk); a.dv = static_cast<int32_t>(d.dv); a.nslots = static_cast<int32_t>(d.nslots);
     a.scale = d.scale;
-    const int vw = d.dv % 4 == 0 && !misaligned(states, 16) ? 4 : 1;
+    constexpr int vw = 4;
     // as many columns a workgroup as the state has, halved while the card has room for more
     // workgroups and a row of the slice is still 64 bytes
     int lg = 0;
@@ -319,13 +343,8 @@ int ssm_linattn_step(const void* q, const void* k, const void* v, const float* g
     const dim3 grid(static_cast<uint32_t>(blocks)), block(kThreads);
     hipStream_t s = static_cast<hipStream_t>(stream);
     ssm_detail::launch_error = hipSuccess;
-    if (d.io_dtype == SSM_BF16) {
-        if (vw == 4) launch_kernel(linattn_step_kernel<uint16_t, 4>, grid, block, 0, s, a);
-        else launch_kernel(linattn_step_kernel<uint16_t, 1>, grid, block, 0, s, a);
-    } else {
-        if (vw == 4) launch_kernel(linattn_step_kernel<float, 4>, grid, block, 0, s, a);
-        else launch_kernel(linattn_step_kernel<float, 1>, grid, block, 0, s, a);
-    }
+    if (d.io_dtype == SSM_BF16) launch_kernel(linattn_step_kernel<uint16_t>, grid, block, 0, s, a);
+    else launch_kernel(linattn_step_kernel<float>, grid, block, 0, s, a);
     return ssm_detail::launch_error == hipSuccess ? SSM_OK : SSM_ERR_HIP;
 }
 
