@@ -460,11 +460,11 @@ __device__ constexpr int p_block(int it, int jb) { return it < 2 ? it : 2 * it -
 // go two to a workgroup (NH), each with its own decays on the same products; other narrow
 // heads take four waves.
 //
-// What bounds it: the issue of vector and matrix instructions.  A wave and chunk of 64 tokens
+// What bounds it: the issue of vector and matrix instructions, with the rows' bytes close behind.  A wave and chunk of 64 tokens
 // of a 128 x 128 head takes 97 matrix products (16 cycles each) and 445 vector instructions
 // (4 cycles each), half of them the split of the state and of the decayed values into bf16
-// parts; counted on 131072 tokens of 16 heads they fill 46% and 53% of the SIMD cycles.  The output pass takes 536 us there and the states pass before it 243 us (3.0 TB/s
-// of rows, against 5.2 TB/s of a plain copy); a float32 output's pass 323 us for dq and dk of
+// parts; counted on 131072 tokens of 16 heads they fill 46% and 53% of the SIMD cycles.  The output pass takes 489 us there (4.4 TB/s of rows; a plain copy 5.15) and the
+// states pass before it 223 us (4.8 TB/s); a float32 output's pass 315 us for dq and dk of
 // 4 x 4096 tokens of 32 heads.  Tried without gain: 32 columns a wave from registers, keys two
 // products ahead, the parts' rests by two-term products.
 //
