@@ -489,9 +489,9 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
     // bf16 rows come straight into LDS, each tile as soon as the last chunk's readers are
     // done with it: x2 (read to the end) and without a read-out x3 have a second tile, where
     // that still leaves room for two workgroups on a CU.  The exact output's third part of P
-    // takes that room: there the state goes on first (EARLY), and then all three tiles are
-    // free.  Two heads' P takes it too: x2 is asked for behind everything else (203 us for
-    // 2 x 8192 tokens of 64 heads of 64 with 128 states, 239 us with the state first).
+    // takes that room: there the state goes on before P x3, and x2 is free after it (EARLY).
+    // Two heads' P takes it too: x2 is asked for behind everything else (203 us for 2 x 8192
+    // tokens of 64 heads of 64 with 128 states, 239 us with the state first).
     // float32 rows are held in registers from one chunk to the next.
     constexpr bool DMA = PARTS == 1, EARLY = EXACT, TWO2 = DMA && !EXACT && !(FULL && KD == 128 && NH == 2),
                    TWO3 = DMA && !FULL;

@@ -643,3 +643,23 @@ def test_expanded_inputs_are_refused():
         ssm.gated_norm_fwd(x, w.expand(5, 8), w)
     with pytest.raises(ValueError, match="overlap"):
         ssm.add_norm_fwd(x, w.expand(5, 8), w)
+
+
+@pytest.mark.parametrize("io,piece,heads,kheads,dk,dv", [("bf16", 192, 3, 3, 128, 128), ("bf16", 256, 4, 1, 64, 64),
+                                                         ("f32", 192, 2, 1, 64, 96), ("f32", 320, 2, 2, 130, 33)])
+def test_pieces_of_many_chunks(io, piece, heads, kheads, dk, dv):
+    """Odd and even numbers of chunks in a piece, pieces that end inside a chunk, decays from mild to a reset."""
+    import torch
+    import selective_state_space_79_amd as ssm
+
+    announce(f"pieces of many chunks {io} {piece} {heads} {kheads} {dk} {dv}")
+    c = Case([piece * 2 + 77, 1, piece, piece + 1, 3 * piece - 30], heads, kheads, dk, dv, io, seed=piece + dk)
+    c.g *= 0.05                         # decays that reach across pieces
+    c.g[piece + 5] = -60.0
+    o, s = ssm.linattn_fwd(c.q, c.k, c.v, c.g, scale=c.scale, cu_seqlens=c.cu, s0=c.s0, return_state=True,
+                           piece_len=piece)
+    r = ssm.linattn_bwd(c.q, c.k, c.v, c.g, do=c.do, scale=c.scale, cu_seqlens=c.cu, s0=c.s0, ds_last=c.ds_last,
+                        piece_len=piece)
+    torch.cuda.synchronize()
+    check_fwd(c, o, s)
+    check_grads(c, r)
