@@ -8,15 +8,15 @@
 // few and leaves the loads in flight to the number of waves.
 //
 // The gradients hold the next row's values while one is worked on, up to 8192 columns (above,
-// the registers for it would lie in scratch memory: 358 us against 186 for the gate norm of
+// the registers for it would lie in scratch memory: 358 us against 156 for the gate norm of
 // 4096 bf16 rows of 16384), and the sums for the weights' gradients in registers over a
-// workgroup's rows; 1024 workgroups' partial sums are then added in a fixed order.
+// workgroup's rows; the workgroups' partial sums are then added in a fixed order.
 //
 // Measured: gated forward 16384 rows of 64 groups of 64 in 75 us (5.4 TB/s; a plain copy 5.15),
 // 1535 wide 38 us (4.0 TB/s); its gradient 16383 rows of 1536 in 69 us (3.7 TB/s, 56 us of it
 // the rows, 5 the partial sums); residual norm 4096 wide 150 us (5.4 TB/s), its gradient at
-// 2048 columns with both weights in 129 us (4.7 TB/s), 4096 without 147 us (5.5 TB/s), 8192
-// 224 us (3.6 TB/s), 16384 581 us (1.4 TB/s, bound by registers).
+// 2048 columns with both weights in 129 us (4.7 TB/s), 4096 without 135 us (6.0 TB/s), 8192
+// 183 us (4.4 TB/s), 16384 451 us (1.8 TB/s, bound by registers).
 #include "rows.h"
 
 namespace {
@@ -611,7 +611,11 @@ inline int64_t blocks_for(int64_t rows, int64_t ngroups, int tpg, int64_t most) 
     return b < one ? one : b;
 }
 
-constexpr int64_t kBwdBlocks = 1024;
+// A gradient's workgroups: as many as the card holds at once, 1024 threads a CU; fewer leave
+// it idle, more only add partial sums.  Measured, us at 256, 512 and 1024 workgroups: 8192 rows
+// of 8192 columns 183, 198, 224; 16384 of 4096 202, 135, 144; at 512, 1024 and 2048: 16384 rows
+// of 32 groups of 128 192, 131, 137.
+inline int64_t bwd_blocks(int tpg) { return 256 * 1024 / (tpg < 256 ? 256 : tpg); }
 constexpr int64_t kFwdBlocks = int64_t(1) << 20;
 
 inline bool vec_row(const void* q, int64_t stride, int64_t e) { return !misaligned(q, 16) && stride * e % 16 == 0; }
@@ -742,7 +746,7 @@ size_t ssm_gated_norm_bwd_workspace_bytes(const ssm_gated_norm_dims* dims) {
     using namespace nrm;
     if (check(dims) != SSM_OK) return 0;
     const int tpg = tpg_for(dims->group);
-    const int64_t blocks = blocks_for(dims->rows, dims->ngroups, tpg, kBwdBlocks);
+    const int64_t blocks = blocks_for(dims->rows, dims->ngroups, tpg, bwd_blocks(tpg));
     const int64_t lanes = blocks * slots_per_block(tpg) / dims->ngroups;
     return static_cast<size_t>(dims->shared_weight ? blocks * dims->group : lanes * dims->ngroups * dims->group) * 4;
 }
@@ -773,7 +777,7 @@ int ssm_gated_norm_bwd(const void* x, const void* z, const float* w, const void*
     a.vec = d.group % 8 == 0 && vec_row(x, a.sx, e) && vec_row(dy, dim, e) && vec_row(dx, dim, e) &&
             (!z || (vec_row(z, a.sz, e) && vec_row(dz, dim, e)));
     const int tpg = tpg_for(d.group);
-    const int64_t blocks = blocks_for(d.rows, d.ngroups, tpg, kBwdBlocks);
+    const int64_t blocks = blocks_for(d.rows, d.ngroups, tpg, bwd_blocks(tpg));
     const int64_t lanes = blocks * slots_per_block(tpg) / d.ngroups;
     hipStream_t s = static_cast<hipStream_t>(stream);
     ssm_detail::launch_error = hipSuccess;
@@ -820,7 +824,8 @@ int ssm_add_norm_fwd(const void* x, const void* res, const float* scale, const f
 size_t ssm_add_norm_bwd_workspace_bytes(const ssm_add_norm_dims* dims) {
     using namespace nrm;
     if (check(dims) != SSM_OK) return 0;
-    return static_cast<size_t>(3 * blocks_for(dims->rows, 1, tpg_for(dims->dim), kBwdBlocks) * dims->dim) * 4;
+    const int tpg = tpg_for(dims->dim);
+    return static_cast<size_t>(3 * blocks_for(dims->rows, 1, tpg, bwd_blocks(tpg)) * dims->dim) * 4;
 }
 
 int ssm_add_norm_bwd(const void* x, const void* r, const float* scale, const float* post, const float* w,
@@ -856,7 +861,7 @@ int ssm_add_norm_bwd(const void* x, const void* r, const float* scale, const flo
     a.vec = d.dim % 8 == 0 && (!x || vec_row(x, a.sx, e)) && vec_row(r, a.sr, f) && vec_row(dy, d.dim, e) &&
             vec_row(dx, d.dim, e) && (!dr || vec_row(dr, d.dim, f)) && (!dres || vec_row(dres, d.dim, f));
     const int tpg = tpg_for(d.dim);
-    const int64_t blocks = blocks_for(d.rows, 1, tpg, kBwdBlocks);
+    const int64_t blocks = blocks_for(d.rows, 1, tpg, bwd_blocks(tpg));
     hipStream_t s = static_cast<hipStream_t>(stream);
     ssm_detail::launch_error = hipSuccess;
     add(a, d, tpg, blocks, true, s);
