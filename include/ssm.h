@@ -449,9 +449,8 @@ SSM_API int ssm_ssd_fwd(const void* u, const void* delta, const float* A, const 
  *
  * Sums and states are float32.  The products run on the matrix cores on bf16 operands;
  * operands that are not bf16 inputs (the state, the decayed products, and everything when
- * io_dtype is SSM_F32) are split into bf16 parts: three, which hold a float32, where a
- * float32 output depends on them (states, float32 rows, dg), else two, which leave out under
- * 2^-17 of each.
+ * io_dtype is SSM_F32) are split into three bf16 parts, which hold a float32.  What a call
+ * asks for does not change how its outputs are formed.
  * A NaN or infinity in a token reaches outputs of earlier tokens of its sequence at most
  * within its block of 64 tokens, and never another sequence.
  * Ownership, asynchrony and the error rules are those of ssm_selective_scan_fwd. */

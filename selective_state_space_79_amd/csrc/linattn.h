@@ -44,7 +44,6 @@ struct LinattnPass {
     int32_t reverse, out_f32;
     int32_t wide;             // rows of x1 .. x3 allow 16-byte loads at 32-bit offsets
     int32_t pairs;            // out allows stores of two bf16
-    int32_t exact;            // a float32 output depends on the state's values
     float wscale, oscale;
 };
 
@@ -54,11 +53,9 @@ struct LinattnPasses {
 };
 
 // The launches return false for sizes that no kernel covers (nothing launched).
-// kLinStates: the pieces' own end states; kLinFull: the outputs; kLinExact: the outputs in
-// float32, with every product of float32's precision (bf16 rows: out_f32 set).
-enum LinattnMode { kLinStates = 0, kLinFull = 1, kLinExact = 2 };
-bool launch_linattn_pass(const LinattnPasses& p, int count, bool f32, LinattnMode mode, hipStream_t s);       // modes 0, 1
-bool launch_linattn_exact(const LinattnPasses& p, int count, bool f32, hipStream_t s);   // (float32 rows: mode 1)
+// kLinStates: the pieces' own end states; kLinFull: the outputs.
+enum LinattnMode { kLinStates = 0, kLinFull = 1 };
+bool launch_linattn_pass(const LinattnPasses& p, int count, bool f32, LinattnMode mode, hipStream_t s);
 void launch_linattn_carry(const LinattnPasses& p, int count, hipStream_t s);
 // How a pass over vd columns is cut: 128 columns of a head to a workgroup, 64, or two heads
 // of up to 64 that share x1 and x2
@@ -95,8 +92,8 @@ __device__ inline float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ inline float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
 // Two values in N bf16 parts each (part 0 is bf16(x), the next the rounded rest, ...), packed
-// in pairs.  One rounding leaves at most 2^-9 of the power of two above x, so two parts leave
-// under 2^-17 of x and three parts, which hold 24 bits, all of a float32.
+// in pairs.  One rounding leaves at most 2^-9 of the power of two above x, so three parts, which
+// hold 24 bits, leave nothing of a float32 (two would leave up to 2^-17 of x).
 template <int N> __device__ inline void split(float a, float b, uint32_t (&w)[N]) {
 #pragma unroll
     for (int n = 0; n < N; ++n) {
@@ -468,37 +465,41 @@ __device__ constexpr int p_block(int it, int jb) { return it < 2 ? it : 2 * it -
 // 4 x 4096 tokens of 32 heads.  Tried without gain: 32 columns a wave from registers, keys two
 // products ahead, the parts' rests by two-term products.
 //
-// Parts: products that end in a float32 output (the exact mode's, and the state where the
-// caller gets it: VP) take three parts of what is not a bf16 input; those that end in a bf16
-// output take two.
+// Parts: what is not a bf16 input (the state, the decayed products and values, float32 rows)
+// goes into the products in three bf16 parts, which hold a float32 whole.  Two parts would take
+// a fifth less of either unit (131072 tokens of 16 heads 776 us against 860) and leave out up to
+// 2^-17 of each operand: outputs where terms cancel show that.
 constexpr int pass_waves(int KD, int NW, int NT) { return KD == 256 ? NW / 4 : NW / 2; }   // per SIMD
 
-template <int PARTS, int KD, int NW, int NT, int C, int MODE, int NH, int VP>
+template <int PARTS, int KD, int NW, int NT, int C, int MODE, int NH>
 __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_kernel(ssm_detail::LinattnPasses passes) {
     using namespace ssm_detail;
     const LinattnPass& p = passes.p[blockIdx.y];
-    constexpr bool FULL = MODE >= kLinFull, EXACT = MODE == kLinExact;
+    constexpr bool FULL = MODE == kLinFull;
     constexpr int T = 64 * NW, BV = 16 * NT * NW, IT = C / 16, JB = C / 32, KB = KD / 32;
     constexpr int TW = NH == 1 ? NW - 1 : NW;         // waves with tiles of P: the one with the decays has none
     constexpr int NTILE = IT * (IT + 1) / 2, MT = (NTILE + TW - 1) / TW;   // tiles of P, and the most of one wave
-    constexpr int SP = EXACT || PARTS == 3 ? 3 : 2, PP = SP;   // parts of the state and of P in the output
+    constexpr int WP = 3;                             // parts of the state, of P and of the decayed values
     constexpr int NBLK = C == 64 ? 6 : 2, PB = NBLK * 512;
     constexpr int HW = BV / NH, WH = NW / NH;         // columns and waves of one head
     static_assert(C == 64 || C == 32, "chunk");
-    static_assert(NH == 1 || (NH == 2 && !EXACT), "heads");
+    static_assert(NH == 1 || NH == 2, "heads");
+    static_assert(NH * PB <= C * BV || NH == 1, "two heads' third part of P fits where x3 was");
     // bf16 rows come straight into LDS, each tile as soon as the last chunk's readers are
     // done with it: x2 (read to the end) and without a read-out x3 have a second tile, where
-    // that still leaves room for two workgroups on a CU.  The exact output's third part of P
-    // takes that room: there the state goes on before P x3, and x2 is free after it (EARLY).
-    // Two heads' P takes it too: x2 is asked for behind everything else (203 us for 2 x 8192
-    // tokens of 64 heads of 64 with 128 states, 239 us with the state first).
-    // float32 rows are held in registers from one chunk to the next.
-    constexpr bool DMA = PARTS == 1, EARLY = EXACT, TWO2 = DMA && !EXACT && !(FULL && KD == 128 && NH == 2),
-                   TWO3 = DMA && !FULL;
+    // that still leaves room for two workgroups on a CU.  P takes that room at 128 state rows,
+    // and two heads' P at 64: there the state goes on before P x3, and x2 is free after it
+    // (EARLY).  At 128 rows two heads' P takes more than that: its third part goes where x3 was,
+    // and x3 is asked for behind everything else (OVER; 250 us against 263 with one workgroup on
+    // a CU, 2 x 8192 tokens of 64 heads).  float32 rows are held in registers from one chunk to
+    // the next.
+    constexpr bool DMA = PARTS == 1, EARLY = DMA && FULL && (KD == 128 || (KD == 64 && NH == 2)),
+                   OVER = EARLY && KD == 128 && NH == 2, TWO2 = DMA && !EARLY, TWO3 = DMA && !FULL;
+    constexpr int PL = OVER ? WP - 1 : WP;            // parts of P in its own place
     __shared__ __align__(16) uint16_t X2a[PARTS * C * KD], X2b[TWO2 ? C * KD : 8];
     __shared__ __align__(16) uint16_t X3a[PARTS * C * BV], X3b[TWO3 ? C * BV : 8];
     __shared__ __align__(16) uint16_t X1[FULL ? PARTS * C * KD : 8];
-    __shared__ __align__(16) uint16_t PTs[FULL ? NH * PP * PB : 8];   // decayed x1 . x2, per head
+    __shared__ __align__(16) uint16_t PTs[FULL ? NH * PL * PB : 8];   // decayed x1 . x2, per head
     __shared__ Decays<C> decs[2][NH];
     const int tid = threadIdx.x, lane = tid & 63, g4 = lane >> 4, l16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -508,7 +509,7 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
     int at = int(blockIdx.x % per);
     if (per % 8 == 0) at = (at % 8) * (per / 8) + at / 8;
     const int64_t pi = blockIdx.x / per;
-    const int slice = at % p.nslices, h0 = at / p.nslices * NH, hw = wave / WH, h = h0 + hw;   // h: this wave's head
+    const int slice = uniform(at % p.nslices), h0 = uniform(at / p.nslices) * NH, hw = wave / WH, h = h0 + hw;   // h: this wave's head
     const int seq = find_seq(p, pi);
     if (seq < 0) return;
     const Seq sq = seq_range(p, seq);
@@ -524,9 +525,9 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
 
     constexpr int E = PARTS == 1 ? 2 : 4;
     const int c_wave = slice * BV + (wave % WH) * 16 * NT;             // this wave's first column of its head
-    const char* b1 = FULL ? static_cast<const char*>(p.x1) + int64_t(h0 / p.r1) * p.kd * E : nullptr;
-    const char* b2 = static_cast<const char*>(p.x2) + int64_t(h0 / p.r2) * p.kd * E;
-    const char* b3 = static_cast<const char*>(p.x3) + (int64_t(h0 / p.r3) * p.vd + slice * BV) * E;
+    const char* b1 = FULL ? static_cast<const char*>(p.x1) + int64_t(uniform(h0 / p.r1)) * p.kd * E : nullptr;
+    const char* b2 = static_cast<const char*>(p.x2) + int64_t(uniform(h0 / p.r2)) * p.kd * E;
+    const char* b3 = static_cast<const char*>(p.x3) + (int64_t(uniform(h0 / p.r3)) * p.vd + slice * BV) * E;
     const int w3 = p.vd - slice * BV;
     const int64_t pitch1 = p.s1 * E, pitch2 = p.s2 * E, pitch3 = p.s3 * E;
 
@@ -550,7 +551,7 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
         }
     // tiles above the diagonal that share a block with one on it stay zero
     if constexpr (FULL) {
-        for (int i = tid; i < NH * PP * PB / 2; i += T) reinterpret_cast<uint32_t*>(PTs)[i] = 0;
+        for (int i = tid; i < NH * PL * PB / 2; i += T) reinterpret_cast<uint32_t*>(PTs)[i] = 0;
     }
 
     const int64_t nch = (hi - lo + C - 1) / C;
@@ -566,14 +567,14 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
     DecayLane<C> dl;
     const float p_scale = p.wscale * p.oscale;
     float gn = 0.0f;
-    auto decay = [&](int64_t n) {
+    auto decay = [&](int64_t n, int lane) {
         const int64_t t = first_of(n) + (rev ? C - 1 - lane : lane), tg = rev ? t + 1 : t;
         return n < nch && lane < C && t < hi && tg < sq.end ? p.g[tg * p.sg + h] : 0.0f;
     };
     if (dec_wave && nch > 0) {
-        if constexpr (FULL) dl.next(decs[0][hw], decay(0), p.wscale, p.oscale, lane);
-        else dl.ahead(decs[0][hw], decay(0), p.wscale, lane);
-        gn = decay(1);
+        if constexpr (FULL) dl.next(decs[0][hw], decay(0, lane), p.wscale, p.oscale, lane);
+        else dl.ahead(decs[0][hw], decay(0, lane), p.wscale, lane);
+        gn = decay(1, lane);
     }
     Tile<PARTS, C, KD, T> t1, t2;
     Tile<PARTS, C, BV, T, HW> t3;
@@ -608,7 +609,7 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
         uint16_t* const X2 = TWO2 && ODD ? X2b : X2a;
         uint16_t* const X3 = TWO3 && ODD ? X3b : X3a;
         Decays<C>& dec = decs[ODD][hw];
-        uint16_t* const PT = PTs + hw * PP * PB;
+        uint16_t* const PT = PTs + hw * PL * PB;
         const int64_t c0 = first_of(n);
         // the lane as the loop's own value: operand addresses are cheap to form anew, and held
         // across the loop they would take the registers that the state needs
@@ -617,7 +618,7 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
         const int tid = 64 * wave + lane, g4 = lane >> 4, l16 = lane & 15;
         if (ahead) {
             // this chunk's rows; what was stored since they were asked for may still be under way
-            if constexpr (!FULL || (!EARLY && !TWO2))
+            if constexpr (!FULL || OVER)
                 wait_memory<0>();
             else if (p.pairs)
                 wait_memory<2 * IT * NT>();
@@ -651,7 +652,7 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
             if (dec_wave && n + 1 < nch) {
                 if constexpr (FULL) dl.next(decs[!ODD][hw], gn, p.wscale, p.oscale, lane);
                 else dl.ahead(decs[!ODD][hw], gn, p.wscale, lane);
-                gn = decay(n + 2);
+                gn = decay(n + 2, lane);
             }
         };
         // the value rows of this wave's columns
@@ -669,6 +670,7 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
         };
 
         f32x4 acc[IT][NT];
+        uint2 third[OVER ? MT : 1][NH];
         if constexpr (FULL) {
             // ---- P = x1 . x2 under the decays, tiles of 16 x 16 on and below the diagonal
 #pragma unroll
@@ -705,11 +707,12 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
                         const float w = __builtin_amdgcn_exp2f((gi - gj[r]) + (ei - ej[r]));
                         a[r] = j0 + r <= i ? raw[r] * (w * p_scale) : 0.0f;
                     }
-                    uint32_t u[PP], v[PP];
-                    split<PP>(a[0], a[1], u);
-                    split<PP>(a[2], a[3], v);
+                    uint32_t u[WP], v[WP];
+                    split<WP>(a[0], a[1], u);
+                    split<WP>(a[2], a[3], v);
 #pragma unroll
-                    for (int k = 0; k < PP; ++k) *reinterpret_cast<uint2*>(PTs + (hh * PP + k) * PB + o) = uint2{u[k], v[k]};
+                    for (int k = 0; k < PL; ++k) *reinterpret_cast<uint2*>(PTs + (hh * PL + k) * PB + o) = uint2{u[k], v[k]};
+                    if constexpr (OVER) third[mm][hh] = uint2{u[WP - 1], v[WP - 1]};
                 }
             }
             next();
@@ -724,19 +727,19 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
                 for (int x = 0; x < IT * PARTS; ++x)
                     q[x / PARTS][x % PARTS] = row_op<KD>(X1 + (x % PARTS) * C * KD, 16 * (x / PARTS), kb, base);
                 if (PARTS == 1) __builtin_amdgcn_sched_barrier(0);
-                u32x4 sp[NT][SP];
+                u32x4 sp[NT][WP];
 #pragma unroll
                 for (int x = 0; x < 4 * NT; ++x) {
                     const int nt = x >> 2, e = x & 3;
                     const f32x4& s = S[2 * kb + (e >> 1)][nt];
-                    uint32_t w[SP];
-                    split<SP>(s[2 * (e & 1)], s[2 * (e & 1) + 1], w);
+                    uint32_t w[WP];
+                    split<WP>(s[2 * (e & 1)], s[2 * (e & 1) + 1], w);
 #pragma unroll
-                    for (int k = 0; k < SP; ++k) sp[nt][k][e] = w[k];
+                    for (int k = 0; k < WP; ++k) sp[nt][k][e] = w[k];
                 }
 #pragma unroll
                 for (int x = 0; x < IT * NT; ++x)
-                    acc[x / NT][x % NT] = mma_parts<PARTS, SP>(q[x / NT], sp[x % NT], acc[x / NT][x % NT]);
+                    acc[x / NT][x % NT] = mma_parts<PARTS, WP>(q[x / NT], sp[x % NT], acc[x / NT][x % NT]);
             }
 #pragma unroll
             for (int it = 0; it < IT; ++it) {
@@ -760,7 +763,7 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
             }
 #pragma unroll
             for (int jb = 0; jb < JB; ++jb) {
-                u32x4 vp[NT][VP];
+                u32x4 vp[NT][WP];
                 const f32x4 f0 = *reinterpret_cast<const f32x4*>(&dec.out[32 * jb + 8 * g4]);
                 const f32x4 f1 = *reinterpret_cast<const f32x4*>(&dec.out[32 * jb + 8 * g4 + 4]);
 #pragma unroll
@@ -773,10 +776,10 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
                         y += bf_hi(v[jb][nt][i][e]);
                     }
                     const f32x4& f = e < 2 ? f0 : f1;
-                    uint32_t w[VP];
-                    split<VP>(x * f[2 * (e & 1)], y * f[2 * (e & 1) + 1], w);
+                    uint32_t w[WP];
+                    split<WP>(x * f[2 * (e & 1)], y * f[2 * (e & 1) + 1], w);
 #pragma unroll
-                    for (int k = 0; k < VP; ++k) vp[nt][k][e] = w[k];
+                    for (int k = 0; k < WP; ++k) vp[nt][k][e] = w[k];
                 }
                 constexpr int AHEAD = PARTS == 1 ? (EARLY ? 2 : 4) : 1;   // operands in flight
 #pragma unroll
@@ -790,24 +793,41 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
                     if (AHEAD > 1) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                     for (int x = 0; x < AHEAD * NT; ++x)
-                        S[m0 + x / NT][x % NT] = mma_parts<PARTS, VP>(k[x / NT], vp[x % NT], S[m0 + x / NT][x % NT]);
+                        S[m0 + x / NT][x % NT] = mma_parts<PARTS, WP>(k[x / NT], vp[x % NT], S[m0 + x / NT][x % NT]);
                 }
             }
         };
         if constexpr (FULL) {
             lds_barrier();                      // P is there; x1 and x3 have been read
-            // the exact output has no registers left to hold the loads' offsets: kept in scratch
-            // memory they would be waited for behind every load and store under way
+            // no registers are left to hold the loads' offsets there (EARLY): kept in scratch memory
+            // they would be waited for behind every load and store under way
             if (ahead && n + 1 < nch) {
-                if constexpr (EARLY) t3.prepare(tid, pitch3, rev, w3);
-                load3(n + 1, X3);
+                if constexpr (!OVER) {
+                    if constexpr (EARLY) t3.prepare(tid, pitch3, rev, w3);
+                    load3(n + 1, X3);
+                }
                 if constexpr (EARLY) t1.prepare(tid, pitch1, rev, p.kd);
                 load1(n + 1);
             }
+            if constexpr (OVER) {               // P's third part; what lies above the diagonal is x3's still
+#pragma unroll
+                for (int mm = 0; mm < MT; ++mm) {
+                    const int m = wave + TW * mm;
+                    if (m >= NTILE + IT) break;
+                    const int z = m - NTILE;    // of 4: the tiles beside (0, 0) and (2, 2) of either head
+                    const int it = z >= 0 ? z & 2 : m < 1 ? 0 : m < 3 ? 1 : m < 6 ? 2 : 3;
+                    const int jt = z >= 0 ? it + 1 : m - it * (it + 1) / 2;
+                    const int o = p_block(it, jt >> 1) * 512 + at_piece<32>(l16, 2 * (jt & 1) + (g4 >> 1)) + 4 * (g4 & 1);
+#pragma unroll
+                    for (int hh = 0; hh < NH; ++hh)
+                        if (z < 0 || (z & 1) == hh)
+                            *reinterpret_cast<uint2*>(X3 + hh * PB + o) = z < 0 ? third[mm][hh] : uint2{0, 0};
+                }
+            }
             if constexpr (EARLY) {
                 onward();
+                if (OVER || (ahead && n + 1 < nch)) lds_barrier();   // x2 has been read; P is there whole
                 if (ahead && n + 1 < nch) {
-                    lds_barrier();              // x2 has been read
                     t2.prepare(tid, pitch2, rev, p.kd);
                     load2(n + 1, X2);
                 }
@@ -818,11 +838,12 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
             for (int jb = 0; jb < JB; ++jb)
 #pragma unroll
                 for (int it = 2 * jb; it < IT; ++it) {
-                    u32x4 q[PP];
+                    u32x4 q[WP];
 #pragma unroll
-                    for (int k = 0; k < PP; ++k) q[k] = row_op<32>(PT + k * PB + p_block(it, jb) * 512, 0, 0, base_p);
+                    for (int k = 0; k < WP; ++k)
+                        q[k] = row_op<32>((k < PL ? PT + k * PB : X3 + hw * PB) + p_block(it, jb) * 512, 0, 0, base_p);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) acc[it][nt] = mma_parts<PP, PARTS>(q, v[jb][nt], acc[it][nt]);
+                    for (int nt = 0; nt < NT; ++nt) acc[it][nt] = mma_parts<WP, PARTS>(q, v[jb][nt], acc[it][nt]);
                 }
             if constexpr (!EARLY) onward();
         } else {
@@ -876,10 +897,11 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
                 }
             }
         }
-        if constexpr (DMA && FULL && !EARLY && !TWO2) {
+        if constexpr (OVER) {
             if (ahead && n + 1 < nch) {
-                lds_barrier();                  // x2 has been read
-                load2(n + 1, X2);
+                lds_barrier();                  // P has been read
+                t3.prepare(tid, pitch3, rev, w3);
+                load3(n + 1, X3);
             }
         }
     };
@@ -926,28 +948,22 @@ template <int MODE> inline bool launch_pass(const ssm_detail::LinattnPasses& q, 
     // two heads in a workgroup share loads and products, but while each head finds a CU of its
     // own four waves of one SIMD each are sooner done than eight (three float32 prompts of up to
     // 130 tokens and 6 heads 26.5 us against 30.7; 2 x 8192 tokens of 64 heads 243 against 208)
-    const bool two = MODE != ssm_detail::kLinExact && p.r1 % 2 == 0 && p.r2 % 2 == 0 && int64_t(p.npieces) * p.H > kCus;
+    const bool two = p.r1 % 2 == 0 && p.r2 % 2 == 0 && int64_t(p.npieces) * p.H > kCus;
     const int shape = ssm_detail::linattn_shape(p.vd, two);
     const int64_t blocks = int64_t(p.npieces) * (shape == ssm_detail::kTwoHeads ? p.H / 2 : p.H) * p.nslices;
     const dim3 grid(static_cast<uint32_t>(blocks), count), block(shape == ssm_detail::kNarrow ? 256 : 512);
     // float32 rows take three times the LDS: chunks of 32 keep two workgroups on a CU
-    constexpr bool EXACT = MODE == ssm_detail::kLinExact;
     const auto start = [&](auto* kernel) { launch_kernel(kernel, grid, block, 0, s, q); };
 #define SSM_LIN_CASE(K, NW, NH)                                                                     \
     do {                                                                                            \
-        if constexpr (EXACT) {                                                                      \
-            start(linattn_pass_kernel<1, K, NW, 1, 64, MODE, NH, 3>);                               \
-        } else {                                                                                    \
-            if (f32) start(linattn_pass_kernel<3, K, NW, 1, 32, MODE, NH, 3>);                      \
-            else if (p.exact) start(linattn_pass_kernel<1, K, NW, 1, 64, MODE, NH, 3>);             \
-            else start(linattn_pass_kernel<1, K, NW, 1, 64, MODE, NH, 2>);                          \
-        }                                                                                           \
+        if (f32) start(linattn_pass_kernel<3, K, NW, 1, 32, MODE, NH>);                             \
+        else start(linattn_pass_kernel<1, K, NW, 1, 64, MODE, NH>);                                 \
     } while (0)
 #define SSM_LIN_WAVES(K)                                                                            \
     do {                                                                                            \
         if (shape == ssm_detail::kWide) SSM_LIN_CASE(K, 8, 1);                                      \
         else if (shape == ssm_detail::kNarrow) SSM_LIN_CASE(K, 4, 1);                               \
-        else if constexpr (!EXACT) SSM_LIN_CASE(K, 8, 2);                                           \
+        else SSM_LIN_CASE(K, 8, 2);                                                                 \
     } while (0)
     if (p.kd <= 64)
         SSM_LIN_WAVES(64);

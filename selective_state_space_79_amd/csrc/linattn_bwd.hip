@@ -9,7 +9,7 @@
 // token to the next dg changes by
 //   dg_{t+1} = dg_t + k_t . dk_t - q_t . dq_t
 // A running sum of these carries the error of every read that came and went.  So dq and dk
-// are formed to float32 here (kLinExact), and the sum starts afresh at each piece from
+// are formed to float32 here, and the sum starts afresh at each piece from
 // <S, dS>, with what it misses at the next piece's start spread over the piece.  dq and dk
 // per head go through float32 arrays, where the heads that share a row are added up, the row
 // products taken and the outputs rounded in one more pass.
@@ -318,10 +318,6 @@ inline int make_grad_plan(const ssm_linattn_dims* d, bool packed, GradPlan* pl) 
 }  // namespace la
 }  // namespace
 
-bool ssm_detail::launch_linattn_exact(const LinattnPasses& p, int count, bool f32, hipStream_t s) {
-    return f32 ? launch_linattn_pass(p, count, true, kLinFull, s) : la::launch_pass<kLinExact>(p, count, false, s);
-}
-
 extern "C" {
 
 size_t ssm_linattn_bwd_workspace_bytes(const ssm_linattn_dims* dims) {
@@ -396,7 +392,6 @@ int ssm_linattn_bwd(const void* q, const void* k, const void* v, const float* g,
     base.nseq = static_cast<int32_t>(d.nseq); base.nslots = base.nseq;
     base.r1 = base.r2 = base.r3 = 1;
     base.wscale = base.oscale = 1.0f;
-    base.exact = gr.dg || gr.ds0;
     base.wide = wide_rows(q, z.q, d.dk, z.e) && wide_rows(k, z.k, d.dk, z.e) && wide_rows(v, z.v, d.dv, z.e) &&
                 wide_rows(dout, z.o, d.dv, z.e);
 
@@ -414,7 +409,7 @@ int ssm_linattn_bwd(const void* q, const void* k, const void* v, const float* g,
     LinattnPass pq = base;   // dq = (do, v, k) from S
     pq.x1 = dout; pq.s1 = z.o; pq.x2 = v; pq.s2 = z.v; pq.x3 = k; pq.s3 = z.k; pq.r3 = rep;
     pq.kd = static_cast<int32_t>(d.dv); pq.vd = static_cast<int32_t>(d.dk); pq.nslices = static_cast<int32_t>(pl.slices_q);
-    pq.s_in = s0; pq.st_t = 1; pq.carry = fwd; pq.oscale = d.scale; pq.exact = 0;
+    pq.s_in = s0; pq.st_t = 1; pq.carry = fwd; pq.oscale = d.scale;
     pq.out = apart ? static_cast<void*>(wq) : gr.dq; pq.out_f32 = apart; pq.so = d.nheads * d.dk;
     pq.pairs = !apart && pair_rows(gr.dq, pq.so, d.dk);
     LinattnPass pk = pq;     // dk = (v, do, q) from dS
@@ -422,17 +417,14 @@ int ssm_linattn_bwd(const void* q, const void* k, const void* v, const float* g,
     pk.s_in = ds_last; pk.carry = rev; pk.oscale = 1.0f; pk.wscale = d.scale; pk.reverse = 1;
     pk.out = apart ? static_cast<void*>(wkk) : gr.dk; pk.pairs = !apart && pair_rows(gr.dk, pk.so, d.dk);
     LinattnPass pv = sr;     // dv = (k, q, do) from dS
-    pv.x1 = k; pv.s1 = z.k; pv.r1 = rep; pv.out = gr.dv; pv.so = wv; pv.s_out = gr.ds0; pv.exact = gr.ds0 != nullptr; pv.pairs = pair_rows(gr.dv, wv, d.dv);
+    pv.x1 = k; pv.s1 = z.k; pv.r1 = rep; pv.out = gr.dv; pv.so = wv; pv.s_out = gr.ds0; pv.pairs = pair_rows(gr.dv, wv, d.dv);
 
     launch_error = hipSuccess;
     if (pl.pieced) {
         launch_linattn_pass({{sf, sr}}, 2, f32, kLinStates, s);
         launch_linattn_carry({{sf, sr}}, 2, s);
     }
-    if (gr.dg)
-        launch_linattn_exact({{pq, pk}}, 2, f32, s);
-    else
-        launch_linattn_pass({{pq, pk}}, 2, f32, kLinFull, s);
+    launch_linattn_pass({{pq, pk}}, 2, f32, kLinFull, s);
     launch_linattn_pass({{pv, pv}}, 1, f32, kLinFull, s);
     if (apart) {
         const GroupArgs ga = {wq, wkk, q, k, gr.dq, gr.dk, gr.dg ? f : nullptr, z.q, z.k, rep, static_cast<int32_t>(d.dk),

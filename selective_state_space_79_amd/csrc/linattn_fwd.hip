@@ -284,7 +284,6 @@ int ssm_linattn_fwd(const void* q, const void* k, const void* v, const float* g,
     p.npieces = static_cast<int32_t>(pl.npieces); p.pieced = pl.pieced;
     p.wide = wide_rows(q, z.q, d.dk, z.e) && wide_rows(k, z.k, d.dk, z.e) && wide_rows(v, z.v, d.dv, z.e);
     p.pairs = pair_rows(o, z.o, d.dv);
-    p.exact = s_last != nullptr;
     p.wscale = 1.0f; p.oscale = d.scale;
     const bool f32 = d.io_dtype == SSM_F32;
     hipStream_t s = static_cast<hipStream_t>(stream);
