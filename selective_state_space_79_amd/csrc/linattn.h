@@ -237,6 +237,22 @@ __device__ inline void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_b
 // and columns past the row's end read as zero and are not written.
 typedef __amdgpu_buffer_rsrc_t Rsrc;
 constexpr uint32_t kPast = 0x80000000u;   // an offset past every window (windows are < 2^31)
+constexpr int64_t kMostHeads = 32767;
+static_assert(64 * kMostHeads * SSM_LINATTN_MAX_DIM * 4 < int64_t(kPast), "a chunk's widest window: float32 rows of all heads");
+
+// Byte offsets of a lane's outputs in a chunk's window: value (4 g4 + r) of the chunk's c tokens,
+// in order of time or against it, at byte `at` of its row.  Columns that the head does not have
+// (`on` false) lie kPast behind their own row, wherever the row steps lead: kPast + [0, window),
+// which neither falls back into the window nor passes 2^32.
+struct StoreRows {
+    int pitch, lane0;
+    __host__ __device__ inline StoreRows(int64_t row_bytes, bool rev, int c, int g4) {
+        pitch = rev ? -int(row_bytes) : int(row_bytes);
+        lane0 = int(row_bytes) * (rev ? c - 1 : 0) + 4 * g4 * pitch;
+    }
+    __host__ __device__ inline uint32_t first(bool on, int at) const { return uint32_t(lane0) + (on ? uint32_t(at) : kPast); }
+    __host__ __device__ inline uint32_t row(int r) const { return uint32_t(r * pitch); }
+};
 
 __device__ inline Rsrc rows_rsrc(const char* row0, int64_t pitch, int64_t rows, int c) {
     const int64_t n = rows < c ? rows : c;
@@ -856,17 +872,16 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
             const int oe = PARTS == 3 || p.out_f32 ? 4 : 2;
             const int64_t pitch64 = p.so * oe;
             const Rsrc ro = rows_rsrc(static_cast<char*>(p.out) + c0 * pitch64 + int64_t(h) * p.vd * oe, pitch64, hi - c0, C);
-            const int pitch = rev ? -int(pitch64) : int(pitch64);
-            const int lane0 = int(pitch64) * (rev ? C - 1 : 0) + 4 * g4 * pitch;
+            const StoreRows to(pitch64, rev, C, g4);
             if (oe == 4) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     const int col = c_wave + 16 * nt + l16;
-                    const uint32_t o0 = col < p.vd ? lane0 + 4 * col : kPast;
+                    const uint32_t o0 = to.first(col < p.vd, 4 * col);
 #pragma unroll
                     for (int x = 0; x < 4 * IT; ++x)
                         __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[x >> 2][nt][x & 3]), ro,
-                                                              o0 + uint32_t((16 * (x >> 2) + (x & 3)) * pitch), 0, 0);
+                                                              o0 + to.row(16 * (x >> 2) + (x & 3)), 0, 0);
                 }
             } else if (p.pairs) {
                 // neighbouring lanes swap one row for another: two columns of one row each
@@ -875,25 +890,25 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     const int col = c_wave + 16 * nt + (l16 & ~1);
-                    const uint32_t o0 = col < p.vd ? lane0 + (odd ? pitch : 0) + 2 * col : kPast;
+                    const uint32_t o0 = to.first(col < p.vd, 2 * col) + (odd ? to.row(1) : 0u);
 #pragma unroll
                     for (int it = 0; it < IT; ++it)
 #pragma unroll
                         for (int r = 0; r < 4; r += 2) {
                             const uint32_t own = pack2(acc[it][nt][r], acc[it][nt][r + 1]);
                             __builtin_amdgcn_raw_buffer_store_b32(__builtin_amdgcn_perm(swap1(own), own, pick), ro,
-                                                                  o0 + uint32_t((16 * it + r) * pitch), 0, 0);
+                                                                  o0 + to.row(16 * it + r), 0, 0);
                         }
                 }
             } else {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     const int col = c_wave + 16 * nt + l16;
-                    const uint32_t o0 = col < p.vd ? lane0 + 2 * col : kPast;
+                    const uint32_t o0 = to.first(col < p.vd, 2 * col);
 #pragma unroll
                     for (int x = 0; x < 4 * IT; ++x)
                         __builtin_amdgcn_raw_buffer_store_b16(IOT<uint16_t>::from_f32(acc[x >> 2][nt][x & 3]), ro,
-                                                              o0 + uint32_t((16 * (x >> 2) + (x & 3)) * pitch), 0, 0);
+                                                              o0 + to.row(16 * (x >> 2) + (x & 3)), 0, 0);
                 }
             }
         }
@@ -989,7 +1004,7 @@ inline int check_dims(const ssm_linattn_dims* d, Sizes* z) {
     if (d->tokens < 1 || d->nseq < 1 || d->nheads < 1 || d->kheads < 1 || d->dk < 1 || d->dv < 1) return SSM_ERR_EMPTY;
     if (d->io_dtype != SSM_F32 && d->io_dtype != SSM_BF16) return SSM_ERR_DTYPE;
     if (d->nheads % d->kheads != 0 || d->dk > SSM_LINATTN_MAX_DIM || d->dv > SSM_LINATTN_MAX_DIM) return SSM_ERR_DIMS;
-    if (d->nseq > 65535 || d->nheads > 32767 || d->tokens > (int64_t(1) << 31) - 1) return SSM_ERR_DIMS;
+    if (d->nseq > 65535 || d->nheads > kMostHeads || d->tokens > (int64_t(1) << 31) - 1) return SSM_ERR_DIMS;
     if (d->head_decay != 0 && d->head_decay != 1) return SSM_ERR_DIMS;
     if (d->reserved != 0) return SSM_ERR_DIMS;
     if (d->piece_len < 0 || d->piece_len % 64 != 0 || d->piece_len > (int64_t(1) << 31)) return SSM_ERR_DIMS;
