@@ -367,10 +367,8 @@ def selective_scan_fwd(u, delta, A, B, C, D=None, z=None, dt_bias=None, *, h0=No
         h_last = torch.empty((u.shape[0], u.shape[1], B.shape[1]), dtype=torch.float32, device=u.device)
     need = ssm_selective_scan_workspace_bytes(dims)
     if need:
-        if workspace is None or workspace.numel() * workspace.element_size() < need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=u.device)
+        workspace, dims.workspace_bytes = blocks._workspace(need, workspace, u.device)
         dims.workspace = workspace.data_ptr()
-        dims.workspace_bytes = workspace.numel() * workspace.element_size()
     if ckpt is not None:
         st = ssm_selective_scan_fwd_ckpt(u, delta, A, B, C, D, z, dt_bias, h0, out, h_last, ckpt, dims, stream)
         if st != SSM_OK:
@@ -460,10 +458,8 @@ def selective_scan_bwd(u, delta, A, B, C, D=None, z=None, dt_bias=None, *, dy, h
     need = ssm_selective_scan_bwd_workspace_bytes(dims)
     if need == 0:
         raise SsmError(SSM_ERR_DIMS, "ssm_selective_scan_bwd_workspace_bytes")
-    if workspace is None or workspace.numel() * workspace.element_size() < need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=u.device)
+    workspace, dims.workspace_bytes = blocks._workspace(need, workspace, u.device)
     dims.workspace = workspace.data_ptr()
-    dims.workspace_bytes = workspace.numel() * workspace.element_size()
     g = SsmGrads(*[out[k].data_ptr() if k in out else None for k, _ in SsmGrads._fields_])
     if ckpt is not None:
         st = ssm_selective_scan_bwd_ckpt(u, delta, A, B, C, D, z, dt_bias, h0, dy, dh_last, ckpt, g, dims, stream)
@@ -524,10 +520,8 @@ def selective_scan_fwd_conv(x, conv_weight, conv_bias, delta, A, B, C, D=None, z
     u = torch.empty_like(x) if return_u else None
     need = ssm_selective_scan_workspace_bytes(dims)
     if need:
-        if workspace is None or workspace.numel() * workspace.element_size() < need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace, dims.workspace_bytes = blocks._workspace(need, workspace, x.device)
         dims.workspace = workspace.data_ptr()
-        dims.workspace_bytes = workspace.numel() * workspace.element_size()
     conv = _conv_struct(conv_weight, conv_bias, silu)
     st = ssm_selective_scan_fwd_conv(x, conv, conv_state, delta, A, B, C, D, z, dt_bias, h0, u, out, h_last, dims,
                                      stream)
@@ -612,10 +606,8 @@ def ssd_fwd(u, delta, A, B, C, D=None, z=None, dt_bias=None, *, h0=None, return_
     h_last = torch.empty((batch, dim, B.shape[1]), dtype=torch.float32, device=u.device) if return_state else None
     need = ssm_ssd_fwd_workspace_bytes(dims)
     if need:
-        if workspace is None or workspace.numel() * workspace.element_size() < need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=u.device)
+        workspace, dims.workspace_bytes = blocks._workspace(need, workspace, u.device)
         dims.workspace = workspace.data_ptr()
-        dims.workspace_bytes = workspace.numel() * workspace.element_size()
     st = ssm_ssd_fwd(u, delta, A, B, C, D, z, dt_bias, h0, out, h_last, dims, stream)
     if st != SSM_OK:
         raise SsmError(st, "ssm_ssd_fwd")

@@ -251,10 +251,15 @@ def _on(stream):
 
 
 def _workspace(need, given, device):
+    """The caller's workspace, or a new one if that is too small, and its bytes.  A view whose
+    elements are strided or expanded is not memory of its own size."""
     import torch
 
     if need == 0:
         return None, 0
+    if given is not None:
+        _need(given.device == device, f"workspace must be on {device}")
+        _need(given.is_contiguous(), "workspace must be contiguous")
     if given is None or given.numel() * given.element_size() < need:
         given = torch.empty(need, dtype=torch.uint8, device=device)
     return given, given.numel() * given.element_size()
