@@ -44,3 +44,50 @@ def test_views_are_refused_by_every_call():
             call(bad)
         with pytest.raises(ValueError, match="must be on cuda"):
             call(torch.empty(1 << 26, dtype=torch.uint8))
+
+
+def test_stated_sizes_are_enough_and_needed():
+    """On fake addresses: with the stated bytes the packed and the dense call both get past the
+    workspace check (to the overlap that is set up behind it), with one byte less at least one
+    does not."""
+    from test_blocks_host import BWD, FWD, at, bwd, fwd, grads, lin
+
+    assert BWD and FWD
+    cu = {"-cu": at(30)}
+    for tokens, nseq in ((4096, 1), (4096, 4), (8192, 8), (100, 2), (64, 64), (131072, 1), (8191, 1), (300, 100), (65, 5)):
+        for nheads, kheads, dk, dv in ((8, 2, 128, 128), (64, 1, 128, 64), (3, 3, 33, 70), (2, 2, 256, 256)):
+            for piece in (0, 64, 1024):
+                for size, call in ((ssm.ssm_linattn_fwd_workspace_bytes, lambda d, **c: fwd(d, o=at(0), **c)),
+                                   (ssm.ssm_linattn_bwd_workspace_bytes, lambda d, **c: bwd(d, grads(dk=at(20)), **c))):
+                    make = lambda: lin(tokens=tokens, nseq=nseq, nheads=nheads, kheads=kheads, dk=dk, dv=dv,   # noqa: E731
+                                       piece_len=piece)
+                    need = size(make())
+                    for less in ([0, 1] if need else [0]):
+                        got = []
+                        for change in (cu, {}):
+                            d = make()
+                            d.workspace, d.workspace_bytes = at(40), need - less
+                            got.append(call(d, **change))
+                        if less:
+                            assert ssm.SSM_ERR_WORKSPACE in got, (tokens, nseq, piece)
+                        else:
+                            assert got == [ssm.SSM_ERR_ALIAS] * 2, (tokens, nseq, piece, got)
+
+
+def test_stated_sizes_of_the_norms():
+    from test_blocks_host import ADD_B, GATED_B, added, at, call, gated
+
+    for rows in (1, 7, 5000, 1 << 20):
+        for n in (1, 64, 200, 2048, 8192, 16384):
+            for groups in (1, 3):
+                for shared in (0, 1):
+                    size = ssm.ssm_gated_norm_bwd_workspace_bytes(gated(rows=rows, ngroups=groups, group=n, shared=shared))
+                    d = gated(rows=rows, ngroups=groups, group=n, shared=shared, ws=at(40), bytes_=size)
+                    assert call("ssm_gated_norm_bwd", d, GATED_B, dx=at(0)) == ssm.SSM_ERR_ALIAS
+                    d.workspace_bytes = size - 1
+                    assert call("ssm_gated_norm_bwd", d, GATED_B, dx=at(0)) == ssm.SSM_ERR_WORKSPACE
+            size = ssm.ssm_add_norm_bwd_workspace_bytes(added(rows=rows, dim=n))
+            d = added(rows=rows, dim=n, ws=at(40), bytes_=size)
+            assert call("ssm_add_norm_bwd", d, ADD_B, dx=at(1)) == ssm.SSM_ERR_ALIAS
+            d.workspace_bytes = size - 1
+            assert call("ssm_add_norm_bwd", d, ADD_B, dx=at(1)) == ssm.SSM_ERR_WORKSPACE
