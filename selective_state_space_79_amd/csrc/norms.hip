@@ -563,34 +563,41 @@ __global__ void __launch_bounds__(block_threads<TPG>(), 4) add_norm_bwd_kernel(A
 
 // Sums `count` partial rows of n values, in a fixed order: 16 columns x 64 rows a workgroup,
 // eight rows of a thread under way at once.  Plane b of the grid's y goes to out0, out1, out2.
+// The columns go round over at most 2^20 workgroups (a grid has fewer than 2^32 threads).
 constexpr int kSumLanes = 64;
+inline uint32_t sum_blocks(int64_t n) {
+    const int64_t b = cdiv(n, 16), most = int64_t(1) << 20;
+    return static_cast<uint32_t>(b < most ? b : most);
+}
 __global__ void __launch_bounds__(16 * kSumLanes) sum_rows_kernel(const float* part, int64_t count, int64_t n,
                                                                   float* out0, float* out1, float* out2) {
     __shared__ float s[kSumLanes][16];
     float* out = blockIdx.y == 0 ? out0 : blockIdx.y == 1 ? out1 : out2;
     if (!out) return;
     const int c = threadIdx.x & 15, r = threadIdx.x >> 4;
-    const int64_t col = int64_t(blockIdx.x) * 16 + c;
-    const float* q = part + blockIdx.y * count * n + col;
-    float v = 0.0f;
-    if (col < n) {
-        int64_t i = r;
-        for (; i + 7 * kSumLanes < count; i += 8 * kSumLanes) {
-            float x[8];
+    for (int64_t c0 = int64_t(blockIdx.x) * 16; c0 < n; c0 += int64_t(gridDim.x) * 16) {
+        const int64_t col = c0 + c;
+        const float* q = part + blockIdx.y * count * n + col;
+        float v = 0.0f;
+        if (col < n) {
+            int64_t i = r;
+            for (; i + 7 * kSumLanes < count; i += 8 * kSumLanes) {
+                float x[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = q[(i + k * kSumLanes) * n];
+                for (int k = 0; k < 8; ++k) x[k] = q[(i + k * kSumLanes) * n];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v += x[k];
+                for (int k = 0; k < 8; ++k) v += x[k];
+            }
+            for (; i < count; i += kSumLanes) v += q[i * n];
         }
-        for (; i < count; i += kSumLanes) v += q[i * n];
-    }
-    s[r][c] = v;
-    __syncthreads();
-    for (int d = kSumLanes / 2; d > 0; d >>= 1) {
-        if (r < d) s[r][c] += s[r + d][c];
+        s[r][c] = v;
         __syncthreads();
+        for (int d = kSumLanes / 2; d > 0; d >>= 1) {
+            if (r < d) s[r][c] += s[r + d][c];
+            __syncthreads();
+        }
+        if (r == 0 && col < n) out[col] = s[0][c];
     }
-    if (r == 0 && col < n) out[col] = s[0][c];
 }
 
 // ---------------------------------------------------------------- host
@@ -783,7 +790,7 @@ int ssm_gated_norm_bwd(const void* x, const void* z, const float* w, const void*
     ssm_detail::launch_error = hipSuccess;
     gated(a, d, tpg, blocks, true, s);
     const int64_t n = d.shared_weight ? d.group : dim;
-    launch_kernel(sum_rows_kernel, dim3(static_cast<uint32_t>(cdiv(n, 16))), dim3(16 * kSumLanes), 0, s, a.part,
+    launch_kernel(sum_rows_kernel, dim3(sum_blocks(n)), dim3(16 * kSumLanes), 0, s, a.part,
                   d.shared_weight ? blocks : lanes, n, dw, static_cast<float*>(nullptr), static_cast<float*>(nullptr));
     return ssm_detail::launch_error == hipSuccess ? SSM_OK : SSM_ERR_HIP;
 }
@@ -865,7 +872,7 @@ int ssm_add_norm_bwd(const void* x, const void* r, const float* scale, const flo
     hipStream_t s = static_cast<hipStream_t>(stream);
     ssm_detail::launch_error = hipSuccess;
     add(a, d, tpg, blocks, true, s);
-    launch_kernel(sum_rows_kernel, dim3(static_cast<uint32_t>(cdiv(d.dim, 16)), 3), dim3(16 * kSumLanes), 0, s, a.part, blocks,
+    launch_kernel(sum_rows_kernel, dim3(sum_blocks(d.dim), 3), dim3(16 * kSumLanes), 0, s, a.part, blocks,
                   d.dim, dw, scale ? dscale : nullptr, post ? dpost : nullptr);
     return ssm_detail::launch_error == hipSuccess ? SSM_OK : SSM_ERR_HIP;
 }
