@@ -544,7 +544,7 @@ typedef struct ssm_gated_norm_dims {
     int32_t io_dtype;
     int32_t gate_first;
     int32_t shared_weight;
-    float eps;         /* > 0 */
+    float eps;         /* 2^-126 (the least normal float32) or more, finite */
     void* workspace;   /* backward: 256-byte aligned device memory */
     size_t workspace_bytes;
 } ssm_gated_norm_dims;
@@ -572,7 +572,7 @@ typedef struct ssm_add_norm_dims {
     int64_t x_stride, res_stride, r_stride, y_stride; /* elements between rows; 0: packed */
     int32_t io_dtype;
     int32_t res_dtype;
-    float eps;         /* > 0 */
+    float eps;         /* 2^-126 (the least normal float32) or more, finite */
     int32_t reserved;  /* must be 0 */
     void* workspace;   /* backward: 256-byte aligned device memory */
     size_t workspace_bytes;

@@ -484,7 +484,7 @@ def _gated_dims(x, z, weight, group_size, gate_first, eps):
 def gated_norm_fwd(x, z, weight, *, group_size=None, gate_first=True, eps=1e-5, out=None, stream=None):
     """RMS norm over groups of x's last dimension with a SiLU gate: norm(x SiLU(z)) weight
     with gate_first, else norm(x) weight SiLU(z); z may be None.  weight: float32 (dim,), or
-    (group_size,) for every group.  out may be x or z.  Returns y, x's shape and dtype."""
+    (group_size,) for every group; eps: 2^-126 or more.  out may be x or z.  Returns y, x's shape and dtype."""
     import torch
 
     _device(x, z, weight, out)
@@ -546,8 +546,8 @@ def add_norm_fwd(x, residual, weight, *, scale=None, post_weight=None, eps=1e-5,
                  stream=None):
     """r = residual + scale * (x, or with post_weight its RMS norm); y = the RMS norm of r
     with weight.  residual: x's dtype or float32, or None (zeros; residual_out then tells
-    r's dtype, else x's); scale, post_weight, weight: float32 (dim,).  residual_out may be
-    residual.  Returns (y, r)."""
+    r's dtype, else x's); scale, post_weight, weight: float32 (dim,); eps: 2^-126 or more.
+    residual_out may be residual.  Returns (y, r)."""
     import torch
 
     _device(x, residual, weight, scale, post_weight, residual_out, out)

@@ -687,6 +687,9 @@ inline void add(const AddArgs& a, const ssm_add_norm_dims& d, int tpg, int64_t b
     }
 }
 
+// The reciprocal square root takes numbers below 2^-126 for zero: a row of zeros would turn NaN.
+inline bool good_eps(float eps) { return eps >= 1.17549435e-38f && eps < 3.4e38f; }
+
 inline int check(const ssm_gated_norm_dims* d) {
     if (!d) return SSM_ERR_NULL;
     if (d->rows < 1 || d->ngroups < 1 || d->group < 1) return SSM_ERR_EMPTY;
@@ -698,7 +701,7 @@ inline int check(const ssm_gated_norm_dims* d) {
     for (const int64_t s : {d->x_stride, d->z_stride, d->y_stride})
         if (s != 0 && (s < dim || s > lim / d->rows)) return SSM_ERR_DIMS;
     if ((d->gate_first != 0 && d->gate_first != 1) || (d->shared_weight != 0 && d->shared_weight != 1)) return SSM_ERR_DIMS;
-    if (!(d->eps > 0.0f) || !(d->eps < 3.4e38f)) return SSM_ERR_DIMS;
+    if (!good_eps(d->eps)) return SSM_ERR_DIMS;
     return SSM_OK;
 }
 
@@ -711,7 +714,7 @@ inline int check(const ssm_add_norm_dims* d) {
     if (d->dim > SSM_NORM_MAX_DIM || d->rows > lim / d->dim || d->reserved != 0) return SSM_ERR_DIMS;
     for (const int64_t s : {d->x_stride, d->res_stride, d->r_stride, d->y_stride})
         if (s != 0 && (s < d->dim || s > lim / d->rows)) return SSM_ERR_DIMS;
-    if (!(d->eps > 0.0f) || !(d->eps < 3.4e38f)) return SSM_ERR_DIMS;
+    if (!good_eps(d->eps)) return SSM_ERR_DIMS;
     return SSM_OK;
 }
 
