@@ -52,10 +52,9 @@ struct LinattnPasses {
     LinattnPass p[2];
 };
 
-// The launches return false for sizes that no kernel covers (nothing launched).
 // kLinStates: the pieces' own end states; kLinFull: the outputs.
 enum LinattnMode { kLinStates = 0, kLinFull = 1 };
-bool launch_linattn_pass(const LinattnPasses& p, int count, bool f32, LinattnMode mode, hipStream_t s);
+void launch_linattn_pass(const LinattnPasses& p, int count, bool f32, LinattnMode mode, hipStream_t s);
 void launch_linattn_carry(const LinattnPasses& p, int count, hipStream_t s);
 // How a pass over vd columns is cut: 128 columns of a head to a workgroup, 64, or two heads
 // of up to 64 that share x1 and x2
@@ -485,14 +484,14 @@ __device__ constexpr int p_block(int it, int jb) { return it < 2 ? it : 2 * it -
 // goes into the products in three bf16 parts, which hold a float32 whole.  Two parts would take
 // a fifth less of either unit (131072 tokens of 16 heads 776 us against 860) and leave out up to
 // 2^-17 of each operand: outputs where terms cancel show that.
-constexpr int pass_waves(int KD, int NW, int NT) { return KD == 256 ? NW / 4 : NW / 2; }   // per SIMD
+constexpr int pass_waves(int KD, int NW) { return KD == 256 ? NW / 4 : NW / 2; }   // per SIMD
 
-template <int PARTS, int KD, int NW, int NT, int C, int MODE, int NH>
-__global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_kernel(ssm_detail::LinattnPasses passes) {
+template <int PARTS, int KD, int NW, int C, int MODE, int NH>
+__global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW)) linattn_pass_kernel(ssm_detail::LinattnPasses passes) {
     using namespace ssm_detail;
     const LinattnPass& p = passes.p[blockIdx.y];
     constexpr bool FULL = MODE == kLinFull;
-    constexpr int T = 64 * NW, BV = 16 * NT * NW, IT = C / 16, JB = C / 32, KB = KD / 32;
+    constexpr int T = 64 * NW, BV = 16 * NW, IT = C / 16, JB = C / 32, KB = KD / 32;
     constexpr int TW = NH == 1 ? NW - 1 : NW;         // waves with tiles of P: the one with the decays has none
     constexpr int NTILE = IT * (IT + 1) / 2, MT = (NTILE + TW - 1) / TW;   // tiles of P, and the most of one wave
     constexpr int WP = 3;                             // parts of the state, of P and of the decayed values
@@ -540,7 +539,7 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
     const bool rev = p.reverse;
 
     constexpr int E = PARTS == 1 ? 2 : 4;
-    const int c_wave = slice * BV + (wave % WH) * 16 * NT;             // this wave's first column of its head
+    const int c_wave = slice * BV + (wave % WH) * 16;             // this wave's first column of its head
     const char* b1 = FULL ? static_cast<const char*>(p.x1) + int64_t(uniform(h0 / p.r1)) * p.kd * E : nullptr;
     const char* b2 = static_cast<const char*>(p.x2) + int64_t(uniform(h0 / p.r2)) * p.kd * E;
     const char* b3 = static_cast<const char*>(p.x3) + (int64_t(uniform(h0 / p.r3)) * p.vd + slice * BV) * E;
@@ -548,7 +547,7 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
     const int64_t pitch1 = p.s1 * E, pitch2 = p.s2 * E, pitch3 = p.s3 * E;
 
     // ------------------------------------------------ starting state
-    f32x4 S[2 * KB][NT];
+    f32x4 S[2 * KB];
     const int64_t rs = p.st_t ? 1 : p.vd, cs = p.st_t ? p.kd : 1;
     const int64_t ssz = int64_t(p.kd) * p.vd;
     const float* src = nullptr;
@@ -561,9 +560,9 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
 #pragma unroll
     for (int m = 0; m < 2 * KB; ++m)
 #pragma unroll
-        for (int x = 0; x < 4 * NT; ++x) {
-            const int nt = x >> 2, r = x & 3, row = 32 * (m >> 1) + 8 * g4 + 4 * (m & 1) + r, col = c_wave + 16 * nt + l16;
-            S[m][nt][r] = src && row < p.kd && col < p.vd ? src[row * rs + col * cs] : 0.0f;
+        for (int r = 0; r < 4; ++r) {
+            const int row = 32 * (m >> 1) + 8 * g4 + 4 * (m & 1) + r, col = c_wave + l16;
+            S[m][r] = src && row < p.kd && col < p.vd ? src[row * rs + col * cs] : 0.0f;
         }
     // tiles above the diagonal that share a block with one on it stay zero
     if constexpr (FULL) {
@@ -637,9 +636,9 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
             if constexpr (!FULL || OVER)
                 wait_memory<0>();
             else if (p.pairs)
-                wait_memory<2 * IT * NT>();
+                wait_memory<2 * IT>();
             else
-                wait_memory<4 * IT * NT>();
+                wait_memory<4 * IT>();
             lds_barrier();
         } else {
             lds_barrier();                      // the last chunk's readers are done
@@ -672,20 +671,17 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
             }
         };
         // the value rows of this wave's columns
-        const int w0 = wave * 16 * NT;           // this wave's first column of the tile
-        static_assert(NT == 1, "one tile of columns a wave");
+        const int w0 = wave * 16;                // this wave's first column of the tile
         const uint32_t base3 = col_base<BV, 0>(w0, lane), base2 = col_base<KD, 1>(0, lane), base = row_base<KD>(lane);
-        u32x4 v[JB][NT][PARTS];
+        u32x4 v[JB][PARTS];
         auto values = [&] {
 #pragma unroll
             for (int jb = 0; jb < JB; ++jb)
 #pragma unroll
-                for (int x = 0; x < NT * PARTS; ++x)
-                    v[jb][x / PARTS][x % PARTS] =
-                        col_op<BV>(X3 + (x % PARTS) * C * BV, 32 * jb, 0, 0, base3);
+                for (int i = 0; i < PARTS; ++i) v[jb][i] = col_op<BV>(X3 + i * C * BV, 32 * jb, 0, 0, base3);
         };
 
-        f32x4 acc[IT][NT];
+        f32x4 acc[IT];
         uint2 third[OVER ? MT : 1][NH];
         if constexpr (FULL) {
             // ---- P = x1 . x2 under the decays, tiles of 16 x 16 on and below the diagonal
@@ -735,7 +731,7 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
             __builtin_amdgcn_s_setprio(1);   // a workgroup in its products goes before one that stores or waits (1.5%)
             // ---- the incoming state's share, e^{G_i} R^T x1_i
 #pragma unroll
-            for (int x = 0; x < IT * NT; ++x) acc[x / NT][x % NT] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int it = 0; it < IT; ++it) acc[it] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
                 u32x4 q[IT][PARTS];
@@ -743,25 +739,23 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
                 for (int x = 0; x < IT * PARTS; ++x)
                     q[x / PARTS][x % PARTS] = row_op<KD>(X1 + (x % PARTS) * C * KD, 16 * (x / PARTS), kb, base);
                 if (PARTS == 1) __builtin_amdgcn_sched_barrier(0);
-                u32x4 sp[NT][WP];
+                u32x4 sp[WP];
 #pragma unroll
-                for (int x = 0; x < 4 * NT; ++x) {
-                    const int nt = x >> 2, e = x & 3;
-                    const f32x4& s = S[2 * kb + (e >> 1)][nt];
+                for (int e = 0; e < 4; ++e) {
+                    const f32x4& s = S[2 * kb + (e >> 1)];
                     uint32_t w[WP];
                     split<WP>(s[2 * (e & 1)], s[2 * (e & 1) + 1], w);
 #pragma unroll
-                    for (int k = 0; k < WP; ++k) sp[nt][k][e] = w[k];
+                    for (int k = 0; k < WP; ++k) sp[k][e] = w[k];
                 }
 #pragma unroll
-                for (int x = 0; x < IT * NT; ++x)
-                    acc[x / NT][x % NT] = mma_parts<PARTS, WP>(q[x / NT], sp[x % NT], acc[x / NT][x % NT]);
+                for (int it = 0; it < IT; ++it) acc[it] = mma_parts<PARTS, WP>(q[it], sp, acc[it]);
             }
 #pragma unroll
             for (int it = 0; it < IT; ++it) {
                 const f32x4 e = *reinterpret_cast<const f32x4*>(&dec.in[16 * it + 4 * g4]);
 #pragma unroll
-                for (int x = 0; x < 4 * NT; ++x) acc[it][x >> 2][x & 3] *= e[x & 3];
+                for (int r = 0; r < 4; ++r) acc[it][r] *= e[r];
             }
         } else {
             next();
@@ -775,27 +769,26 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
 #pragma unroll
                 for (int m = 0; m < 2 * KB; ++m)
 #pragma unroll
-                    for (int x = 0; x < 4 * NT; ++x) S[m][x >> 2][x & 3] *= fold;
+                    for (int r = 0; r < 4; ++r) S[m][r] *= fold;
             }
 #pragma unroll
             for (int jb = 0; jb < JB; ++jb) {
-                u32x4 vp[NT][WP];
+                u32x4 vp[WP];
                 const f32x4 f0 = *reinterpret_cast<const f32x4*>(&dec.out[32 * jb + 8 * g4]);
                 const f32x4 f1 = *reinterpret_cast<const f32x4*>(&dec.out[32 * jb + 8 * g4 + 4]);
 #pragma unroll
-                for (int z = 0; z < 4 * NT; ++z) {
-                    const int nt = z >> 2, e = z & 3;
-                    float x = bf_lo(v[jb][nt][PARTS - 1][e]), y = bf_hi(v[jb][nt][PARTS - 1][e]);
+                for (int e = 0; e < 4; ++e) {
+                    float x = bf_lo(v[jb][PARTS - 1][e]), y = bf_hi(v[jb][PARTS - 1][e]);
 #pragma unroll
                     for (int i = PARTS - 2; i >= 0; --i) {
-                        x += bf_lo(v[jb][nt][i][e]);
-                        y += bf_hi(v[jb][nt][i][e]);
+                        x += bf_lo(v[jb][i][e]);
+                        y += bf_hi(v[jb][i][e]);
                     }
                     const f32x4& f = e < 2 ? f0 : f1;
                     uint32_t w[WP];
                     split<WP>(x * f[2 * (e & 1)], y * f[2 * (e & 1) + 1], w);
 #pragma unroll
-                    for (int k = 0; k < WP; ++k) vp[nt][k][e] = w[k];
+                    for (int k = 0; k < WP; ++k) vp[k][e] = w[k];
                 }
                 constexpr int AHEAD = PARTS == 1 ? (EARLY ? 2 : 4) : 1;   // operands in flight
 #pragma unroll
@@ -808,8 +801,7 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
                     }
                     if (AHEAD > 1) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int x = 0; x < AHEAD * NT; ++x)
-                        S[m0 + x / NT][x % NT] = mma_parts<PARTS, WP>(k[x / NT], vp[x % NT], S[m0 + x / NT][x % NT]);
+                    for (int x = 0; x < AHEAD; ++x) S[m0 + x] = mma_parts<PARTS, WP>(k[x], vp, S[m0 + x]);
                 }
             }
         };
@@ -858,8 +850,7 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
 #pragma unroll
                     for (int k = 0; k < WP; ++k)
                         q[k] = row_op<32>((k < PL ? PT + k * PB : X3 + hw * PB) + p_block(it, jb) * 512, 0, 0, base_p);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) acc[it][nt] = mma_parts<WP, PARTS>(q, v[jb][nt], acc[it][nt]);
+                    acc[it] = mma_parts<WP, PARTS>(q, v[jb], acc[it]);
                 }
             if constexpr (!EARLY) onward();
         } else {
@@ -874,42 +865,33 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
             const Rsrc ro = rows_rsrc(static_cast<char*>(p.out) + c0 * pitch64 + int64_t(h) * p.vd * oe, pitch64, hi - c0, C);
             const StoreRows to(pitch64, rev, C, g4);
             if (oe == 4) {
+                const int col = c_wave + l16;
+                const uint32_t o0 = to.first(col < p.vd, 4 * col);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const int col = c_wave + 16 * nt + l16;
-                    const uint32_t o0 = to.first(col < p.vd, 4 * col);
-#pragma unroll
-                    for (int x = 0; x < 4 * IT; ++x)
-                        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[x >> 2][nt][x & 3]), ro,
-                                                              o0 + to.row(16 * (x >> 2) + (x & 3)), 0, 0);
-                }
+                for (int x = 0; x < 4 * IT; ++x)
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[x >> 2][x & 3]), ro,
+                                                          o0 + to.row(16 * (x >> 2) + (x & 3)), 0, 0);
             } else if (p.pairs) {
                 // neighbouring lanes swap one row for another: two columns of one row each
                 const bool odd = lane & 1;
                 const uint32_t pick = odd ? 0x03020706u : 0x05040100u;   // own and the neighbour's halves
+                const int col = c_wave + (l16 & ~1);
+                const uint32_t o0 = to.first(col < p.vd, 2 * col) + (odd ? to.row(1) : 0u);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const int col = c_wave + 16 * nt + (l16 & ~1);
-                    const uint32_t o0 = to.first(col < p.vd, 2 * col) + (odd ? to.row(1) : 0u);
+                for (int it = 0; it < IT; ++it)
 #pragma unroll
-                    for (int it = 0; it < IT; ++it)
-#pragma unroll
-                        for (int r = 0; r < 4; r += 2) {
-                            const uint32_t own = pack2(acc[it][nt][r], acc[it][nt][r + 1]);
-                            __builtin_amdgcn_raw_buffer_store_b32(__builtin_amdgcn_perm(swap1(own), own, pick), ro,
-                                                                  o0 + to.row(16 * it + r), 0, 0);
-                        }
-                }
+                    for (int r = 0; r < 4; r += 2) {
+                        const uint32_t own = pack2(acc[it][r], acc[it][r + 1]);
+                        __builtin_amdgcn_raw_buffer_store_b32(__builtin_amdgcn_perm(swap1(own), own, pick), ro,
+                                                              o0 + to.row(16 * it + r), 0, 0);
+                    }
             } else {
+                const int col = c_wave + l16;
+                const uint32_t o0 = to.first(col < p.vd, 2 * col);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const int col = c_wave + 16 * nt + l16;
-                    const uint32_t o0 = to.first(col < p.vd, 2 * col);
-#pragma unroll
-                    for (int x = 0; x < 4 * IT; ++x)
-                        __builtin_amdgcn_raw_buffer_store_b16(IOT<uint16_t>::from_f32(acc[x >> 2][nt][x & 3]), ro,
-                                                              o0 + to.row(16 * (x >> 2) + (x & 3)), 0, 0);
-                }
+                for (int x = 0; x < 4 * IT; ++x)
+                    __builtin_amdgcn_raw_buffer_store_b16(IOT<uint16_t>::from_f32(acc[x >> 2][x & 3]), ro,
+                                                          o0 + to.row(16 * (x >> 2) + (x & 3)), 0, 0);
             }
         }
         if constexpr (OVER) {
@@ -950,15 +932,15 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW, NT)) linattn_pass_
 #pragma unroll
         for (int m = 0; m < 2 * KB; ++m)
 #pragma unroll
-            for (int x = 0; x < 4 * NT; ++x) {
-                const int nt = x >> 2, r = x & 3, row = 32 * (m >> 1) + 8 * g4 + 4 * (m & 1) + r, col = c_wave + 16 * nt + l16;
-                if (row < p.kd && col < p.vd) dst[row * rs + col * cs] = mul * S[m][nt][r];
+            for (int r = 0; r < 4; ++r) {
+                const int row = 32 * (m >> 1) + 8 * g4 + 4 * (m & 1) + r, col = c_wave + l16;
+                if (row < p.kd && col < p.vd) dst[row * rs + col * cs] = mul * S[m][r];
             }
     }
 }
 
 // Chooses the kernel of a pass's sizes and starts it.
-template <int MODE> inline bool launch_pass(const ssm_detail::LinattnPasses& q, int count, bool f32, hipStream_t s) {
+template <int MODE> inline void launch_pass(const ssm_detail::LinattnPasses& q, int count, bool f32, hipStream_t s) {
     const LinattnPass& p = q.p[0];
     // two heads in a workgroup share loads and products, but while each head finds a CU of its
     // own four waves of one SIMD each are sooner done than eight (three float32 prompts of up to
@@ -971,8 +953,8 @@ template <int MODE> inline bool launch_pass(const ssm_detail::LinattnPasses& q, 
     const auto start = [&](auto* kernel) { launch_kernel(kernel, grid, block, 0, s, q); };
 #define SSM_LIN_CASE(K, NW, NH)                                                                     \
     do {                                                                                            \
-        if (f32) start(linattn_pass_kernel<3, K, NW, 1, 32, MODE, NH>);                             \
-        else start(linattn_pass_kernel<1, K, NW, 1, 64, MODE, NH>);                                 \
+        if (f32) start(linattn_pass_kernel<3, K, NW, 32, MODE, NH>);                             \
+        else start(linattn_pass_kernel<1, K, NW, 64, MODE, NH>);                                 \
     } while (0)
 #define SSM_LIN_WAVES(K)                                                                            \
     do {                                                                                            \
@@ -984,13 +966,10 @@ template <int MODE> inline bool launch_pass(const ssm_detail::LinattnPasses& q, 
         SSM_LIN_WAVES(64);
     else if (p.kd <= 128)
         SSM_LIN_WAVES(128);
-    else if (p.kd <= 256)
-        SSM_LIN_WAVES(256);
     else
-        return false;
+        SSM_LIN_WAVES(256);
 #undef SSM_LIN_WAVES
 #undef SSM_LIN_CASE
-    return true;
 }
 
 // ---------------------------------------------------------------- host: checks

@@ -208,8 +208,9 @@ inline int make_plan(const ssm_linattn_dims* d, bool packed, Plan* pl) {
 }  // namespace la
 }  // namespace
 
-bool ssm_detail::launch_linattn_pass(const LinattnPasses& p, int count, bool f32, LinattnMode mode, hipStream_t s) {
-    return mode == kLinStates ? la::launch_pass<kLinStates>(p, count, f32, s) : la::launch_pass<kLinFull>(p, count, f32, s);
+void ssm_detail::launch_linattn_pass(const LinattnPasses& p, int count, bool f32, LinattnMode mode, hipStream_t s) {
+    if (mode == kLinStates) la::launch_pass<kLinStates>(p, count, f32, s);
+    else la::launch_pass<kLinFull>(p, count, f32, s);
 }
 
 void ssm_detail::launch_linattn_carry(const LinattnPasses& q, int count, hipStream_t s) {

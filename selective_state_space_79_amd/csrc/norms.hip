@@ -169,7 +169,7 @@ struct Place {
     int group;
     bool on;
 };
-template <int TPG> __device__ inline Place place(int64_t rows, int ngroups) {
+template <int TPG> __device__ inline Place place(int ngroups) {
     constexpr int spb = block_threads<TPG>() / TPG;
     int own = threadIdx.x / TPG;
     if (TPG >= 64) own = __builtin_amdgcn_readfirstlane(own);   // rows' addresses on the scalar unit
@@ -179,7 +179,6 @@ template <int TPG> __device__ inline Place place(int64_t rows, int ngroups) {
     p.row = slot / ngroups;
     p.group = int(slot % ngroups);
     p.on = p.row < p.step;
-    (void)rows;
     return p;
 }
 
@@ -201,7 +200,7 @@ __global__ void __launch_bounds__(block_threads<TPG>()) gated_norm_fwd_kernel(Ga
     __shared__ float red[Summer<TPG>::kFloats];
     Summer<TPG> sum{red};
     const int lane = threadIdx.x % TPG;
-    const Place at = place<TPG>(p.rows, p.ngroups);
+    const Place at = place<TPG>(p.ngroups);
     const int64_t off = int64_t(at.group) * p.n;
     V8 w[V];
 #pragma unroll
@@ -280,7 +279,7 @@ __global__ void __launch_bounds__(block_threads<TPG>(), 4) gated_norm_bwd_kernel
     __shared__ __align__(16) float wl[V * 8 * T];   // weights; at the end the slots' sums
     Summer<TPG> sum{red};
     const int tid = threadIdx.x, lane = tid % TPG;
-    const Place at = place<TPG>(p.rows, p.ngroups);
+    const Place at = place<TPG>(p.ngroups);
     const int64_t off = int64_t(at.group) * p.n, dim = int64_t(p.ngroups) * p.n;
     V8 dw[V];
 #pragma unroll
@@ -379,7 +378,7 @@ __global__ void __launch_bounds__(block_threads<TPG>()) add_norm_fwd_kernel(AddA
     __shared__ float red[Summer<TPG>::kFloats];
     Summer<TPG> sum{red};
     const int lane = threadIdx.x % TPG;
-    const Place at = place<TPG>(p.rows, 1);
+    const Place at = place<TPG>(1);
     const int64_t loops = (p.rows + at.step - 1) / at.step;
     for (int64_t l = 0; l < loops; ++l) {
         const int64_t row = at.row + l * at.step;
@@ -438,7 +437,7 @@ __global__ void __launch_bounds__(block_threads<TPG>(), 4) add_norm_bwd_kernel(A
     __shared__ __align__(16) float wl[HELD ? 3 * PL : 4];   // w, scale, post; at the end the slots' sums
     Summer<TPG> sum{red};
     const int tid = threadIdx.x, lane = tid % TPG;
-    const Place at = place<TPG>(p.rows, 1);
+    const Place at = place<TPG>(1);
     V8 dw[V], dsc[V], dpo[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
