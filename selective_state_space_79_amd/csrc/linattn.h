@@ -389,8 +389,10 @@ template <int PARTS, int C, int W, int T, int HW = W> struct Tile {   // T threa
 
 // Decays of one chunk.  The sums run in float64 and are kept in two floats, so that a
 // difference of two of them is right to float32 of the difference, however far they fell.
-// The state in registers is R / s with a scale s that takes the chunks' decays in its place
-// (no product per value and chunk); it is folded in before it leaves 2^-60 .. 2^60.
+// The state in registers is R / s with a scale s that takes the chunks' decays in its place, in
+// float64: slow decays are rounded once a half-life instead of once a chunk.  It is folded in
+// where it would fall to 1/2, so that R / s reaches no further than R does (further down costs
+// range, not time: the same within 1% at 2^-60).
 template <int C> struct __align__(16) Decays {
     float hi[C], lo[C];   // G in log2 units
     float in[C];          // o s e^{G_i}: the incoming state's share at row i
@@ -443,7 +445,7 @@ template <int C> struct DecayLane {
         g = g < kMinDecay ? kMinDecay : g;
         const double s = scan_f64(lane < C ? double(g) * 1.4426950408889634 : 0.0);
         const double end = lane_f64(s, C - 1);
-        const bool fold = !(fabs(scale + end) < 60.0);
+        const bool fold = !(fabs(scale + end) < 1.0);
         if (lane < C) {
             const float hi = float(s);
             d.hi[lane] = hi;
