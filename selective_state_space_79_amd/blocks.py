@@ -112,7 +112,11 @@ def _call(name, args, device, stream):
 
     f = _fn(name)
     index = device if device >= 0 else torch.cuda.current_device()
-    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        _need(stream.device_index == index, f"stream must be one of cuda:{index}, the tensors' device")
+        raw = stream.cuda_stream
     # a launch goes to the current device, so that has to be the tensors'
     if index == torch._C._cuda_getDevice():
         return f(*args, raw)
