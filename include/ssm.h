@@ -452,7 +452,9 @@ SSM_API int ssm_ssd_fwd(const void* u, const void* delta, const float* A, const 
  * io_dtype is SSM_F32) are split into three bf16 parts, which hold a float32.  What a call
  * asks for does not change how its outputs are formed.
  * A NaN or infinity in a token reaches outputs of earlier tokens of its sequence at most
- * within its block of 64 tokens, and never another sequence.
+ * within its block of 64 tokens (gradients: of later tokens in like manner; dg: within its
+ * piece), and never another sequence.  An infinite state or value may give NaN where the sum
+ * would be infinite.
  * Ownership, asynchrony and the error rules are those of ssm_selective_scan_fwd. */
 
 /* Largest dk and dv. */
@@ -508,7 +510,8 @@ typedef struct ssm_linattn_grads {
 
 /* Bytes of workspace of ssm_linattn_bwd (never 0 for valid dims; 0 for dims it refuses):
  * the states and state gradients at the pieces' ends, and float32 dq and dk per head (heads
- * that share them are added up, and dg is formed, from these). */
+ * that share them are added up, and dg is formed, from these): 8 tokens nheads dk bytes and
+ * about the states of tokens / 1024 + nseq pieces twice. */
 SSM_API size_t ssm_linattn_bwd_workspace_bytes(const ssm_linattn_dims* dims);
 
 /* Enqueue the gradients of

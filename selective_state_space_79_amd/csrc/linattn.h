@@ -474,13 +474,16 @@ __device__ constexpr int p_block(int it, int jb) { return it < 2 ? it : 2 * it -
 // go two to a workgroup (NH), each with its own decays on the same products; other narrow
 // heads take four waves.
 //
-// What bounds it: the issue of vector and matrix instructions, with the rows' bytes close behind.  A wave and chunk of 64 tokens
-// of a 128 x 128 head takes 97 matrix products (16 cycles each) and 445 vector instructions
-// (4 cycles each), half of them the split of the state and of the decayed values into bf16
-// parts; counted on 131072 tokens of 16 heads they fill 46% and 53% of the SIMD cycles.  The output pass takes 489 us there (4.4 TB/s of rows; a plain copy 5.15) and the
-// states pass before it 223 us (4.8 TB/s); a float32 output's pass 315 us for dq and dk of
-// 4 x 4096 tokens of 32 heads.  Tried without gain: 32 columns a wave from registers, keys two
-// products ahead, the parts' rests by two-term products.
+// What bounds it: the issue of vector and matrix instructions.  A wave and chunk of 64 tokens of
+// a 128 x 128 head takes 119 matrix products (16 cycles each) and 600 vector instructions (4
+// cycles each), half of them the split of the state and of the decayed values into bf16 parts;
+// counted on 131072 tokens of 16 heads matrix products run in 46% of the SIMD cycles and vector
+// instructions in 58%, both at once in 16%: one or the other in 88%.  LDS is busy in 55% of the
+// cycles, 45% of those in bank conflicts.  The output pass takes 571 us there (3.8 TB/s of rows;
+// a plain copy 5.15) and the states pass before it 221 us (4.9 TB/s; one or the other in 75%); dq
+// and dk in float32 of 4 x 4096 tokens of 32 heads 308 us.  Tried without gain: 32 columns a wave
+// from registers, keys two products ahead, the parts' rests by two-term products, the heads of
+// the second round of P's tiles on waves of their own.
 //
 // Parts: what is not a bf16 input (the state, the decayed products and values, float32 rows)
 // goes into the products in three bf16 parts, which hold a float32 whole.  Two parts would take
@@ -507,8 +510,8 @@ __global__ void __launch_bounds__(64 * NW, pass_waves(KD, NW)) linattn_pass_kern
     // that still leaves room for two workgroups on a CU.  P takes that room at 128 state rows,
     // and two heads' P at 64: there the state goes on before P x3, and x2 is free after it
     // (EARLY).  At 128 rows two heads' P takes more than that: its third part goes where x3 was,
-    // and x3 is asked for behind everything else (OVER; 250 us against 263 with one workgroup on
-    // a CU, 2 x 8192 tokens of 64 heads).  float32 rows are held in registers from one chunk to
+    // and x3 is asked for behind everything else (OVER; 250 us against 263 with one workgroup
+    // on a CU, 2 x 8192 tokens of 64 heads).  float32 rows are held in registers from one chunk to
     // the next.
     constexpr bool DMA = PARTS == 1, EARLY = DMA && FULL && (KD == 128 || (KD == 64 && NH == 2)),
                    OVER = EARLY && KD == 128 && NH == 2, TWO2 = DMA && !EARLY, TWO3 = DMA && !FULL;
@@ -946,7 +949,8 @@ template <int MODE> inline void launch_pass(const ssm_detail::LinattnPasses& q, 
     const LinattnPass& p = q.p[0];
     // two heads in a workgroup share loads and products, but while each head finds a CU of its
     // own four waves of one SIMD each are sooner done than eight (three float32 prompts of up to
-    // 130 tokens and 6 heads 26.5 us against 30.7; 2 x 8192 tokens of 64 heads 243 against 208)
+    // 130 tokens and 6 heads 26.5 us against 30.7 with two; 2 x 8192 tokens of 64 heads 286 us
+    // against 254 with two)
     const bool two = p.r1 % 2 == 0 && p.r2 % 2 == 0 && int64_t(p.npieces) * p.H > kCus;
     const int shape = ssm_detail::linattn_shape(p.vd, two);
     const int64_t blocks = int64_t(p.npieces) * (shape == ssm_detail::kTwoHeads ? p.H / 2 : p.H) * p.nslices;

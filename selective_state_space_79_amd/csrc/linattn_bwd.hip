@@ -191,8 +191,8 @@ __global__ void __launch_bounds__(kThreads) linattn_dg_sum_kernel(GradTail t) {
 
 // From dq and dk per head in float32: the sums over the heads that share a row, rounded, and
 // f = k . dk - q . dq of each token and head.  LPR lanes take a row, 4 columns each (VW of
-// them in one access).  Bound by the bytes of the parts: 138 us for 16384 tokens of 32 heads of
-// 128 in groups of 4 (671 MB, 4.9 TB/s).
+// them in one access).  Bound by the bytes of the parts: 133 us for 16384 tokens of 32 heads of
+// 128 in groups of 4 (671 MB, 5.0 TB/s).
 struct GroupArgs {
     const float* dq;
     const float* dk;
@@ -290,7 +290,8 @@ struct GradPlan {
 };
 
 // Pieces of at most 1024 tokens: the error of dg's running sum grows with the piece, and the
-// states of pieces this long are a sixteenth of the rows' bytes at dk = dv = 128.
+// states of pieces this long are a sixteenth of the rows' bytes at dk = dv = 128.  A layer of 4 x
+// 4096 tokens and 32 heads takes 740 us in pieces of 1024, 828 of 512, 794 of 2048.
 inline int make_grad_plan(const ssm_linattn_dims* d, bool packed, GradPlan* pl) {
     pl->slices_q = cdiv(d->dk, ssm_detail::linattn_slice(d->dk));
     pl->slices_s = cdiv(d->dv, ssm_detail::linattn_slice(d->dv));

@@ -174,14 +174,17 @@ struct Plan {
     size_t carry, tot;   // bytes
 };
 
-// Pieces along the tokens.  A workgroup walks its piece chunk by chunk, 3.6 us for 64 tokens
-// of a 128 x 128 head alone on its CU and 8.8 us for two side by side, so work is cut into the
+// Pieces along the tokens.  A workgroup walks its piece chunk by chunk, 7.2 us for 64 tokens
+// of a 128 x 128 head alone on its CU and 10.4 us for two side by side, so work is cut into the
 // 512 workgroups that the card holds at once; more, smaller pieces only add states to carry.
-// Measured, us: 131072 tokens of 16 heads 723 in pieces of 4096, 787 of 2048, 810 of 8192; 8
-// ragged prompts of 8192 tokens in all, 32 heads, 161 in pieces of 512, 180 of 320, 154 of 704,
-// 270 of 2048; 2 x 8192 tokens of 64 shared heads of 64 189 in pieces of 1024, 222 of 512, 273
-// of 2048.  Cutting costs two launches and a second pass over keys and values:
-// sequences of up to 256 tokens stay whole.
+// Measured on the same inputs again and again, us, the rule's own piece first: 131072 tokens of
+// 16 heads 836 in pieces of 4096, 875 of 2048, 955 of 8192; 8 ragged prompts of 8192 tokens in
+// all, 32 heads, 160 in pieces of 512, 193 of 320, 176 of 576, 158 of 704, 175 of 1024, 303 of
+// 2048; 2 x 8192 tokens of 64 shared heads of 64 227 in pieces of 1024, 283 of 512, 355 of 2048.
+// Cutting costs two launches and a second pass over keys and values: sequences of up to 256
+// tokens stay whole.  The lengths of packed sequences are not known here: they are taken for one
+// sequence of all tokens, so short ones get the two launches for nothing (64 prompts of 128
+// tokens and 32 heads of 128 x 128 131 us and a workspace of 168 MB that stays unused).
 inline int64_t choose_piece(const ssm_linattn_dims* d, int64_t units, int64_t each) {
     const int64_t want = 512 / units;   // pieces of the whole call
     if (want < 2 || each <= 256) return 0;

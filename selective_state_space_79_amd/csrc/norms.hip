@@ -12,11 +12,14 @@
 // 4096 bf16 rows of 16384), and the sums for the weights' gradients in registers over a
 // workgroup's rows; the workgroups' partial sums are then added in a fixed order.
 //
-// Measured: gated forward 16384 rows of 64 groups of 64 in 75 us (5.4 TB/s; a plain copy 5.15),
-// 1535 wide 38 us (4.0 TB/s); its gradient 16383 rows of 1536 in 69 us (3.7 TB/s, 56 us of it
-// the rows, 5 the partial sums); residual norm 4096 wide 150 us (5.4 TB/s), its gradient at
-// 2048 columns with both weights in 129 us (4.7 TB/s), 4096 without 135 us (6.0 TB/s), 8192
-// 183 us (4.4 TB/s), 16384 451 us (1.8 TB/s, bound by registers).
+// Measured on 16384 bf16 rows, the bytes of rows that are read and written (a plain copy runs at
+// 5.15 TB/s): gated forward of 64 groups of 64 in 75 us (5.4 TB/s), 1536 wide 30 us (5.1), 1535
+// wide 37 us (4.0); its gradient at 1536 columns 57 us on the same inputs again and again (4.4
+// TB/s) and 69 on others each time (3.6; 54 us of it the rows, 5 the partial sums), at 4096 147 us
+// (4.6); residual norm 4096 wide 97 us (5.6 TB/s), with a float32 residual and both weights 165 us
+// (4.9); its gradient at 2048 columns with a float32 residual and both weights 130 us (4.6), at
+// 4096 with a bf16 one without weights 136 us (4.9), 8192 rows of 8192 with both weights 183 us
+// (4.4), 4096 rows of 16384 452 us (1.8, bound by registers).
 #include "rows.h"
 
 namespace {
