@@ -463,7 +463,9 @@ SSM_API int ssm_ssd_fwd(const void* u, const void* delta, const float* A, const 
 typedef struct ssm_linattn_dims {
     int64_t tokens;    /* >= 1: rows of q, k, v, o and g */
     int64_t nseq;      /* 1 .. 65535 sequences (single-token step: equal to tokens) */
-    int64_t nheads;    /* 1 .. 32767: heads of v, o, g and the states */
+    int64_t nheads;    /* 1 .. 32767: heads of v, o, g and the states.  Sequences (or pieces of
+                          them) x nheads x 128-column slices of a head: at most 2^22, else
+                          SSM_ERR_DIMS (single-token step: 2^23, slices of 16 columns at least) */
     int64_t kheads;    /* >= 1 heads of q and k; nheads % kheads == 0 */
     int64_t dk, dv;    /* 1 .. SSM_LINATTN_MAX_DIM */
     int64_t q_stride, k_stride, v_stride, o_stride; /* elements between tokens; 0: packed;
