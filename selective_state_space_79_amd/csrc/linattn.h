@@ -959,8 +959,8 @@ template <int MODE> inline void launch_pass(const ssm_detail::LinattnPasses& q, 
     const auto start = [&](auto* kernel) { launch_kernel(kernel, grid, block, 0, s, q); };
 #define SSM_LIN_CASE(K, NW, NH)                                                                     \
     do {                                                                                            \
-        if (f32) start(linattn_pass_kernel<3, K, NW, 32, MODE, NH>);                             \
-        else start(linattn_pass_kernel<1, K, NW, 64, MODE, NH>);                                 \
+        if (f32) start(linattn_pass_kernel<3, K, NW, 32, MODE, NH>);                                \
+        else start(linattn_pass_kernel<1, K, NW, 64, MODE, NH>);                                    \
     } while (0)
 #define SSM_LIN_WAVES(K)                                                                            \
     do {                                                                                            \
