@@ -528,6 +528,70 @@ SSM_API int ssm_linattn_bwd(const void* q, const void* k, const void* v, const f
                             const ssm_linattn_dims* dims, void* stream);
 
 /* ------------------------------------------------------------------------------
+ * The gated delta rule: linear attention whose writes first take back what the state holds
+ * under the same key.  Per head h, with a state S of dk x dv float32 values, a decay and a
+ * step size beta for each token:
+ *
+ *   S'_t = e^{g_t} S_{t-1}               what the state still holds
+ *   r_t  = v_t - S'_t^T k_t              what it lacks under the key
+ *   S_t  = S'_t + beta_t k_t r_t^T       o_t = scale * S_t^T q_t
+ *
+ * Layouts, sequences, slots, states, strides and rules are those of ssm_linattn_* above (and
+ * its dims), with
+ *   beta : float32 (tokens, nheads), any values; a state stays bounded where 0 <= beta |k|^2
+ *          <= 2.  Keys and queries are taken as they are: a caller who wants them of length
+ *          one scales them (ssm_gated_norm_fwd over heads of dk, without a gate and with a weight of
+ *          dk^-1/2, does).
+ * Inside a block of 64 tokens (SSM_F32: 32; gradients: 32 also where dk or dv is over 128) the
+ * rows r solve a triangular system; the products are held to float32 as those of
+ * ssm_linattn_* are.  A NaN or infinity in a token may reach all tokens of its block and what
+ * follows in its sequence (gradients: what comes before), never another sequence. */
+
+/* Bytes of workspace of ssm_delta_fwd (never 0 for valid dims; 0 for dims it refuses): the
+ * blocks' triangular matrices, 18432 bytes (SSM_F32: 6144) for each block and head, and with
+ * pieces a state and a dk x dk transition for each piece and head. */
+SSM_API size_t ssm_delta_fwd_workspace_bytes(const ssm_linattn_dims* dims);
+
+/* Enqueue the forward over whole sequences; as ssm_linattn_fwd, with beta and a workspace that
+ * is always needed.  Returns an ssm_status value. */
+SSM_API int ssm_delta_fwd(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                          const int32_t* cu_seqlens, const int32_t* slots, const float* s0, void* o, float* s_last,
+                          const ssm_linattn_dims* dims, void* stream);
+
+/* One token of each sequence (tokens == nseq, no cu_seqlens): states read and updated in
+ * place (required), o written.  Needs no workspace. */
+SSM_API int ssm_delta_step(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                           const int32_t* slots, float* states, void* o, const ssm_linattn_dims* dims, void* stream);
+
+/* Where ssm_delta_bwd writes the gradients (device pointers, packed):
+ *   dq, dk : (tokens, kheads, dk) in io_dtype, summed over the heads that share them
+ *   dv     : (tokens, nheads, dv) in io_dtype
+ *   dg     : float32, the shape of g
+ *   dbeta  : float32 (tokens, nheads)
+ *   ds0    : float32 (nseq, nheads, dk, dv); required with s0, nullable without */
+typedef struct ssm_delta_grads {
+    void* dq;
+    void* dk;
+    void* dv;
+    float* dg;
+    float* dbeta;
+    float* ds0;
+} ssm_delta_grads;
+
+/* Bytes of workspace of ssm_delta_bwd (never 0 for valid dims; 0 for dims it refuses): the
+ * triangular matrices, the state before and the state gradient behind each block (8 dk dv bytes a
+ * block and head), where heads share q and k also float32 dq and dk of each head, and
+ * with pieces two states and two transitions for each piece and head. */
+SSM_API size_t ssm_delta_bwd_workspace_bytes(const ssm_linattn_dims* dims);
+
+/* Enqueue the gradients of
+ *     sum dout * o  +  sum ds_last * s_last
+ * for the forward with the same q, k, v, g, beta, cu_seqlens and s0; as ssm_linattn_bwd. */
+SSM_API int ssm_delta_bwd(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                          const int32_t* cu_seqlens, const float* s0, const void* dout, const float* ds_last,
+                          const ssm_delta_grads* grads, const ssm_linattn_dims* dims, void* stream);
+
+/* ------------------------------------------------------------------------------
  * The norms around a block.  RMS norm of n values x with a weight w:
  *     norm(x; w)_i = w_i x_i / sqrt(mean_j x_j^2 + eps)
  * Rows are last-index contiguous; sums and statistics are float32. */
@@ -595,6 +659,30 @@ SSM_API size_t ssm_add_norm_bwd_workspace_bytes(const ssm_add_norm_dims* dims);
 SSM_API int ssm_add_norm_bwd(const void* x, const void* r, const float* scale, const float* post, const float* w,
                              const void* dy, const void* dr, void* dx, void* dres, float* dw, float* dscale,
                              float* dpost, const ssm_add_norm_dims* dims, void* stream);
+
+/* Layer norm, the norm before a block that takes the mean out as well:
+ *   y_i = w_i (x_i - mean) / sqrt(mean_j (x_j - mean)^2 + eps) + b_i
+ *   x, y : (rows, dim) in io_dtype;  w, b : float32 (dim,), b nullable (no bias)
+ * The mean is taken before the squares, so that a mean far from zero costs no digits.  y may be
+ * x itself (same stride), else it overlaps no input. */
+typedef struct ssm_layer_norm_dims {
+    int64_t rows;      /* >= 1 */
+    int64_t dim;       /* 1 .. SSM_NORM_MAX_DIM */
+    int64_t x_stride, y_stride; /* elements between rows; 0: packed */
+    int32_t io_dtype;
+    float eps;         /* 2^-126 (the least normal float32) or more, finite */
+    void* workspace;   /* backward: 256-byte aligned device memory */
+    size_t workspace_bytes;
+} ssm_layer_norm_dims;
+
+SSM_API int ssm_layer_norm_fwd(const void* x, const float* w, const float* b, void* y, const ssm_layer_norm_dims* dims,
+                               void* stream);
+SSM_API size_t ssm_layer_norm_bwd_workspace_bytes(const ssm_layer_norm_dims* dims);
+/* Gradients of sum(dy * y).  dy, dx: packed (rows, dim) in io_dtype (y_stride is ignored); dw,
+ * db: float32 (dim,), summed over the rows in a fixed order, db nullable (not wanted).  Outputs
+ * overlap no input, one another or the workspace. */
+SSM_API int ssm_layer_norm_bwd(const void* x, const float* w, const void* dy, void* dx, float* dw, float* db,
+                               const ssm_layer_norm_dims* dims, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,7 +1,8 @@
 """The operators of a block around a recurrent mixer, as bound from libssm.so: linear
-attention with a decay for each head (``linattn_fwd``, ``linattn_step``, ``linattn_bwd``) and
-the norms before and after a block (``gated_norm_fwd``, ``gated_norm_bwd``, ``add_norm_fwd``,
-``add_norm_bwd``).
+attention with a decay for each head (``linattn_fwd``, ``linattn_step``, ``linattn_bwd``), the
+gated delta rule (``delta_fwd``, ``delta_step``, ``delta_bwd``) and the norms before and after a
+block (``gated_norm_fwd``, ``gated_norm_bwd``, ``add_norm_fwd``, ``add_norm_bwd``,
+``layer_norm_fwd``, ``layer_norm_bwd``).
 
 Argument marshalling only, like the rest of the package; include/ssm.h states what each call
 computes.  The ``ssm_*`` functions carry the C names, take the tensors of the call (or None)
@@ -18,7 +19,10 @@ __all__ = ["SSM_LINATTN_MAX_DIM", "SSM_NORM_MAX_DIM", "SsmLinattnDims", "SsmLina
            "gated_norm_bwd", "add_norm_fwd", "add_norm_bwd", "ssm_linattn_fwd", "ssm_linattn_step", "ssm_linattn_bwd",
            "ssm_linattn_fwd_workspace_bytes", "ssm_linattn_bwd_workspace_bytes", "ssm_gated_norm_fwd",
            "ssm_gated_norm_bwd", "ssm_gated_norm_bwd_workspace_bytes", "ssm_add_norm_fwd", "ssm_add_norm_bwd",
-           "ssm_add_norm_bwd_workspace_bytes"]
+           "ssm_add_norm_bwd_workspace_bytes", "SsmDeltaGrads", "SsmLayerNormDims", "delta_fwd", "delta_step",
+           "delta_bwd", "layer_norm_fwd", "layer_norm_bwd", "ssm_delta_fwd", "ssm_delta_step", "ssm_delta_bwd",
+           "ssm_delta_fwd_workspace_bytes", "ssm_delta_bwd_workspace_bytes", "ssm_layer_norm_fwd",
+           "ssm_layer_norm_bwd", "ssm_layer_norm_bwd_workspace_bytes"]
 
 _vp = ctypes.c_void_p
 _ref = ctypes.byref
@@ -55,6 +59,17 @@ class SsmAddNormDims(ctypes.Structure):
                 ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t)]
 
 
+class SsmDeltaGrads(ctypes.Structure):
+    """Mirror of ``ssm_delta_grads`` in include/ssm.h (device pointers; None = NULL)."""
+    _fields_ = [(name, _vp) for name in ("dq", "dk", "dv", "dg", "dbeta", "ds0")]
+
+
+class SsmLayerNormDims(ctypes.Structure):
+    """Mirror of ``ssm_layer_norm_dims`` in include/ssm.h."""
+    _fields_ = [("rows", _i64), ("dim", _i64), ("x_stride", _i64), ("y_stride", _i64), ("io_dtype", _i32), ("eps", _f32),
+                ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t)]
+
+
 # C name -> (pointers before the struct arguments, struct types); a stream follows
 _CALLS = {
     "ssm_linattn_fwd": (9, (SsmLinattnDims,)),
@@ -64,12 +79,20 @@ _CALLS = {
     "ssm_gated_norm_bwd": (7, (SsmGatedNormDims,)),
     "ssm_add_norm_fwd": (7, (SsmAddNormDims,)),
     "ssm_add_norm_bwd": (12, (SsmAddNormDims,)),
+    "ssm_delta_fwd": (10, (SsmLinattnDims,)),
+    "ssm_delta_step": (8, (SsmLinattnDims,)),
+    "ssm_delta_bwd": (9, (SsmDeltaGrads, SsmLinattnDims)),
+    "ssm_layer_norm_fwd": (4, (SsmLayerNormDims,)),
+    "ssm_layer_norm_bwd": (6, (SsmLayerNormDims,)),
 }
 _SIZES = {
     "ssm_linattn_fwd_workspace_bytes": SsmLinattnDims,
     "ssm_linattn_bwd_workspace_bytes": SsmLinattnDims,
     "ssm_gated_norm_bwd_workspace_bytes": SsmGatedNormDims,
     "ssm_add_norm_bwd_workspace_bytes": SsmAddNormDims,
+    "ssm_delta_fwd_workspace_bytes": SsmLinattnDims,
+    "ssm_delta_bwd_workspace_bytes": SsmLinattnDims,
+    "ssm_layer_norm_bwd_workspace_bytes": SsmLayerNormDims,
 }
 EXPORTED = tuple(_CALLS) + tuple(_SIZES)
 
@@ -183,6 +206,50 @@ def ssm_gated_norm_bwd_workspace_bytes(dims) -> int:
 
 def ssm_add_norm_bwd_workspace_bytes(dims) -> int:
     return int(_fn("ssm_add_norm_bwd_workspace_bytes")(_ref(dims)))
+
+
+def ssm_delta_fwd(q, k, v, g, beta, cu_seqlens, slots, s0, o, s_last, dims, stream=None) -> int:
+    """C entry point of the delta rule's forward; returns the status."""
+    return _call("ssm_delta_fwd", (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+                                   _ptr(cu_seqlens), _ptr(slots), _ptr(s0), o.data_ptr(), _ptr(s_last), _ref(dims)),
+                 q.get_device(), stream)
+
+
+def ssm_delta_step(q, k, v, g, beta, slots, states, o, dims, stream=None) -> int:
+    """C entry point of the delta rule's single-token step; returns the status."""
+    return _call("ssm_delta_step", (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(slots),
+                                    states.data_ptr(), o.data_ptr(), _ref(dims)), q.get_device(), stream)
+
+
+def ssm_delta_bwd(q, k, v, g, beta, cu_seqlens, s0, do, ds_last, grads, dims, stream=None) -> int:
+    """C entry point of the delta rule's gradients; returns the status."""
+    return _call("ssm_delta_bwd", (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+                                   _ptr(cu_seqlens), _ptr(s0), do.data_ptr(), _ptr(ds_last), _ref(grads), _ref(dims)),
+                 q.get_device(), stream)
+
+
+def ssm_layer_norm_fwd(x, w, b, y, dims, stream=None) -> int:
+    """C entry point of the layer norm; returns the status."""
+    return _call("ssm_layer_norm_fwd", (x.data_ptr(), w.data_ptr(), _ptr(b), y.data_ptr(), _ref(dims)), x.get_device(),
+                 stream)
+
+
+def ssm_layer_norm_bwd(x, w, dy, dx, dw, db, dims, stream=None) -> int:
+    """C entry point of the layer norm's gradients; returns the status."""
+    return _call("ssm_layer_norm_bwd", (x.data_ptr(), w.data_ptr(), dy.data_ptr(), dx.data_ptr(), dw.data_ptr(), _ptr(db),
+                                        _ref(dims)), x.get_device(), stream)
+
+
+def ssm_delta_fwd_workspace_bytes(dims) -> int:
+    return int(_fn("ssm_delta_fwd_workspace_bytes")(_ref(dims)))
+
+
+def ssm_delta_bwd_workspace_bytes(dims) -> int:
+    return int(_fn("ssm_delta_bwd_workspace_bytes")(_ref(dims)))
+
+
+def ssm_layer_norm_bwd_workspace_bytes(dims) -> int:
+    return int(_fn("ssm_layer_norm_bwd_workspace_bytes")(_ref(dims)))
 
 
 # ------------------------------------------------------------------ checks
@@ -441,6 +508,104 @@ def linattn_bwd(q, k, v, g, *, do, scale=1.0, cu_seqlens=None, s0=None, ds_last=
     return res
 
 
+# ------------------------------------------------------------------ the gated delta rule
+def _delta_dims(q, k, v, g, beta, scale, nseq):
+    import torch
+
+    dims = _linattn_dims(q, k, v, g, scale, nseq)
+    _dense("beta", beta, torch.float32, v.shape[:-1])
+    return dims
+
+
+def delta_fwd(q, k, v, g, beta, *, scale=1.0, cu_seqlens=None, s0=None, s_last=None, slots=None, return_state=False,
+              out=None, workspace=None, piece_len=0, stream=None):
+    """The gated delta rule: S' = e^{g_t} S_{t-1}, S_t = S' + beta_t k_t (v_t - S'^T k_t)^T,
+    o_t = scale S_t^T q_t.
+
+    beta: float32 (tokens, heads) (or (batch, L, heads)); the other arguments, and what is
+    returned, are those of linattn_fwd.  Keys are taken as they are: states stay bounded where
+    0 <= beta |k|^2 <= 2.
+    """
+    import torch
+
+    _device(q, k, v, g, beta, cu_seqlens, s0, s_last, slots, out, workspace)
+    nseq = _packed(q, cu_seqlens)
+    dims = _delta_dims(q, k, v, g, beta, scale, nseq)
+    dims.piece_len = piece_len
+    with _on(stream):
+        if return_state or s0 is not None or s_last is not None:
+            s_last = _states(dims, q, s0, s_last, slots, return_state)
+        if slots is not None:
+            _dense("slots", slots, torch.int32, (dims.nseq,))
+        o = _rows_out(out, v, dims)
+        need = _fn("ssm_delta_fwd_workspace_bytes")(_ref(dims))
+        workspace, dims.workspace_bytes = _workspace(need, workspace, q.device)
+        dims.workspace = _ptr(workspace)
+        st = ssm_delta_fwd(q, k, v, g, beta, cu_seqlens, slots, s0, o, s_last, dims, stream)
+    _ok(st, "ssm_delta_fwd")
+    return (o, s_last) if return_state else o
+
+
+def delta_step(q, k, v, g, beta, states, *, slots=None, scale=1.0, out=None, stream=None):
+    """One token of each sequence: q, k (batch, kheads, dk), v (batch, heads, dv), g
+    (batch, heads) or (heads,), beta (batch, heads); states float32 (nslots, heads, dk, dv),
+    updated in place; slots int32 (batch,) names each sequence's state (default: in order).
+    Rows whose slot is out of range or named before are skipped.  Returns o."""
+    import torch
+
+    _device(q, k, v, g, beta, states, slots, out)
+    sq = q.shape
+    if len(sq) != 3:
+        raise ValueError("q must be (batch, heads, dk)")
+    dims = _delta_dims(q, k, v, g, beta, scale, sq[0])
+    ss = states.shape
+    dims.nslots = ss[0]
+    _dense("states", states, torch.float32, (ss[0], v.shape[1], sq[2], v.shape[2]))
+    if slots is not None:
+        _dense("slots", slots, torch.int32, (sq[0],))
+    with _on(stream):
+        o = _rows_out(out, v, dims)
+        st = ssm_delta_step(q, k, v, g, beta, slots, states, o, dims, stream)
+    _ok(st, "ssm_delta_step")
+    return o
+
+
+def delta_bwd(q, k, v, g, beta, *, do, scale=1.0, cu_seqlens=None, s0=None, ds_last=None, workspace=None, piece_len=0,
+              stream=None) -> dict:
+    """Gradients of sum(do * o) + sum(ds_last * s_last) of delta_fwd with the same inputs
+    (states in the order of the sequences).  Returns a dict: dq, dk, dv (q's dtype), dg
+    (float32, g's shape), dbeta (float32) and, with s0, ds0 (float32).  Rows of no sequence are
+    zero."""
+    import torch
+
+    _device(q, k, v, g, beta, do, cu_seqlens, s0, ds_last, workspace)
+    nseq = _packed(q, cu_seqlens)
+    dims = _delta_dims(q, k, v, g, beta, scale, nseq)
+    dims.piece_len = piece_len
+    if do.dtype is not v.dtype or do.shape != v.shape:
+        raise ValueError("do must have the shape and dtype of v")
+    dims.o_stride = _step("do", do, do.shape)
+    state = (dims.nseq, dims.nheads, dims.dk, dims.dv)
+    for name, t in (("s0", s0), ("ds_last", ds_last)):
+        if t is not None:
+            _dense(name, t, torch.float32, state)
+    dims.nslots = dims.nseq
+    dev = q.device
+    with _on(stream):
+        res = {"dq": torch.empty(q.shape, dtype=q.dtype, device=dev), "dk": torch.empty(k.shape, dtype=q.dtype, device=dev),
+               "dv": torch.empty(v.shape, dtype=q.dtype, device=dev), "dg": torch.empty(g.shape, dtype=g.dtype, device=dev),
+               "dbeta": torch.empty(beta.shape, dtype=beta.dtype, device=dev)}
+        if s0 is not None:
+            res["ds0"] = torch.empty(state, dtype=s0.dtype, device=dev)
+        need = _fn("ssm_delta_bwd_workspace_bytes")(_ref(dims))
+        workspace, dims.workspace_bytes = _workspace(need, workspace, dev)
+        dims.workspace = _ptr(workspace)
+        grads = SsmDeltaGrads(*[_ptr(res.get(n)) for n, _ in SsmDeltaGrads._fields_])
+        st = ssm_delta_bwd(q, k, v, g, beta, cu_seqlens, s0, do, ds_last, grads, dims, stream)
+    _ok(st, "ssm_delta_bwd")
+    return res
+
+
 # ------------------------------------------------------------------ norms
 def _matrix(name, t, sh):
     """Elements between the rows of a tensor whose leading dimensions collapse (0: packed)."""
@@ -600,4 +765,54 @@ def add_norm_bwd(x, r, weight, *, dy, dr=None, scale=None, post_weight=None, eps
         dims.workspace = _ptr(workspace)
         _ok(ssm_add_norm_bwd(x, r, scale, post_weight, weight, dy, dr, res["dx"], res["dresidual"], res["dweight"],
                              res.get("dscale"), res.get("dpost_weight"), dims, stream), "ssm_add_norm_bwd")
+    return res
+
+
+def _layer_dims(x, weight, bias, eps):
+    import torch
+
+    sh = x.shape
+    sx, dim = _matrix("x", x, sh), sh[-1]
+    _dense("weight", weight, torch.float32, (dim,))
+    if bias is not None:
+        _dense("bias", bias, torch.float32, (dim,))
+    return SsmLayerNormDims(_rows(x, sh), dim, sx, 0, _io("x", x), eps, None, 0)
+
+
+def layer_norm_fwd(x, weight, bias=None, *, eps=1e-5, out=None, stream=None):
+    """Layer norm of x's last dimension: (x - mean) / sqrt(var + eps) weight + bias.  weight, bias:
+    float32 (dim,), bias may be None; eps: 2^-126 or more.  out may be x.  Returns y, x's shape
+    and dtype."""
+    import torch
+
+    _device(x, weight, bias, out)
+    dims = _layer_dims(x, weight, bias, eps)
+    with _on(stream):
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        else:
+            if out.dtype is not x.dtype or out.shape != x.shape:
+                raise ValueError("out must have the shape and dtype of x")
+            dims.y_stride = _matrix("out", out, out.shape)
+        _ok(ssm_layer_norm_fwd(x, weight, bias, out, dims, stream), "ssm_layer_norm_fwd")
+    return out
+
+
+def layer_norm_bwd(x, weight, *, dy, bias=True, eps=1e-5, workspace=None, stream=None) -> dict:
+    """Gradients of sum(dy * y) of layer_norm_fwd: dx (x's dtype), dweight and, unless bias is
+    False, dbias (float32)."""
+    import torch
+
+    _device(x, weight, dy, workspace)
+    dims = _layer_dims(x, weight, None, eps)
+    _dense("dy", dy, x.dtype, x.shape)
+    with _on(stream):
+        res = {"dx": torch.empty(x.shape, dtype=x.dtype, device=x.device), "dweight": torch.empty_like(weight)}
+        if bias:
+            res["dbias"] = torch.empty_like(weight)
+        need = ssm_layer_norm_bwd_workspace_bytes(dims)
+        workspace, dims.workspace_bytes = _workspace(need, workspace, x.device)
+        dims.workspace = _ptr(workspace)
+        _ok(ssm_layer_norm_bwd(x, weight, dy, res["dx"], res["dweight"], res.get("dbias"), dims, stream),
+            "ssm_layer_norm_bwd")
     return res

@@ -1,0 +1,899 @@
+// delta_fwd.hip -- the gated delta rule: the triangular systems of all chunks, the walk over
+// them (packed sequences, cut into pieces along the tokens when there are few heads and
+// sequences) and the single-token step.
+#include "delta.h"
+
+namespace {
+namespace dl {
+
+using namespace ssm_detail;
+
+// ---------------------------------------------------------------- the triangular systems
+// A = (I + beta M)^-1 of one chunk and head, unit lower triangular.  The diagonal blocks of 16
+// by forward substitution, a column a lane; then the blocks below, -A_22 M_21 A_11, first of 16
+// in 32 and then of 32 in 64, in float32 products (with bf16 parts the splits would cost more
+// than these few products).  Forward substitution and not powers of M: for equal keys these
+// grow like binomials and cancel.
+template <int PARTS, int KD, int C>
+__global__ void __launch_bounds__(kThreads) delta_tri_kernel(DeltaPass p) {
+    constexpr int IT = C / 16, KB = KD / 32, NTILE = IT * (IT + 1) / 2, P = C + 4, NB = tri_blocks<C>();
+    __shared__ __align__(16) uint16_t K[PARTS * C * KD];
+    __shared__ __align__(16) float M[C * P], A[C * P];
+    __shared__ Steps<C> st;
+    const int tid = threadIdx.x, lane = tid & 63, g4 = lane >> 4, l16 = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const Chunks ch(p, C);
+    const int64_t ci = blockIdx.x;
+    const int h = blockIdx.y;
+    const int seq = find_seq(ch, ci);
+    if (seq < 0) return;
+    const Seq sq = seq_range(ch, seq);
+    const int64_t c0 = sq.start + (ci - piece_base(ch, seq)) * C;
+    if (c0 < sq.start || c0 >= sq.end) return;
+    Rows<PARTS, C, KD, kThreads> rk;
+    rk.prepare(p.k, int64_t(h / p.rep) * p.dk, p.sk, p.dk, tid);
+    if (p.wide) {
+        rk.load(K, wave, c0, sq.end);
+        if constexpr (PARTS > 1) rk.store(K, tid);
+    } else {
+        rk.copy(K, tid, c0, sq.end);
+    }
+    if (wave == 3) {
+        const int64_t t = c0 + lane;
+        const bool on = lane < C && t < sq.end;
+        put_steps<C>(st, on ? p.g[t * p.sg + h] : 0.0f, on ? p.beta[t * p.H + h] : 0.0f, lane);
+    }
+    wait_memory<0>();
+    __syncthreads();
+    const uint32_t base = row_base<KD>(lane);
+    for (int m = wave; m < NTILE; m += 4) {
+        const int it = m < 1 ? 0 : m < 3 ? 1 : m < 6 ? 2 : 3, jt = m - it * (it + 1) / 2;
+        f32x4 a = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+            u32x4 x[PARTS], y[PARTS];
+#pragma unroll
+            for (int i = 0; i < PARTS; ++i) {
+                x[i] = row_op<KD>(K + i * C * KD, 16 * jt, kb, base);
+                y[i] = row_op<KD>(K + i * C * KD, 16 * it, kb, base);
+            }
+            a = mma_parts<PARTS, PARTS>(x, y, a);
+        }
+        const int i = 16 * it + l16, j0 = 16 * jt + 4 * g4;
+        const float gi = st.hi[i], ei = st.lo[i], b = st.beta[i];
+        f32x4 w;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            w[r] = j0 + r < i ? a[r] * (b * __builtin_amdgcn_exp2f((gi - st.hi[j0 + r]) + (ei - st.lo[j0 + r]))) : 0.0f;
+        *reinterpret_cast<f32x4*>(&M[i * P + j0]) = w;
+    }
+    __syncthreads();
+    if (wave == 0 && g4 < IT) {
+        float x[16];
+        const float* m = M + (16 * g4) * P + 16 * g4;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float v = i == l16 ? 1.0f : 0.0f;
+#pragma unroll
+            for (int j4 = 0; j4 < i; j4 += 4) {
+                const f32x4 w = *reinterpret_cast<const f32x4*>(m + i * P + j4);
+#pragma unroll
+                for (int j = j4; j < j4 + 4 && j < i; ++j) v = fmaf(-w[j - j4], x[j], v);
+            }
+            x[i] = v;
+            A[(16 * g4 + i) * P + 16 * g4 + l16] = v;
+        }
+    }
+    __syncthreads();
+    const auto f32 = [](float a, float b, const f32x4& c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); };
+    // 16 in 32: of the contraction, lane group g takes 4g + r in step r, so that a float4 is the
+    // left operand of four steps and a product the right one of the next
+    if (wave < IT / 2) {
+        const int a0 = 32 * wave, b0 = a0 + 16;
+        const f32x4 m = *reinterpret_cast<const f32x4*>(&M[(b0 + l16) * P + a0 + 4 * g4]);
+        f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f}, y = x;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x = f32(m[r], A[(a0 + 4 * g4 + r) * P + a0 + l16], x);
+        const f32x4 a = *reinterpret_cast<const f32x4*>(&A[(b0 + l16) * P + b0 + 4 * g4]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) y = f32(a[r], x[r], y);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) A[(b0 + 4 * g4 + r) * P + a0 + l16] = -y[r];
+    }
+    __syncthreads();
+    if constexpr (C == 64) {   // 32 in 64, 16 columns a wave
+        if (wave < 2) {
+            f32x4 x[2];
+#pragma unroll
+            for (int rt = 0; rt < 2; ++rt) {
+                x[rt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                for (int kt = wave; kt < 2; ++kt) {   // A's first block row has no second block
+                    const f32x4 m = *reinterpret_cast<const f32x4*>(&M[(32 + 16 * rt + l16) * P + 16 * kt + 4 * g4]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) x[rt] = f32(m[r], A[(16 * kt + 4 * g4 + r) * P + 16 * wave + l16], x[rt]);
+                }
+            }
+#pragma unroll
+            for (int rt = 0; rt < 2; ++rt) {
+                f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int kt = 0; kt <= rt; ++kt) {
+                    const f32x4 a = *reinterpret_cast<const f32x4*>(&A[(32 + 16 * rt + l16) * P + 32 + 16 * kt + 4 * g4]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) y = f32(a[r], x[kt][r], y);
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) A[(32 + 16 * rt + 4 * g4 + r) * P + 16 * wave + l16] = -y[r];
+            }
+        }
+        __syncthreads();
+    }
+    // out: tiles in paired rows, the pieces of a row as the walk's reads want them
+    uint16_t* const out = p.tri + (ci * p.H + h) * tri_elems<C>();
+    const int m = lane >> 2, piece = (lane & 3) ^ twist<32>(m);
+    for (int b = wave; b < NB; b += 4) {
+        const int it = C == 32 ? b : b < 2 ? b : 2 + (b - 2) / 2, jb = C == 32 ? 0 : b < 2 ? 0 : (b - 2) & 1;
+        const int i = 32 * (it >> 1) + 8 * (m >> 2) + 4 * (it & 1) + (m & 3), j0 = 32 * jb + 8 * piece;
+        u32x4 v[3];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int j = j0 + 2 * e;
+            uint32_t w[3];
+            split<3>(j <= i ? A[i * P + j] : 0.0f, j + 1 <= i ? A[i * P + j + 1] : 0.0f, w);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) v[k][e] = w[k];
+        }
+#pragma unroll
+        for (int k = 0; k < 3; ++k) *reinterpret_cast<u32x4*>(out + (k * NB + b) * 512 + 8 * lane) = v[k];
+    }
+}
+
+// ---------------------------------------------------------------- the walk
+// One workgroup walks one piece of one head's sequence for 64 columns of the state, 16 a wave.
+template <int PARTS, int KD, int C, int MODE>
+__global__ void __launch_bounds__(kThreads, KD == 256 ? 1 : 2) delta_pass_kernel(DeltaPass p) {
+    constexpr bool FULL = MODE == kDeltaFull, KEEP = MODE == kDeltaKeep, DMA = PARTS == 1;
+    constexpr int IT = C / 16, JB = C / 32, KB = KD / 32, NTILE = IT * (IT + 1) / 2, NB = tri_blocks<C>(), PB = NB * 512;
+    constexpr int WP = 3;   // parts of what is not a bf16 input
+    __shared__ __align__(16) uint16_t K[PARTS * C * KD], V[PARTS * C * kCols], A[WP * PB];
+    __shared__ __align__(16) uint16_t Q[FULL ? PARTS * C * KD : 8], Ps[FULL ? WP * PB : 8];
+    __shared__ Steps<C> steps[2];
+    const int tid = threadIdx.x, lane = tid & 63, g4 = lane >> 4, l16 = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const Where w = find_piece(p, MODE == kDeltaStates ? p.vslices + p.kslices : p.vslices, !KEEP);
+    // columns of the transition: the same walk from the unit matrix, without values
+    const bool trans = MODE == kDeltaStates && w.slice >= p.vslices;
+    // no piece starts from a last one's state, but its transition leads back in the gradients
+    if (!w.on || (MODE == kDeltaStates && w.last && !(trans && p.trans_t))) return;
+    const int width = trans ? p.dk : p.dv, h = w.h;
+    const int c_slice = (trans ? w.slice - p.vslices : w.slice) * kCols, c_wave = c_slice + 16 * wave, col = c_wave + l16;
+    const bool active = c_wave < width;                      // this wave has columns
+    const int64_t lo = w.lo, hi = w.hi, ssz = int64_t(p.dk) * p.dv;
+
+    f32x4 S[2 * KB];
+    const float* src = nullptr;
+    if constexpr (MODE != kDeltaStates) {
+        if (p.pieced && w.sq.end - w.sq.start > p.piece)
+            src = p.carry + (w.pi * p.H + h) * ssz;
+        else if (p.s_in)
+            src = p.s_in + (int64_t(w.slot) * p.H + h) * ssz;
+    }
+#pragma unroll
+    for (int m = 0; m < 2 * KB; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = 32 * (m >> 1) + 8 * g4 + 4 * (m & 1) + r;
+            S[m][r] = trans ? (row == col ? 1.0f : 0.0f) : src && row < p.dk && col < p.dv ? src[int64_t(row) * p.dv + col] : 0.0f;
+        }
+    if constexpr (FULL) {   // tiles above the diagonal that share a block with one on it stay zero
+        for (int i = tid; i < WP * PB / 2; i += kThreads) reinterpret_cast<uint32_t*>(Ps)[i] = 0;
+    }
+
+    const int64_t nch = (hi - lo + C - 1) / C;
+    const Chunks ch(p, C);
+    const int64_t first = uniform(piece_base(ch, w.seq)) + (lo - w.sq.start) / C;
+    const uint16_t* const tri = p.tri + (first * p.H + h) * tri_elems<C>();
+    auto load_a = [&](int64_t n, int lane) { load_tri<C, 4>(tri + n * p.H * tri_elems<C>(), A, wave, lane); };
+    const bool step_wave = wave == 3;
+    float gn = 0.0f, bn = 0.0f;
+    auto fetch = [&](int64_t n, int lane) {
+        const int64_t t = lo + n * C + lane;
+        const bool on = n < nch && lane < C && t < hi;
+        gn = on ? p.g[t * p.sg + h] : 0.0f;
+        bn = on ? p.beta[t * p.H + h] : 0.0f;
+    };
+    if (step_wave) {
+        fetch(0, lane);
+        put_steps<C>(steps[0], gn, bn, lane);
+        fetch(1, lane);
+    }
+    Rows<PARTS, C, KD, kThreads> rk, rq;
+    Rows<PARTS, C, kCols, kThreads> rv;
+    rk.prepare(p.k, int64_t(h / p.rep) * p.dk, p.sk, p.dk, tid);
+    rq.prepare(p.q, int64_t(h / p.rep) * p.dk, p.sq, p.dk, tid);
+    rv.prepare(p.v, int64_t(h) * p.dv + c_slice, p.sv, p.dv - c_slice, tid);
+    const bool ahead = DMA && p.wide;
+    if (nch > 0) {
+        if (p.wide) {
+            rk.load(K, wave, lo, hi);
+            if (!trans) rv.load(V, wave, lo, hi);
+            if constexpr (FULL) rq.load(Q, wave, lo, hi);
+        }
+        load_a(0, lane);
+    }
+    wait_memory<0>();
+
+    for (int64_t n = 0; n < nch; ++n) {
+        const int64_t c0 = lo + n * C;
+        const Steps<C>& st = steps[n & 1];
+        // the lane as the loop's own value: operand addresses are cheap to form anew
+        int lane = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+        asm volatile("" : "+v"(lane));
+        const int tid = 64 * wave + lane, g4 = lane >> 4, l16 = lane & 15;
+        if (ahead) {
+            wait_memory<0>();
+            lds_barrier();
+        } else {
+            wait_memory<0>();
+            lds_barrier();
+            if (!DMA && p.wide) {
+                rk.store(K, tid);
+                if (!trans) rv.store(V, tid);
+                if constexpr (FULL) rq.store(Q, tid);
+                if (n + 1 < nch) {
+                    rk.load(K, wave, c0 + C, hi);
+                    if (!trans) rv.load(V, wave, c0 + C, hi);
+                    if constexpr (FULL) rq.load(Q, wave, c0 + C, hi);
+                }
+            } else {
+                rk.copy(K, tid, c0, hi);
+                if (!trans) rv.copy(V, tid, c0, hi);
+                if constexpr (FULL) rq.copy(Q, tid, c0, hi);
+            }
+            lds_barrier();
+        }
+        if constexpr (KEEP) {
+            if (active) {
+                float* const at = p.keep + ((first + n) * p.H + h) * ssz;
+#pragma unroll
+                for (int m = 0; m < 2 * KB; ++m)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int row = 32 * (m >> 1) + 8 * g4 + 4 * (m & 1) + r;
+                        if (row < p.dk && col < p.dv) at[int64_t(row) * p.dv + col] = S[m][r];
+                    }
+            }
+        }
+        const uint32_t base = row_base<KD>(lane), bpair = pair_base<KD>(lane);
+        if constexpr (FULL) {
+            // ---- P, tiles on and below the diagonal
+            for (int m = wave; m < NTILE; m += 4) {
+                const int it = m < 1 ? 0 : m < 3 ? 1 : m < 6 ? 2 : 3, jt = m - it * (it + 1) / 2;
+                f32x4 a = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) {
+                    u32x4 x[PARTS], y[PARTS];
+#pragma unroll
+                    for (int i = 0; i < PARTS; ++i) {
+                        x[i] = row_op<KD>(K + i * C * KD, 16 * jt, kb, base);
+                        y[i] = row_op<KD>(Q + i * C * KD, 16 * it, kb, base);
+                    }
+                    a = mma_parts<PARTS, PARTS>(x, y, a);
+                }
+                const int i = 16 * it + l16, j0 = 16 * jt + 4 * g4;
+                const int o = p_block(it, jt >> 1) * 512 + at_piece<32>(l16, 2 * (jt & 1) + (g4 >> 1)) + 4 * (g4 & 1);
+                const float gi = st.hi[i], ei = st.lo[i];
+                const f32x4 gj = *reinterpret_cast<const f32x4*>(&st.hi[j0]), ej = *reinterpret_cast<const f32x4*>(&st.lo[j0]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float e = __builtin_amdgcn_exp2f((gi - gj[r]) + (ei - ej[r]));
+                    a[r] = j0 + r <= i ? a[r] * (e * p.scale) : 0.0f;
+                }
+                uint32_t x[WP], y[WP];
+                split<WP>(a[0], a[1], x);
+                split<WP>(a[2], a[3], y);
+#pragma unroll
+                for (int k = 0; k < WP; ++k) *reinterpret_cast<uint2*>(Ps + k * PB + o) = uint2{x[k], y[k]};
+            }
+        }
+        if (step_wave && n + 1 < nch) {
+            put_steps<C>(steps[(n + 1) & 1], gn, bn, lane);
+            fetch(n + 2, lane);
+        }
+        // ---- what the state is read for: K S (paired rows) and Q S
+        f32x4 acc[IT], o[IT];
+        u32x4 xp[JB][WP];
+        if (active) {
+#pragma unroll
+            for (int i = 0; i < IT; ++i) acc[i] = o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+                u32x4 sp[WP];
+                pair_parts<WP>(S[2 * kb], S[2 * kb + 1], sp);
+#pragma unroll
+                for (int i = 0; i < IT; ++i) {
+                    u32x4 a[PARTS];
+#pragma unroll
+                    for (int x = 0; x < PARTS; ++x) a[x] = pair_op<KD>(K + x * C * KD, 32 * (i >> 1), i & 1, kb, bpair);
+                    acc[i] = mma_parts<PARTS, WP>(a, sp, acc[i]);
+                }
+                if constexpr (FULL) {
+#pragma unroll
+                    for (int i = 0; i < IT; ++i) {
+                        u32x4 a[PARTS];
+#pragma unroll
+                        for (int x = 0; x < PARTS; ++x) a[x] = row_op<KD>(Q + x * C * KD, 16 * i, kb, base);
+                        o[i] = mma_parts<PARTS, WP>(a, sp, o[i]);
+                    }
+                }
+            }
+            // beta X = beta V - beta e^G K S
+            const uint32_t bv = col_base<kCols, 0>(16 * wave, lane);
+#pragma unroll
+            for (int jb = 0; jb < JB; ++jb) {
+                f32x4 x[2];
+                u32x4 v[PARTS];
+                if (!trans) {
+#pragma unroll
+                    for (int i = 0; i < PARTS; ++i) v[i] = col_op<kCols>(V + i * C * kCols, 32 * jb, 0, 0, bv);
+                }
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int t0 = 32 * jb + 8 * g4 + 4 * half;
+                    const f32x4 f = *reinterpret_cast<const f32x4*>(&st.bin[t0]), b = *reinterpret_cast<const f32x4*>(&st.beta[t0]);
+#pragma unroll
+                    for (int r = 0; r < 4; r += 2) {
+                        float y = 0.0f, z = 0.0f;
+                        if (!trans) unpack<PARTS>(v, 2 * half + r / 2, y, z);
+                        x[half][r] = fmaf(-f[r], acc[2 * jb + half][r], b[r] * y);
+                        x[half][r + 1] = fmaf(-f[r + 1], acc[2 * jb + half][r + 1], b[r + 1] * z);
+                    }
+                }
+                pair_parts<WP>(x[0], x[1], xp[jb]);
+            }
+            if constexpr (FULL) {
+#pragma unroll
+                for (int i = 0; i < IT; ++i) {
+                    const f32x4 e = *reinterpret_cast<const f32x4*>(&st.in[16 * i + 4 * g4]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) o[i][r] *= e[r] * p.scale;
+                }
+            }
+        }
+        lds_barrier();      // P is there; q and v have been read
+        if (ahead && n + 1 < nch) {
+            if (!trans) rv.load(V, wave, c0 + C, hi);
+            if constexpr (FULL) rq.load(Q, wave, c0 + C, hi);
+        }
+        const uint32_t b32 = row_base<32>(lane);
+        if (active) {
+            // ---- U = A beta X
+#pragma unroll
+            for (int i = 0; i < IT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < IT; ++i)
+#pragma unroll
+                for (int jb = 0; jb <= i / 2; ++jb) {
+                    u32x4 a[WP];
+#pragma unroll
+                    for (int k = 0; k < WP; ++k) a[k] = row_op<32>(A + k * PB + p_block(i, jb) * 512, 0, 0, b32);
+                    acc[i] = mma_parts<WP, WP>(a, xp[jb], acc[i]);
+                }
+            // ---- the outgoing state
+            const uint32_t bk = col_base<KD, 1>(0, lane);
+            const float tail = st.tail;
+#pragma unroll
+            for (int m = 0; m < 2 * KB; ++m)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) S[m][r] *= tail;
+#pragma unroll
+            for (int jb = 0; jb < JB; ++jb) {
+                f32x4 x[2];
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const f32x4 f = *reinterpret_cast<const f32x4*>(&st.out[32 * jb + 8 * g4 + 4 * half]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) x[half][r] = acc[2 * jb + half][r] * f[r];
+                }
+                u32x4 up[WP];
+                pair_parts<WP>(x[0], x[1], up);
+#pragma unroll
+                for (int m = 0; m < 2 * KB; ++m) {
+                    u32x4 k[PARTS];
+#pragma unroll
+                    for (int i = 0; i < PARTS; ++i) k[i] = col_op<KD>(K + i * C * KD, 32 * jb, m >> 1, m & 1, bk);
+                    S[m] = mma_parts<PARTS, WP>(k, up, S[m]);
+                }
+            }
+        }
+        lds_barrier();      // k and A have been read
+        if (n + 1 < nch) {
+            if (ahead) rk.load(K, wave, c0 + C, hi);
+            load_a(n + 1, lane);
+        }
+        if constexpr (FULL) {
+            if (active) {
+                // ---- the chunk's own share, P U
+#pragma unroll
+                for (int jb = 0; jb < JB; ++jb) {
+                    u32x4 up[WP];
+                    pair_parts<WP>(acc[2 * jb], acc[2 * jb + 1], up);
+#pragma unroll
+                    for (int i = 2 * jb; i < IT; ++i) {
+                        u32x4 a[WP];
+#pragma unroll
+                        for (int k = 0; k < WP; ++k) a[k] = row_op<32>(Ps + k * PB + p_block(i, jb) * 512, 0, 0, b32);
+                        o[i] = mma_parts<WP, WP>(a, up, o[i]);
+                    }
+                }
+                constexpr int OE = PARTS == 1 ? 2 : 4;
+                const int64_t pitch = p.so * OE;
+                store_tiles<C, false>(o, static_cast<char*>(p.out) + c0 * pitch + int64_t(h) * p.dv * OE, pitch, hi - c0, c_wave,
+                                      p.dv, PARTS > 1, p.pairs, lane);
+            }
+        }
+    }
+
+    // ---------------------------------------------- the state that leaves
+    if (!active) return;
+    float *dst = nullptr, *dst_t = nullptr;
+    int64_t rs = p.dv;
+    if constexpr (MODE == kDeltaStates) {
+        if (trans) {
+            rs = p.dk;
+            dst = p.trans + (w.pi * p.H + h) * int64_t(p.dk) * p.dk;
+            if (p.trans_t) dst_t = p.trans_t + (w.pi * p.H + h) * int64_t(p.dk) * p.dk;
+        } else {
+            dst = p.carry + (w.pi * p.H + h) * ssz;
+        }
+    } else if (FULL && w.last && p.s_out) {
+        dst = p.s_out + (int64_t(w.slot) * p.H + h) * ssz;
+    }
+    if (!dst) return;
+#pragma unroll
+    for (int m = 0; m < 2 * KB; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = 32 * (m >> 1) + 8 * g4 + 4 * (m & 1) + r;
+            if (row < p.dk && col < width) {
+                dst[int64_t(row) * rs + col] = S[m][r];
+                if (dst_t) dst_t[int64_t(col) * p.dk + row] = S[m][r];
+            }
+        }
+}
+
+// ---------------------------------------------------------------- pieces' starting states
+// Walks the pieces of one sequence and head for 64 columns of the state: each piece's own end
+// state N is replaced by the state S it starts from, and the next one starts from W S + N with
+// the piece's transition W (against time its transpose).
+template <int KD, bool REV>
+__global__ void __launch_bounds__(kThreads) delta_carry_kernel(DeltaPass p) {
+    constexpr int KB = KD / 32, WP = 3;
+    const int lane = threadIdx.x & 63, g4 = lane >> 4, l16 = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int slice = blockIdx.x, h = blockIdx.y, seq = blockIdx.z;
+    const int slot = REV ? seq : find_slot(p.slots, p.nslots, seq);
+    if (slot < 0) return;
+    const Seq sq = seq_range(p, seq);
+    const int64_t base = uniform(piece_base(p, seq));
+    int64_t n = (sq.end - sq.start + p.piece - 1) / p.piece;
+    if (n < 2) return;   // a single piece starts from the user's state
+    if (base + n > p.npieces) n = p.npieces - base;
+    const int c_wave = slice * kCols + 16 * wave, col = c_wave + l16;
+    if (c_wave >= p.dv) return;
+    const int64_t ssz = int64_t(p.dk) * p.dv, tsz = int64_t(p.dk) * p.dk;
+    f32x4 S[2 * KB];
+    const auto row = [&](int m, int r) { return 32 * (m >> 1) + 8 * g4 + 4 * (m & 1) + r; };
+    const float* src = p.s_in ? p.s_in + (int64_t(slot) * p.H + h) * ssz : nullptr;
+#pragma unroll
+    for (int m = 0; m < 2 * KB; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            S[m][r] = src && row(m, r) < p.dk && col < p.dv ? src[int64_t(row(m, r)) * p.dv + col] : 0.0f;
+    const bool vec = p.dk % 4 == 0;
+    for (int64_t k = 0; k < n; ++k) {
+        const int64_t at = (base + (REV ? n - 1 - k : k)) * p.H + h;
+        float* const own = p.carry + at * ssz;
+        const float* const tr = (REV ? p.trans_t : p.trans) + at * tsz;
+        f32x4 N[2 * KB];
+#pragma unroll
+        for (int m = 0; m < 2 * KB; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const bool in = row(m, r) < p.dk && col < p.dv;
+                N[m][r] = in && k + 1 < n ? own[int64_t(row(m, r)) * p.dv + col] : 0.0f;
+                if (in) own[int64_t(row(m, r)) * p.dv + col] = S[m][r];
+            }
+        if (k + 1 == n) break;
+        u32x4 sp[KB][WP];
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) pair_parts<WP>(S[2 * kb], S[2 * kb + 1], sp[kb]);
+#pragma unroll
+        for (int m = 0; m < 2 * KB; ++m) {
+            const int out = 32 * (m >> 1) + 8 * (l16 >> 2) + 4 * (m & 1) + (l16 & 3);   // this lane's row of W
+            const float* const wr = tr + int64_t(out) * p.dk;
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+                const int c = 32 * kb + 8 * g4;
+                f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f}, y = x;
+                if (vec) {
+                    if (out < p.dk && c < p.dk) x = *reinterpret_cast<const f32x4*>(wr + c);
+                    if (out < p.dk && c + 4 < p.dk) y = *reinterpret_cast<const f32x4*>(wr + c + 4);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (out < p.dk && c + e < p.dk) x[e] = wr[c + e];
+                        if (out < p.dk && c + 4 + e < p.dk) y[e] = wr[c + 4 + e];
+                    }
+                }
+                u32x4 a[WP];
+                pair_parts<WP>(x, y, a);
+                N[m] = mma_parts<WP, WP>(a, sp[kb], N[m]);
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < 2 * KB; ++m) S[m] = N[m];
+    }
+}
+
+// ---------------------------------------------------------------- single tokens
+struct StepArgs {
+    const void* q;
+    const void* k;
+    const void* v;
+    const float* g;
+    const float* beta;
+    const int32_t* slots;
+    float* states;
+    void* o;
+    int64_t sq, sk, sv, so, sg;
+    int32_t H, rep, dk, dv, nslots, nslices, tpr_log2;
+    float scale;
+};
+
+// One workgroup per sequence, head and slice of up to 64 of the state's columns, which it holds
+// in registers: R rows of 4 columns a thread, all asked for at once.  What the old state holds
+// under k and under q is summed over the rows in one pass and one exchange, and the output is
+// (S'^T q + (k . q) u) scale, so the state is read once and written once.
+template <typename IO, int R>
+__global__ void __launch_bounds__(kThreads) delta_step_kernel(StepArgs p) {
+    constexpr int VW = 4;
+    __shared__ float sq[SSM_LINATTN_MAX_DIM], sk[SSM_LINATTN_MAX_DIM];
+    __shared__ __align__(16) float red[2][kThreads * VW];
+    __shared__ __align__(16) float us[kCols];
+    __shared__ float kq[kWaves];
+    __shared__ int dups[kWaves];
+    const int tid = threadIdx.x;
+    const int per = p.H * p.nslices;
+    const int b = blockIdx.x / per, at = blockIdx.x % per, h = at / p.nslices, slice = at % p.nslices;
+    int slot = b;
+    bool dup = false;
+    if (p.slots) {
+        slot = p.slots[b];
+        if (slot < 0 || slot >= p.nslots) return;
+        for (int i = tid; i < b; i += kThreads) dup = dup || p.slots[i] == slot;
+    }
+    const int tpr = 1 << p.tpr_log2, rows = kThreads >> p.tpr_log2;
+    const int r0 = tid >> p.tpr_log2, c0 = VW * (tid & (tpr - 1)), w = VW * tpr, col = slice * w + c0;
+    const bool on = col < p.dv, whole = col + VW <= p.dv;
+    float* S = p.states + (int64_t(slot) * p.H + h) * p.dk * p.dv + col;
+    f32x4 s[R];
+#pragma unroll
+    for (int n = 0; n < R; ++n) {
+        const int r = r0 + n * rows;
+        s[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (on && r < p.dk) {
+            if (whole) {
+                __builtin_memcpy(&s[n], S + int64_t(r) * p.dv, sizeof(s[n]));
+            } else {
+#pragma unroll
+                for (int e = 0; e < VW; ++e)
+                    if (col + e < p.dv) s[n][e] = S[int64_t(r) * p.dv + e];
+            }
+        }
+    }
+    const IO* q = static_cast<const IO*>(p.q) + b * p.sq + int64_t(h / p.rep) * p.dk;
+    const IO* k = static_cast<const IO*>(p.k) + b * p.sk + int64_t(h / p.rep) * p.dk;
+    float both = 0.0f;
+    {
+        const float x = tid < p.dk ? IOT<IO>::to_f32(q[tid]) : 0.0f, y = tid < p.dk ? IOT<IO>::to_f32(k[tid]) : 0.0f;
+        sq[tid] = x;
+        sk[tid] = y;
+        both = x * y;
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) both += __shfl_xor(both, d);
+    if ((tid & 63) == 0) kq[tid >> 6] = both;
+    if (p.slots) {
+        const bool any = __ballot(dup) != 0;
+        if ((tid & 63) == 0) dups[tid >> 6] = any;
+    }
+    float g = p.g[b * p.sg + h];
+    g = g < kMinDecay ? kMinDecay : g;
+    const float a = __builtin_amdgcn_exp2f(g * kLog2e), beta = p.beta[int64_t(b) * p.H + h];
+    float v = 0.0f;
+    if (tid < w && slice * w + tid < p.dv) v = IOT<IO>::to_f32(static_cast<const IO*>(p.v)[b * p.sv + int64_t(h) * p.dv + slice * w + tid]);
+    __syncthreads();
+    if (p.slots && (dups[0] | dups[1] | dups[2] | dups[3])) return;
+    f32x4 xk = {0.0f, 0.0f, 0.0f, 0.0f}, xq = xk;
+#pragma unroll
+    for (int n = 0; n < R; ++n) {
+        const int r = r0 + n * rows;
+        if (r < p.dk) {
+            xk += sk[r] * s[n];
+            xq += sq[r] * s[n];
+        }
+    }
+    *reinterpret_cast<f32x4*>(&red[0][tid * VW]) = xk;
+    *reinterpret_cast<f32x4*>(&red[1][tid * VW]) = xq;
+    __syncthreads();
+    if (tid < w) {
+        float y = 0.0f, z = 0.0f;
+        for (int r = 0; r < rows; ++r) {
+            y += red[0][r * w + tid];
+            z += red[1][r * w + tid];
+        }
+        const float u = beta * fmaf(-a, y, v);
+        us[tid] = u;
+        const int cc = slice * w + tid;
+        if (cc < p.dv)
+            static_cast<IO*>(p.o)[b * p.so + int64_t(h) * p.dv + cc] =
+                IOT<IO>::from_f32(p.scale * fmaf((kq[0] + kq[1]) + (kq[2] + kq[3]), u, a * z));
+    }
+    __syncthreads();
+    const f32x4 u = *reinterpret_cast<const f32x4*>(&us[c0]);
+#pragma unroll
+    for (int n = 0; n < R; ++n) {
+        const int r = r0 + n * rows;
+        if (!(on && r < p.dk)) continue;
+        const f32x4 x = a * s[n] + sk[r] * u;
+        if (whole) {
+            __builtin_memcpy(S + int64_t(r) * p.dv, &x, sizeof(x));
+        } else {
+#pragma unroll
+            for (int e = 0; e < VW; ++e)
+                if (col + e < p.dv) S[int64_t(r) * p.dv + e] = x[e];
+        }
+    }
+}
+
+// ---------------------------------------------------------------- host: plans
+struct Plan {
+    int chunk;
+    int64_t nchunks, piece, npieces;
+    bool pieced;
+    size_t tri, carry, trans;   // bytes
+    size_t bytes() const { return tri + carry + trans; }
+};
+
+// Pieces along the tokens cost a walk from zero and one from the unit matrix before the walk for
+// the outputs: they pay where the card would stand mostly idle.
+inline int64_t choose_piece(const ssm_linattn_dims* d, int64_t each) {
+    const int64_t units = d->nheads * cdiv(d->dv, kCols) * (d->tokens / each);
+    const int64_t want = 512 / units;
+    if (want < 5 || each < 1024) return 0;
+    int64_t piece = cdiv(cdiv(each, want), 64) * 64;
+    if (piece < 512) piece = 512;
+    return piece < each ? piece : 0;
+}
+
+inline int make_plan(const ssm_linattn_dims* d, bool packed, Plan* pl) {
+    pl->chunk = d->io_dtype == SSM_BF16 ? 64 : 32;
+    const int64_t vs = cdiv(d->dv, kCols), ks = cdiv(d->dk, kCols);
+    const int64_t each = packed ? d->tokens : d->tokens / d->nseq;
+    int64_t piece = d->piece_len;
+    if (piece == 0) piece = choose_piece(d, each);
+    pl->pieced = piece > 0 && piece < each;
+    pl->piece = pl->pieced ? piece : (int64_t(1) << 31);
+    pl->npieces = !pl->pieced ? d->nseq : packed ? d->tokens / piece + d->nseq : d->nseq * cdiv(each, piece);
+    pl->nchunks = count_chunks(d, packed, pl->chunk);
+    if (pl->npieces > kMostGroups / (d->nheads * (vs + ks)) || pl->nchunks > 2 * kMostGroups) return SSM_ERR_DIMS;
+    const int64_t tri = pl->chunk == 64 ? tri_elems<64>() : tri_elems<32>();
+    pl->tri = up256(static_cast<size_t>(pl->nchunks * d->nheads * tri) * 2);
+    pl->carry = pl->pieced ? up256(static_cast<size_t>(pl->npieces * d->nheads * d->dk * d->dv) * 4) : 0;
+    pl->trans = pl->pieced ? up256(static_cast<size_t>(pl->npieces * d->nheads * d->dk * d->dk) * 4) : 0;
+    return SSM_OK;
+}
+
+template <int C> void run_tri(const DeltaPass& p, bool f32, int64_t nchunks, hipStream_t s) {
+    const dim3 grid(static_cast<uint32_t>(nchunks), p.H), block(kThreads);
+#define SSM_TRI(K)                                                                                                \
+    do {                                                                                                          \
+        if constexpr (C == 32) {                                                                                  \
+            if (f32) launch_kernel(delta_tri_kernel<3, K, C>, grid, block, 0, s, p);                              \
+            else launch_kernel(delta_tri_kernel<1, K, C>, grid, block, 0, s, p);                                  \
+        } else {                                                                                                  \
+            launch_kernel(delta_tri_kernel<1, K, C>, grid, block, 0, s, p);                                       \
+        }                                                                                                         \
+    } while (0)
+    if (p.dk <= 64) SSM_TRI(64);
+    else if (p.dk <= 128) SSM_TRI(128);
+    else SSM_TRI(256);
+#undef SSM_TRI
+}
+
+template <int C, int MODE> void run_pass(const DeltaPass& p, bool f32, hipStream_t s) {
+    const int64_t slices = MODE == kDeltaStates ? p.vslices + p.kslices : p.vslices;
+    const dim3 grid(static_cast<uint32_t>(int64_t(p.npieces) * p.H * slices)), block(kThreads);
+#define SSM_PASS(K)                                                                                               \
+    do {                                                                                                          \
+        if constexpr (C == 32) {                                                                                  \
+            if (f32) launch_kernel(delta_pass_kernel<3, K, C, MODE>, grid, block, 0, s, p);                       \
+            else if constexpr (MODE != kDeltaFull) launch_kernel(delta_pass_kernel<1, K, C, MODE>, grid, block, 0, s, p); \
+        } else if constexpr (K <= 128 || MODE != kDeltaKeep) {                                                                                                  \
+            launch_kernel(delta_pass_kernel<1, K, C, MODE>, grid, block, 0, s, p);                                \
+        }                                                                                                         \
+    } while (0)
+    if (p.dk <= 64) SSM_PASS(64);
+    else if (p.dk <= 128) SSM_PASS(128);
+    else SSM_PASS(256);
+#undef SSM_PASS
+}
+
+}  // namespace dl
+}  // namespace
+
+void ssm_detail::launch_delta_tri(const DeltaPass& p, bool f32, int chunk, int64_t nchunks, hipStream_t s) {
+    if (chunk == 64) dl::run_tri<64>(p, f32, nchunks, s);
+    else dl::run_tri<32>(p, f32, nchunks, s);
+}
+
+void ssm_detail::launch_delta_pass(const DeltaPass& p, bool f32, int chunk, DeltaMode mode, hipStream_t s) {
+    if (chunk == 64) {
+        if (mode == kDeltaStates) dl::run_pass<64, kDeltaStates>(p, f32, s);
+        else if (mode == kDeltaFull) dl::run_pass<64, kDeltaFull>(p, f32, s);
+        else dl::run_pass<64, kDeltaKeep>(p, f32, s);
+    } else {
+        if (mode == kDeltaStates) dl::run_pass<32, kDeltaStates>(p, f32, s);
+        else if (mode == kDeltaFull) dl::run_pass<32, kDeltaFull>(p, f32, s);
+        else dl::run_pass<32, kDeltaKeep>(p, f32, s);
+    }
+}
+
+void ssm_detail::launch_delta_carry(const DeltaPass& p, bool reverse, hipStream_t s) {
+    const dim3 grid(p.vslices, p.H, p.nseq), block(dl::kThreads);
+#define SSM_CARRY(K)                                                                        \
+    do {                                                                                    \
+        if (reverse) launch_kernel(dl::delta_carry_kernel<K, true>, grid, block, 0, s, p);  \
+        else launch_kernel(dl::delta_carry_kernel<K, false>, grid, block, 0, s, p);         \
+    } while (0)
+    if (p.dk <= 64) SSM_CARRY(64);
+    else if (p.dk <= 128) SSM_CARRY(128);
+    else SSM_CARRY(256);
+#undef SSM_CARRY
+}
+
+extern "C" {
+
+size_t ssm_delta_fwd_workspace_bytes(const ssm_linattn_dims* dims) {
+    la::Sizes z;
+    dl::Plan pl;
+    if (la::check_dims(dims, &z) != SSM_OK) return 0;
+    // with and without cu_seqlens: the larger of the two
+    size_t n = 0;
+    if (dl::make_plan(dims, true, &pl) == SSM_OK) n = pl.bytes();
+    if (dims->tokens % dims->nseq == 0 && dl::make_plan(dims, false, &pl) == SSM_OK && pl.bytes() > n) n = pl.bytes();
+    return n;
+}
+
+int ssm_delta_fwd(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                  const int32_t* cu_seqlens, const int32_t* slots, const float* s0, void* o, float* s_last,
+                  const ssm_linattn_dims* dims, void* stream) {
+    using namespace dl;
+    if (!dims || !q || !k || !v || !g || !beta || !o) return SSM_ERR_NULL;
+    if (slots && !s0 && !s_last) return SSM_ERR_NULL;
+    Sizes z;
+    int st = check_dims(dims, &z);
+    if (st != SSM_OK) return st;
+    const ssm_linattn_dims& d = *dims;
+    if (!cu_seqlens && d.tokens % d.nseq != 0) return SSM_ERR_DIMS;
+    const bool states = s0 || s_last;
+    const int64_t lim = int64_t(1) << 40;
+    if (states && (d.nslots < 1 || d.nslots > (int64_t(1) << 31) - 1 || (!slots && d.nslots < d.nseq) ||
+                   d.nslots > lim / (d.nheads * d.dk * d.dv)))
+        return SSM_ERR_DIMS;
+    if (misaligned(q, z.e) || misaligned(k, z.e) || misaligned(v, z.e) || misaligned(o, z.e) || misaligned(g, 4) ||
+        misaligned(beta, 4) || misaligned(cu_seqlens, 4) || misaligned(slots, 4) || misaligned(s0, 4) || misaligned(s_last, 4))
+        return SSM_ERR_ALIGN;
+    Plan pl;
+    st = make_plan(dims, cu_seqlens != nullptr, &pl);
+    if (st != SSM_OK) return st;
+    const size_t need = pl.bytes();
+    if (!d.workspace || d.workspace_bytes < need || misaligned(d.workspace, 256)) return SSM_ERR_WORKSPACE;
+    const size_t nstate = states ? static_cast<size_t>(d.nslots * d.nheads * d.dk * d.dv) * 4 : 0;
+    const int64_t wk = d.kheads * d.dk, wv = d.nheads * d.dv;
+    const Area in[] = {rows_of(q, d.tokens, z.q, wk, z.e), rows_of(k, d.tokens, z.k, wk, z.e),
+                       rows_of(v, d.tokens, z.v, wv, z.e),
+                       flat(g, static_cast<size_t>(d.nheads * (d.head_decay ? 1 : d.tokens)) * 4),
+                       flat(beta, static_cast<size_t>(d.nheads * d.tokens) * 4),
+                       flat(cu_seqlens, static_cast<size_t>(d.nseq + 1) * 4), flat(slots, static_cast<size_t>(d.nseq) * 4),
+                       flat(s0 == s_last ? nullptr : s0, nstate)};
+    const Area out[] = {rows_of(o, d.tokens, z.o, wv, z.e), flat(s_last, nstate), flat(d.workspace, need)};
+    if (clash(in, out)) return SSM_ERR_ALIAS;
+
+    DeltaPass p = {};
+    p.q = q; p.k = k; p.v = v; p.out = o; p.g = g; p.beta = beta; p.cu = cu_seqlens; p.slots = slots;
+    p.s_in = s0; p.s_out = s_last;
+    p.sq = z.q; p.sk = z.k; p.sv = z.v; p.so = z.o; p.sg = d.head_decay ? 0 : d.nheads;
+    p.T = d.tokens; p.L = cu_seqlens ? 0 : d.tokens / d.nseq;
+    p.piece = pl.piece;
+    p.rep = static_cast<int32_t>(d.nheads / d.kheads); p.H = static_cast<int32_t>(d.nheads);
+    p.dk = static_cast<int32_t>(d.dk); p.dv = static_cast<int32_t>(d.dv);
+    p.vslices = static_cast<int32_t>(cdiv(d.dv, kCols)); p.kslices = static_cast<int32_t>(cdiv(d.dk, kCols));
+    p.nseq = static_cast<int32_t>(d.nseq); p.nslots = static_cast<int32_t>(states ? d.nslots : d.nseq);
+    p.npieces = static_cast<int32_t>(pl.npieces); p.pieced = pl.pieced;
+    p.wide = wide_rows(q, z.q, d.dk, z.e) && wide_rows(k, z.k, d.dk, z.e) && wide_rows(v, z.v, d.dv, z.e);
+    p.pairs = pair_rows(o, z.o, d.dv);
+    p.scale = d.scale;
+    char* ws = static_cast<char*>(d.workspace);
+    p.tri = reinterpret_cast<uint16_t*>(ws);
+    p.carry = reinterpret_cast<float*>(ws + pl.tri);
+    p.trans = reinterpret_cast<float*>(ws + pl.tri + pl.carry);
+    const bool f32 = d.io_dtype == SSM_F32;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    launch_error = hipSuccess;
+    launch_delta_tri(p, f32, pl.chunk, pl.nchunks, s);
+    if (pl.pieced) {
+        launch_delta_pass(p, f32, pl.chunk, kDeltaStates, s);
+        launch_delta_carry(p, false, s);
+    }
+    launch_delta_pass(p, f32, pl.chunk, kDeltaFull, s);
+    return launch_error == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+}
+
+int ssm_delta_step(const void* q, const void* k, const void* v, const float* g, const float* beta, const int32_t* slots,
+                   float* states, void* o, const ssm_linattn_dims* dims, void* stream) {
+    using namespace dl;
+    if (!dims || !q || !k || !v || !g || !beta || !states || !o) return SSM_ERR_NULL;
+    Sizes z;
+    const int st = check_dims(dims, &z);
+    if (st != SSM_OK) return st;
+    const ssm_linattn_dims& d = *dims;
+    if (d.tokens != d.nseq) return SSM_ERR_DIMS;
+    if (d.nslots < 1 || d.nslots > (int64_t(1) << 31) - 1 || (!slots && d.nslots < d.nseq) ||
+        d.nslots > (int64_t(1) << 40) / (d.nheads * d.dk * d.dv))
+        return SSM_ERR_DIMS;
+    if (misaligned(q, z.e) || misaligned(k, z.e) || misaligned(v, z.e) || misaligned(o, z.e) || misaligned(g, 4) ||
+        misaligned(beta, 4) || misaligned(slots, 4) || misaligned(states, 4))
+        return SSM_ERR_ALIGN;
+    const size_t nstate = static_cast<size_t>(d.nslots * d.nheads * d.dk * d.dv) * 4;
+    const int64_t wk = d.kheads * d.dk, wv = d.nheads * d.dv;
+    const Area in[] = {rows_of(q, d.tokens, z.q, wk, z.e), rows_of(k, d.tokens, z.k, wk, z.e),
+                       rows_of(v, d.tokens, z.v, wv, z.e),
+                       flat(g, static_cast<size_t>(d.nheads * (d.head_decay ? 1 : d.tokens)) * 4),
+                       flat(beta, static_cast<size_t>(d.nheads * d.tokens) * 4), flat(slots, static_cast<size_t>(d.nseq) * 4)};
+    const Area out[] = {rows_of(o, d.tokens, z.o, wv, z.e), flat(states, nstate)};
+    if (clash(in, out)) return SSM_ERR_ALIAS;
+
+    StepArgs a = {};
+    a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.slots = slots; a.states = states; a.o = o;
+    a.sq = z.q; a.sk = z.k; a.sv = z.v; a.so = z.o; a.sg = d.head_decay ? 0 : d.nheads;
+    a.H = static_cast<int32_t>(d.nheads); a.rep = static_cast<int32_t>(d.nheads / d.kheads);
+    a.dk = static_cast<int32_t>(d.dk); a.dv = static_cast<int32_t>(d.dv); a.nslots = static_cast<int32_t>(d.nslots);
+    a.scale = d.scale;
+    // up to 64 columns a workgroup, halved while the card has room for more workgroups and a row
+    // of the slice is still 64 bytes
+    int lg = 0;
+    while ((4 << lg) < d.dv && lg < 4) ++lg;
+    while ((4 << lg) > 16 && cdiv(d.dv, 4 << lg) * d.nheads * d.nseq < 512) --lg;
+    a.tpr_log2 = lg;
+    a.nslices = static_cast<int32_t>(cdiv(d.dv, 4 << lg));
+    const int64_t blocks = d.nseq * d.nheads * a.nslices;
+    if (blocks > 2 * kMostGroups) return SSM_ERR_DIMS;
+    const dim3 grid(static_cast<uint32_t>(blocks)), block(kThreads);
+    const int rows = static_cast<int>(cdiv(d.dk, kThreads >> lg));   // of a thread: 16 at most
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    launch_error = hipSuccess;
+#define SSM_STEP(R)                                                                                  \
+    do {                                                                                             \
+        if (d.io_dtype == SSM_BF16) launch_kernel(delta_step_kernel<uint16_t, R>, grid, block, 0, s, a); \
+        else launch_kernel(delta_step_kernel<float, R>, grid, block, 0, s, a);                       \
+    } while (0)
+    if (rows <= 4) SSM_STEP(4);
+    else if (rows <= 8) SSM_STEP(8);
+    else SSM_STEP(16);
+#undef SSM_STEP
+    return launch_error == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+}
+
+}  // extern "C"

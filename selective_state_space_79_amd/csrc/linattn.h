@@ -119,7 +119,7 @@ __device__ inline int64_t uniform(int64_t v) {
     return int64_t(uint64_t(uint32_t(uniform(int(v)))) | (uint64_t(uint32_t(uniform(int(v >> 32)))) << 32));
 }
 
-__device__ inline Seq seq_range(const LinattnPass& p, int s) {
+template <typename P> __device__ inline Seq seq_range(const P& p, int s) {
     if (!p.cu) return {int64_t(s) * p.L, int64_t(s + 1) * p.L};
     int64_t a = uniform(p.cu[s]), b = uniform(p.cu[s + 1]);
     a = a < 0 ? 0 : (a > p.T ? p.T : a);
@@ -130,7 +130,7 @@ __device__ inline Seq seq_range(const LinattnPass& p, int s) {
 // Pieces are numbered floor(start / piece) + s upwards for sequence s: the next sequence's
 // first number is never below the end of this one's, because floor((start + n) / piece) + 1
 // >= floor(start / piece) + ceil(n / piece).  Numbers that no piece has are skipped.
-__device__ inline int64_t piece_base(const LinattnPass& p, int s) {
+template <typename P> __device__ inline int64_t piece_base(const P& p, int s) {
     if (!p.cu) return int64_t(s) * ((p.L + p.piece - 1) / p.piece);
     int64_t a = p.cu[s];
     a = a < 0 ? 0 : (a > p.T ? p.T : a);
@@ -138,7 +138,7 @@ __device__ inline int64_t piece_base(const LinattnPass& p, int s) {
 }
 
 // The sequence of piece number `pi`, or -1: each round of 64 lanes narrows the range 64-fold.
-__device__ inline int find_seq(const LinattnPass& p, int64_t pi) {
+template <typename P> __device__ inline int find_seq(const P& p, int64_t pi) {
     if (!p.cu) {
         const int s = int(pi / ((p.L + p.piece - 1) / p.piece));
         return s < p.nseq ? s : -1;

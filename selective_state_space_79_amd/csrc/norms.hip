@@ -1,5 +1,6 @@
-// norms.hip -- RMS norms around a block: the gated norm behind a mixer and the residual
-// addition between two blocks with the norms on both sides of it, forward and backward.
+// norms.hip -- norms around a block, forward and backward: the gated RMS norm behind a mixer,
+// the residual addition between two blocks with the RMS norms on both sides of it, and the layer
+// norm.
 //
 // Every kernel reads its rows once into registers, 8 neighbouring values per thread, and
 // is bound by those bytes.  A row (or group) belongs to TPG threads: 8 .. 64 lanes of a
@@ -563,6 +564,146 @@ __global__ void __launch_bounds__(block_threads<TPG>(), 4) add_norm_bwd_kernel(A
     if (p.post) store_part<TPG, V>(p.part + 2 * plane, dpo, at, 1, p.n, true, wl);
 }
 
+struct LayerArgs {
+    const void* x;
+    const float* w;
+    const float* b;
+    const void* dy;
+    void* y;        // dx in the backward
+    float* part;    // [blocks][dim] of dw, then of db
+    int64_t rows, sx, sy;
+    int32_t n, vec, bias;
+    float eps, inv_n;
+};
+
+// x less the row's mean; columns behind the row's end stay zero, which the squares need.
+__device__ inline void centre(V8& x, float mean, int col, int n) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x.e[e] = col + e < n ? x.e[e] - mean : 0.0f;
+}
+
+// The mean first and the squares about it then, both from the row in registers: one more
+// exchange than sums of x and x^2 would need, which cancel where a mean is far from zero.
+template <typename IO, int TPG, int V>
+__global__ void __launch_bounds__(block_threads<TPG>()) layer_norm_fwd_kernel(LayerArgs p) {
+    __shared__ float red[Summer<TPG>::kFloats];
+    Summer<TPG> sum{red};
+    const int lane = threadIdx.x % TPG;
+    const Place at = place<TPG>(1);
+    const int64_t loops = (p.rows + at.step - 1) / at.step;
+    for (int64_t l = 0; l < loops; ++l) {
+        const int64_t row = at.row + l * at.step;
+        const bool on = at.on && row < p.rows;
+        V8 x[V];
+        float q = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            x[i] = load8<IO>(static_cast<const IO*>(p.x) + row * p.sx, 8 * (lane + TPG * i), p.n, on, p.vec);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) q += x[i].e[e];
+        }
+        const float mean = sum(q) * p.inv_n;
+        q = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            centre(x[i], mean, 8 * (lane + TPG * i), p.n);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) q = fmaf(x[i].e[e], x[i].e[e], q);
+        }
+        const float rs = __builtin_amdgcn_rsqf(fmaf(sum(q), p.inv_n, p.eps));
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int col = 8 * (lane + TPG * i);
+            const V8 w = load8<float>(p.w, col, p.n, true, p.vec), b = load8<float>(p.b, col, p.n, p.b != nullptr, p.vec);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[i].e[e] = fmaf(x[i].e[e] * rs, w.e[e], b.e[e]);
+            store8<IO>(static_cast<IO*>(p.y) + row * p.sy, col, p.n, on, p.vec, x[i]);
+        }
+    }
+}
+
+// With n = (x - mean) rs and d = dy w:  dx = rs (d - mean(d) - n mean(d n)), dw = sum dy n,
+// db = sum dy.  The sums of d and of d (x - mean) go with that of the squares.
+template <typename IO, int TPG, int V>
+__global__ void __launch_bounds__(block_threads<TPG>(), 4) layer_norm_bwd_kernel(LayerArgs p) {
+    constexpr int T = block_threads<TPG>();
+    __shared__ float red[Summer<TPG>::kFloats];
+    __shared__ __align__(16) float wl[V * 8 * T];   // weights; at the end the slots' sums
+    Summer<TPG> sum{red};
+    const int tid = threadIdx.x, lane = tid % TPG;
+    const Place at = place<TPG>(1);
+    V8 dw[V], db[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        LdsWeights<T>{wl + i * 8 * T}.put(loadw(p.w, 8 * (lane + TPG * i), p.n), tid);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[i].e[e] = db[i].e[e] = 0.0f;
+    }
+    const int64_t loops = (p.rows + at.step - 1) / at.step;
+    Raw8<IO> nx[V], ng[V];   // the next row's
+    auto fetch = [&](int64_t row) {
+        const bool on = at.on && row < p.rows;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int col = 8 * (lane + TPG * i);
+            nx[i].load(static_cast<const IO*>(p.x) + row * p.sx, col, p.n, on, p.vec);
+            ng[i].load(static_cast<const IO*>(p.dy) + row * p.n, col, p.n, on, p.vec);
+        }
+    };
+    if (V == 1) fetch(at.row);
+    for (int64_t l = 0; l < loops; ++l) {
+        const int64_t row = at.row + l * at.step;
+        const bool on = at.on && row < p.rows;
+        if (V > 1) fetch(row);
+        Raw8<IO> rx[V], rg[V];
+        float q = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            rx[i] = nx[i];
+            rg[i] = ng[i];
+            const V8 x = rx[i].values();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) q += x.e[e];
+        }
+        if (V == 1 && l + 1 < loops) fetch(row + at.step);
+        const float mean = sum(q) * p.inv_n;
+        float s[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            V8 x = rx[i].values();
+            const V8 g = rg[i].values(), w = LdsWeights<T>{wl + i * 8 * T}.get(tid);
+            centre(x, mean, 8 * (lane + TPG * i), p.n);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float d = g.e[e] * w.e[e];
+                s[0] = fmaf(x.e[e], x.e[e], s[0]);
+                s[1] += d;
+                s[2] = fmaf(d, x.e[e], s[2]);
+            }
+        }
+        sum.all(s);
+        const float rs = __builtin_amdgcn_rsqf(fmaf(s[0], p.inv_n, p.eps));
+        const float m = s[1] * p.inv_n, k = s[2] * p.inv_n * rs * rs;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int col = 8 * (lane + TPG * i);
+            V8 x = rx[i].values();
+            const V8 g = rg[i].values(), w = LdsWeights<T>{wl + i * 8 * T}.get(tid);
+            centre(x, mean, col, p.n);
+            V8 dx;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                dw[i].e[e] = fmaf(g.e[e], x.e[e] * rs, dw[i].e[e]);
+                db[i].e[e] += g.e[e];
+                dx.e[e] = rs * (fmaf(g.e[e], w.e[e], -m) - x.e[e] * k);
+            }
+            store8<IO>(static_cast<IO*>(p.y) + row * p.n, col, p.n, on, p.vec, dx);
+        }
+    }
+    store_part<TPG, V>(p.part, dw, at, 1, p.n, true, wl);
+    if (p.bias) store_part<TPG, V>(p.part + int64_t(gridDim.x) * p.n, db, at, 1, p.n, true, wl);
+}
+
 // Sums `count` partial rows of n values, in a fixed order: 16 columns x 64 rows a workgroup,
 // eight rows of a thread under way at once.  Plane b of the grid's y goes to out0, out1, out2.
 // The columns go round over at most 2^20 workgroups (a grid has fewer than 2^32 threads).
@@ -669,6 +810,18 @@ template <typename IO, typename RT> void run_add(const AddArgs& a, int tpg, int6
 #undef SSM_DO
 }
 
+template <typename IO> void run_layer(const LayerArgs& a, int tpg, int64_t blocks, bool bwd, hipStream_t s) {
+    const dim3 grid(static_cast<uint32_t>(blocks)), block(tpg < 256 ? 256 : tpg);
+    const int64_t n = a.n;
+#define SSM_DO(T, V)                                                                                   \
+    do {                                                                                               \
+        if (bwd) launch_kernel(layer_norm_bwd_kernel<IO, T, V>, grid, block, 0, s, a);                  \
+        else launch_kernel(layer_norm_fwd_kernel<IO, T, V>, grid, block, 0, s, a);                      \
+    } while (0)
+    SSM_NORM_TPG(SSM_DO)
+#undef SSM_DO
+}
+
 inline void gated(const GatedArgs& a, const ssm_gated_norm_dims& d, int tpg, int64_t blocks, bool bwd, hipStream_t s) {
     if (d.io_dtype == SSM_BF16) {
         if (d.gate_first) run_gated<uint16_t, true>(a, tpg, blocks, bwd, s);
@@ -715,6 +868,18 @@ inline int check(const ssm_add_norm_dims* d) {
     const int64_t lim = int64_t(1) << 40;
     if (d->dim > SSM_NORM_MAX_DIM || d->rows > lim / d->dim || d->reserved != 0) return SSM_ERR_DIMS;
     for (const int64_t s : {d->x_stride, d->res_stride, d->r_stride, d->y_stride})
+        if (s != 0 && (s < d->dim || s > lim / d->rows)) return SSM_ERR_DIMS;
+    if (!good_eps(d->eps)) return SSM_ERR_DIMS;
+    return SSM_OK;
+}
+
+inline int check(const ssm_layer_norm_dims* d) {
+    if (!d) return SSM_ERR_NULL;
+    if (d->rows < 1 || d->dim < 1) return SSM_ERR_EMPTY;
+    if (d->io_dtype != SSM_F32 && d->io_dtype != SSM_BF16) return SSM_ERR_DTYPE;
+    const int64_t lim = int64_t(1) << 40;
+    if (d->dim > SSM_NORM_MAX_DIM || d->rows > lim / d->dim) return SSM_ERR_DIMS;
+    for (const int64_t s : {d->x_stride, d->y_stride})
         if (s != 0 && (s < d->dim || s > lim / d->rows)) return SSM_ERR_DIMS;
     if (!good_eps(d->eps)) return SSM_ERR_DIMS;
     return SSM_OK;
@@ -879,6 +1044,74 @@ int ssm_add_norm_bwd(const void* x, const void* r, const float* scale, const flo
     add(a, d, tpg, blocks, true, s);
     launch_kernel(sum_rows_kernel, dim3(sum_blocks(d.dim), 3), dim3(16 * kSumLanes), 0, s, a.part, blocks,
                   d.dim, dw, scale ? dscale : nullptr, post ? dpost : nullptr);
+    return ssm_detail::launch_error == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+}
+
+int ssm_layer_norm_fwd(const void* x, const float* w, const float* b, void* y, const ssm_layer_norm_dims* dims,
+                       void* stream) {
+    using namespace nrm;
+    if (!dims || !x || !w || !y) return SSM_ERR_NULL;
+    const int st = check(dims);
+    if (st != SSM_OK) return st;
+    const ssm_layer_norm_dims& d = *dims;
+    const int64_t e = size_of(d.io_dtype);
+    if (misaligned(x, e) || misaligned(y, e) || misaligned(w, 4) || misaligned(b, 4)) return SSM_ERR_ALIGN;
+    LayerArgs a = {};
+    a.x = x; a.w = w; a.b = b; a.y = y;
+    a.rows = d.rows; a.n = static_cast<int32_t>(d.dim);
+    a.sx = d.x_stride ? d.x_stride : d.dim;
+    a.sy = d.y_stride ? d.y_stride : d.dim;
+    const size_t nw = static_cast<size_t>(d.dim) * 4;
+    const Area in[] = {rows_of(y == x && a.sy == a.sx ? nullptr : x, d.rows, a.sx, d.dim, e), flat(w, nw), flat(b, nw)};
+    const Area out[] = {rows_of(y, d.rows, a.sy, d.dim, e)};
+    if (clash(in, out)) return SSM_ERR_ALIAS;
+    a.eps = d.eps; a.inv_n = 1.0f / static_cast<float>(d.dim);
+    a.vec = d.dim % 8 == 0 && vec_row(x, a.sx, e) && vec_row(y, a.sy, e) && !misaligned(w, 16) && !misaligned(b, 16);
+    const int tpg = tpg_for(d.dim);
+    const int64_t blocks = blocks_for(d.rows, 1, tpg, kFwdBlocks);
+    ssm_detail::launch_error = hipSuccess;
+    if (d.io_dtype == SSM_BF16) run_layer<uint16_t>(a, tpg, blocks, false, static_cast<hipStream_t>(stream));
+    else run_layer<float>(a, tpg, blocks, false, static_cast<hipStream_t>(stream));
+    return ssm_detail::launch_error == hipSuccess ? SSM_OK : SSM_ERR_HIP;
+}
+
+size_t ssm_layer_norm_bwd_workspace_bytes(const ssm_layer_norm_dims* dims) {
+    using namespace nrm;
+    if (check(dims) != SSM_OK) return 0;
+    const int tpg = tpg_for(dims->dim);
+    return static_cast<size_t>(2 * blocks_for(dims->rows, 1, tpg, bwd_blocks(tpg)) * dims->dim) * 4;
+}
+
+int ssm_layer_norm_bwd(const void* x, const float* w, const void* dy, void* dx, float* dw, float* db,
+                       const ssm_layer_norm_dims* dims, void* stream) {
+    using namespace nrm;
+    if (!dims || !x || !w || !dy || !dx || !dw) return SSM_ERR_NULL;
+    const int st = check(dims);
+    if (st != SSM_OK) return st;
+    const ssm_layer_norm_dims& d = *dims;
+    const int64_t e = size_of(d.io_dtype);
+    if (misaligned(x, e) || misaligned(dy, e) || misaligned(dx, e) || misaligned(w, 4) || misaligned(dw, 4) || misaligned(db, 4))
+        return SSM_ERR_ALIGN;
+    const size_t need = ssm_layer_norm_bwd_workspace_bytes(dims);
+    if (!d.workspace || d.workspace_bytes < need || misaligned(d.workspace, 256)) return SSM_ERR_WORKSPACE;
+    LayerArgs a = {};
+    a.x = x; a.w = w; a.dy = dy; a.y = dx; a.part = static_cast<float*>(d.workspace); a.bias = db != nullptr;
+    a.rows = d.rows; a.n = static_cast<int32_t>(d.dim);
+    a.sx = d.x_stride ? d.x_stride : d.dim;
+    const size_t nw = static_cast<size_t>(d.dim) * 4, all = static_cast<size_t>(d.rows * d.dim * e);
+    const Area in[] = {rows_of(x, d.rows, a.sx, d.dim, e), flat(dy, all), flat(w, nw)};
+    const Area out[] = {flat(dx, all), flat(dw, nw), flat(db, nw), flat(d.workspace, need)};
+    if (clash(in, out)) return SSM_ERR_ALIAS;
+    a.eps = d.eps; a.inv_n = 1.0f / static_cast<float>(d.dim);
+    a.vec = d.dim % 8 == 0 && vec_row(x, a.sx, e) && vec_row(dy, d.dim, e) && vec_row(dx, d.dim, e);
+    const int tpg = tpg_for(d.dim);
+    const int64_t blocks = blocks_for(d.rows, 1, tpg, bwd_blocks(tpg));
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    ssm_detail::launch_error = hipSuccess;
+    if (d.io_dtype == SSM_BF16) run_layer<uint16_t>(a, tpg, blocks, true, s);
+    else run_layer<float>(a, tpg, blocks, true, s);
+    launch_kernel(sum_rows_kernel, dim3(sum_blocks(d.dim), db ? 2 : 1), dim3(16 * kSumLanes), 0, s, a.part, blocks, d.dim,
+                  dw, db, static_cast<float*>(nullptr));
     return ssm_detail::launch_error == hipSuccess ? SSM_OK : SSM_ERR_HIP;
 }
 
