@@ -23,6 +23,8 @@
 // the next one's operand as it stands ("paired rows" below).
 #pragma once
 
+#include <type_traits>
+
 #include "linattn.h"
 
 namespace ssm_detail {
@@ -38,8 +40,11 @@ struct DeltaPass {
     const int32_t* slots;
     const float* s_in;        // user's starting states, nullable
     float* s_out;             // user's final states, nullable
-    uint16_t* tri;            // [chunks][H][3 parts][blocks of 16 x 32]: A
+    uint16_t* tri;            // [blocks][H][3 parts][tiles' pairs of 16 x 32]: A
+    float* steps;             // [chunks][H]: decays and steps of a walk's chunk (Steps<32>)
     float* keep;              // [chunks][H][dk][dv]: the state each chunk starts from (reverse: its gradient behind)
+    float* rows;              // [T][H][dv]: U (reverse: Z), with keep
+    void* dv_out;             // the gradient of v (with keep, against time)
     float* carry;             // [pieces][H][dk][dv]: the pieces' own end states, then their starting states
     float* trans;             // [pieces][H][dk][dk]: what a piece makes of the state it starts from
     float* trans_t;           // the same transposed, nullable
@@ -47,18 +52,20 @@ struct DeltaPass {
     int64_t T, L;
     int64_t piece;            // tokens of a piece (a multiple of the chunk)
     int32_t rep, H, dk, dv;
+    int32_t block;            // tokens of A, keep: a chunk (32), or two of them
     int32_t vslices, kslices; // of 64 columns of v, and of the transition
     int32_t nseq, nslots, npieces, pieced;
     int32_t wide, pairs;
     float scale;
+    float least;              // the least size of a step that the gradients count with
 };
 
 // kDeltaStates: the pieces' own end states and transitions; kDeltaFull: the outputs (reverse:
 // the final gradients alone); kDeltaKeep: the state at each chunk's start (reverse: its gradient
 // at the chunk's end).
 enum DeltaMode { kDeltaStates = 0, kDeltaFull = 1, kDeltaKeep = 2 };
-void launch_delta_tri(const DeltaPass& p, bool f32, int chunk, int64_t nchunks, hipStream_t s);
-void launch_delta_pass(const DeltaPass& p, bool f32, int chunk, DeltaMode mode, hipStream_t s);
+void launch_delta_tri(const DeltaPass& p, bool f32, int64_t nchunks, hipStream_t s);
+void launch_delta_pass(const DeltaPass& p, bool f32, DeltaMode mode, hipStream_t s);
 void launch_delta_carry(const DeltaPass& p, bool reverse, hipStream_t s);
 
 }  // namespace ssm_detail
@@ -70,6 +77,7 @@ using namespace la;
 using ssm_detail::DeltaPass;
 
 constexpr int kCols = 64;   // columns of the state a workgroup: four waves of 16
+constexpr int kChunk = 32;  // tokens of a walk's chunk
 
 // blocks of 16 x 32 on and below the diagonal of a chunk (p_block numbers them)
 template <int C> constexpr int tri_blocks() { return C == 64 ? 6 : 2; }
@@ -93,24 +101,28 @@ template <int C> struct __align__(16) Steps {
     float out[C];          // e^{G_C - G_i}
     float beta[C];
     float bin[C];          // beta_i e^{G_i}
-    float tail;            // e^{G_C}
+    float given[C];        // beta as it came
+    float tail[C];         // e^{G_C}
 };
 // One wave: lane r brings row r's log decay and beta.  The sums run in float64, so that a
 // difference of two of them is right to float32 of the difference, however far they fell.
-template <int C> __device__ inline void put_steps(Steps<C>& d, float g, float beta, int lane) {
+// Returns the sums up to each row, in log2 units.
+__device__ inline double sum_decays(float g, bool on) {
     g = g < kMinDecay ? kMinDecay : g;
-    const double s = scan_f64(lane < C ? double(g) * 1.4426950408889634 : 0.0);
-    const double end = lane_f64(s, C - 1);
-    if (lane < C) {
-        const float hi = float(s), e = exp2_of(s);
-        d.hi[lane] = hi;
-        d.lo[lane] = float(s - double(hi));
-        d.in[lane] = e;
-        d.out[lane] = exp2_of(end - s);
-        d.beta[lane] = beta;
-        d.bin[lane] = beta * e;
-        if (lane == 0) d.tail = exp2_of(end);
-    }
+    return scan_f64(on ? double(g) * 1.4426950408889634 : 0.0);
+}
+// Row r's values from the sums up to it and up to the chunk's end; zero steps count as `least`.
+template <int C> __device__ inline void put_steps(Steps<C>& d, double s, double end, float beta, float least, int r) {
+    const float hi = float(s), e = exp2_of(s);
+    const float b = fabsf(beta) < least ? copysignf(least, beta) : beta;
+    d.hi[r] = hi;
+    d.lo[r] = float(s - double(hi));
+    d.in[r] = e;
+    d.out[r] = exp2_of(end - s);
+    d.beta[r] = b;
+    d.bin[r] = b * e;
+    d.given[r] = beta;
+    d.tail[r] = exp2_of(end);
 }
 
 // Operand along the rows of a tile in paired order: lane 16g + i takes columns 32 kb + 8g ..
@@ -124,15 +136,15 @@ template <int W> __device__ inline u32x4 pair_op(const uint16_t* t, int r0, int 
 }
 
 // A transposed as a left operand: its tiles hold paired rows, so the contraction's tokens 8g ..
-// + 7 of a pair are rows 4g .. + 3 of the pair's two tiles.  Output rows in paired order.
+// + 7 are rows 4g .. + 3 of the two tiles.  Output rows in paired order.
 __device__ inline uint32_t tri_t_base(int lane) {
     const int g = lane >> 4;
     return 2 * ((4 * g + ((lane >> 2) & 3)) * 32 + 8 * ((lane & 3) ^ g));
 }
-__device__ inline u32x4 tri_t_op(const uint16_t* t, int ip, int jp, int half, uint32_t base) {
+__device__ inline u32x4 tri_t_op(const uint16_t* t, int half, uint32_t base) {
     const char* const at = reinterpret_cast<const char*>(t) + base + 8 * half;
-    const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 1024 * p_block(2 * ip, jp)));
-    const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 1024 * p_block(2 * ip + 1, jp)));
+    const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
+    const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 1024));
     const uint2 u = __builtin_bit_cast(uint2, x), v = __builtin_bit_cast(uint2, y);
     return u32x4{u.x, u.y, v.x, v.y};
 }
@@ -161,14 +173,81 @@ template <int PARTS> __device__ inline void unpack(const u32x4 (&v)[PARTS], int 
     }
 }
 
-// A matrix of A's kind from memory straight into LDS, a kilobyte a wave at a time.
-template <int C, int NW> __device__ inline void load_tri(const uint16_t* from, uint16_t* to, int wave, int lane) {
-    constexpr int KB = tri_elems<C>() / 512;
-    const u32x4 w = rows_window(reinterpret_cast<const char*>(from), 2 * tri_elems<C>(), 1, 1);
+// c[t] += a[t] b for N tiles, part by part over all of them: products that wait for one another
+// lie N apart.
+template <int N, int NA, int NB>
+__device__ inline void mma_tiles(const u32x4 (&a)[N][NA], const u32x4 (&b)[NB], f32x4* c) {
+    constexpr int most = (NA > NB ? NA : NB) - 1;
 #pragma unroll
-    for (int i = 0; i < (KB + NW - 1) / NW; ++i) {
-        const int b = wave + NW * i;
-        if (b < KB) load_lds16(w, lds_address(to) + 1024 * b, uint32_t(1024 * b + 16 * lane));
+    for (int i = 0; i < NA; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+            if (i + j <= most) {
+#pragma unroll
+                for (int t = 0; t < N; ++t) c[t] = mma(a[t][i], b[j], c[t]);
+            }
+}
+
+// Four values each of the four lanes of a quad, transposed: lane b gets value b of each.
+__device__ inline f32x4 quad_transpose(const f32x4& x, int lane) {
+    const auto swap = [](float v, auto ctrl) {
+        return __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(v), decltype(ctrl)::value, 0xf, 0xf, true));
+    };
+    using One = std::integral_constant<int, 0xB1>;   // lane ^ 1
+    using Two = std::integral_constant<int, 0x4E>;   // lane ^ 2
+    const bool o1 = lane & 1, o2 = lane & 2;
+    f32x4 y, z;
+#pragma unroll
+    for (int h = 0; h < 4; h += 2) {
+        const float give = swap(o1 ? x[h] : x[h + 1], One{});
+        y[h] = o1 ? give : x[h];
+        y[h + 1] = o1 ? x[h + 1] : give;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float give = swap(o2 ? y[h] : y[h + 2], Two{});
+        z[h] = o2 ? give : y[h];
+        z[h + 2] = o2 ? y[h + 2] : give;
+    }
+    return z;
+}
+
+// A wave's 16 columns from c_wave on of a state (null: zeros), in the layout of a product's tiles.
+template <int KB> __device__ inline void load_state(f32x4 (&S)[2 * KB], const float* at, int dk, int dv, int c_wave, int lane) {
+    const int g4 = lane >> 4, col = c_wave + (lane & 15);
+    const Rsrc ro = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(at), 0, at ? dk * dv * 4 : 0, 0x00020000);
+    const uint32_t o0 = (col < dv ? uint32_t(4 * col) : kPast) + uint32_t(32 * g4 * dv);
+#pragma unroll
+    for (int m = 0; m < 2 * KB; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            S[m][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+                ro, o0 + uint32_t(4 * (32 * (m >> 1) + 4 * (m & 1) + r) * dv), 0, 0));
+}
+
+// Writes a wave's 16 columns from c_wave on of a state.  Through a window on the whole state, so
+// that rows and columns it does not have are dropped and every wave has as many stores under way.
+// With `vec` (dv in whole fours) four lanes swap rows for columns: a quarter of the stores.
+template <int KB>
+__device__ inline void store_state(const f32x4 (&S)[2 * KB], float* at, int dk, int dv, int c_wave, bool vec, int lane) {
+    const int g4 = lane >> 4, l16 = lane & 15;
+    const Rsrc ro = __builtin_amdgcn_make_buffer_rsrc(at, 0, dk * dv * 4, 0x00020000);
+    if (vec) {
+        const int col = c_wave + (l16 & ~3);
+        const uint32_t o0 = (col < dv ? uint32_t(4 * col) : kPast) + uint32_t(4 * (8 * g4 + (l16 & 3)) * dv);
+#pragma unroll
+        for (int m = 0; m < 2 * KB; ++m)
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, quad_transpose(S[m], lane)), ro,
+                                                   o0 + uint32_t(4 * (32 * (m >> 1) + 4 * (m & 1)) * dv), 0, 0);
+    } else {
+        const int col = c_wave + l16;
+        const uint32_t o0 = (col < dv ? uint32_t(4 * col) : kPast) + uint32_t(32 * g4 * dv);
+#pragma unroll
+        for (int m = 0; m < 2 * KB; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[m][r]), ro,
+                                                      o0 + uint32_t(4 * (32 * (m >> 1) + 4 * (m & 1) + r) * dv), 0, 0);
     }
 }
 
@@ -261,43 +340,90 @@ __device__ inline void store_tiles(const f32x4 (&o)[C / 16], char* row0, int64_t
     }
 }
 
-// P transposed, the left operand of P^T dO: tiles of 16 tokens j in paired rows, the
-// contraction over the tokens i of the same or a later pair.
-template <int C> __device__ constexpr int pt_block(int jt, int ip) { return C == 32 ? jt : jt < 2 ? 2 * jt + ip : 2 + jt; }
-template <int PARTS, int KD, int C, int NW>
-__device__ inline void put_pt(const uint16_t* Q, const uint16_t* K, uint16_t* PT, const Steps<C>& st, float scale, int wave,
+// P transposed, the left operand of P^T dO: tiles of 16 tokens j in paired rows, the contraction
+// over all tokens i of the chunk; a tile a wave.
+template <int PARTS, int KD>
+__device__ inline void put_pt(const uint16_t* Q, const uint16_t* K, uint16_t* PT, const Steps<kChunk>& st, float scale, int wave,
                               int lane) {
-    constexpr int N = C == 64 ? 12 : 4, KB = KD / 32, PB = tri_blocks<C>() * 512;
-    const int g4 = lane >> 4, l16 = lane & 15;
+    constexpr int KB = KD / 32, TE = kChunk * KD;
+    const int g4 = lane >> 4, l16 = lane & 15, jt = wave >> 1, it = wave & 1;
     const uint32_t base = row_base<KD>(lane), bpair = pair_base<KD>(lane);
-    for (int m = wave; m < N; m += NW) {
-        const int jt = C == 32 ? m >> 1 : m < 8 ? m >> 2 : 2 + ((m - 8) >> 1), it = C == 32 ? m & 1 : m < 8 ? m & 3 : 2 + (m & 1);
-        f32x4 a = {0.0f, 0.0f, 0.0f, 0.0f};
+    f32x4 a = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-            u32x4 x[PARTS], y[PARTS];
+    for (int kb = 0; kb < KB; ++kb) {
+        u32x4 x[PARTS], y[PARTS];
 #pragma unroll
-            for (int i = 0; i < PARTS; ++i) {
-                x[i] = row_op<KD>(Q + i * C * KD, 16 * it, kb, base);
-                y[i] = pair_op<KD>(K + i * C * KD, 32 * (jt >> 1), jt & 1, kb, bpair);
-            }
-            a = mma_parts<PARTS, PARTS>(x, y, a);
+        for (int i = 0; i < PARTS; ++i) {
+            x[i] = row_op<KD>(Q + i * TE, 16 * it, kb, base);
+            y[i] = pair_op<KD>(K + i * TE, 0, jt, kb, bpair);
         }
-        const int j = 32 * (jt >> 1) + 8 * (l16 >> 2) + 4 * (jt & 1) + (l16 & 3), i0 = 16 * it + 4 * g4;
-        const float gj = st.hi[j], ej = st.lo[j];
-        const f32x4 gi = *reinterpret_cast<const f32x4*>(&st.hi[i0]), ei = *reinterpret_cast<const f32x4*>(&st.lo[i0]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const float e = __builtin_amdgcn_exp2f((gi[r] - gj) + (ei[r] - ej));
-            a[r] = j <= i0 + r ? a[r] * (e * scale) : 0.0f;
-        }
-        uint32_t x[3], y[3];
-        split<3>(a[0], a[1], x);
-        split<3>(a[2], a[3], y);
-        uint16_t* const o = PT + pt_block<C>(jt, it >> 1) * 512 + at_piece<32>(l16, 2 * (it & 1) + (g4 >> 1)) + 4 * (g4 & 1);
-#pragma unroll
-        for (int k = 0; k < 3; ++k) *reinterpret_cast<uint2*>(o + k * PB) = uint2{x[k], y[k]};
+        a = mma_parts<PARTS, PARTS>(x, y, a);
     }
+    const int j = 8 * (l16 >> 2) + 4 * jt + (l16 & 3), i0 = 16 * it + 4 * g4;
+    const float gj = st.hi[j], ej = st.lo[j];
+    const f32x4 gi = *reinterpret_cast<const f32x4*>(&st.hi[i0]), ei = *reinterpret_cast<const f32x4*>(&st.lo[i0]);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const float e = __builtin_amdgcn_exp2f((gi[r] - gj) + (ei[r] - ej));
+        a[r] = j <= i0 + r ? a[r] * (e * scale) : 0.0f;
+    }
+    uint32_t x[3], y[3];
+    split<3>(a[0], a[1], x);
+    split<3>(a[2], a[3], y);
+    uint16_t* const o = PT + jt * 512 + at_piece<32>(l16, 2 * it + (g4 >> 1)) + 4 * (g4 & 1);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) *reinterpret_cast<uint2*>(o + k * 1024) = uint2{x[k], y[k]};
+}
+
+// Where the blocks of A and of kept states lie that a piece's chunks belong to.
+struct Blocked {
+    int64_t first;     // number of the piece's first block
+    int two;           // 1: two chunks to a block
+    template <typename P> __device__ inline Blocked(const P& p, const Where& w, int64_t lo) {
+        const Chunks ch(p, p.block);
+        two = p.block > kChunk;
+        first = uniform(piece_base(ch, w.seq)) + (lo - w.sq.start) / p.block;
+    }
+    __device__ inline int64_t block(int64_t n) const { return first + (n >> two); }
+    __device__ inline bool starts(int64_t n) const { return !two || (n & 1) == 0; }
+    // A of a chunk into LDS: the blocks on the diagonal of a larger matrix's inverse are the
+    // inverses of its own
+    __device__ inline void load(uint16_t* to, Steps<kChunk>* st, const DeltaPass& p, int64_t n, int h, int wave, int lane) const {
+        constexpr int NB = tri_blocks<kChunk>();
+        const int64_t all = two ? tri_elems<64>() : tri_elems<32>();
+        const u32x4 w = rows_window(reinterpret_cast<const char*>(p.tri + (block(n) * p.H + h) * all), 2 * all, 1, 1);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int b = wave + 4 * i, part = b >> 1, half = b & 1;   // 3 parts of 2 blocks
+            if (b >= 3 * NB) break;
+            const int from = !two ? b : 6 * part + ((n & 1) ? 3 + 2 * half : half);
+            load_lds16(w, lds_address(to) + 1024 * b, uint32_t(1024 * from + 16 * lane));
+        }
+        static_assert(sizeof(Steps<kChunk>) == 1024, "what a wave loads at once");
+        if (wave == 3)
+            load_lds16(rows_window(reinterpret_cast<const char*>(p.steps + (((first << two) + n) * p.H + h) * 256),
+                                   1024, 1, 1), lds_address(st), 16 * lane);
+    }
+};
+
+// Pieces along the tokens.  They cost a walk from zero and one from the unit matrix before the
+// walk for the outputs, a little more than twice the work, so they pay where sequences are long
+// for what the card has to do in all: where a sequence's own chunks, one after the other, take
+// longer (`worth` is the ratio of the two costs).  The lengths of packed sequences are not known
+// here; the longest is taken for twice the mean.
+inline int64_t choose_piece(const ssm_linattn_dims* d, bool packed, int64_t worth) {
+    const int64_t units = d->nheads * cdiv(d->dv, kCols), mean = cdiv(d->tokens, d->nseq);
+    const int64_t longest = packed && d->nseq > 1 ? (2 * mean < d->tokens ? 2 * mean : d->tokens) : mean;
+    if (longest < 1024 || units * cdiv(d->tokens, worth) >= longest) return 0;
+    // as many workgroups as the card holds at once, three a CU
+    const int64_t want = 3 * kCus / units;
+    int64_t piece = cdiv(cdiv(d->tokens, want < 1 ? 1 : want), 64) * 64;
+    if (piece < 256) piece = 256;
+    return piece < longest ? piece : 0;
+}
+
+constexpr int pass_waves(int KD, int PARTS, int MODE) {   // per SIMD
+    return KD == 256 ? (PARTS == 1 ? 2 : 1) : PARTS == 1 && MODE == ssm_detail::kDeltaFull ? 3 : 2;
 }
 
 }  // namespace dl

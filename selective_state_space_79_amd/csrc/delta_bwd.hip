@@ -7,16 +7,16 @@
 //   dQ = scale e^G dO S_in^T + D K           D_ij = scale e^{G_i-G_j} dO_i . U_j, j <= i
 //   dK = e^{G_C-G} U dS_out^T - e^G dR S_in^T + D^T Q + (N + N^T) K
 //                                            N_ij = -beta_i e^{G_i-G_j} Z_i . U_j, j < i
-//   dbeta_i = Z_i . r_i = Z_i . X_i - sum_{j<i} (Z_i . U_j) M_ij
+//   dbeta_i = Z_i . r_i = Z_i . U_i / beta_i
 //
-// (r = U / beta, but beta may be zero.)  The decay of token t scales all that the state holds
+// The decay of token t scales all that the state holds
 // then, so dg_t = <dS'_t, S'_t>; between tokens it changes by what is read and what is written:
 //
 //   dg_t = dg_{t+1} + o_t . do_t - v_t . dv_t        behind a chunk <dS_out, S_out>
 //
 // and o_t . do_t = q_t . dq_t.  Two walks over the chunks, the forward's and one against time,
-// leave S_in and dS_out of every chunk in memory; all gradients of a chunk are then formed by a
-// workgroup of its own.
+// leave S_in and U, dS_out and Z of every chunk in memory; all gradients of a chunk are then
+// formed by a workgroup of its own.
 #include "delta.h"
 
 namespace {
@@ -24,69 +24,58 @@ namespace dl {
 
 using namespace ssm_detail;
 
+// Steps below this count as this in the gradients, so that r = U / beta is there for a step of
+// zero too.  What they then add to a state is 2^-64 of what a step of one would, far below its
+// rounding; the gradient of v is formed with the step as it came.
+constexpr float kLeastStep = 5.42101086e-20f;   // 2^-64
+
 // ---------------------------------------------------------------- the walk against time
-// As delta_pass_kernel, with the gradient of the state in the registers; p.v is the gradient of o.
-template <int PARTS, int KD, int C, int MODE>
+// As delta_pass_kernel without outputs, with the gradient of the state in the registers; p.v is
+// the gradient of o.
+template <int PARTS, int KD, int MODE>
 __global__ void __launch_bounds__(kThreads, KD == 256 ? 1 : 2) delta_rev_kernel(DeltaPass p) {
-    constexpr bool DMA = PARTS == 1;
-    constexpr int IT = C / 16, JB = C / 32, KB = KD / 32, NB = tri_blocks<C>(), PB = NB * 512, WP = 3;
-    __shared__ __align__(16) uint16_t K[PARTS * C * KD], Q[PARTS * C * KD], V[PARTS * C * kCols], A[WP * PB], PT[WP * PB];
+    constexpr bool KEEP = MODE == kDeltaKeep, DMA = PARTS == 1;
+    constexpr int C = kChunk, IT = C / 16, KB = KD / 32, PB = 2 * 512, WP = 3;
+    constexpr int SETS = DMA ? 2 : 1, KE = PARTS * C * KD, VE = PARTS * C * kCols;
+    __shared__ __align__(16) uint16_t Ks[SETS * KE], Qs[SETS * KE], Vs[SETS * VE], As[2 * WP * PB], PT[WP * PB];
     __shared__ Steps<C> steps[2];
     const int tid = threadIdx.x, lane = tid & 63, g4 = lane >> 4, l16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const Where w = find_piece(p, p.vslices, false);
     if (!w.on || (MODE == kDeltaStates && w.first)) return;   // no piece starts from a first one's gradient
-    const int h = w.h, c_slice = w.slice * kCols, c_wave = c_slice + 16 * wave, col = c_wave + l16;
+    const int h = w.h, c_slice = w.slice * kCols, c_wave = c_slice + 16 * wave;
     const bool active = c_wave < p.dv;
     const int64_t lo = w.lo, hi = w.hi, ssz = int64_t(p.dk) * p.dv;
 
     f32x4 S[2 * KB];
     const float* src = nullptr;
-    if constexpr (MODE != kDeltaStates) {
+    if constexpr (KEEP) {
         if (p.pieced && w.sq.end - w.sq.start > p.piece)
             src = p.carry + (w.pi * p.H + h) * ssz;
         else if (p.s_in)
             src = p.s_in + (int64_t(w.slot) * p.H + h) * ssz;
     }
-#pragma unroll
-    for (int m = 0; m < 2 * KB; ++m)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = 32 * (m >> 1) + 8 * g4 + 4 * (m & 1) + r;
-            S[m][r] = src && row < p.dk && col < p.dv ? src[int64_t(row) * p.dv + col] : 0.0f;
-        }
+    load_state<KB>(S, src, p.dk, p.dv, c_wave, lane);
 
     const int64_t nch = (hi - lo + C - 1) / C;
-    const Chunks ch(p, C);
-    const int64_t first = uniform(piece_base(ch, w.seq)) + (lo - w.sq.start) / C;
-    const uint16_t* const tri = p.tri + (first * p.H + h) * tri_elems<C>();
-    auto load_a = [&](int64_t n, int lane) { load_tri<C, 4>(tri + n * p.H * tri_elems<C>(), A, wave, lane); };
-    const bool step_wave = wave == 3;
-    float gn = 0.0f, bn = 0.0f;
-    auto fetch = [&](int64_t n, int lane) {
-        const int64_t t = lo + n * C + lane;
-        const bool on = n >= 0 && lane < C && t < hi;
-        gn = on ? p.g[t * p.sg + h] : 0.0f;
-        bn = on ? p.beta[t * p.H + h] : 0.0f;
-    };
-    if (step_wave) {
-        fetch(nch - 1, lane);
-        put_steps<C>(steps[(nch - 1) & 1], gn, bn, lane);
-        fetch(nch - 2, lane);
-    }
+    const Blocked at(p, w, lo);
     Rows<PARTS, C, KD, kThreads> rk, rq;
     Rows<PARTS, C, kCols, kThreads> rv;
     rk.prepare(p.k, int64_t(h / p.rep) * p.dk, p.sk, p.dk, tid);
     rq.prepare(p.q, int64_t(h / p.rep) * p.dk, p.sq, p.dk, tid);
     rv.prepare(p.v, int64_t(h) * p.dv + c_slice, p.sv, p.dv - c_slice, tid);
     const bool ahead = DMA && p.wide;
+    auto load = [&](int64_t n) {
+        const bool odd = SETS == 2 && (n & 1);
+        rk.load(Ks + (odd ? KE : 0), wave, lo + n * C, hi);
+        rq.load(Qs + (odd ? KE : 0), wave, lo + n * C, hi);
+        rv.load(Vs + (odd ? VE : 0), wave, lo + n * C, hi);
+    };
+    auto load_a = [&](int64_t n, int lane) { at.load(As + (n & 1 ? WP * PB : 0), &steps[n & 1], p, n, h, wave, lane); };
+    // a block's last chunk is the first one here
+    auto starts = [&](int64_t n) { return !at.two || (n & 1) || n == nch - 1; };
     if (nch > 0) {
-        const int64_t c0 = lo + (nch - 1) * C;
-        if (p.wide) {
-            rk.load(K, wave, c0, hi);
-            rq.load(Q, wave, c0, hi);
-            rv.load(V, wave, c0, hi);
-        }
+        if (p.wide) load(nch - 1);
         load_a(nch - 1, lane);
     }
     wait_memory<0>();
@@ -94,21 +83,29 @@ __global__ void __launch_bounds__(kThreads, KD == 256 ? 1 : 2) delta_rev_kernel(
     for (int64_t n = nch - 1; n >= 0; --n) {
         const int64_t c0 = lo + n * C;
         const Steps<C>& st = steps[n & 1];
+        const bool odd = SETS == 2 && (n & 1);
+        uint16_t* const K = Ks + (odd ? KE : 0);
+        uint16_t* const Q = Qs + (odd ? KE : 0);
+        uint16_t* const V = Vs + (odd ? VE : 0);
+        const uint16_t* const A = As + (n & 1 ? WP * PB : 0);
         int lane = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
         asm volatile("" : "+v"(lane));
         const int tid = 64 * wave + lane, g4 = lane >> 4, l16 = lane & 15;
-        wait_memory<0>();
+        // what a wave stored since this chunk's rows were asked for may still be under way
+        constexpr int OUT = C / 4 + C / 8;   // Z, and the gradient of v in pairs or more
+        if (!active || !KEEP)
+            wait_memory<0>();
+        else if (starts(n + 1))
+            wait_memory<2 * KB + OUT>();
+        else
+            wait_memory<OUT>();
         lds_barrier();
         if (!ahead) {
             if (!DMA && p.wide) {
                 rk.store(K, tid);
                 rq.store(Q, tid);
                 rv.store(V, tid);
-                if (n > 0) {
-                    rk.load(K, wave, c0 - C, hi);
-                    rq.load(Q, wave, c0 - C, hi);
-                    rv.load(V, wave, c0 - C, hi);
-                }
+                if (n > 0) load(n - 1);
             } else {
                 rk.copy(K, tid, c0, hi);
                 rq.copy(Q, tid, c0, hi);
@@ -116,139 +113,133 @@ __global__ void __launch_bounds__(kThreads, KD == 256 ? 1 : 2) delta_rev_kernel(
             }
             lds_barrier();
         }
-        if (MODE == kDeltaKeep && active) {
-            float* const at = p.keep + ((first + n) * p.H + h) * ssz;
-#pragma unroll
-            for (int m = 0; m < 2 * KB; ++m)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = 32 * (m >> 1) + 8 * g4 + 4 * (m & 1) + r;
-                    if (row < p.dk && col < p.dv) at[int64_t(row) * p.dv + col] = S[m][r];
-                }
+        if (n > 0) {
+            if (ahead) load(n - 1);
+            load_a(n - 1, lane);
         }
-        put_pt<PARTS, KD, C, 4>(Q, K, PT, st, p.scale, wave, lane);
-        if (step_wave && n > 0) {
-            put_steps<C>(steps[(n - 1) & 1], gn, bn, lane);
-            fetch(n - 2, lane);
+        if constexpr (KEEP) {
+            if (active && starts(n))
+                store_state<KB>(S, p.keep + (at.block(n) * p.H + h) * ssz, p.dk, p.dv, c_wave, p.dv % 4 == 0, lane);
         }
+        put_pt<PARTS, KD>(Q, K, PT, st, p.scale, wave, lane);
         // ---- what reaches U from behind: e^{G_C - G} K dS
         f32x4 acc[IT];
-        u32x4 v[JB][PARTS];
+        u32x4 v[PARTS], ab[IT][WP];
         if (active) {
             const uint32_t bpair = pair_base<KD>(lane);
 #pragma unroll
             for (int i = 0; i < IT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            u32x4 ka[2][IT][PARTS];   // operands one step ahead
+            auto read = [&](int kb) {
+#pragma unroll
+                for (int i = 0; i < IT; ++i)
+#pragma unroll
+                    for (int x = 0; x < PARTS; ++x) ka[kb & 1][i][x] = pair_op<KD>(K + x * C * KD, 0, i, kb, bpair);
+            };
+            read(0);
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
+                if (kb + 1 < KB) read(kb + 1);
                 u32x4 sp[WP];
                 pair_parts<WP>(S[2 * kb], S[2 * kb + 1], sp);
-#pragma unroll
-                for (int i = 0; i < IT; ++i) {
-                    u32x4 a[PARTS];
-#pragma unroll
-                    for (int x = 0; x < PARTS; ++x) a[x] = pair_op<KD>(K + x * C * KD, 32 * (i >> 1), i & 1, kb, bpair);
-                    acc[i] = mma_parts<PARTS, WP>(a, sp, acc[i]);
-                }
+                mma_tiles<IT, PARTS, WP>(ka[kb & 1], sp, acc);
+                __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
             for (int i = 0; i < IT; ++i) {
-                const f32x4 e = *reinterpret_cast<const f32x4*>(&st.out[32 * (i >> 1) + 8 * g4 + 4 * (i & 1)]);
+                const f32x4 e = *reinterpret_cast<const f32x4*>(&st.out[8 * g4 + 4 * i]);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) acc[i][r] *= e[r];
             }
-            const uint32_t bv = col_base<kCols, 0>(16 * wave, lane);
+            const uint32_t bv = col_base<kCols, 0>(16 * wave, lane), bt = tri_t_base(lane);
 #pragma unroll
-            for (int jb = 0; jb < JB; ++jb)
-#pragma unroll
-                for (int i = 0; i < PARTS; ++i) v[jb][i] = col_op<kCols>(V + i * C * kCols, 32 * jb, 0, 0, bv);
-        }
-        lds_barrier();      // P^T is there; the gradient of o has been read
-        if (ahead && n > 0) rv.load(V, wave, c0 - C, hi);
-        if (active) {
-            const uint32_t b32 = row_base<32>(lane), bt = tri_t_base(lane), bk = col_base<KD, 1>(0, lane);
+            for (int i = 0; i < PARTS; ++i) v[i] = col_op<kCols>(V + i * C * kCols, 0, 0, 0, bv);
 #pragma unroll
             for (int i = 0; i < IT; ++i)
 #pragma unroll
-                for (int ip = i / 2; ip < JB; ++ip) {
-                    u32x4 a[WP];
+                for (int k = 0; k < WP; ++k) ab[i][k] = tri_t_op(A + k * PB, i, bt);
+        }
+        lds_barrier();      // P^T is there
+        if (active) {
+            const uint32_t b32 = row_base<32>(lane), bk = col_base<KD, 1>(0, lane);
+            {
+                u32x4 pt[IT][WP];
 #pragma unroll
-                    for (int k = 0; k < WP; ++k) a[k] = row_op<32>(PT + k * PB + pt_block<C>(i, ip) * 512, 0, 0, b32);
-                    acc[i] = mma_parts<WP, PARTS>(a, v[ip], acc[i]);
-                }
-            u32x4 up[JB][WP];
+                for (int i = 0; i < IT; ++i)
 #pragma unroll
-            for (int ip = 0; ip < JB; ++ip) pair_parts<WP>(acc[2 * ip], acc[2 * ip + 1], up[ip]);
-#pragma unroll
-            for (int i = 0; i < IT; ++i) {
-                acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int ip = i / 2; ip < JB; ++ip) {
-                    u32x4 a[WP];
-#pragma unroll
-                    for (int k = 0; k < WP; ++k) a[k] = tri_t_op(A + k * PB, ip, i >> 1, i & 1, bt);
-                    acc[i] = mma_parts<WP, WP>(a, up[ip], acc[i]);
-                }
+                    for (int k = 0; k < WP; ++k) pt[i][k] = row_op<32>(PT + k * PB + 512 * i, 0, 0, b32);
+                mma_tiles<IT, WP, PARTS>(pt, v, acc);
             }
+            u32x4 up[WP];
+            pair_parts<WP>(acc[0], acc[1], up);
+#pragma unroll
+            for (int i = 0; i < IT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            mma_tiles<IT, WP, WP>(ab, up, acc);
             // ---- the gradient of the incoming state
-            const float tail = st.tail;
+            constexpr int G = 4;       // tiles of the state at a time
+            u32x4 qa[G][PARTS], ka[G][PARTS];
+            auto read = [&](int m0) {
 #pragma unroll
-            for (int m = 0; m < 2 * KB; ++m)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) S[m][r] *= tail;
-#pragma unroll
-            for (int jb = 0; jb < JB; ++jb) {
-                f32x4 x[2], y[2];
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int t0 = 32 * jb + 8 * g4 + 4 * half;
-                    const f32x4 e = *reinterpret_cast<const f32x4*>(&st.in[t0]), b = *reinterpret_cast<const f32x4*>(&st.bin[t0]);
-#pragma unroll
-                    for (int r = 0; r < 4; r += 2) {
-                        float u, z;
-                        unpack<PARTS>(v[jb], 2 * half + r / 2, u, z);
-                        x[half][r] = u * (e[r] * p.scale);
-                        x[half][r + 1] = z * (e[r + 1] * p.scale);
-                    }
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) y[half][r] = -b[r] * acc[2 * jb + half][r];
-                }
-                u32x4 dp[WP], rp[WP];
-                pair_parts<WP>(x[0], x[1], dp);
-                pair_parts<WP>(y[0], y[1], rp);
-#pragma unroll
-                for (int m = 0; m < 2 * KB; ++m) {
-                    u32x4 a[PARTS], b[PARTS];
+                for (int m = 0; m < G; ++m)
 #pragma unroll
                     for (int i = 0; i < PARTS; ++i) {
-                        a[i] = col_op<KD>(Q + i * C * KD, 32 * jb, m >> 1, m & 1, bk);
-                        b[i] = col_op<KD>(K + i * C * KD, 32 * jb, m >> 1, m & 1, bk);
+                        qa[m][i] = col_op<KD>(Q + i * C * KD, 0, (m0 + m) >> 1, m & 1, bk);
+                        ka[m][i] = col_op<KD>(K + i * C * KD, 0, (m0 + m) >> 1, m & 1, bk);
                     }
-                    S[m] = mma_parts<PARTS, WP>(a, dp, S[m]);
-                    S[m] = mma_parts<PARTS, WP>(b, rp, S[m]);
+            };
+            read(0);
+            f32x4 x[2], y[2];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int t0 = 8 * g4 + 4 * half;
+                const f32x4 e = *reinterpret_cast<const f32x4*>(&st.in[t0]), b = *reinterpret_cast<const f32x4*>(&st.bin[t0]);
+#pragma unroll
+                for (int r = 0; r < 4; r += 2) {
+                    float a, z;
+                    unpack<PARTS>(v, 2 * half + r / 2, a, z);
+                    x[half][r] = a * (e[r] * p.scale);
+                    x[half][r + 1] = z * (e[r + 1] * p.scale);
                 }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) y[half][r] = -b[r] * acc[half][r];
             }
-        }
-        lds_barrier();      // q, k and A have been read
-        if (n > 0) {
-            if (ahead) {
-                rk.load(K, wave, c0 - C, hi);
-                rq.load(Q, wave, c0 - C, hi);
+            u32x4 dp[WP], rp[WP];
+            pair_parts<WP>(x[0], x[1], dp);
+            pair_parts<WP>(y[0], y[1], rp);
+            const float tail = st.tail[0];
+#pragma unroll
+            for (int m0 = 0; m0 < 2 * KB; m0 += G) {
+                if (m0 > 0) read(m0);
+#pragma unroll
+                for (int m = m0; m < m0 + G; ++m)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) S[m][r] *= tail;
+                mma_tiles<G, PARTS, WP>(qa, dp, &S[m0]);
+                mma_tiles<G, PARTS, WP>(ka, rp, &S[m0]);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            load_a(n - 1, lane);
+            if constexpr (KEEP) {
+                const int64_t pitch = int64_t(p.H) * p.dv * 4;
+                store_tiles<C, true>(acc, reinterpret_cast<char*>(p.rows) + c0 * pitch + int64_t(h) * p.dv * 4, pitch, hi - c0,
+                                     c_wave, p.dv, true, false, lane);
+#pragma unroll
+                for (int i = 0; i < IT; ++i) {
+                    const f32x4 b = *reinterpret_cast<const f32x4*>(&st.given[8 * g4 + 4 * i]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[i][r] *= b[r];
+                }
+                constexpr int E = PARTS == 1 ? 2 : 4;
+                const int64_t vp = int64_t(p.H) * p.dv * E;
+                store_tiles<C, true>(acc, static_cast<char*>(p.dv_out) + c0 * vp + int64_t(h) * p.dv * E, vp, hi - c0, c_wave, p.dv,
+                                     PARTS > 1, p.pairs, lane);
+            }
         }
     }
     if (!active) return;
     float* dst = nullptr;
     if constexpr (MODE == kDeltaStates) dst = p.carry + (w.pi * p.H + h) * ssz;
     else if (w.first && p.s_out) dst = p.s_out + (int64_t(w.slot) * p.H + h) * ssz;
-    if (!dst) return;
-#pragma unroll
-    for (int m = 0; m < 2 * KB; ++m)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = 32 * (m >> 1) + 8 * g4 + 4 * (m & 1) + r;
-            if (row < p.dk && col < p.dv) dst[int64_t(row) * p.dv + col] = S[m][r];
-        }
+    if (dst) store_state<KB>(S, dst, p.dk, p.dv, c_wave, false, lane);
 }
 
 // ---------------------------------------------------------------- a chunk's gradients
@@ -256,42 +247,50 @@ struct GradArgs {
     DeltaPass p;
     const void* dout;
     const float* keep_d;    // [chunks][H][dk][dv]: dS_out
+    const float* z;         // [T][H][dv]: Z
     void* dq;               // I/O type, or float32 per head (wide_out)
     void* dk;
-    void* dv;
     float* dbeta;
     float* dg;
     double* part;           // [chunks][H] sums of dg (a decay per head), else null
     int64_t so, sdq;        // elements between tokens of dout, of dq and dk
-    int32_t wide_out, pairs_k, pairs_v;
+    int32_t wide_out, pairs_k;
 };
 
 template <int CTRL> __device__ inline float plus_lane(float v) {
     return v + __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(v), CTRL, 0xf, 0xf, true));
 }
-// The sum over the 16 lanes of a row, in each of them.
-__device__ inline float sum16(float v) {
-    v = plus_lane<0xB1>(v);
-    v = plus_lane<0x4E>(v);
-    v = plus_lane<0x141>(v);
-    return plus_lane<0x140>(v);
-}
+// The sum over 4, 8 or 16 neighbouring lanes, in each of them.
+__device__ inline float sum4(float v) { return plus_lane<0x4E>(plus_lane<0xB1>(v)); }
+__device__ inline float sum8(float v) { return plus_lane<0x141>(sum4(v)); }
+__device__ inline float sum16(float v) { return plus_lane<0x140>(sum8(v)); }
 
-// 8 values from column c on of a row of w float32 values; zero behind its end.
-__device__ inline void load_row8(const float* row, bool on, int c, int w, bool vec, f32x4& x, f32x4& y) {
-    x = y = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    if (!on) return;
-    if (vec) {
-        if (c < w) x = *reinterpret_cast<const f32x4*>(row + c);
-        if (c + 4 < w) y = *reinterpret_cast<const f32x4*>(row + c + 4);
-    } else {
+// Four values from column c on of a row of w, as they lie in memory; zero behind its end.  With
+// `vec` a row's values come in whole fours.
+template <typename IO> struct Raw4 {
+    uint32_t u[sizeof(IO)];
+    __device__ inline void load(const IO* row, bool on, int c, int w, bool vec) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (c + e < w) x[e] = row[c + e];
-            if (c + 4 + e < w) y[e] = row[c + 4 + e];
+        for (int k = 0; k < int(sizeof(IO)); ++k) u[k] = 0;
+        if (!on || c >= w) return;
+        if (vec) {
+            __builtin_memcpy(u, __builtin_assume_aligned(row + c, 4 * sizeof(IO)), sizeof(u));
+        } else {
+            IO raw[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) raw[e] = c + e < w ? row[c + e] : IO(0);
+            __builtin_memcpy(u, raw, sizeof(u));
         }
     }
-}
+    __device__ inline f32x4 values() const {
+        IO raw[4];
+        __builtin_memcpy(raw, u, sizeof(raw));
+        f32x4 x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = IOT<IO>::to_f32(raw[e]);
+        return x;
+    }
+};
 
 // Transposed left operand from 16 x 32 blocks in order of the rows: tile jt of the columns, the
 // contraction over the 32 rows of pair ib.
@@ -306,33 +305,26 @@ template <int C> __device__ inline u32x4 block_t_op(const uint16_t* t, int ib, i
     return u32x4{u.x, u.y, v.x, v.y};
 }
 
-constexpr int kGradThreads = 512, kGradWaves = 8;
-
-// One workgroup per chunk and head.  First each wave forms U and Z of 16 columns of v (VS at a
-// time) from the states of both sides, as the walks do; they go to LDS, and each wave
-// then takes 16 columns of dq and dk, for which the states are read along their rows; the two
-// matrices over the chunk's tokens, D and N, are shared out in tiles.
-template <int PARTS, int KD, int C, int VS>
-__global__ void __launch_bounds__(kGradThreads, 2) delta_grad_kernel(GradArgs ga) {
+// One workgroup per chunk and head: what is contracted over the columns of v goes in steps of 32
+// of them, U, Z and the gradient of o through LDS, the states along their rows straight into
+// registers, 16 or 32 columns of dq and dk a wave; the two matrices over the chunk's tokens, D and
+// N, are shared out in tiles.
+template <int PARTS, int KD, int C, int W>   // W waves
+__global__ void __launch_bounds__(64 * W, 2) delta_grad_kernel(GradArgs ga) {
+    typedef typename std::conditional<PARTS == 1, uint16_t, float>::type IO;
     const DeltaPass& p = ga.p;
     constexpr int IT = C / 16, JB = C / 32, KB = KD / 32, NB = tri_blocks<C>(), PB = NB * 512, WP = 3, TRI = WP * PB;
-    constexpr int NTILE = IT * (IT + 1) / 2, MT = (NTILE + kGradWaves - 1) / kGradWaves;
-    constexpr int NC = KD > 128 ? KD / 128 : 1;      // tiles of 16 columns of dq and dk a wave
-    constexpr int VB = VS / 32;
-    // at 64 tokens the first step's matrices lie where U and Z go after it
-    constexpr bool ALIAS = C == 64;
-    constexpr int UZE = 2 * WP * C * VS;
-    static_assert(PARTS * C * VS + (ALIAS ? 2 * TRI : 0) <= UZE && 2 * TRI <= UZE, "what shares the place of U and Z fits");
-    __shared__ __align__(16) uint16_t K[PARTS * C * KD], Q[PARTS * C * KD], O[PARTS * C * VS], UZ[UZE];
-    __shared__ __align__(16) uint16_t own[ALIAS ? 8 : 2 * TRI];
+    constexpr int NTILE = IT * (IT + 1) / 2, MT = (NTILE + W - 1) / W;
+    constexpr int NC = KD / (16 * W);                // tiles of 16 columns of dq and dk a wave
+    constexpr int CPT = 32 * C / (64 * W) > 4 ? 8 : 4, N4 = CPT / 4;   // columns a thread brings of a step's rows
+    constexpr int STEP = (2 * WP + PARTS) * C * 32;  // U, Z and the gradient of o, 32 columns
+    __shared__ __align__(16) uint16_t K[PARTS * C * KD], Q[PARTS * C * KD], buf[STEP > 2 * TRI ? STEP : 2 * TRI];
     __shared__ Steps<C> st;
-    __shared__ float pz[kGradWaves][C], pg[kGradWaves][C], pm[IT][C];
-    __shared__ double ps[kGradWaves];
-    uint16_t* const V = UZ;
-    uint16_t* const A = ALIAS ? UZ + PARTS * C * VS : own;
-    uint16_t* const PT = A + TRI;
-    uint16_t* const Us = UZ;
-    uint16_t* const Zs = UZ + WP * C * VS;
+    __shared__ float pg[W][C], zu[C], vz[C];
+    __shared__ double ps[W];
+    uint16_t* const Us = buf;
+    uint16_t* const Zs = buf + WP * C * 32;
+    uint16_t* const Os = buf + 2 * WP * C * 32;
 
     const int tid = threadIdx.x, lane = tid & 63, g4 = lane >> 4, l16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -349,17 +341,29 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grad_kernel(GradArgs ga
     const int64_t ssz = int64_t(p.dk) * p.dv;
     const float* const Sin = p.keep + (ci * p.H + h) * ssz;
     const float* const Sout = ga.keep_d + (ci * p.H + h) * ssz;
-
-    for (int i = tid; i < kGradWaves * C; i += kGradThreads) (&pz[0][0])[i] = (&pg[0][0])[i] = 0.0f;
-    for (int i = tid; i < IT * C; i += kGradThreads) (&pm[0][0])[i] = 0.0f;
-    if (lane == 0) ps[wave] = 0.0;
-    if (wave == 7) {
+    Rows<PARTS, C, KD, 64 * W> rk, rq;
+    rk.prepare(p.k, int64_t(h / p.rep) * p.dk, p.sk, p.dk, tid);
+    rq.prepare(p.q, int64_t(h / p.rep) * p.dk, p.sq, p.dk, tid);
+    if (p.wide) {
+        rk.load(K, wave, c0, hi);
+        rq.load(Q, wave, c0, hi);
+        if constexpr (PARTS > 1) {
+            rk.store(K, tid);
+            rq.store(Q, tid);
+        }
+    } else {
+        rk.copy(K, tid, c0, hi);
+        rq.copy(Q, tid, c0, hi);
+    }
+    for (int i = tid; i < W * C; i += 64 * W) (&pg[0][0])[i] = 0.0f;
+    if (wave == W - 1) {
         const int64_t t = c0 + lane;
         const bool on = lane < C && t < hi;
-        put_steps<C>(st, on ? p.g[t * p.sg + h] : 0.0f, on ? p.beta[t * p.H + h] : 0.0f, lane);
+        const double s = sum_decays(on ? p.g[t * p.sg + h] : 0.0f, lane < C), end = lane_f64(s, C - 1);
+        if (lane < C) put_steps<C>(st, s, end, on ? p.beta[t * p.H + h] : 0.0f, p.least, lane);
     }
-    f32x4 aq[NC][IT], az[NC][IT], au[NC][IT], ap[MT], an[MT];
     const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+    f32x4 aq[NC][IT], az[NC][IT], au[NC][IT], ap[MT], an[MT];
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -370,277 +374,165 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grad_kernel(GradArgs ga
         it = m < 1 ? 0 : m < 3 ? 1 : m < 6 ? 2 : 3;
         jt = m - it * (it + 1) / 2;
     };
-    {
-        Rows<PARTS, C, KD, kGradThreads> rk, rq;
-        rk.prepare(p.k, int64_t(h / p.rep) * p.dk, p.sk, p.dk, tid);
-        rq.prepare(p.q, int64_t(h / p.rep) * p.dk, p.sq, p.dk, tid);
-        if (p.wide) {
-            rk.load(K, wave, c0, hi);
-            rq.load(Q, wave, c0, hi);
-            if constexpr (PARTS > 1) {
-                rk.store(K, tid);
-                rq.store(Q, tid);
-            }
-        } else {
-            rk.copy(K, tid, c0, hi);
-            rq.copy(Q, tid, c0, hi);
-        }
-        load_tri<C, kGradWaves>(p.tri + (ci * p.H + h) * tri_elems<C>(), A, wave, lane);
-    }
+    // rows of a step: 4 or 8 threads a token
+    const int ts = tid / (32 / CPT), cs = CPT * (tid % (32 / CPT));
+    const bool mine = ts < C, here = mine && c0 + ts < hi;
     const bool vec = p.dv % 4 == 0;
-    const int slices = (p.dv + VS - 1) / VS;
-    for (int sl = 0; sl < slices; ++sl) {
-        const int c_slice = sl * VS;
-        {
-            Rows<PARTS, C, VS, kGradThreads> ro, rv;
-            ro.prepare(ga.dout, int64_t(h) * p.dv + c_slice, ga.so, p.dv - c_slice, tid);
-            rv.prepare(p.v, int64_t(h) * p.dv + c_slice, p.sv, p.dv - c_slice, tid);
-            if (p.wide) {
-                ro.load(O, wave, c0, hi);
-                rv.load(V, wave, c0, hi);
-                if constexpr (PARTS > 1) {
-                    ro.store(O, tid);
-                    rv.store(V, tid);
+    const IO* const vrow = static_cast<const IO*>(p.v) + (c0 + ts) * p.sv + int64_t(h) * p.dv;
+    const IO* const orow = static_cast<const IO*>(ga.dout) + (c0 + ts) * ga.so + int64_t(h) * p.dv;
+    u32x4 nu[N4], nz[N4], ns[NC][2], nd[NC][2];
+    Raw4<IO> nv[N4], no[N4];
+    const Rsrc wu = rows_rsrc(reinterpret_cast<char*>(p.rows + (c0 * p.H + h) * p.dv), int64_t(p.H) * p.dv * 4, hi - c0, C);
+    const Rsrc wz = rows_rsrc(const_cast<char*>(reinterpret_cast<const char*>(ga.z + (c0 * p.H + h) * p.dv)), int64_t(p.H) * p.dv * 4, hi - c0, C);
+    const Rsrc ws = rows_rsrc(const_cast<char*>(reinterpret_cast<const char*>(Sin)), ssz * 4, 1, 1);
+    const Rsrc wd = rows_rsrc(const_cast<char*>(reinterpret_cast<const char*>(Sout)), ssz * 4, 1, 1);
+    // four values at column c of a row of v that begins at byte `row` of a window
+    const auto four = [&](const Rsrc& w, uint32_t row, int c) {
+        if (vec) return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(w, c < p.dv ? row + 4 * c : kPast, 0, 0));
+        u32x4 x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = __builtin_amdgcn_raw_buffer_load_b32(w, c + e < p.dv ? row + 4 * (c + e) : kPast, 0, 0);
+        return x;
+    };
+    const uint32_t trow = mine ? uint32_t(ts) * uint32_t(p.H * p.dv * 4) : kPast;
+    const auto ask = [&](int c) {
+#pragma unroll
+        for (int x = 0; x < N4; ++x) {
+            nu[x] = four(wu, trow, c + cs + 4 * x);
+            nz[x] = four(wz, trow, c + cs + 4 * x);
+            nv[x].load(vrow, here, c + cs + 4 * x, p.dv, p.wide);
+            no[x].load(orow, here, c + cs + 4 * x, p.dv, p.wide);
+        }
+    };
+    const auto ask_state = [&](const Rsrc& w, u32x4 (&n)[NC][2], int c) {
+#pragma unroll
+        for (int k = 0; k < NC; ++k)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)   // rows it does not have lie behind the window
+                n[k][x] = four(w, uint32_t(16 * (wave + W * k) + l16) * uint32_t(p.dv * 4), c + 8 * g4 + 4 * x);
+    };
+    const auto f4 = [](const u32x4& x) { return __builtin_bit_cast(f32x4, x); };
+    float s_zu = 0.0f, s_vz = 0.0f;
+    double cross = 0.0;
+    ask(0);
+    ask_state(ws, ns, 0);
+    ask_state(wd, nd, 0);
+    const uint32_t b32 = row_base<32>(lane);
+    for (int c = 0; c < p.dv; c += 32) {
+        if (mine) {
+#pragma unroll
+            for (int x = 0; x < N4; ++x) {
+                const f32x4 u = f4(nu[x]), z = f4(nz[x]), v = nv[x].values();
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s_zu = fmaf(z[e], u[e], s_zu);
+                    s_vz = fmaf(v[e], z[e], s_vz);
                 }
-            } else {
-                ro.copy(O, tid, c0, hi);
-                rv.copy(V, tid, c0, hi);
+                // rows lie in tiles of 16 x 32, part by part
+                const int cc = cs + 4 * x, to = (ts >> 4) * 512 + at_piece<32>(ts & 15, cc >> 3) + (cc & 4);
+                const auto put = [&](uint16_t* at, const f32x4& x, auto parts) {
+                    constexpr int N = decltype(parts)::value;
+                    uint32_t a[N], b[N];
+                    split<N>(x[0], x[1], a);
+                    split<N>(x[2], x[3], b);
+#pragma unroll
+                    for (int k = 0; k < N; ++k) *reinterpret_cast<uint2*>(at + k * C * 32 + to) = uint2{a[k], b[k]};
+                };
+                put(Us, u, std::integral_constant<int, WP>{});
+                put(Zs, z, std::integral_constant<int, WP>{});
+                put(Os, no[x].values(), std::integral_constant<int, PARTS>{});
             }
         }
-        wait_memory<0>();
-        __syncthreads();
-        if (sl == 0) {
-            put_pt<PARTS, KD, C, kGradWaves>(Q, K, PT, st, p.scale, wave, lane);
-            __syncthreads();
+        u32x4 sp[NC][WP];
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) cross = fma(double(f4(ns[n][x])[e]), double(f4(nd[n][x])[e]), cross);
+            pair_parts<WP>(f4(ns[n][0]), f4(ns[n][1]), sp[n]);
         }
-        // ---------------------------------------- U and Z of this wave's columns
-        f32x4 U[IT], Z[IT];
-        if (wave < VS / 16) {
-            const int c_wave = c_slice + 16 * wave, col = c_wave + l16;
-            const uint32_t bpair = pair_base<KD>(lane);
-            f32x4 W[IT];
-            double cross = 0.0;
-#pragma unroll
-            for (int i = 0; i < IT; ++i) U[i] = W[i] = zero;
-#pragma unroll
-            for (int kb = 0; kb < KB; ++kb) {
-                f32x4 s[2], d[2];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int row = 32 * kb + 8 * g4 + e;
-                    const bool on = row < p.dk && col < p.dv;
-                    s[e >> 2][e & 3] = on ? Sin[int64_t(row) * p.dv + col] : 0.0f;
-                    d[e >> 2][e & 3] = on ? Sout[int64_t(row) * p.dv + col] : 0.0f;
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) cross = fma(double(s[e >> 2][e & 3]), double(d[e >> 2][e & 3]), cross);
-                u32x4 sp[WP], dp[WP];
-                pair_parts<WP>(s[0], s[1], sp);
-                pair_parts<WP>(d[0], d[1], dp);
-#pragma unroll
-                for (int i = 0; i < IT; ++i) {
-                    u32x4 a[PARTS];
-#pragma unroll
-                    for (int x = 0; x < PARTS; ++x) a[x] = pair_op<KD>(K + x * C * KD, 32 * (i >> 1), i & 1, kb, bpair);
-                    U[i] = mma_parts<PARTS, WP>(a, sp, U[i]);
-                    W[i] = mma_parts<PARTS, WP>(a, dp, W[i]);
-                }
-            }
-            cross *= double(st.tail);
-            const uint32_t bv = col_base<VS, 0>(16 * wave, lane), b32 = row_base<32>(lane), bt = tri_t_base(lane);
-            f32x4 X[IT];
-            u32x4 xp[JB][WP], op[JB][PARTS], v[JB][PARTS];
-#pragma unroll
-            for (int jb = 0; jb < JB; ++jb) {
-                f32x4 x[2];
-#pragma unroll
-                for (int i = 0; i < PARTS; ++i) {
-                    v[jb][i] = col_op<VS>(V + i * C * VS, 32 * jb, 0, 0, bv);
-                    op[jb][i] = col_op<VS>(O + i * C * VS, 32 * jb, 0, 0, bv);
-                }
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int t0 = 32 * jb + 8 * g4 + 4 * half;
-                    const f32x4 f = *reinterpret_cast<const f32x4*>(&st.in[t0]), b = *reinterpret_cast<const f32x4*>(&st.beta[t0]);
-                    f32x4& X1 = X[2 * jb + half];
-#pragma unroll
-                    for (int r = 0; r < 4; r += 2) {
-                        float y, z;
-                        unpack<PARTS>(v[jb], 2 * half + r / 2, y, z);
-                        X1[r] = fmaf(-f[r], U[2 * jb + half][r], y);
-                        X1[r + 1] = fmaf(-f[r + 1], U[2 * jb + half][r + 1], z);
-                    }
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) x[half][r] = b[r] * X1[r];
-                }
-                pair_parts<WP>(x[0], x[1], xp[jb]);
-            }
-#pragma unroll
-            for (int i = 0; i < IT; ++i) {
-                U[i] = zero;
-#pragma unroll
-                for (int jb = 0; jb <= i / 2; ++jb) {
-                    u32x4 a[WP];
-#pragma unroll
-                    for (int k = 0; k < WP; ++k) a[k] = row_op<32>(A + k * PB + p_block(i, jb) * 512, 0, 0, b32);
-                    U[i] = mma_parts<WP, WP>(a, xp[jb], U[i]);
-                }
-                const f32x4 e = *reinterpret_cast<const f32x4*>(&st.out[32 * (i >> 1) + 8 * g4 + 4 * (i & 1)]);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    W[i][r] *= e[r];
-                    cross = fma(double(U[i][r]), double(W[i][r]), cross);
-                }
-#pragma unroll
-                for (int ip = i / 2; ip < JB; ++ip) {
-                    u32x4 a[WP];
-#pragma unroll
-                    for (int k = 0; k < WP; ++k) a[k] = row_op<32>(PT + k * PB + pt_block<C>(i, ip) * 512, 0, 0, b32);
-                    W[i] = mma_parts<WP, PARTS>(a, op[ip], W[i]);
-                }
-            }
-            u32x4 wp[JB][WP];
-#pragma unroll
-            for (int ip = 0; ip < JB; ++ip) pair_parts<WP>(W[2 * ip], W[2 * ip + 1], wp[ip]);
-#pragma unroll
-            for (int i = 0; i < IT; ++i) {
-                Z[i] = zero;
-#pragma unroll
-                for (int ip = i / 2; ip < JB; ++ip) {
-                    u32x4 a[WP];
-#pragma unroll
-                    for (int k = 0; k < WP; ++k) a[k] = tri_t_op(A + k * PB, ip, i >> 1, i & 1, bt);
-                    Z[i] = mma_parts<WP, WP>(a, wp[ip], Z[i]);
-                }
-                const int t0 = 32 * (i >> 1) + 8 * g4 + 4 * (i & 1);
-                const f32x4 b = *reinterpret_cast<const f32x4*>(&st.beta[t0]);
-                float vv[4];
-#pragma unroll
-                for (int r = 0; r < 4; r += 2) unpack<PARTS>(v[i >> 1], 2 * (i & 1) + r / 2, vv[r], vv[r + 1]);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    W[i][r] = b[r] * Z[i][r];
-                    const float zx = sum16(Z[i][r] * X[i][r]), vr = sum16(vv[r] * W[i][r]);
-                    if (l16 == 0) {
-                        pz[wave][t0 + r] += zx;
-                        pg[wave][t0 + r] -= vr;
-                    }
-                }
-            }
-            constexpr int E = PARTS == 1 ? 2 : 4;
-            const int64_t pitch = int64_t(p.H) * p.dv * E;
-            store_tiles<C, true>(W, static_cast<char*>(ga.dv) + c0 * pitch + int64_t(h) * p.dv * E, pitch, hi - c0, c_wave, p.dv,
-                                 PARTS > 1, ga.pairs_v, lane);
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) cross += __shfl_xor(cross, d);
-            if (lane == 0) ps[wave] += cross;
+        lds_barrier();
+        const bool more = c + 32 < p.dv;
+        if (more) {
+            ask(c + 32);
+            ask_state(ws, ns, c + 32);
         }
-        __syncthreads();        // v and, at 64 tokens, A and P^T have been read
-        if (wave < VS / 16) {
+        // one state after the other: both in parts would not fit the registers
 #pragma unroll
-            for (int i = 0; i < IT; ++i)
+        for (int i = 0; i < IT; ++i) {
+            u32x4 o[PARTS], z[WP];
 #pragma unroll
-                for (int r = 0; r < 4; r += 2) {
-                    const int t = 32 * (i >> 1) + 8 * g4 + 4 * (i & 1) + r, c = 16 * wave + l16;
-                    uint32_t u[WP], z[WP];
-                    split<WP>(U[i][r], U[i][r + 1], u);
-                    split<WP>(Z[i][r], Z[i][r + 1], z);
+            for (int k = 0; k < PARTS; ++k) o[k] = row_op<32>(Os + k * C * 32 + 512 * i, 0, 0, b32);
 #pragma unroll
-                    for (int k = 0; k < WP; ++k) {
-                        const int o0 = k * C * VS + at_piece<VS>(t, c >> 3) + (c & 7), o1 = k * C * VS + at_piece<VS>(t + 1, c >> 3) + (c & 7);
-                        Us[o0] = static_cast<uint16_t>(u[k]);
-                        Us[o1] = static_cast<uint16_t>(u[k] >> 16);
-                        Zs[o0] = static_cast<uint16_t>(z[k]);
-                        Zs[o1] = static_cast<uint16_t>(z[k] >> 16);
-                    }
-                }
-        }
-        __syncthreads();
-        // ---------------------------------------- products over the columns of v
-        const uint32_t bvs = row_base<VS>(lane);
+            for (int k = 0; k < WP; ++k) z[k] = row_op<32>(Zs + k * C * 32 + 512 * i, 0, 0, b32);
 #pragma unroll
-        for (int vb = 0; vb < VB; ++vb) {
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                const int i0 = 16 * (wave + kGradWaves * c), row = i0 + l16;
-                if (i0 >= p.dk) continue;
-                f32x4 x, y;
-                u32x4 sp[WP], dp[WP];
-                load_row8(Sin + int64_t(row) * p.dv, row < p.dk, c_slice + 32 * vb + 8 * g4, p.dv, vec, x, y);
-                pair_parts<WP>(x, y, sp);
-                load_row8(Sout + int64_t(row) * p.dv, row < p.dk, c_slice + 32 * vb + 8 * g4, p.dv, vec, x, y);
-                pair_parts<WP>(x, y, dp);
-#pragma unroll
-                for (int i = 0; i < IT; ++i) {
-                    u32x4 o[PARTS], u[WP], z[WP];
-#pragma unroll
-                    for (int k = 0; k < PARTS; ++k) o[k] = row_op<VS>(O + k * C * VS, 16 * i, vb, bvs);
-#pragma unroll
-                    for (int k = 0; k < WP; ++k) {
-                        u[k] = row_op<VS>(Us + k * C * VS, 16 * i, vb, bvs);
-                        z[k] = row_op<VS>(Zs + k * C * VS, 16 * i, vb, bvs);
-                    }
-                    aq[c][i] = mma_parts<PARTS, WP>(o, sp, aq[c][i]);
-                    az[c][i] = mma_parts<WP, WP>(z, sp, az[c][i]);
-                    au[c][i] = mma_parts<WP, WP>(u, dp, au[c][i]);
-                }
+            for (int n = 0; n < NC; ++n) {
+                aq[n][i] = mma_parts<PARTS, WP>(o, sp[n], aq[n][i]);
+                az[n][i] = mma_parts<WP, WP>(z, sp[n], az[n][i]);
             }
-#pragma unroll
-            for (int mm = 0; mm < MT; ++mm) {
-                const int m = wave + kGradWaves * mm;
-                if (m >= NTILE) break;
-                int it, jt;
-                tile(m, it, jt);
-                u32x4 o[PARTS], u[WP], z[WP];
-#pragma unroll
-                for (int k = 0; k < PARTS; ++k) o[k] = row_op<VS>(O + k * C * VS, 16 * it, vb, bvs);
-#pragma unroll
-                for (int k = 0; k < WP; ++k) {
-                    u[k] = row_op<VS>(Us + k * C * VS, 16 * jt, vb, bvs);
-                    z[k] = row_op<VS>(Zs + k * C * VS, 16 * it, vb, bvs);
-                }
-                ap[mm] = mma_parts<WP, PARTS>(u, o, ap[mm]);
-                an[mm] = mma_parts<WP, WP>(u, z, an[mm]);
-            }
+            __builtin_amdgcn_sched_barrier(0);   // operands read further ahead would not fit either
         }
-        __syncthreads();        // U, Z and the gradient of o have been read
+#pragma unroll
+        for (int n = 0; n < NC; ++n) pair_parts<WP>(f4(nd[n][0]), f4(nd[n][1]), sp[n]);
+        if (more) ask_state(wd, nd, c + 32);
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            u32x4 u[WP];
+#pragma unroll
+            for (int k = 0; k < WP; ++k) u[k] = row_op<32>(Us + k * C * 32 + 512 * i, 0, 0, b32);
+#pragma unroll
+            for (int n = 0; n < NC; ++n) au[n][i] = mma_parts<WP, WP>(u, sp[n], au[n][i]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int mm = 0; mm < MT; ++mm) {
+            const int m = wave + W * mm;
+            if (m >= NTILE) break;
+            int it, jt;
+            tile(m, it, jt);
+            u32x4 o[PARTS], u[WP], z[WP];
+#pragma unroll
+            for (int k = 0; k < PARTS; ++k) o[k] = row_op<32>(Os + k * C * 32 + 512 * it, 0, 0, b32);
+#pragma unroll
+            for (int k = 0; k < WP; ++k) {
+                u[k] = row_op<32>(Us + k * C * 32 + 512 * jt, 0, 0, b32);
+                z[k] = row_op<32>(Zs + k * C * 32 + 512 * it, 0, 0, b32);
+            }
+            ap[mm] = mma_parts<WP, PARTS>(u, o, ap[mm]);
+            an[mm] = mma_parts<WP, WP>(u, z, an[mm]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        lds_barrier();
     }
+    s_zu = CPT == 8 ? sum4(s_zu) : sum8(s_zu);
+    s_vz = CPT == 8 ? sum4(s_vz) : sum8(s_vz);
+    if (mine && cs == 0) {
+        zu[ts] = s_zu;
+        vz[ts] = s_vz;
+    }
+    cross *= double(st.tail[0]);
+    wait_memory<0>();
+    __syncthreads();        // q and k are there
     // ---------------------------------------- D and N, tiles on and below the diagonal
-    uint16_t* const Ds = UZ;
-    uint16_t* const Ns = UZ + TRI;
+    uint16_t* const Ds = buf;
+    uint16_t* const Ns = buf + TRI;
     const uint32_t base = row_base<KD>(lane);
 #pragma unroll
     for (int mm = 0; mm < MT; ++mm) {
-        const int m = wave + kGradWaves * mm;
+        const int m = wave + W * mm;
         if (m >= NTILE) break;
         int it, jt;
         tile(m, it, jt);
-        f32x4 kk = zero;
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-            u32x4 x[PARTS], y[PARTS];
-#pragma unroll
-            for (int i = 0; i < PARTS; ++i) {
-                x[i] = row_op<KD>(K + i * C * KD, 16 * jt, kb, base);
-                y[i] = row_op<KD>(K + i * C * KD, 16 * it, kb, base);
-            }
-            kk = mma_parts<PARTS, PARTS>(x, y, kk);
-        }
         const int i = 16 * it + l16, j0 = 16 * jt + 4 * g4;
         const float gi = st.hi[i], ei = st.lo[i], b = st.beta[i];
-        float miss = 0.0f;
         f32x4 d, n;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const float e = __builtin_amdgcn_exp2f((gi - st.hi[j0 + r]) + (ei - st.lo[j0 + r]));
             d[r] = j0 + r <= i ? ap[mm][r] * (e * p.scale) : 0.0f;
-            const float z = j0 + r < i ? an[mm][r] * e : 0.0f;
-            n[r] = -b * z;
-            miss = fmaf(z, j0 + r < i ? kk[r] : 0.0f, miss);
+            n[r] = j0 + r < i ? -b * (an[mm][r] * e) : 0.0f;
         }
-        miss += __shfl_xor(miss, 16);
-        miss += __shfl_xor(miss, 32);
-        if (g4 == 0) pm[jt][i] = miss;
         const int o = p_block(it, jt >> 1) * 512 + 4 * (g4 & 1);
         const int at = o + at_piece<32>(l16, 2 * (jt & 1) + (g4 >> 1)), above = o + at_piece<32>(l16, 2 + (g4 >> 1));
         uint32_t x[WP], y[WP], u[WP], v[WP];
@@ -660,13 +552,19 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grad_kernel(GradArgs ga
     }
     __syncthreads();
     // ---------------------------------------- dq and dk of this wave's columns
+    const auto element = [&](const uint16_t* t, int r, int col) {
+        const int o = at_piece<KD>(r, col >> 3) + (col & 7);
+        float x = 0.0f;
+#pragma unroll
+        for (int w = PARTS - 1; w >= 0; --w) x += __uint_as_float(uint32_t(t[w * C * KD + o]) << 16);
+        return x;
+    };
     {
-        const uint32_t b32 = row_base<32>(lane);
         const int oe = PARTS > 1 || ga.wide_out ? 4 : 2;
         const int64_t pitch = ga.sdq * oe, at = c0 * pitch + int64_t(ga.wide_out ? h : h / p.rep) * p.dk * oe;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            const int i0 = 16 * (wave + kGradWaves * c);
+            const int i0 = 16 * (wave + W * c);
             if (i0 >= p.dk) continue;
 #pragma unroll
             for (int i = 0; i < IT; ++i) {
@@ -676,7 +574,10 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grad_kernel(GradArgs ga
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     aq[c][i][r] *= e[r] * p.scale;
-                    au[c][i][r] = fmaf(l[r], au[c][i][r], -f[r] * az[c][i][r]);
+                    au[c][i][r] *= l[r];
+                    // u_j . dS_out^T k_j of the tokens
+                    cross = fma(double(au[c][i][r]), double(element(K, t0 + r, i0 + l16)), cross);
+                    au[c][i][r] = fmaf(-f[r], az[c][i][r], au[c][i][r]);
                 }
             }
             const uint32_t bc = col_base<KD, 0>(i0, lane);
@@ -717,36 +618,31 @@ __global__ void __launch_bounds__(kGradThreads, 2) delta_grad_kernel(GradArgs ga
             for (int i = 0; i < IT; ++i)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int t = 16 * i + 4 * g4 + r, col = i0 + l16, o = at_piece<KD>(t, col >> 3) + (col & 7);
-                    float x = 0.0f;
-#pragma unroll
-                    for (int w = PARTS - 1; w >= 0; --w) x += __uint_as_float(uint32_t(Q[w * C * KD + o]) << 16);
-                    const float s = sum16(x * aq[c][i][r]);
+                    const int t = 16 * i + 4 * g4 + r;
+                    const float s = sum16(element(Q, t, i0 + l16) * aq[c][i][r]);
                     if (l16 == 0) pg[wave][t] += s;
                 }
         }
     }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) cross += __shfl_xor(cross, d);
+    if (lane == 0) ps[wave] = cross;
     __syncthreads();
     if (wave == 0) {
         double x = 0.0, end = 0.0;
-        float z = 0.0f;
         const int64_t t = c0 + lane;
         const bool on = lane < C && t < hi;
         if (lane < C) {
+            x = -double(st.beta[lane] * vz[lane]);
 #pragma unroll
-            for (int k = 0; k < kGradWaves; ++k) {
-                x += double(pg[k][lane]);
-                z += pz[k][lane];
-            }
-#pragma unroll
-            for (int k = 0; k < IT; ++k) z -= pm[k][lane];
+            for (int k = 0; k < W; ++k) x += double(pg[k][lane]);
         }
 #pragma unroll
-        for (int k = 0; k < kGradWaves; ++k) end += ps[k];
+        for (int k = 0; k < W; ++k) end += ps[k];
         const double s = scan_f64(x);                       // of the tokens up to this one
         const double dg = end + (lane_f64(s, 63) - s) + x;
         if (on) {
-            ga.dbeta[t * p.H + h] = z;
+            ga.dbeta[t * p.H + h] = zu[lane] / st.beta[lane];     // Z . r = Z . U / beta
             if (!ga.part) ga.dg[t * p.H + h] = float(dg);
         }
         if (ga.part) {
@@ -818,14 +714,14 @@ struct GradPlan {
     int chunk;
     int64_t nchunks, piece, npieces;
     bool pieced;
-    size_t tri, keep, carry, trans, part, wide;   // bytes of one buffer each
+    size_t tri, steps, keep, rows, carry, trans, part, wide;   // bytes of one buffer each
     size_t bytes;
 };
 
 inline int make_grad_plan(const ssm_linattn_dims* d, bool packed, GradPlan* pl) {
-    pl->chunk = d->io_dtype == SSM_BF16 && d->dk <= 128 && d->dv <= 128 ? 64 : 32;
+    pl->chunk = d->io_dtype == SSM_BF16 ? 64 : 32;
     const int64_t each = packed ? d->tokens : d->tokens / d->nseq;
-    const int64_t piece = d->piece_len;
+    const int64_t piece = d->piece_len ? d->piece_len : choose_piece(d, packed, 60);
     pl->pieced = piece > 0 && piece < each;
     pl->piece = pl->pieced ? piece : (int64_t(1) << 31);
     pl->npieces = !pl->pieced ? d->nseq : packed ? d->tokens / piece + d->nseq : d->nseq * cdiv(each, piece);
@@ -835,25 +731,23 @@ inline int make_grad_plan(const ssm_linattn_dims* d, bool packed, GradPlan* pl) 
     const size_t nk = static_cast<size_t>(pl->nchunks * d->nheads), np = static_cast<size_t>(pl->npieces * d->nheads);
     const size_t state = static_cast<size_t>(d->dk * d->dv) * 4;
     pl->tri = up256(nk * (pl->chunk == 64 ? tri_elems<64>() : tri_elems<32>()) * 2);
+    pl->steps = nk * static_cast<size_t>(pl->chunk / kChunk) * sizeof(Steps<kChunk>);
     pl->keep = up256(nk * state);
+    pl->rows = up256(static_cast<size_t>(d->tokens * d->nheads * d->dv) * 4);
     pl->carry = pl->pieced ? up256(np * state) : 0;
     pl->trans = pl->pieced ? up256(np * static_cast<size_t>(d->dk * d->dk) * 4) : 0;
     pl->part = d->head_decay ? up256(nk * 8) : 0;
     pl->wide = d->nheads > d->kheads ? up256(static_cast<size_t>(d->tokens * d->nheads * d->dk) * 4) : 0;
-    pl->bytes = pl->tri + 2 * (pl->keep + pl->carry + pl->trans + pl->wide) + pl->part;
+    pl->bytes = pl->tri + pl->steps + 2 * (pl->keep + pl->rows + pl->carry + pl->trans + pl->wide) + pl->part;
     return SSM_OK;
 }
 
-template <int C, int MODE> void run_rev(const DeltaPass& p, bool f32, hipStream_t s) {
+template <int MODE> void run_rev(const DeltaPass& p, bool f32, hipStream_t s) {
     const dim3 grid(static_cast<uint32_t>(int64_t(p.npieces) * p.H * p.vslices)), block(kThreads);
 #define SSM_REV(K)                                                                                  \
     do {                                                                                            \
-        if constexpr (C == 32) {                                                                    \
-            if (f32) launch_kernel(delta_rev_kernel<3, K, C, MODE>, grid, block, 0, s, p);          \
-            else launch_kernel(delta_rev_kernel<1, K, C, MODE>, grid, block, 0, s, p);              \
-        } else if constexpr (K <= 128) {                                                            \
-            launch_kernel(delta_rev_kernel<1, K, C, MODE>, grid, block, 0, s, p);                   \
-        }                                                                                           \
+        if (f32) launch_kernel(delta_rev_kernel<3, K, MODE>, grid, block, 0, s, p);                 \
+        else launch_kernel(delta_rev_kernel<1, K, MODE>, grid, block, 0, s, p);                     \
     } while (0)
     if (p.dk <= 64) SSM_REV(64);
     else if (p.dk <= 128) SSM_REV(128);
@@ -861,31 +755,17 @@ template <int C, int MODE> void run_rev(const DeltaPass& p, bool f32, hipStream_
 #undef SSM_REV
 }
 
-inline void run_rev(const DeltaPass& p, bool f32, int chunk, bool keep, hipStream_t s) {
-    if (chunk == 64) {
-        if (keep) run_rev<64, kDeltaKeep>(p, f32, s);
-        else run_rev<64, kDeltaStates>(p, f32, s);
-    } else {
-        if (keep) run_rev<32, kDeltaKeep>(p, f32, s);
-        else run_rev<32, kDeltaStates>(p, f32, s);
-    }
-}
-
-inline void run_grad(const GradArgs& a, bool f32, int chunk, int64_t nchunks, hipStream_t s) {
-    const dim3 grid(static_cast<uint32_t>(nchunks), a.p.H), block(kGradThreads);
-    const auto start = [&](auto* kernel) { launch_kernel(kernel, grid, block, 0, s, a); };
-    const int dk = a.p.dk;
-    if (chunk == 64) {
-        if (dk <= 64) start(delta_grad_kernel<1, 64, 64, 128>);
-        else start(delta_grad_kernel<1, 128, 64, 128>);
-    } else if (!f32) {
-        if (dk <= 128) start(delta_grad_kernel<1, 128, 32, 128>);
-        else start(delta_grad_kernel<1, 256, 32, 128>);
-    } else {
-        if (dk <= 64) start(delta_grad_kernel<3, 64, 32, 128>);
-        else if (dk <= 128) start(delta_grad_kernel<3, 128, 32, 128>);
-        else start(delta_grad_kernel<3, 256, 32, 64>);   // 128 columns of v would not fit the LDS
-    }
+inline void run_grad(const GradArgs& a, bool f32, int64_t nchunks, hipStream_t s) {
+    const dim3 grid(static_cast<uint32_t>(nchunks), a.p.H);
+#define SSM_GRAD(K, W)                                                                              \
+    do {                                                                                            \
+        if (f32) launch_kernel(delta_grad_kernel<3, K, 32, W>, grid, dim3(64 * W), 0, s, a);        \
+        else launch_kernel(delta_grad_kernel<1, K, 64, W>, grid, dim3(64 * W), 0, s, a);            \
+    } while (0)
+    if (a.p.dk <= 64) SSM_GRAD(64, 4);
+    else if (a.p.dk <= 128) SSM_GRAD(128, 4);
+    else SSM_GRAD(256, 8);
+#undef SSM_GRAD
 }
 
 template <typename IO> void run_fold(const FoldArgs& a, bool v4, hipStream_t s) {
@@ -954,8 +834,11 @@ int ssm_delta_bwd(const void* q, const void* k, const void* v, const float* g, c
         return reinterpret_cast<float*>(r);
     };
     uint16_t* const tri = reinterpret_cast<uint16_t*>(take(pl.tri));
+    float* const steps = take(pl.steps);
     float* const keep_s = take(pl.keep);
     float* const keep_d = take(pl.keep);
+    float* const rows_u = take(pl.rows);
+    float* const rows_z = take(pl.rows);
     float* const carry_s = take(pl.carry);
     float* const carry_d = take(pl.carry);
     float* const trans = take(pl.trans);
@@ -967,10 +850,10 @@ int ssm_delta_bwd(const void* q, const void* k, const void* v, const float* g, c
     const bool f32 = d.io_dtype == SSM_F32, shared = d.nheads > d.kheads;
     DeltaPass f = {};
     f.q = q; f.k = k; f.v = v; f.g = g; f.beta = beta; f.cu = cu_seqlens; f.s_in = s0;
-    f.tri = tri; f.keep = keep_s; f.carry = carry_s; f.trans = trans; f.trans_t = trans_t;
+    f.tri = tri; f.steps = steps; f.keep = keep_s; f.carry = carry_s; f.trans = trans; f.trans_t = trans_t;
     f.sq = z.q; f.sk = z.k; f.sv = z.v; f.sg = d.head_decay ? 0 : d.nheads;
     f.T = d.tokens; f.L = cu_seqlens ? 0 : d.tokens / d.nseq;
-    f.piece = pl.piece;
+    f.piece = pl.piece; f.block = pl.chunk;
     f.rep = static_cast<int32_t>(d.nheads / d.kheads); f.H = static_cast<int32_t>(d.nheads);
     f.dk = static_cast<int32_t>(d.dk); f.dv = static_cast<int32_t>(d.dv);
     f.vslices = static_cast<int32_t>(cdiv(d.dv, kCols)); f.kslices = static_cast<int32_t>(cdiv(d.dk, kCols));
@@ -978,29 +861,29 @@ int ssm_delta_bwd(const void* q, const void* k, const void* v, const float* g, c
     f.npieces = static_cast<int32_t>(pl.npieces); f.pieced = pl.pieced;
     f.wide = wide_rows(q, z.q, d.dk, z.e) && wide_rows(k, z.k, d.dk, z.e) && wide_rows(v, z.v, d.dv, z.e) &&
              wide_rows(dout, z.o, d.dv, z.e);
-    f.scale = d.scale;
+    f.scale = d.scale; f.least = kLeastStep; f.rows = rows_u;
     DeltaPass r = f;     // against time
     r.v = dout; r.sv = z.o; r.s_in = ds_last; r.s_out = gr.ds0; r.keep = keep_d; r.carry = carry_d;
+    r.rows = rows_z; r.dv_out = gr.dv; r.pairs = pair_rows(gr.dv, wv, d.dv);
     GradArgs a = {};
-    a.p = f; a.dout = dout; a.keep_d = keep_d; a.so = z.o;
-    a.dq = shared ? static_cast<void*>(wq) : gr.dq; a.dk = shared ? static_cast<void*>(wkk) : gr.dk; a.dv = gr.dv;
+    a.p = f; a.dout = dout; a.keep_d = keep_d; a.z = rows_z; a.so = z.o;
+    a.dq = shared ? static_cast<void*>(wq) : gr.dq; a.dk = shared ? static_cast<void*>(wkk) : gr.dk;
     a.dbeta = gr.dbeta; a.dg = gr.dg; a.part = d.head_decay ? part : nullptr;
     a.sdq = d.nheads * d.dk; a.wide_out = shared;
     a.pairs_k = !shared && pair_rows(gr.dq, a.sdq, d.dk) && pair_rows(gr.dk, a.sdq, d.dk);
-    a.pairs_v = pair_rows(gr.dv, wv, d.dv);
 
     hipStream_t s = static_cast<hipStream_t>(stream);
     launch_error = hipSuccess;
-    launch_delta_tri(f, f32, pl.chunk, pl.nchunks, s);
+    launch_delta_tri(f, f32, pl.nchunks, s);
     if (pl.pieced) {
-        launch_delta_pass(f, f32, pl.chunk, kDeltaStates, s);
+        launch_delta_pass(f, f32, kDeltaStates, s);
         launch_delta_carry(f, false, s);
-        run_rev(r, f32, pl.chunk, false, s);
+        run_rev<kDeltaStates>(r, f32, s);
         launch_delta_carry(r, true, s);
     }
-    launch_delta_pass(f, f32, pl.chunk, kDeltaKeep, s);
-    run_rev(r, f32, pl.chunk, true, s);
-    run_grad(a, f32, pl.chunk, pl.nchunks, s);
+    launch_delta_pass(f, f32, kDeltaKeep, s);
+    run_rev<kDeltaKeep>(r, f32, s);
+    run_grad(a, f32, pl.nchunks, s);
     if (shared) {
         const FoldArgs fa = {{wq, wkk}, {gr.dq, gr.dk}, d.tokens * d.kheads, f.rep, f.dk};
         const bool v4 = d.dk % 4 == 0 && !misaligned(gr.dq, 4 * z.e) && !misaligned(gr.dk, 4 * z.e);

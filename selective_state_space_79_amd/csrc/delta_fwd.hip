@@ -41,7 +41,17 @@ __global__ void __launch_bounds__(kThreads) delta_tri_kernel(DeltaPass p) {
     if (wave == 3) {
         const int64_t t = c0 + lane;
         const bool on = lane < C && t < sq.end;
-        put_steps<C>(st, on ? p.g[t * p.sg + h] : 0.0f, on ? p.beta[t * p.H + h] : 0.0f, lane);
+        const float beta = on ? p.beta[t * p.H + h] : 0.0f;
+        const double s = sum_decays(on ? p.g[t * p.sg + h] : 0.0f, lane < C), end = lane_f64(s, C - 1);
+        if (lane < C) put_steps<C>(st, s, end, beta, p.least, lane);
+        // for the walks' chunks, sums of their own
+        constexpr int per = C / kChunk;
+        const double middle = per == 2 ? lane_f64(s, kChunk - 1) : 0.0;
+        const bool second = lane >= kChunk;
+        auto* const to = reinterpret_cast<Steps<kChunk>*>(p.steps + ((ci * per + (second ? 1 : 0)) * p.H + h) * 256);
+        if (lane < C)
+            put_steps<kChunk>(*to, second ? s - middle : s, second || per == 1 ? end - (second ? middle : 0.0) : middle, beta, p.least,
+                              lane % kChunk);
     }
     wait_memory<0>();
     __syncthreads();
@@ -149,14 +159,19 @@ __global__ void __launch_bounds__(kThreads) delta_tri_kernel(DeltaPass p) {
 }
 
 // ---------------------------------------------------------------- the walk
-// One workgroup walks one piece of one head's sequence for 64 columns of the state, 16 a wave.
-template <int PARTS, int KD, int C, int MODE>
-__global__ void __launch_bounds__(kThreads, KD == 256 ? 1 : 2) delta_pass_kernel(DeltaPass p) {
+// One workgroup walks one piece of one head's sequence for 64 columns of the state, 16 a wave, in
+// chunks of 32 tokens: 64 would halve the splits of the state into parts, but take the LDS of
+// four workgroups on a CU and twice the time from chunk to chunk.
+//
+// With outputs one set of tiles, and the next chunk's rows are asked for as soon as this one's
+// are read; without, two sets and one barrier a chunk.
+template <int PARTS, int KD, int MODE>
+__global__ void __launch_bounds__(kThreads, pass_waves(KD, PARTS, MODE)) delta_pass_kernel(DeltaPass p) {
     constexpr bool FULL = MODE == kDeltaFull, KEEP = MODE == kDeltaKeep, DMA = PARTS == 1;
-    constexpr int IT = C / 16, JB = C / 32, KB = KD / 32, NTILE = IT * (IT + 1) / 2, NB = tri_blocks<C>(), PB = NB * 512;
-    constexpr int WP = 3;   // parts of what is not a bf16 input
-    __shared__ __align__(16) uint16_t K[PARTS * C * KD], V[PARTS * C * kCols], A[WP * PB];
-    __shared__ __align__(16) uint16_t Q[FULL ? PARTS * C * KD : 8], Ps[FULL ? WP * PB : 8];
+    constexpr int C = kChunk, IT = C / 16, KB = KD / 32, NTILE = 3, PB = 2 * 512, WP = 3;   // parts of what is no bf16 input
+    constexpr int SETS = FULL || !DMA ? 1 : 2, ASETS = FULL ? 1 : 2, KE = PARTS * C * KD, VE = PARTS * C * kCols;
+    __shared__ __align__(16) uint16_t Ks[SETS * KE], Vs[SETS * VE], As[ASETS * WP * PB];
+    __shared__ __align__(16) uint16_t Q[FULL ? KE : 8], Ps[FULL ? WP * PB : 8];
     __shared__ Steps<C> steps[2];
     const int tid = threadIdx.x, lane = tid & 63, g4 = lane >> 4, l16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -178,46 +193,35 @@ __global__ void __launch_bounds__(kThreads, KD == 256 ? 1 : 2) delta_pass_kernel
         else if (p.s_in)
             src = p.s_in + (int64_t(w.slot) * p.H + h) * ssz;
     }
+    load_state<KB>(S, src, p.dk, p.dv, c_wave, lane);
+    if (trans) {
 #pragma unroll
-    for (int m = 0; m < 2 * KB; ++m)
+        for (int m = 0; m < 2 * KB; ++m)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = 32 * (m >> 1) + 8 * g4 + 4 * (m & 1) + r;
-            S[m][r] = trans ? (row == col ? 1.0f : 0.0f) : src && row < p.dk && col < p.dv ? src[int64_t(row) * p.dv + col] : 0.0f;
-        }
-    if constexpr (FULL) {   // tiles above the diagonal that share a block with one on it stay zero
+            for (int r = 0; r < 4; ++r) S[m][r] = 32 * (m >> 1) + 8 * g4 + 4 * (m & 1) + r == col ? 1.0f : 0.0f;
+    }
+    if constexpr (FULL) {   // the tile above the diagonal that shares a block with one on it stays zero
         for (int i = tid; i < WP * PB / 2; i += kThreads) reinterpret_cast<uint32_t*>(Ps)[i] = 0;
     }
 
     const int64_t nch = (hi - lo + C - 1) / C;
-    const Chunks ch(p, C);
-    const int64_t first = uniform(piece_base(ch, w.seq)) + (lo - w.sq.start) / C;
-    const uint16_t* const tri = p.tri + (first * p.H + h) * tri_elems<C>();
-    auto load_a = [&](int64_t n, int lane) { load_tri<C, 4>(tri + n * p.H * tri_elems<C>(), A, wave, lane); };
-    const bool step_wave = wave == 3;
-    float gn = 0.0f, bn = 0.0f;
-    auto fetch = [&](int64_t n, int lane) {
-        const int64_t t = lo + n * C + lane;
-        const bool on = n < nch && lane < C && t < hi;
-        gn = on ? p.g[t * p.sg + h] : 0.0f;
-        bn = on ? p.beta[t * p.H + h] : 0.0f;
-    };
-    if (step_wave) {
-        fetch(0, lane);
-        put_steps<C>(steps[0], gn, bn, lane);
-        fetch(1, lane);
-    }
+    const Blocked at(p, w, lo);
     Rows<PARTS, C, KD, kThreads> rk, rq;
     Rows<PARTS, C, kCols, kThreads> rv;
     rk.prepare(p.k, int64_t(h / p.rep) * p.dk, p.sk, p.dk, tid);
     rq.prepare(p.q, int64_t(h / p.rep) * p.dk, p.sq, p.dk, tid);
     rv.prepare(p.v, int64_t(h) * p.dv + c_slice, p.sv, p.dv - c_slice, tid);
     const bool ahead = DMA && p.wide;
+    auto load_k = [&](int64_t n) { rk.load(Ks + (SETS == 2 && n & 1 ? KE : 0), wave, lo + n * C, hi); };
+    auto load_qv = [&](int64_t n) {
+        if (!trans) rv.load(Vs + (SETS == 2 && n & 1 ? VE : 0), wave, lo + n * C, hi);
+        if constexpr (FULL) rq.load(Q, wave, lo + n * C, hi);
+    };
+    auto load_a = [&](int64_t n, int lane) { at.load(As + (ASETS == 2 && n & 1 ? WP * PB : 0), &steps[n & 1], p, n, h, wave, lane); };
     if (nch > 0) {
         if (p.wide) {
-            rk.load(K, wave, lo, hi);
-            if (!trans) rv.load(V, wave, lo, hi);
-            if constexpr (FULL) rq.load(Q, wave, lo, hi);
+            load_k(0);
+            load_qv(0);
         }
         load_a(0, lane);
     }
@@ -226,24 +230,32 @@ __global__ void __launch_bounds__(kThreads, KD == 256 ? 1 : 2) delta_pass_kernel
     for (int64_t n = 0; n < nch; ++n) {
         const int64_t c0 = lo + n * C;
         const Steps<C>& st = steps[n & 1];
+        uint16_t* const K = Ks + (SETS == 2 && n & 1 ? KE : 0);
+        uint16_t* const V = Vs + (SETS == 2 && n & 1 ? VE : 0);
+        const uint16_t* const A = As + (ASETS == 2 && n & 1 ? WP * PB : 0);
         // the lane as the loop's own value: operand addresses are cheap to form anew
         int lane = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
         asm volatile("" : "+v"(lane));
         const int tid = 64 * wave + lane, g4 = lane >> 4, l16 = lane & 15;
-        if (ahead) {
+        // this chunk's rows and A; what a wave stored since they were asked for may still be under way
+        constexpr int OUT = C / 4;
+        if (!active || MODE == kDeltaStates)
             wait_memory<0>();
-            lds_barrier();
-        } else {
-            wait_memory<0>();
-            lds_barrier();
+        else if (FULL && DMA && p.pairs)
+            wait_memory<OUT / 2>();
+        else if (KEEP && at.starts(n - 1))
+            wait_memory<2 * KB + OUT>();
+        else
+            wait_memory<OUT>();
+        lds_barrier();
+        if (!ahead) {
             if (!DMA && p.wide) {
                 rk.store(K, tid);
                 if (!trans) rv.store(V, tid);
                 if constexpr (FULL) rq.store(Q, tid);
                 if (n + 1 < nch) {
-                    rk.load(K, wave, c0 + C, hi);
-                    if (!trans) rv.load(V, wave, c0 + C, hi);
-                    if constexpr (FULL) rq.load(Q, wave, c0 + C, hi);
+                    load_k(n + 1);
+                    load_qv(n + 1);
                 }
             } else {
                 rk.copy(K, tid, c0, hi);
@@ -252,23 +264,22 @@ __global__ void __launch_bounds__(kThreads, KD == 256 ? 1 : 2) delta_pass_kernel
             }
             lds_barrier();
         }
-        if constexpr (KEEP) {
-            if (active) {
-                float* const at = p.keep + ((first + n) * p.H + h) * ssz;
-#pragma unroll
-                for (int m = 0; m < 2 * KB; ++m)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int row = 32 * (m >> 1) + 8 * g4 + 4 * (m & 1) + r;
-                        if (row < p.dk && col < p.dv) at[int64_t(row) * p.dv + col] = S[m][r];
-                    }
+        if (ASETS == 2 && n + 1 < nch) {
+            if (SETS == 2 && ahead) {
+                load_k(n + 1);
+                load_qv(n + 1);
             }
+            load_a(n + 1, lane);
         }
-        const uint32_t base = row_base<KD>(lane), bpair = pair_base<KD>(lane);
+        if constexpr (KEEP) {
+            if (active && at.starts(n))
+                store_state<KB>(S, p.keep + (at.block(n) * p.H + h) * ssz, p.dk, p.dv, c_wave, p.dv % 4 == 0, lane);
+        }
+        const uint32_t base = row_base<KD>(lane), bpair = pair_base<KD>(lane), b32 = row_base<32>(lane);
         if constexpr (FULL) {
             // ---- P, tiles on and below the diagonal
-            for (int m = wave; m < NTILE; m += 4) {
-                const int it = m < 1 ? 0 : m < 3 ? 1 : m < 6 ? 2 : 3, jt = m - it * (it + 1) / 2;
+            if (wave < NTILE) {
+                const int it = wave < 1 ? 0 : 1, jt = wave - it;
                 f32x4 a = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb) {
@@ -281,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, KD == 256 ? 1 : 2) delta_pass_kernel
                     a = mma_parts<PARTS, PARTS>(x, y, a);
                 }
                 const int i = 16 * it + l16, j0 = 16 * jt + 4 * g4;
-                const int o = p_block(it, jt >> 1) * 512 + at_piece<32>(l16, 2 * (jt & 1) + (g4 >> 1)) + 4 * (g4 & 1);
+                const int o = 512 * it + at_piece<32>(l16, 2 * jt + (g4 >> 1)) + 4 * (g4 & 1);
                 const float gi = st.hi[i], ei = st.lo[i];
                 const f32x4 gj = *reinterpret_cast<const f32x4*>(&st.hi[j0]), ej = *reinterpret_cast<const f32x4*>(&st.lo[j0]);
 #pragma unroll
@@ -296,61 +307,57 @@ __global__ void __launch_bounds__(kThreads, KD == 256 ? 1 : 2) delta_pass_kernel
                 for (int k = 0; k < WP; ++k) *reinterpret_cast<uint2*>(Ps + k * PB + o) = uint2{x[k], y[k]};
             }
         }
-        if (step_wave && n + 1 < nch) {
-            put_steps<C>(steps[(n + 1) & 1], gn, bn, lane);
-            fetch(n + 2, lane);
-        }
         // ---- what the state is read for: K S (paired rows) and Q S
         f32x4 acc[IT], o[IT];
-        u32x4 xp[JB][WP];
+        u32x4 xp[WP], ab[IT][WP];
         if (active) {
 #pragma unroll
             for (int i = 0; i < IT; ++i) acc[i] = o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            u32x4 ka[2][IT][PARTS], qa[2][IT][PARTS];   // operands one step ahead
+            auto read = [&](int kb) {
+#pragma unroll
+                for (int i = 0; i < IT; ++i)
+#pragma unroll
+                    for (int x = 0; x < PARTS; ++x) {
+                        ka[kb & 1][i][x] = pair_op<KD>(K + x * C * KD, 0, i, kb, bpair);
+                        if constexpr (FULL) qa[kb & 1][i][x] = row_op<KD>(Q + x * C * KD, 16 * i, kb, base);
+                    }
+            };
+            read(0);
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
+                if (kb + 1 < KB) read(kb + 1);
                 u32x4 sp[WP];
                 pair_parts<WP>(S[2 * kb], S[2 * kb + 1], sp);
-#pragma unroll
-                for (int i = 0; i < IT; ++i) {
-                    u32x4 a[PARTS];
-#pragma unroll
-                    for (int x = 0; x < PARTS; ++x) a[x] = pair_op<KD>(K + x * C * KD, 32 * (i >> 1), i & 1, kb, bpair);
-                    acc[i] = mma_parts<PARTS, WP>(a, sp, acc[i]);
-                }
-                if constexpr (FULL) {
-#pragma unroll
-                    for (int i = 0; i < IT; ++i) {
-                        u32x4 a[PARTS];
-#pragma unroll
-                        for (int x = 0; x < PARTS; ++x) a[x] = row_op<KD>(Q + x * C * KD, 16 * i, kb, base);
-                        o[i] = mma_parts<PARTS, WP>(a, sp, o[i]);
-                    }
-                }
+                mma_tiles<IT, PARTS, WP>(ka[kb & 1], sp, acc);
+                if constexpr (FULL) mma_tiles<IT, PARTS, WP>(qa[kb & 1], sp, o);
+                __builtin_amdgcn_sched_barrier(0);
             }
+#pragma unroll
+            for (int i = 0; i < IT; ++i)
+#pragma unroll
+                for (int k = 0; k < WP; ++k) ab[i][k] = row_op<32>(A + k * PB + 512 * i, 0, 0, b32);
             // beta X = beta V - beta e^G K S
-            const uint32_t bv = col_base<kCols, 0>(16 * wave, lane);
+            f32x4 x[2];
+            u32x4 v[PARTS];
+            if (!trans) {
+                const uint32_t bv = col_base<kCols, 0>(16 * wave, lane);
 #pragma unroll
-            for (int jb = 0; jb < JB; ++jb) {
-                f32x4 x[2];
-                u32x4 v[PARTS];
-                if (!trans) {
-#pragma unroll
-                    for (int i = 0; i < PARTS; ++i) v[i] = col_op<kCols>(V + i * C * kCols, 32 * jb, 0, 0, bv);
-                }
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int t0 = 32 * jb + 8 * g4 + 4 * half;
-                    const f32x4 f = *reinterpret_cast<const f32x4*>(&st.bin[t0]), b = *reinterpret_cast<const f32x4*>(&st.beta[t0]);
-#pragma unroll
-                    for (int r = 0; r < 4; r += 2) {
-                        float y = 0.0f, z = 0.0f;
-                        if (!trans) unpack<PARTS>(v, 2 * half + r / 2, y, z);
-                        x[half][r] = fmaf(-f[r], acc[2 * jb + half][r], b[r] * y);
-                        x[half][r + 1] = fmaf(-f[r + 1], acc[2 * jb + half][r + 1], b[r + 1] * z);
-                    }
-                }
-                pair_parts<WP>(x[0], x[1], xp[jb]);
+                for (int i = 0; i < PARTS; ++i) v[i] = col_op<kCols>(V + i * C * kCols, 0, 0, 0, bv);
             }
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int t0 = 8 * g4 + 4 * half;
+                const f32x4 f = *reinterpret_cast<const f32x4*>(&st.bin[t0]), b = *reinterpret_cast<const f32x4*>(&st.beta[t0]);
+#pragma unroll
+                for (int r = 0; r < 4; r += 2) {
+                    float y = 0.0f, z = 0.0f;
+                    if (!trans) unpack<PARTS>(v, 2 * half + r / 2, y, z);
+                    x[half][r] = fmaf(-f[r], acc[half][r], b[r] * y);
+                    x[half][r + 1] = fmaf(-f[r + 1], acc[half][r + 1], b[r + 1] * z);
+                }
+            }
+            pair_parts<WP>(x[0], x[1], xp);
             if constexpr (FULL) {
 #pragma unroll
                 for (int i = 0; i < IT; ++i) {
@@ -360,72 +367,67 @@ __global__ void __launch_bounds__(kThreads, KD == 256 ? 1 : 2) delta_pass_kernel
                 }
             }
         }
-        lds_barrier();      // P is there; q and v have been read
-        if (ahead && n + 1 < nch) {
-            if (!trans) rv.load(V, wave, c0 + C, hi);
-            if constexpr (FULL) rq.load(Q, wave, c0 + C, hi);
+        if constexpr (FULL) {
+            lds_barrier();      // P is there; q and v have been read
+            if (ahead && n + 1 < nch) load_qv(n + 1);
         }
-        const uint32_t b32 = row_base<32>(lane);
         if (active) {
             // ---- U = A beta X
 #pragma unroll
             for (int i = 0; i < IT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int i = 0; i < IT; ++i)
-#pragma unroll
-                for (int jb = 0; jb <= i / 2; ++jb) {
-                    u32x4 a[WP];
-#pragma unroll
-                    for (int k = 0; k < WP; ++k) a[k] = row_op<32>(A + k * PB + p_block(i, jb) * 512, 0, 0, b32);
-                    acc[i] = mma_parts<WP, WP>(a, xp[jb], acc[i]);
-                }
+            mma_tiles<IT, WP, WP>(ab, xp, acc);
+            if constexpr (KEEP) {
+                const int64_t pitch = int64_t(p.H) * p.dv * 4;
+                store_tiles<C, true>(acc, reinterpret_cast<char*>(p.rows) + c0 * pitch + int64_t(h) * p.dv * 4, pitch, hi - c0,
+                                     c_wave, p.dv, true, false, lane);
+            }
             // ---- the outgoing state
             const uint32_t bk = col_base<KD, 1>(0, lane);
-            const float tail = st.tail;
+            constexpr int G = KB < 4 ? 2 * KB : 8;       // tiles of the state at a time
+            u32x4 ka[G][PARTS];
+            auto read = [&](int m0) {
 #pragma unroll
-            for (int m = 0; m < 2 * KB; ++m)
+                for (int m = 0; m < G; ++m)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) S[m][r] *= tail;
+                    for (int i = 0; i < PARTS; ++i) ka[m][i] = col_op<KD>(K + i * C * KD, 0, (m0 + m) >> 1, m & 1, bk);
+            };
+            read(0);
+            f32x4 x[2];
 #pragma unroll
-            for (int jb = 0; jb < JB; ++jb) {
-                f32x4 x[2];
+            for (int half = 0; half < 2; ++half) {
+                const f32x4 f = *reinterpret_cast<const f32x4*>(&st.out[8 * g4 + 4 * half]);
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const f32x4 f = *reinterpret_cast<const f32x4*>(&st.out[32 * jb + 8 * g4 + 4 * half]);
+                for (int r = 0; r < 4; ++r) x[half][r] = acc[half][r] * f[r];
+            }
+            u32x4 up[WP];
+            pair_parts<WP>(x[0], x[1], up);
+            const float tail = st.tail[0];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) x[half][r] = acc[2 * jb + half][r] * f[r];
-                }
-                u32x4 up[WP];
-                pair_parts<WP>(x[0], x[1], up);
+            for (int m0 = 0; m0 < 2 * KB; m0 += G) {
+                if (m0 > 0) read(m0);
 #pragma unroll
-                for (int m = 0; m < 2 * KB; ++m) {
-                    u32x4 k[PARTS];
+                for (int m = m0; m < m0 + G; ++m)
 #pragma unroll
-                    for (int i = 0; i < PARTS; ++i) k[i] = col_op<KD>(K + i * C * KD, 32 * jb, m >> 1, m & 1, bk);
-                    S[m] = mma_parts<PARTS, WP>(k, up, S[m]);
-                }
+                    for (int r = 0; r < 4; ++r) S[m][r] *= tail;
+                mma_tiles<G, PARTS, WP>(ka, up, &S[m0]);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
-        lds_barrier();      // k and A have been read
-        if (n + 1 < nch) {
-            if (ahead) rk.load(K, wave, c0 + C, hi);
-            load_a(n + 1, lane);
-        }
         if constexpr (FULL) {
+            lds_barrier();      // k and A have been read
+            if (n + 1 < nch) {
+                if (ahead) load_k(n + 1);
+                load_a(n + 1, lane);
+            }
             if (active) {
                 // ---- the chunk's own share, P U
 #pragma unroll
-                for (int jb = 0; jb < JB; ++jb) {
-                    u32x4 up[WP];
-                    pair_parts<WP>(acc[2 * jb], acc[2 * jb + 1], up);
+                for (int i = 0; i < IT; ++i)
 #pragma unroll
-                    for (int i = 2 * jb; i < IT; ++i) {
-                        u32x4 a[WP];
-#pragma unroll
-                        for (int k = 0; k < WP; ++k) a[k] = row_op<32>(Ps + k * PB + p_block(i, jb) * 512, 0, 0, b32);
-                        o[i] = mma_parts<WP, WP>(a, up, o[i]);
-                    }
-                }
+                    for (int k = 0; k < WP; ++k) ab[i][k] = row_op<32>(Ps + k * PB + 512 * i, 0, 0, b32);
+                u32x4 up[WP];
+                pair_parts<WP>(acc[0], acc[1], up);
+                mma_tiles<IT, WP, WP>(ab, up, o);
                 constexpr int OE = PARTS == 1 ? 2 : 4;
                 const int64_t pitch = p.so * OE;
                 store_tiles<C, false>(o, static_cast<char*>(p.out) + c0 * pitch + int64_t(h) * p.dv * OE, pitch, hi - c0, c_wave,
@@ -436,42 +438,41 @@ __global__ void __launch_bounds__(kThreads, KD == 256 ? 1 : 2) delta_pass_kernel
 
     // ---------------------------------------------- the state that leaves
     if (!active) return;
-    float *dst = nullptr, *dst_t = nullptr;
-    int64_t rs = p.dv;
     if constexpr (MODE == kDeltaStates) {
         if (trans) {
-            rs = p.dk;
-            dst = p.trans + (w.pi * p.H + h) * int64_t(p.dk) * p.dk;
-            if (p.trans_t) dst_t = p.trans_t + (w.pi * p.H + h) * int64_t(p.dk) * p.dk;
+            const int64_t to = (w.pi * p.H + h) * int64_t(p.dk) * p.dk;
+            store_state<KB>(S, p.trans + to, p.dk, p.dk, c_wave, p.dk % 4 == 0, lane);
+            if (p.trans_t) {
+#pragma unroll
+                for (int m = 0; m < 2 * KB; ++m)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int row = 32 * (m >> 1) + 8 * g4 + 4 * (m & 1) + r;
+                        if (row < p.dk && col < p.dk) p.trans_t[to + int64_t(col) * p.dk + row] = S[m][r];
+                    }
+            }
         } else {
-            dst = p.carry + (w.pi * p.H + h) * ssz;
+            store_state<KB>(S, p.carry + (w.pi * p.H + h) * ssz, p.dk, p.dv, c_wave, p.dv % 4 == 0, lane);
         }
     } else if (FULL && w.last && p.s_out) {
-        dst = p.s_out + (int64_t(w.slot) * p.H + h) * ssz;
+        store_state<KB>(S, p.s_out + (int64_t(w.slot) * p.H + h) * ssz, p.dk, p.dv, c_wave, false, lane);
     }
-    if (!dst) return;
-#pragma unroll
-    for (int m = 0; m < 2 * KB; ++m)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = 32 * (m >> 1) + 8 * g4 + 4 * (m & 1) + r;
-            if (row < p.dk && col < width) {
-                dst[int64_t(row) * rs + col] = S[m][r];
-                if (dst_t) dst_t[int64_t(col) * p.dk + row] = S[m][r];
-            }
-        }
 }
 
 // ---------------------------------------------------------------- pieces' starting states
-// Walks the pieces of one sequence and head for 64 columns of the state: each piece's own end
-// state N is replaced by the state S it starts from, and the next one starts from W S + N with
-// the piece's transition W (against time its transpose).
+// Walks the pieces of one sequence and head for 128 columns of the state, 16 a wave: each piece's
+// own end state N is replaced by the state S it starts from, and the next one starts from W S + N
+// with the piece's transition W (against time its transpose).  W does not depend on what came
+// before, so its rows are asked for four tiles of 16 ahead, and all waves share their split.
+constexpr int kCarryThreads = 512, kCarryCols = 128;
+
 template <int KD, bool REV>
-__global__ void __launch_bounds__(kThreads) delta_carry_kernel(DeltaPass p) {
-    constexpr int KB = KD / 32, WP = 3;
-    const int lane = threadIdx.x & 63, g4 = lane >> 4, l16 = lane & 15;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int slice = blockIdx.x, h = blockIdx.y, seq = blockIdx.z;
+__global__ void __launch_bounds__(kCarryThreads) delta_carry_kernel(DeltaPass p) {
+    constexpr int KB = KD / 32, WP = 3, VPT = KD / 32, AHEAD = 4;   // values of a tile a thread brings
+    __shared__ __align__(16) uint16_t Ws[2][WP * 16 * KD];
+    const int tid = threadIdx.x, lane = tid & 63, g4 = lane >> 4, l16 = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int h = blockIdx.y, seq = blockIdx.z;
     const int slot = REV ? seq : find_slot(p.slots, p.nslots, seq);
     if (slot < 0) return;
     const Seq sq = seq_range(p, seq);
@@ -479,60 +480,62 @@ __global__ void __launch_bounds__(kThreads) delta_carry_kernel(DeltaPass p) {
     int64_t n = (sq.end - sq.start + p.piece - 1) / p.piece;
     if (n < 2) return;   // a single piece starts from the user's state
     if (base + n > p.npieces) n = p.npieces - base;
-    const int c_wave = slice * kCols + 16 * wave, col = c_wave + l16;
-    if (c_wave >= p.dv) return;
+    const int c_wave = blockIdx.x * kCarryCols + 16 * wave;
     const int64_t ssz = int64_t(p.dk) * p.dv, tsz = int64_t(p.dk) * p.dk;
+    const auto number = [&](int64_t k) { return (base + (REV ? n - 1 - k : k)) * p.H + h; };
     f32x4 S[2 * KB];
-    const auto row = [&](int m, int r) { return 32 * (m >> 1) + 8 * g4 + 4 * (m & 1) + r; };
-    const float* src = p.s_in ? p.s_in + (int64_t(slot) * p.H + h) * ssz : nullptr;
+    load_state<KB>(S, p.s_in ? p.s_in + (int64_t(slot) * p.H + h) * ssz : nullptr, p.dk, p.dv, c_wave, lane);
+    // tile m of the rows of piece k's transition: row ti in the order of the state's tiles
+    const int ti = tid >> 5, tc = (tid & 31) * VPT, to = at_piece<KD>(ti, tc >> 3) + (tc & 7);
+    float ahead[AHEAD][VPT];
+    const auto ask = [&](int64_t k, int m, float (&x)[VPT]) {
+        const int out = 32 * (m >> 1) + 8 * (ti >> 2) + 4 * (m & 1) + (ti & 3);
+        const float* const q = (REV ? p.trans_t : p.trans) + number(k) * tsz + int64_t(out) * p.dk + tc;
+        if (k + 1 >= n) return;
+        if (p.dk % VPT == 0 && VPT > 1) {
 #pragma unroll
-    for (int m = 0; m < 2 * KB; ++m)
+            for (int e = 0; e < VPT; ++e) x[e] = 0.0f;
+            if (out < p.dk && tc < p.dk) __builtin_memcpy(x, q, sizeof(x));
+        } else {
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-            S[m][r] = src && row(m, r) < p.dk && col < p.dv ? src[int64_t(row(m, r)) * p.dv + col] : 0.0f;
-    const bool vec = p.dk % 4 == 0;
+            for (int e = 0; e < VPT; ++e) x[e] = out < p.dk && tc + e < p.dk ? q[e] : 0.0f;
+        }
+    };
+#pragma unroll
+    for (int m = 0; m < AHEAD; ++m) ask(0, m, ahead[m]);
+    const uint32_t b = row_base<KD>(lane);
     for (int64_t k = 0; k < n; ++k) {
-        const int64_t at = (base + (REV ? n - 1 - k : k)) * p.H + h;
-        float* const own = p.carry + at * ssz;
-        const float* const tr = (REV ? p.trans_t : p.trans) + at * tsz;
+        float* const own = p.carry + number(k) * ssz;
         f32x4 N[2 * KB];
-#pragma unroll
-        for (int m = 0; m < 2 * KB; ++m)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const bool in = row(m, r) < p.dk && col < p.dv;
-                N[m][r] = in && k + 1 < n ? own[int64_t(row(m, r)) * p.dv + col] : 0.0f;
-                if (in) own[int64_t(row(m, r)) * p.dv + col] = S[m][r];
-            }
-        if (k + 1 == n) break;
+        load_state<KB>(N, k + 1 < n ? own : nullptr, p.dk, p.dv, c_wave, lane);
+        store_state<KB>(S, own, p.dk, p.dv, c_wave, p.dv % 4 == 0, lane);
+        if (k + 1 == n) return;
         u32x4 sp[KB][WP];
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) pair_parts<WP>(S[2 * kb], S[2 * kb + 1], sp[kb]);
 #pragma unroll
         for (int m = 0; m < 2 * KB; ++m) {
-            const int out = 32 * (m >> 1) + 8 * (l16 >> 2) + 4 * (m & 1) + (l16 & 3);   // this lane's row of W
-            const float* const wr = tr + int64_t(out) * p.dk;
+            uint16_t* const W = Ws[m & 1];
+            float (&x)[VPT] = ahead[m % AHEAD];
+#pragma unroll
+            for (int e = 0; e < VPT; e += 2) {
+                uint32_t w[WP];
+                split<WP>(x[e], x[e + 1], w);
+#pragma unroll
+                for (int c = 0; c < WP; ++c) *reinterpret_cast<uint32_t*>(W + c * 16 * KD + to + e) = w[c];
+            }
+            ask(k + (m + AHEAD) / (2 * KB), (m + AHEAD) % (2 * KB), x);
+            lds_barrier();      // the tile is there, and the one before has been read
+            f32x4 c[2] = {N[m], {0.0f, 0.0f, 0.0f, 0.0f}};
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
-                const int c = 32 * kb + 8 * g4;
-                f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f}, y = x;
-                if (vec) {
-                    if (out < p.dk && c < p.dk) x = *reinterpret_cast<const f32x4*>(wr + c);
-                    if (out < p.dk && c + 4 < p.dk) y = *reinterpret_cast<const f32x4*>(wr + c + 4);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (out < p.dk && c + e < p.dk) x[e] = wr[c + e];
-                        if (out < p.dk && c + 4 + e < p.dk) y[e] = wr[c + 4 + e];
-                    }
-                }
                 u32x4 a[WP];
-                pair_parts<WP>(x, y, a);
-                N[m] = mma_parts<WP, WP>(a, sp[kb], N[m]);
-            }
-        }
 #pragma unroll
-        for (int m = 0; m < 2 * KB; ++m) S[m] = N[m];
+                for (int i = 0; i < WP; ++i) a[i] = row_op<KD>(W + i * 16 * KD, 0, kb, b);
+                c[kb & 1] = mma_parts<WP, WP>(a, sp[kb], c[kb & 1]);
+            }
+            S[m] = c[0] + c[1];
+        }
     }
 }
 
@@ -659,37 +662,24 @@ __global__ void __launch_bounds__(kThreads) delta_step_kernel(StepArgs p) {
 
 // ---------------------------------------------------------------- host: plans
 struct Plan {
-    int chunk;
     int64_t nchunks, piece, npieces;
     bool pieced;
-    size_t tri, carry, trans;   // bytes
-    size_t bytes() const { return tri + carry + trans; }
+    size_t tri, steps, carry, trans;   // bytes
+    size_t bytes() const { return tri + steps + carry + trans; }
 };
 
-// Pieces along the tokens cost a walk from zero and one from the unit matrix before the walk for
-// the outputs: they pay where the card would stand mostly idle.
-inline int64_t choose_piece(const ssm_linattn_dims* d, int64_t each) {
-    const int64_t units = d->nheads * cdiv(d->dv, kCols) * (d->tokens / each);
-    const int64_t want = 512 / units;
-    if (want < 5 || each < 1024) return 0;
-    int64_t piece = cdiv(cdiv(each, want), 64) * 64;
-    if (piece < 512) piece = 512;
-    return piece < each ? piece : 0;
-}
-
 inline int make_plan(const ssm_linattn_dims* d, bool packed, Plan* pl) {
-    pl->chunk = d->io_dtype == SSM_BF16 ? 64 : 32;
     const int64_t vs = cdiv(d->dv, kCols), ks = cdiv(d->dk, kCols);
     const int64_t each = packed ? d->tokens : d->tokens / d->nseq;
     int64_t piece = d->piece_len;
-    if (piece == 0) piece = choose_piece(d, each);
+    if (piece == 0) piece = choose_piece(d, packed, 110);
     pl->pieced = piece > 0 && piece < each;
     pl->piece = pl->pieced ? piece : (int64_t(1) << 31);
     pl->npieces = !pl->pieced ? d->nseq : packed ? d->tokens / piece + d->nseq : d->nseq * cdiv(each, piece);
-    pl->nchunks = count_chunks(d, packed, pl->chunk);
+    pl->nchunks = count_chunks(d, packed, kChunk);
     if (pl->npieces > kMostGroups / (d->nheads * (vs + ks)) || pl->nchunks > 2 * kMostGroups) return SSM_ERR_DIMS;
-    const int64_t tri = pl->chunk == 64 ? tri_elems<64>() : tri_elems<32>();
-    pl->tri = up256(static_cast<size_t>(pl->nchunks * d->nheads * tri) * 2);
+    pl->tri = up256(static_cast<size_t>(pl->nchunks * d->nheads * tri_elems<kChunk>()) * 2);
+    pl->steps = static_cast<size_t>(pl->nchunks * d->nheads) * sizeof(Steps<kChunk>);
     pl->carry = pl->pieced ? up256(static_cast<size_t>(pl->npieces * d->nheads * d->dk * d->dv) * 4) : 0;
     pl->trans = pl->pieced ? up256(static_cast<size_t>(pl->npieces * d->nheads * d->dk * d->dk) * 4) : 0;
     return SSM_OK;
@@ -712,17 +702,13 @@ template <int C> void run_tri(const DeltaPass& p, bool f32, int64_t nchunks, hip
 #undef SSM_TRI
 }
 
-template <int C, int MODE> void run_pass(const DeltaPass& p, bool f32, hipStream_t s) {
+template <int MODE> void run_pass(const DeltaPass& p, bool f32, hipStream_t s) {
     const int64_t slices = MODE == kDeltaStates ? p.vslices + p.kslices : p.vslices;
     const dim3 grid(static_cast<uint32_t>(int64_t(p.npieces) * p.H * slices)), block(kThreads);
-#define SSM_PASS(K)                                                                                               \
-    do {                                                                                                          \
-        if constexpr (C == 32) {                                                                                  \
-            if (f32) launch_kernel(delta_pass_kernel<3, K, C, MODE>, grid, block, 0, s, p);                       \
-            else if constexpr (MODE != kDeltaFull) launch_kernel(delta_pass_kernel<1, K, C, MODE>, grid, block, 0, s, p); \
-        } else if constexpr (K <= 128 || MODE != kDeltaKeep) {                                                                                                  \
-            launch_kernel(delta_pass_kernel<1, K, C, MODE>, grid, block, 0, s, p);                                \
-        }                                                                                                         \
+#define SSM_PASS(K)                                                                                 \
+    do {                                                                                            \
+        if (f32) launch_kernel(delta_pass_kernel<3, K, MODE>, grid, block, 0, s, p);                \
+        else launch_kernel(delta_pass_kernel<1, K, MODE>, grid, block, 0, s, p);                    \
     } while (0)
     if (p.dk <= 64) SSM_PASS(64);
     else if (p.dk <= 128) SSM_PASS(128);
@@ -733,25 +719,19 @@ template <int C, int MODE> void run_pass(const DeltaPass& p, bool f32, hipStream
 }  // namespace dl
 }  // namespace
 
-void ssm_detail::launch_delta_tri(const DeltaPass& p, bool f32, int chunk, int64_t nchunks, hipStream_t s) {
-    if (chunk == 64) dl::run_tri<64>(p, f32, nchunks, s);
+void ssm_detail::launch_delta_tri(const DeltaPass& p, bool f32, int64_t nchunks, hipStream_t s) {
+    if (p.block == 64) dl::run_tri<64>(p, f32, nchunks, s);
     else dl::run_tri<32>(p, f32, nchunks, s);
 }
 
-void ssm_detail::launch_delta_pass(const DeltaPass& p, bool f32, int chunk, DeltaMode mode, hipStream_t s) {
-    if (chunk == 64) {
-        if (mode == kDeltaStates) dl::run_pass<64, kDeltaStates>(p, f32, s);
-        else if (mode == kDeltaFull) dl::run_pass<64, kDeltaFull>(p, f32, s);
-        else dl::run_pass<64, kDeltaKeep>(p, f32, s);
-    } else {
-        if (mode == kDeltaStates) dl::run_pass<32, kDeltaStates>(p, f32, s);
-        else if (mode == kDeltaFull) dl::run_pass<32, kDeltaFull>(p, f32, s);
-        else dl::run_pass<32, kDeltaKeep>(p, f32, s);
-    }
+void ssm_detail::launch_delta_pass(const DeltaPass& p, bool f32, DeltaMode mode, hipStream_t s) {
+    if (mode == kDeltaStates) dl::run_pass<kDeltaStates>(p, f32, s);
+    else if (mode == kDeltaFull) dl::run_pass<kDeltaFull>(p, f32, s);
+    else dl::run_pass<kDeltaKeep>(p, f32, s);
 }
 
 void ssm_detail::launch_delta_carry(const DeltaPass& p, bool reverse, hipStream_t s) {
-    const dim3 grid(p.vslices, p.H, p.nseq), block(dl::kThreads);
+    const dim3 grid(static_cast<uint32_t>(cdiv(p.dv, dl::kCarryCols)), p.H, p.nseq), block(dl::kCarryThreads);
 #define SSM_CARRY(K)                                                                        \
     do {                                                                                    \
         if (reverse) launch_kernel(dl::delta_carry_kernel<K, true>, grid, block, 0, s, p);  \
@@ -816,7 +796,7 @@ int ssm_delta_fwd(const void* q, const void* k, const void* v, const float* g, c
     p.s_in = s0; p.s_out = s_last;
     p.sq = z.q; p.sk = z.k; p.sv = z.v; p.so = z.o; p.sg = d.head_decay ? 0 : d.nheads;
     p.T = d.tokens; p.L = cu_seqlens ? 0 : d.tokens / d.nseq;
-    p.piece = pl.piece;
+    p.piece = pl.piece; p.block = kChunk;
     p.rep = static_cast<int32_t>(d.nheads / d.kheads); p.H = static_cast<int32_t>(d.nheads);
     p.dk = static_cast<int32_t>(d.dk); p.dv = static_cast<int32_t>(d.dv);
     p.vslices = static_cast<int32_t>(cdiv(d.dv, kCols)); p.kslices = static_cast<int32_t>(cdiv(d.dk, kCols));
@@ -827,17 +807,18 @@ int ssm_delta_fwd(const void* q, const void* k, const void* v, const float* g, c
     p.scale = d.scale;
     char* ws = static_cast<char*>(d.workspace);
     p.tri = reinterpret_cast<uint16_t*>(ws);
-    p.carry = reinterpret_cast<float*>(ws + pl.tri);
-    p.trans = reinterpret_cast<float*>(ws + pl.tri + pl.carry);
+    p.steps = reinterpret_cast<float*>(ws + pl.tri);
+    p.carry = reinterpret_cast<float*>(ws + pl.tri + pl.steps);
+    p.trans = reinterpret_cast<float*>(ws + pl.tri + pl.steps + pl.carry);
     const bool f32 = d.io_dtype == SSM_F32;
     hipStream_t s = static_cast<hipStream_t>(stream);
     launch_error = hipSuccess;
-    launch_delta_tri(p, f32, pl.chunk, pl.nchunks, s);
+    launch_delta_tri(p, f32, pl.nchunks, s);
     if (pl.pieced) {
-        launch_delta_pass(p, f32, pl.chunk, kDeltaStates, s);
+        launch_delta_pass(p, f32, kDeltaStates, s);
         launch_delta_carry(p, false, s);
     }
-    launch_delta_pass(p, f32, pl.chunk, kDeltaFull, s);
+    launch_delta_pass(p, f32, kDeltaFull, s);
     return launch_error == hipSuccess ? SSM_OK : SSM_ERR_HIP;
 }
 
