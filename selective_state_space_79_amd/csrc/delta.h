@@ -285,15 +285,15 @@ template <typename P> __device__ inline Where find_piece(const P& p, int nslices
     const int per = p.H * nslices;
     int at = int(blockIdx.x % per);
     if (per % 8 == 0) at = (at % 8) * (per / 8) + at / 8;   // neighbouring heads to one XCD
-    w.pi = blockIdx.x / per;
+    w.pi = uniform(int(blockIdx.x / per));
     w.slice = uniform(at % nslices);
     w.h = uniform(at / nslices);
-    const int seq = w.seq = find_seq(p, w.pi);
+    const int seq = w.seq = uniform(find_seq(p, w.pi));
     if (seq < 0) return w;
     w.sq = seq_range(p, seq);
-    const int64_t local = w.pi - piece_base(p, seq), len = w.sq.end - w.sq.start;
+    const int64_t local = uniform(w.pi - piece_base(p, seq)), len = w.sq.end - w.sq.start;
     if (local < 0 || (local > 0 && local * p.piece >= len)) return w;
-    w.slot = need_slot ? find_slot(p.slots, p.nslots, seq) : seq;
+    w.slot = need_slot ? uniform(find_slot(p.slots, p.nslots, seq)) : seq;
     if (w.slot < 0) return w;
     w.lo = w.sq.start + local * p.piece;
     w.hi = w.sq.end - w.lo > p.piece ? w.lo + p.piece : w.sq.end;
@@ -382,7 +382,7 @@ struct Blocked {
     template <typename P> __device__ inline Blocked(const P& p, const Where& w, int64_t lo) {
         const Chunks ch(p, p.block);
         two = p.block > kChunk;
-        first = uniform(piece_base(ch, w.seq)) + (lo - w.sq.start) / p.block;
+        first = uniform(piece_base(ch, w.seq) + ((lo - w.sq.start) >> (two ? 6 : 5)));
     }
     __device__ inline int64_t block(int64_t n) const { return first + (n >> two); }
     __device__ inline bool starts(int64_t n) const { return !two || (n & 1) == 0; }

@@ -163,13 +163,13 @@ __global__ void __launch_bounds__(kThreads) delta_tri_kernel(DeltaPass p) {
 // chunks of 32 tokens: 64 would halve the splits of the state into parts, but take the LDS of
 // four workgroups on a CU and twice the time from chunk to chunk.
 //
-// With outputs one set of tiles, and the next chunk's rows are asked for as soon as this one's
-// are read; without, two sets and one barrier a chunk.
+// Two sets of tiles, so that the next chunk's rows and A are asked for a chunk ahead; queries have
+// one, refilled as soon as they are read.  (float32 rows pass through registers.)
 template <int PARTS, int KD, int MODE>
 __global__ void __launch_bounds__(kThreads, pass_waves(KD, PARTS, MODE)) delta_pass_kernel(DeltaPass p) {
     constexpr bool FULL = MODE == kDeltaFull, KEEP = MODE == kDeltaKeep, DMA = PARTS == 1;
     constexpr int C = kChunk, IT = C / 16, KB = KD / 32, NTILE = 3, PB = 2 * 512, WP = 3;   // parts of what is no bf16 input
-    constexpr int SETS = FULL || !DMA ? 1 : 2, ASETS = FULL ? 1 : 2, KE = PARTS * C * KD, VE = PARTS * C * kCols;
+    constexpr int SETS = DMA ? 2 : 1, ASETS = FULL && !DMA ? 1 : 2, KE = PARTS * C * KD, VE = PARTS * C * kCols;
     __shared__ __align__(16) uint16_t Ks[SETS * KE], Vs[SETS * VE], As[ASETS * WP * PB];
     __shared__ __align__(16) uint16_t Q[FULL ? KE : 8], Ps[FULL ? WP * PB : 8];
     __shared__ Steps<C> steps[2];
@@ -213,15 +213,18 @@ __global__ void __launch_bounds__(kThreads, pass_waves(KD, PARTS, MODE)) delta_p
     rv.prepare(p.v, int64_t(h) * p.dv + c_slice, p.sv, p.dv - c_slice, tid);
     const bool ahead = DMA && p.wide;
     auto load_k = [&](int64_t n) { rk.load(Ks + (SETS == 2 && n & 1 ? KE : 0), wave, lo + n * C, hi); };
-    auto load_qv = [&](int64_t n) {
+    auto load_v = [&](int64_t n) {
         if (!trans) rv.load(Vs + (SETS == 2 && n & 1 ? VE : 0), wave, lo + n * C, hi);
+    };
+    auto load_q = [&](int64_t n) {
         if constexpr (FULL) rq.load(Q, wave, lo + n * C, hi);
     };
     auto load_a = [&](int64_t n, int lane) { at.load(As + (ASETS == 2 && n & 1 ? WP * PB : 0), &steps[n & 1], p, n, h, wave, lane); };
     if (nch > 0) {
         if (p.wide) {
             load_k(0);
-            load_qv(0);
+            load_v(0);
+            load_q(0);
         }
         load_a(0, lane);
     }
@@ -255,7 +258,8 @@ __global__ void __launch_bounds__(kThreads, pass_waves(KD, PARTS, MODE)) delta_p
                 if constexpr (FULL) rq.store(Q, tid);
                 if (n + 1 < nch) {
                     load_k(n + 1);
-                    load_qv(n + 1);
+                    load_v(n + 1);
+                    load_q(n + 1);
                 }
             } else {
                 rk.copy(K, tid, c0, hi);
@@ -265,9 +269,9 @@ __global__ void __launch_bounds__(kThreads, pass_waves(KD, PARTS, MODE)) delta_p
             lds_barrier();
         }
         if (ASETS == 2 && n + 1 < nch) {
-            if (SETS == 2 && ahead) {
+            if (ahead) {
                 load_k(n + 1);
-                load_qv(n + 1);
+                load_v(n + 1);
             }
             load_a(n + 1, lane);
         }
@@ -276,52 +280,28 @@ __global__ void __launch_bounds__(kThreads, pass_waves(KD, PARTS, MODE)) delta_p
                 store_state<KB>(S, p.keep + (at.block(n) * p.H + h) * ssz, p.dk, p.dv, c_wave, p.dv % 4 == 0, lane);
         }
         const uint32_t base = row_base<KD>(lane), bpair = pair_base<KD>(lane), b32 = row_base<32>(lane);
-        if constexpr (FULL) {
-            // ---- P, tiles on and below the diagonal
-            if (wave < NTILE) {
-                const int it = wave < 1 ? 0 : 1, jt = wave - it;
-                f32x4 a = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb) {
-                    u32x4 x[PARTS], y[PARTS];
-#pragma unroll
-                    for (int i = 0; i < PARTS; ++i) {
-                        x[i] = row_op<KD>(K + i * C * KD, 16 * jt, kb, base);
-                        y[i] = row_op<KD>(Q + i * C * KD, 16 * it, kb, base);
-                    }
-                    a = mma_parts<PARTS, PARTS>(x, y, a);
-                }
-                const int i = 16 * it + l16, j0 = 16 * jt + 4 * g4;
-                const int o = 512 * it + at_piece<32>(l16, 2 * jt + (g4 >> 1)) + 4 * (g4 & 1);
-                const float gi = st.hi[i], ei = st.lo[i];
-                const f32x4 gj = *reinterpret_cast<const f32x4*>(&st.hi[j0]), ej = *reinterpret_cast<const f32x4*>(&st.lo[j0]);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float e = __builtin_amdgcn_exp2f((gi - gj[r]) + (ei - ej[r]));
-                    a[r] = j0 + r <= i ? a[r] * (e * p.scale) : 0.0f;
-                }
-                uint32_t x[WP], y[WP];
-                split<WP>(a[0], a[1], x);
-                split<WP>(a[2], a[3], y);
-#pragma unroll
-                for (int k = 0; k < WP; ++k) *reinterpret_cast<uint2*>(Ps + k * PB + o) = uint2{x[k], y[k]};
-            }
-        }
         // ---- what the state is read for: K S (paired rows) and Q S
-        f32x4 acc[IT], o[IT];
+        f32x4 acc[IT], o[IT], pt = {0.0f, 0.0f, 0.0f, 0.0f};
         u32x4 xp[WP], ab[IT][WP];
+        // a tile of P on or below the diagonal each but the last wave
+        const int pi = wave < 1 ? 0 : 1, pj = wave < 2 ? 0 : 1;
         if (active) {
 #pragma unroll
             for (int i = 0; i < IT; ++i) acc[i] = o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            u32x4 ka[2][IT][PARTS], qa[2][IT][PARTS];   // operands one step ahead
+            u32x4 ka[2][IT][PARTS], qa[2][IT][PARTS], px[2][PARTS], py[2][PARTS];   // operands one step ahead
             auto read = [&](int kb) {
 #pragma unroll
-                for (int i = 0; i < IT; ++i)
+                for (int x = 0; x < PARTS; ++x) {
 #pragma unroll
-                    for (int x = 0; x < PARTS; ++x) {
+                    for (int i = 0; i < IT; ++i) {
                         ka[kb & 1][i][x] = pair_op<KD>(K + x * C * KD, 0, i, kb, bpair);
                         if constexpr (FULL) qa[kb & 1][i][x] = row_op<KD>(Q + x * C * KD, 16 * i, kb, base);
                     }
+                    if constexpr (FULL) {
+                        px[kb & 1][x] = row_op<KD>(K + x * C * KD, 16 * pj, kb, base);
+                        py[kb & 1][x] = row_op<KD>(Q + x * C * KD, 16 * pi, kb, base);
+                    }
+                }
             };
             read(0);
 #pragma unroll
@@ -330,8 +310,11 @@ __global__ void __launch_bounds__(kThreads, pass_waves(KD, PARTS, MODE)) delta_p
                 u32x4 sp[WP];
                 pair_parts<WP>(S[2 * kb], S[2 * kb + 1], sp);
                 mma_tiles<IT, PARTS, WP>(ka[kb & 1], sp, acc);
-                if constexpr (FULL) mma_tiles<IT, PARTS, WP>(qa[kb & 1], sp, o);
-                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (FULL) {
+                    mma_tiles<IT, PARTS, WP>(qa[kb & 1], sp, o);
+                    pt = mma_parts<PARTS, PARTS>(px[kb & 1], py[kb & 1], pt);
+                }
+                if constexpr (!DMA) __builtin_amdgcn_sched_barrier(0);   // three parts of operands fill the registers
             }
 #pragma unroll
             for (int i = 0; i < IT; ++i)
@@ -368,8 +351,36 @@ __global__ void __launch_bounds__(kThreads, pass_waves(KD, PARTS, MODE)) delta_p
             }
         }
         if constexpr (FULL) {
-            lds_barrier();      // P is there; q and v have been read
-            if (ahead && n + 1 < nch) load_qv(n + 1);
+            if (!active) {      // the others have it from their walk over the state's rows
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) {
+                    u32x4 x[PARTS], y[PARTS];
+#pragma unroll
+                    for (int i = 0; i < PARTS; ++i) {
+                        x[i] = row_op<KD>(K + i * C * KD, 16 * pj, kb, base);
+                        y[i] = row_op<KD>(Q + i * C * KD, 16 * pi, kb, base);
+                    }
+                    pt = mma_parts<PARTS, PARTS>(x, y, pt);
+                }
+            }
+            if (wave < NTILE) {
+                const int i = 16 * pi + l16, j0 = 16 * pj + 4 * g4;
+                const int to = 512 * pi + at_piece<32>(l16, 2 * pj + (g4 >> 1)) + 4 * (g4 & 1);
+                const float gi = st.hi[i], ei = st.lo[i];
+                const f32x4 gj = *reinterpret_cast<const f32x4*>(&st.hi[j0]), ej = *reinterpret_cast<const f32x4*>(&st.lo[j0]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float e = __builtin_amdgcn_exp2f((gi - gj[r]) + (ei - ej[r]));
+                    pt[r] = j0 + r <= i ? pt[r] * (e * p.scale) : 0.0f;
+                }
+                uint32_t x[WP], y[WP];
+                split<WP>(pt[0], pt[1], x);
+                split<WP>(pt[2], pt[3], y);
+#pragma unroll
+                for (int k = 0; k < WP; ++k) *reinterpret_cast<uint2*>(Ps + k * PB + to) = uint2{x[k], y[k]};
+            }
+            lds_barrier();      // P is there; q has been read
+            if (ahead && n + 1 < nch) load_q(n + 1);
         }
         if (active) {
             // ---- U = A beta X
@@ -383,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, pass_waves(KD, PARTS, MODE)) delta_p
             }
             // ---- the outgoing state
             const uint32_t bk = col_base<KD, 1>(0, lane);
-            constexpr int G = KB < 4 ? 2 * KB : 8;       // tiles of the state at a time
+            constexpr int G = FULL || KB < 4 ? 4 : 8;       // tiles of the state at a time
             u32x4 ka[G][PARTS];
             auto read = [&](int m0) {
 #pragma unroll
@@ -414,10 +425,9 @@ __global__ void __launch_bounds__(kThreads, pass_waves(KD, PARTS, MODE)) delta_p
             }
         }
         if constexpr (FULL) {
-            lds_barrier();      // k and A have been read
-            if (n + 1 < nch) {
-                if (ahead) load_k(n + 1);
-                load_a(n + 1, lane);
+            if constexpr (ASETS == 1) {
+                lds_barrier();      // A has been read
+                if (n + 1 < nch) load_a(n + 1, lane);
             }
             if (active) {
                 // ---- the chunk's own share, P U

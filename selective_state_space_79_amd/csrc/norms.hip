@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(block_threads<TPG>()) layer_norm_fwd_kernel(La
 #pragma unroll
             for (int e = 0; e < 8; ++e) q += x[i].e[e];
         }
-        const float mean = sum(q) * p.inv_n;
+        const float mean = sum(q) / static_cast<float>(p.n);   // not times 1/n: equal values leave no deviation
         q = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -666,7 +666,7 @@ __global__ void __launch_bounds__(block_threads<TPG>(), 4) layer_norm_bwd_kernel
             for (int e = 0; e < 8; ++e) q += x.e[e];
         }
         if (V == 1 && l + 1 < loops) fetch(row + at.step);
-        const float mean = sum(q) * p.inv_n;
+        const float mean = sum(q) / static_cast<float>(p.n);
         float s[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < V; ++i) {
