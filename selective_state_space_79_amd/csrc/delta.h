@@ -65,7 +65,6 @@ struct DeltaPass {
 // at the chunk's end).
 enum DeltaMode { kDeltaStates = 0, kDeltaFull = 1, kDeltaKeep = 2 };
 void launch_delta_tri(const DeltaPass& p, bool f32, int64_t nchunks, hipStream_t s);
-void launch_delta_pass(const DeltaPass& p, bool f32, DeltaMode mode, hipStream_t s);
 void launch_delta_carry(const DeltaPass& p, bool reverse, hipStream_t s);
 
 }  // namespace ssm_detail
@@ -272,20 +271,20 @@ template <int PARTS, int C, int W, int T> struct Rows {
     }
 };
 
-// Where a workgroup's piece lies, or that it has none.
+// Where a workgroup's piece lies (its number: `unit`), or that it has none.
 struct Where {
     int64_t pi, lo, hi;
     Seq sq;
     int slice, h, seq, slot;
     bool first, last, on;
 };
-template <typename P> __device__ inline Where find_piece(const P& p, int nslices, bool need_slot) {
+template <typename P> __device__ inline Where find_piece(const P& p, uint32_t unit, int nslices, bool need_slot) {
     Where w;
     w.on = false;
     const int per = p.H * nslices;
-    int at = int(blockIdx.x % per);
+    int at = int(unit % per);
     if (per % 8 == 0) at = (at % 8) * (per / 8) + at / 8;   // neighbouring heads to one XCD
-    w.pi = uniform(int(blockIdx.x / per));
+    w.pi = uniform(int(unit / per));
     w.slice = uniform(at % nslices);
     w.h = uniform(at / nslices);
     const int seq = w.seq = uniform(find_seq(p, w.pi));
@@ -420,10 +419,6 @@ inline int64_t choose_piece(const ssm_linattn_dims* d, bool packed, int64_t wort
     int64_t piece = cdiv(cdiv(d->tokens, want < 1 ? 1 : want), 64) * 64;
     if (piece < 256) piece = 256;
     return piece < longest ? piece : 0;
-}
-
-constexpr int pass_waves(int KD, int PARTS, int MODE) {   // per SIMD
-    return KD == 256 ? (PARTS == 1 ? 2 : 1) : PARTS == 1 && MODE == ssm_detail::kDeltaFull ? 3 : 2;
 }
 
 }  // namespace dl

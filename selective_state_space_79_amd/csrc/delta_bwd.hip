@@ -17,7 +17,7 @@
 // and o_t . do_t = q_t . dq_t.  Two walks over the chunks, the forward's and one against time,
 // leave S_in and U, dS_out and Z of every chunk in memory; all gradients of a chunk are then
 // formed by a workgroup of its own.
-#include "delta.h"
+#include "delta_walk.h"
 
 namespace {
 namespace dl {
@@ -29,218 +29,20 @@ using namespace ssm_detail;
 // rounding; the gradient of v is formed with the step as it came.
 constexpr float kLeastStep = 5.42101086e-20f;   // 2^-64
 
-// ---------------------------------------------------------------- the walk against time
-// As delta_pass_kernel without outputs, with the gradient of the state in the registers; p.v is
-// the gradient of o.
+// ---------------------------------------------------------------- the walks, with time and against it
+// Neither waits for the other, and one alone leaves a SIMD without work between a chunk's
+// products: one launch has the workgroups of both.
 template <int PARTS, int KD, int MODE>
-__global__ void __launch_bounds__(kThreads, KD == 256 ? 1 : 2) delta_rev_kernel(DeltaPass p) {
-    constexpr bool KEEP = MODE == kDeltaKeep, DMA = PARTS == 1;
-    constexpr int C = kChunk, IT = C / 16, KB = KD / 32, PB = 2 * 512, WP = 3;
-    constexpr int SETS = DMA ? 2 : 1, KE = PARTS * C * KD, VE = PARTS * C * kCols;
-    __shared__ __align__(16) uint16_t Ks[SETS * KE], Qs[SETS * KE], Vs[SETS * VE], As[2 * WP * PB], PT[WP * PB];
-    __shared__ Steps<C> steps[2];
-    const int tid = threadIdx.x, lane = tid & 63, g4 = lane >> 4, l16 = lane & 15;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const Where w = find_piece(p, p.vslices, false);
-    if (!w.on || (MODE == kDeltaStates && w.first)) return;   // no piece starts from a first one's gradient
-    const int h = w.h, c_slice = w.slice * kCols, c_wave = c_slice + 16 * wave;
-    const bool active = c_wave < p.dv;
-    const int64_t lo = w.lo, hi = w.hi, ssz = int64_t(p.dk) * p.dv;
-
-    f32x4 S[2 * KB];
-    const float* src = nullptr;
-    if constexpr (KEEP) {
-        if (p.pieced && w.sq.end - w.sq.start > p.piece)
-            src = p.carry + (w.pi * p.H + h) * ssz;
-        else if (p.s_in)
-            src = p.s_in + (int64_t(w.slot) * p.H + h) * ssz;
-    }
-    load_state<KB>(S, src, p.dk, p.dv, c_wave, lane);
-
-    const int64_t nch = (hi - lo + C - 1) / C;
-    const Blocked at(p, w, lo);
-    Rows<PARTS, C, KD, kThreads> rk, rq;
-    Rows<PARTS, C, kCols, kThreads> rv;
-    rk.prepare(p.k, int64_t(h / p.rep) * p.dk, p.sk, p.dk, tid);
-    rq.prepare(p.q, int64_t(h / p.rep) * p.dk, p.sq, p.dk, tid);
-    rv.prepare(p.v, int64_t(h) * p.dv + c_slice, p.sv, p.dv - c_slice, tid);
-    const bool ahead = DMA && p.wide;
-    auto load = [&](int64_t n) {
-        const bool odd = SETS == 2 && (n & 1);
-        rk.load(Ks + (odd ? KE : 0), wave, lo + n * C, hi);
-        rq.load(Qs + (odd ? KE : 0), wave, lo + n * C, hi);
-        rv.load(Vs + (odd ? VE : 0), wave, lo + n * C, hi);
+__global__ void __launch_bounds__(kThreads, KD == 256 ? 1 : 2) delta_walks_kernel(DeltaPass f, DeltaPass r, uint32_t nf) {
+    union Room {
+        PassRoom<PARTS, KD, MODE> f;
+        RevRoom<PARTS, KD> r;
     };
-    auto load_a = [&](int64_t n, int lane) { at.load(As + (n & 1 ? WP * PB : 0), &steps[n & 1], p, n, h, wave, lane); };
-    // a block's last chunk is the first one here
-    auto starts = [&](int64_t n) { return !at.two || (n & 1) || n == nch - 1; };
-    if (nch > 0) {
-        if (p.wide) load(nch - 1);
-        load_a(nch - 1, lane);
-    }
-    wait_memory<0>();
-
-    for (int64_t n = nch - 1; n >= 0; --n) {
-        const int64_t c0 = lo + n * C;
-        const Steps<C>& st = steps[n & 1];
-        const bool odd = SETS == 2 && (n & 1);
-        uint16_t* const K = Ks + (odd ? KE : 0);
-        uint16_t* const Q = Qs + (odd ? KE : 0);
-        uint16_t* const V = Vs + (odd ? VE : 0);
-        const uint16_t* const A = As + (n & 1 ? WP * PB : 0);
-        int lane = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
-        asm volatile("" : "+v"(lane));
-        const int tid = 64 * wave + lane, g4 = lane >> 4, l16 = lane & 15;
-        // what a wave stored since this chunk's rows were asked for may still be under way
-        constexpr int OUT = C / 4 + C / 8;   // Z, and the gradient of v in pairs or more
-        if (!active || !KEEP)
-            wait_memory<0>();
-        else if (starts(n + 1))
-            wait_memory<2 * KB + OUT>();
-        else
-            wait_memory<OUT>();
-        lds_barrier();
-        if (!ahead) {
-            if (!DMA && p.wide) {
-                rk.store(K, tid);
-                rq.store(Q, tid);
-                rv.store(V, tid);
-                if (n > 0) load(n - 1);
-            } else {
-                rk.copy(K, tid, c0, hi);
-                rq.copy(Q, tid, c0, hi);
-                rv.copy(V, tid, c0, hi);
-            }
-            lds_barrier();
-        }
-        if (n > 0) {
-            if (ahead) load(n - 1);
-            load_a(n - 1, lane);
-        }
-        if constexpr (KEEP) {
-            if (active && starts(n))
-                store_state<KB>(S, p.keep + (at.block(n) * p.H + h) * ssz, p.dk, p.dv, c_wave, p.dv % 4 == 0, lane);
-        }
-        put_pt<PARTS, KD>(Q, K, PT, st, p.scale, wave, lane);
-        // ---- what reaches U from behind: e^{G_C - G} K dS
-        f32x4 acc[IT];
-        u32x4 v[PARTS], ab[IT][WP];
-        if (active) {
-            const uint32_t bpair = pair_base<KD>(lane);
-#pragma unroll
-            for (int i = 0; i < IT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            u32x4 ka[2][IT][PARTS];   // operands one step ahead
-            auto read = [&](int kb) {
-#pragma unroll
-                for (int i = 0; i < IT; ++i)
-#pragma unroll
-                    for (int x = 0; x < PARTS; ++x) ka[kb & 1][i][x] = pair_op<KD>(K + x * C * KD, 0, i, kb, bpair);
-            };
-            read(0);
-#pragma unroll
-            for (int kb = 0; kb < KB; ++kb) {
-                if (kb + 1 < KB) read(kb + 1);
-                u32x4 sp[WP];
-                pair_parts<WP>(S[2 * kb], S[2 * kb + 1], sp);
-                mma_tiles<IT, PARTS, WP>(ka[kb & 1], sp, acc);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-#pragma unroll
-            for (int i = 0; i < IT; ++i) {
-                const f32x4 e = *reinterpret_cast<const f32x4*>(&st.out[8 * g4 + 4 * i]);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) acc[i][r] *= e[r];
-            }
-            const uint32_t bv = col_base<kCols, 0>(16 * wave, lane), bt = tri_t_base(lane);
-#pragma unroll
-            for (int i = 0; i < PARTS; ++i) v[i] = col_op<kCols>(V + i * C * kCols, 0, 0, 0, bv);
-#pragma unroll
-            for (int i = 0; i < IT; ++i)
-#pragma unroll
-                for (int k = 0; k < WP; ++k) ab[i][k] = tri_t_op(A + k * PB, i, bt);
-        }
-        lds_barrier();      // P^T is there
-        if (active) {
-            const uint32_t b32 = row_base<32>(lane), bk = col_base<KD, 1>(0, lane);
-            {
-                u32x4 pt[IT][WP];
-#pragma unroll
-                for (int i = 0; i < IT; ++i)
-#pragma unroll
-                    for (int k = 0; k < WP; ++k) pt[i][k] = row_op<32>(PT + k * PB + 512 * i, 0, 0, b32);
-                mma_tiles<IT, WP, PARTS>(pt, v, acc);
-            }
-            u32x4 up[WP];
-            pair_parts<WP>(acc[0], acc[1], up);
-#pragma unroll
-            for (int i = 0; i < IT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            mma_tiles<IT, WP, WP>(ab, up, acc);
-            // ---- the gradient of the incoming state
-            constexpr int G = 4;       // tiles of the state at a time
-            u32x4 qa[G][PARTS], ka[G][PARTS];
-            auto read = [&](int m0) {
-#pragma unroll
-                for (int m = 0; m < G; ++m)
-#pragma unroll
-                    for (int i = 0; i < PARTS; ++i) {
-                        qa[m][i] = col_op<KD>(Q + i * C * KD, 0, (m0 + m) >> 1, m & 1, bk);
-                        ka[m][i] = col_op<KD>(K + i * C * KD, 0, (m0 + m) >> 1, m & 1, bk);
-                    }
-            };
-            read(0);
-            f32x4 x[2], y[2];
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int t0 = 8 * g4 + 4 * half;
-                const f32x4 e = *reinterpret_cast<const f32x4*>(&st.in[t0]), b = *reinterpret_cast<const f32x4*>(&st.bin[t0]);
-#pragma unroll
-                for (int r = 0; r < 4; r += 2) {
-                    float a, z;
-                    unpack<PARTS>(v, 2 * half + r / 2, a, z);
-                    x[half][r] = a * (e[r] * p.scale);
-                    x[half][r + 1] = z * (e[r + 1] * p.scale);
-                }
-#pragma unroll
-                for (int r = 0; r < 4; ++r) y[half][r] = -b[r] * acc[half][r];
-            }
-            u32x4 dp[WP], rp[WP];
-            pair_parts<WP>(x[0], x[1], dp);
-            pair_parts<WP>(y[0], y[1], rp);
-            const float tail = st.tail[0];
-#pragma unroll
-            for (int m0 = 0; m0 < 2 * KB; m0 += G) {
-                if (m0 > 0) read(m0);
-#pragma unroll
-                for (int m = m0; m < m0 + G; ++m)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) S[m][r] *= tail;
-                mma_tiles<G, PARTS, WP>(qa, dp, &S[m0]);
-                mma_tiles<G, PARTS, WP>(ka, rp, &S[m0]);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            if constexpr (KEEP) {
-                const int64_t pitch = int64_t(p.H) * p.dv * 4;
-                store_tiles<C, true>(acc, reinterpret_cast<char*>(p.rows) + c0 * pitch + int64_t(h) * p.dv * 4, pitch, hi - c0,
-                                     c_wave, p.dv, true, false, lane);
-#pragma unroll
-                for (int i = 0; i < IT; ++i) {
-                    const f32x4 b = *reinterpret_cast<const f32x4*>(&st.given[8 * g4 + 4 * i]);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[i][r] *= b[r];
-                }
-                constexpr int E = PARTS == 1 ? 2 : 4;
-                const int64_t vp = int64_t(p.H) * p.dv * E;
-                store_tiles<C, true>(acc, static_cast<char*>(p.dv_out) + c0 * vp + int64_t(h) * p.dv * E, vp, hi - c0, c_wave, p.dv,
-                                     PARTS > 1, p.pairs, lane);
-            }
-        }
-    }
-    if (!active) return;
-    float* dst = nullptr;
-    if constexpr (MODE == kDeltaStates) dst = p.carry + (w.pi * p.H + h) * ssz;
-    else if (w.first && p.s_out) dst = p.s_out + (int64_t(w.slot) * p.H + h) * ssz;
-    if (dst) store_state<KB>(S, dst, p.dk, p.dv, c_wave, false, lane);
+    __shared__ Room room;
+    if (blockIdx.x < nf) pass_walk<PARTS, KD, MODE>(f, blockIdx.x, room.f);
+    else rev_walk<PARTS, KD, MODE>(r, blockIdx.x - nf, room.r);
 }
+
 
 // ---------------------------------------------------------------- a chunk's gradients
 struct GradArgs {
@@ -742,17 +544,19 @@ inline int make_grad_plan(const ssm_linattn_dims* d, bool packed, GradPlan* pl) 
     return SSM_OK;
 }
 
-template <int MODE> void run_rev(const DeltaPass& p, bool f32, hipStream_t s) {
-    const dim3 grid(static_cast<uint32_t>(int64_t(p.npieces) * p.H * p.vslices)), block(kThreads);
-#define SSM_REV(K)                                                                                  \
+template <int MODE> void run_walks(const DeltaPass& f, const DeltaPass& r, bool f32, hipStream_t s) {
+    const int64_t units = int64_t(f.npieces) * f.H;
+    const uint32_t nf = static_cast<uint32_t>(units * (MODE == kDeltaStates ? f.vslices + f.kslices : f.vslices));
+    const dim3 grid(nf + static_cast<uint32_t>(units * f.vslices)), block(kThreads);
+#define SSM_WALKS(K)                                                                                \
     do {                                                                                            \
-        if (f32) launch_kernel(delta_rev_kernel<3, K, MODE>, grid, block, 0, s, p);                 \
-        else launch_kernel(delta_rev_kernel<1, K, MODE>, grid, block, 0, s, p);                     \
+        if (f32) launch_kernel(delta_walks_kernel<3, K, MODE>, grid, block, 0, s, f, r, nf);        \
+        else launch_kernel(delta_walks_kernel<1, K, MODE>, grid, block, 0, s, f, r, nf);            \
     } while (0)
-    if (p.dk <= 64) SSM_REV(64);
-    else if (p.dk <= 128) SSM_REV(128);
-    else SSM_REV(256);
-#undef SSM_REV
+    if (f.dk <= 64) SSM_WALKS(64);
+    else if (f.dk <= 128) SSM_WALKS(128);
+    else SSM_WALKS(256);
+#undef SSM_WALKS
 }
 
 inline void run_grad(const GradArgs& a, bool f32, int64_t nchunks, hipStream_t s) {
@@ -876,13 +680,11 @@ int ssm_delta_bwd(const void* q, const void* k, const void* v, const float* g, c
     launch_error = hipSuccess;
     launch_delta_tri(f, f32, pl.nchunks, s);
     if (pl.pieced) {
-        launch_delta_pass(f, f32, kDeltaStates, s);
+        run_walks<kDeltaStates>(f, r, f32, s);
         launch_delta_carry(f, false, s);
-        run_rev<kDeltaStates>(r, f32, s);
         launch_delta_carry(r, true, s);
     }
-    launch_delta_pass(f, f32, kDeltaKeep, s);
-    run_rev<kDeltaKeep>(r, f32, s);
+    run_walks<kDeltaKeep>(f, r, f32, s);
     run_grad(a, f32, pl.nchunks, s);
     if (shared) {
         const FoldArgs fa = {{wq, wkk}, {gr.dq, gr.dk}, d.tokens * d.kheads, f.rep, f.dk};

@@ -1,7 +1,7 @@
 // delta_fwd.hip -- the gated delta rule: the triangular systems of all chunks, the walk over
 // them (packed sequences, cut into pieces along the tokens when there are few heads and
 // sequences) and the single-token step.
-#include "delta.h"
+#include "delta_walk.h"
 
 namespace {
 namespace dl {
@@ -159,314 +159,10 @@ __global__ void __launch_bounds__(kThreads) delta_tri_kernel(DeltaPass p) {
 }
 
 // ---------------------------------------------------------------- the walk
-// One workgroup walks one piece of one head's sequence for 64 columns of the state, 16 a wave, in
-// chunks of 32 tokens: 64 would halve the splits of the state into parts, but take the LDS of
-// four workgroups on a CU and twice the time from chunk to chunk.
-//
-// Two sets of tiles, so that the next chunk's rows and A are asked for a chunk ahead; queries have
-// one, refilled as soon as they are read.  (float32 rows pass through registers.)
 template <int PARTS, int KD, int MODE>
 __global__ void __launch_bounds__(kThreads, pass_waves(KD, PARTS, MODE)) delta_pass_kernel(DeltaPass p) {
-    constexpr bool FULL = MODE == kDeltaFull, KEEP = MODE == kDeltaKeep, DMA = PARTS == 1;
-    constexpr int C = kChunk, IT = C / 16, KB = KD / 32, NTILE = 3, PB = 2 * 512, WP = 3;   // parts of what is no bf16 input
-    constexpr int SETS = DMA ? 2 : 1, ASETS = FULL && !DMA ? 1 : 2, KE = PARTS * C * KD, VE = PARTS * C * kCols;
-    __shared__ __align__(16) uint16_t Ks[SETS * KE], Vs[SETS * VE], As[ASETS * WP * PB];
-    __shared__ __align__(16) uint16_t Q[FULL ? KE : 8], Ps[FULL ? WP * PB : 8];
-    __shared__ Steps<C> steps[2];
-    const int tid = threadIdx.x, lane = tid & 63, g4 = lane >> 4, l16 = lane & 15;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const Where w = find_piece(p, MODE == kDeltaStates ? p.vslices + p.kslices : p.vslices, !KEEP);
-    // columns of the transition: the same walk from the unit matrix, without values
-    const bool trans = MODE == kDeltaStates && w.slice >= p.vslices;
-    // no piece starts from a last one's state, but its transition leads back in the gradients
-    if (!w.on || (MODE == kDeltaStates && w.last && !(trans && p.trans_t))) return;
-    const int width = trans ? p.dk : p.dv, h = w.h;
-    const int c_slice = (trans ? w.slice - p.vslices : w.slice) * kCols, c_wave = c_slice + 16 * wave, col = c_wave + l16;
-    const bool active = c_wave < width;                      // this wave has columns
-    const int64_t lo = w.lo, hi = w.hi, ssz = int64_t(p.dk) * p.dv;
-
-    f32x4 S[2 * KB];
-    const float* src = nullptr;
-    if constexpr (MODE != kDeltaStates) {
-        if (p.pieced && w.sq.end - w.sq.start > p.piece)
-            src = p.carry + (w.pi * p.H + h) * ssz;
-        else if (p.s_in)
-            src = p.s_in + (int64_t(w.slot) * p.H + h) * ssz;
-    }
-    load_state<KB>(S, src, p.dk, p.dv, c_wave, lane);
-    if (trans) {
-#pragma unroll
-        for (int m = 0; m < 2 * KB; ++m)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) S[m][r] = 32 * (m >> 1) + 8 * g4 + 4 * (m & 1) + r == col ? 1.0f : 0.0f;
-    }
-    if constexpr (FULL) {   // the tile above the diagonal that shares a block with one on it stays zero
-        for (int i = tid; i < WP * PB / 2; i += kThreads) reinterpret_cast<uint32_t*>(Ps)[i] = 0;
-    }
-
-    const int64_t nch = (hi - lo + C - 1) / C;
-    const Blocked at(p, w, lo);
-    Rows<PARTS, C, KD, kThreads> rk, rq;
-    Rows<PARTS, C, kCols, kThreads> rv;
-    rk.prepare(p.k, int64_t(h / p.rep) * p.dk, p.sk, p.dk, tid);
-    rq.prepare(p.q, int64_t(h / p.rep) * p.dk, p.sq, p.dk, tid);
-    rv.prepare(p.v, int64_t(h) * p.dv + c_slice, p.sv, p.dv - c_slice, tid);
-    const bool ahead = DMA && p.wide;
-    auto load_k = [&](int64_t n) { rk.load(Ks + (SETS == 2 && n & 1 ? KE : 0), wave, lo + n * C, hi); };
-    auto load_v = [&](int64_t n) {
-        if (!trans) rv.load(Vs + (SETS == 2 && n & 1 ? VE : 0), wave, lo + n * C, hi);
-    };
-    auto load_q = [&](int64_t n) {
-        if constexpr (FULL) rq.load(Q, wave, lo + n * C, hi);
-    };
-    auto load_a = [&](int64_t n, int lane) { at.load(As + (ASETS == 2 && n & 1 ? WP * PB : 0), &steps[n & 1], p, n, h, wave, lane); };
-    if (nch > 0) {
-        if (p.wide) {
-            load_k(0);
-            load_v(0);
-            load_q(0);
-        }
-        load_a(0, lane);
-    }
-    wait_memory<0>();
-
-    for (int64_t n = 0; n < nch; ++n) {
-        const int64_t c0 = lo + n * C;
-        const Steps<C>& st = steps[n & 1];
-        uint16_t* const K = Ks + (SETS == 2 && n & 1 ? KE : 0);
-        uint16_t* const V = Vs + (SETS == 2 && n & 1 ? VE : 0);
-        const uint16_t* const A = As + (ASETS == 2 && n & 1 ? WP * PB : 0);
-        // the lane as the loop's own value: operand addresses are cheap to form anew
-        int lane = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
-        asm volatile("" : "+v"(lane));
-        const int tid = 64 * wave + lane, g4 = lane >> 4, l16 = lane & 15;
-        // this chunk's rows and A; what a wave stored since they were asked for may still be under way
-        constexpr int OUT = C / 4;
-        if (!active || MODE == kDeltaStates)
-            wait_memory<0>();
-        else if (FULL && DMA && p.pairs)
-            wait_memory<OUT / 2>();
-        else if (KEEP && at.starts(n - 1))
-            wait_memory<2 * KB + OUT>();
-        else
-            wait_memory<OUT>();
-        lds_barrier();
-        if (!ahead) {
-            if (!DMA && p.wide) {
-                rk.store(K, tid);
-                if (!trans) rv.store(V, tid);
-                if constexpr (FULL) rq.store(Q, tid);
-                if (n + 1 < nch) {
-                    load_k(n + 1);
-                    load_v(n + 1);
-                    load_q(n + 1);
-                }
-            } else {
-                rk.copy(K, tid, c0, hi);
-                if (!trans) rv.copy(V, tid, c0, hi);
-                if constexpr (FULL) rq.copy(Q, tid, c0, hi);
-            }
-            lds_barrier();
-        }
-        if (ASETS == 2 && n + 1 < nch) {
-            if (ahead) {
-                load_k(n + 1);
-                load_v(n + 1);
-            }
-            load_a(n + 1, lane);
-        }
-        if constexpr (KEEP) {
-            if (active && at.starts(n))
-                store_state<KB>(S, p.keep + (at.block(n) * p.H + h) * ssz, p.dk, p.dv, c_wave, p.dv % 4 == 0, lane);
-        }
-        const uint32_t base = row_base<KD>(lane), bpair = pair_base<KD>(lane), b32 = row_base<32>(lane);
-        // ---- what the state is read for: K S (paired rows) and Q S
-        f32x4 acc[IT], o[IT], pt = {0.0f, 0.0f, 0.0f, 0.0f};
-        u32x4 xp[WP], ab[IT][WP];
-        // a tile of P on or below the diagonal each but the last wave
-        const int pi = wave < 1 ? 0 : 1, pj = wave < 2 ? 0 : 1;
-        if (active) {
-#pragma unroll
-            for (int i = 0; i < IT; ++i) acc[i] = o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            u32x4 ka[2][IT][PARTS], qa[2][IT][PARTS], px[2][PARTS], py[2][PARTS];   // operands one step ahead
-            auto read = [&](int kb) {
-#pragma unroll
-                for (int x = 0; x < PARTS; ++x) {
-#pragma unroll
-                    for (int i = 0; i < IT; ++i) {
-                        ka[kb & 1][i][x] = pair_op<KD>(K + x * C * KD, 0, i, kb, bpair);
-                        if constexpr (FULL) qa[kb & 1][i][x] = row_op<KD>(Q + x * C * KD, 16 * i, kb, base);
-                    }
-                    if constexpr (FULL) {
-                        px[kb & 1][x] = row_op<KD>(K + x * C * KD, 16 * pj, kb, base);
-                        py[kb & 1][x] = row_op<KD>(Q + x * C * KD, 16 * pi, kb, base);
-                    }
-                }
-            };
-            read(0);
-#pragma unroll
-            for (int kb = 0; kb < KB; ++kb) {
-                if (kb + 1 < KB) read(kb + 1);
-                u32x4 sp[WP];
-                pair_parts<WP>(S[2 * kb], S[2 * kb + 1], sp);
-                mma_tiles<IT, PARTS, WP>(ka[kb & 1], sp, acc);
-                if constexpr (FULL) {
-                    mma_tiles<IT, PARTS, WP>(qa[kb & 1], sp, o);
-                    pt = mma_parts<PARTS, PARTS>(px[kb & 1], py[kb & 1], pt);
-                }
-                if constexpr (!DMA) __builtin_amdgcn_sched_barrier(0);   // three parts of operands fill the registers
-            }
-#pragma unroll
-            for (int i = 0; i < IT; ++i)
-#pragma unroll
-                for (int k = 0; k < WP; ++k) ab[i][k] = row_op<32>(A + k * PB + 512 * i, 0, 0, b32);
-            // beta X = beta V - beta e^G K S
-            f32x4 x[2];
-            u32x4 v[PARTS];
-            if (!trans) {
-                const uint32_t bv = col_base<kCols, 0>(16 * wave, lane);
-#pragma unroll
-                for (int i = 0; i < PARTS; ++i) v[i] = col_op<kCols>(V + i * C * kCols, 0, 0, 0, bv);
-            }
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int t0 = 8 * g4 + 4 * half;
-                const f32x4 f = *reinterpret_cast<const f32x4*>(&st.bin[t0]), b = *reinterpret_cast<const f32x4*>(&st.beta[t0]);
-#pragma unroll
-                for (int r = 0; r < 4; r += 2) {
-                    float y = 0.0f, z = 0.0f;
-                    if (!trans) unpack<PARTS>(v, 2 * half + r / 2, y, z);
-                    x[half][r] = fmaf(-f[r], acc[half][r], b[r] * y);
-                    x[half][r + 1] = fmaf(-f[r + 1], acc[half][r + 1], b[r + 1] * z);
-                }
-            }
-            pair_parts<WP>(x[0], x[1], xp);
-            if constexpr (FULL) {
-#pragma unroll
-                for (int i = 0; i < IT; ++i) {
-                    const f32x4 e = *reinterpret_cast<const f32x4*>(&st.in[16 * i + 4 * g4]);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) o[i][r] *= e[r] * p.scale;
-                }
-            }
-        }
-        if constexpr (FULL) {
-            if (!active) {      // the others have it from their walk over the state's rows
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb) {
-                    u32x4 x[PARTS], y[PARTS];
-#pragma unroll
-                    for (int i = 0; i < PARTS; ++i) {
-                        x[i] = row_op<KD>(K + i * C * KD, 16 * pj, kb, base);
-                        y[i] = row_op<KD>(Q + i * C * KD, 16 * pi, kb, base);
-                    }
-                    pt = mma_parts<PARTS, PARTS>(x, y, pt);
-                }
-            }
-            if (wave < NTILE) {
-                const int i = 16 * pi + l16, j0 = 16 * pj + 4 * g4;
-                const int to = 512 * pi + at_piece<32>(l16, 2 * pj + (g4 >> 1)) + 4 * (g4 & 1);
-                const float gi = st.hi[i], ei = st.lo[i];
-                const f32x4 gj = *reinterpret_cast<const f32x4*>(&st.hi[j0]), ej = *reinterpret_cast<const f32x4*>(&st.lo[j0]);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float e = __builtin_amdgcn_exp2f((gi - gj[r]) + (ei - ej[r]));
-                    pt[r] = j0 + r <= i ? pt[r] * (e * p.scale) : 0.0f;
-                }
-                uint32_t x[WP], y[WP];
-                split<WP>(pt[0], pt[1], x);
-                split<WP>(pt[2], pt[3], y);
-#pragma unroll
-                for (int k = 0; k < WP; ++k) *reinterpret_cast<uint2*>(Ps + k * PB + to) = uint2{x[k], y[k]};
-            }
-            lds_barrier();      // P is there; q has been read
-            if (ahead && n + 1 < nch) load_q(n + 1);
-        }
-        if (active) {
-            // ---- U = A beta X
-#pragma unroll
-            for (int i = 0; i < IT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            mma_tiles<IT, WP, WP>(ab, xp, acc);
-            if constexpr (KEEP) {
-                const int64_t pitch = int64_t(p.H) * p.dv * 4;
-                store_tiles<C, true>(acc, reinterpret_cast<char*>(p.rows) + c0 * pitch + int64_t(h) * p.dv * 4, pitch, hi - c0,
-                                     c_wave, p.dv, true, false, lane);
-            }
-            // ---- the outgoing state
-            const uint32_t bk = col_base<KD, 1>(0, lane);
-            constexpr int G = FULL || KB < 4 ? 4 : 8;       // tiles of the state at a time
-            u32x4 ka[G][PARTS];
-            auto read = [&](int m0) {
-#pragma unroll
-                for (int m = 0; m < G; ++m)
-#pragma unroll
-                    for (int i = 0; i < PARTS; ++i) ka[m][i] = col_op<KD>(K + i * C * KD, 0, (m0 + m) >> 1, m & 1, bk);
-            };
-            read(0);
-            f32x4 x[2];
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const f32x4 f = *reinterpret_cast<const f32x4*>(&st.out[8 * g4 + 4 * half]);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) x[half][r] = acc[half][r] * f[r];
-            }
-            u32x4 up[WP];
-            pair_parts<WP>(x[0], x[1], up);
-            const float tail = st.tail[0];
-#pragma unroll
-            for (int m0 = 0; m0 < 2 * KB; m0 += G) {
-                if (m0 > 0) read(m0);
-#pragma unroll
-                for (int m = m0; m < m0 + G; ++m)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) S[m][r] *= tail;
-                mma_tiles<G, PARTS, WP>(ka, up, &S[m0]);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-        }
-        if constexpr (FULL) {
-            if constexpr (ASETS == 1) {
-                lds_barrier();      // A has been read
-                if (n + 1 < nch) load_a(n + 1, lane);
-            }
-            if (active) {
-                // ---- the chunk's own share, P U
-#pragma unroll
-                for (int i = 0; i < IT; ++i)
-#pragma unroll
-                    for (int k = 0; k < WP; ++k) ab[i][k] = row_op<32>(Ps + k * PB + 512 * i, 0, 0, b32);
-                u32x4 up[WP];
-                pair_parts<WP>(acc[0], acc[1], up);
-                mma_tiles<IT, WP, WP>(ab, up, o);
-                constexpr int OE = PARTS == 1 ? 2 : 4;
-                const int64_t pitch = p.so * OE;
-                store_tiles<C, false>(o, static_cast<char*>(p.out) + c0 * pitch + int64_t(h) * p.dv * OE, pitch, hi - c0, c_wave,
-                                      p.dv, PARTS > 1, p.pairs, lane);
-            }
-        }
-    }
-
-    // ---------------------------------------------- the state that leaves
-    if (!active) return;
-    if constexpr (MODE == kDeltaStates) {
-        if (trans) {
-            const int64_t to = (w.pi * p.H + h) * int64_t(p.dk) * p.dk;
-            store_state<KB>(S, p.trans + to, p.dk, p.dk, c_wave, p.dk % 4 == 0, lane);
-            if (p.trans_t) {
-#pragma unroll
-                for (int m = 0; m < 2 * KB; ++m)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int row = 32 * (m >> 1) + 8 * g4 + 4 * (m & 1) + r;
-                        if (row < p.dk && col < p.dk) p.trans_t[to + int64_t(col) * p.dk + row] = S[m][r];
-                    }
-            }
-        } else {
-            store_state<KB>(S, p.carry + (w.pi * p.H + h) * ssz, p.dk, p.dv, c_wave, p.dv % 4 == 0, lane);
-        }
-    } else if (FULL && w.last && p.s_out) {
-        store_state<KB>(S, p.s_out + (int64_t(w.slot) * p.H + h) * ssz, p.dk, p.dv, c_wave, false, lane);
-    }
+    __shared__ PassRoom<PARTS, KD, MODE> room;
+    pass_walk<PARTS, KD, MODE>(p, blockIdx.x, room);
 }
 
 // ---------------------------------------------------------------- pieces' starting states
@@ -734,12 +430,6 @@ void ssm_detail::launch_delta_tri(const DeltaPass& p, bool f32, int64_t nchunks,
     else dl::run_tri<32>(p, f32, nchunks, s);
 }
 
-void ssm_detail::launch_delta_pass(const DeltaPass& p, bool f32, DeltaMode mode, hipStream_t s) {
-    if (mode == kDeltaStates) dl::run_pass<kDeltaStates>(p, f32, s);
-    else if (mode == kDeltaFull) dl::run_pass<kDeltaFull>(p, f32, s);
-    else dl::run_pass<kDeltaKeep>(p, f32, s);
-}
-
 void ssm_detail::launch_delta_carry(const DeltaPass& p, bool reverse, hipStream_t s) {
     const dim3 grid(static_cast<uint32_t>(cdiv(p.dv, dl::kCarryCols)), p.H, p.nseq), block(dl::kCarryThreads);
 #define SSM_CARRY(K)                                                                        \
@@ -825,10 +515,10 @@ int ssm_delta_fwd(const void* q, const void* k, const void* v, const float* g, c
     launch_error = hipSuccess;
     launch_delta_tri(p, f32, pl.nchunks, s);
     if (pl.pieced) {
-        launch_delta_pass(p, f32, kDeltaStates, s);
+        run_pass<kDeltaStates>(p, f32, s);
         launch_delta_carry(p, false, s);
     }
-    launch_delta_pass(p, f32, kDeltaFull, s);
+    run_pass<kDeltaFull>(p, f32, s);
     return launch_error == hipSuccess ? SSM_OK : SSM_ERR_HIP;
 }
 
