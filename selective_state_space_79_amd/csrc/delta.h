@@ -65,7 +65,7 @@ struct DeltaPass {
 // at the chunk's end).
 enum DeltaMode { kDeltaStates = 0, kDeltaFull = 1, kDeltaKeep = 2 };
 void launch_delta_tri(const DeltaPass& p, bool f32, int64_t nchunks, hipStream_t s);
-void launch_delta_carry(const DeltaPass& p, bool reverse, hipStream_t s);
+void launch_delta_carry(const DeltaPass& p, const DeltaPass* r, hipStream_t s);   // r: the walk against time
 
 }  // namespace ssm_detail
 

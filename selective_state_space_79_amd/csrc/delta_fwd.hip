@@ -173,12 +173,11 @@ __global__ void __launch_bounds__(kThreads, pass_waves(KD, PARTS, MODE)) delta_p
 constexpr int kCarryThreads = 512, kCarryCols = 128;
 
 template <int KD, bool REV>
-__global__ void __launch_bounds__(kCarryThreads) delta_carry_kernel(DeltaPass p) {
+__device__ __forceinline__ void carry_walk(const DeltaPass& p, int h, uint16_t (&Ws)[2][3 * 16 * KD]) {
     constexpr int KB = KD / 32, WP = 3, VPT = KD / 32, AHEAD = 4;   // values of a tile a thread brings
-    __shared__ __align__(16) uint16_t Ws[2][WP * 16 * KD];
     const int tid = threadIdx.x, lane = tid & 63, g4 = lane >> 4, l16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int h = blockIdx.y, seq = blockIdx.z;
+    const int seq = blockIdx.z;
     const int slot = REV ? seq : find_slot(p.slots, p.nslots, seq);
     if (slot < 0) return;
     const Seq sq = seq_range(p, seq);
@@ -243,6 +242,15 @@ __global__ void __launch_bounds__(kCarryThreads) delta_carry_kernel(DeltaPass p)
             S[m] = c[0] + c[1];
         }
     }
+}
+
+// The heads of p and, of the gradients, those of r behind them.
+template <int KD, bool GRADS>
+__global__ void __launch_bounds__(kCarryThreads) delta_carry_kernel(DeltaPass p, DeltaPass r) {
+    __shared__ __align__(16) uint16_t Ws[2][3 * 16 * KD];
+    const int h = blockIdx.y;
+    if (!GRADS || h < p.H) carry_walk<KD, false>(p, h, Ws);
+    else carry_walk<KD, true>(r, h - p.H, Ws);
 }
 
 // ---------------------------------------------------------------- single tokens
@@ -430,12 +438,12 @@ void ssm_detail::launch_delta_tri(const DeltaPass& p, bool f32, int64_t nchunks,
     else dl::run_tri<32>(p, f32, nchunks, s);
 }
 
-void ssm_detail::launch_delta_carry(const DeltaPass& p, bool reverse, hipStream_t s) {
-    const dim3 grid(static_cast<uint32_t>(cdiv(p.dv, dl::kCarryCols)), p.H, p.nseq), block(dl::kCarryThreads);
+void ssm_detail::launch_delta_carry(const DeltaPass& p, const DeltaPass* r, hipStream_t s) {
+    const dim3 grid(static_cast<uint32_t>(cdiv(p.dv, dl::kCarryCols)), r ? 2 * p.H : p.H, p.nseq), block(dl::kCarryThreads);
 #define SSM_CARRY(K)                                                                        \
     do {                                                                                    \
-        if (reverse) launch_kernel(dl::delta_carry_kernel<K, true>, grid, block, 0, s, p);  \
-        else launch_kernel(dl::delta_carry_kernel<K, false>, grid, block, 0, s, p);         \
+        if (r) launch_kernel(dl::delta_carry_kernel<K, true>, grid, block, 0, s, p, *r);    \
+        else launch_kernel(dl::delta_carry_kernel<K, false>, grid, block, 0, s, p, p);      \
     } while (0)
     if (p.dk <= 64) SSM_CARRY(64);
     else if (p.dk <= 128) SSM_CARRY(128);
@@ -516,7 +524,7 @@ int ssm_delta_fwd(const void* q, const void* k, const void* v, const float* g, c
     launch_delta_tri(p, f32, pl.nchunks, s);
     if (pl.pieced) {
         run_pass<kDeltaStates>(p, f32, s);
-        launch_delta_carry(p, false, s);
+        launch_delta_carry(p, nullptr, s);
     }
     run_pass<kDeltaFull>(p, f32, s);
     return launch_error == hipSuccess ? SSM_OK : SSM_ERR_HIP;

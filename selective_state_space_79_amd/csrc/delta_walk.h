@@ -44,7 +44,7 @@ __device__ __forceinline__ void pass_walk(const DeltaPass& p, uint32_t unit, Pas
     // columns of the transition: the same walk from the unit matrix, without values
     const bool trans = MODE == kDeltaStates && w.slice >= p.vslices;
     // no piece starts from a last one's state, but its transition leads back in the gradients
-    if (!w.on || (MODE == kDeltaStates && w.last && !(trans && p.trans_t))) return;
+    if (!w.on || (MODE == kDeltaStates && w.last && !(trans && p.trans_t && !w.first))) return;
     const int width = trans ? p.dk : p.dv, h = w.h;
     const int c_slice = (trans ? w.slice - p.vslices : w.slice) * kCols, c_wave = c_slice + 16 * wave, col = c_wave + l16;
     const bool active = c_wave < width;                      // this wave has columns
