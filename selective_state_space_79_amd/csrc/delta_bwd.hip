@@ -258,10 +258,7 @@ __global__ void __launch_bounds__(64 * W, 2) delta_grad_kernel(GradArgs ga) {
         }
         lds_barrier();
         const bool more = c + 32 < p.dv;
-        if (more) {
-            ask(c + 32);
-            ask_state(ws, ns, c + 32);
-        }
+        if (more) ask(c + 32);
         // one state after the other: both in parts would not fit the registers
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
@@ -279,7 +276,7 @@ __global__ void __launch_bounds__(64 * W, 2) delta_grad_kernel(GradArgs ga) {
         }
 #pragma unroll
         for (int n = 0; n < NC; ++n) pair_parts<WP>(f4(nd[n][0]), f4(nd[n][1]), sp[n]);
-        if (more) ask_state(wd, nd, c + 32);
+        if (more) ask_state(ws, ns, c + 32);
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             u32x4 u[WP];
@@ -289,6 +286,7 @@ __global__ void __launch_bounds__(64 * W, 2) delta_grad_kernel(GradArgs ga) {
             for (int n = 0; n < NC; ++n) au[n][i] = mma_parts<WP, WP>(u, sp[n], au[n][i]);
             __builtin_amdgcn_sched_barrier(0);
         }
+        if (more) ask_state(wd, nd, c + 32);
 #pragma unroll
         for (int mm = 0; mm < MT; ++mm) {
             const int m = wave + W * mm;
