@@ -52,12 +52,15 @@ struct GradArgs {
     const void* dout;
     const float* keep_d;    // [chunks][H][dk][dv]: dS_out
     const float* z;         // [T][H][dv]: Z
-    void* dq;               // I/O type, or float32 per head (wide_out)
+    void* dq;               // I/O type, [T][kheads][dk]
     void* dk;
+    float* sum_q;           // float32: sums over the heads so far, or each head's (wide_out)
+    float* sum_k;
     float* dbeta;
     float* dg;
     double* part;           // [chunks][H] sums of dg (a decay per head), else null
     int64_t so, sdq;        // elements between tokens of dout, of dq and dk
+    int32_t heads;          // of a workgroup
     int32_t wide_out, pairs_k;
 };
 
@@ -109,7 +112,21 @@ template <int C> __device__ inline u32x4 block_t_op(const uint16_t* t, int ib, i
     return u32x4{u.x, u.y, v.x, v.y};
 }
 
-// One workgroup per chunk and head: what is contracted over the columns of v goes in steps of 32
+// Adds the tiles that store_tiles left as float32 in order of the tokens.
+template <int C>
+__device__ inline void add_tiles(f32x4 (&o)[C / 16], const float* row0, int64_t pitch, int64_t rows, int c_wave, int width, int lane) {
+    const Rsrc ro = rows_rsrc(reinterpret_cast<char*>(const_cast<float*>(row0)), pitch, rows, C);
+    const StoreRows to(pitch, false, C, lane >> 4);
+    const int col = c_wave + (lane & 15);
+    const uint32_t o0 = to.first(col < width, 4 * col);
+    uint32_t x[C / 4];
+#pragma unroll
+    for (int i = 0; i < C / 4; ++i) x[i] = __builtin_amdgcn_raw_buffer_load_b32(ro, o0 + to.row(16 * (i >> 2) + (i & 3)), 0, 0);
+#pragma unroll
+    for (int i = 0; i < C / 4; ++i) o[i >> 2][i & 3] += __uint_as_float(x[i]);
+}
+
+// One workgroup per chunk and head (or the heads that share its q and k, one after the other): what is contracted over the columns of v goes in steps of 32
 // of them, U, Z and the gradient of o through LDS, the states along their rows straight into
 // registers, 16 or 32 columns of dq and dk a wave; the two matrices over the chunk's tokens, D and
 // N, are shared out in tiles.
@@ -130,24 +147,22 @@ __global__ void __launch_bounds__(64 * W, 2) delta_grad_kernel(GradArgs ga) {
     uint16_t* const Zs = buf + WP * C * 32;
     uint16_t* const Os = buf + 2 * WP * C * 32;
 
-    const int tid = threadIdx.x, lane = tid & 63, g4 = lane >> 4, l16 = lane & 15;
+    const int tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const Chunks ch(p, C);
     const int64_t ci = blockIdx.x;
-    const int h = blockIdx.y;
+    const int h0 = blockIdx.y * ga.heads, hk = h0 / p.rep;
     const int seq = find_seq(ch, ci);
     const Seq sq = seq < 0 ? Seq{0, 0} : seq_range(ch, seq);
     const int64_t c0 = seq < 0 ? 0 : sq.start + (ci - piece_base(ch, seq)) * C, hi = sq.end;
     if (seq < 0 || c0 < sq.start || c0 >= hi) {
-        if (ga.part && tid == 0) ga.part[ci * p.H + h] = 0.0;
+        for (int h = h0 + tid; ga.part && h < h0 + ga.heads; h += 64 * W) ga.part[ci * p.H + h] = 0.0;
         return;
     }
     const int64_t ssz = int64_t(p.dk) * p.dv;
-    const float* const Sin = p.keep + (ci * p.H + h) * ssz;
-    const float* const Sout = ga.keep_d + (ci * p.H + h) * ssz;
     Rows<PARTS, C, KD, 64 * W> rk, rq;
-    rk.prepare(p.k, int64_t(h / p.rep) * p.dk, p.sk, p.dk, tid);
-    rq.prepare(p.q, int64_t(h / p.rep) * p.dk, p.sq, p.dk, tid);
+    rk.prepare(p.k, int64_t(hk) * p.dk, p.sk, p.dk, tid);
+    rq.prepare(p.q, int64_t(hk) * p.dk, p.sq, p.dk, tid);
     if (p.wide) {
         rk.load(K, wave, c0, hi);
         rq.load(Q, wave, c0, hi);
@@ -159,297 +174,316 @@ __global__ void __launch_bounds__(64 * W, 2) delta_grad_kernel(GradArgs ga) {
         rk.copy(K, tid, c0, hi);
         rq.copy(Q, tid, c0, hi);
     }
-    for (int i = tid; i < W * C; i += 64 * W) (&pg[0][0])[i] = 0.0f;
-    if (wave == W - 1) {
-        const int64_t t = c0 + lane;
-        const bool on = lane < C && t < hi;
-        const double s = sum_decays(on ? p.g[t * p.sg + h] : 0.0f, lane < C), end = lane_f64(s, C - 1);
-        if (lane < C) put_steps<C>(st, s, end, on ? p.beta[t * p.H + h] : 0.0f, p.least, lane);
-    }
-    const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-    f32x4 aq[NC][IT], az[NC][IT], au[NC][IT], ap[MT], an[MT];
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int i = 0; i < IT; ++i) aq[c][i] = az[c][i] = au[c][i] = zero;
-#pragma unroll
-    for (int m = 0; m < MT; ++m) ap[m] = an[m] = zero;
-    const auto tile = [](int m, int& it, int& jt) {
-        it = m < 1 ? 0 : m < 3 ? 1 : m < 6 ? 2 : 3;
-        jt = m - it * (it + 1) / 2;
-    };
-    // rows of a step: 4 or 8 threads a token
-    const int ts = tid / (32 / CPT), cs = CPT * (tid % (32 / CPT));
-    const bool mine = ts < C, here = mine && c0 + ts < hi;
-    const bool vec = p.dv % 4 == 0;
-    const IO* const vrow = static_cast<const IO*>(p.v) + (c0 + ts) * p.sv + int64_t(h) * p.dv;
-    const IO* const orow = static_cast<const IO*>(ga.dout) + (c0 + ts) * ga.so + int64_t(h) * p.dv;
-    u32x4 nu[N4], nz[N4], ns[NC][2], nd[NC][2];
-    Raw4<IO> nv[N4], no[N4];
-    const Rsrc wu = rows_rsrc(reinterpret_cast<char*>(p.rows + (c0 * p.H + h) * p.dv), int64_t(p.H) * p.dv * 4, hi - c0, C);
-    const Rsrc wz = rows_rsrc(const_cast<char*>(reinterpret_cast<const char*>(ga.z + (c0 * p.H + h) * p.dv)), int64_t(p.H) * p.dv * 4, hi - c0, C);
-    const Rsrc ws = rows_rsrc(const_cast<char*>(reinterpret_cast<const char*>(Sin)), ssz * 4, 1, 1);
-    const Rsrc wd = rows_rsrc(const_cast<char*>(reinterpret_cast<const char*>(Sout)), ssz * 4, 1, 1);
-    // four values at column c of a row of v that begins at byte `row` of a window
-    const auto four = [&](const Rsrc& w, uint32_t row, int c) {
-        if (vec) return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(w, c < p.dv ? row + 4 * c : kPast, 0, 0));
-        u32x4 x;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = __builtin_amdgcn_raw_buffer_load_b32(w, c + e < p.dv ? row + 4 * (c + e) : kPast, 0, 0);
-        return x;
-    };
-    const uint32_t trow = mine ? uint32_t(ts) * uint32_t(p.H * p.dv * 4) : kPast;
-    const auto ask = [&](int c) {
-#pragma unroll
-        for (int x = 0; x < N4; ++x) {
-            nu[x] = four(wu, trow, c + cs + 4 * x);
-            nz[x] = four(wz, trow, c + cs + 4 * x);
-            nv[x].load(vrow, here, c + cs + 4 * x, p.dv, p.wide);
-            no[x].load(orow, here, c + cs + 4 * x, p.dv, p.wide);
+    for (int h = h0; h < h0 + ga.heads; ++h) {
+        if (h > h0) __syncthreads();    // the last head's sums have been read
+        // the lane as the loop's own value: operand addresses are cheap to form anew
+        int lane = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+        asm volatile("" : "+v"(lane));
+        const int tid = 64 * wave + lane, g4 = lane >> 4, l16 = lane & 15;
+        const float* const Sin = p.keep + (ci * p.H + h) * ssz;
+        const float* const Sout = ga.keep_d + (ci * p.H + h) * ssz;
+        for (int i = tid; i < W * C; i += 64 * W) (&pg[0][0])[i] = 0.0f;
+        if (wave == W - 1) {
+            const int64_t t = c0 + lane;
+            const bool on = lane < C && t < hi;
+            const double s = sum_decays(on ? p.g[t * p.sg + h] : 0.0f, lane < C), end = lane_f64(s, C - 1);
+            if (lane < C) put_steps<C>(st, s, end, on ? p.beta[t * p.H + h] : 0.0f, p.least, lane);
         }
-    };
-    const auto ask_state = [&](const Rsrc& w, u32x4 (&n)[NC][2], int c) {
+        const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+        f32x4 aq[NC][IT], az[NC][IT], au[NC][IT], ap[MT], an[MT];
 #pragma unroll
-        for (int k = 0; k < NC; ++k)
+        for (int c = 0; c < NC; ++c)
 #pragma unroll
-            for (int x = 0; x < 2; ++x)   // rows it does not have lie behind the window
-                n[k][x] = four(w, uint32_t(16 * (wave + W * k) + l16) * uint32_t(p.dv * 4), c + 8 * g4 + 4 * x);
-    };
-    const auto f4 = [](const u32x4& x) { return __builtin_bit_cast(f32x4, x); };
-    float s_zu = 0.0f, s_vz = 0.0f;
-    double cross = 0.0;
-    ask(0);
-    ask_state(ws, ns, 0);
-    ask_state(wd, nd, 0);
-    const uint32_t b32 = row_base<32>(lane);
-    for (int c = 0; c < p.dv; c += 32) {
-        if (mine) {
+            for (int i = 0; i < IT; ++i) aq[c][i] = az[c][i] = au[c][i] = zero;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) ap[m] = an[m] = zero;
+        const auto tile = [](int m, int& it, int& jt) {
+            it = m < 1 ? 0 : m < 3 ? 1 : m < 6 ? 2 : 3;
+            jt = m - it * (it + 1) / 2;
+        };
+        // rows of a step: 4 or 8 threads a token
+        const int ts = tid / (32 / CPT), cs = CPT * (tid % (32 / CPT));
+        const bool mine = ts < C, here = mine && c0 + ts < hi;
+        const bool vec = p.dv % 4 == 0;
+        const IO* const vrow = static_cast<const IO*>(p.v) + (c0 + ts) * p.sv + int64_t(h) * p.dv;
+        const IO* const orow = static_cast<const IO*>(ga.dout) + (c0 + ts) * ga.so + int64_t(h) * p.dv;
+        u32x4 nu[N4], nz[N4], ns[NC][2], nd[NC][2];
+        Raw4<IO> nv[N4], no[N4];
+        const Rsrc wu = rows_rsrc(reinterpret_cast<char*>(p.rows + (c0 * p.H + h) * p.dv), int64_t(p.H) * p.dv * 4, hi - c0, C);
+        const Rsrc wz = rows_rsrc(const_cast<char*>(reinterpret_cast<const char*>(ga.z + (c0 * p.H + h) * p.dv)), int64_t(p.H) * p.dv * 4, hi - c0, C);
+        const Rsrc ws = rows_rsrc(const_cast<char*>(reinterpret_cast<const char*>(Sin)), ssz * 4, 1, 1);
+        const Rsrc wd = rows_rsrc(const_cast<char*>(reinterpret_cast<const char*>(Sout)), ssz * 4, 1, 1);
+        // four values at column c of a row of v that begins at byte `row` of a window
+        const auto four = [&](const Rsrc& w, uint32_t row, int c) {
+            if (vec) return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(w, c < p.dv ? row + 4 * c : kPast, 0, 0));
+            u32x4 x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = __builtin_amdgcn_raw_buffer_load_b32(w, c + e < p.dv ? row + 4 * (c + e) : kPast, 0, 0);
+            return x;
+        };
+        const uint32_t trow = mine ? uint32_t(ts) * uint32_t(p.H * p.dv * 4) : kPast;
+        const auto ask = [&](int c) {
 #pragma unroll
             for (int x = 0; x < N4; ++x) {
-                const f32x4 u = f4(nu[x]), z = f4(nz[x]), v = nv[x].values();
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    s_zu = fmaf(z[e], u[e], s_zu);
-                    s_vz = fmaf(v[e], z[e], s_vz);
-                }
-                // rows lie in tiles of 16 x 32, part by part
-                const int cc = cs + 4 * x, to = (ts >> 4) * 512 + at_piece<32>(ts & 15, cc >> 3) + (cc & 4);
-                const auto put = [&](uint16_t* at, const f32x4& x, auto parts) {
-                    constexpr int N = decltype(parts)::value;
-                    uint32_t a[N], b[N];
-                    split<N>(x[0], x[1], a);
-                    split<N>(x[2], x[3], b);
-#pragma unroll
-                    for (int k = 0; k < N; ++k) *reinterpret_cast<uint2*>(at + k * C * 32 + to) = uint2{a[k], b[k]};
-                };
-                put(Us, u, std::integral_constant<int, WP>{});
-                put(Zs, z, std::integral_constant<int, WP>{});
-                put(Os, no[x].values(), std::integral_constant<int, PARTS>{});
+                nu[x] = four(wu, trow, c + cs + 4 * x);
+                nz[x] = four(wz, trow, c + cs + 4 * x);
+                nv[x].load(vrow, here, c + cs + 4 * x, p.dv, p.wide);
+                no[x].load(orow, here, c + cs + 4 * x, p.dv, p.wide);
             }
-        }
-        u32x4 sp[NC][WP];
+        };
+        const auto ask_state = [&](const Rsrc& w, u32x4 (&n)[NC][2], int c) {
 #pragma unroll
-        for (int n = 0; n < NC; ++n) {
+            for (int k = 0; k < NC; ++k)
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+                for (int x = 0; x < 2; ++x)   // rows it does not have lie behind the window
+                    n[k][x] = four(w, uint32_t(16 * (wave + W * k) + l16) * uint32_t(p.dv * 4), c + 8 * g4 + 4 * x);
+        };
+        const auto f4 = [](const u32x4& x) { return __builtin_bit_cast(f32x4, x); };
+        float s_zu = 0.0f, s_vz = 0.0f;
+        double cross = 0.0;
+        ask(0);
+        ask_state(ws, ns, 0);
+        ask_state(wd, nd, 0);
+        const uint32_t b32 = row_base<32>(lane);
+        for (int c = 0; c < p.dv; c += 32) {
+            if (mine) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) cross = fma(double(f4(ns[n][x])[e]), double(f4(nd[n][x])[e]), cross);
-            pair_parts<WP>(f4(ns[n][0]), f4(ns[n][1]), sp[n]);
-        }
-        lds_barrier();
-        const bool more = c + 32 < p.dv;
-        if (more) ask(c + 32);
-        // one state after the other: both in parts would not fit the registers
+                for (int x = 0; x < N4; ++x) {
+                    const f32x4 u = f4(nu[x]), z = f4(nz[x]), v = nv[x].values();
 #pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            u32x4 o[PARTS], z[WP];
+                    for (int e = 0; e < 4; ++e) {
+                        s_zu = fmaf(z[e], u[e], s_zu);
+                        s_vz = fmaf(v[e], z[e], s_vz);
+                    }
+                    // rows lie in tiles of 16 x 32, part by part
+                    const int cc = cs + 4 * x, to = (ts >> 4) * 512 + at_piece<32>(ts & 15, cc >> 3) + (cc & 4);
+                    const auto put = [&](uint16_t* at, const f32x4& x, auto parts) {
+                        constexpr int N = decltype(parts)::value;
+                        uint32_t a[N], b[N];
+                        split<N>(x[0], x[1], a);
+                        split<N>(x[2], x[3], b);
 #pragma unroll
-            for (int k = 0; k < PARTS; ++k) o[k] = row_op<32>(Os + k * C * 32 + 512 * i, 0, 0, b32);
-#pragma unroll
-            for (int k = 0; k < WP; ++k) z[k] = row_op<32>(Zs + k * C * 32 + 512 * i, 0, 0, b32);
+                        for (int k = 0; k < N; ++k) *reinterpret_cast<uint2*>(at + k * C * 32 + to) = uint2{a[k], b[k]};
+                    };
+                    put(Us, u, std::integral_constant<int, WP>{});
+                    put(Zs, z, std::integral_constant<int, WP>{});
+                    put(Os, no[x].values(), std::integral_constant<int, PARTS>{});
+                }
+            }
+            u32x4 sp[NC][WP];
 #pragma unroll
             for (int n = 0; n < NC; ++n) {
-                aq[n][i] = mma_parts<PARTS, WP>(o, sp[n], aq[n][i]);
-                az[n][i] = mma_parts<WP, WP>(z, sp[n], az[n][i]);
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) cross = fma(double(f4(ns[n][x])[e]), double(f4(nd[n][x])[e]), cross);
+                pair_parts<WP>(f4(ns[n][0]), f4(ns[n][1]), sp[n]);
             }
-            __builtin_amdgcn_sched_barrier(0);   // operands read further ahead would not fit either
+            lds_barrier();
+            const bool more = c + 32 < p.dv;
+            if (more) ask(c + 32);
+            // one state after the other: both in parts would not fit the registers
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                u32x4 o[PARTS], z[WP];
+#pragma unroll
+                for (int k = 0; k < PARTS; ++k) o[k] = row_op<32>(Os + k * C * 32 + 512 * i, 0, 0, b32);
+#pragma unroll
+                for (int k = 0; k < WP; ++k) z[k] = row_op<32>(Zs + k * C * 32 + 512 * i, 0, 0, b32);
+#pragma unroll
+                for (int n = 0; n < NC; ++n) {
+                    aq[n][i] = mma_parts<PARTS, WP>(o, sp[n], aq[n][i]);
+                    az[n][i] = mma_parts<WP, WP>(z, sp[n], az[n][i]);
+                }
+                __builtin_amdgcn_sched_barrier(0);   // operands read further ahead would not fit either
+            }
+#pragma unroll
+            for (int n = 0; n < NC; ++n) pair_parts<WP>(f4(nd[n][0]), f4(nd[n][1]), sp[n]);
+            if (more) ask_state(ws, ns, c + 32);
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                u32x4 u[WP];
+#pragma unroll
+                for (int k = 0; k < WP; ++k) u[k] = row_op<32>(Us + k * C * 32 + 512 * i, 0, 0, b32);
+#pragma unroll
+                for (int n = 0; n < NC; ++n) au[n][i] = mma_parts<WP, WP>(u, sp[n], au[n][i]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if (more) ask_state(wd, nd, c + 32);
+#pragma unroll
+            for (int mm = 0; mm < MT; ++mm) {
+                const int m = wave + W * mm;
+                if (m >= NTILE) break;
+                int it, jt;
+                tile(m, it, jt);
+                u32x4 o[PARTS], u[WP], z[WP];
+#pragma unroll
+                for (int k = 0; k < PARTS; ++k) o[k] = row_op<32>(Os + k * C * 32 + 512 * it, 0, 0, b32);
+#pragma unroll
+                for (int k = 0; k < WP; ++k) {
+                    u[k] = row_op<32>(Us + k * C * 32 + 512 * jt, 0, 0, b32);
+                    z[k] = row_op<32>(Zs + k * C * 32 + 512 * it, 0, 0, b32);
+                }
+                ap[mm] = mma_parts<WP, PARTS>(u, o, ap[mm]);
+                an[mm] = mma_parts<WP, WP>(u, z, an[mm]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            lds_barrier();
         }
-#pragma unroll
-        for (int n = 0; n < NC; ++n) pair_parts<WP>(f4(nd[n][0]), f4(nd[n][1]), sp[n]);
-        if (more) ask_state(ws, ns, c + 32);
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            u32x4 u[WP];
-#pragma unroll
-            for (int k = 0; k < WP; ++k) u[k] = row_op<32>(Us + k * C * 32 + 512 * i, 0, 0, b32);
-#pragma unroll
-            for (int n = 0; n < NC; ++n) au[n][i] = mma_parts<WP, WP>(u, sp[n], au[n][i]);
-            __builtin_amdgcn_sched_barrier(0);
+        s_zu = CPT == 8 ? sum4(s_zu) : sum8(s_zu);
+        s_vz = CPT == 8 ? sum4(s_vz) : sum8(s_vz);
+        if (mine && cs == 0) {
+            zu[ts] = s_zu;
+            vz[ts] = s_vz;
         }
-        if (more) ask_state(wd, nd, c + 32);
+        cross *= double(st.tail[0]);
+        wait_memory<0>();
+        __syncthreads();        // q and k are there
+        // ---------------------------------------- D and N, tiles on and below the diagonal
+        uint16_t* const Ds = buf;
+        uint16_t* const Ns = buf + TRI;
+        const uint32_t base = row_base<KD>(lane);
 #pragma unroll
         for (int mm = 0; mm < MT; ++mm) {
             const int m = wave + W * mm;
             if (m >= NTILE) break;
             int it, jt;
             tile(m, it, jt);
-            u32x4 o[PARTS], u[WP], z[WP];
+            const int i = 16 * it + l16, j0 = 16 * jt + 4 * g4;
+            const float gi = st.hi[i], ei = st.lo[i], b = st.beta[i];
+            f32x4 d, n;
 #pragma unroll
-            for (int k = 0; k < PARTS; ++k) o[k] = row_op<32>(Os + k * C * 32 + 512 * it, 0, 0, b32);
+            for (int r = 0; r < 4; ++r) {
+                const float e = __builtin_amdgcn_exp2f((gi - st.hi[j0 + r]) + (ei - st.lo[j0 + r]));
+                d[r] = j0 + r <= i ? ap[mm][r] * (e * p.scale) : 0.0f;
+                n[r] = j0 + r < i ? -b * (an[mm][r] * e) : 0.0f;
+            }
+            const int o = p_block(it, jt >> 1) * 512 + 4 * (g4 & 1);
+            const int at = o + at_piece<32>(l16, 2 * (jt & 1) + (g4 >> 1)), above = o + at_piece<32>(l16, 2 + (g4 >> 1));
+            uint32_t x[WP], y[WP], u[WP], v[WP];
+            split<WP>(d[0], d[1], x);
+            split<WP>(d[2], d[3], y);
+            split<WP>(n[0], n[1], u);
+            split<WP>(n[2], n[3], v);
 #pragma unroll
             for (int k = 0; k < WP; ++k) {
-                u[k] = row_op<32>(Us + k * C * 32 + 512 * jt, 0, 0, b32);
-                z[k] = row_op<32>(Zs + k * C * 32 + 512 * it, 0, 0, b32);
-            }
-            ap[mm] = mma_parts<WP, PARTS>(u, o, ap[mm]);
-            an[mm] = mma_parts<WP, WP>(u, z, an[mm]);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        lds_barrier();
-    }
-    s_zu = CPT == 8 ? sum4(s_zu) : sum8(s_zu);
-    s_vz = CPT == 8 ? sum4(s_vz) : sum8(s_vz);
-    if (mine && cs == 0) {
-        zu[ts] = s_zu;
-        vz[ts] = s_vz;
-    }
-    cross *= double(st.tail[0]);
-    wait_memory<0>();
-    __syncthreads();        // q and k are there
-    // ---------------------------------------- D and N, tiles on and below the diagonal
-    uint16_t* const Ds = buf;
-    uint16_t* const Ns = buf + TRI;
-    const uint32_t base = row_base<KD>(lane);
-#pragma unroll
-    for (int mm = 0; mm < MT; ++mm) {
-        const int m = wave + W * mm;
-        if (m >= NTILE) break;
-        int it, jt;
-        tile(m, it, jt);
-        const int i = 16 * it + l16, j0 = 16 * jt + 4 * g4;
-        const float gi = st.hi[i], ei = st.lo[i], b = st.beta[i];
-        f32x4 d, n;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const float e = __builtin_amdgcn_exp2f((gi - st.hi[j0 + r]) + (ei - st.lo[j0 + r]));
-            d[r] = j0 + r <= i ? ap[mm][r] * (e * p.scale) : 0.0f;
-            n[r] = j0 + r < i ? -b * (an[mm][r] * e) : 0.0f;
-        }
-        const int o = p_block(it, jt >> 1) * 512 + 4 * (g4 & 1);
-        const int at = o + at_piece<32>(l16, 2 * (jt & 1) + (g4 >> 1)), above = o + at_piece<32>(l16, 2 + (g4 >> 1));
-        uint32_t x[WP], y[WP], u[WP], v[WP];
-        split<WP>(d[0], d[1], x);
-        split<WP>(d[2], d[3], y);
-        split<WP>(n[0], n[1], u);
-        split<WP>(n[2], n[3], v);
-#pragma unroll
-        for (int k = 0; k < WP; ++k) {
-            *reinterpret_cast<uint2*>(Ds + k * PB + at) = uint2{x[k], y[k]};
-            *reinterpret_cast<uint2*>(Ns + k * PB + at) = uint2{u[k], v[k]};
-            if (it == jt && (it & 1) == 0) {   // the tile above the diagonal that shares this block
-                *reinterpret_cast<uint2*>(Ds + k * PB + above) = uint2{0, 0};
-                *reinterpret_cast<uint2*>(Ns + k * PB + above) = uint2{0, 0};
-            }
-        }
-    }
-    __syncthreads();
-    // ---------------------------------------- dq and dk of this wave's columns
-    const auto element = [&](const uint16_t* t, int r, int col) {
-        const int o = at_piece<KD>(r, col >> 3) + (col & 7);
-        float x = 0.0f;
-#pragma unroll
-        for (int w = PARTS - 1; w >= 0; --w) x += __uint_as_float(uint32_t(t[w * C * KD + o]) << 16);
-        return x;
-    };
-    {
-        const int oe = PARTS > 1 || ga.wide_out ? 4 : 2;
-        const int64_t pitch = ga.sdq * oe, at = c0 * pitch + int64_t(ga.wide_out ? h : h / p.rep) * p.dk * oe;
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            const int i0 = 16 * (wave + W * c);
-            if (i0 >= p.dk) continue;
-#pragma unroll
-            for (int i = 0; i < IT; ++i) {
-                const int t0 = 16 * i + 4 * g4;
-                const f32x4 e = *reinterpret_cast<const f32x4*>(&st.in[t0]), f = *reinterpret_cast<const f32x4*>(&st.bin[t0]);
-                const f32x4 l = *reinterpret_cast<const f32x4*>(&st.out[t0]);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    aq[c][i][r] *= e[r] * p.scale;
-                    au[c][i][r] *= l[r];
-                    // u_j . dS_out^T k_j of the tokens
-                    cross = fma(double(au[c][i][r]), double(element(K, t0 + r, i0 + l16)), cross);
-                    au[c][i][r] = fmaf(-f[r], az[c][i][r], au[c][i][r]);
+                *reinterpret_cast<uint2*>(Ds + k * PB + at) = uint2{x[k], y[k]};
+                *reinterpret_cast<uint2*>(Ns + k * PB + at) = uint2{u[k], v[k]};
+                if (it == jt && (it & 1) == 0) {   // the tile above the diagonal that shares this block
+                    *reinterpret_cast<uint2*>(Ds + k * PB + above) = uint2{0, 0};
+                    *reinterpret_cast<uint2*>(Ns + k * PB + above) = uint2{0, 0};
                 }
             }
-            const uint32_t bc = col_base<KD, 0>(i0, lane);
-            u32x4 k[JB][PARTS], q[JB][PARTS];
+        }
+        __syncthreads();
+        // ---------------------------------------- dq and dk of this wave's columns
+        const auto element = [&](const uint16_t* t, int r, int col) {
+            const int o = at_piece<KD>(r, col >> 3) + (col & 7);
+            float x = 0.0f;
 #pragma unroll
-            for (int jb = 0; jb < JB; ++jb)
+            for (int w = PARTS - 1; w >= 0; --w) x += __uint_as_float(uint32_t(t[w * C * KD + o]) << 16);
+            return x;
+        };
+        {
+            // a head of those that share q and k adds to the sum of the ones before it, or stands alone
+            const bool sum = h > h0, wide = PARTS > 1 || ga.wide_out || h + 1 < h0 + ga.heads;
+            const int64_t row0 = c0 * ga.sdq + int64_t(ga.wide_out ? h : hk) * p.dk, pitch4 = ga.sdq * 4;
+            float *const tq = ga.sum_q + row0, *const tk = ga.sum_k + row0;
+            const int oe = wide ? 4 : 2;
+            const int64_t pitch = ga.sdq * oe;
+            char* const to_q = wide ? reinterpret_cast<char*>(tq) : static_cast<char*>(ga.dq) + row0 * oe;
+            char* const to_k = wide ? reinterpret_cast<char*>(tk) : static_cast<char*>(ga.dk) + row0 * oe;
 #pragma unroll
-                for (int i = 0; i < PARTS; ++i) {
-                    k[jb][i] = col_op<KD>(K + i * C * KD, 32 * jb, 0, 0, bc);
-                    q[jb][i] = col_op<KD>(Q + i * C * KD, 32 * jb, 0, 0, bc);
-                }
+            for (int c = 0; c < NC; ++c) {
+                const int i0 = 16 * (wave + W * c);
+                if (i0 >= p.dk) continue;
 #pragma unroll
-            for (int i = 0; i < IT; ++i)
+                for (int i = 0; i < IT; ++i) {
+                    const int t0 = 16 * i + 4 * g4;
+                    const f32x4 e = *reinterpret_cast<const f32x4*>(&st.in[t0]), f = *reinterpret_cast<const f32x4*>(&st.bin[t0]);
+                    const f32x4 l = *reinterpret_cast<const f32x4*>(&st.out[t0]);
 #pragma unroll
-                for (int jb = 0; jb < JB; ++jb) {
-                    u32x4 a[WP];
-                    if (jb <= i / 2) {
-#pragma unroll
-                        for (int w = 0; w < WP; ++w) a[w] = row_op<32>(Ds + w * PB + p_block(i, jb) * 512, 0, 0, b32);
-                        aq[c][i] = mma_parts<WP, PARTS>(a, k[jb], aq[c][i]);
-#pragma unroll
-                        for (int w = 0; w < WP; ++w) a[w] = row_op<32>(Ns + w * PB + p_block(i, jb) * 512, 0, 0, b32);
-                        au[c][i] = mma_parts<WP, PARTS>(a, k[jb], au[c][i]);
-                    }
-                    if (jb >= i / 2) {
-#pragma unroll
-                        for (int w = 0; w < WP; ++w) a[w] = block_t_op<C>(Ds + w * PB, jb, i, lane);
-                        au[c][i] = mma_parts<WP, PARTS>(a, q[jb], au[c][i]);
-#pragma unroll
-                        for (int w = 0; w < WP; ++w) a[w] = block_t_op<C>(Ns + w * PB, jb, i, lane);
-                        au[c][i] = mma_parts<WP, PARTS>(a, k[jb], au[c][i]);
+                    for (int r = 0; r < 4; ++r) {
+                        aq[c][i][r] *= e[r] * p.scale;
+                        au[c][i][r] *= l[r];
+                        // u_j . dS_out^T k_j of the tokens
+                        cross = fma(double(au[c][i][r]), double(element(K, t0 + r, i0 + l16)), cross);
+                        au[c][i][r] = fmaf(-f[r], az[c][i][r], au[c][i][r]);
                     }
                 }
-            store_tiles<C, false>(aq[c], static_cast<char*>(ga.dq) + at, pitch, hi - c0, i0, p.dk, oe == 4, ga.pairs_k, lane);
-            store_tiles<C, false>(au[c], static_cast<char*>(ga.dk) + at, pitch, hi - c0, i0, p.dk, oe == 4, ga.pairs_k, lane);
-            // o . do = q . dq of each token
+                const uint32_t bc = col_base<KD, 0>(i0, lane);
+                u32x4 k[JB][PARTS], q[JB][PARTS];
 #pragma unroll
-            for (int i = 0; i < IT; ++i)
+                for (int jb = 0; jb < JB; ++jb)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int t = 16 * i + 4 * g4 + r;
-                    const float s = sum16(element(Q, t, i0 + l16) * aq[c][i][r]);
-                    if (l16 == 0) pg[wave][t] += s;
+                    for (int i = 0; i < PARTS; ++i) {
+                        k[jb][i] = col_op<KD>(K + i * C * KD, 32 * jb, 0, 0, bc);
+                        q[jb][i] = col_op<KD>(Q + i * C * KD, 32 * jb, 0, 0, bc);
+                    }
+#pragma unroll
+                for (int i = 0; i < IT; ++i)
+#pragma unroll
+                    for (int jb = 0; jb < JB; ++jb) {
+                        u32x4 a[WP];
+                        if (jb <= i / 2) {
+#pragma unroll
+                            for (int w = 0; w < WP; ++w) a[w] = row_op<32>(Ds + w * PB + p_block(i, jb) * 512, 0, 0, b32);
+                            aq[c][i] = mma_parts<WP, PARTS>(a, k[jb], aq[c][i]);
+#pragma unroll
+                            for (int w = 0; w < WP; ++w) a[w] = row_op<32>(Ns + w * PB + p_block(i, jb) * 512, 0, 0, b32);
+                            au[c][i] = mma_parts<WP, PARTS>(a, k[jb], au[c][i]);
+                        }
+                        if (jb >= i / 2) {
+#pragma unroll
+                            for (int w = 0; w < WP; ++w) a[w] = block_t_op<C>(Ds + w * PB, jb, i, lane);
+                            au[c][i] = mma_parts<WP, PARTS>(a, q[jb], au[c][i]);
+#pragma unroll
+                            for (int w = 0; w < WP; ++w) a[w] = block_t_op<C>(Ns + w * PB, jb, i, lane);
+                            au[c][i] = mma_parts<WP, PARTS>(a, k[jb], au[c][i]);
+                        }
+                    }
+                // o . do = q . dq of each token
+#pragma unroll
+                for (int i = 0; i < IT; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int t = 16 * i + 4 * g4 + r;
+                        const float s = sum16(element(Q, t, i0 + l16) * aq[c][i][r]);
+                        if (l16 == 0) pg[wave][t] += s;
+                    }
+                if (sum) {
+                    add_tiles<C>(aq[c], tq, pitch4, hi - c0, i0, p.dk, lane);
+                    add_tiles<C>(au[c], tk, pitch4, hi - c0, i0, p.dk, lane);
                 }
-        }
-    }
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) cross += __shfl_xor(cross, d);
-    if (lane == 0) ps[wave] = cross;
-    __syncthreads();
-    if (wave == 0) {
-        double x = 0.0, end = 0.0;
-        const int64_t t = c0 + lane;
-        const bool on = lane < C && t < hi;
-        if (lane < C) {
-            x = -double(st.beta[lane] * vz[lane]);
-#pragma unroll
-            for (int k = 0; k < W; ++k) x += double(pg[k][lane]);
+                store_tiles<C, false>(aq[c], to_q, pitch, hi - c0, i0, p.dk, wide, ga.pairs_k, lane);
+                store_tiles<C, false>(au[c], to_k, pitch, hi - c0, i0, p.dk, wide, ga.pairs_k, lane);
+            }
         }
 #pragma unroll
-        for (int k = 0; k < W; ++k) end += ps[k];
-        const double s = scan_f64(x);                       // of the tokens up to this one
-        const double dg = end + (lane_f64(s, 63) - s) + x;
-        if (on) {
-            ga.dbeta[t * p.H + h] = zu[lane] / st.beta[lane];     // Z . r = Z . U / beta
-            if (!ga.part) ga.dg[t * p.H + h] = float(dg);
-        }
-        if (ga.part) {
-            const double all = lane_f64(scan_f64(on ? dg : 0.0), 63);
-            if (lane == 0) ga.part[ci * p.H + h] = all;
+        for (int d = 1; d < 64; d <<= 1) cross += __shfl_xor(cross, d);
+        if (lane == 0) ps[wave] = cross;
+        __syncthreads();
+        if (wave == 0) {
+            double x = 0.0, end = 0.0;
+            const int64_t t = c0 + lane;
+            const bool on = lane < C && t < hi;
+            if (lane < C) {
+                x = -double(st.beta[lane] * vz[lane]);
+#pragma unroll
+                for (int k = 0; k < W; ++k) x += double(pg[k][lane]);
+            }
+#pragma unroll
+            for (int k = 0; k < W; ++k) end += ps[k];
+            const double s = scan_f64(x);                       // of the tokens up to this one
+            const double dg = end + (lane_f64(s, 63) - s) + x;
+            if (on) {
+                ga.dbeta[t * p.H + h] = zu[lane] / st.beta[lane];     // Z . r = Z . U / beta
+                if (!ga.part) ga.dg[t * p.H + h] = float(dg);
+            }
+            if (ga.part) {
+                const double all = lane_f64(scan_f64(on ? dg : 0.0), 63);
+                if (lane == 0) ga.part[ci * p.H + h] = all;
+            }
         }
     }
 }
@@ -513,7 +547,7 @@ __global__ void __launch_bounds__(kThreads) delta_zero_kernel(DeltaPass p, ZeroR
 
 // ---------------------------------------------------------------- host
 struct GradPlan {
-    int chunk;
+    int chunk, heads;   // heads of a workgroup over a chunk's gradients
     int64_t nchunks, piece, npieces;
     bool pieced;
     size_t tri, steps, keep, rows, carry, trans, part, wide;   // bytes of one buffer each
@@ -555,7 +589,12 @@ inline int make_grad_plan(const ssm_linattn_dims* d, bool packed, GradPlan* pl) 
     pl->carry = pl->pieced ? up256(np * state) : 0;
     pl->trans = pl->pieced ? up256(np * static_cast<size_t>(d->dk * d->dk) * 4) : 0;
     pl->part = d->head_decay ? up256(nk * 8) : 0;
-    pl->wide = d->nheads > d->kheads ? up256(static_cast<size_t>(d->tokens * d->nheads * d->dk) * 4) : 0;
+    // Heads that share q and k go one after the other where the chunks fill the card without them,
+    // and else leave their gradients to be summed.  Measured, us: XX
+    const bool shared = d->nheads > d->kheads, in_turn = shared && pl->nchunks * d->kheads >= 4 * kCus;
+    pl->heads = in_turn ? static_cast<int>(d->nheads / d->kheads) : 1;
+    const size_t wide = shared && !in_turn ? d->nheads : in_turn && d->io_dtype == SSM_BF16 ? d->kheads : 0;
+    pl->wide = up256(static_cast<size_t>(d->tokens * d->dk) * wide * 4);
     pl->bytes = pl->tri + pl->steps + 2 * (pl->keep + pl->rows + pl->carry + pl->trans + pl->wide) + pl->part;
     return SSM_OK;
 }
@@ -576,7 +615,7 @@ template <int MODE> void run_walks(const DeltaPass& f, const DeltaPass& r, bool 
 }
 
 inline void run_grad(const GradArgs& a, bool f32, int64_t nchunks, hipStream_t s) {
-    const dim3 grid(static_cast<uint32_t>(nchunks), a.p.H);
+    const dim3 grid(static_cast<uint32_t>(nchunks), a.p.H / a.heads);
 #define SSM_GRAD(K, W)                                                                              \
     do {                                                                                            \
         if (f32) launch_kernel(delta_grad_kernel<3, K, 32, W>, grid, dim3(64 * W), 0, s, a);        \
@@ -687,10 +726,14 @@ int ssm_delta_bwd(const void* q, const void* k, const void* v, const float* g, c
     r.rows = rows_z; r.dv_out = gr.dv; r.pairs = pair_rows(gr.dv, wv, d.dv);
     GradArgs a = {};
     a.p = f; a.dout = dout; a.keep_d = keep_d; a.z = rows_z; a.so = z.o;
-    a.dq = shared ? static_cast<void*>(wq) : gr.dq; a.dk = shared ? static_cast<void*>(wkk) : gr.dk;
+    a.heads = pl.heads; a.wide_out = shared && pl.heads == 1;
+    a.dq = gr.dq; a.dk = gr.dk;
+    // float32 sums stand where they belong; those of bf16 gradients, and each head's, in the workspace
+    a.sum_q = f32 && !a.wide_out ? static_cast<float*>(gr.dq) : wq;
+    a.sum_k = f32 && !a.wide_out ? static_cast<float*>(gr.dk) : wkk;
     a.dbeta = gr.dbeta; a.dg = gr.dg; a.part = d.head_decay ? part : nullptr;
-    a.sdq = d.nheads * d.dk; a.wide_out = shared;
-    a.pairs_k = !shared && pair_rows(gr.dq, a.sdq, d.dk) && pair_rows(gr.dk, a.sdq, d.dk);
+    a.sdq = (a.wide_out ? d.nheads : d.kheads) * d.dk;
+    a.pairs_k = pair_rows(gr.dq, a.sdq, d.dk) && pair_rows(gr.dk, a.sdq, d.dk);
 
     hipStream_t s = static_cast<hipStream_t>(stream);
     launch_error = hipSuccess;
@@ -701,7 +744,7 @@ int ssm_delta_bwd(const void* q, const void* k, const void* v, const float* g, c
     }
     run_walks<kDeltaKeep>(f, r, f32, s);
     run_grad(a, f32, pl.nchunks, s);
-    if (shared) {
+    if (a.wide_out) {
         const FoldArgs fa = {{wq, wkk}, {gr.dq, gr.dk}, d.tokens * d.kheads, f.rep, f.dk};
         const bool v4 = d.dk % 4 == 0 && !misaligned(gr.dq, 4 * z.e) && !misaligned(gr.dk, 4 * z.e);
         if (f32) run_fold<float>(fa, v4, s);

@@ -575,6 +575,25 @@ def test_many_short_sequences():
     check_grads(c, r)
 
 
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("decay", ["token", "head"])
+@pytest.mark.parametrize("heads,kheads,dk,dv", [(6, 2, 40, 24), (8, 2, 128, 33), (4, 2, 200, 64)])
+def test_shared_heads_of_many_chunks(heads, kheads, dk, dv, decay, io):
+    """Enough chunks that the heads which share q and k go one after the other in the gradients."""
+    import torch
+    import selective_state_space_79_amd as ssm
+
+    announce(f"delta shared heads of many chunks {heads} {kheads} {dk} {dv} {decay} {io}")
+    rng = np.random.default_rng(21)
+    lens = [70, 0, 33] + [int(x) for x in rng.integers(0, 3, 600)]
+    c = Case(lens, heads, kheads, dk, dv, io, decay, seed=heads)
+    r = ssm.delta_bwd(*c.rows(), do=c.do, scale=c.scale, cu_seqlens=c.cu, s0=c.s0, ds_last=c.ds_last)
+    again = ssm.delta_bwd(*c.rows(), do=c.do, scale=c.scale, cu_seqlens=c.cu, s0=c.s0, ds_last=c.ds_last)
+    torch.cuda.synchronize()
+    check_grads(c, r)
+    assert all(torch.equal(r[n], again[n]) for n in r)
+
+
 def test_offsets_past_32_bits():
     """Rows and states behind the first 2^31 elements: bitwise the results of a call of their own."""
     import torch
