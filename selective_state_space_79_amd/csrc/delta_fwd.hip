@@ -166,15 +166,16 @@ __global__ void __launch_bounds__(kThreads, pass_waves(KD, PARTS, MODE)) delta_p
 }
 
 // ---------------------------------------------------------------- pieces' starting states
-// Walks the pieces of one sequence and head for 128 columns of the state, 16 a wave: each piece's
+// Walks the pieces of one sequence and head for 64 columns of the state (128 with keys over 128:
+// registers), 16 a wave: each piece's
 // own end state N is replaced by the state S it starts from, and the next one starts from W S + N
 // with the piece's transition W (against time its transpose).  W does not depend on what came
 // before, so its rows are asked for four tiles of 16 ahead, and all waves share their split.
-constexpr int kCarryThreads = 512, kCarryCols = 128;
+constexpr int carry_threads(int KD) { return KD == 256 ? 512 : 256; }
 
 template <int KD, bool REV>
 __device__ __forceinline__ void carry_walk(const DeltaPass& p, int h, uint16_t (&Ws)[2][3 * 16 * KD]) {
-    constexpr int KB = KD / 32, WP = 3, VPT = KD / 32, AHEAD = 4;   // values of a tile a thread brings
+    constexpr int KB = KD / 32, WP = 3, TPR = carry_threads(KD) / 16, VPT = KD / TPR, AHEAD = 4;   // threads of a tile's row, values of each
     const int tid = threadIdx.x, lane = tid & 63, g4 = lane >> 4, l16 = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int seq = blockIdx.z;
@@ -185,13 +186,13 @@ __device__ __forceinline__ void carry_walk(const DeltaPass& p, int h, uint16_t (
     int64_t n = (sq.end - sq.start + p.piece - 1) / p.piece;
     if (n < 2) return;   // a single piece starts from the user's state
     if (base + n > p.npieces) n = p.npieces - base;
-    const int c_wave = blockIdx.x * kCarryCols + 16 * wave;
+    const int c_wave = blockIdx.x * (carry_threads(KD) / 4) + 16 * wave;
     const int64_t ssz = int64_t(p.dk) * p.dv, tsz = int64_t(p.dk) * p.dk;
     const auto number = [&](int64_t k) { return (base + (REV ? n - 1 - k : k)) * p.H + h; };
     f32x4 S[2 * KB];
     load_state<KB>(S, p.s_in ? p.s_in + (int64_t(slot) * p.H + h) * ssz : nullptr, p.dk, p.dv, c_wave, lane);
     // tile m of the rows of piece k's transition: row ti in the order of the state's tiles
-    const int ti = tid >> 5, tc = (tid & 31) * VPT, to = at_piece<KD>(ti, tc >> 3) + (tc & 7);
+    const int ti = tid / TPR, tc = tid % TPR * VPT, to = at_piece<KD>(ti, tc >> 3) + (tc & 7);
     float ahead[AHEAD][VPT];
     const auto ask = [&](int64_t k, int m, float (&x)[VPT]) {
         const int out = 32 * (m >> 1) + 8 * (ti >> 2) + 4 * (m & 1) + (ti & 3);
@@ -246,7 +247,7 @@ __device__ __forceinline__ void carry_walk(const DeltaPass& p, int h, uint16_t (
 
 // The heads of p and, of the gradients, those of r behind them.
 template <int KD, bool GRADS>
-__global__ void __launch_bounds__(kCarryThreads) delta_carry_kernel(DeltaPass p, DeltaPass r) {
+__global__ void __launch_bounds__(carry_threads(KD)) delta_carry_kernel(DeltaPass p, DeltaPass r) {
     __shared__ __align__(16) uint16_t Ws[2][3 * 16 * KD];
     const int h = blockIdx.y;
     if (!GRADS || h < p.H) carry_walk<KD, false>(p, h, Ws);
@@ -439,9 +440,10 @@ void ssm_detail::launch_delta_tri(const DeltaPass& p, bool f32, int64_t nchunks,
 }
 
 void ssm_detail::launch_delta_carry(const DeltaPass& p, const DeltaPass* r, hipStream_t s) {
-    const dim3 grid(static_cast<uint32_t>(cdiv(p.dv, dl::kCarryCols)), r ? 2 * p.H : p.H, p.nseq), block(dl::kCarryThreads);
 #define SSM_CARRY(K)                                                                        \
     do {                                                                                    \
+        const dim3 block(dl::carry_threads(K)),                                             \
+            grid(static_cast<uint32_t>(cdiv(p.dv, block.x / 4)), r ? 2 * p.H : p.H, p.nseq); \
         if (r) launch_kernel(dl::delta_carry_kernel<K, true>, grid, block, 0, s, p, *r);    \
         else launch_kernel(dl::delta_carry_kernel<K, false>, grid, block, 0, s, p, p);      \
     } while (0)
