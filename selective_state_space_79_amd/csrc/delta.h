@@ -23,6 +23,7 @@
 // the next one's operand as it stands ("paired rows" below).
 #pragma once
 
+#include <cmath>
 #include <type_traits>
 
 #include "linattn.h"
@@ -405,20 +406,27 @@ struct Blocked {
     }
 };
 
-// Pieces along the tokens.  They cost a walk from zero and one from the unit matrix before the
-// walk for the outputs, a little more than twice the work, so they pay where sequences are long
-// for what the card has to do in all: where a sequence's own chunks, one after the other, take
-// longer (`worth` is the ratio of the two costs).  The lengths of packed sequences are not known
-// here; the longest is taken for twice the mean.
-inline int64_t choose_piece(const ssm_linattn_dims* d, bool packed, int64_t worth) {
-    const int64_t units = d->nheads * cdiv(d->dv, kCols), mean = cdiv(d->tokens, d->nseq);
-    const int64_t longest = packed && d->nseq > 1 ? (2 * mean < d->tokens ? 2 * mean : d->tokens) : mean;
-    if (longest < 1024 || units * cdiv(d->tokens, worth) >= longest) return 0;
-    // as many workgroups as the card holds at once, three a CU
-    const int64_t want = 3 * kCus / units;
-    int64_t piece = cdiv(cdiv(d->tokens, want < 1 ? 1 : want), 64) * 64;
-    if (piece < 256) piece = 256;
-    return piece < longest ? piece : 0;
+// Pieces along the tokens, the library's choice: 0 for none.  A sequence's chunks go one after the
+// other, so its length is what a call takes while the card has room; in pieces it takes `turns`
+// times a piece's and what a full card adds (its own states and transitions first, twice the work
+// of a walk), and the joints, each the time of dk / 2 tokens (more where the state fills the
+// registers).  All in tokens of a walk; `share` workgroups of a walk fill a CU.  The lengths of
+// packed sequences are not known here; the longest is taken for one and a half times the mean.
+//
+// Measured, us in pieces and whole, heads of 128 in bf16: forward 8192 tokens of 16 heads 231 and
+// 683, of 64 heads 616 and 743, of 128 heads 923 and 789 (whole is chosen), 2 x 4096 of 32 299 and
+// 365, 4 x 4096 of 32 529 and 395 (whole); 1000 + 333 + 47 float32 tokens of 8 heads of 64 and 96
+// 63 and 121.  Gradients: 8192 of 16 heads 624 and 1061, of 4096 and
+// 32 heads 602 and 653, of 4096 and 16 heads of 256 1027 and 943 (whole).
+inline int64_t choose_piece(const ssm_linattn_dims* d, bool packed, int share, int turns) {
+    const double mean = double(d->tokens) / d->nseq;
+    const double longest = packed && d->nseq > 1 ? 1.5 * mean : mean;
+    const double load = double(d->tokens) * d->nheads * cdiv(d->dv, kCols) / kCus;   // a workgroup on each CU
+    const double joint = d->dk > 128 ? d->dk * d->dk / 256.0 : 0.5 * d->dk;
+    const double least = std::sqrt(0.5 * joint * longest);
+    const int64_t piece = static_cast<int64_t>(std::ceil((load / share > least ? load / share : least) / 64)) * 64;
+    // 128: what two more launches take
+    return turns * double(piece) + 1.2 * load + joint * longest / piece + 128 < longest ? piece : 0;
 }
 
 }  // namespace dl

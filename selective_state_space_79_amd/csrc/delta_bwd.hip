@@ -17,8 +17,6 @@
 // and o_t . do_t = q_t . dq_t.  Two walks over the chunks, the forward's and one against time,
 // leave S_in and U, dS_out and Z of every chunk in memory; all gradients of a chunk are then
 // formed by a workgroup of its own.
-#include <cmath>
-
 #include "delta_walk.h"
 
 namespace {
@@ -554,26 +552,10 @@ struct GradPlan {
     size_t bytes;
 };
 
-// Pieces along the tokens, the gradients' choice: 0 for none.  A sequence's chunks one after the
-// other against twice a piece's (its own state and transition first, with a third matrix of
-// workgroups where they fill the card) and the joints, 3/4 dk tokens' time each.  The lengths of packed
-// sequences are not known here; the longest is taken for one and a half times the mean.  Measured,
-// us in pieces and whole: 8192 tokens of 16 heads of 128 698 and 1105, of 32 heads 1245 and 1377,
-// 4096 of 32 660 and 686, 2048 of 32 362 and 348, 2 x 8192 of 32 2324 and 1902; float32, 1000 +
-// 333 + 47 tokens of 8 heads of 64 and 96 99 and 153.
-inline int64_t grad_piece(const ssm_linattn_dims* d, bool packed) {
-    const double mean = double(d->tokens) / d->nseq;
-    const double longest = packed && d->nseq > 1 ? 1.5 * mean : mean;
-    const double load = double(d->tokens) * d->nheads * cdiv(d->dv, kCols) / kCus;   // a workgroup on each CU
-    const double joint = 0.75 * d->dk, least = std::sqrt(0.5 * joint * longest);
-    const int64_t piece = static_cast<int64_t>((load > least ? load : least) / 64 + 1) * 64;
-    return 2.0 * piece + 1.2 * load + joint * longest / piece < longest ? piece : 0;
-}
-
 inline int make_grad_plan(const ssm_linattn_dims* d, bool packed, GradPlan* pl) {
     pl->chunk = d->io_dtype == SSM_BF16 ? 64 : 32;
     const int64_t each = packed ? d->tokens : d->tokens / d->nseq;
-    const int64_t piece = d->piece_len ? d->piece_len : grad_piece(d, packed);
+    const int64_t piece = d->piece_len ? d->piece_len : choose_piece(d, packed, 1, 2);
     pl->pieced = piece > 0 && piece < each;
     pl->piece = pl->pieced ? piece : (int64_t(1) << 31);
     pl->npieces = !pl->pieced ? d->nseq : packed ? d->tokens / piece + d->nseq : d->nseq * cdiv(each, piece);

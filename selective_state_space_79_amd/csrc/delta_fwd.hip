@@ -387,7 +387,7 @@ inline int make_plan(const ssm_linattn_dims* d, bool packed, Plan* pl) {
     const int64_t vs = cdiv(d->dv, kCols), ks = cdiv(d->dk, kCols);
     const int64_t each = packed ? d->tokens : d->tokens / d->nseq;
     int64_t piece = d->piece_len;
-    if (piece == 0) piece = choose_piece(d, packed, 110);
+    if (piece == 0) piece = choose_piece(d, packed, 2, 1);
     pl->pieced = piece > 0 && piece < each;
     pl->piece = pl->pieced ? piece : (int64_t(1) << 31);
     pl->npieces = !pl->pieced ? d->nseq : packed ? d->tokens / piece + d->nseq : d->nseq * cdiv(each, piece);
