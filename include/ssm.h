@@ -542,14 +542,15 @@ SSM_API int ssm_linattn_bwd(const void* q, const void* k, const void* v, const f
  *          <= 2.  Keys and queries are taken as they are: a caller who wants them of length
  *          one scales them (ssm_gated_norm_fwd over heads of dk, without a gate and with a weight of
  *          dk^-1/2, does).
- * Inside a block of 64 tokens (SSM_F32: 32; gradients: 32 also where dk or dv is over 128) the
- * rows r solve a triangular system; the products are held to float32 as those of
- * ssm_linattn_* are.  A NaN or infinity in a token may reach all tokens of its block and what
- * follows in its sequence (gradients: what comes before), never another sequence. */
+ * Inside a block of 32 tokens (gradients of SSM_BF16: 64) the rows r solve a triangular system;
+ * the products are held to float32 as those of ssm_linattn_* are.  A NaN or infinity in a token may
+ * reach all tokens of its block and what follows in its sequence (gradients: what comes before),
+ * never another sequence.  In the gradients a step beta below 2^-64 in size counts as 2^-64 of its
+ * sign (but for the gradient of v). */
 
 /* Bytes of workspace of ssm_delta_fwd (never 0 for valid dims; 0 for dims it refuses): the
- * blocks' triangular matrices, 18432 bytes (SSM_F32: 6144) for each block and head, and with
- * pieces a state and a dk x dk transition for each piece and head. */
+ * blocks' triangular matrices and decays, 7168 bytes for each block and head, and with pieces a
+ * state and a dk x dk transition for each piece and head. */
 SSM_API size_t ssm_delta_fwd_workspace_bytes(const ssm_linattn_dims* dims);
 
 /* Enqueue the forward over whole sequences; as ssm_linattn_fwd, with beta and a workspace that
@@ -579,8 +580,10 @@ typedef struct ssm_delta_grads {
 } ssm_delta_grads;
 
 /* Bytes of workspace of ssm_delta_bwd (never 0 for valid dims; 0 for dims it refuses): the
- * triangular matrices, the state before and the state gradient behind each block (8 dk dv bytes a
- * block and head), where heads share q and k also float32 dq and dk of each head, and
+ * triangular matrices and decays (SSM_BF16: 20480 bytes for each block of 64 tokens and head), the
+ * state before and the state gradient behind each block (8 dk dv bytes a block and head), two
+ * float32 rows of dv values for each token and head, where heads share q and k also float32 dq and
+ * dk of each head (or, of SSM_BF16 with enough blocks to fill the card, of each shared head), and
  * with pieces two states and two transitions for each piece and head. */
 SSM_API size_t ssm_delta_bwd_workspace_bytes(const ssm_linattn_dims* dims);
 

@@ -1,7 +1,8 @@
 """Python binding of libssm.so, the MI355X selective scan (forward, decode step,
 backward, fused convolution front end, and the chunked scalar-decay pass with
 per-head step sizes), and of the operators of a block around it (``blocks.py``: linear
-attention with a decay for each head, norms with gate and residual scale).
+attention with a decay for each head, the gated delta rule, norms with gate and residual
+scale, layer norm).
 
 Argument marshalling only: every step runs in the HIP kernels of ``csrc/`` behind the C
 ABI of ``include/ssm.h``.  There is no CPU or PyTorch fallback: if the library is missing,

@@ -43,7 +43,7 @@ struct DeltaPass {
     float* s_out;             // user's final states, nullable
     uint16_t* tri;            // [blocks][H][3 parts][tiles' pairs of 16 x 32]: A
     float* steps;             // [chunks][H]: decays and steps of a walk's chunk (Steps<32>)
-    float* keep;              // [chunks][H][dk][dv]: the state each chunk starts from (reverse: its gradient behind)
+    float* keep;              // [blocks][H][dk][dv]: the state each block starts from (reverse: its gradient behind)
     float* rows;              // [T][H][dv]: U (reverse: Z), with keep
     void* dv_out;             // the gradient of v (with keep, against time)
     float* carry;             // [pieces][H][dk][dv]: the pieces' own end states, then their starting states
@@ -61,9 +61,8 @@ struct DeltaPass {
     float least;              // the least size of a step that the gradients count with
 };
 
-// kDeltaStates: the pieces' own end states and transitions; kDeltaFull: the outputs (reverse:
-// the final gradients alone); kDeltaKeep: the state at each chunk's start (reverse: its gradient
-// at the chunk's end).
+// kDeltaStates: the pieces' own end states and transitions; kDeltaFull: the outputs;
+// kDeltaKeep: the state at each block's start and U (reverse: its gradient at the block's end, and Z).
 enum DeltaMode { kDeltaStates = 0, kDeltaFull = 1, kDeltaKeep = 2 };
 void launch_delta_tri(const DeltaPass& p, bool f32, int64_t nchunks, hipStream_t s);
 void launch_delta_carry(const DeltaPass& p, const DeltaPass* r, hipStream_t s);   // r: the walk against time

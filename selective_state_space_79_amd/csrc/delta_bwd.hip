@@ -31,7 +31,10 @@ constexpr float kLeastStep = 5.42101086e-20f;   // 2^-64
 
 // ---------------------------------------------------------------- the walks, with time and against it
 // Neither waits for the other, and one alone leaves a SIMD without work between a chunk's
-// products: one launch has the workgroups of both.
+// products: one launch has the workgroups of both, two of which fit a CU.  4 x 4096 tokens of 32
+// heads of 128: 335 and 510 us one after the other, 670 together, in which 1.7 GB of states, U and
+// Z are written; a wave a SIMD issues vector instructions in 38% of its cycles alone, and both walks
+// in 50%.  Three float32 documents of 8 heads: 85 and 124 us, and 127.
 template <int PARTS, int KD, int MODE>
 __global__ void __launch_bounds__(kThreads, KD == 256 ? 1 : 2) delta_walks_kernel(DeltaPass f, DeltaPass r, uint32_t nf) {
     union Room {
@@ -124,10 +127,16 @@ __device__ inline void add_tiles(f32x4 (&o)[C / 16], const float* row0, int64_t 
     for (int i = 0; i < C / 4; ++i) o[i >> 2][i & 3] += __uint_as_float(x[i]);
 }
 
-// One workgroup per chunk and head (or the heads that share its q and k, one after the other): what is contracted over the columns of v goes in steps of 32
-// of them, U, Z and the gradient of o through LDS, the states along their rows straight into
-// registers, 16 or 32 columns of dq and dk a wave; the two matrices over the chunk's tokens, D and
-// N, are shared out in tiles.
+// One workgroup per chunk and head, or the heads that share its q and k one after the other: what is
+// contracted over the columns of v goes in steps of 32 of them, U, Z and the gradient of o through
+// LDS, the states along their rows straight into registers, 16 or 32 columns of dq and dk a wave; the
+// two matrices over the chunk's tokens, D and N, are shared out in tiles.
+//
+// The states take 128 of the 240 KB that a chunk of 64 tokens and a head of 128 x 128 reads, so the
+// bytes bound it: 4 x 4096 tokens of 32 heads, two on each q and k, in 720 us at about 4.4 TB/s
+// (vector instructions in 35% of the cycles, matrix products in 23%).  Loads are asked for a step
+// ahead, as far as 256 registers allow: all at the step's start, 28 registers a lane lay in scratch
+// memory, and those bytes took 50 us.
 template <int PARTS, int KD, int C, int W>   // W waves
 __global__ void __launch_bounds__(64 * W, 2) delta_grad_kernel(GradArgs ga) {
     typedef typename std::conditional<PARTS == 1, uint16_t, float>::type IO;
@@ -572,8 +581,10 @@ inline int make_grad_plan(const ssm_linattn_dims* d, bool packed, GradPlan* pl) 
     pl->trans = pl->pieced ? up256(np * static_cast<size_t>(d->dk * d->dk) * 4) : 0;
     pl->part = d->head_decay ? up256(nk * 8) : 0;
     // Heads that share q and k go one after the other where the chunks fill the card without them,
-    // and else leave their gradients to be summed.  Measured, us: XX
-    const bool shared = d->nheads > d->kheads, in_turn = shared && pl->nchunks * d->kheads >= 4 * kCus;
+    // and else leave their gradients in float32 to be summed.  Measured, us in turn and summed, heads
+    // of 128 in bf16: 128 workgroups (2048 tokens, 32 heads on 4) 491 and 361, 256 (on 8) 388 and
+    // 347, 512 (2048 on 16; 4096 on 8) 355 and 366, 611 and 635, 4096 (4 x 4096 on 16) 1463 and 1591.
+    const bool shared = d->nheads > d->kheads, in_turn = shared && pl->nchunks * d->kheads >= 2 * kCus;
     pl->heads = in_turn ? static_cast<int>(d->nheads / d->kheads) : 1;
     const size_t wide = shared && !in_turn ? d->nheads : in_turn && d->io_dtype == SSM_BF16 ? d->kheads : 0;
     pl->wide = up256(static_cast<size_t>(d->tokens * d->dk) * wide * 4);

@@ -31,6 +31,15 @@ template <int PARTS, int KD> struct RevRoom {
 // One workgroup walks one piece of one head's sequence for 64 columns of the state, 16 a wave, in
 // chunks of 32 tokens: 64 would halve the splits of the state into parts, but take the LDS of
 // four workgroups on a CU and twice the time from chunk to chunk.
+//
+// 131072 tokens of 16 heads of 128 in 16 pieces: outputs 1090 us, the pieces' own states and
+// transitions (twice the columns) 1280.  Bound by issue: matrix products run in 37% and 34% of the
+// cycles, vector instructions in 62% and 66% (products among them); of the latter 264 of 408 a
+// chunk split float32 values into parts.  A wave alone on its SIMD takes 2.3 us a chunk, two to
+// three 2.0, so a CU gains little from more than one workgroup: whole sequences wait for
+// themselves (8 ragged prompts of 1 to 3001 tokens, 287 us).  Not kept: products interleaved with
+// the splits by hand (slower), the splits' rests by two-term dot products (3 to 6%, and not right
+// in one form), a fourth wave a SIMD for the pieces' states (0%).
 template <int PARTS, int KD, int MODE>
 __device__ __forceinline__ void pass_walk(const DeltaPass& p, uint32_t unit, PassRoom<PARTS, KD, MODE>& room) {
     constexpr bool FULL = MODE == kDeltaFull, KEEP = MODE == kDeltaKeep, DMA = PARTS == 1;
