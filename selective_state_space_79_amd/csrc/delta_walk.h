@@ -39,7 +39,9 @@ template <int PARTS, int KD> struct RevRoom {
 // three 2.0, so a CU gains little from more than one workgroup: whole sequences wait for
 // themselves (8 ragged prompts of 1 to 3001 tokens, 287 us).  Not kept: products interleaved with
 // the splits by hand (slower), the splits' rests by two-term dot products (3 to 6%, and not right
-// in one form), a fourth wave a SIMD for the pieces' states (0%).
+// in one form), a fourth wave a SIMD for the pieces' states (0%), the next chunk's loads one by one
+// between the products (the ragged prompts 297 -> 326 us: 950 of a chunk's 7000 cycles go into their
+// issue wherever it is), their windows from increments (1%).
 template <int PARTS, int KD, int MODE>
 __device__ __forceinline__ void pass_walk(const DeltaPass& p, uint32_t unit, PassRoom<PARTS, KD, MODE>& room) {
     constexpr bool FULL = MODE == kDeltaFull, KEEP = MODE == kDeltaKeep, DMA = PARTS == 1;
