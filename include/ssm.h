@@ -666,8 +666,8 @@ SSM_API int ssm_add_norm_bwd(const void* x, const void* r, const float* scale, c
 /* Layer norm, the norm before a block that takes the mean out as well:
  *   y_i = w_i (x_i - mean) / sqrt(mean_j (x_j - mean)^2 + eps) + b_i
  *   x, y : (rows, dim) in io_dtype;  w, b : float32 (dim,), b nullable (no bias)
- * The mean is taken before the squares, so that a mean far from zero costs no digits.  y may be
- * x itself (same stride), else it overlaps no input. */
+ * The mean is taken before the squares and held beyond float32, so that a mean far from zero costs no
+ * digits and a row of equal values is b.  y may be x itself (same stride), else it overlaps no input. */
 typedef struct ssm_layer_norm_dims {
     int64_t rows;      /* >= 1 */
     int64_t dim;       /* 1 .. SSM_NORM_MAX_DIM */

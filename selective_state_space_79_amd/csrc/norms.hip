@@ -131,6 +131,22 @@ template <int N> __device__ inline float lanes_sum(float v) {
     return v;
 }
 
+// The same in float64, a word at a time.
+template <int CTRL> __device__ inline double plus_dpp(double v) {
+    const int lo = __builtin_amdgcn_update_dpp(0, __double2loint(v), CTRL, 0xf, 0xf, true);
+    const int hi = __builtin_amdgcn_update_dpp(0, __double2hiint(v), CTRL, 0xf, 0xf, true);
+    return v + __hiloint2double(hi, lo);
+}
+template <int N> __device__ inline double lanes_sum(double v) {
+    if (N > 1) v = plus_dpp<0xB1>(v);
+    if (N > 2) v = plus_dpp<0x4E>(v);
+    if (N > 4) v = plus_dpp<0x141>(v);
+    if (N > 8) v = plus_dpp<0x140>(v);
+    if (N > 16) v += __shfl_xor(v, 16);
+    if (N > 32) v += __shfl_xor(v, 32);
+    return v;
+}
+
 // Sums over the TPG threads of a group, one or several at once.  With more than one wave, a
 // slot of LDS per wave; two sets are used in turn, so one barrier is enough.  The barrier
 // waits for LDS only: rows asked for ahead stay under way.
@@ -162,6 +178,23 @@ template <int TPG> struct Summer {
         float x[1] = {v};
         all(x);
         return x[0];
+    }
+    __device__ inline double operator()(double v) {
+        v = lanes_sum<(TPG < 64 ? TPG : 64)>(v);
+        if constexpr (TPG > 64) {
+            constexpr int per = TPG / 64;
+            const int wave = threadIdx.x >> 6;
+            float* r = red + turn * kWaves * kMost;
+            turn ^= 1;
+            if ((threadIdx.x & 63) == 0) {
+                r[wave * kMost] = __int_as_float(__double2loint(v));
+                r[wave * kMost + 1] = __int_as_float(__double2hiint(v));
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            const int from = (wave / per * per + (threadIdx.x & (per - 1))) * kMost;
+            v = lanes_sum<per>(__hiloint2double(__float_as_int(r[from + 1]), __float_as_int(r[from])));
+        }
+        return v;
     }
 };
 
@@ -574,17 +607,40 @@ struct LayerArgs {
     int64_t rows, sx, sy;
     int32_t n, vec, bias;
     float eps, inv_n;
+    double inv_n64;
 };
 
-// x less the row's mean; columns behind the row's end stay zero, which the squares need.
-__device__ inline void centre(V8& x, float mean, int col, int n) {
+// A thread's share of a row's sum: of float32 values in float64.  Up to 16 bf16 values add up in
+// float32 as they are where they are of like size, and else below 2^-20 of the deviations.
+template <typename IO> struct RowSum {
+    typedef typename std::conditional<sizeof(IO) == 2, float, double>::type Of;
+    Of q = 0;
+    __device__ inline void add(const V8& x) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x.e[e] = col + e < n ? x.e[e] - mean : 0.0f;
-}
+        for (int e = 0; e < 8; ++e) q += x.e[e];
+    }
+};
+
+// A row's mean as two floats: the nearest one, and what that leaves of it, which is exactly zero
+// where all values are equal (a product of n and a float is whole in float64).
+struct Mean {
+    float hi, lo;
+    __device__ inline Mean(double sum, const LayerArgs& p) {
+        hi = static_cast<float>(sum * p.inv_n64);
+        lo = static_cast<float>(fma(-static_cast<double>(hi), static_cast<double>(p.n), sum) * p.inv_n64);
+    }
+    // x less the mean; columns behind the row's end stay zero, which the squares need
+    __device__ inline void out_of(V8& x, int col, int n) const {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x.e[e] = col + e < n ? (x.e[e] - hi) - lo : 0.0f;
+    }
+};
 
 // The mean first and the squares about it then, both from the row in registers: one more
-// exchange than sums of x and x^2 would need, which cancel where a mean is far from zero.
-// 16384 bf16 rows of 2048 in 25 us (5.4 TB/s), 4 of 4096 in 3.1.
+// exchange than sums of x and x^2 would need, which cancel where a mean is far from zero.  For the
+// same reason the mean is summed and kept beyond float32: an error of its last place is one of every
+// deviation (y of three values of 1.7e9 would be off by 0.7).  That takes 0 to 3%; a second sum, of the
+// deviations, would take 1 to 11%.  16384 bf16 rows of 2048 in 25 us (5.3 TB/s), 4 of 4096 in 3.0.
 template <typename IO, int TPG, int V>
 __global__ void __launch_bounds__(block_threads<TPG>()) layer_norm_fwd_kernel(LayerArgs p) {
     __shared__ float red[Summer<TPG>::kFloats];
@@ -596,18 +652,17 @@ __global__ void __launch_bounds__(block_threads<TPG>()) layer_norm_fwd_kernel(La
         const int64_t row = at.row + l * at.step;
         const bool on = at.on && row < p.rows;
         V8 x[V];
-        float q = 0.0f;
+        RowSum<IO> all;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             x[i] = load8<IO>(static_cast<const IO*>(p.x) + row * p.sx, 8 * (lane + TPG * i), p.n, on, p.vec);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) q += x[i].e[e];
+            all.add(x[i]);
         }
-        const float mean = sum(q) / static_cast<float>(p.n);   // not times 1/n: equal values leave no deviation
-        q = 0.0f;
+        const Mean mean(sum(static_cast<double>(all.q)), p);
+        float q = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            centre(x[i], mean, 8 * (lane + TPG * i), p.n);
+            mean.out_of(x[i], 8 * (lane + TPG * i), p.n);
 #pragma unroll
             for (int e = 0; e < 8; ++e) q = fmaf(x[i].e[e], x[i].e[e], q);
         }
@@ -625,7 +680,7 @@ __global__ void __launch_bounds__(block_threads<TPG>()) layer_norm_fwd_kernel(La
 
 // With n = (x - mean) rs and d = dy w:  dx = rs (d - mean(d) - n mean(d n)), dw = sum dy n,
 // db = sum dy.  The sums of d and of d (x - mean) go with that of the squares.  16384 bf16 rows of
-// 4096 in 98 us (4.1 TB/s of rows) and 7 for the partial sums, 8191 float32 rows of 1535 in 32 (4.7)
+// 4096 in 102 us (3.9 TB/s of rows) and 7 for the partial sums, 8191 float32 rows of 1535 in 33 (4.5)
 // and 4.5.  Not kept: two rows at a time, or rows asked for two ahead (0 to 2%).
 template <typename IO, int TPG, int V>
 __global__ void __launch_bounds__(block_threads<TPG>(), 4) layer_norm_bwd_kernel(LayerArgs p) {
@@ -659,23 +714,21 @@ __global__ void __launch_bounds__(block_threads<TPG>(), 4) layer_norm_bwd_kernel
         const bool on = at.on && row < p.rows;
         if (V > 1) fetch(row);
         Raw8<IO> rx[V], rg[V];
-        float q = 0.0f;
+        RowSum<IO> all;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             rx[i] = nx[i];
             rg[i] = ng[i];
-            const V8 x = rx[i].values();
-#pragma unroll
-            for (int e = 0; e < 8; ++e) q += x.e[e];
+            all.add(rx[i].values());
         }
         if (V == 1 && l + 1 < loops) fetch(row + at.step);
-        const float mean = sum(q) / static_cast<float>(p.n);
+        const Mean mean(sum(static_cast<double>(all.q)), p);
         float s[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             V8 x = rx[i].values();
             const V8 g = rg[i].values(), w = LdsWeights<T>{wl + i * 8 * T}.get(tid);
-            centre(x, mean, 8 * (lane + TPG * i), p.n);
+            mean.out_of(x, 8 * (lane + TPG * i), p.n);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float d = g.e[e] * w.e[e];
@@ -692,7 +745,7 @@ __global__ void __launch_bounds__(block_threads<TPG>(), 4) layer_norm_bwd_kernel
             const int col = 8 * (lane + TPG * i);
             V8 x = rx[i].values();
             const V8 g = rg[i].values(), w = LdsWeights<T>{wl + i * 8 * T}.get(tid);
-            centre(x, mean, col, p.n);
+            mean.out_of(x, col, p.n);
             V8 dx;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -1068,7 +1121,7 @@ int ssm_layer_norm_fwd(const void* x, const float* w, const float* b, void* y, c
     const Area in[] = {rows_of(y == x && a.sy == a.sx ? nullptr : x, d.rows, a.sx, d.dim, e), flat(w, nw), flat(b, nw)};
     const Area out[] = {rows_of(y, d.rows, a.sy, d.dim, e)};
     if (clash(in, out)) return SSM_ERR_ALIAS;
-    a.eps = d.eps; a.inv_n = 1.0f / static_cast<float>(d.dim);
+    a.eps = d.eps; a.inv_n = 1.0f / static_cast<float>(d.dim); a.inv_n64 = 1.0 / static_cast<double>(d.dim);
     a.vec = d.dim % 8 == 0 && vec_row(x, a.sx, e) && vec_row(y, a.sy, e) && !misaligned(w, 16) && !misaligned(b, 16);
     const int tpg = tpg_for(d.dim);
     const int64_t blocks = blocks_for(d.rows, 1, tpg, kFwdBlocks);
@@ -1105,7 +1158,7 @@ int ssm_layer_norm_bwd(const void* x, const float* w, const void* dy, void* dx, 
     const Area in[] = {rows_of(x, d.rows, a.sx, d.dim, e), flat(dy, all), flat(w, nw)};
     const Area out[] = {flat(dx, all), flat(dw, nw), flat(db, nw), flat(d.workspace, need)};
     if (clash(in, out)) return SSM_ERR_ALIAS;
-    a.eps = d.eps; a.inv_n = 1.0f / static_cast<float>(d.dim);
+    a.eps = d.eps; a.inv_n = 1.0f / static_cast<float>(d.dim); a.inv_n64 = 1.0 / static_cast<double>(d.dim);
     a.vec = d.dim % 8 == 0 && vec_row(x, a.sx, e) && vec_row(dy, d.dim, e) && vec_row(dx, d.dim, e);
     const int tpg = tpg_for(d.dim);
     const int64_t blocks = blocks_for(d.rows, 1, tpg, bwd_blocks(tpg));
