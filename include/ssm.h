@@ -546,7 +546,11 @@ SSM_API int ssm_linattn_bwd(const void* q, const void* k, const void* v, const f
  * the products are held to float32 as those of ssm_linattn_* are.  A NaN or infinity in a token may
  * reach all tokens of its block and what follows in its sequence (gradients: what comes before),
  * never another sequence.  In the gradients a step beta below 2^-64 in size counts as 2^-64 of its
- * sign (but for the gradient of v). */
+ * sign (but for the gradient of v).
+ * Limits, SSM_ERR_DIMS past them, in place of those that ssm_linattn_dims names: sequences x nheads x
+ * 64-column slices of v at most 2^23 (gradients: 2^22; single-token step: as there), where piece_len
+ * cuts pieces x nheads x slices of v and of the keys (gradients: slices of v twice) at most 2^23;
+ * tokens / 32 + nseq at most 2^23 (gradients: 2^22, of SSM_BF16 tokens / 64). */
 
 /* Bytes of workspace of ssm_delta_fwd (never 0 for valid dims; 0 for dims it refuses): the
  * blocks' triangular matrices and decays, 7168 bytes for each block and head, and with pieces a

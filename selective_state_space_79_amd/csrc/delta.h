@@ -428,5 +428,25 @@ inline int64_t choose_piece(const ssm_linattn_dims* d, bool packed, int share, i
     return turns * double(piece) + 1.2 * load + joint * longest / piece + 128 < longest ? piece : 0;
 }
 
+// Workgroups of a walk's launch: 2^31 threads, where a grid has fewer than 2^32.
+constexpr int64_t kMostWalks = 2 * kMostGroups;
+
+// How the sequences are cut, and the numbers that their pieces have.
+struct Cut {
+    int64_t piece, npieces;
+    bool pieced;
+};
+// Cuts as the caller asks, or into pieces of `choice` tokens (0: none).  A piece and head is `whole`
+// workgroups of the largest launch where nothing is cut and `cut` where something is.  False where a
+// launch would pass its limit, which the library's own pieces never do: it cuts only where sequences x
+// heads x slices of v are under 320, and then makes no more than 512 pieces of a slice.
+inline bool cut_sequences(const ssm_linattn_dims* d, bool packed, int64_t choice, int64_t whole, int64_t cut, Cut* c) {
+    const int64_t each = packed ? d->tokens : d->tokens / d->nseq, piece = d->piece_len ? d->piece_len : choice;
+    c->pieced = piece > 0 && piece < each;
+    c->piece = c->pieced ? piece : (int64_t(1) << 31);
+    c->npieces = !c->pieced ? d->nseq : packed ? d->tokens / piece + d->nseq : d->nseq * cdiv(each, piece);
+    return c->npieces <= kMostWalks / (d->nheads * (c->pieced ? cut : whole));
+}
+
 }  // namespace dl
 }  // namespace

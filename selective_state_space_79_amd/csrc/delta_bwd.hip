@@ -553,24 +553,18 @@ __global__ void __launch_bounds__(kThreads) delta_zero_kernel(DeltaPass p, ZeroR
 }
 
 // ---------------------------------------------------------------- host
-struct GradPlan {
+struct GradPlan : Cut {
     int chunk, heads;   // heads of a workgroup over a chunk's gradients
-    int64_t nchunks, piece, npieces;
-    bool pieced;
+    int64_t nchunks;
     size_t tri, steps, keep, rows, carry, trans, part, wide;   // bytes of one buffer each
     size_t bytes;
 };
 
 inline int make_grad_plan(const ssm_linattn_dims* d, bool packed, GradPlan* pl) {
+    const int64_t vs = cdiv(d->dv, kCols), ks = cdiv(d->dk, kCols);
     pl->chunk = d->io_dtype == SSM_BF16 ? 64 : 32;
-    const int64_t each = packed ? d->tokens : d->tokens / d->nseq;
-    const int64_t piece = d->piece_len ? d->piece_len : choose_piece(d, packed, 1, 2);
-    pl->pieced = piece > 0 && piece < each;
-    pl->piece = pl->pieced ? piece : (int64_t(1) << 31);
-    pl->npieces = !pl->pieced ? d->nseq : packed ? d->tokens / piece + d->nseq : d->nseq * cdiv(each, piece);
     pl->nchunks = count_chunks(d, packed, pl->chunk);
-    if (pl->npieces > kMostGroups / (d->nheads * (cdiv(d->dv, kCols) + cdiv(d->dk, kCols))) || pl->nchunks > kMostGroups)
-        return SSM_ERR_DIMS;
+    if (!cut_sequences(d, packed, choose_piece(d, packed, 1, 2), 2 * vs, 2 * vs + ks, pl) || pl->nchunks > kMostGroups) return SSM_ERR_DIMS;
     const size_t nk = static_cast<size_t>(pl->nchunks * d->nheads), np = static_cast<size_t>(pl->npieces * d->nheads);
     const size_t state = static_cast<size_t>(d->dk * d->dv) * 4;
     pl->tri = up256(nk * (pl->chunk == 64 ? tri_elems<64>() : tri_elems<32>()) * 2);

@@ -380,23 +380,16 @@ __global__ void __launch_bounds__(kThreads) delta_step_kernel(StepArgs p) {
 }
 
 // ---------------------------------------------------------------- host: plans
-struct Plan {
-    int64_t nchunks, piece, npieces;
-    bool pieced;
+struct Plan : Cut {
+    int64_t nchunks;
     size_t tri, steps, carry, trans;   // bytes
     size_t bytes() const { return tri + steps + carry + trans; }
 };
 
 inline int make_plan(const ssm_linattn_dims* d, bool packed, Plan* pl) {
     const int64_t vs = cdiv(d->dv, kCols), ks = cdiv(d->dk, kCols);
-    const int64_t each = packed ? d->tokens : d->tokens / d->nseq;
-    int64_t piece = d->piece_len;
-    if (piece == 0) piece = choose_piece(d, packed, 2, 1);
-    pl->pieced = piece > 0 && piece < each;
-    pl->piece = pl->pieced ? piece : (int64_t(1) << 31);
-    pl->npieces = !pl->pieced ? d->nseq : packed ? d->tokens / piece + d->nseq : d->nseq * cdiv(each, piece);
     pl->nchunks = count_chunks(d, packed, kChunk);
-    if (pl->npieces > kMostGroups / (d->nheads * (vs + ks)) || pl->nchunks > 2 * kMostGroups) return SSM_ERR_DIMS;
+    if (!cut_sequences(d, packed, choose_piece(d, packed, 2, 1), vs, vs + ks, pl) || pl->nchunks > 2 * kMostGroups) return SSM_ERR_DIMS;
     pl->tri = up256(static_cast<size_t>(pl->nchunks * d->nheads * tri_elems<kChunk>()) * 2);
     pl->steps = static_cast<size_t>(pl->nchunks * d->nheads) * sizeof(Steps<kChunk>);
     pl->carry = pl->pieced ? up256(static_cast<size_t>(pl->npieces * d->nheads * d->dk * d->dv) * 4) : 0;
