@@ -9,13 +9,17 @@
 //                                            N_ij = -beta_i e^{G_i-G_j} Z_i . U_j, j < i
 //   dbeta_i = Z_i . r_i = Z_i . U_i / beta_i
 //
-// The decay of token t scales all that the state holds
-// then, so dg_t = <dS'_t, S'_t>; between tokens it changes by what is read and what is written:
+// The decay of token t scales all that is written before it and read at it or later, so with what
+// token i reads of S_in, what of token j's row is left in dS_out, and what i reads of j,
 //
-//   dg_t = dg_{t+1} + o_t . do_t - v_t . dv_t        behind a chunk <dS_out, S_out>
+//   in_i = scale e^{G_i} dO_i . S_in^T q_i - beta_i e^{G_i} Z_i . S_in^T k_i
+//   out_j = e^{G_C-G_j} U_j . dS_out^T k_j           W_ij = D_ij q_i . k_j + N_ij k_i . k_j, j < i
+//   dg_t = e^{G_C} <S_in, dS_out> + sum_{i>=t} in_i + sum_{j<t} out_j + sum_{i>=t>j} W_ij
 //
-// and o_t . do_t = q_t . dq_t.  Two walks over the chunks, the forward's and one against time,
-// leave S_in and U, dS_out and Z of every chunk in memory; all gradients of a chunk are then
+// Each term has the decays between as a factor.  (dg_t = dg_{t+1} + q_t . dq_t - v_t . dv_t, which
+// needs no W, holds what a token reads of itself twice, without any decay: a dg of e^-10 would be what
+// two such numbers leave of each other.)  Two walks over the chunks, the forward's and one against
+// time, leave S_in and U, dS_out and Z of every chunk in memory; all gradients of a chunk are then
 // formed by a workgroup of its own.
 #include "delta_walk.h"
 
@@ -130,13 +134,15 @@ __device__ inline void add_tiles(f32x4 (&o)[C / 16], const float* row0, int64_t 
 // One workgroup per chunk and head, or the heads that share its q and k one after the other: what is
 // contracted over the columns of v goes in steps of 32 of them, U, Z and the gradient of o through
 // LDS, the states along their rows straight into registers, 16 or 32 columns of dq and dk a wave; the
-// two matrices over the chunk's tokens, D and N, are shared out in tiles.
+// matrices over the chunk's tokens, D, N and W, are shared out in tiles.
 //
-// The states take 128 of the 240 KB that a chunk of 64 tokens and a head of 128 x 128 reads, so the
-// bytes bound it: 4 x 4096 tokens of 32 heads, two on each q and k, in 720 us at about 4.4 TB/s
-// (vector instructions in 35% of the cycles, matrix products in 23%).  Loads are asked for a step
-// ahead, as far as 256 registers allow: all at the step's start, 28 registers a lane lay in scratch
-// memory, and those bytes took 50 us.
+// The states take 128 of the 224 KB that a chunk of 64 tokens and a head of 128 x 128 reads, so the
+// bytes and their latency bound it: 4 x 4096 tokens of 32 heads, two on each q and k, in 762 us, 2.4 GB
+// read and 0.5 written by the counters (2.1 and 0.5 are needed), 3.9 TB/s; waves wait in 53% of their
+// cycles, vector instructions and matrix products take 30 and 23% of a SIMD's.  W, its sums and those of
+// what comes in and goes out take 30 us more than the rows of v and the one sum without them did.  Loads
+// are asked for a step ahead, as far as 256 registers allow: all at the step's start, 28 registers a lane
+// lay in scratch memory, and those bytes took 50 us.
 template <int PARTS, int KD, int C, int W>   // W waves
 __global__ void __launch_bounds__(64 * W, 2) delta_grad_kernel(GradArgs ga) {
     typedef typename std::conditional<PARTS == 1, uint16_t, float>::type IO;
@@ -148,7 +154,7 @@ __global__ void __launch_bounds__(64 * W, 2) delta_grad_kernel(GradArgs ga) {
     constexpr int STEP = (2 * WP + PARTS) * C * 32;  // U, Z and the gradient of o, 32 columns
     __shared__ __align__(16) uint16_t K[PARTS * C * KD], Q[PARTS * C * KD], buf[STEP > 2 * TRI ? STEP : 2 * TRI];
     __shared__ Steps<C> st;
-    __shared__ float pg[W][C], zu[C], vz[C];
+    __shared__ __align__(16) float pin[W][C], pout[W][C], wrow[IT][C], wcol[IT][C], zu[C];
     __shared__ double ps[W];
     uint16_t* const Us = buf;
     uint16_t* const Zs = buf + WP * C * 32;
@@ -189,7 +195,7 @@ __global__ void __launch_bounds__(64 * W, 2) delta_grad_kernel(GradArgs ga) {
         const int tid = 64 * wave + lane, g4 = lane >> 4, l16 = lane & 15;
         const float* const Sin = p.keep + (ci * p.H + h) * ssz;
         const float* const Sout = ga.keep_d + (ci * p.H + h) * ssz;
-        for (int i = tid; i < W * C; i += 64 * W) (&pg[0][0])[i] = 0.0f;
+        for (int i = tid; i < W * C; i += 64 * W) (&pin[0][0])[i] = (&pout[0][0])[i] = 0.0f;
         if (wave == W - 1) {
             const int64_t t = c0 + lane;
             const bool on = lane < C && t < hi;
@@ -212,10 +218,9 @@ __global__ void __launch_bounds__(64 * W, 2) delta_grad_kernel(GradArgs ga) {
         const int ts = tid / (32 / CPT), cs = CPT * (tid % (32 / CPT));
         const bool mine = ts < C, here = mine && c0 + ts < hi;
         const bool vec = p.dv % 4 == 0;
-        const IO* const vrow = static_cast<const IO*>(p.v) + (c0 + ts) * p.sv + int64_t(h) * p.dv;
         const IO* const orow = static_cast<const IO*>(ga.dout) + (c0 + ts) * ga.so + int64_t(h) * p.dv;
         u32x4 nu[N4], nz[N4], ns[NC][2], nd[NC][2];
-        Raw4<IO> nv[N4], no[N4];
+        Raw4<IO> no[N4];
         const Rsrc wu = rows_rsrc(reinterpret_cast<char*>(p.rows + (c0 * p.H + h) * p.dv), int64_t(p.H) * p.dv * 4, hi - c0, C);
         const Rsrc wz = rows_rsrc(const_cast<char*>(reinterpret_cast<const char*>(ga.z + (c0 * p.H + h) * p.dv)), int64_t(p.H) * p.dv * 4, hi - c0, C);
         const Rsrc ws = rows_rsrc(const_cast<char*>(reinterpret_cast<const char*>(Sin)), ssz * 4, 1, 1);
@@ -234,7 +239,6 @@ __global__ void __launch_bounds__(64 * W, 2) delta_grad_kernel(GradArgs ga) {
             for (int x = 0; x < N4; ++x) {
                 nu[x] = four(wu, trow, c + cs + 4 * x);
                 nz[x] = four(wz, trow, c + cs + 4 * x);
-                nv[x].load(vrow, here, c + cs + 4 * x, p.dv, p.wide);
                 no[x].load(orow, here, c + cs + 4 * x, p.dv, p.wide);
             }
         };
@@ -246,7 +250,7 @@ __global__ void __launch_bounds__(64 * W, 2) delta_grad_kernel(GradArgs ga) {
                     n[k][x] = four(w, uint32_t(16 * (wave + W * k) + l16) * uint32_t(p.dv * 4), c + 8 * g4 + 4 * x);
         };
         const auto f4 = [](const u32x4& x) { return __builtin_bit_cast(f32x4, x); };
-        float s_zu = 0.0f, s_vz = 0.0f;
+        float s_zu = 0.0f;
         double cross = 0.0;
         ask(0);
         ask_state(ws, ns, 0);
@@ -256,12 +260,9 @@ __global__ void __launch_bounds__(64 * W, 2) delta_grad_kernel(GradArgs ga) {
             if (mine) {
 #pragma unroll
                 for (int x = 0; x < N4; ++x) {
-                    const f32x4 u = f4(nu[x]), z = f4(nz[x]), v = nv[x].values();
+                    const f32x4 u = f4(nu[x]), z = f4(nz[x]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        s_zu = fmaf(z[e], u[e], s_zu);
-                        s_vz = fmaf(v[e], z[e], s_vz);
-                    }
+                    for (int e = 0; e < 4; ++e) s_zu = fmaf(z[e], u[e], s_zu);
                     // rows lie in tiles of 16 x 32, part by part
                     const int cc = cs + 4 * x, to = (ts >> 4) * 512 + at_piece<32>(ts & 15, cc >> 3) + (cc & 4);
                     const auto put = [&](uint16_t* at, const f32x4& x, auto parts) {
@@ -338,15 +339,11 @@ __global__ void __launch_bounds__(64 * W, 2) delta_grad_kernel(GradArgs ga) {
             lds_barrier();
         }
         s_zu = CPT == 8 ? sum4(s_zu) : sum8(s_zu);
-        s_vz = CPT == 8 ? sum4(s_vz) : sum8(s_vz);
-        if (mine && cs == 0) {
-            zu[ts] = s_zu;
-            vz[ts] = s_vz;
-        }
+        if (mine && cs == 0) zu[ts] = s_zu;
         cross *= double(st.tail[0]);
         wait_memory<0>();
         __syncthreads();        // q and k are there
-        // ---------------------------------------- D and N, tiles on and below the diagonal
+        // ---------------------------------------- D, N and W, tiles on and below the diagonal
         uint16_t* const Ds = buf;
         uint16_t* const Ns = buf + TRI;
         const uint32_t base = row_base<KD>(lane);
@@ -358,12 +355,36 @@ __global__ void __launch_bounds__(64 * W, 2) delta_grad_kernel(GradArgs ga) {
             tile(m, it, jt);
             const int i = 16 * it + l16, j0 = 16 * jt + 4 * g4;
             const float gi = st.hi[i], ei = st.lo[i], b = st.beta[i];
-            f32x4 d, n;
+            f32x4 qk = zero, kk = zero;
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+                u32x4 x[PARTS], y[PARTS], z[PARTS];
+#pragma unroll
+                for (int k = 0; k < PARTS; ++k) {
+                    x[k] = row_op<KD>(K + k * C * KD, 16 * jt, kb, base);
+                    y[k] = row_op<KD>(Q + k * C * KD, 16 * it, kb, base);
+                    z[k] = row_op<KD>(K + k * C * KD, 16 * it, kb, base);
+                }
+                qk = mma_parts<PARTS, PARTS>(x, y, qk);
+                kk = mma_parts<PARTS, PARTS>(x, z, kk);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            f32x4 d, n, w;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const float e = __builtin_amdgcn_exp2f((gi - st.hi[j0 + r]) + (ei - st.lo[j0 + r]));
                 d[r] = j0 + r <= i ? ap[mm][r] * (e * p.scale) : 0.0f;
                 n[r] = j0 + r < i ? -b * (an[mm][r] * e) : 0.0f;
+                w[r] = j0 + r < i ? fmaf(d[r], qk[r], n[r] * kk[r]) : 0.0f;
+            }
+            {
+                float s = (w[0] + w[1]) + (w[2] + w[3]);
+                s += __shfl_xor(s, 16);
+                s += __shfl_xor(s, 32);
+                if (g4 == 0) wrow[jt][i] = s;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) w[r] = sum16(w[r]);
+                if (l16 == 0) *reinterpret_cast<f32x4*>(&wcol[it][j0]) = w;
             }
             const int o = p_block(it, jt >> 1) * 512 + 4 * (g4 & 1);
             const int at = o + at_piece<32>(l16, 2 * (jt & 1) + (g4 >> 1)), above = o + at_piece<32>(l16, 2 + (g4 >> 1));
@@ -411,11 +432,15 @@ __global__ void __launch_bounds__(64 * W, 2) delta_grad_kernel(GradArgs ga) {
                     const f32x4 l = *reinterpret_cast<const f32x4*>(&st.out[t0]);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
+                        const float q = element(Q, t0 + r, i0 + l16), k = element(K, t0 + r, i0 + l16), z = f[r] * az[c][i][r];
                         aq[c][i][r] *= e[r] * p.scale;
                         au[c][i][r] *= l[r];
-                        // u_j . dS_out^T k_j of the tokens
-                        cross = fma(double(au[c][i][r]), double(element(K, t0 + r, i0 + l16)), cross);
-                        au[c][i][r] = fmaf(-f[r], az[c][i][r], au[c][i][r]);
+                        const float in = sum16(fmaf(q, aq[c][i][r], -(z * k))), out = sum16(au[c][i][r] * k);
+                        if (l16 == 0) {
+                            pin[wave][t0 + r] += in;
+                            pout[wave][t0 + r] += out;
+                        }
+                        au[c][i][r] -= z;
                     }
                 }
                 const uint32_t bc = col_base<KD, 0>(i0, lane);
@@ -449,15 +474,6 @@ __global__ void __launch_bounds__(64 * W, 2) delta_grad_kernel(GradArgs ga) {
                             au[c][i] = mma_parts<WP, PARTS>(a, k[jb], au[c][i]);
                         }
                     }
-                // o . do = q . dq of each token
-#pragma unroll
-                for (int i = 0; i < IT; ++i)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int t = 16 * i + 4 * g4 + r;
-                        const float s = sum16(element(Q, t, i0 + l16) * aq[c][i][r]);
-                        if (l16 == 0) pg[wave][t] += s;
-                    }
                 if (sum) {
                     add_tiles<C>(aq[c], tq, pitch4, hi - c0, i0, p.dk, lane);
                     add_tiles<C>(au[c], tk, pitch4, hi - c0, i0, p.dk, lane);
@@ -471,18 +487,28 @@ __global__ void __launch_bounds__(64 * W, 2) delta_grad_kernel(GradArgs ga) {
         if (lane == 0) ps[wave] = cross;
         __syncthreads();
         if (wave == 0) {
-            double x = 0.0, end = 0.0;
+            double x = 0.0, y = 0.0, dg = 0.0;
             const int64_t t = c0 + lane;
             const bool on = lane < C && t < hi;
             if (lane < C) {
-                x = -double(st.beta[lane] * vz[lane]);
+                // the sum of W over i >= t > j by rows less columns from t on
 #pragma unroll
-                for (int k = 0; k < W; ++k) x += double(pg[k][lane]);
+                for (int k = 0; k < IT; ++k) {
+                    if (k <= lane / 16) x += double(wrow[k][lane]);
+                    if (k >= lane / 16) x -= double(wcol[k][lane]);
+                }
+#pragma unroll
+                for (int k = 0; k < W; ++k) {
+                    x += double(pin[k][lane]);
+                    y += double(pout[k][lane]);
+                }
             }
 #pragma unroll
-            for (int k = 0; k < W; ++k) end += ps[k];
-            const double s = scan_f64(x);                       // of the tokens up to this one
-            const double dg = end + (lane_f64(s, 63) - s) + x;
+            for (int k = 0; k < W; ++k) dg += ps[k];
+            // from this token on, and up to the one before: no differences of longer sums, which would
+            // leave 2^-53 of what no decay has made small
+            const double after = __shfl(scan_f64(__shfl(x, 63 - lane)), 63 - lane), before = __shfl_up(scan_f64(y), 1);
+            dg += after + (lane > 0 ? before : 0.0);
             if (on) {
                 ga.dbeta[t * p.H + h] = zu[lane] / st.beta[lane];     // Z . r = Z . U / beta
                 if (!ga.part) ga.dg[t * p.H + h] = float(dg);
