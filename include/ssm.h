@@ -547,6 +547,9 @@ SSM_API int ssm_linattn_bwd(const void* q, const void* k, const void* v, const f
  * reach all tokens of its block and what follows in its sequence (gradients: what comes before),
  * never another sequence.  In the gradients a step beta below 2^-64 in size counts as 2^-64 of its
  * sign (but for the gradient of v).
+ * The library cuts long sequences into pieces where that is faster, by the mean length of packed ones:
+ * for one long sequence among many short ones give piece_len (1024 to 4096), which cuts only what is
+ * longer.
  * Limits, SSM_ERR_DIMS past them, in place of those that ssm_linattn_dims names: sequences x nheads x
  * 64-column slices of v at most 2^23 (gradients: 2^22; single-token step: as there), where piece_len
  * cuts pieces x nheads x slices of v and of the keys (gradients: slices of v twice) at most 2^23;

@@ -524,7 +524,8 @@ def delta_fwd(q, k, v, g, beta, *, scale=1.0, cu_seqlens=None, s0=None, s_last=N
 
     beta: float32 (tokens, heads) (or (batch, L, heads)); the other arguments, and what is
     returned, are those of linattn_fwd.  Keys are taken as they are: states stay bounded where
-    0 <= beta |k|^2 <= 2.
+    0 <= beta |k|^2 <= 2.  The library cuts sequences by their mean length: for one long sequence
+    packed with many short ones give piece_len (1024 to 4096, here and in delta_bwd).
     """
     import torch
 

@@ -408,15 +408,17 @@ struct Blocked {
 // Pieces along the tokens, the library's choice: 0 for none.  A sequence's chunks go one after the
 // other, so its length is what a call takes while the card has room; in pieces it takes `turns`
 // times a piece's and what a full card adds (its own states and transitions first, twice the work
-// of a walk), and the joints, each the time of dk / 2 tokens (more where the state fills the
-// registers).  All in tokens of a walk; `share` workgroups of a walk fill a CU.  The lengths of
-// packed sequences are not known here; the longest is taken for one and a half times the mean.
+// of a walk), and the joints, each the time of dk / 2 tokens (more with keys over 128, whose carry
+// keeps part of its values in scratch memory).  All in tokens of a walk; `share` workgroups of a walk fill a CU.  The lengths of
+// packed sequences are not known here; the longest is taken for one and a half times the mean, so one
+// long sequence among many short ones stays whole unless the caller names a piece (16384 + 15 x 64 tokens
+// of 8 heads of 128: 1357 us whole, 284 in pieces of 1024; gradients 2374 and 723).
 //
 // Measured, us in pieces and whole, heads of 128 in bf16: forward 8192 tokens of 16 heads 231 and
 // 683, of 64 heads 616 and 743, of 128 heads 923 and 789 (whole is chosen), 2 x 4096 of 32 299 and
 // 365, 4 x 4096 of 32 529 and 395 (whole); 1000 + 333 + 47 float32 tokens of 8 heads of 64 and 96
-// 63 and 121.  Gradients: 8192 of 16 heads 624 and 1061, of 4096 and
-// 32 heads 602 and 653, of 4096 and 16 heads of 256 1027 and 943 (whole).
+// 63 and 121.  Gradients: 8192 of 16 heads 641 and 1068, of 4096 and
+// 32 heads 609 and 664, of 4096 and 16 heads of 256 1018 and 938 (whole).
 inline int64_t choose_piece(const ssm_linattn_dims* d, bool packed, int share, int turns) {
     const double mean = double(d->tokens) / d->nseq;
     const double longest = packed && d->nseq > 1 ? 1.5 * mean : mean;

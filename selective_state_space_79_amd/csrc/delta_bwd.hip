@@ -602,8 +602,8 @@ inline int make_grad_plan(const ssm_linattn_dims* d, bool packed, GradPlan* pl) 
     pl->part = d->head_decay ? up256(nk * 8) : 0;
     // Heads that share q and k go one after the other where the chunks fill the card without them,
     // and else leave their gradients in float32 to be summed.  Measured, us in turn and summed, heads
-    // of 128 in bf16: 128 workgroups (2048 tokens, 32 heads on 4) 491 and 361, 256 (on 8) 388 and
-    // 347, 512 (2048 on 16; 4096 on 8) 355 and 366, 611 and 635, 4096 (4 x 4096 on 16) 1463 and 1591.
+    // of 128 in bf16: 128 workgroups (2048 tokens, 32 heads on 4) 484 and 355, 256 (on 8) 393 and
+    // 346, 512 (2048 on 16; 4096 on 8) 333 and 348, 603 and 632, 4096 (4 x 4096 on 16) 1441 and 1560.
     const bool shared = d->nheads > d->kheads, in_turn = shared && pl->nchunks * d->kheads >= 2 * kCus;
     pl->heads = in_turn ? static_cast<int>(d->nheads / d->kheads) : 1;
     const size_t wide = shared && !in_turn ? d->nheads : in_turn && d->io_dtype == SSM_BF16 ? d->kheads : 0;

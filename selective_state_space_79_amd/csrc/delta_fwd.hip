@@ -167,8 +167,9 @@ __global__ void __launch_bounds__(kThreads, pass_waves(KD, PARTS, MODE)) delta_p
 }
 
 // ---------------------------------------------------------------- pieces' starting states
-// Walks the pieces of one sequence and head for 64 columns of the state (128 with keys over 128:
-// registers), 16 a wave: each piece's own end state N is replaced by the state S it starts from, and
+// Walks the pieces of one sequence and head for 64 columns of the state (128 with keys over 128, where
+// 512 threads share the rows of W; their 256 registers do not hold S, N, the parts and the rows ahead,
+// and 564 bytes of a lane lie in scratch memory), 16 a wave: each piece's own end state N is replaced by the state S it starts from, and
 // the next one starts from W S + N with the piece's transition W (against time its transpose).  W
 // does not depend on what came before, so its rows are asked for four tiles of 16 ahead, and all
 // waves share their split.  A piece after the other is latency: 16 pieces of 16 heads of 128 in
@@ -276,7 +277,8 @@ struct StepArgs {
 // under k and under q is summed over the rows in one pass and one exchange, and the output is
 // (S'^T q + (k . q) u) scale, so the state is read once and written once.  Bound by those bytes:
 // 256 sequences of 32 heads of 128 x 128 in 198 us on the card, 5.4 TB/s; one sequence of 32 heads
-// of 128 x 128 in 6.0, the latency of one round of loads.
+// of 128 x 128 in 6.0, the latency of one round of loads and, with slices of 16 columns, of sixteen
+// threads that add up 64 rows.
 template <typename IO, int R>
 __global__ void __launch_bounds__(kThreads) delta_step_kernel(StepArgs p) {
     constexpr int VW = 4;

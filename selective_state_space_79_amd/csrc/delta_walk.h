@@ -33,15 +33,15 @@ template <int PARTS, int KD> struct RevRoom {
 // four workgroups on a CU and twice the time from chunk to chunk.
 //
 // 131072 tokens of 16 heads of 128 in 16 pieces: outputs 1090 us, the pieces' own states and
-// transitions (twice the columns) 1280.  Bound by issue: matrix products run in 37% and 34% of the
-// cycles, vector instructions in 62% and 66% (products among them); of the latter 264 of 408 a
-// chunk split float32 values into parts.  A wave alone on its SIMD takes 2.3 us a chunk, two to
-// three 2.0, so a CU gains little from more than one workgroup: whole sequences wait for
-// themselves (8 ragged prompts of 1 to 3001 tokens, 287 us).  Not kept: products interleaved with
-// the splits by hand (slower), the splits' rests by two-term dot products (3 to 6%, and not right
-// in one form), a fourth wave a SIMD for the pieces' states (0%), the next chunk's loads one by one
-// between the products (the ragged prompts 297 -> 326 us: 950 of a chunk's 7000 cycles go into their
-// issue wherever it is), their windows from increments (1%).
+// transitions (twice the columns) 1280.  Bound by issue: matrix products run in 37% and 35% of the
+// cycles, other vector instructions in 52% and 58%, both at once in 11% and 13%, one or the other in
+// 78% and 80%; of the vector instructions 264 of 408 a chunk split float32 values into parts.  A wave
+// alone on its SIMD takes 2.3 us a chunk, two to three 2.0, so a CU gains little from more than one
+// workgroup: whole sequences wait for themselves (8 ragged prompts of 1 to 3001 tokens, 287 us).  Not
+// kept: products interleaved with the splits by hand (slower), the splits' rests by two-term dot
+// products (3 to 6%, and not right in one form), a fourth wave a SIMD for the pieces' states (0%), the
+// next chunk's loads one by one between the products (the ragged prompts 297 -> 326 us: 950 of a
+// chunk's 7000 cycles go into their issue wherever it is), their windows from increments (1%).
 template <int PARTS, int KD, int MODE>
 __device__ __forceinline__ void pass_walk(const DeltaPass& p, uint32_t unit, PassRoom<PARTS, KD, MODE>& room) {
     constexpr bool FULL = MODE == kDeltaFull, KEEP = MODE == kDeltaKeep, DMA = PARTS == 1;
